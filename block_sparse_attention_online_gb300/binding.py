@@ -31,10 +31,22 @@ EXPORTED = ("attn_skip_prefill", "attn_skip_prefill_from_host", "attn_skip_prefi
             "attn_skip_lambda_for_target", "attn_skip_selftest_wait_timeout",
             "attn_skip_last_device_error", "attn_skip_status_string",
             "attn_skip_santa_workspace", "attn_skip_santa_decode",
-            "attn_skip_santa_decode_noalloc")
+            "attn_skip_santa_decode_noalloc", "attn_skip_kv_append", "attn_skip_kv_gather",
+            "attn_skip_chunk_paged", "attn_skip_chunk_paged_splits")
 
 #: Samplers of attn_skip_santa_decode.
 SANTA_MODES = {"iid": 0, "sys": 1, "strat": 2}
+
+#: Formats of a paged cache.
+KV_FORMATS = {"bf16": 0, "e4m3": 1, "nvfp4": 2}
+
+
+class _KvPages(ctypes.Structure):
+    """attn_kv_pages."""
+    _fields_ = [("format", ctypes.c_int), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("page_stride", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_bs", ctypes.c_void_p), ("v_bs", ctypes.c_void_p)]
 
 
 class AttnSkipError(RuntimeError):
@@ -88,6 +100,12 @@ def load() -> ctypes.CDLL:
                                            P, P, i, P, P, P]
     lib.attn_skip_santa_decode_noalloc.argtypes = [P, P, P, i, i, i, i, i, i, i, i64, i64, f, i,
                                                    i, P, i, i, P, P, P]
+    lib.attn_skip_kv_append.argtypes = [P, P, P, i, i64, i64, i, i, P, P, P, i, P]
+    lib.attn_skip_kv_gather.argtypes = [P, i, i, P, P, P, i, i, P, P, P]
+    lib.attn_skip_chunk_paged.argtypes = [P, P, i64, i, i, i, P, i, P, i, P, i, f, P, i, i, P, P,
+                                          P, P, P, P]
+    lib.attn_skip_chunk_paged_splits.argtypes = [i] * 7
+    lib.attn_skip_chunk_paged_splits.restype = ctypes.c_int
     lib.attn_skip_status_string.argtypes = [i]
     lib.attn_skip_status_string.restype = ctypes.c_char_p
     for fn in ("attn_skip_prefill", "attn_skip_prefill_blocks", "attn_skip_prefill_varlen",
@@ -97,7 +115,8 @@ def load() -> ctypes.CDLL:
                "attn_skip_lambda_for_sparsity", "attn_skip_fit_lambda_model",
                "attn_skip_selftest_wait_timeout", "attn_skip_last_device_error",
                "attn_skip_santa_workspace", "attn_skip_santa_decode",
-               "attn_skip_santa_decode_noalloc"):
+               "attn_skip_santa_decode_noalloc", "attn_skip_kv_append", "attn_skip_kv_gather",
+               "attn_skip_chunk_paged"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -581,6 +600,234 @@ def attn_skip_santa_decode_noalloc(q, k, v, n_samples, mode, u, o, idx=None, n_t
                             f"B*Hq*n_tiles*2 <= {NOALLOC_STAT_FLOATS} statistics floats)", st)
     _check("attn_skip_santa_decode_noalloc", st)
     return o
+
+
+class PagedKV:
+    """A paged key/value cache: the pool tensors of one layer, on one CUDA device.
+
+    ``fmt`` ``"bf16"``: k, v [n_pages, Hkv, page_size, 128] bf16; ``"e4m3"``: the
+    same shape as uint8 codes, with k_scale, v_scale [n_pages, Hkv, page_size]
+    uint8; ``"nvfp4"``: k, v [n_pages, Hkv, page_size, 64] uint8, the scales and
+    k_bs, v_bs [n_pages, Hkv, page_size, 8] uint8.  k and v may have pages
+    further apart than one page (views of one pool that holds both); within a
+    page and in the scales the layout is dense.  The tensors are the cache: they
+    are kept, not copied."""
+
+    def __init__(self, fmt, k, v, k_scale=None, v_scale=None, k_bs=None, v_bs=None):
+        code = KV_FORMATS[fmt]
+        n_pages, Hkv, page_size, width = k.shape
+        want = torch.bfloat16 if fmt == "bf16" else torch.uint8
+        d = 2 * width if fmt == "nvfp4" else width
+        if v.shape != k.shape or k.dtype != want or v.dtype != want:
+            raise ValueError(f"k and v must be {want} tensors of one shape")
+        for x in (k, v):
+            if x.stride()[1:] != (page_size * width, width, 1):
+                raise ValueError("k and v must be dense within a page")
+        if k.stride(0) != v.stride(0):
+            raise ValueError("k and v must have the same page stride")
+        rows = (n_pages, Hkv, page_size)
+        need = {"bf16": (), "e4m3": ((k_scale, rows), (v_scale, rows)),
+                "nvfp4": ((k_scale, rows), (v_scale, rows), (k_bs, rows + (d // 16,)),
+                          (v_bs, rows + (d // 16,)))}[fmt]
+        given = [x for x in (k_scale, v_scale, k_bs, v_bs) if x is not None]
+        if len(given) != len(need):
+            raise ValueError(f"an {fmt} cache takes {len(need)} scale tensors")
+        for x, shape in need:
+            if x is None or x.dtype != torch.uint8 or tuple(x.shape) != shape \
+                    or not x.is_contiguous():
+                raise ValueError(f"scales must be contiguous uint8 tensors, {shape} expected")
+        for x in (k, v, *given):
+            if not x.is_cuda or x.device != k.device:
+                raise ValueError("tensors must be on one CUDA device")
+        self.format, self.n_pages, self.Hkv, self.page_size, self.d = fmt, n_pages, Hkv, page_size, d
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k_bs, self.v_bs, self.device = k_bs, v_bs, k.device
+        p = [x.data_ptr() if x is not None else None for x in (k, v, k_scale, v_scale, k_bs, v_bs)]
+        # The page stride matters, and is meaningful, only between pages.
+        stride = k.stride(0) * k.element_size() if n_pages > 1 else 0
+        self._c = _KvPages(code, n_pages, page_size, Hkv, d, stride, *p)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, fmt, n_pages, page_size, Hkv, d=128, device="cuda"):
+        """A cache with freshly allocated, unwritten pages."""
+        def u8(*shape):
+            return torch.empty(*shape, dtype=torch.uint8, device=device)
+        rows = (n_pages, Hkv, page_size)
+        if fmt == "bf16":
+            return cls(fmt, *(torch.empty(*rows, d, dtype=torch.bfloat16, device=device)
+                              for _ in range(2)))
+        if fmt == "e4m3":
+            return cls(fmt, u8(*rows, d), u8(*rows, d), u8(*rows), u8(*rows))
+        return cls(fmt, u8(*rows, d // 2), u8(*rows, d // 2), u8(*rows), u8(*rows),
+                   u8(*rows, d // 16), u8(*rows, d // 16))
+
+
+def _paged_call(kv, stream, call, *tensors):
+    """Run ``call(stream pointer)`` on the cache's device.  What it allocates
+    belongs to the stream it launches on."""
+    for x in tensors:
+        if x.device != kv.device:
+            raise ValueError("tensors must be on the cache's device")
+    if stream is None and torch.cuda.current_device() == kv.device.index:
+        return call(torch._C._cuda_getCurrentRawStream(kv.device.index))
+    with torch.cuda.device(kv.device):
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _int32(n_seq, page_table, **lengths):
+    """Shapes of the device arrays of a batch."""
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n_seq \
+            or not page_table.is_contiguous():
+        raise ValueError(f"page_table must be a contiguous int32 tensor [{n_seq}, max_pages]")
+    for name, x in lengths.items():
+        if x.dtype != torch.int32 or x.shape != (n_seq,) or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor [{n_seq}]")
+
+
+def _cu(name, cu):
+    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 2 or not cu.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [n_seq + 1]")
+    return cu.numel() - 1
+
+
+def _token_rows(name, x, heads, d):
+    """Token stride of x [total, heads, d]; the rows of a token must be dense."""
+    if x.dim() != 3 or x.shape[1:] != (heads, d):
+        raise ValueError(f"{name} must have shape [total, {heads}, {d}]")
+    if x.shape[0] and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != d)):
+        raise ValueError(f"the heads of a token of {name} must be dense")
+    return x.stride(0) if x.shape[0] > 1 else heads * d
+
+
+def attn_skip_kv_append(kv, k_new, v_new, cu_seqlens, kv_len, page_table, stream=None):
+    """Write new rows k_new, v_new [total, Hkv, 128] (bf16 or fp32; the token
+    stride is free) into the cache ``kv``, quantised for its format.  Sequence
+    s's rows cu_seqlens[s] .. cu_seqlens[s+1] take the last positions below
+    kv_len[s]; int32 device tensors, page_table [n_seq, max_pages]."""
+    n_seq = _cu("cu_seqlens", cu_seqlens)
+    _int32(n_seq, page_table, kv_len=kv_len)
+    ks, vs = _token_rows("k_new", k_new, kv.Hkv, kv.d), _token_rows("v_new", v_new, kv.Hkv, kv.d)
+    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new and v_new must agree in shape and dtype")
+    dt = _dtype_code(k_new)
+    _check("attn_skip_kv_append", _paged_call(
+        kv, stream, lambda s: load().attn_skip_kv_append(
+            kv._ref, k_new.data_ptr(), v_new.data_ptr(), dt, ks, vs, n_seq, k_new.shape[0],
+            cu_seqlens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+            s), k_new, v_new, cu_seqlens, kv_len, page_table))
+
+
+def attn_skip_kv_gather(kv, cu_rows, start, page_table, total, out_dtype=torch.bfloat16, out=None,
+                        stream=None):
+    """Read rows back: positions start[s] (``None``: 0) and on of sequence s,
+    cu_rows[s+1] - cu_rows[s] of them.  Returns dense ``(k, v)`` [total, Hkv,
+    128] of ``out_dtype`` (bf16 or fp32)."""
+    n_seq = _cu("cu_rows", cu_rows)
+    _int32(n_seq, page_table, **({} if start is None else {"start": start}))
+
+    def call(s):
+        if out is None:
+            k, v = (torch.empty(total, kv.Hkv, kv.d, dtype=out_dtype, device=kv.device)
+                    for _ in range(2))
+        else:
+            k, v = out
+            if total and k.data_ptr() == v.data_ptr():
+                raise ValueError("the two outputs must be different tensors")
+            for x in out:
+                if x.shape != (total, kv.Hkv, kv.d) or x.dtype != k.dtype or not x.is_contiguous() \
+                        or x.device != kv.device:
+                    raise ValueError(f"out must be contiguous [{total}, {kv.Hkv}, {kv.d}] tensors")
+        st = load().attn_skip_kv_gather(
+            kv._ref, n_seq, total, cu_rows.data_ptr(), None if start is None else start.data_ptr(),
+            page_table.data_ptr(), page_table.shape[1], _dtype_code(k), k.data_ptr(), v.data_ptr(),
+            s)
+        _check("attn_skip_kv_gather", st)
+        return k, v
+    return _paged_call(kv, stream, call, cu_rows, page_table, *(() if start is None else (start,)))
+
+
+def attn_skip_chunk_paged_splits(kv, n_seq, total, Hq, max_chunk, max_kv):
+    """A split count for :func:`attn_skip_chunk_paged` (host only)."""
+    return load().attn_skip_chunk_paged_splits(KV_FORMATS[kv.format], n_seq, total, Hq, kv.Hkv,
+                                               max_chunk, max_kv)
+
+
+def chunk_bitmap_shape(n_seq, Hq, Hkv, max_chunk, max_kv, n_splits):
+    tt = 128 // (Hq // Hkv)
+    bps = -(-(-(-max_kv // 128)) // n_splits)
+    return (n_seq, Hkv, -(-max_chunk // tt), n_splits, -(-bps // 32))
+
+
+def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_table, lambdas,
+                          causal=True, scale=0.0, n_splits=0, with_bits=False, out=None,
+                          workspace=None, stream=None):
+    """Attention of the new tokens q [total, Hq, 128] bf16 (the token stride is
+    free) of a batch of sequences over the paged cache ``kv``, which already
+    holds their keys and values; one new token per sequence is a decode step.
+    ``max_chunk`` and ``max_kv`` bound the chunk lengths and kv_len; ``lambdas``
+    fp32 [n_seq]; ``n_splits`` 0 takes attn_skip_chunk_paged_splits' count.
+    Returns ``(o [total, Hq, 128] bf16, lse [total, Hq], skip_bits)``, skip_bits
+    ``None`` without ``with_bits``.  ``out`` may pass these three, ``workspace``
+    the partials ``(o_part [total, Hq, n_splits, 128], lse_part [total, Hq,
+    n_splits])`` fp32 of n_splits > 1."""
+    n_seq = _cu("cu_seqlens", cu_seqlens)
+    _int32(n_seq, page_table, kv_len=kv_len)
+    total, Hq, d = q.shape
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    qs = _token_rows("q", q, Hq, kv.d)
+    if lambdas.dtype != torch.float32 or lambdas.shape != (n_seq,) or not lambdas.is_contiguous():
+        raise ValueError(f"lambdas must be a contiguous float32 tensor [{n_seq}]")
+    if Hq % kv.Hkv or Hq // kv.Hkv > 128:
+        raise ValueError(f"{Hq} query heads do not fit {kv.Hkv} KV heads")
+    if n_splits == 0:
+        n_splits = attn_skip_chunk_paged_splits(kv, n_seq, total, Hq, max_chunk, max_kv)
+
+    def call(s):
+        bits = None
+        if out is not None:
+            o, lse, bits = out
+            _like("out", o, (total, Hq, d), torch.bfloat16, kv.device)
+            _like("out", lse, (total, Hq), torch.float32, kv.device)
+        else:
+            o = torch.empty(total, Hq, d, dtype=torch.bfloat16, device=kv.device)
+            lse = torch.empty(total, Hq, dtype=torch.float32, device=kv.device)
+        if with_bits and bits is None:
+            bits = torch.empty(chunk_bitmap_shape(n_seq, Hq, kv.Hkv, max_chunk, max_kv, n_splits),
+                               dtype=torch.int32, device=kv.device)
+        elif bits is not None:
+            _like("skip_bits", bits, chunk_bitmap_shape(n_seq, Hq, kv.Hkv, max_chunk, max_kv,
+                                                        n_splits), torch.int32, kv.device)
+        op = lp = None
+        if n_splits > 1:
+            if workspace is None:
+                op = torch.empty(total, Hq, n_splits, d, dtype=torch.float32, device=kv.device)
+                lp = torch.empty(total, Hq, n_splits, dtype=torch.float32, device=kv.device)
+            else:
+                op, lp = workspace
+                _like("workspace", op, (total, Hq, n_splits, d), torch.float32, kv.device)
+                _like("workspace", lp, (total, Hq, n_splits), torch.float32, kv.device)
+        st = load().attn_skip_chunk_paged(
+            kv._ref, q.data_ptr(), qs, Hq, n_seq, total, cu_seqlens.data_ptr(), max_chunk,
+            kv_len.data_ptr(), max_kv, page_table.data_ptr(), page_table.shape[1], scale,
+            lambdas.data_ptr(), int(bool(causal)), n_splits, o.data_ptr(), lse.data_ptr(),
+            None if bits is None else bits.data_ptr(), None if op is None else op.data_ptr(),
+            None if lp is None else lp.data_ptr(), s)
+        _check("attn_skip_chunk_paged", st)
+        return o, lse, bits
+    return _paged_call(kv, stream, call, q, cu_seqlens, kv_len, page_table, lambdas)
+
+
+def _like(name, x, shape, dtype, device):
+    if tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous() \
+            or x.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
 
 
 def attn_skip_selftest_wait_timeout(stream=None, device=None):

@@ -518,6 +518,155 @@ extern "C" attn_status attn_skip_selftest_wait_timeout(void *stream) {
   return from_cuda(launch_selftest_wait(err, (cudaStream_t)stream));
 }
 
+namespace attn_skip {
+namespace {
+
+constexpr int kMaxPositions = 1 << 30;  // positions of a sequence: int arithmetic in the kernels
+
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+// The checks that the paged-cache calls share; fills the kernels' view.
+attn_status pages_check(const attn_kv_pages *kv, int n_seq, int total, const int32_t *cu,
+                        const int32_t *page_table, int max_pages, KvPages &p) {
+  if (!kv || !kv->k || !kv->v || !cu || !page_table) return ATTN_EINVAL;
+  if (kv->format != ATTN_KV_BF16 && kv->format != ATTN_KV_E4M3 && kv->format != ATTN_KV_NVFP4)
+    return ATTN_EINVAL;
+  if (n_seq <= 0 || total < 0 || kv->n_pages <= 0 || kv->page_size <= 0 || kv->Hkv <= 0 ||
+      kv->d <= 0 || max_pages <= 0)
+    return ATTN_EINVAL;
+  const int ps = kv->page_size;
+  if (kv->d != 128) return ATTN_EUNSUPPORTED;
+  if (ps != 16 && ps != 32 && ps != 64 && ps % 128 != 0) return ATTN_EUNSUPPORTED;
+  if ((int64_t)max_pages * ps > kMaxPositions || ps > kMaxPositions || kv->Hkv > (1 << 16))
+    return ATTN_EUNSUPPORTED;
+  const int64_t row = kv->format == ATTN_KV_BF16 ? 256 : kv->format == ATTN_KV_E4M3 ? 128 : 64;
+  const int64_t dense = (int64_t)kv->Hkv * ps * row;
+  if (kv->page_stride != 0 && (kv->page_stride < dense || kv->page_stride % 16 != 0 ||
+                               kv->page_stride >= (int64_t)1 << 40))
+    return ATTN_EINVAL;
+  if (!aligned16(kv->k) || !aligned16(kv->v) || !aligned4(cu) || !aligned4(page_table))
+    return ATTN_EINVAL;
+  if (kv->format != ATTN_KV_BF16 && (!kv->k_scale || !kv->v_scale || !aligned16(kv->k_scale) ||
+                                     !aligned16(kv->v_scale)))
+    return ATTN_EINVAL;
+  if (kv->format == ATTN_KV_NVFP4 &&
+      (!kv->k_bs || !kv->v_bs || !aligned16(kv->k_bs) || !aligned16(kv->v_bs)))
+    return ATTN_EINVAL;
+  p.format = (int)kv->format;
+  p.n_pages = kv->n_pages; p.page_size = ps; p.Hkv = kv->Hkv;
+  p.page_stride = kv->page_stride ? kv->page_stride : dense;
+  p.k = kv->k; p.v = kv->v;
+  p.k_scale = kv->k_scale; p.v_scale = kv->v_scale;
+  p.k_bs = kv->k_bs; p.v_bs = kv->v_bs;
+  return ATTN_OK;
+}
+
+}  // namespace
+}  // namespace attn_skip
+
+extern "C" attn_status attn_skip_kv_append(const attn_kv_pages *kv, const void *k_new,
+                                           const void *v_new, attn_dtype dt,
+                                           int64_t k_tok_stride, int64_t v_tok_stride, int n_seq,
+                                           int total, const int32_t *cu_seqlens,
+                                           const int32_t *kv_len, const int32_t *page_table,
+                                           int max_pages, void *stream) {
+  KvAppendArgs a{};
+  const attn_status st =
+      pages_check(kv, n_seq, total, cu_seqlens, page_table, max_pages, a.pages);
+  if (st != ATTN_OK) return st;
+  if (!kv_len || !aligned4(kv_len) || (dt != ATTN_BF16 && dt != ATTN_F32)) return ATTN_EINVAL;
+  if (total == 0) return ATTN_OK;
+  if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return ATTN_EINVAL;
+  const int64_t dense = (int64_t)kv->Hkv * 128;
+  if (k_tok_stride < dense || v_tok_stride < dense || k_tok_stride % 8 || v_tok_stride % 8)
+    return ATTN_EINVAL;
+  if ((int64_t)total * 2 * kv->Hkv > (int64_t)0x7fffffff * 16) return ATTN_EUNSUPPORTED;
+  a.k_new = k_new; a.v_new = v_new;
+  a.k_tok_stride = k_tok_stride; a.v_tok_stride = v_tok_stride;
+  a.src_f32 = dt == ATTN_F32; a.n_seq = n_seq; a.total = total; a.max_pages = max_pages;
+  a.cu_seqlens = cu_seqlens; a.kv_len = kv_len; a.page_table = page_table;
+  const cudaError_t e = error_word(&a.err);
+  if (e != cudaSuccess) return from_cuda(e);
+  return from_cuda(launch_kv_append(a, (cudaStream_t)stream));
+}
+
+extern "C" attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
+                                           const int32_t *cu_rows, const int32_t *start,
+                                           const int32_t *page_table, int max_pages,
+                                           attn_dtype out_dt, void *k_out, void *v_out,
+                                           void *stream) {
+  KvGatherArgs a{};
+  const attn_status st = pages_check(kv, n_seq, total, cu_rows, page_table, max_pages, a.pages);
+  if (st != ATTN_OK) return st;
+  if (!aligned4(start) || (out_dt != ATTN_BF16 && out_dt != ATTN_F32)) return ATTN_EINVAL;
+  if (total == 0) return ATTN_OK;
+  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return ATTN_EINVAL;
+  if ((int64_t)total * 2 * kv->Hkv > (int64_t)0x7fffffff * 16) return ATTN_EUNSUPPORTED;
+  a.k_out = k_out; a.v_out = v_out;
+  a.out_f32 = out_dt == ATTN_F32; a.n_seq = n_seq; a.total = total; a.max_pages = max_pages;
+  a.cu_rows = cu_rows; a.start = start; a.page_table = page_table;
+  const cudaError_t e = error_word(&a.err);
+  if (e != cudaSuccess) return from_cuda(e);
+  return from_cuda(launch_kv_gather(a, (cudaStream_t)stream));
+}
+
+extern "C" int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, int total, int Hq,
+                                            int Hkv, int max_chunk, int max_kv) {
+  if (n_seq <= 0 || total <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 ||
+      max_chunk <= 0 || max_kv <= 0 || max_kv > kMaxPositions)
+    return 1;
+  return chunk_paged_splits(n_seq, total, max_chunk, max_kv, Hkv, 128 / (Hq / Hkv), (int)format);
+}
+
+extern "C" attn_status attn_skip_chunk_paged(
+    const attn_kv_pages *kv, const void *q, int64_t q_tok_stride, int Hq, int n_seq, int total,
+    const int32_t *cu_seqlens, int max_chunk, const int32_t *kv_len, int max_kv,
+    const int32_t *page_table, int max_pages, float scale, const float *lambda, int causal,
+    int n_splits, void *o, float *lse, uint32_t *skip_bits, float *o_part, float *lse_part,
+    void *stream) {
+  ChunkArgs a{};
+  const attn_status st =
+      pages_check(kv, n_seq, total, cu_seqlens, page_table, max_pages, a.pages);
+  if (st != ATTN_OK) return st;
+  if (!kv_len || !lambda || !aligned4(kv_len) || !aligned4(lambda)) return ATTN_EINVAL;
+  if (Hq <= 0 || Hq % kv->Hkv != 0 || max_chunk < 0 || max_kv < 0 || !(scale == scale))
+    return ATTN_EINVAL;
+  if (n_splits < 1 || n_splits > 1024) return ATTN_EINVAL;
+  if (max_kv > (int64_t)max_pages * kv->page_size) return ATTN_EINVAL;
+  const int G = Hq / kv->Hkv;
+  if (G > 128) return ATTN_EUNSUPPORTED;
+  if (total == 0 && max_chunk == 0) return ATTN_OK;
+  if (max_chunk == 0) return ATTN_EINVAL;
+  const int64_t nb = (max_kv + 127L) / 128;
+  a.TT = 128 / G;
+  a.n_t = (max_chunk + a.TT - 1) / a.TT;
+  a.bps = (int)((nb + n_splits - 1) / n_splits);
+  a.words = (a.bps + 31) / 32;
+  if (skip_bits && !aligned4(skip_bits)) return ATTN_EINVAL;
+  if (total == 0) {  // no new token: only the bitmap to clear
+    const size_t bytes = (size_t)n_seq * kv->Hkv * a.n_t * n_splits * a.words * 4;
+    if (!skip_bits || bytes == 0) return ATTN_OK;
+    return from_cuda(cudaMemsetAsync(skip_bits, 0, bytes, (cudaStream_t)stream));
+  }
+  if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned4(lse)) return ATTN_EINVAL;
+  if (q_tok_stride < (int64_t)Hq * 128 || q_tok_stride % 8 || q_tok_stride >= (int64_t)1 << 38)
+    return ATTN_EINVAL;
+  if (n_splits > 1 && (!o_part || !lse_part || !aligned16(o_part) || !aligned4(lse_part)))
+    return ATTN_EINVAL;
+  a.q = q; a.q_tok_stride = q_tok_stride;
+  a.o = o; a.lse = lse; a.bits = skip_bits; a.o_part = o_part; a.lse_part = lse_part;
+  a.n_seq = n_seq; a.Hq = Hq; a.Hkv = kv->Hkv; a.G = G; a.total = total;
+  a.max_chunk = max_chunk; a.max_kv = max_kv; a.max_pages = max_pages; a.causal = causal ? 1 : 0;
+  a.n_splits = n_splits;
+  a.cu_seqlens = cu_seqlens; a.kv_len = kv_len; a.page_table = page_table; a.lambda = lambda;
+  a.scale = scale > 0.f ? scale : (float)(1.0 / sqrt(128.0));
+  const cudaError_t e = error_word(&a.err);
+  if (e != cudaSuccess) return from_cuda(e);
+  if ((int64_t)total * Hq > (int64_t)0x7fffffff * 4) return ATTN_EUNSUPPORTED;
+  const cudaError_t l = launch_chunk_paged(a, (cudaStream_t)stream);
+  return l == cudaErrorNotYetImplemented ? ATTN_EUNSUPPORTED : from_cuda(l);
+}
+
 extern "C" attn_status attn_skip_last_device_error(void *stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return from_cuda(e);

@@ -1,0 +1,1065 @@
+// Attention of a chunk of new tokens over a paged key/value cache, with
+// softmax-threshold block skipping (d = 128, 128-key blocks), on tcgen05.
+//
+// Method: the BLASST page, sections "BLASST 的判定准则" (Eq. 5), "Prefill 内核：
+// 砍计算" and "Decode 内核：砍带宽"; the loop is that of the prefill kernel.  With
+// i a token of a sequence's chunk of n tokens and kv the sequence's cached
+// length (chunk included), query (i, head) sits at position p = kv - n + i and
+//     s_c = scale <q, k_c>,   c < kv,   causal: c <= p
+//     O = sum_c exp(s_c - LSE) v_c,   LSE = ln sum_c exp(s_c)   (kept blocks)
+//
+// One CTA per (tile, KV head, split).  A tile is TT = floor(128 / G)
+// consecutive tokens times the G query heads that share the KV head, so the
+// 128 rows of the products are full for chunks of any length above 128 / G and
+// every key is read once for G heads (a tile of one head's 128 tokens would
+// leave a decode step 1 row of 128).  Row r is token r / G, head r % G: one
+// TMA box of G heads x TT tokens.  A split owns bps blocks of the key axis and
+// restarts its running max; with more than one split the partial outputs are
+// merged by log-sum-exp in a second launch.
+//
+// Warp roles:
+//   0-3   deciders: row max of S_j, vote against the running max, AND;
+//   4-7   exponentials: P_j = exp2(S_j - ref) into TMEM, row sums, O rescale;
+//   8     key producer: page ids, then one copy per page (or part of a page);
+//   9     Q.K^T issuer; a bf16 cache has two (9, 12: even / odd blocks), since a
+//         thread that issues tcgen05.mma is held until the tensor pipe takes
+//         each instruction;
+//   10    value producer, kept blocks only;
+//   11    P.V issuer;
+//   12-15, 16-19 (E4M3 and NVFP4 caches) key and value converters: codes from
+//         a staging ring to bf16 tiles in the layout that TMA gives a bf16
+//         cache.  A code times its power-of-two row scale is exact in bf16, so
+//         the rest of the kernel is the same and its numerics are those of a
+//         bf16 cache that holds the read-back rows.
+// A warp quarter whose 32 rows lie past the tile's last row (decode: G rows)
+// takes part in the barriers and touches no score.
+//
+// Rows of the last block at or past kv (a page's unwritten tail, pages never
+// loaded) may hold anything: their scores are replaced by -inf and their value
+// rows by zeros in shared memory.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "internal.h"
+#include "tc_common.cuh"
+
+namespace attn_skip {
+namespace {
+
+using namespace tc;
+
+constexpr int D = 128;    // head size
+constexpr int BM = 128;   // rows of a tile
+constexpr int BN = 128;   // keys per block
+constexpr int NR = 4;     // barrier ring of the blocks (even, and longer than NS)
+constexpr int NV = 2;     // bf16 value tiles
+constexpr int NS = 3;     // TMEM S buffers
+constexpr int NDEC = 4;   // decision ring
+constexpr int NQ = 4;     // warps per row role
+constexpr int kDeciderBarrier = 1, kSetupBarrier = 2;
+constexpr int WARP_K = 8, WARP_MMA = 9, WARP_V = 10, WARP_PV = 11;
+constexpr int WARP_MMA2 = 12;             // bf16 cache
+constexpr int WARP_KC = 12, WARP_VC = 16;  // quantised caches
+constexpr uint32_t TILE_BYTES = BM * D * 2;
+constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TMEM_O = NS * BN;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.0f;  // exp reference may lag the max by 2^8
+constexpr uint32_t IDESC_QK = idesc_bf16_f32(BM, BN, 0);
+constexpr uint32_t IDESC_PV = idesc_bf16_f32(BM, D, 1);
+constexpr uint32_t NEG_INF_BITS = 0xff800000u;
+
+// Per format: bf16 key tiles (NKD), the staging rings of the quantised formats
+// (NC stages each for keys and values) and what a staged block holds.
+template <int FMT> struct Cfg;
+template <> struct Cfg<kKvBf16> {
+  static constexpr int NKD = 4, NC = 0, WARPS = 13;
+  static constexpr uint32_t ROW = 2 * D, CODES = 0, BS = 0;
+};
+template <> struct Cfg<kKvE4m3> {
+  static constexpr int NKD = 2, NC = 2, WARPS = 20;
+  static constexpr uint32_t ROW = D, CODES = BN * D, BS = 0;
+};
+template <> struct Cfg<kKvNvfp4> {
+  static constexpr int NKD = 2, NC = 3, WARPS = 20;
+  static constexpr uint32_t ROW = D / 2, CODES = BN * D / 2, BS = BN * D / 16;
+};
+template <int FMT> struct Layout {
+  using C = Cfg<FMT>;
+  static constexpr uint32_t Q = 0, K = TILE_BYTES, V = K + C::NKD * TILE_BYTES;
+  static constexpr uint32_t STAGE = FMT == kKvBf16 ? 0 : C::CODES + C::BS + BN;  // codes, block scales, row scales
+  static constexpr uint32_t KC = V + NV * TILE_BYTES, VC = KC + C::NC * STAGE;
+  static constexpr uint32_t END = VC + C::NC * STAGE;
+};
+
+struct TileInfo {
+  int s;          // sequence, -1: no tile for this CTA
+  int t;          // tile of the sequence
+  int tok0, ntok; // its first packed token, its tokens
+  int pos0;       // position of its first token
+  int kv;         // the sequence's cached length
+  int j0, nb;     // first block, blocks
+  float ln_lam;
+};
+
+struct Shared {
+  uint64_t q_full;
+  uint64_t ready[NR];    // slot c % NR: block c's key tile is in and its S buffer free
+  uint64_t qk_done[NR];  // slot c % NR: block c's Q.K^T complete
+  uint64_t v_full[NV], v_empty[NV];
+  uint64_t p_full[NS], pv_done[NS];
+  uint64_t dec_full[NDEC], dec_read[NDEC];
+  uint64_t l_full;
+  uint64_t v_tail;       // the last block's value rows, before their tail is zeroed
+  uint64_t kc_full[3], kc_empty[3], vc_full[3], vc_empty[3];
+  int dec[NDEC];
+  // [S buffer][row] running max after the buffer's block (log2 units).  Row
+  // sums and exp references for the epilogue take the first two buffers' place
+  // at the end: row r's words are read and written by its two threads alone.
+  float mdec[NS][BM];
+  TileInfo tile;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(Layout<kKvBf16>::END + sizeof(Shared) <= 227 * 1024, "shared memory budget");
+static_assert(Layout<kKvE4m3>::END + sizeof(Shared) <= 227 * 1024, "shared memory budget");
+static_assert(Layout<kKvNvfp4>::END + sizeof(Shared) <= 227 * 1024, "shared memory budget");
+static_assert(NR % 2 == 0 && NR > NS, "barrier ring: even, and longer than the S buffer ring");
+
+__device__ __forceinline__ uint64_t kmajor_base(uint32_t tile) {
+  return smem_desc_sw128(tile, 16u, 1024u);
+}
+__device__ __forceinline__ constexpr uint64_t kmajor_step(int kk) {
+  return (uint64_t)(((uint32_t)(kk >> 2) * HALF_BYTES + (uint32_t)(kk & 3) * 32u) >> 4);
+}
+__device__ __forceinline__ uint64_t vmajor_base(uint32_t tile) {
+  return smem_desc_sw128(tile, HALF_BYTES, 1024u);
+}
+__device__ __forceinline__ constexpr uint64_t vmajor_step(int kk) {
+  return (uint64_t)(((uint32_t)kk * 2048u) >> 4);
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int c0, int c1, int c2, int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "l"(policy)
+      : "memory");
+}
+
+// Keys of columns [kbase, kbase + 128) at or past the row's limit become -inf
+// in this warp's TMEM lanes; 32 keys at a time, chunks without a hidden key
+// are left alone.
+__device__ __noinline__ void mask_block_tmem(uint32_t sa, int left) {
+  uint32_t ninf[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) ninf[i] = NEG_INF_BITS;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int lim = left - 32 * c;
+    if (__all_sync(0xffffffffu, lim >= 32)) continue;
+    if (__all_sync(0xffffffffu, lim <= 0)) {
+      tmem_st32(sa + 32 * c, ninf);
+      continue;
+    }
+    uint32_t x[32];
+    tmem_ld32(sa + 32 * c, x);
+    tmem_wait_ld_regs(x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = i < lim ? x[i] : NEG_INF_BITS;
+    tmem_st32(sa + 32 * c, x);
+  }
+  tmem_wait_st();
+}
+
+__device__ __forceinline__ float chunk_max(const uint32_t (&s)[32]) {
+  float m[11];
+#pragma unroll
+  for (int i = 0; i < 10; ++i)
+    m[i] = fmax3(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]),
+                 __uint_as_float(s[3 * i + 2]));
+  m[10] = fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31]));
+  const float a = fmax3(m[0], m[1], m[2]), b = fmax3(m[3], m[4], m[5]);
+  const float c = fmax3(m[6], m[7], m[8]), d = fmaxf(m[9], m[10]);
+  return fmaxf(fmax3(a, b, c), d);
+}
+
+// P = exp2(s * sl2 - ref) for 32 keys as 16 packed bf16 pairs (the P.V
+// product's operand type; the row sum takes the unrounded fp32 values).
+__device__ __forceinline__ void chunk_exp(const uint32_t (&s)[32], uint64_t sl2x2,
+                                          uint64_t negref2, uint64_t (&acc)[2], uint32_t *pk) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x0, x1;
+    f2_split(f2_fma(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sl2x2,
+                    negref2),
+             x0, x1);
+    const float p0 = ex2(x0), p1 = ex2(x1);
+    acc[i & 1] = f2_add(acc[i & 1], f2(p0, p1));
+    pk[i] = pack_bf16x2(p0, p1);
+  }
+}
+
+// ------------------------------------------------------------- tile of a CTA --
+// Tiles run sequence by sequence, each sequence's last (longest) tile first;
+// one warp locates tile i by running sums over 32 sequences at a time.
+__device__ __noinline__ void locate(const ChunkArgs &a, int i, int split, int lane, bool report,
+                                    TileInfo *out) {
+  bool bad = false, found = false;
+  int before = 0;
+  for (int b = 0; b < a.n_seq && (report || !found); b += 32) {
+    const int s = b + lane;
+    int c0 = 0, len = 0, kv = 0;
+    float lam = 0.f;
+    if (s < a.n_seq) {
+      c0 = __ldg(a.cu_seqlens + s);
+      const int c1 = __ldg(a.cu_seqlens + s + 1);
+      kv = __ldg(a.kv_len + s);
+      lam = __ldg(a.lambda + s);
+      len = c1 - c0;
+      // Bad bounds: the sequence has no tile.  A bad cached length: an empty
+      // cache.  A bad threshold: 0.
+      if (c0 < 0 || c1 < c0 || len > a.max_chunk || c1 > a.total) { len = 0; bad = true; }
+      if (kv < 0 || kv > a.max_kv) { kv = 0; bad = true; }
+      if (!(lam >= 0.f && lam < 1.f)) { lam = 0.f; bad = true; }
+    }
+    const int nt = (len + a.TT - 1) / a.TT;
+    int upto = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    upto += before;
+    if (!found && i >= upto - nt && i < upto) {
+      TileInfo x;
+      x.s = s;
+      x.t = upto - 1 - i;
+      x.tok0 = c0 + x.t * a.TT;
+      x.ntok = min(a.TT, len - x.t * a.TT);
+      x.pos0 = kv - len + x.t * a.TT;
+      x.kv = kv;
+      // Keys that some row of the tile sees, then this split's blocks of them.
+      const int seen = a.causal ? max(0, x.pos0 + x.ntok) : kv;
+      const int blocks = (seen + BN - 1) / BN;
+      x.j0 = split * a.bps;
+      x.nb = max(0, min(blocks, x.j0 + a.bps) - x.j0);
+      x.ln_lam = lam > 0.f ? logf(lam) : -INFINITY;
+      *out = x;
+      found = true;
+    }
+    found = __any_sync(0xffffffffu, found);
+    before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (!found && lane == 0) out->s = -1;
+  if (report && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err, kErrBadArg);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------- page windows --
+// The pages of a sequence, 32 parts at a time: lane l holds the page id of part
+// base + l (a part is a page, or 128 rows of a larger page); the next 32 are
+// loaded one window ahead.  A page id out of range is reported and page 0 read
+// in its place.
+struct Pages {
+  const int32_t *table;  // the sequence's row
+  int sub, ps, n_pages, n_parts, base, cur, nxt;
+  bool bad;
+
+  __device__ __forceinline__ int load(int u) {
+    if (u >= n_parts) return 0;
+    const int id = __ldg(table + (int64_t)u * sub / ps);
+    if (id < 0 || id >= n_pages) {
+      bad = true;
+      return 0;
+    }
+    return id;
+  }
+  __device__ __forceinline__ void init(const ChunkArgs &a, const TileInfo &x, int lane) {
+    table = a.page_table + (int64_t)x.s * a.max_pages;
+    ps = a.pages.page_size;
+    sub = min(ps, BN);
+    n_pages = a.pages.n_pages;
+    n_parts = (x.kv + sub - 1) / sub;
+    bad = false;
+    base = (x.j0 * (BN / sub)) & ~31;
+    cur = load(base + lane);
+    nxt = load(base + 32 + lane);
+  }
+  // Page of part u0 + lane for lanes below the parts of a block; whole warp.
+  __device__ __forceinline__ int of_block(int u0, int lane) {
+    const int b = u0 & ~31;
+    if (b != base) {
+      cur = b == base + 32 ? nxt : load(b + lane);
+      base = b;
+      nxt = load(b + 32 + lane);
+    }
+    return __shfl_sync(0xffffffffu, cur, (u0 - b + lane) & 31);
+  }
+};
+
+// ------------------------------------------------------------- conversions --
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Four E4M3 codes as two bf16 pairs of value * 2^-120: the exponent and
+// fraction bits at the top of a bf16 fraction, which reads E4M3's subnormals
+// as bf16 subnormals.  The caller's multiplication by 2^120 * 2^e gives the
+// value (exact).
+__device__ __forceinline__ void e4m3x4_raw(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+  lo = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
+  hi = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+}
+
+// bf16 pair of 2^(e - 7) = 2^120 times the scale of byte e; NaN for 255.  Bytes
+// above 134 do not fit one bf16 factor: the rest comes as a second one.
+__device__ __forceinline__ uint32_t row_factor(uint32_t e) {
+  const uint32_t f = e == 255u ? 0x7fc0u : (min(e, 134u) + 120u) << 7;
+  return f | (f << 16);
+}
+__device__ __forceinline__ uint32_t row_factor2(uint32_t e) {
+  const uint32_t f = e > 134u && e != 255u ? (e - 7u) << 7 : 0x3f80u;
+  return f | (f << 16);
+}
+
+// Eight E2M1 codes (element 2i in byte i's low nibble) as four bf16 pairs:
+// exponent and fraction bits at the bottom of a bf16 exponent, read as value *
+// 2^-126 (0.5 as a subnormal), times 2^126.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  uint32_t p[4];  // p[k]: elements k and k + 4
+  p[0] = ((w << 6) & 0x01c001c0u) | ((w << 12) & 0x80008000u);
+  p[1] = ((w << 2) & 0x01c001c0u) | ((w << 8) & 0x80008000u);
+  p[2] = ((w >> 2) & 0x01c001c0u) | ((w << 4) & 0x80008000u);
+  p[3] = ((w >> 6) & 0x01c001c0u) | (w & 0x80008000u);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) p[k] = mul_bf16x2(p[k], 0x7e807e80u);
+  h[0] = __byte_perm(p[0], p[1], 0x5410);
+  h[1] = __byte_perm(p[2], p[3], 0x5410);
+  h[2] = __byte_perm(p[0], p[1], 0x7632);
+  h[3] = __byte_perm(p[2], p[3], 0x7632);
+}
+
+// One staged block to a bf16 tile: warp w of four takes rows 32 w .. 32 w + 31,
+// eight lanes a row (sixteen codes each).  Lanes of the upper half of a row
+// store their two 16-byte chunks in the other order, so that a store
+// instruction's eight lanes of a row meet eight different bank groups.
+// rows_left: rows at or past it become zero (values of the last block).
+template <int FMT>
+__device__ __forceinline__ void convert_block(const uint8_t *stage, uint32_t tile, int w, int lane,
+                                              int rows_left) {
+  const int cg = lane & 7, half = cg >> 2;
+  const uint8_t *scales = stage + Cfg<FMT>::CODES + Cfg<FMT>::BS;
+#pragma unroll 4
+  for (int i = 0; i < 8; ++i) {
+    const int r = w * 32 + i * 4 + (lane >> 3);
+    const uint32_t e = scales[r];
+    uint32_t h[8];
+    if constexpr (FMT == kKvE4m3) {
+      const uint4 c = *reinterpret_cast<const uint4 *>(stage + r * D + cg * 16);
+      e4m3x4_raw(c.x, h[0], h[1]);
+      e4m3x4_raw(c.y, h[2], h[3]);
+      e4m3x4_raw(c.z, h[4], h[5]);
+      e4m3x4_raw(c.w, h[6], h[7]);
+      const uint32_t f = row_factor(e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k] = mul_bf16x2(h[k], f);
+    } else {
+      const uint2 c = *reinterpret_cast<const uint2 *>(stage + r * (D / 2) + cg * 8);
+      uint32_t a[4], b[4];
+      e2m1x8(c.x, a);
+      e2m1x8(c.y, b);
+      // Block scale times row scale (at most four significant bits: exact).
+      const uint32_t s = stage[Cfg<FMT>::CODES + r * (D / 16) + cg];
+      const uint32_t f = mul_bf16x2((s & 0x7fu) * 0x00100010u, row_factor(e));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h[k] = mul_bf16x2(a[k], f);
+        h[k + 4] = mul_bf16x2(b[k], f);
+      }
+    }
+    if (__any_sync(0xffffffffu, e > 134u)) {
+      const uint32_t f2 = row_factor2(e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k] = mul_bf16x2(h[k], f2);
+    }
+    if (r >= rows_left) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k] = 0u;
+    }
+    const uint32_t row = tile + half * HALF_BYTES + r * 128;
+    const int c0 = (2 * cg) & 7;
+    const uint32_t a0 = row + ((c0 ^ (r & 7)) * 16), a1 = row + (((c0 + 1) ^ (r & 7)) * 16);
+    if (half == 0) {
+      st_shared_v4(a0, h[0], h[1], h[2], h[3]);
+      st_shared_v4(a1, h[4], h[5], h[6], h[7]);
+    } else {
+      st_shared_v4(a1, h[4], h[5], h[6], h[7]);
+      st_shared_v4(a0, h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
+    chunk_paged_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const ChunkArgs a,
+                       const int q_box_tokens) {
+  using C = Cfg<FMT>;
+  using L = Layout<FMT>;
+  constexpr bool QUANT = FMT != kKvBf16;
+  constexpr int NKD = C::NKD, NC = QUANT ? C::NC : 1;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Shared &sh = *reinterpret_cast<Shared *>(smem_raw + L::END);
+  const uint32_t base = smem_u32(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (base & 1023u) {  // the swizzled layouts need a 1024-byte aligned base
+    if (tid == 0) atomicOr(a.err, kErrLayout);
+    return;
+  }
+  const int sp = (int)(blockIdx.x % a.n_splits);
+  const int hk = (int)(blockIdx.x / a.n_splits) % a.Hkv;
+  const int ti = (int)(blockIdx.x / a.n_splits / a.Hkv);
+  volatile int *abort = &sh.abort;
+  auto bar = [&](uint64_t *b) { return smem_u32(b); };
+  auto wait = [&](uint64_t *b, int phase) {
+    return mbar_wait(smem_u32(b), phase & 1, abort, a.err, kErrTimeout);
+  };
+  auto wait_warp = [&](uint64_t *b, int phase) {
+    return mbar_wait_warp(smem_u32(b), phase & 1, abort, a.err, kErrTimeout);
+  };
+
+  const uint64_t keep_l2 = policy_evict_last();    // read again by the other tiles of the sequence
+  const uint64_t stream_l2 = policy_evict_first();  // read once
+  const uint64_t kv_pol = a.max_chunk > a.TT ? keep_l2 : stream_l2;
+  Pages pages{};  // of the producer warps
+  // One block's rows (codes and scales) into the staging area or tile at dst,
+  // part by part, one lane a part.  The arrival with the byte count comes first.
+  auto load_block = [&](bool value, int j, uint32_t dst, uint64_t *full) {
+    const int sub = pages.sub, ppb = BN / sub, u0 = j * ppb;
+    const int n = min(ppb, pages.n_parts - u0);
+    const int page = pages.of_block(u0, lane);
+    const int slot = (u0 + lane) * sub % pages.ps;
+    if (lane == 0) mbar_expect_tx(bar(full), n * sub * (C::ROW + (QUANT ? 1 + C::BS / BN : 0)));
+    __syncwarp();
+    if (lane < n) {
+      if constexpr (!QUANT) {
+        const CUtensorMap *m = value ? &tm_v : &tm_k;
+        const uint32_t d = dst + lane * sub * 128;
+        tma_load_4d(d, m, bar(full), 0, slot, hk, page, kv_pol);
+        tma_load_4d(d + HALF_BYTES, m, bar(full), 64, slot, hk, page, kv_pol);
+      } else {
+        const int64_t row = ((int64_t)page * a.Hkv + hk) * pages.ps + slot;
+        const uint8_t *src = (const uint8_t *)(value ? a.pages.v : a.pages.k) +
+                             (int64_t)page * a.pages.page_stride +
+                             ((int64_t)hk * pages.ps + slot) * C::ROW;
+        const uint32_t r0 = lane * sub;
+        bulk_load(dst + r0 * C::ROW, src, sub * C::ROW, bar(full), kv_pol);
+        if constexpr (FMT == kKvNvfp4)
+          bulk_load(dst + C::CODES + r0 * (D / 16), (value ? a.pages.v_bs : a.pages.k_bs) + row * (D / 16),
+                    sub * (D / 16), bar(full), kv_pol);
+        bulk_load(dst + C::CODES + C::BS + r0, (value ? a.pages.v_scale : a.pages.k_scale) + row, sub,
+                  bar(full), kv_pol);
+      }
+    }
+    __syncwarp();
+  };
+  auto k_dst = [&](int c) { return QUANT ? base + L::KC + (c % NC) * L::STAGE : base + L::K + (c % NKD) * TILE_BYTES; };
+  auto k_bar = [&](int c) { return QUANT ? &sh.kc_full[c % NC] : &sh.ready[c % NR]; };
+
+  // Set-up: the key producer initialises the barriers while the value
+  // producer's warp locates the tile; Q and the first keys are then in flight
+  // during the rest of the set-up.
+  constexpr int K_AHEAD = QUANT ? NC : NKD;  // key blocks that the ring holds
+  int p_c = 0;
+  if (warp == WARP_K && lane == 0) {
+    prefetch_tmap(&tm_q);
+    if constexpr (!QUANT) prefetch_tmap(&tm_k);
+    mbar_init(bar(&sh.q_full), 1);
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(bar(&sh.ready[i]), (QUANT ? 4 : 1) + 1);  // the key tile, the S buffer
+      mbar_init(bar(&sh.qk_done[i]), 1);
+    }
+    for (int i = 0; i < NS; ++i) mbar_arrive(bar(&sh.ready[i]));  // buffers free at first
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(bar(&sh.v_full[i]), QUANT ? 4 : 1);
+      mbar_init(bar(&sh.v_empty[i]), 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bar(&sh.p_full[i]), NQ);
+      mbar_init(bar(&sh.pv_done[i]), 1);
+    }
+    mbar_init(bar(&sh.l_full), NQ);
+    mbar_init(bar(&sh.v_tail), 1);
+    for (int i = 0; i < NDEC; ++i) {
+      mbar_init(bar(&sh.dec_full[i]), 1);
+      mbar_init(bar(&sh.dec_read[i]), 2 + NQ + (QUANT ? 4 : 0));
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(bar(&sh.kc_full[i]), 1);
+      mbar_init(bar(&sh.vc_full[i]), 1);
+      mbar_init(bar(&sh.kc_empty[i]), 4);
+      mbar_init(bar(&sh.vc_empty[i]), 4);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();  // the initialised barriers, seen by the TMA loads
+  }
+  if (warp == WARP_MMA) tmem_alloc(smem_u32(&sh.tmem_base), TMEM_COLS);
+  if (warp == WARP_V) {
+    if constexpr (!QUANT) {
+      if (lane == 0) prefetch_tmap(&tm_v);
+    }
+    locate(a, ti, sp, lane, blockIdx.x == 0, &sh.tile);
+  }
+  if (warp == WARP_V || warp == WARP_K) named_bar_sync(kSetupBarrier, 64);
+  if (warp == WARP_K && sh.tile.s >= 0 && sh.tile.nb > 0) {
+    const TileInfo x = sh.tile;
+    fence_proxy_async_smem();  // lane 0's barriers, for every lane's copies
+    pages.init(a, x, lane);
+    if (lane == 0) {
+      mbar_expect_tx(bar(&sh.q_full), 2 * 128 * a.G * q_box_tokens);
+      tma_load_3d(base + L::Q, &tm_q, bar(&sh.q_full), 0, hk * a.G, x.tok0, stream_l2);
+      tma_load_3d(base + L::Q + HALF_BYTES, &tm_q, bar(&sh.q_full), 64, hk * a.G, x.tok0, stream_l2);
+    }
+    __syncwarp();
+    for (; p_c < x.nb && p_c < K_AHEAD; ++p_c) load_block(false, x.j0 + p_c, k_dst(p_c), k_bar(p_c));
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;
+  const TileInfo x = sh.tile;
+  const int nb = x.nb;
+  const int rows = x.s >= 0 ? x.ntok * a.G : 0;
+
+  if (x.s < 0) {
+    // no tile for this CTA
+  } else if (nb == 0) {
+    // No visible key: O = 0, LSE = -inf (one split), or a partial of no weight.
+    for (int i = tid; i < rows * (D / 8); i += C::WARPS * 32) {
+      const int r = i / (D / 8);
+      const int64_t orow = (int64_t)(x.tok0 + r / a.G) * a.Hq + hk * a.G + r % a.G;
+      if (a.n_splits == 1)
+        reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + orow * D)[i % (D / 8)] =
+            make_uint4(0, 0, 0, 0);
+      if (i % (D / 8) == 0)
+        (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] = -INFINITY;
+    }
+  } else if (warp == WARP_K) {
+    // -------------------------------------------------------- key producer --
+    int issued = p_c;
+    for (int c = p_c; c < nb && !*abort; ++c) {
+      // The ring's slot last held block c - K_AHEAD.
+      if (!(QUANT ? wait_warp(&sh.kc_empty[c % NC], c / NC - 1)
+                  : wait_warp(&sh.qk_done[c % NR], c / NR - 1)))
+        break;
+      load_block(false, x.j0 + c, k_dst(c), k_bar(c));
+      ++issued;
+    }
+    if (__any_sync(0xffffffffu, pages.bad) && lane == 0) atomicOr(a.err, kErrBadArg);
+    if (lane == 0) {
+      // Drain: the last load of each slot has landed before exit.
+      mbar_wait_drain(bar(&sh.q_full), 0);
+      for (int s = 0; s < K_AHEAD && s < issued; ++s) {
+        const int last = s + ((issued - 1 - s) / K_AHEAD) * K_AHEAD;
+        mbar_wait_drain(bar(k_bar(s)), (last / K_AHEAD) & 1);
+      }
+    }
+  } else if (warp == WARP_V) {
+    // ------------------------------------------------------ value producer --
+    pages.init(a, x, lane);
+    int vi = 0;
+    bool tail = false;
+    for (int c = 0; c < nb && !*abort; ++c) {
+      if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) break;
+      const int keep = sh.dec[c % NDEC];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&sh.dec_read[c % NDEC]));
+      if (!keep) continue;
+      const int j = x.j0 + c;
+      if constexpr (QUANT) {
+        const int s = vi % NC;
+        if (vi >= NC && !wait_warp(&sh.vc_empty[s], vi / NC - 1)) break;
+        load_block(true, j, base + L::VC + s * L::STAGE, &sh.vc_full[s]);
+      } else {
+        const int s = vi % NV;
+        if (vi >= NV && !wait_warp(&sh.v_empty[s], vi / NV - 1)) break;
+        const uint32_t dst = base + L::V + s * TILE_BYTES;
+        const int left = x.kv - j * BN;  // rows of the block below kv
+        if (left >= BN) {
+          load_block(true, j, dst, &sh.v_full[s]);
+        } else {  // the last block of the sequence: zero the rows at or past kv
+          tail = true;
+          load_block(true, j, dst, &sh.v_tail);
+          if (!wait_warp(&sh.v_tail, 0)) break;
+          for (int i = lane; i < (BN - left) * 16; i += 32)
+            st_shared_v4(dst + (i & 8 ? HALF_BYTES : 0) + (left + (i >> 4)) * 128 + (i & 7) * 16, 0,
+                         0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&sh.v_full[s]));
+        }
+      }
+      ++vi;
+    }
+    if (lane == 0) {
+      constexpr int N = QUANT ? NC : NV;
+      if (tail) mbar_wait_drain(bar(&sh.v_tail), 0);
+      for (int s = 0; s < N && s < vi; ++s) {
+        const int last = s + ((vi - 1 - s) / N) * N;
+        mbar_wait_drain(bar(QUANT ? &sh.vc_full[s] : &sh.v_full[s]), (last / N) & 1);
+      }
+    }
+  } else if (warp == WARP_MMA || (!QUANT && warp == WARP_MMA2)) {
+    // ------------------------------------------------------ Q.K^T issuers --
+    const int mine = warp == WARP_MMA ? 0 : 1;
+    const bool ok = wait_warp(&sh.q_full, 0);
+    fence_after_sync();
+    const uint64_t qdesc = kmajor_base(base + L::Q);
+    for (int c = mine; ok && c < nb; c += QUANT ? 1 : 2) {
+      if (!wait_warp(&sh.ready[c % NR], c / NR)) break;
+      fence_after_sync();
+      if (lane == 0) {
+        const uint64_t kd = kmajor_base(base + L::K + (c % NKD) * TILE_BYTES);
+        const uint32_t d_s = tmem + (c % NS) * BN;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_ss(d_s, qdesc + kmajor_step(kk), kd + kmajor_step(kk), IDESC_QK, kk > 0);
+        mma_commit(bar(&sh.qk_done[c % NR]));
+      }
+      __syncwarp();
+    }
+  } else if (warp == WARP_PV) {
+    // ---------------------------------------------------------- P.V issuer --
+    if (lane == 0) {
+      int kc = 0;
+      for (int c = 0; c < nb && !*abort; ++c) {
+        if (!wait(&sh.dec_full[c % NDEC], c / NDEC)) break;
+        const int keep = sh.dec[c % NDEC];
+        mbar_arrive(bar(&sh.dec_read[c % NDEC]));
+        if (!keep) continue;
+        const int pb = kc % NS, vs = kc % NV;
+        if (!wait(&sh.p_full[pb], kc / NS) || !wait(&sh.v_full[vs], kc / NV)) break;
+        fence_after_sync();
+        const uint32_t pt = tmem + (c % NS) * BN;
+        const uint64_t vd = vmajor_base(base + L::V + vs * TILE_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_bf16_ts(tmem + TMEM_O, pt + kk * 8, vd + vmajor_step(kk), IDESC_PV,
+                      kk > 0 || kc > 0 ? 1u : 0u);
+        mma_commit(bar(&sh.v_empty[vs]));
+        mma_commit(bar(&sh.ready[(c + NS) % NR]));  // S buffer free for block c + NS
+        mma_commit(bar(&sh.pv_done[pb]));
+        ++kc;
+      }
+    }
+  } else if (QUANT && warp >= WARP_KC && warp < WARP_VC) {
+    // ------------------------------------------------------ key converters --
+    if constexpr (QUANT) {
+      for (int c = 0; c < nb; ++c) {
+        if (!wait_warp(&sh.kc_full[c % NC], c / NC)) break;
+        // The tile last fed block c - NKD's Q.K^T.
+        if (c >= NKD && !wait_warp(&sh.qk_done[(c - NKD) % NR], (c - NKD) / NR)) break;
+        convert_block<FMT>(smem_raw + L::KC + (c % NC) * L::STAGE, base + L::K + (c % NKD) * TILE_BYTES,
+                           warp - WARP_KC, lane, BN);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(&sh.ready[c % NR]));
+          mbar_arrive(bar(&sh.kc_empty[c % NC]));
+        }
+      }
+    }
+  } else if (QUANT && warp >= WARP_VC) {
+    // ---------------------------------------------------- value converters --
+    if constexpr (QUANT) {
+      int vi = 0;
+      for (int c = 0; c < nb && !*abort; ++c) {
+        if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) break;
+        const int keep = sh.dec[c % NDEC];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh.dec_read[c % NDEC]));
+        if (!keep) continue;
+        if (!wait_warp(&sh.vc_full[vi % NC], vi / NC)) break;
+        if (vi >= NV && !wait_warp(&sh.v_empty[vi % NV], vi / NV - 1)) break;
+        convert_block<FMT>(smem_raw + L::VC + (vi % NC) * L::STAGE, base + L::V + (vi % NV) * TILE_BYTES,
+                           warp - WARP_VC, lane, x.kv - (x.j0 + c) * BN);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(&sh.v_full[vi % NV]));
+          mbar_arrive(bar(&sh.vc_empty[vi % NC]));
+        }
+        ++vi;
+      }
+    }
+  } else {
+    // ------------------------------------------------- deciders / exponentials --
+    const bool decider = warp < NQ;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row == TMEM lane
+    const bool valid = r < rows;
+    const bool active = quarter * 32 < rows;  // the warp has a row
+    const int tok = r / a.G;
+    const int limit = a.causal && valid ? x.pos0 + tok + 1 : x.kv;  // the row sees keys below it
+    const int min_limit = a.causal ? x.pos0 + 1 : x.kv;             // the tile's smallest
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const float sl2 = a.scale * kLog2e;
+    float mref = -INFINITY, l = 0.f;
+    int kc = 0;
+    bool ok = true;
+
+    if (decider) {
+      const float c2 = x.ln_lam * kLog2e;
+      float m2 = -INFINITY;
+      uint32_t word = 0;
+      uint32_t *bits = a.bits ? a.bits + ((((int64_t)x.s * a.Hkv + hk) * a.n_t + x.t) * a.n_splits + sp) * a.words
+                              : nullptr;
+      for (int c = 0; c < nb; ++c) {
+        // After a failed wait the loop still runs to its end, so that the four
+        // warps meet the vote barrier equally often.
+        if (ok) ok = wait_warp(&sh.qk_done[c % NR], c / NR);
+        bool keep_vote = false;
+        if (ok && active) {
+          fence_after_sync();
+          const uint32_t sa = lane_base + (c % NS) * BN;
+          const int key0 = (x.j0 + c) * BN;
+          if (key0 + BN > min_limit) mask_block_tmem(sa, limit - key0);
+          float mt;
+          if constexpr (QUANT) {  // 20 warps: fewer registers a thread
+            uint32_t x0[32], x1[32];
+            tmem_ld32(sa, x0);
+            tmem_ld32(sa + 32, x1);
+            tmem_wait_ld_regs(x0);
+            tmem_wait_ld_regs(x1);
+            mt = fmaxf(chunk_max(x0), chunk_max(x1));
+            tmem_ld32(sa + 64, x0);
+            tmem_ld32(sa + 96, x1);
+            tmem_wait_ld_regs(x0);
+            tmem_wait_ld_regs(x1);
+            mt = fmax3(mt, chunk_max(x0), chunk_max(x1));
+          } else {
+            uint32_t x0[32], x1[32], x2[32], x3[32];
+            tmem_ld32(sa, x0);
+            tmem_ld32(sa + 32, x1);
+            tmem_ld32(sa + 64, x2);
+            tmem_ld32(sa + 96, x3);
+            tmem_wait_ld_regs(x0);
+            tmem_wait_ld_regs(x1);
+            tmem_wait_ld_regs(x2);
+            tmem_wait_ld_regs(x3);
+            mt = fmaxf(fmaxf(chunk_max(x0), chunk_max(x1)), fmaxf(chunk_max(x2), chunk_max(x3)));
+          }
+          const float pm2 = mt * sl2;
+          // With ln(lambda) < 0, "rowmax - m_new < c" is "rowmax - m_old < c".
+          const float diff = mt == -INFINITY ? -INFINITY : pm2 - m2;
+          keep_vote = !__all_sync(0xffffffffu, !valid || diff < c2 || mt == -INFINITY);
+          m2 = fmaxf(m2, pm2);
+          sh.mdec[c % NS][r] = m2;
+          fence_before_sync();  // this warp's reads of S_j are complete
+        }
+        const bool keep = bar_red_or(kDeciderBarrier, NQ * 32, keep_vote);
+        if (!ok) continue;
+        if (lane == 0 && warp == (c & (NQ - 1))) {
+          if (!keep) mbar_arrive(bar(&sh.ready[(c + NS) % NR]));  // its S buffer is free
+          if (c < NDEC || wait(&sh.dec_read[c % NDEC], c / NDEC - 1)) {
+            sh.dec[c % NDEC] = keep ? 1 : 0;
+            mbar_arrive(bar(&sh.dec_full[c % NDEC]));
+          }
+        }
+        if (tid == 0 && bits) {
+          if (!keep) word |= 1u << (c & 31);
+          if ((c & 31) == 31 || c == nb - 1) {
+            bits[c >> 5] = word;
+            word = 0;
+          }
+        }
+      }
+    } else {
+      for (int c = 0; c < nb; ++c) {
+        if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) {
+          ok = false;
+          break;
+        }
+        const int keep = sh.dec[c % NDEC];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh.dec_read[c % NDEC]));
+        if (!keep) continue;
+        if (active) {
+          const float mnew = sh.mdec[c % NS][r];
+          bool rescale = false;
+          float alpha = 1.f;
+          if (mref == -INFINITY) {
+            mref = mnew;
+          } else if (valid && mnew > mref + kRescaleLog2) {
+            alpha = ex2(mref - mnew);
+            mref = mnew;
+            rescale = true;
+          }
+          fence_after_sync();
+          const uint32_t sa = lane_base + (c % NS) * BN;  // masked by the deciders
+          // A row without a visible key so far has only -inf scores: P = 0.
+          const float nref = mref == -INFINITY ? 0.f : -mref;
+          const uint64_t sl2x2 = f2(sl2, sl2), negref2 = f2(nref, nref);
+          uint64_t acc2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+          if constexpr (QUANT) {
+#pragma unroll 1
+            for (int hh = 0; hh < 2; ++hh) {
+              uint32_t s[32], pk[32];
+              tmem_ld32(sa + 64 * hh, s);
+              tmem_wait_ld_regs(s);
+              chunk_exp(s, sl2x2, negref2, acc2, pk);
+              tmem_ld32(sa + 64 * hh + 32, s);
+              tmem_wait_ld_regs(s);
+              chunk_exp(s, sl2x2, negref2, acc2, pk + 16);
+              tmem_st32(sa + 32 * hh, pk);
+            }
+          } else {
+#pragma unroll 1
+            for (int hh = 0; hh < 2; ++hh) {
+              // The P pairs of keys [64 hh, 64 hh + 64) land in columns [32 hh,
+              // 32 hh + 32), whose scores this or the previous half has loaded.
+              uint32_t s0[32], s1[32], pk[32];
+              tmem_ld32(sa + 64 * hh, s0);
+              tmem_ld32(sa + 64 * hh + 32, s1);
+              tmem_wait_ld_regs(s0);
+              tmem_wait_ld_regs(s1);
+              chunk_exp(s0, sl2x2, negref2, acc2, pk);
+              chunk_exp(s1, sl2x2, negref2, acc2, pk + 16);
+              tmem_st32(sa + 32 * hh, pk);
+            }
+          }
+          tmem_wait_st();
+          float acc[4];
+          f2_split(acc2[0], acc[0], acc[1]);
+          f2_split(acc2[1], acc[2], acc[3]);
+          l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+          if (__any_sync(0xffffffffu, rescale) && kc >= 1) {
+            if (!wait_warp(&sh.pv_done[(kc - 1) % NS], (kc - 1) / NS)) {
+              ok = false;
+              break;
+            }
+            fence_after_sync();
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t o[32];
+              const uint32_t oa = lane_base + TMEM_O + cc * 32;
+              tmem_ld32(oa, o);
+              tmem_wait_ld_regs(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(oa, o);
+            }
+            tmem_wait_st();
+          }
+          fence_before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh.p_full[kc % NS]));
+        ++kc;
+      }
+      if (ok && kc > 0) ok = wait_warp(&sh.pv_done[(kc - 1) % NS], (kc - 1) / NS);
+      // No kept block: O was never written.
+      sh.mdec[0][r] = kc > 0 ? l : 0.f;
+      sh.mdec[1][r] = mref;
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&sh.l_full));
+    }
+
+    // ---- epilogue: deciders take O columns [0,64), exponential warps [64,128)
+    if (ok) ok = wait_warp(&sh.l_full, 0);
+    if (ok && active) {
+      fence_after_sync();
+      const float lrow = sh.mdec[0][r];
+      const bool empty = lrow == 0.f;  // no key kept for this row
+      const float inv = empty ? 0.f : 1.f / lrow;
+      const int col0 = decider ? 0 : 64;
+      const int64_t orow = (int64_t)(x.tok0 + tok) * a.Hq + hk * a.G + (r - tok * a.G);
+#pragma unroll 1
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(lane_base + TMEM_O + col0 + cc * 32, o);
+        tmem_wait_ld_regs(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          o[i] = empty ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+        if (!valid) continue;
+        if (a.n_splits == 1) {
+          uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + orow * D + col0 + cc * 32);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[q] = make_uint4(
+                pack_bf16x2(__uint_as_float(o[8 * q]), __uint_as_float(o[8 * q + 1])),
+                pack_bf16x2(__uint_as_float(o[8 * q + 2]), __uint_as_float(o[8 * q + 3])),
+                pack_bf16x2(__uint_as_float(o[8 * q + 4]), __uint_as_float(o[8 * q + 5])),
+                pack_bf16x2(__uint_as_float(o[8 * q + 6]), __uint_as_float(o[8 * q + 7])));
+        } else {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.o_part + (orow * a.n_splits + sp) * D + col0 + cc * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+      }
+      if (valid && !decider)
+        (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] =
+            empty ? -INFINITY : sh.mdec[1][r] * kLn2 + logf(lrow);
+    }
+  }
+
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    fence_after_sync();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Merge of the split partials: LSE = ln sum_s exp(LSE_s), O = sum_s
+// exp(LSE_s - LSE) O_s, splits without a key (LSE_s = -inf, O_s not written)
+// left out.  One warp a row (token, query head), four columns a lane; rows
+// behind the last sequence keep what they held.
+constexpr int MERGE_WARPS = 4;
+__global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const ChunkArgs a) {
+  const int64_t row = (int64_t)blockIdx.x * MERGE_WARPS + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= (int64_t)a.total * a.Hq) return;
+  const int tok = (int)(row / a.Hq);
+  // A token outside every (valid) sequence has no partial.
+  int hi = a.n_seq, lo = 0;
+  while (lo < hi) {  // entries of cu[1..n] that are <= tok
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.cu_seqlens + mid + 1) <= tok) lo = mid + 1;
+    else hi = mid;
+  }
+  if (lo >= a.n_seq) return;
+  const int c0 = __ldg(a.cu_seqlens + lo), c1 = __ldg(a.cu_seqlens + lo + 1);
+  if (c0 < 0 || c0 > tok || c1 - c0 > a.max_chunk || c1 > a.total) return;
+  const float *ls = a.lse_part + row * a.n_splits;
+  float m = -INFINITY;
+  for (int s = lane; s < a.n_splits; s += 32) m = fmaxf(m, ls[s]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float z = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 *op = reinterpret_cast<const float4 *>(a.o_part + row * a.n_splits * D) + lane;
+  for (int s = 0; s < a.n_splits; ++s) {
+    const float x = ls[s];
+    if (x == -INFINITY) continue;
+    const float w = expf(x - m);
+    const float4 v = op[s * (D / 4)];
+    z += w;
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  const float inv = m == -INFINITY ? 0.f : 1.f / z;
+  reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.o + row * D)[lane] =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : m + logf(z);
+}
+
+// 4-D map over the rows of a bf16 page pool: (column, slot, head, page).
+bool make_map_pages(CUtensorMap *m, const KvPages &p, const void *ptr) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {D, (cuuint64_t)p.page_size, (cuuint64_t)p.Hkv, (cuuint64_t)p.n_pages};
+  const cuuint64_t strides[3] = {D * 2, (cuuint64_t)p.page_size * D * 2, (cuuint64_t)p.page_stride};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(p.page_size < BN ? p.page_size : BN), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Q: (column, head, token), box 64 columns x G heads x `tokens` tokens.
+bool make_map_q(CUtensorMap *m, const ChunkArgs &a, int tokens) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {D, (cuuint64_t)a.Hq, (cuuint64_t)a.total};
+  const cuuint64_t strides[2] = {D * 2, (cuuint64_t)a.q_tok_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t tiles_bound(int n_seq, int total, int max_chunk, int TT) {
+  const int64_t by_len = (int64_t)n_seq * ((max_chunk + TT - 1) / TT);
+  const int64_t by_total = (int64_t)(total + TT - 1) / TT + n_seq;
+  return by_len < by_total ? by_len : by_total;
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                       const ChunkArgs &a, int q_tokens, unsigned grid, cudaStream_t s) {
+  constexpr uint32_t smem = Layout<FMT>::END + ((sizeof(Shared) + 15) / 16) * 16;
+  cudaError_t e = cudaFuncSetAttribute(chunk_paged_kernel<FMT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  chunk_paged_kernel<FMT><<<grid, Cfg<FMT>::WARPS * 32, smem, s>>>(mq, mk, mv, a, q_tokens);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// The split count that a host-side model of the launch finds cheapest: waves of
+// one CTA an SM, each a set-up and its share of the blocks.
+int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv, int TT, int format) {
+  const int sms = 152;
+  const int64_t units = tiles_bound(n_seq, total, max_chunk, TT) * Hkv;
+  const int nb = (max_kv + BN - 1) / BN;
+  const double block_us = format == kKvBf16 ? 1.2 : 0.8, setup_us = 4.0, merge_us = 3.0;
+  int best = 1;
+  double best_t = 0;
+  for (int n = 1; n <= 64 && n <= (nb > 0 ? nb : 1); ++n) {
+    const int bps = (nb + n - 1) / n;
+    if (n > 1 && (nb + bps - 1) / bps < n) continue;  // the last splits would be empty
+    const int64_t waves = (units * n + sms - 1) / sms;
+    const double t = waves * (setup_us + bps * block_us) + (n > 1 ? merge_us : 0);
+    if (n == 1 || t < best_t) {
+      best = n;
+      best_t = t;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_chunk_paged(const ChunkArgs &a, cudaStream_t s) {
+  const int64_t units = tiles_bound(a.n_seq, a.total, a.max_chunk, a.TT) * a.Hkv * a.n_splits;
+  if (units > 0x7fffffffL) return cudaErrorNotYetImplemented;  // more CTAs than a grid has
+  CUtensorMap mq, mk{}, mv{};
+  const int q_tokens = a.TT < a.max_chunk ? a.TT : a.max_chunk;
+  if (!make_map_q(&mq, a, q_tokens)) return cudaErrorInvalidValue;
+  if (a.pages.format == kKvBf16 &&
+      (!make_map_pages(&mk, a.pages, a.pages.k) || !make_map_pages(&mv, a.pages, a.pages.v)))
+    return cudaErrorInvalidValue;
+  if (a.bits) {  // words of tiles that a sequence does not have, and of untraversed blocks
+    const cudaError_t e = cudaMemsetAsync(
+        a.bits, 0, (size_t)a.n_seq * a.Hkv * a.n_t * a.n_splits * a.words * 4, s);
+    if (e != cudaSuccess) return e;
+  }
+  const unsigned grid = (unsigned)units;
+  cudaError_t e = a.pages.format == kKvBf16   ? launch_fmt<kKvBf16>(mq, mk, mv, a, q_tokens, grid, s)
+                  : a.pages.format == kKvE4m3 ? launch_fmt<kKvE4m3>(mq, mk, mv, a, q_tokens, grid, s)
+                                              : launch_fmt<kKvNvfp4>(mq, mk, mv, a, q_tokens, grid, s);
+  if (e != cudaSuccess || a.n_splits == 1) return e;
+  const int64_t rows = (int64_t)a.total * a.Hq;
+  merge_kernel<<<(unsigned)((rows + MERGE_WARPS - 1) / MERGE_WARPS), MERGE_WARPS * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace attn_skip

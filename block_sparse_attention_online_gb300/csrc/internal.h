@@ -89,6 +89,57 @@ struct CombineArgs {
   int out_bf16;
 };
 
+// The paged key/value cache (the fields of attn_kv_pages, checked).
+enum : int { kKvBf16 = 0, kKvE4m3 = 1, kKvNvfp4 = 2 };
+
+struct KvPages {
+  int format, n_pages, page_size, Hkv;
+  int64_t page_stride;        // bytes from page to page in k and v
+  void *k, *v;                // rows [n_pages][Hkv][page_size]
+  uint8_t *k_scale, *v_scale; // E8M0 row scales [n_pages][Hkv][page_size]
+  uint8_t *k_bs, *v_bs;       // NVFP4: E4M3 block scales [n_pages][Hkv][page_size][8]
+};
+
+struct KvAppendArgs {
+  KvPages pages;
+  const void *k_new, *v_new;           // [total][Hkv][128], tokens *_tok_stride elements apart
+  int64_t k_tok_stride, v_tok_stride;
+  int src_f32, n_seq, total, max_pages;
+  const int32_t *cu_seqlens, *kv_len, *page_table;
+  unsigned *err;
+};
+
+struct KvGatherArgs {
+  KvPages pages;
+  void *k_out, *v_out;                 // [total][Hkv][128]
+  int out_f32, n_seq, total, max_pages;
+  const int32_t *cu_rows, *start, *page_table;
+  unsigned *err;
+};
+
+// Attention of a chunk of new tokens per sequence over the paged cache.
+struct ChunkArgs {
+  KvPages pages;
+  const void *q;                       // bf16 [total][Hq][128], tokens q_tok_stride elements apart
+  int64_t q_tok_stride;
+  void *o;                             // bf16 [total][Hq][128]
+  float *lse;                          // [total][Hq]
+  uint32_t *bits;                      // [n_seq][Hkv][n_t][n_splits][words], or null
+  float *o_part, *lse_part;            // [total][Hq][n_splits][128] / [..][n_splits] (n_splits > 1)
+  int n_seq, Hq, Hkv, G, TT;           // TT: tokens per tile, floor(128 / G)
+  int total, max_chunk, max_kv, max_pages, causal;
+  int n_splits, bps, n_t, words;       // bps: blocks per split
+  const int32_t *cu_seqlens, *kv_len, *page_table;
+  const float *lambda;
+  float scale;
+  unsigned *err;
+};
+
+cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
+cudaError_t launch_kv_gather(const KvGatherArgs &a, cudaStream_t s);
+cudaError_t launch_chunk_paged(const ChunkArgs &a, cudaStream_t s);
+int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv, int TT, int format);
+
 cudaError_t launch_prefill_f32(const PrefillArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t s);
 cudaError_t launch_decode_bf16(const DecodeArgs &a, cudaStream_t s);

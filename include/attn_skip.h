@@ -501,6 +501,160 @@ attn_status attn_skip_santa_decode_noalloc(const void *q, const void *k, const v
                                            void *o, int32_t *idx, void *stream);
 
 /*
+ * Paged key/value cache: pages of page_size rows per KV head, shared by the
+ * sequences of a batch through a page table.  The pages have no counterpart on
+ * the BLASST page, which takes the cache as given; they are how a serving loop
+ * keeps sequences that grow.
+ *
+ * A row is the 128 elements of one (token, KV head).  Formats:
+ *   ATTN_KV_BF16   128 bf16 values (256 bytes)
+ *   ATTN_KV_E4M3   128 E4M3 codes (128 bytes) and a row scale
+ *   ATTN_KV_NVFP4  128 E2M1 codes, element 2i in byte i's low nibble (64
+ *                  bytes), 8 E4M3 block scales (one per 16 elements) and a
+ *                  row scale
+ * A row scale is one byte b (E8M0): 2^(b - 127), and 255 makes the whole row
+ * NaN.  Element = 2^(b - 127) * E4M3(code), or 2^(b - 127) * E4M3(block scale)
+ * * E2M1(code).  A scale that is a power of two keeps every stored element
+ * exact in bf16 (at most 4, or 6, significant bits), for scale bytes of 17 and
+ * above; codes and block scales hold no E4M3 NaN.
+ *
+ *  k, v         first row of page 0; row (slot r, head h) of a page at
+ *               (h * page_size + r) * row bytes, pages page_stride bytes apart
+ *               (0: dense, Hkv * page_size rows).  One allocation may hold k
+ *               and v of a page next to each other.  16-byte aligned.
+ *  k_scale, v_scale  [n_pages, Hkv, page_size] bytes (not for ATTN_KV_BF16)
+ *  k_bs, v_bs        [n_pages, Hkv, page_size, 8] bytes (ATTN_KV_NVFP4 only)
+ *  page_size    16, 32, 64 or a multiple of 128; d = 128
+ * Page tables are int32 [n_seq, max_pages] on the device: position p of
+ * sequence s is slot p % page_size of page page_table[s, p / page_size].
+ * Entries behind a sequence's last position are not read.
+ */
+typedef enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1, ATTN_KV_NVFP4 = 2 } attn_kv_format;
+
+typedef struct {
+  attn_kv_format format;
+  int n_pages, page_size, Hkv, d;
+  int64_t page_stride;
+  void *k, *v;
+  uint8_t *k_scale, *v_scale;
+  uint8_t *k_bs, *v_bs;
+} attn_kv_pages;
+
+/*
+ * Write new key and value rows into the cache, quantising them on the way.
+ *
+ * With x a row in fp32 and top = 448 (E4M3) or 6 * 448 (NVFP4), the row scale
+ * is the smallest 2^e with max|x| <= top * 2^e, e clamped to [-110, 120]
+ * (e = 0 for a row of zeros).  E4M3: code = x / 2^e rounded to nearest even.
+ * NVFP4: with y = x / 2^e, the block scale b is the smallest E4M3 value with
+ * 6 b >= max|y| over the 16 elements, code = E2M1(y / b) rounded to nearest
+ * even.  A row with an infinity or a NaN is stored as a NaN row (scale byte
+ * 255, codes 0).  ATTN_KV_BF16 rounds fp32 rows to nearest even and keeps
+ * bf16 rows, whatever they hold.
+ *
+ *  k_new, v_new  [total, Hkv, 128] (dt: ATTN_BF16 or ATTN_F32), tokens
+ *                k_tok_stride / v_tok_stride elements apart (multiples of 8;
+ *                slices of one fused projection are fine)
+ *  cu_seqlens    [n_seq + 1] int32 (device): sequence s's new tokens are rows
+ *                [cu_seqlens[s], cu_seqlens[s+1]); rows from cu_seqlens[n_seq]
+ *                on are ignored
+ *  kv_len        [n_seq] int32 (device): cached length with the new tokens;
+ *                the n new tokens take positions kv_len - n .. kv_len - 1
+ *                (a position below 0, of a chunk longer than kv_len, is not
+ *                written)
+ * No other row of the cache changes.  Two new rows that name the same slot (a
+ * page that two sequences share and both write) leave a mixture there.
+ * EINVAL: a null pointer that the format needs, n_seq <= 0, total < 0, a bad
+ * size, stride or alignment (16 bytes, 4 for int32 arrays).  The device arrays
+ * are checked by the kernel: nothing is written for a sequence whose bounds or
+ * length are out of range (kv_len above max_pages * page_size among them) nor
+ * for a page id outside [0, n_pages), and attn_skip_last_device_error then
+ * returns ATTN_EINVAL.  total = 0 launches nothing.
+ */
+attn_status attn_skip_kv_append(const attn_kv_pages *kv, const void *k_new, const void *v_new,
+                                attn_dtype dt, int64_t k_tok_stride, int64_t v_tok_stride,
+                                int n_seq, int total, const int32_t *cu_seqlens,
+                                const int32_t *kv_len, const int32_t *page_table, int max_pages,
+                                void *stream);
+
+/*
+ * Read rows of the cache back: positions start[s] .. start[s] + n - 1 of
+ * sequence s, n = cu_rows[s+1] - cu_rows[s], as dense rows.  Exact for fp32
+ * outputs and, for quantised formats, for bf16 outputs too (a stored element
+ * has at most 6 significant bits).
+ *
+ *  cu_rows  [n_seq + 1] int32 (device), start [n_seq] int32 (device) or NULL
+ *           (all 0)
+ *  k_out, v_out  [total, Hkv, 128] (out_dt); rows from cu_rows[n_seq] on stay
+ *           as they were
+ * Errors as for attn_skip_kv_append; a position outside [0, max_pages *
+ * page_size), of a page id out of range or of a sequence with bad bounds reads
+ * as zeros and is reported by attn_skip_last_device_error (ATTN_EINVAL).
+ */
+attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
+                                const int32_t *cu_rows, const int32_t *start,
+                                const int32_t *page_table, int max_pages, attn_dtype out_dt,
+                                void *k_out, void *v_out, void *stream);
+
+/*
+ * Attention of a chunk of new tokens per sequence over the paged cache, with
+ * block skipping: chunked prefill (n new tokens on top of a cached prefix),
+ * drafted tokens, and decode (n = 1), ragged over the batch.
+ *
+ * Defines: the loop of attn_skip_prefill (sections "BLASST 的判定准则", "Prefill
+ * 内核：砍计算", "Decode 内核：砍带宽") on query tiles that hold G = Hq / Hkv
+ * heads times TT = floor(128 / G) consecutive tokens of a chunk, keys in blocks
+ * of 128 positions.  Query i of a chunk of n sits at position kv_len - n + i;
+ * causal: key c is visible iff c <= that position, else iff c < kv_len.  The
+ * block axis is cut into n_splits ranges of bps = ceil(ceil(max_kv / 128) /
+ * n_splits) blocks; each restarts its running max (FlashDecoding) and the
+ * results are merged by log-sum-exp.  A tile skips a block of its split when
+ * rowmax - m_new < ln(lambda) for all its rows.  A row that sees no key gets
+ * O = 0, LSE = -inf.
+ *
+ *  q           [total, Hq, 128] bf16, tokens q_tok_stride elements apart (a
+ *              multiple of 8); query head h reads KV head h / G, 1 <= G <= 128
+ *  cu_seqlens  [n_seq + 1], kv_len [n_seq] int32 (device): as for
+ *              attn_skip_kv_append, whose rows are in the cache by now
+ *  max_chunk, max_kv  host bounds on the chunk lengths and on kv_len;
+ *              max_kv <= max_pages * page_size
+ *  lambda      [n_seq] fp32 (device), each in [0, 1); 0 = dense
+ *  n_splits    1 .. 1024.  attn_skip_chunk_paged_splits proposes a count (it
+ *              has no influence on the result at lambda = 0 beyond rounding)
+ *  o           [total, Hq, 128] bf16, lse [total, Hq] fp32: written for the
+ *              rows of the sequences, others stay as they were
+ *  skip_bits   [n_seq, Hkv, ceil(max_chunk / TT), n_splits, ceil(bps / 32)]
+ *              uint32 or NULL: bit p of split s is block s * bps + p; every
+ *              word is written
+ *  o_part, lse_part  workspace of total * Hq * n_splits * 128 and total * Hq *
+ *              n_splits floats for n_splits > 1 (else NULL is fine); calls
+ *              that overlap on the GPU need their own
+ * A quantised cache is widened to bf16 on the chip (exact), products
+ * accumulate in fp32, P is rounded to bf16 for the P.V product; statistics
+ * are fp32.  Cache rows at or past kv_len may hold anything.  A value row that
+ * is not finite, and in sight of some row of a tile, reaches every row of it.
+ * EINVAL as for attn_skip_kv_append, for max_chunk or max_kv < 0 or beyond the
+ * page table and for n_splits out of range; head size or G out of range are
+ * EUNSUPPORTED.  Checked by the kernel and reported by
+ * attn_skip_last_device_error (ATTN_EINVAL): a sequence with bad bounds (its
+ * rows are not written), a kv_len outside [0, max_kv] (treated as 0), a lambda
+ * outside [0, 1) (treated as 0), a page id outside [0, n_pages) (page 0 is
+ * read in its place: the sequence's outputs mean nothing).
+ */
+attn_status attn_skip_chunk_paged(const attn_kv_pages *kv, const void *q, int64_t q_tok_stride,
+                                  int Hq, int n_seq, int total, const int32_t *cu_seqlens,
+                                  int max_chunk, const int32_t *kv_len, int max_kv,
+                                  const int32_t *page_table, int max_pages, float scale,
+                                  const float *lambda, int causal, int n_splits, void *o,
+                                  float *lse, uint32_t *skip_bits, float *o_part,
+                                  float *lse_part, void *stream);
+
+/* A split count for attn_skip_chunk_paged (host only; 1 for sizes that the call
+ * itself refuses). */
+int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, int total, int Hq, int Hkv,
+                                 int max_chunk, int max_kv);
+
+/*
  * Diagnostic: launches one small CTA that allocates TMEM and then waits, with
  * the same bounded wait as every kernel, on an mbarrier phase that nothing
  * completes.  After the 1 s limit the wait gives up, the CTA raises its abort
@@ -514,7 +668,7 @@ attn_status attn_skip_selftest_wait_timeout(void *stream);
  * Synchronises `stream`, then reads and clears the current device's error
  * word: ATTN_ETIMEOUT if a kernel gave up a bounded wait since the last read,
  * ATTN_EINVAL if a kernel found a device-side argument out of range (the
- * varlen lengths and thresholds), ATTN_EINTERNAL if a kernel found its shared
+ * varlen and paged-cache lengths, page ids and thresholds), ATTN_EINTERNAL if a kernel found its shared
  * memory misaligned, ATTN_ECUDA on a CUDA error, else ATTN_OK.
  */
 attn_status attn_skip_last_device_error(void *stream);
