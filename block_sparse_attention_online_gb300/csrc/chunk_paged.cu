@@ -27,10 +27,20 @@
 //   10    value producer, kept blocks only;
 //   11    P.V issuer;
 //   12-15, 16-19 (E4M3 and NVFP4 caches) key and value converters: codes from
-//         a staging ring to bf16 tiles in the layout that TMA gives a bf16
-//         cache.  A code times its power-of-two row scale is exact in bf16, so
-//         the rest of the kernel is the same and its numerics are those of a
-//         bf16 cache that holds the read-back rows.
+//         a staging ring to fp16 tiles in the layout that TMA gives a bf16
+//         cache; before that, Q to fp16.
+//
+// Quantised caches.  cvt widens two codes to fp16 in one instruction, at the
+// rate of any other; a bf16 pair takes five.  fp16's range is met by exponents
+// that cost nothing per score: with E_k and E_v the largest row-scale exponents
+// of a block's keys and values, the tiles hold code * 2^(e - E) (exact for e >=
+// E - 15, otherwise off by at most 2^-25 2^E), the scores of the block are
+// scaled by 2^E_k, and P takes 2^E_v: P'_c = 2^(s_c + E_v - ref), with ref the
+// running max of (row max + E_v) over the blocks, so P' stays in fp16's range
+// and its smallest step, 2^-24, is that fraction of the largest contribution;
+// the row sum takes sum P' * 2^-E_v.  A query row enters as fp16(q * 2^x), 2^x
+// the largest power of two with max|q| 2^x <= 2^15.
+//
 // A warp quarter whose 32 rows lie past the tile's last row (decode: G rows)
 // takes part in the barriers and touches no score.
 //
@@ -56,6 +66,7 @@ constexpr int NR = 4;     // barrier ring of the blocks (even, and longer than N
 constexpr int NV = 2;     // bf16 value tiles
 constexpr int NS = 3;     // TMEM S buffers
 constexpr int NDEC = 4;   // decision ring
+constexpr int NE = 8;     // scale exponent ring of the quantised formats
 constexpr int NQ = 4;     // warps per row role
 constexpr int kDeciderBarrier = 1, kSetupBarrier = 2;
 constexpr int WARP_K = 8, WARP_MMA = 9, WARP_V = 10, WARP_PV = 11;
@@ -70,6 +81,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;  // exp reference may lag the max by 2^8
 constexpr uint32_t IDESC_QK = idesc_bf16_f32(BM, BN, 0);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(BM, D, 1);
+constexpr uint32_t IDESC_QK16 = idesc_f16_f32(BM, BN, 0);
+constexpr uint32_t IDESC_PV16 = idesc_f16_f32(BM, D, 1);
 constexpr uint32_t NEG_INF_BITS = 0xff800000u;
 
 // Per format: bf16 key tiles (NKD), the staging rings of the quantised formats
@@ -90,9 +103,11 @@ template <> struct Cfg<kKvNvfp4> {
 template <int FMT> struct Layout {
   using C = Cfg<FMT>;
   static constexpr uint32_t Q = 0, K = TILE_BYTES, V = K + C::NKD * TILE_BYTES;
-  static constexpr uint32_t STAGE = FMT == kKvBf16 ? 0 : C::CODES + C::BS + BN;  // codes, block scales, row scales
-  static constexpr uint32_t KC = V + NV * TILE_BYTES, VC = KC + C::NC * STAGE;
-  static constexpr uint32_t END = VC + C::NC * STAGE;
+  // A staged block: codes, block scales, row scales; a key block's stage also
+  // holds the row scales of its values (needed before the values are).
+  static constexpr uint32_t SCALES = C::CODES + C::BS, KSTAGE = SCALES + 2 * BN, VSTAGE = SCALES + BN;
+  static constexpr uint32_t KC = V + NV * TILE_BYTES, VC = KC + C::NC * KSTAGE;
+  static constexpr uint32_t END = VC + C::NC * VSTAGE;
 };
 
 struct TileInfo {
@@ -102,7 +117,7 @@ struct TileInfo {
   int pos0;       // position of its first token
   int kv;         // the sequence's cached length
   int j0, nb;     // first block, blocks
-  float ln_lam;
+  float ln_lam;   // -inf: dense, every block is kept
 };
 
 struct Shared {
@@ -115,7 +130,13 @@ struct Shared {
   uint64_t l_full;
   uint64_t v_tail;       // the last block's value rows, before their tail is zeroed
   uint64_t kc_full[3], kc_empty[3], vc_full[3], vc_empty[3];
+  uint64_t q_ready;      // Q as fp16
   int dec[NDEC];
+  // Scale bytes (E_k, E_v) of block c, slot c % NE.  Slot reuse: block c + NE is
+  // converted after block c + NE - NKD's Q.K^T, whose S buffer was block c +
+  // NE - NKD - NS's (NE - NKD - NS > 0), by then read by everyone.
+  uint16_t esc[NE];
+  int8_t qexp[BM];       // x of the query rows
   // [S buffer][row] running max after the buffer's block (log2 units).  Row
   // sums and exp references for the epilogue take the first two buffers' place
   // at the end: row r's words are read and written by its two threads alone.
@@ -140,6 +161,36 @@ __device__ __forceinline__ uint64_t vmajor_base(uint32_t tile) {
 }
 __device__ __forceinline__ constexpr uint64_t vmajor_step(int kk) {
   return (uint64_t)(((uint32_t)kk * 2048u) >> 4);
+}
+
+// The bounded waits of the other kernels, but a thread that finds its phase
+// incomplete sleeps in the barrier unit, for up to 20 us a try, instead of
+// asking again at once: most of the twenty warps wait most of the time, and the
+// converters need the issue slots.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, volatile int *abort,
+                                                unsigned *err) {
+  if (mbar_sleep(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    if (mbar_sleep(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicOr(err, kErrTimeout);
+      return false;
+    }
+  }
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
@@ -189,8 +240,9 @@ __device__ __forceinline__ float chunk_max(const uint32_t (&s)[32]) {
   return fmaxf(fmax3(a, b, c), d);
 }
 
-// P = exp2(s * sl2 - ref) for 32 keys as 16 packed bf16 pairs (the P.V
-// product's operand type; the row sum takes the unrounded fp32 values).
+// P = exp2(s * sl2 - ref) for 32 keys as 16 packed bf16 (fp16) pairs, the P.V
+// product's operand type; the row sum takes the unrounded fp32 values.
+template <bool F16>
 __device__ __forceinline__ void chunk_exp(const uint32_t (&s)[32], uint64_t sl2x2,
                                           uint64_t negref2, uint64_t (&acc)[2], uint32_t *pk) {
 #pragma unroll
@@ -201,7 +253,7 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&s)[32], uint64_t sl2x
              x0, x1);
     const float p0 = ex2(x0), p1 = ex2(x1);
     acc[i & 1] = f2_add(acc[i & 1], f2(p0, p1));
-    pk[i] = pack_bf16x2(p0, p1);
+    pk[i] = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
   }
 }
 
@@ -304,107 +356,180 @@ struct Pages {
 };
 
 // ------------------------------------------------------------- conversions --
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-
-// Four E4M3 codes as two bf16 pairs of value * 2^-120: the exponent and
-// fraction bits at the top of a bf16 fraction, which reads E4M3's subnormals
-// as bf16 subnormals.  The caller's multiplication by 2^120 * 2^e gives the
-// value (exact).
-__device__ __forceinline__ void e4m3x4_raw(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-  lo = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
-  hi = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+// Four E4M3 codes as two fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
-
-// bf16 pair of 2^(e - 7) = 2^120 times the scale of byte e; NaN for 255.  Bytes
-// above 134 do not fit one bf16 factor: the rest comes as a second one.
-__device__ __forceinline__ uint32_t row_factor(uint32_t e) {
-  const uint32_t f = e == 255u ? 0x7fc0u : (min(e, 134u) + 120u) << 7;
-  return f | (f << 16);
-}
-__device__ __forceinline__ uint32_t row_factor2(uint32_t e) {
-  const uint32_t f = e > 134u && e != 255u ? (e - 7u) << 7 : 0x3f80u;
-  return f | (f << 16);
-}
-
-// Eight E2M1 codes (element 2i in byte i's low nibble) as four bf16 pairs:
-// exponent and fraction bits at the bottom of a bf16 exponent, read as value *
-// 2^-126 (0.5 as a subnormal), times 2^126.
+// Eight E2M1 codes (element 2i in byte i's low nibble) as four fp16 pairs (exact).
 __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
-  uint32_t p[4];  // p[k]: elements k and k + 4
-  p[0] = ((w << 6) & 0x01c001c0u) | ((w << 12) & 0x80008000u);
-  p[1] = ((w << 2) & 0x01c001c0u) | ((w << 8) & 0x80008000u);
-  p[2] = ((w >> 2) & 0x01c001c0u) | ((w << 4) & 0x80008000u);
-  p[3] = ((w >> 6) & 0x01c001c0u) | (w & 0x80008000u);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) p[k] = mul_bf16x2(p[k], 0x7e807e80u);
-  h[0] = __byte_perm(p[0], p[1], 0x5410);
-  h[1] = __byte_perm(p[2], p[3], 0x5410);
-  h[2] = __byte_perm(p[0], p[1], 0x7632);
-  h[3] = __byte_perm(p[2], p[3], 0x7632);
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
 
-// One staged block to a bf16 tile: warp w of four takes rows 32 w .. 32 w + 31,
-// eight lanes a row (sixteen codes each).  Lanes of the upper half of a row
-// store their two 16-byte chunks in the other order, so that a store
+// fp16 pair of 2^(byte - top): 1 for a row of zeros above the block's top, 0
+// below 2^-24, NaN for byte 255.
+__device__ __forceinline__ uint32_t row_factor(int byte, int top) {
+  const int r = min(byte - top, 0);
+  uint32_t f = r >= -14 ? (uint32_t)(r + 15) << 10 : r >= -24 ? 1u << (r + 24) : 0u;
+  if (byte == 255) f = 0x7e00u;
+  return f | (f << 16);
+}
+
+// The largest scale byte of a block's rows below `left`; whole warp, lane l
+// brings the bytes of rows 4 l .. 4 l + 3.  Rows of byte 255 (NaN) do not count,
+// nor, where the bytes are too far apart for one exponent to serve, rows of
+// zeros, which the writer gives byte 127: their codes are looked up in the
+// cache (not in the staging area: a block's values come after its scales).
+template <int FMT>
+__device__ __noinline__ int block_top_slow(const ChunkArgs &a, const TileInfo &x, int hk, int j,
+                                           bool value, const uint8_t *scales, int lane, int left) {
+  const KvPages &p = a.pages;
+  int top = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * lane + i;
+    if (r >= left || scales[r] == 255) continue;
+    uint32_t any = 1;
+    if (scales[r] == 127) {
+      const int pos = j * BN + r;
+      int page = __ldg(a.page_table + (int64_t)x.s * a.max_pages + pos / p.page_size);
+      if (page < 0 || page >= p.n_pages) page = 0;
+      const uint4 *c = reinterpret_cast<const uint4 *>(
+          (const uint8_t *)(value ? p.v : p.k) + page * p.page_stride +
+          ((int64_t)hk * p.page_size + pos % p.page_size) * Cfg<FMT>::ROW);
+      any = 0;
+      for (uint32_t k = 0; k < Cfg<FMT>::ROW / 16; ++k) {
+        const uint4 w = __ldg(c + k);
+        any |= w.x | w.y | w.z | w.w;
+      }
+      any &= FMT == kKvE4m3 ? 0x7f7f7f7fu : 0x77777777u;
+    }
+    if (any) top = max(top, (int)scales[r]);
+  }
+  top = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
+  return top ? top : 127;
+}
+
+template <int FMT>
+__device__ __forceinline__ int block_top(const ChunkArgs &a, const TileInfo &x, int hk, int j,
+                                         bool value, const uint8_t *scales, int lane) {
+  const uint32_t w = reinterpret_cast<const uint32_t *>(scales)[lane];
+  const int left = x.kv - j * BN, mine = left - 4 * lane;  // rows that count: the block's, this lane's
+  const uint32_t mask = mine >= 4 ? 0xffffffffu : mine <= 0 ? 0u : (1u << (8 * mine)) - 1u;
+  const uint32_t u = w & mask, v = w | ~mask;
+  const uint32_t hi = max(max(u & 255u, (u >> 8) & 255u), max((u >> 16) & 255u, u >> 24));
+  const uint32_t lo = min(min(v & 255u, (v >> 8) & 255u), min((v >> 16) & 255u, v >> 24));
+  const int top = (int)__reduce_max_sync(0xffffffffu, hi);
+  const int low = (int)__reduce_min_sync(0xffffffffu, lo);
+  if (top < 255 && top - low <= 15) return top;
+  return block_top_slow<FMT>(a, x, hk, j, value, scales, lane, left);
+}
+
+// One staged block to an fp16 tile: warp w of four takes rows 32 w .. 32 w + 31,
+// eight lanes a row (sixteen codes each).  All codes are read before the first
+// store (a store orders every later load behind it).  Lane l forms the factor
+// of row 32 w + l; a row's lanes fetch it by a shuffle.  Lanes of the upper half
+// of a row store their two 16-byte chunks in the other order, so that a store
 // instruction's eight lanes of a row meet eight different bank groups.
 // rows_left: rows at or past it become zero (values of the last block).
 template <int FMT>
 __device__ __forceinline__ void convert_block(const uint8_t *stage, uint32_t tile, int w, int lane,
-                                              int rows_left) {
-  const int cg = lane & 7, half = cg >> 2;
-  const uint8_t *scales = stage + Cfg<FMT>::CODES + Cfg<FMT>::BS;
-#pragma unroll 4
+                                              int top, int rows_left) {
+  const int cg = lane & 7, rl = lane >> 3;
+  const bool upper = cg >= 4;
+  const uint32_t fl = row_factor(stage[Layout<FMT>::SCALES + w * 32 + lane], top);
+  uint4 c[8];
+  uint32_t bsc[8];
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int r = w * 32 + i * 4 + (lane >> 3);
-    const uint32_t e = scales[r];
+    const int r = w * 32 + i * 4 + rl;
+    if constexpr (FMT == kKvE4m3) {
+      c[i] = *reinterpret_cast<const uint4 *>(stage + r * D + cg * 16);
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2 *>(stage + r * (D / 2) + cg * 8);
+      c[i].x = v.x;
+      c[i].y = v.y;
+      bsc[i] = stage[Cfg<FMT>::CODES + r * (D / 16) + cg];
+    }
+  }
+  const uint32_t row0 = tile + (upper ? HALF_BYTES : 0) + (w * 32 + rl) * 128;
+  const int c0 = (2 * cg) & 7;  // 16-byte chunk c of row r sits at c ^ (r % 8)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t f = __shfl_sync(0xffffffffu, fl, i * 4 + rl);
     uint32_t h[8];
     if constexpr (FMT == kKvE4m3) {
-      const uint4 c = *reinterpret_cast<const uint4 *>(stage + r * D + cg * 16);
-      e4m3x4_raw(c.x, h[0], h[1]);
-      e4m3x4_raw(c.y, h[2], h[3]);
-      e4m3x4_raw(c.z, h[4], h[5]);
-      e4m3x4_raw(c.w, h[6], h[7]);
-      const uint32_t f = row_factor(e);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) h[k] = mul_bf16x2(h[k], f);
+      e4m3x4(c[i].x, h[0], h[1]);
+      e4m3x4(c[i].y, h[2], h[3]);
+      e4m3x4(c[i].z, h[4], h[5]);
+      e4m3x4(c[i].w, h[6], h[7]);
     } else {
-      const uint2 c = *reinterpret_cast<const uint2 *>(stage + r * (D / 2) + cg * 8);
-      uint32_t a[4], b[4];
-      e2m1x8(c.x, a);
-      e2m1x8(c.y, b);
-      // Block scale times row scale (at most four significant bits: exact).
-      const uint32_t s = stage[Cfg<FMT>::CODES + r * (D / 16) + cg];
-      const uint32_t f = mul_bf16x2((s & 0x7fu) * 0x00100010u, row_factor(e));
+      uint32_t a[4], b[4], s0, s1;
+      e2m1x8(c[i].x, a);
+      e2m1x8(c[i].y, b);
+      e4m3x4(bsc[i] * 0x101u, s0, s1);  // the block scale as a pair
+      f = mul_f16x2(s0, f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        h[k] = mul_bf16x2(a[k], f);
-        h[k + 4] = mul_bf16x2(b[k], f);
+        h[k] = a[k];
+        h[k + 4] = b[k];
       }
     }
-    if (__any_sync(0xffffffffu, e > 134u)) {
-      const uint32_t f2 = row_factor2(e);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[k] = mul_bf16x2(h[k], f2);
-    }
-    if (r >= rows_left) {
+    for (int k = 0; k < 8; ++k) h[k] = mul_f16x2(h[k], f);
+    const int rr = i * 4 + rl;
+    if (rows_left < BN && w * 32 + rr >= rows_left) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) h[k] = 0u;
     }
-    const uint32_t row = tile + half * HALF_BYTES + r * 128;
-    const int c0 = (2 * cg) & 7;
-    const uint32_t a0 = row + ((c0 ^ (r & 7)) * 16), a1 = row + (((c0 + 1) ^ (r & 7)) * 16);
-    if (half == 0) {
+    const uint32_t x = rr & 7;
+    const uint32_t row = row0 + i * 512;
+    const uint32_t a0 = row + ((c0 ^ x) * 16), a1 = a0 ^ 16u;  // c0 is even: c0 + 1 differs in one bit
+    if (!upper) {
       st_shared_v4(a0, h[0], h[1], h[2], h[3]);
       st_shared_v4(a1, h[4], h[5], h[6], h[7]);
     } else {
       st_shared_v4(a1, h[4], h[5], h[6], h[7]);
       st_shared_v4(a0, h[0], h[1], h[2], h[3]);
     }
+  }
+}
+
+// Query rows [r0, r1) of the swizzled bf16 tile to fp16, in place: sixteen lanes
+// a row, one 16-byte chunk each.
+__device__ __forceinline__ void convert_q(uint32_t tile, int r0, int r1, int lane, int8_t *qexp) {
+  for (int r = r0 + (lane >> 4); r < ((r1 + 1) & ~1); r += 2) {
+    const uint32_t at = tile + ((lane & 8) ? HALF_BYTES : 0) + r * 128 + (lane & 7) * 16;
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at)
+                 : "memory");
+    float x[8], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+      m = fmaxf(m, isfinite(x[i]) ? fabsf(x[i]) : 0.f);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int b = __float_as_int(m);
+    int e = 15 + 127 - (b >> 23) - ((b & 0x7fffff) != 0 ? 1 : 0);
+    e = m > 0.f ? min(e, 100) : 0;
+    const float f = __int_as_float((e + 127) << 23);  // e in [-113, 100]
+    st_shared_v4(at, pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f),
+                 pack_f16x2(x[4] * f, x[5] * f), pack_f16x2(x[6] * f, x[7] * f));
+    if ((lane & 15) == 0) qexp[r] = (int8_t)e;
   }
 }
 
@@ -432,10 +557,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   volatile int *abort = &sh.abort;
   auto bar = [&](uint64_t *b) { return smem_u32(b); };
   auto wait = [&](uint64_t *b, int phase) {
-    return mbar_wait(smem_u32(b), phase & 1, abort, a.err, kErrTimeout);
+    return mbar_wait_sleep(smem_u32(b), phase & 1, abort, a.err);
   };
   auto wait_warp = [&](uint64_t *b, int phase) {
-    return mbar_wait_warp(smem_u32(b), phase & 1, abort, a.err, kErrTimeout);
+    return __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(b), phase & 1, abort, a.err));
   };
 
   const uint64_t keep_l2 = policy_evict_last();    // read again by the other tiles of the sequence
@@ -449,7 +574,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     const int n = min(ppb, pages.n_parts - u0);
     const int page = pages.of_block(u0, lane);
     const int slot = (u0 + lane) * sub % pages.ps;
-    if (lane == 0) mbar_expect_tx(bar(full), n * sub * (C::ROW + (QUANT ? 1 + C::BS / BN : 0)));
+    if (lane == 0) mbar_expect_tx(bar(full), n * sub * (C::ROW + (QUANT ? (value ? 1 : 2) + C::BS / BN : 0)));
     __syncwarp();
     if (lane < n) {
       if constexpr (!QUANT) {
@@ -467,13 +592,14 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         if constexpr (FMT == kKvNvfp4)
           bulk_load(dst + C::CODES + r0 * (D / 16), (value ? a.pages.v_bs : a.pages.k_bs) + row * (D / 16),
                     sub * (D / 16), bar(full), kv_pol);
-        bulk_load(dst + C::CODES + C::BS + r0, (value ? a.pages.v_scale : a.pages.k_scale) + row, sub,
+        bulk_load(dst + L::SCALES + r0, (value ? a.pages.v_scale : a.pages.k_scale) + row, sub,
                   bar(full), kv_pol);
+        if (!value) bulk_load(dst + L::SCALES + BN + r0, a.pages.v_scale + row, sub, bar(full), kv_pol);
       }
     }
     __syncwarp();
   };
-  auto k_dst = [&](int c) { return QUANT ? base + L::KC + (c % NC) * L::STAGE : base + L::K + (c % NKD) * TILE_BYTES; };
+  auto k_dst = [&](int c) { return QUANT ? base + L::KC + (c % NC) * L::KSTAGE : base + L::K + (c % NKD) * TILE_BYTES; };
   auto k_bar = [&](int c) { return QUANT ? &sh.kc_full[c % NC] : &sh.ready[c % NR]; };
 
   // Set-up: the key producer initialises the barriers while the value
@@ -485,6 +611,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     prefetch_tmap(&tm_q);
     if constexpr (!QUANT) prefetch_tmap(&tm_k);
     mbar_init(bar(&sh.q_full), 1);
+    mbar_init(bar(&sh.q_ready), 8);
     for (int i = 0; i < NR; ++i) {
       mbar_init(bar(&sh.ready[i]), (QUANT ? 4 : 1) + 1);  // the key tile, the S buffer
       mbar_init(bar(&sh.qk_done[i]), 1);
@@ -502,7 +629,6 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     mbar_init(bar(&sh.v_tail), 1);
     for (int i = 0; i < NDEC; ++i) {
       mbar_init(bar(&sh.dec_full[i]), 1);
-      mbar_init(bar(&sh.dec_read[i]), 2 + NQ + (QUANT ? 4 : 0));
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(bar(&sh.kc_full[i]), 1);
@@ -524,6 +650,13 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   if (warp == WARP_V || warp == WARP_K) named_bar_sync(kSetupBarrier, 64);
   if (warp == WARP_K && sh.tile.s >= 0 && sh.tile.nb > 0) {
     const TileInfo x = sh.tile;
+    if (lane == 0) {
+      // Readers of a decision: the P.V issuer and the exponential warps; with a
+      // threshold also the value producer and converters.
+      const int readers = 1 + NQ + (x.ln_lam == -INFINITY ? 0 : QUANT ? 5 : 1);
+      for (int i = 0; i < NDEC; ++i) mbar_init(bar(&sh.dec_read[i]), readers);
+      fence_mbar_init();
+    }
     fence_proxy_async_smem();  // lane 0's barriers, for every lane's copies
     pages.init(a, x, lane);
     if (lane == 0) {
@@ -541,6 +674,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   const TileInfo x = sh.tile;
   const int nb = x.nb;
   const int rows = x.s >= 0 ? x.ntok * a.G : 0;
+  const bool dense = x.ln_lam == -INFINITY;
 
   if (x.s < 0) {
     // no tile for this CTA
@@ -581,16 +715,20 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     int vi = 0;
     bool tail = false;
     for (int c = 0; c < nb && !*abort; ++c) {
-      if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) break;
-      const int keep = sh.dec[c % NDEC];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(&sh.dec_read[c % NDEC]));
-      if (!keep) continue;
+      // A dense tile keeps every block: its values need no decision and load
+      // as far ahead as their ring allows.
+      if (!dense) {
+        if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) break;
+        const int keep = sh.dec[c % NDEC];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh.dec_read[c % NDEC]));
+        if (!keep) continue;
+      }
       const int j = x.j0 + c;
       if constexpr (QUANT) {
         const int s = vi % NC;
         if (vi >= NC && !wait_warp(&sh.vc_empty[s], vi / NC - 1)) break;
-        load_block(true, j, base + L::VC + s * L::STAGE, &sh.vc_full[s]);
+        load_block(true, j, base + L::VC + s * L::VSTAGE, &sh.vc_full[s]);
       } else {
         const int s = vi % NV;
         if (vi >= NV && !wait_warp(&sh.v_empty[s], vi / NV - 1)) break;
@@ -623,7 +761,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   } else if (warp == WARP_MMA || (!QUANT && warp == WARP_MMA2)) {
     // ------------------------------------------------------ Q.K^T issuers --
     const int mine = warp == WARP_MMA ? 0 : 1;
-    const bool ok = wait_warp(&sh.q_full, 0);
+    const bool ok = wait_warp(QUANT ? &sh.q_ready : &sh.q_full, 0);
     fence_after_sync();
     const uint64_t qdesc = kmajor_base(base + L::Q);
     for (int c = mine; ok && c < nb; c += QUANT ? 1 : 2) {
@@ -634,7 +772,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         const uint32_t d_s = tmem + (c % NS) * BN;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_ss(d_s, qdesc + kmajor_step(kk), kd + kmajor_step(kk), IDESC_QK, kk > 0);
+          mma_bf16_ss(d_s, qdesc + kmajor_step(kk), kd + kmajor_step(kk), QUANT ? IDESC_QK16 : IDESC_QK,
+                      kk > 0);
         mma_commit(bar(&sh.qk_done[c % NR]));
       }
       __syncwarp();
@@ -655,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         const uint64_t vd = vmajor_base(base + L::V + vs * TILE_BYTES);
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          mma_bf16_ts(tmem + TMEM_O, pt + kk * 8, vd + vmajor_step(kk), IDESC_PV,
+          mma_bf16_ts(tmem + TMEM_O, pt + kk * 8, vd + vmajor_step(kk), QUANT ? IDESC_PV16 : IDESC_PV,
                       kk > 0 || kc > 0 ? 1u : 0u);
         mma_commit(bar(&sh.v_empty[vs]));
         mma_commit(bar(&sh.ready[(c + NS) % NR]));  // S buffer free for block c + NS
@@ -666,12 +805,24 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   } else if (QUANT && warp >= WARP_KC && warp < WARP_VC) {
     // ------------------------------------------------------ key converters --
     if constexpr (QUANT) {
+      const int w = warp - WARP_KC;
+      if (wait_warp(&sh.q_full, 0)) {
+        convert_q(base + L::Q, w * 16, min(rows, w * 16 + 16), lane, sh.qexp);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh.q_ready));
+      }
       for (int c = 0; c < nb; ++c) {
         if (!wait_warp(&sh.kc_full[c % NC], c / NC)) break;
         // The tile last fed block c - NKD's Q.K^T.
         if (c >= NKD && !wait_warp(&sh.qk_done[(c - NKD) % NR], (c - NKD) / NR)) break;
-        convert_block<FMT>(smem_raw + L::KC + (c % NC) * L::STAGE, base + L::K + (c % NKD) * TILE_BYTES,
-                           warp - WARP_KC, lane, BN);
+        const uint8_t *stage = smem_raw + L::KC + (c % NC) * L::KSTAGE;
+        const int ek = block_top<FMT>(a, x, hk, x.j0 + c, false, stage + L::SCALES, lane);
+        if (w == 0) {
+          const int ev = block_top<FMT>(a, x, hk, x.j0 + c, true, stage + L::SCALES + BN, lane);
+          if (lane == 0) sh.esc[c % NE] = (uint16_t)(ek | (ev << 8));
+        }
+        convert_block<FMT>(stage, base + L::K + (c % NKD) * TILE_BYTES, w, lane, ek, BN);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -683,17 +834,28 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   } else if (QUANT && warp >= WARP_VC) {
     // ---------------------------------------------------- value converters --
     if constexpr (QUANT) {
+      const int w = warp - WARP_VC;
+      if (wait_warp(&sh.q_full, 0)) {
+        convert_q(base + L::Q, 64 + w * 16, min(rows, 64 + w * 16 + 16), lane, sh.qexp);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh.q_ready));
+      }
       int vi = 0;
       for (int c = 0; c < nb && !*abort; ++c) {
-        if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) break;
-        const int keep = sh.dec[c % NDEC];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(&sh.dec_read[c % NDEC]));
-        if (!keep) continue;
+        if (!dense) {
+          if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) break;
+          const int keep = sh.dec[c % NDEC];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&sh.dec_read[c % NDEC]));
+          if (!keep) continue;
+        }
         if (!wait_warp(&sh.vc_full[vi % NC], vi / NC)) break;
         if (vi >= NV && !wait_warp(&sh.v_empty[vi % NV], vi / NV - 1)) break;
-        convert_block<FMT>(smem_raw + L::VC + (vi % NC) * L::STAGE, base + L::V + (vi % NV) * TILE_BYTES,
-                           warp - WARP_VC, lane, x.kv - (x.j0 + c) * BN);
+        const uint8_t *stage = smem_raw + L::VC + (vi % NC) * L::VSTAGE;
+        const int ev = block_top<FMT>(a, x, hk, x.j0 + c, true, stage + L::SCALES, lane);
+        convert_block<FMT>(stage, base + L::V + (vi % NV) * TILE_BYTES, w, lane, ev,
+                           x.kv - (x.j0 + c) * BN);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -718,10 +880,24 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     float mref = -INFINITY, l = 0.f;
     int kc = 0;
     bool ok = true;
+    // A quantised cache: raw score to log2 units for a block of key exponent E_k,
+    // sl2 * 2^(E_k - x) (kept normal, so that a masked score stays -inf).
+    int qx = 0;
+    if constexpr (QUANT) {
+      if (active) {
+        ok = wait_warp(&sh.q_ready, 0);
+        qx = sh.qexp[r] + 127;
+      }
+    }
+    auto block_sl2 = [&](int ek) {
+      const int e = max(-126, min(126, ek - qx));
+      return fmaxf(sl2 * __int_as_float((e + 127) << 23), 1.17549435e-38f);
+    };
 
     if (decider) {
       const float c2 = x.ln_lam * kLog2e;
-      float m2 = -INFINITY;
+      float m2 = -INFINITY;  // running max (log2 units)
+      float t2 = -INFINITY;  // running max of (row max + E_v), the exponentials' reference
       uint32_t word = 0;
       uint32_t *bits = a.bits ? a.bits + ((((int64_t)x.s * a.Hkv + hk) * a.n_t + x.t) * a.n_splits + sp) * a.words
                               : nullptr;
@@ -760,12 +936,19 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
             tmem_wait_ld_regs(x3);
             mt = fmaxf(fmaxf(chunk_max(x0), chunk_max(x1)), fmaxf(chunk_max(x2), chunk_max(x3)));
           }
-          const float pm2 = mt * sl2;
+          int ek = 0, ev = 127;
+          if constexpr (QUANT) {
+            const int e = sh.esc[c % NE];
+            ek = e & 255;
+            ev = e >> 8;
+          }
+          const float pm2 = mt * (QUANT ? block_sl2(ek) : sl2);
           // With ln(lambda) < 0, "rowmax - m_new < c" is "rowmax - m_old < c".
           const float diff = mt == -INFINITY ? -INFINITY : pm2 - m2;
-          keep_vote = !__all_sync(0xffffffffu, !valid || diff < c2 || mt == -INFINITY);
+          keep_vote = dense || !__all_sync(0xffffffffu, !valid || diff < c2 || mt == -INFINITY);
           m2 = fmaxf(m2, pm2);
-          sh.mdec[c % NS][r] = m2;
+          t2 = fmaxf(t2, pm2 + (float)(ev - 127));
+          sh.mdec[c % NS][r] = t2;
           fence_before_sync();  // this warp's reads of S_j are complete
         }
         const bool keep = bar_red_or(kDeciderBarrier, NQ * 32, keep_vote);
@@ -809,8 +992,15 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
           fence_after_sync();
           const uint32_t sa = lane_base + (c % NS) * BN;  // masked by the deciders
           // A row without a visible key so far has only -inf scores: P = 0.
-          const float nref = mref == -INFINITY ? 0.f : -mref;
-          const uint64_t sl2x2 = f2(sl2, sl2), negref2 = f2(nref, nref);
+          int ek = 0, ev = 127;
+          if constexpr (QUANT) {
+            const int e = sh.esc[c % NE];
+            ek = e & 255;
+            ev = e >> 8;
+          }
+          const float nref = mref == -INFINITY ? 0.f : (float)(ev - 127) - mref;
+          const float bl2 = QUANT ? block_sl2(ek) : sl2;
+          const uint64_t sl2x2 = f2(bl2, bl2), negref2 = f2(nref, nref);
           uint64_t acc2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
           if constexpr (QUANT) {
 #pragma unroll 1
@@ -818,10 +1008,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
               uint32_t s[32], pk[32];
               tmem_ld32(sa + 64 * hh, s);
               tmem_wait_ld_regs(s);
-              chunk_exp(s, sl2x2, negref2, acc2, pk);
+              chunk_exp<true>(s, sl2x2, negref2, acc2, pk);
               tmem_ld32(sa + 64 * hh + 32, s);
               tmem_wait_ld_regs(s);
-              chunk_exp(s, sl2x2, negref2, acc2, pk + 16);
+              chunk_exp<true>(s, sl2x2, negref2, acc2, pk + 16);
               tmem_st32(sa + 32 * hh, pk);
             }
           } else {
@@ -834,8 +1024,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
               tmem_ld32(sa + 64 * hh + 32, s1);
               tmem_wait_ld_regs(s0);
               tmem_wait_ld_regs(s1);
-              chunk_exp(s0, sl2x2, negref2, acc2, pk);
-              chunk_exp(s1, sl2x2, negref2, acc2, pk + 16);
+              chunk_exp<false>(s0, sl2x2, negref2, acc2, pk);
+              chunk_exp<false>(s1, sl2x2, negref2, acc2, pk + 16);
               tmem_st32(sa + 32 * hh, pk);
             }
           }
@@ -843,7 +1033,9 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
           float acc[4];
           f2_split(acc2[0], acc[0], acc[1]);
           f2_split(acc2[1], acc[2], acc[3]);
-          l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+          float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          if constexpr (QUANT) sum *= __int_as_float(max(1, 254 - ev) << 23);  // sum P' 2^-E_v
+          l = l * alpha + sum;
           if (__any_sync(0xffffffffu, rescale) && kc >= 1) {
             if (!wait_warp(&sh.pv_done[(kc - 1) % NS], (kc - 1) / NS)) {
               ok = false;
