@@ -41,8 +41,8 @@
 // the row sum takes sum P' * 2^-E_v.  A query row enters as fp16(q * 2^x), 2^x
 // the largest power of two with max|q| 2^x <= 2^15.
 //
-// A warp quarter whose 32 rows lie past the tile's last row (decode: G rows)
-// takes part in the barriers and touches no score.
+// A warp quarter whose 32 rows lie past the tile's last row (decode: G rows) has
+// no decider and no exponential warp: they go to the end at once.
 //
 // Rows of the last block at or past kv (a page's unwritten tail, pages never
 // loaded) may hold anything: their scores are replaced by -inf and their value
@@ -163,27 +163,17 @@ __device__ __forceinline__ constexpr uint64_t vmajor_step(int kk) {
   return (uint64_t)(((uint32_t)kk * 2048u) >> 4);
 }
 
-// The bounded waits of the other kernels, but a thread that finds its phase
-// incomplete sleeps in the barrier unit, for up to 20 us a try, instead of
-// asking again at once: most of the twenty warps wait most of the time, and the
-// converters need the issue slots.
-__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, volatile int *abort,
-                                                unsigned *err) {
-  if (mbar_sleep(bar, parity)) return true;
+// The bounded waits of the other kernels with their slow path out of line (some
+// forty waits share the instruction cache) and with sixteen tries between two
+// looks at the abort flag and the clock (most warps wait most of the time, and
+// the converters need the issue slots).
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort,
+                                            unsigned *err) {
   const uint64_t t0 = globaltimer();
   while (true) {
-    if (mbar_sleep(bar, parity)) return true;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (globaltimer() - t0 > kWaitLimitNs) {
       *abort = 1;
@@ -191,6 +181,10 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, v
       return false;
     }
   }
+}
+__device__ __forceinline__ bool mbar_wait_shared(uint32_t bar, uint32_t parity, volatile int *abort,
+                                                 unsigned *err) {
+  return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, abort, err);
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
@@ -264,6 +258,7 @@ __device__ __noinline__ void locate(const ChunkArgs &a, int i, int split, int la
                                     TileInfo *out) {
   bool bad = false, found = false;
   int before = 0;
+#pragma unroll 1
   for (int b = 0; b < a.n_seq && (report || !found); b += 32) {
     const int s = b + lane;
     int c0 = 0, len = 0, kv = 0;
@@ -313,47 +308,85 @@ __device__ __noinline__ void locate(const ChunkArgs &a, int i, int split, int la
   __syncwarp();
 }
 
-// ------------------------------------------------------------- page windows --
-// The pages of a sequence, 32 parts at a time: lane l holds the page id of part
-// base + l (a part is a page, or 128 rows of a larger page); the next 32 are
+// ------------------------------------------------------------------- pages --
+// What a producer warp needs to copy blocks.  A part is a page, or 128 rows of a
+// larger page; lane l holds the page id of part base + l, and the next 32 are
 // loaded one window ahead.  A page id out of range is reported and page 0 read
 // in its place.
-struct Pages {
+struct Producer {
   const int32_t *table;  // the sequence's row
-  int sub, ps, n_pages, n_parts, base, cur, nxt;
+  int sub, per_page;     // rows of a part, parts of a page
+  int n_parts, base, cur, nxt, hk;
+  uint64_t policy;
   bool bad;
-
-  __device__ __forceinline__ int load(int u) {
-    if (u >= n_parts) return 0;
-    const int id = __ldg(table + (int64_t)u * sub / ps);
-    if (id < 0 || id >= n_pages) {
-      bad = true;
-      return 0;
-    }
-    return id;
-  }
-  __device__ __forceinline__ void init(const ChunkArgs &a, const TileInfo &x, int lane) {
-    table = a.page_table + (int64_t)x.s * a.max_pages;
-    ps = a.pages.page_size;
-    sub = min(ps, BN);
-    n_pages = a.pages.n_pages;
-    n_parts = (x.kv + sub - 1) / sub;
-    bad = false;
-    base = (x.j0 * (BN / sub)) & ~31;
-    cur = load(base + lane);
-    nxt = load(base + 32 + lane);
-  }
-  // Page of part u0 + lane for lanes below the parts of a block; whole warp.
-  __device__ __forceinline__ int of_block(int u0, int lane) {
-    const int b = u0 & ~31;
-    if (b != base) {
-      cur = b == base + 32 ? nxt : load(b + lane);
-      base = b;
-      nxt = load(b + 32 + lane);
-    }
-    return __shfl_sync(0xffffffffu, cur, (u0 - b + lane) & 31);
-  }
 };
+
+__device__ __forceinline__ int page_of_part(const ChunkArgs &a, Producer &p, int u) {
+  if (u >= p.n_parts) return 0;
+  const int id = __ldg(p.table + (unsigned)u / (unsigned)p.per_page);
+  if (id < 0 || id >= a.pages.n_pages) {
+    p.bad = true;
+    return 0;
+  }
+  return id;
+}
+
+__device__ __noinline__ void producer_init(const ChunkArgs &a, Producer &p, const TileInfo &x, int hk,
+                                           int lane) {
+  p.table = a.page_table + (int64_t)x.s * a.max_pages;
+  p.sub = min(a.pages.page_size, BN);
+  p.per_page = a.pages.page_size / p.sub;
+  p.n_parts = (x.kv + p.sub - 1) / p.sub;
+  p.bad = false;
+  p.hk = hk;
+  // Keys and values are read again by the other tiles of the sequence, or once.
+  p.policy = a.max_chunk > a.TT ? policy_evict_last() : policy_evict_first();
+  p.base = (x.j0 * (BN / p.sub)) & ~31;
+  p.cur = page_of_part(a, p, p.base + lane);
+  p.nxt = page_of_part(a, p, p.base + 32 + lane);
+}
+
+// Block j's rows (codes and scales) into the staging area or tile at dst, part by
+// part, one lane a part; whole warp.  The arrival with the byte count comes
+// first.  Out of line: its four callers share the instruction cache.
+template <int FMT>
+__device__ __noinline__ void load_block(const ChunkArgs &a, Producer &p, const CUtensorMap *map,
+                                        bool value, int j, uint32_t dst, uint32_t full, int lane) {
+  using C = Cfg<FMT>;
+  constexpr bool QUANT = FMT != kKvBf16;
+  const int sub = p.sub, ppb = BN / sub, u0 = j * ppb;
+  const int n = min(ppb, p.n_parts - u0);
+  const int b = u0 & ~31;
+  if (b != p.base) {
+    p.cur = b == p.base + 32 ? p.nxt : page_of_part(a, p, b + lane);
+    p.base = b;
+    p.nxt = page_of_part(a, p, b + 32 + lane);
+  }
+  const int page = __shfl_sync(0xffffffffu, p.cur, (u0 - b + lane) & 31);
+  const int slot = (int)((unsigned)(u0 + lane) % (unsigned)p.per_page) * sub;
+  if (lane == 0) mbar_expect_tx(full, n * sub * (C::ROW + (QUANT ? (value ? 1 : 2) + C::BS / BN : 0)));
+  __syncwarp();
+  if (lane < n) {
+    if constexpr (!QUANT) {
+      const uint32_t d = dst + lane * sub * 128;
+      tma_load_4d(d, map, full, 0, slot, p.hk, page, p.policy);
+      tma_load_4d(d + HALF_BYTES, map, full, 64, slot, p.hk, page, p.policy);
+    } else {
+      const KvPages &g = a.pages;
+      const int64_t row = ((int64_t)page * g.Hkv + p.hk) * g.page_size + slot;
+      const uint8_t *src = (const uint8_t *)(value ? g.v : g.k) + (int64_t)page * g.page_stride +
+                           ((int64_t)p.hk * g.page_size + slot) * C::ROW;
+      const uint32_t r0 = lane * sub, scales = dst + Layout<FMT>::SCALES + r0;
+      bulk_load(dst + r0 * C::ROW, src, sub * C::ROW, full, p.policy);
+      if constexpr (FMT == kKvNvfp4)
+        bulk_load(dst + C::CODES + r0 * (D / 16), (value ? g.v_bs : g.k_bs) + row * (D / 16),
+                  sub * (D / 16), full, p.policy);
+      bulk_load(scales, (value ? g.v_scale : g.k_scale) + row, sub, full, p.policy);
+      if (!value) bulk_load(scales + BN, g.v_scale + row, sub, full, p.policy);
+    }
+  }
+  __syncwarp();
+}
 
 // ------------------------------------------------------------- conversions --
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -396,6 +429,7 @@ __device__ __noinline__ int block_top_slow(const ChunkArgs &a, const TileInfo &x
                                            bool value, const uint8_t *scales, int lane, int left) {
   const KvPages &p = a.pages;
   int top = 0;
+#pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * lane + i;
     if (r >= left || scales[r] == 255) continue;
@@ -436,11 +470,14 @@ __device__ __forceinline__ int block_top(const ChunkArgs &a, const TileInfo &x, 
 }
 
 // One staged block to an fp16 tile: warp w of four takes rows 32 w .. 32 w + 31,
-// eight lanes a row (sixteen codes each).  All codes are read before the first
-// store (a store orders every later load behind it).  Lane l forms the factor
-// of row 32 w + l; a row's lanes fetch it by a shuffle.  Lanes of the upper half
-// of a row store their two 16-byte chunks in the other order, so that a store
-// instruction's eight lanes of a row meet eight different bank groups.
+// eight lanes a row (sixteen codes each), four rows a step.  The next step's
+// codes are read before a step's stores (a store orders every later load
+// behind it).  The steps are a loop: twenty warps in eight roles share the
+// instruction cache, and unrolled they ran three times slower, at its refill
+// rate.  Lane l forms the factor of row 32 w + l; a row's lanes fetch it by a
+// shuffle.  Lanes of the upper half of a row store their two 16-byte chunks in
+// the other order, so that a store instruction's eight lanes of a row meet
+// eight different bank groups.
 // rows_left: rows at or past it become zero (values of the last block).
 template <int FMT>
 __device__ __forceinline__ void convert_block(const uint8_t *stage, uint32_t tile, int w, int lane,
@@ -448,60 +485,61 @@ __device__ __forceinline__ void convert_block(const uint8_t *stage, uint32_t til
   const int cg = lane & 7, rl = lane >> 3;
   const bool upper = cg >= 4;
   const uint32_t fl = row_factor(stage[Layout<FMT>::SCALES + w * 32 + lane], top);
-  uint4 c[8];
-  uint32_t bsc[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = w * 32 + i * 4 + rl;
+  const int r0 = w * 32 + rl;
+  const uint8_t *src = stage + r0 * Cfg<FMT>::ROW + cg * (Cfg<FMT>::ROW / 8);
+  const uint8_t *bsrc = stage + Cfg<FMT>::CODES + r0 * (D / 16) + cg;
+  // Chunk c of row r sits at c ^ (r % 8); the lane's pair is 2 cg % 8 and the
+  // next, and r % 8 is rl or rl + 4 in turn.
+  const uint32_t dst = tile + (upper ? HALF_BYTES : 0) + r0 * 128;
+  uint32_t at = ((((2 * cg) & 7) ^ rl) * 16) ^ (upper ? 16u : 0u);
+  uint4 c{};
+  uint32_t b = 0;
+  auto load = [&](int i) {
     if constexpr (FMT == kKvE4m3) {
-      c[i] = *reinterpret_cast<const uint4 *>(stage + r * D + cg * 16);
+      c = *reinterpret_cast<const uint4 *>(src + i * 4 * D);
     } else {
-      const uint2 v = *reinterpret_cast<const uint2 *>(stage + r * (D / 2) + cg * 8);
-      c[i].x = v.x;
-      c[i].y = v.y;
-      bsc[i] = stage[Cfg<FMT>::CODES + r * (D / 16) + cg];
+      const uint2 v = *reinterpret_cast<const uint2 *>(src + i * 4 * (D / 2));
+      c.x = v.x;
+      c.y = v.y;
+      b = bsrc[i * 4 * (D / 16)];
     }
-  }
-  const uint32_t row0 = tile + (upper ? HALF_BYTES : 0) + (w * 32 + rl) * 128;
-  const int c0 = (2 * cg) & 7;  // 16-byte chunk c of row r sits at c ^ (r % 8)
-#pragma unroll
+  };
+  load(0);
+#pragma unroll 1
   for (int i = 0; i < 8; ++i) {
     uint32_t f = __shfl_sync(0xffffffffu, fl, i * 4 + rl);
     uint32_t h[8];
     if constexpr (FMT == kKvE4m3) {
-      e4m3x4(c[i].x, h[0], h[1]);
-      e4m3x4(c[i].y, h[2], h[3]);
-      e4m3x4(c[i].z, h[4], h[5]);
-      e4m3x4(c[i].w, h[6], h[7]);
+      e4m3x4(c.x, h[0], h[1]);
+      e4m3x4(c.y, h[2], h[3]);
+      e4m3x4(c.z, h[4], h[5]);
+      e4m3x4(c.w, h[6], h[7]);
     } else {
-      uint32_t a[4], b[4], s0, s1;
-      e2m1x8(c[i].x, a);
-      e2m1x8(c[i].y, b);
-      e4m3x4(bsc[i] * 0x101u, s0, s1);  // the block scale as a pair
+      uint32_t s0, s1;
+      e2m1x8(c.x, *reinterpret_cast<uint32_t(*)[4]>(&h[0]));
+      e2m1x8(c.y, *reinterpret_cast<uint32_t(*)[4]>(&h[4]));
+      e4m3x4(b * 0x101u, s0, s1);  // the block scale as a pair
       f = mul_f16x2(s0, f);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h[k] = a[k];
-        h[k + 4] = b[k];
-      }
     }
+    load(min(i + 1, 7));
 #pragma unroll
     for (int k = 0; k < 8; ++k) h[k] = mul_f16x2(h[k], f);
-    const int rr = i * 4 + rl;
-    if (rows_left < BN && w * 32 + rr >= rows_left) {
+    if (rows_left < BN && r0 + i * 4 >= rows_left) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) h[k] = 0u;
     }
-    const uint32_t x = rr & 7;
-    const uint32_t row = row0 + i * 512;
-    const uint32_t a0 = row + ((c0 ^ x) * 16), a1 = a0 ^ 16u;  // c0 is even: c0 + 1 differs in one bit
-    if (!upper) {
-      st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-      st_shared_v4(a1, h[4], h[5], h[6], h[7]);
-    } else {
-      st_shared_v4(a1, h[4], h[5], h[6], h[7]);
-      st_shared_v4(a0, h[0], h[1], h[2], h[3]);
+    if (upper) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t t = h[k];
+        h[k] = h[k + 4];
+        h[k + 4] = t;
+      }
     }
+    const uint32_t a0 = dst + i * 512 + at;
+    st_shared_v4(a0, h[0], h[1], h[2], h[3]);
+    st_shared_v4(a0 ^ 16u, h[4], h[5], h[6], h[7]);
+    at ^= 64u;
   }
 }
 
@@ -537,8 +575,8 @@ template <int FMT>
 __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     chunk_paged_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const ChunkArgs a,
-                       const int q_box_tokens) {
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ ChunkArgs a, const int q_box_tokens) {
   using C = Cfg<FMT>;
   using L = Layout<FMT>;
   constexpr bool QUANT = FMT != kKvBf16;
@@ -557,50 +595,18 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   volatile int *abort = &sh.abort;
   auto bar = [&](uint64_t *b) { return smem_u32(b); };
   auto wait = [&](uint64_t *b, int phase) {
-    return mbar_wait_sleep(smem_u32(b), phase & 1, abort, a.err);
+    return mbar_wait_shared(smem_u32(b), phase & 1, abort, a.err);
   };
   auto wait_warp = [&](uint64_t *b, int phase) {
-    return __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(b), phase & 1, abort, a.err));
+    return __all_sync(0xffffffffu, mbar_wait_shared(smem_u32(b), phase & 1, abort, a.err));
   };
 
-  const uint64_t keep_l2 = policy_evict_last();    // read again by the other tiles of the sequence
-  const uint64_t stream_l2 = policy_evict_first();  // read once
-  const uint64_t kv_pol = a.max_chunk > a.TT ? keep_l2 : stream_l2;
-  Pages pages{};  // of the producer warps
-  // One block's rows (codes and scales) into the staging area or tile at dst,
-  // part by part, one lane a part.  The arrival with the byte count comes first.
-  auto load_block = [&](bool value, int j, uint32_t dst, uint64_t *full) {
-    const int sub = pages.sub, ppb = BN / sub, u0 = j * ppb;
-    const int n = min(ppb, pages.n_parts - u0);
-    const int page = pages.of_block(u0, lane);
-    const int slot = (u0 + lane) * sub % pages.ps;
-    if (lane == 0) mbar_expect_tx(bar(full), n * sub * (C::ROW + (QUANT ? (value ? 1 : 2) + C::BS / BN : 0)));
-    __syncwarp();
-    if (lane < n) {
-      if constexpr (!QUANT) {
-        const CUtensorMap *m = value ? &tm_v : &tm_k;
-        const uint32_t d = dst + lane * sub * 128;
-        tma_load_4d(d, m, bar(full), 0, slot, hk, page, kv_pol);
-        tma_load_4d(d + HALF_BYTES, m, bar(full), 64, slot, hk, page, kv_pol);
-      } else {
-        const int64_t row = ((int64_t)page * a.Hkv + hk) * pages.ps + slot;
-        const uint8_t *src = (const uint8_t *)(value ? a.pages.v : a.pages.k) +
-                             (int64_t)page * a.pages.page_stride +
-                             ((int64_t)hk * pages.ps + slot) * C::ROW;
-        const uint32_t r0 = lane * sub;
-        bulk_load(dst + r0 * C::ROW, src, sub * C::ROW, bar(full), kv_pol);
-        if constexpr (FMT == kKvNvfp4)
-          bulk_load(dst + C::CODES + r0 * (D / 16), (value ? a.pages.v_bs : a.pages.k_bs) + row * (D / 16),
-                    sub * (D / 16), bar(full), kv_pol);
-        bulk_load(dst + L::SCALES + r0, (value ? a.pages.v_scale : a.pages.k_scale) + row, sub,
-                  bar(full), kv_pol);
-        if (!value) bulk_load(dst + L::SCALES + BN + r0, a.pages.v_scale + row, sub, bar(full), kv_pol);
-      }
-    }
-    __syncwarp();
-  };
+  Producer pages;  // of the two producer warps
   auto k_dst = [&](int c) { return QUANT ? base + L::KC + (c % NC) * L::KSTAGE : base + L::K + (c % NKD) * TILE_BYTES; };
   auto k_bar = [&](int c) { return QUANT ? &sh.kc_full[c % NC] : &sh.ready[c % NR]; };
+  auto load_k = [&](int c) {
+    load_block<FMT>(a, pages, &tm_k, false, sh.tile.j0 + c, k_dst(c), bar(k_bar(c)), lane);
+  };
 
   // Set-up: the key producer initialises the barriers while the value
   // producer's warp locates the tile; Q and the first keys are then in flight
@@ -621,11 +627,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
       mbar_init(bar(&sh.v_full[i]), QUANT ? 4 : 1);
       mbar_init(bar(&sh.v_empty[i]), 1);
     }
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(bar(&sh.p_full[i]), NQ);
-      mbar_init(bar(&sh.pv_done[i]), 1);
-    }
-    mbar_init(bar(&sh.l_full), NQ);
+    for (int i = 0; i < NS; ++i) mbar_init(bar(&sh.pv_done[i]), 1);
     mbar_init(bar(&sh.v_tail), 1);
     for (int i = 0; i < NDEC; ++i) {
       mbar_init(bar(&sh.dec_full[i]), 1);
@@ -651,21 +653,26 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   if (warp == WARP_K && sh.tile.s >= 0 && sh.tile.nb > 0) {
     const TileInfo x = sh.tile;
     if (lane == 0) {
-      // Readers of a decision: the P.V issuer and the exponential warps; with a
-      // threshold also the value producer and converters.
-      const int readers = 1 + NQ + (x.ln_lam == -INFINITY ? 0 : QUANT ? 5 : 1);
+      // Readers of a decision: the P.V issuer and the exponential warps that have
+      // rows; with a threshold also the value producer and converters.
+      const int nq = (x.ntok * a.G + 31) / 32;
+      const int readers = 1 + nq + (x.ln_lam == -INFINITY ? 0 : QUANT ? 5 : 1);
       for (int i = 0; i < NDEC; ++i) mbar_init(bar(&sh.dec_read[i]), readers);
+      for (int i = 0; i < NS; ++i) mbar_init(bar(&sh.p_full[i]), nq);
+      mbar_init(bar(&sh.l_full), nq);
       fence_mbar_init();
     }
     fence_proxy_async_smem();  // lane 0's barriers, for every lane's copies
-    pages.init(a, x, lane);
+    producer_init(a, pages, x, hk, lane);
     if (lane == 0) {
+      const uint64_t once = policy_evict_first();
       mbar_expect_tx(bar(&sh.q_full), 2 * 128 * a.G * q_box_tokens);
-      tma_load_3d(base + L::Q, &tm_q, bar(&sh.q_full), 0, hk * a.G, x.tok0, stream_l2);
-      tma_load_3d(base + L::Q + HALF_BYTES, &tm_q, bar(&sh.q_full), 64, hk * a.G, x.tok0, stream_l2);
+      tma_load_3d(base + L::Q, &tm_q, bar(&sh.q_full), 0, hk * a.G, x.tok0, once);
+      tma_load_3d(base + L::Q + HALF_BYTES, &tm_q, bar(&sh.q_full), 64, hk * a.G, x.tok0, once);
     }
     __syncwarp();
-    for (; p_c < x.nb && p_c < K_AHEAD; ++p_c) load_block(false, x.j0 + p_c, k_dst(p_c), k_bar(p_c));
+#pragma unroll 1
+    for (; p_c < x.nb && p_c < K_AHEAD; ++p_c) load_k(p_c);
   }
   fence_before_sync();
   __syncthreads();
@@ -680,6 +687,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     // no tile for this CTA
   } else if (nb == 0) {
     // No visible key: O = 0, LSE = -inf (one split), or a partial of no weight.
+#pragma unroll 1
     for (int i = tid; i < rows * (D / 8); i += C::WARPS * 32) {
       const int r = i / (D / 8);
       const int64_t orow = (int64_t)(x.tok0 + r / a.G) * a.Hq + hk * a.G + r % a.G;
@@ -692,18 +700,20 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   } else if (warp == WARP_K) {
     // -------------------------------------------------------- key producer --
     int issued = p_c;
+#pragma unroll 1
     for (int c = p_c; c < nb && !*abort; ++c) {
       // The ring's slot last held block c - K_AHEAD.
       if (!(QUANT ? wait_warp(&sh.kc_empty[c % NC], c / NC - 1)
                   : wait_warp(&sh.qk_done[c % NR], c / NR - 1)))
         break;
-      load_block(false, x.j0 + c, k_dst(c), k_bar(c));
+      load_k(c);
       ++issued;
     }
     if (__any_sync(0xffffffffu, pages.bad) && lane == 0) atomicOr(a.err, kErrBadArg);
     if (lane == 0) {
       // Drain: the last load of each slot has landed before exit.
       mbar_wait_drain(bar(&sh.q_full), 0);
+#pragma unroll 1
       for (int s = 0; s < K_AHEAD && s < issued; ++s) {
         const int last = s + ((issued - 1 - s) / K_AHEAD) * K_AHEAD;
         mbar_wait_drain(bar(k_bar(s)), (last / K_AHEAD) & 1);
@@ -711,9 +721,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     }
   } else if (warp == WARP_V) {
     // ------------------------------------------------------ value producer --
-    pages.init(a, x, lane);
+    producer_init(a, pages, x, hk, lane);
     int vi = 0;
     bool tail = false;
+#pragma unroll 1
     for (int c = 0; c < nb && !*abort; ++c) {
       // A dense tile keeps every block: its values need no decision and load
       // as far ahead as their ring allows.
@@ -725,34 +736,31 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         if (!keep) continue;
       }
       const int j = x.j0 + c;
-      if constexpr (QUANT) {
-        const int s = vi % NC;
-        if (vi >= NC && !wait_warp(&sh.vc_empty[s], vi / NC - 1)) break;
-        load_block(true, j, base + L::VC + s * L::VSTAGE, &sh.vc_full[s]);
-      } else {
-        const int s = vi % NV;
-        if (vi >= NV && !wait_warp(&sh.v_empty[s], vi / NV - 1)) break;
-        const uint32_t dst = base + L::V + s * TILE_BYTES;
-        const int left = x.kv - j * BN;  // rows of the block below kv
-        if (left >= BN) {
-          load_block(true, j, dst, &sh.v_full[s]);
-        } else {  // the last block of the sequence: zero the rows at or past kv
-          tail = true;
-          load_block(true, j, dst, &sh.v_tail);
-          if (!wait_warp(&sh.v_tail, 0)) break;
-          for (int i = lane; i < (BN - left) * 16; i += 32)
-            st_shared_v4(dst + (i & 8 ? HALF_BYTES : 0) + (left + (i >> 4)) * 128 + (i & 7) * 16, 0,
-                         0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(&sh.v_full[s]));
-        }
+      constexpr int N = QUANT ? NC : NV;
+      const int s = vi % N;
+      if (vi >= N && !wait_warp(QUANT ? &sh.vc_empty[s] : &sh.v_empty[s], vi / N - 1)) break;
+      const uint32_t dst = base + (QUANT ? L::VC + s * L::VSTAGE : L::V + s * TILE_BYTES);
+      const int left = x.kv - j * BN;  // rows of the block below kv
+      const bool cut = !QUANT && left < BN;  // the last block: zero the rows at or past kv
+      load_block<FMT>(a, pages, &tm_v, true, j, dst,
+                      bar(QUANT ? &sh.vc_full[s] : cut ? &sh.v_tail : &sh.v_full[s]), lane);
+      if (cut) {
+        tail = true;
+        if (!wait_warp(&sh.v_tail, 0)) break;
+#pragma unroll 1
+        for (int i = lane; i < (BN - left) * 16; i += 32)
+          st_shared_v4(dst + (i & 8 ? HALF_BYTES : 0) + (left + (i >> 4)) * 128 + (i & 7) * 16, 0, 0,
+                       0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh.v_full[s]));
       }
       ++vi;
     }
     if (lane == 0) {
       constexpr int N = QUANT ? NC : NV;
       if (tail) mbar_wait_drain(bar(&sh.v_tail), 0);
+#pragma unroll 1
       for (int s = 0; s < N && s < vi; ++s) {
         const int last = s + ((vi - 1 - s) / N) * N;
         mbar_wait_drain(bar(QUANT ? &sh.vc_full[s] : &sh.v_full[s]), (last / N) & 1);
@@ -764,6 +772,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     const bool ok = wait_warp(QUANT ? &sh.q_ready : &sh.q_full, 0);
     fence_after_sync();
     const uint64_t qdesc = kmajor_base(base + L::Q);
+#pragma unroll 1
     for (int c = mine; ok && c < nb; c += QUANT ? 1 : 2) {
       if (!wait_warp(&sh.ready[c % NR], c / NR)) break;
       fence_after_sync();
@@ -782,6 +791,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     // ---------------------------------------------------------- P.V issuer --
     if (lane == 0) {
       int kc = 0;
+#pragma unroll 1
       for (int c = 0; c < nb && !*abort; ++c) {
         if (!wait(&sh.dec_full[c % NDEC], c / NDEC)) break;
         const int keep = sh.dec[c % NDEC];
@@ -812,6 +822,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&sh.q_ready));
       }
+#pragma unroll 1
       for (int c = 0; c < nb; ++c) {
         if (!wait_warp(&sh.kc_full[c % NC], c / NC)) break;
         // The tile last fed block c - NKD's Q.K^T.
@@ -842,6 +853,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         if (lane == 0) mbar_arrive(bar(&sh.q_ready));
       }
       int vi = 0;
+#pragma unroll 1
       for (int c = 0; c < nb && !*abort; ++c) {
         if (!dense) {
           if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) break;
@@ -865,13 +877,13 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         ++vi;
       }
     }
-  } else {
+  } else if ((warp & 3) * 32 < rows) {
     // ------------------------------------------------- deciders / exponentials --
     const bool decider = warp < NQ;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row == TMEM lane
     const bool valid = r < rows;
-    const bool active = quarter * 32 < rows;  // the warp has a row
+    const int nq = (rows + 31) / 32;    // quarters that have rows
     const int tok = r / a.G;
     const int limit = a.causal && valid ? x.pos0 + tok + 1 : x.kv;  // the row sees keys below it
     const int min_limit = a.causal ? x.pos0 + 1 : x.kv;             // the tile's smallest
@@ -884,10 +896,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     // sl2 * 2^(E_k - x) (kept normal, so that a masked score stays -inf).
     int qx = 0;
     if constexpr (QUANT) {
-      if (active) {
-        ok = wait_warp(&sh.q_ready, 0);
-        qx = sh.qexp[r] + 127;
-      }
+      ok = wait_warp(&sh.q_ready, 0);
+      qx = sh.qexp[r] + 127;
     }
     auto block_sl2 = [&](int ek) {
       const int e = max(-126, min(126, ek - qx));
@@ -901,29 +911,29 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
       uint32_t word = 0;
       uint32_t *bits = a.bits ? a.bits + ((((int64_t)x.s * a.Hkv + hk) * a.n_t + x.t) * a.n_splits + sp) * a.words
                               : nullptr;
+#pragma unroll 1
       for (int c = 0; c < nb; ++c) {
-        // After a failed wait the loop still runs to its end, so that the four
+        // After a failed wait the loop still runs to its end, so that the
         // warps meet the vote barrier equally often.
         if (ok) ok = wait_warp(&sh.qk_done[c % NR], c / NR);
         bool keep_vote = false;
-        if (ok && active) {
+        if (ok) {
           fence_after_sync();
           const uint32_t sa = lane_base + (c % NS) * BN;
           const int key0 = (x.j0 + c) * BN;
           if (key0 + BN > min_limit) mask_block_tmem(sa, limit - key0);
           float mt;
           if constexpr (QUANT) {  // 20 warps: fewer registers a thread
-            uint32_t x0[32], x1[32];
-            tmem_ld32(sa, x0);
-            tmem_ld32(sa + 32, x1);
-            tmem_wait_ld_regs(x0);
-            tmem_wait_ld_regs(x1);
-            mt = fmaxf(chunk_max(x0), chunk_max(x1));
-            tmem_ld32(sa + 64, x0);
-            tmem_ld32(sa + 96, x1);
-            tmem_wait_ld_regs(x0);
-            tmem_wait_ld_regs(x1);
-            mt = fmax3(mt, chunk_max(x0), chunk_max(x1));
+            mt = -INFINITY;
+#pragma unroll 1
+            for (int hh = 0; hh < 2; ++hh) {
+              uint32_t x0[32], x1[32];
+              tmem_ld32(sa + 64 * hh, x0);
+              tmem_ld32(sa + 64 * hh + 32, x1);
+              tmem_wait_ld_regs(x0);
+              tmem_wait_ld_regs(x1);
+              mt = fmax3(mt, chunk_max(x0), chunk_max(x1));
+            }
           } else {
             uint32_t x0[32], x1[32], x2[32], x3[32];
             tmem_ld32(sa, x0);
@@ -951,9 +961,9 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
           sh.mdec[c % NS][r] = t2;
           fence_before_sync();  // this warp's reads of S_j are complete
         }
-        const bool keep = bar_red_or(kDeciderBarrier, NQ * 32, keep_vote);
+        const bool keep = bar_red_or(kDeciderBarrier, nq * 32, keep_vote);
         if (!ok) continue;
-        if (lane == 0 && warp == (c & (NQ - 1))) {
+        if (lane == 0 && warp == (nq == NQ ? c & (NQ - 1) : 0)) {
           if (!keep) mbar_arrive(bar(&sh.ready[(c + NS) % NR]));  // its S buffer is free
           if (c < NDEC || wait(&sh.dec_read[c % NDEC], c / NDEC - 1)) {
             sh.dec[c % NDEC] = keep ? 1 : 0;
@@ -969,6 +979,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         }
       }
     } else {
+#pragma unroll 1
       for (int c = 0; c < nb; ++c) {
         if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) {
           ok = false;
@@ -978,84 +989,82 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&sh.dec_read[c % NDEC]));
         if (!keep) continue;
-        if (active) {
-          const float mnew = sh.mdec[c % NS][r];
-          bool rescale = false;
-          float alpha = 1.f;
-          if (mref == -INFINITY) {
-            mref = mnew;
-          } else if (valid && mnew > mref + kRescaleLog2) {
-            alpha = ex2(mref - mnew);
-            mref = mnew;
-            rescale = true;
+        const float mnew = sh.mdec[c % NS][r];
+        bool rescale = false;
+        float alpha = 1.f;
+        if (mref == -INFINITY) {
+          mref = mnew;
+        } else if (valid && mnew > mref + kRescaleLog2) {
+          alpha = ex2(mref - mnew);
+          mref = mnew;
+          rescale = true;
+        }
+        fence_after_sync();
+        const uint32_t sa = lane_base + (c % NS) * BN;  // masked by the deciders
+        // A row without a visible key so far has only -inf scores: P = 0.
+        int ek = 0, ev = 127;
+        if constexpr (QUANT) {
+          const int e = sh.esc[c % NE];
+          ek = e & 255;
+          ev = e >> 8;
+        }
+        const float nref = mref == -INFINITY ? 0.f : (float)(ev - 127) - mref;
+        const float bl2 = QUANT ? block_sl2(ek) : sl2;
+        const uint64_t sl2x2 = f2(bl2, bl2), negref2 = f2(nref, nref);
+        uint64_t acc2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+        if constexpr (QUANT) {
+#pragma unroll 1
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t s[32], pk[32];
+            tmem_ld32(sa + 64 * hh, s);
+            tmem_wait_ld_regs(s);
+            chunk_exp<true>(s, sl2x2, negref2, acc2, pk);
+            tmem_ld32(sa + 64 * hh + 32, s);
+            tmem_wait_ld_regs(s);
+            chunk_exp<true>(s, sl2x2, negref2, acc2, pk + 16);
+            tmem_st32(sa + 32 * hh, pk);
+          }
+        } else {
+#pragma unroll 1
+          for (int hh = 0; hh < 2; ++hh) {
+            // The P pairs of keys [64 hh, 64 hh + 64) land in columns [32 hh,
+            // 32 hh + 32), whose scores this or the previous half has loaded.
+            uint32_t s0[32], s1[32], pk[32];
+            tmem_ld32(sa + 64 * hh, s0);
+            tmem_ld32(sa + 64 * hh + 32, s1);
+            tmem_wait_ld_regs(s0);
+            tmem_wait_ld_regs(s1);
+            chunk_exp<false>(s0, sl2x2, negref2, acc2, pk);
+            chunk_exp<false>(s1, sl2x2, negref2, acc2, pk + 16);
+            tmem_st32(sa + 32 * hh, pk);
+          }
+        }
+        tmem_wait_st();
+        float acc[4];
+        f2_split(acc2[0], acc[0], acc[1]);
+        f2_split(acc2[1], acc[2], acc[3]);
+        float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        if constexpr (QUANT) sum *= __int_as_float(max(1, 254 - ev) << 23);  // sum P' 2^-E_v
+        l = l * alpha + sum;
+        if (__any_sync(0xffffffffu, rescale) && kc >= 1) {
+          if (!wait_warp(&sh.pv_done[(kc - 1) % NS], (kc - 1) / NS)) {
+            ok = false;
+            break;
           }
           fence_after_sync();
-          const uint32_t sa = lane_base + (c % NS) * BN;  // masked by the deciders
-          // A row without a visible key so far has only -inf scores: P = 0.
-          int ek = 0, ev = 127;
-          if constexpr (QUANT) {
-            const int e = sh.esc[c % NE];
-            ek = e & 255;
-            ev = e >> 8;
-          }
-          const float nref = mref == -INFINITY ? 0.f : (float)(ev - 127) - mref;
-          const float bl2 = QUANT ? block_sl2(ek) : sl2;
-          const uint64_t sl2x2 = f2(bl2, bl2), negref2 = f2(nref, nref);
-          uint64_t acc2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-          if constexpr (QUANT) {
 #pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
-              uint32_t s[32], pk[32];
-              tmem_ld32(sa + 64 * hh, s);
-              tmem_wait_ld_regs(s);
-              chunk_exp<true>(s, sl2x2, negref2, acc2, pk);
-              tmem_ld32(sa + 64 * hh + 32, s);
-              tmem_wait_ld_regs(s);
-              chunk_exp<true>(s, sl2x2, negref2, acc2, pk + 16);
-              tmem_st32(sa + 32 * hh, pk);
-            }
-          } else {
-#pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
-              // The P pairs of keys [64 hh, 64 hh + 64) land in columns [32 hh,
-              // 32 hh + 32), whose scores this or the previous half has loaded.
-              uint32_t s0[32], s1[32], pk[32];
-              tmem_ld32(sa + 64 * hh, s0);
-              tmem_ld32(sa + 64 * hh + 32, s1);
-              tmem_wait_ld_regs(s0);
-              tmem_wait_ld_regs(s1);
-              chunk_exp<false>(s0, sl2x2, negref2, acc2, pk);
-              chunk_exp<false>(s1, sl2x2, negref2, acc2, pk + 16);
-              tmem_st32(sa + 32 * hh, pk);
-            }
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            const uint32_t oa = lane_base + TMEM_O + cc * 32;
+            tmem_ld32(oa, o);
+            tmem_wait_ld_regs(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(oa, o);
           }
           tmem_wait_st();
-          float acc[4];
-          f2_split(acc2[0], acc[0], acc[1]);
-          f2_split(acc2[1], acc[2], acc[3]);
-          float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          if constexpr (QUANT) sum *= __int_as_float(max(1, 254 - ev) << 23);  // sum P' 2^-E_v
-          l = l * alpha + sum;
-          if (__any_sync(0xffffffffu, rescale) && kc >= 1) {
-            if (!wait_warp(&sh.pv_done[(kc - 1) % NS], (kc - 1) / NS)) {
-              ok = false;
-              break;
-            }
-            fence_after_sync();
-#pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t o[32];
-              const uint32_t oa = lane_base + TMEM_O + cc * 32;
-              tmem_ld32(oa, o);
-              tmem_wait_ld_regs(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(oa, o);
-            }
-            tmem_wait_st();
-          }
-          fence_before_sync();
         }
+        fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&sh.p_full[kc % NS]));
         ++kc;
@@ -1071,7 +1080,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
 
     // ---- epilogue: deciders take O columns [0,64), exponential warps [64,128)
     if (ok) ok = wait_warp(&sh.l_full, 0);
-    if (ok && active) {
+    if (ok) {
       fence_after_sync();
       const float lrow = sh.mdec[0][r];
       const bool empty = lrow == 0.f;  // no key kept for this row
@@ -1140,12 +1149,14 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const ChunkArgs
   if (c0 < 0 || c0 > tok || c1 - c0 > a.max_chunk || c1 > a.total) return;
   const float *ls = a.lse_part + row * a.n_splits;
   float m = -INFINITY;
+#pragma unroll 1
   for (int s = lane; s < a.n_splits; s += 32) m = fmaxf(m, ls[s]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float z = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4 *op = reinterpret_cast<const float4 *>(a.o_part + row * a.n_splits * D) + lane;
+#pragma unroll 4
   for (int s = 0; s < a.n_splits; ++s) {
     const float x = ls[s];
     if (x == -INFINITY) continue;
