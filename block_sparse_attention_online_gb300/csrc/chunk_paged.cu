@@ -42,7 +42,14 @@
 // the largest power of two with max|q| 2^x <= 2^15.
 //
 // A warp quarter whose 32 rows lie past the tile's last row (decode: G rows) has
-// no decider and no exponential warp: they go to the end at once.
+// no decider and no exponential warp: they convert, or go to the end at once.
+//
+// Tiles of at most 32 rows (decode, drafted tokens) stand in all four quarters of
+// the 128 product rows: quarter w exponentiates keys 32 w .. 32 w + 31 of each
+// block against its own running reference, its P holding zeros for the other
+// keys, and the four partial outputs are merged as splits are.  One warp with
+// all 128 keys of a handful of rows was what bounded decode over the quantised
+// caches (3600 cycles a block on an SM whose other warps convert).
 //
 // Rows of the last block at or past kv (a page's unwritten tail, pages never
 // loaded) may hold anything: their scores are replaced by -inf and their value
@@ -68,7 +75,8 @@ constexpr int NS = 3;     // TMEM S buffers
 constexpr int NDEC = 4;   // decision ring
 constexpr int NE = 8;     // scale exponent ring of the quantised formats
 constexpr int NQ = 4;     // warps per row role
-constexpr int kDeciderBarrier = 1, kSetupBarrier = 2;
+constexpr int kDeciderBarrier = 1, kSetupBarrier = 2, kMergeBarrier = 3;
+constexpr int MERGE_STRIDE = D + 4;  // floats a row: a row's 16-byte stores meet other banks than the next's
 constexpr int WARP_K = 8, WARP_MMA = 9, WARP_V = 10, WARP_PV = 11;
 constexpr int WARP_MMA2 = 12;             // bf16 cache
 constexpr int WARP_KC = 12, WARP_VC = 16;  // quantised caches
@@ -140,6 +148,8 @@ struct Shared {
   // [S buffer][row] running max after the buffer's block (log2 units).  Row
   // sums and exp references for the epilogue take the first two buffers' place
   // at the end: row r's words are read and written by its two threads alone.
+  // REP: the exponential warps take the maximum themselves, and the last buffer
+  // holds the row maxima of the quarters' keys.
   float mdec[NS][BM];
   TileInfo tile;
   uint32_t tmem_base;
@@ -148,6 +158,7 @@ struct Shared {
 static_assert(Layout<kKvBf16>::END + sizeof(Shared) <= 227 * 1024, "shared memory budget");
 static_assert(Layout<kKvE4m3>::END + sizeof(Shared) <= 227 * 1024, "shared memory budget");
 static_assert(Layout<kKvNvfp4>::END + sizeof(Shared) <= 227 * 1024, "shared memory budget");
+static_assert(NQ * 32 * MERGE_STRIDE * 4 <= (2 + NV) * TILE_BYTES, "merge area: the key and value tiles");
 static_assert(NR % 2 == 0 && NR > NS, "barrier ring: even, and longer than the S buffer ring");
 
 __device__ __forceinline__ uint64_t kmajor_base(uint32_t tile) {
@@ -197,15 +208,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// Keys of columns [kbase, kbase + 128) at or past the row's limit become -inf
-// in this warp's TMEM lanes; 32 keys at a time, chunks without a hidden key
-// are left alone.
-__device__ __noinline__ void mask_block_tmem(uint32_t sa, int left) {
+// Of 32 * chunks keys, those at or past the row's `left` become -inf in this
+// warp's TMEM lanes; 32 keys at a time, chunks without a hidden key are left
+// alone.
+__device__ __noinline__ void mask_block_tmem(uint32_t sa, int left, int chunks) {
   uint32_t ninf[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) ninf[i] = NEG_INF_BITS;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < chunks; ++c) {
     const int lim = left - 32 * c;
     if (__all_sync(0xffffffffu, lim >= 32)) continue;
     if (__all_sync(0xffffffffu, lim <= 0)) {
@@ -220,6 +231,15 @@ __device__ __noinline__ void mask_block_tmem(uint32_t sa, int left) {
     tmem_st32(sa + 32 * c, x);
   }
   tmem_wait_st();
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 __device__ __forceinline__ float chunk_max(const uint32_t (&s)[32]) {
@@ -421,9 +441,9 @@ __device__ __forceinline__ uint32_t row_factor(int byte, int top) {
 
 // The largest scale byte of a block's rows below `left`; whole warp, lane l
 // brings the bytes of rows 4 l .. 4 l + 3.  Rows of byte 255 (NaN) do not count,
-// nor, where the bytes are too far apart for one exponent to serve, rows of
-// zeros, which the writer gives byte 127: their codes are looked up in the
-// cache (not in the staging area: a block's values come after its scales).
+// nor rows of zeros, which the writer gives byte 127: where that is the largest
+// byte, the codes are looked up in the cache (not in the staging area: a block's
+// values come after its scales).
 template <int FMT>
 __device__ __noinline__ int block_top_slow(const ChunkArgs &a, const TileInfo &x, int hk, int j,
                                            bool value, const uint8_t *scales, int lane, int left) {
@@ -457,57 +477,42 @@ __device__ __noinline__ int block_top_slow(const ChunkArgs &a, const TileInfo &x
 template <int FMT>
 __device__ __forceinline__ int block_top(const ChunkArgs &a, const TileInfo &x, int hk, int j,
                                          bool value, const uint8_t *scales, int lane) {
-  const uint32_t w = reinterpret_cast<const uint32_t *>(scales)[lane];
-  const int left = x.kv - j * BN, mine = left - 4 * lane;  // rows that count: the block's, this lane's
-  const uint32_t mask = mine >= 4 ? 0xffffffffu : mine <= 0 ? 0u : (1u << (8 * mine)) - 1u;
-  const uint32_t u = w & mask, v = w | ~mask;
-  const uint32_t hi = max(max(u & 255u, (u >> 8) & 255u), max((u >> 16) & 255u, u >> 24));
-  const uint32_t lo = min(min(v & 255u, (v >> 8) & 255u), min((v >> 16) & 255u, v >> 24));
-  const int top = (int)__reduce_max_sync(0xffffffffu, hi);
-  const int low = (int)__reduce_min_sync(0xffffffffu, lo);
-  if (top < 255 && top - low <= 15) return top;
+  uint32_t w = reinterpret_cast<const uint32_t *>(scales)[lane];
+  const int left = x.kv - j * BN;  // rows of the block that count
+  if (left < BN) {
+    const int mine = left - 4 * lane;
+    w &= mine >= 4 ? 0xffffffffu : mine <= 0 ? 0u : (1u << (8 * mine)) - 1u;
+  }
+  const uint32_t m = __vmaxu2(w & 0x00ff00ffu, (w >> 8) & 0x00ff00ffu);
+  const int top = (int)__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+  if (top != 255 && top != 127 && top != 0) return top;
   return block_top_slow<FMT>(a, x, hk, j, value, scales, lane, left);
 }
 
-// One staged block to an fp16 tile: warp w of four takes rows 32 w .. 32 w + 31,
-// eight lanes a row (sixteen codes each), four rows a step.  The next step's
-// codes are read before a step's stores (a store orders every later load
-// behind it).  The steps are a loop: twenty warps in eight roles share the
-// instruction cache, and unrolled they ran three times slower, at its refill
-// rate.  Lane l forms the factor of row 32 w + l; a row's lanes fetch it by a
-// shuffle.  Lanes of the upper half of a row store their two 16-byte chunks in
-// the other order, so that a store instruction's eight lanes of a row meet
-// eight different bank groups.
-// rows_left: rows at or past it become zero (values of the last block).
-template <int FMT>
-__device__ __forceinline__ void convert_block(const uint8_t *stage, uint32_t tile, int w, int lane,
-                                              int top, int rows_left) {
-  const int cg = lane & 7, rl = lane >> 3;
-  const bool upper = cg >= 4;
-  const uint32_t fl = row_factor(stage[Layout<FMT>::SCALES + w * 32 + lane], top);
-  const int r0 = w * 32 + rl;
-  const uint8_t *src = stage + r0 * Cfg<FMT>::ROW + cg * (Cfg<FMT>::ROW / 8);
-  const uint8_t *bsrc = stage + Cfg<FMT>::CODES + r0 * (D / 16) + cg;
-  // Chunk c of row r sits at c ^ (r % 8); the lane's pair is 2 cg % 8 and the
-  // next, and r % 8 is rl or rl + 4 in turn.
-  const uint32_t dst = tile + (upper ? HALF_BYTES : 0) + r0 * 128;
-  uint32_t at = ((((2 * cg) & 7) ^ rl) * 16) ^ (upper ? 16u : 0u);
-  uint4 c{};
-  uint32_t b = 0;
-  auto load = [&](int i) {
+// Step g of a staged block to an fp16 tile: rows 4 g .. 4 g + 3, eight lanes a
+// row, sixteen codes each.  Lanes of the upper half of a row store their two
+// 16-byte chunks in the other order, so that a store instruction's eight lanes
+// of a row meet eight different bank groups.
+template <int FMT> struct Step {
+  uint4 c;
+  uint32_t b, byte;
+
+  __device__ __forceinline__ void load(const uint8_t *stage, int g, int lane) {
+    const int r = g * 4 + (lane >> 3), cg = lane & 7;
+    byte = stage[Layout<FMT>::SCALES + r];
     if constexpr (FMT == kKvE4m3) {
-      c = *reinterpret_cast<const uint4 *>(src + i * 4 * D);
+      c = *reinterpret_cast<const uint4 *>(stage + r * D + cg * 16);
     } else {
-      const uint2 v = *reinterpret_cast<const uint2 *>(src + i * 4 * (D / 2));
+      const uint2 v = *reinterpret_cast<const uint2 *>(stage + r * (D / 2) + cg * 8);
       c.x = v.x;
       c.y = v.y;
-      b = bsrc[i * 4 * (D / 16)];
+      b = stage[Cfg<FMT>::CODES + r * (D / 16) + cg];
     }
-  };
-  load(0);
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    uint32_t f = __shfl_sync(0xffffffffu, fl, i * 4 + rl);
+  }
+  __device__ __forceinline__ void store(uint32_t tile, int g, int lane, int top, int rows_left) {
+    const int rl = lane >> 3, cg = lane & 7;
+    const bool upper = cg >= 4;
+    uint32_t f = row_factor(byte, top);
     uint32_t h[8];
     if constexpr (FMT == kKvE4m3) {
       e4m3x4(c.x, h[0], h[1]);
@@ -521,25 +526,41 @@ __device__ __forceinline__ void convert_block(const uint8_t *stage, uint32_t til
       e4m3x4(b * 0x101u, s0, s1);  // the block scale as a pair
       f = mul_f16x2(s0, f);
     }
-    load(min(i + 1, 7));
 #pragma unroll
     for (int k = 0; k < 8; ++k) h[k] = mul_f16x2(h[k], f);
-    if (rows_left < BN && r0 + i * 4 >= rows_left) {
+    if (rows_left < BN && g * 4 + rl >= rows_left) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) h[k] = 0u;
     }
-    if (upper) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t t = h[k];
-        h[k] = h[k + 4];
-        h[k + 4] = t;
-      }
+    // Chunk c of row r sits at c ^ (r % 8); the lane's pair is 2 cg % 8 and the next.
+    const uint32_t row = tile + (upper ? HALF_BYTES : 0) + (g * 4 + rl) * 128;
+    const uint32_t a0 = row + ((((2 * cg) & 7) ^ ((g & 1) * 4 + rl)) * 16), a1 = a0 ^ 16u;
+    if (!upper) {
+      st_shared_v4(a0, h[0], h[1], h[2], h[3]);
+      st_shared_v4(a1, h[4], h[5], h[6], h[7]);
+    } else {
+      st_shared_v4(a1, h[4], h[5], h[6], h[7]);
+      st_shared_v4(a0, h[0], h[1], h[2], h[3]);
     }
-    const uint32_t a0 = dst + i * 512 + at;
-    st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-    st_shared_v4(a0 ^ 16u, h[4], h[5], h[6], h[7]);
-    at ^= 64u;
+  }
+};
+
+// Warp w of n takes steps w, w + n, ..; two at a time, their codes read before
+// the first store (a store orders every later load behind it).  The steps are a
+// loop: twenty warps in eight roles share the instruction cache, and unrolled
+// they ran three times slower, at its refill rate.
+// rows_left: rows at or past it become zero (values of the last block).
+template <int FMT>
+__device__ __forceinline__ void convert_block(const uint8_t *stage, uint32_t tile, int w, int n,
+                                              int lane, int top, int rows_left) {
+#pragma unroll 1
+  for (int g = w; g < BN / 4; g += 2 * n) {
+    Step<FMT> s, t;
+    s.load(stage, g, lane);
+    const bool two = g + n < BN / 4;
+    if (two) t.load(stage, g + n, lane);
+    s.store(tile, g, lane, top, rows_left);
+    if (two) t.store(tile, g + n, lane, top, rows_left);
   }
 }
 
@@ -571,7 +592,8 @@ __device__ __forceinline__ void convert_q(uint32_t tile, int r0, int r1, int lan
   }
 }
 
-template <int FMT>
+// REP: tiles of at most 32 rows, once in each quarter of the products' 128 rows.
+template <int FMT, bool REP>
 __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     chunk_paged_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
@@ -619,12 +641,11 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     mbar_init(bar(&sh.q_full), 1);
     mbar_init(bar(&sh.q_ready), 8);
     for (int i = 0; i < NR; ++i) {
-      mbar_init(bar(&sh.ready[i]), (QUANT ? 4 : 1) + 1);  // the key tile, the S buffer
+      if (!QUANT) mbar_init(bar(&sh.ready[i]), 2);  // the key tile, the S buffer
       mbar_init(bar(&sh.qk_done[i]), 1);
     }
-    for (int i = 0; i < NS; ++i) mbar_arrive(bar(&sh.ready[i]));  // buffers free at first
     for (int i = 0; i < NV; ++i) {
-      mbar_init(bar(&sh.v_full[i]), QUANT ? 4 : 1);
+      if (!QUANT) mbar_init(bar(&sh.v_full[i]), 1);
       mbar_init(bar(&sh.v_empty[i]), 1);
     }
     for (int i = 0; i < NS; ++i) mbar_init(bar(&sh.pv_done[i]), 1);
@@ -635,8 +656,6 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     for (int i = 0; i < 3; ++i) {
       mbar_init(bar(&sh.kc_full[i]), 1);
       mbar_init(bar(&sh.vc_full[i]), 1);
-      mbar_init(bar(&sh.kc_empty[i]), 4);
-      mbar_init(bar(&sh.vc_empty[i]), 4);
     }
     sh.abort = 0;
     fence_mbar_init();
@@ -655,9 +674,18 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     if (lane == 0) {
       // Readers of a decision: the P.V issuer and the exponential warps that have
       // rows; with a threshold also the value producer and converters.
-      const int nq = (x.ntok * a.G + 31) / 32;
-      const int readers = 1 + nq + (x.ln_lam == -INFINITY ? 0 : QUANT ? 5 : 1);
+      const int nq = REP ? NQ : (x.ntok * a.G + 31) / 32, nc = 8 - nq;  // see below
+      const int readers = 1 + nq + (x.ln_lam == -INFINITY ? 0 : QUANT ? 1 + nc : 1);
       for (int i = 0; i < NDEC; ++i) mbar_init(bar(&sh.dec_read[i]), readers);
+      if constexpr (QUANT) {
+        for (int i = 0; i < NR; ++i) mbar_init(bar(&sh.ready[i]), nc + 1);
+        for (int i = 0; i < NV; ++i) mbar_init(bar(&sh.v_full[i]), nc);
+        for (int i = 0; i < 3; ++i) {
+          mbar_init(bar(&sh.kc_empty[i]), nc);
+          mbar_init(bar(&sh.vc_empty[i]), nc);
+        }
+      }
+      for (int i = 0; i < NS; ++i) mbar_arrive(bar(&sh.ready[i]));  // S buffers free at first
       for (int i = 0; i < NS; ++i) mbar_init(bar(&sh.p_full[i]), nq);
       mbar_init(bar(&sh.l_full), nq);
       fence_mbar_init();
@@ -666,9 +694,13 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     producer_init(a, pages, x, hk, lane);
     if (lane == 0) {
       const uint64_t once = policy_evict_first();
-      mbar_expect_tx(bar(&sh.q_full), 2 * 128 * a.G * q_box_tokens);
-      tma_load_3d(base + L::Q, &tm_q, bar(&sh.q_full), 0, hk * a.G, x.tok0, once);
-      tma_load_3d(base + L::Q + HALF_BYTES, &tm_q, bar(&sh.q_full), 64, hk * a.G, x.tok0, once);
+      constexpr int COPIES = REP ? 4 : 1;
+      mbar_expect_tx(bar(&sh.q_full), COPIES * 2 * 128 * a.G * q_box_tokens);
+      for (int i = 0; i < COPIES; ++i) {
+        const uint32_t dst = base + L::Q + i * 32 * 128;
+        tma_load_3d(dst, &tm_q, bar(&sh.q_full), 0, hk * a.G, x.tok0, once);
+        tma_load_3d(dst + HALF_BYTES, &tm_q, bar(&sh.q_full), 64, hk * a.G, x.tok0, once);
+      }
     }
     __syncwarp();
 #pragma unroll 1
@@ -682,6 +714,14 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   const int nb = x.nb;
   const int rows = x.s >= 0 ? x.ntok * a.G : 0;
   const bool dense = x.ln_lam == -INFINITY;
+  // Quarters that have rows; the deciders (exponential warps) of the others help
+  // the key (value) converters, so a decode step has seven of each.
+  const int nq = REP ? NQ : (rows + 31) / 32, nc = 8 - nq, quarter = warp & 3;
+  const bool k_conv = QUANT && ((warp >= WARP_KC && warp < WARP_VC) || (warp < NQ && quarter >= nq));
+  const bool v_conv = QUANT && (warp >= WARP_VC || (warp >= NQ && warp < 2 * NQ && quarter >= nq));
+  const int cw = warp >= WARP_KC ? quarter : 4 + quarter - nq;  // a converter's number
+  // End of the query rows in [r, r + 16).
+  auto q_end = [&](int r) { return min(r + 16, REP ? (r & ~31) + rows : rows); };
 
   if (x.s < 0) {
     // no tile for this CTA
@@ -812,12 +852,11 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         ++kc;
       }
     }
-  } else if (QUANT && warp >= WARP_KC && warp < WARP_VC) {
+  } else if (k_conv) {
     // ------------------------------------------------------ key converters --
     if constexpr (QUANT) {
-      const int w = warp - WARP_KC;
-      if (wait_warp(&sh.q_full, 0)) {
-        convert_q(base + L::Q, w * 16, min(rows, w * 16 + 16), lane, sh.qexp);
+      if (cw < 4 && wait_warp(&sh.q_full, 0)) {
+        convert_q(base + L::Q, cw * 16, q_end(cw * 16), lane, sh.qexp);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&sh.q_ready));
@@ -829,11 +868,11 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         if (c >= NKD && !wait_warp(&sh.qk_done[(c - NKD) % NR], (c - NKD) / NR)) break;
         const uint8_t *stage = smem_raw + L::KC + (c % NC) * L::KSTAGE;
         const int ek = block_top<FMT>(a, x, hk, x.j0 + c, false, stage + L::SCALES, lane);
-        if (w == 0) {
+        if (cw == 0) {
           const int ev = block_top<FMT>(a, x, hk, x.j0 + c, true, stage + L::SCALES + BN, lane);
           if (lane == 0) sh.esc[c % NE] = (uint16_t)(ek | (ev << 8));
         }
-        convert_block<FMT>(stage, base + L::K + (c % NKD) * TILE_BYTES, w, lane, ek, BN);
+        convert_block<FMT>(stage, base + L::K + (c % NKD) * TILE_BYTES, cw, nc, lane, ek, BN);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -842,12 +881,11 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         }
       }
     }
-  } else if (QUANT && warp >= WARP_VC) {
+  } else if (v_conv) {
     // ---------------------------------------------------- value converters --
     if constexpr (QUANT) {
-      const int w = warp - WARP_VC;
-      if (wait_warp(&sh.q_full, 0)) {
-        convert_q(base + L::Q, 64 + w * 16, min(rows, 64 + w * 16 + 16), lane, sh.qexp);
+      if (cw < 4 && wait_warp(&sh.q_full, 0)) {
+        convert_q(base + L::Q, 64 + cw * 16, q_end(64 + cw * 16), lane, sh.qexp);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&sh.q_ready));
@@ -866,7 +904,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         if (vi >= NV && !wait_warp(&sh.v_empty[vi % NV], vi / NV - 1)) break;
         const uint8_t *stage = smem_raw + L::VC + (vi % NC) * L::VSTAGE;
         const int ev = block_top<FMT>(a, x, hk, x.j0 + c, true, stage + L::SCALES, lane);
-        convert_block<FMT>(stage, base + L::V + (vi % NV) * TILE_BYTES, w, lane, ev,
+        convert_block<FMT>(stage, base + L::V + (vi % NV) * TILE_BYTES, cw, nc, lane, ev,
                            x.kv - (x.j0 + c) * BN);
         fence_proxy_async_smem();
         __syncwarp();
@@ -877,18 +915,18 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         ++vi;
       }
     }
-  } else if ((warp & 3) * 32 < rows) {
+  } else if (quarter < nq) {
     // ------------------------------------------------- deciders / exponentials --
     const bool decider = warp < NQ;
-    const int quarter = warp & 3;
-    const int r = quarter * 32 + lane;  // row == TMEM lane
-    const bool valid = r < rows;
-    const int nq = (rows + 31) / 32;    // quarters that have rows
-    const int tok = r / a.G;
+    const int r = quarter * 32 + lane;  // TMEM lane
+    const int row = REP ? lane : r;     // row of the tile
+    const bool valid = row < rows;
+    const int tok = row / a.G;
     const int limit = a.causal && valid ? x.pos0 + tok + 1 : x.kv;  // the row sees keys below it
     const int min_limit = a.causal ? x.pos0 + 1 : x.kv;             // the tile's smallest
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const float sl2 = a.scale * kLog2e;
+    float t2 = -INFINITY;  // running max of (row max + E_v), the exponentials' reference
     float mref = -INFINITY, l = 0.f;
     int kc = 0;
     bool ok = true;
@@ -907,7 +945,6 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     if (decider) {
       const float c2 = x.ln_lam * kLog2e;
       float m2 = -INFINITY;  // running max (log2 units)
-      float t2 = -INFINITY;  // running max of (row max + E_v), the exponentials' reference
       uint32_t word = 0;
       uint32_t *bits = a.bits ? a.bits + ((((int64_t)x.s * a.Hkv + hk) * a.n_t + x.t) * a.n_splits + sp) * a.words
                               : nullptr;
@@ -919,11 +956,16 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         bool keep_vote = false;
         if (ok) {
           fence_after_sync();
-          const uint32_t sa = lane_base + (c % NS) * BN;
-          const int key0 = (x.j0 + c) * BN;
-          if (key0 + BN > min_limit) mask_block_tmem(sa, limit - key0);
+          const uint32_t sa = lane_base + (c % NS) * BN + (REP ? 32 * quarter : 0);
+          const int key0 = (x.j0 + c) * BN + (REP ? 32 * quarter : 0);
+          if (key0 + (REP ? 32 : BN) > min_limit) mask_block_tmem(sa, limit - key0, REP ? 1 : 4);
           float mt;
-          if constexpr (QUANT) {  // 20 warps: fewer registers a thread
+          if constexpr (REP) {
+            uint32_t x0[32];
+            tmem_ld32(sa, x0);
+            tmem_wait_ld_regs(x0);
+            mt = chunk_max(x0);
+          } else if constexpr (QUANT) {  // 20 warps: fewer registers a thread
             mt = -INFINITY;
 #pragma unroll 1
             for (int hh = 0; hh < 2; ++hh) {
@@ -952,14 +994,26 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
             ek = e & 255;
             ev = e >> 8;
           }
-          const float pm2 = mt * (QUANT ? block_sl2(ek) : sl2);
+          const float bl2 = QUANT ? block_sl2(ek) : sl2;
+          if constexpr (REP) {
+            if (!dense) {  // the rows' maxima over all four quarters' keys
+              sh.mdec[2][r] = mt;  // (read before the vote barrier of the last block)
+              named_bar_sync(kDeciderBarrier, NQ * 32);
+              mt = fmaxf(fmaxf(sh.mdec[2][lane], sh.mdec[2][32 + lane]),
+                         fmaxf(sh.mdec[2][64 + lane], sh.mdec[2][96 + lane]));
+            }
+          } else {
+            t2 = fmaxf(t2, mt * bl2 + (float)(ev - 127));
+            sh.mdec[c % NS][r] = t2;
+          }
+          const float pm2 = mt * bl2;
           // With ln(lambda) < 0, "rowmax - m_new < c" is "rowmax - m_old < c".
           const float diff = mt == -INFINITY ? -INFINITY : pm2 - m2;
           keep_vote = dense || !__all_sync(0xffffffffu, !valid || diff < c2 || mt == -INFINITY);
           m2 = fmaxf(m2, pm2);
-          t2 = fmaxf(t2, pm2 + (float)(ev - 127));
-          sh.mdec[c % NS][r] = t2;
           fence_before_sync();  // this warp's reads of S_j are complete
+        } else if (REP && !dense) {
+          named_bar_sync(kDeciderBarrier, NQ * 32);
         }
         const bool keep = bar_red_or(kDeciderBarrier, nq * 32, keep_vote);
         if (!ok) continue;
@@ -989,7 +1043,25 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(&sh.dec_read[c % NDEC]));
         if (!keep) continue;
-        const float mnew = sh.mdec[c % NS][r];
+        fence_after_sync();
+        const uint32_t sa = lane_base + (c % NS) * BN;  // masked by the deciders
+        int ek = 0, ev = 127;
+        if constexpr (QUANT) {
+          const int e = sh.esc[c % NE];
+          ek = e & 255;
+          ev = e >> 8;
+        }
+        const float bl2 = QUANT ? block_sl2(ek) : sl2;
+        uint32_t own[REP ? 32 : 1];  // REP: the scores of the quarter's 32 keys
+        float mnew;
+        if constexpr (REP) {
+          tmem_ld32(sa + 32 * quarter, own);
+          tmem_wait_ld_regs(own);
+          t2 = fmaxf(t2, chunk_max(own) * bl2 + (float)(ev - 127));
+          mnew = t2;
+        } else {
+          mnew = sh.mdec[c % NS][r];
+        }
         bool rescale = false;
         float alpha = 1.f;
         if (mref == -INFINITY) {
@@ -999,20 +1071,21 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
           mref = mnew;
           rescale = true;
         }
-        fence_after_sync();
-        const uint32_t sa = lane_base + (c % NS) * BN;  // masked by the deciders
         // A row without a visible key so far has only -inf scores: P = 0.
-        int ek = 0, ev = 127;
-        if constexpr (QUANT) {
-          const int e = sh.esc[c % NE];
-          ek = e & 255;
-          ev = e >> 8;
-        }
         const float nref = mref == -INFINITY ? 0.f : (float)(ev - 127) - mref;
-        const float bl2 = QUANT ? block_sl2(ek) : sl2;
         const uint64_t sl2x2 = f2(bl2, bl2), negref2 = f2(nref, nref);
         uint64_t acc2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-        if constexpr (QUANT) {
+        if constexpr (REP) {
+          // The quarter's 32 keys; zeros for the others (their scores in these
+          // lanes have no reader).
+          uint32_t pk[16], zero[16];
+          chunk_exp<QUANT>(own, sl2x2, negref2, acc2, pk);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) zero[i] = 0u;
+          tmem_st16(sa + 16 * quarter, pk);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) tmem_st16(sa + 16 * ((quarter + i) & 3), zero);
+        } else if constexpr (QUANT) {
 #pragma unroll 1
           for (int hh = 0; hh < 2; ++hh) {
             uint32_t s[32], pk[32];
@@ -1080,24 +1153,59 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
 
     // ---- epilogue: deciders take O columns [0,64), exponential warps [64,128)
     if (ok) ok = wait_warp(&sh.l_full, 0);
+    const int64_t orow = (int64_t)(x.tok0 + tok) * a.Hq + hk * a.G + (row - tok * a.G);
+    const int col0 = decider ? 0 : 64;
+    // Four consecutive columns of an output row.
+    auto put = [&](int64_t at, int col, float v0, float v1, float v2, float v3) {
+      if (a.n_splits == 1)
+        *reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.o + at * D + col) =
+            make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3));
+      else
+        *reinterpret_cast<float4 *>(a.o_part + (at * a.n_splits + sp) * D + col) =
+            make_float4(v0, v1, v2, v3);
+    };
+    float lrow = 0.f, lref = -INFINITY, w = 0.f;  // row sum, its reference, this lane's weight
     if (ok) {
       fence_after_sync();
-      const float lrow = sh.mdec[0][r];
-      const bool empty = lrow == 0.f;  // no key kept for this row
-      const float inv = empty ? 0.f : 1.f / lrow;
-      const int col0 = decider ? 0 : 64;
-      const int64_t orow = (int64_t)(x.tok0 + tok) * a.Hq + hk * a.G + (r - tok * a.G);
+      if constexpr (REP) {  // merge the quarters' states
+        float lq[NQ], mq[NQ];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          lq[i] = sh.mdec[0][i * 32 + lane];
+          mq[i] = sh.mdec[1][i * 32 + lane];
+          // A quarter that met no key of the row has no say in the reference.
+          if (lq[i] != 0.f) lref = fmaxf(lref, mq[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          const float wi = lq[i] == 0.f ? 0.f : ex2(mq[i] - lref);
+          lrow += lq[i] * wi;
+          if (i == quarter) w = wi;
+        }
+      } else {
+        lrow = sh.mdec[0][r];
+        lref = sh.mdec[1][r];
+        w = lrow == 0.f ? 0.f : 1.f;  // no key kept for this row: O = 0
+      }
+      const float inv = lrow == 0.f ? 0.f : w / lrow;
+      const bool none = w == 0.f;  // (the accumulator may hold anything)
 #pragma unroll 1
       for (int cc = 0; cc < 2; ++cc) {
         uint32_t o[32];
-        tmem_ld32(lane_base + TMEM_O + col0 + cc * 32, o);
+        const int col = col0 + cc * 32;
+        tmem_ld32(lane_base + TMEM_O + col, o);
         tmem_wait_ld_regs(o);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          o[i] = empty ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+          o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
         if (!valid) continue;
-        if (a.n_splits == 1) {
-          uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + orow * D + col0 + cc * 32);
+        if constexpr (REP) {
+          const uint32_t at = base + L::K + (uint32_t)((r * MERGE_STRIDE + col) * 4);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_shared_v4(at + q * 16, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        } else if (a.n_splits == 1) {
+          uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + orow * D + col);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             dst[q] = make_uint4(
@@ -1106,15 +1214,38 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
                 pack_bf16x2(__uint_as_float(o[8 * q + 4]), __uint_as_float(o[8 * q + 5])),
                 pack_bf16x2(__uint_as_float(o[8 * q + 6]), __uint_as_float(o[8 * q + 7])));
         } else {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.o_part + (orow * a.n_splits + sp) * D + col0 + cc * 32);
+          uint4 *dst = reinterpret_cast<uint4 *>(a.o_part + (orow * a.n_splits + sp) * D + col);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
-      if (valid && !decider)
+      if (valid && !decider && (!REP || quarter == 0))
         (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] =
-            empty ? -INFINITY : sh.mdec[1][r] * kLn2 + logf(lrow);
+            lrow == 0.f ? -INFINITY : lref * kLn2 + logf(lrow);
+    }
+    if constexpr (REP) {
+      // The four quarters' weighted rows stand in the key and value tiles, which
+      // nothing reads any more; 256 threads add them up, four columns each.
+      named_bar_sync(kMergeBarrier, 2 * NQ * 32);
+      if (ok) {
+#pragma unroll 1
+        for (int i = tid; i < rows * (D / 4); i += 2 * NQ * 32) {
+          const int rr = i / (D / 4), col = i % (D / 4) * 4;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const float4 u = *reinterpret_cast<const float4 *>(
+                smem_raw + L::K + ((q * 32 + rr) * MERGE_STRIDE + col) * 4);
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+          }
+          const int t = rr / a.G;
+          put((int64_t)(x.tok0 + t) * a.Hq + hk * a.G + (rr - t * a.G), col, v.x, v.y, v.z, v.w);
+        }
+      }
     }
   }
 
@@ -1206,15 +1337,22 @@ int64_t tiles_bound(int n_seq, int total, int max_chunk, int TT) {
   return by_len < by_total ? by_len : by_total;
 }
 
+template <int FMT, bool REP>
+cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                       const ChunkArgs &a, int q_tokens, unsigned grid, cudaStream_t s) {
+  constexpr uint32_t smem = Layout<FMT>::END + ((sizeof(Shared) + 15) / 16) * 16;
+  cudaError_t e = cudaFuncSetAttribute(chunk_paged_kernel<FMT, REP>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  chunk_paged_kernel<FMT, REP><<<grid, Cfg<FMT>::WARPS * 32, smem, s>>>(mq, mk, mv, a, q_tokens);
+  return cudaGetLastError();
+}
+
 template <int FMT>
 cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                        const ChunkArgs &a, int q_tokens, unsigned grid, cudaStream_t s) {
-  constexpr uint32_t smem = Layout<FMT>::END + ((sizeof(Shared) + 15) / 16) * 16;
-  cudaError_t e = cudaFuncSetAttribute(chunk_paged_kernel<FMT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  chunk_paged_kernel<FMT><<<grid, Cfg<FMT>::WARPS * 32, smem, s>>>(mq, mk, mv, a, q_tokens);
-  return cudaGetLastError();
+  return a.G * q_tokens <= 32 ? launch_one<FMT, true>(mq, mk, mv, a, q_tokens, grid, s)
+                              : launch_one<FMT, false>(mq, mk, mv, a, q_tokens, grid, s);
 }
 
 }  // namespace
