@@ -1,0 +1,676 @@
+// Decode over the quantised paged caches: attention of tiles of at most eight
+// rows (query heads of a KV head times new tokens) over E4M3 or NVFP4 pages, with
+// softmax-threshold block skipping (d = 128, 128-key blocks), on warp-level
+// m16n8k16 products.
+//
+// The mathematics is that of the chunk kernel (a tile of few rows of it).  Here
+// the keys are the 16 rows of a product and the tile's rows its 8 columns, so
+// codes go from shared memory to fp16 operand registers (one cvt per two codes)
+// and a row scale multiplies one score instead of 128 elements:
+//   S^T = K Q^T        A = codes of 16 keys, B = fp16 queries (2^x scaled)
+//   s_c = S_c * scale * 2^(e_k,c - x)         (log2 units)
+//   P_c = 2^(s_c + e_v,c - ref),  ref the running max of s_c + e_v,c of the warp
+//   O^T += V^T P       A = codes of 16 keys, transposed by byte pairs, B = P
+//   l += P_c 2^(-e_v,c)
+// An NVFP4 code times its block scale is an fp16 (exact); P is rounded to fp16,
+// whose smallest step, 2^-24, is that fraction of the largest contribution.
+//
+// One CTA per (sequence, KV head, split), two on an SM.  Eight warps share each
+// 128-key block, 16 keys a warp, each with its own running reference, row sums
+// and outputs, merged at the end as splits are; two more warps fetch keys and
+// values through TMA rings (two CTAs hold about 200 KB of cache in flight).
+// Why not tcgen05: its operands come from shared memory, and writing a block's
+// 64 KB there as fp16 costs more issue slots than the cache costs bandwidth
+// (16 sequences of 32768 tokens, E4M3: 418 us on that path).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "internal.h"
+#include "paged_common.cuh"
+#include "tc_common.cuh"
+
+namespace attn_skip {
+namespace {
+
+using namespace tc;
+
+constexpr int NCW = 8;            // compute warps
+constexpr int WARP_K = NCW, WARP_V = NCW + 1;
+constexpr int NT = (NCW + 2) * 32;
+constexpr int ROWS = 8;           // rows of a tile (columns of the products)
+constexpr int NDEC = 4;           // decision ring
+constexpr int kVoteBarrier = 1;
+constexpr int MERGE_STRIDE = D + 4;
+
+template <int FMT> struct Cfg;
+template <> struct Cfg<kKvE4m3> {
+  static constexpr int NST = 3;  // stages of keys, and of values
+  static constexpr uint32_t ROW = D, BS = 0;
+};
+template <> struct Cfg<kKvNvfp4> {
+  static constexpr int NST = 5;
+  static constexpr uint32_t ROW = D / 2, BS = BN * D / 16;
+};
+template <int FMT> struct Layout {
+  using C = Cfg<FMT>;
+  static constexpr uint32_t CODES = BN * C::ROW;
+  // Code tiles first (1024-byte aligned), then block scales and row scales: a
+  // key stage also has the row scales of its values, needed before they are.
+  static constexpr uint32_t K = 0, V = K + C::NST * CODES, KX = V + C::NST * CODES;
+  static constexpr uint32_t KXS = C::BS + 2 * BN, VX = KX + C::NST * KXS;
+  static constexpr uint32_t END = VX + C::NST * C::BS;
+};
+
+struct Shared {
+  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+  uint64_t dec_full[NDEC], dec_empty[NDEC];
+  int dec[NDEC];
+  float rmax[2][NCW][ROWS];        // row maxima of the warps' keys, blocks of either parity
+  float ml[2][NCW][ROWS];          // the warps' references and row sums
+  TileInfo tile;
+  int abort;
+};
+static_assert(2 * (Layout<kKvE4m3>::END + sizeof(Shared) + 1024) <= 228 * 1024, "two CTAs an SM");
+static_assert(2 * (Layout<kKvNvfp4>::END + sizeof(Shared) + 1024) <= 228 * 1024, "two CTAs an SM");
+static_assert(NCW * ROWS * MERGE_STRIDE * 4 <= Layout<kKvNvfp4>::KX, "merge area: the code tiles");
+
+// Key of the warp's sixteen that is row m of its products: chosen so that the
+// eight lanes of a 16-byte load (and the sixteen of an 8-byte load) meet
+// different banks of the swizzled tiles, for the key reads (rows m) and the
+// transposed value reads (rows 2 t, 2 t + 1, ..).
+template <int FMT> __device__ __forceinline__ int key_of(int m) {
+  if constexpr (FMT == kKvE4m3) return m;
+  const int b0 = m & 1, b1 = (m >> 1) & 1;
+  return (m & 12) | (b0 << 1) | (b1 ^ b0);
+}
+
+// Byte address of 16-byte chunk c of row r of a swizzled code tile.
+template <int FMT> __device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int r, int c) {
+  if constexpr (FMT == kKvE4m3) return tile + r * 128 + ((c ^ (r & 7)) << 4);
+  return tile + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 2^(byte - 127) as fp32; NaN for 255.
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return byte == 255u ? NAN : byte == 0u ? 5.877471754111438e-39f : __uint_as_float(byte << 23);
+}
+
+// Block j's rows into stage buffers: codes by TMA (swizzled), scales by bulk
+// copies; part by part, one lane a part.  Whole warp.
+template <int FMT>
+__device__ __forceinline__ void load_block(const ChunkArgs &a, Producer &p, const CUtensorMap *map,
+                                           bool value, int j, uint32_t codes, uint32_t extra,
+                                           uint32_t full, int lane) {
+  using C = Cfg<FMT>;
+  const int sub = p.sub;
+  const Part x = part_of(a, p, j, lane);
+  if (lane == 0)
+    mbar_expect_tx(full, x.n * sub * (C::ROW + C::BS / BN + (value ? 0 : 2)));
+  __syncwarp();
+  if (lane < x.n) {
+    const KvPages &g = a.pages;
+    const int64_t row = ((int64_t)x.page * g.Hkv + p.hk) * g.page_size + x.slot;
+    const uint32_t r0 = lane * sub;
+    tma_load_4d(codes + r0 * C::ROW, map, full, 0, x.slot, p.hk, x.page, p.policy);
+    if constexpr (FMT == kKvNvfp4)
+      bulk_load(extra + r0 * (D / 16), (value ? g.v_bs : g.k_bs) + row * (D / 16), sub * (D / 16),
+                full, p.policy);
+    if (!value) {
+      bulk_load(extra + C::BS + r0, g.k_scale + row, sub, full, p.policy);
+      bulk_load(extra + C::BS + BN + r0, g.v_scale + row, sub, full, p.policy);
+    }
+  }
+  __syncwarp();
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(NT, 2)
+    decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ ChunkArgs a) {
+  using C = Cfg<FMT>;
+  using L = Layout<FMT>;
+  constexpr int NST = C::NST;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Shared &sh = *reinterpret_cast<Shared *>(smem_raw + L::END);
+  const uint32_t base = smem_u32(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (base & 1023u) {  // the swizzled layouts need a 1024-byte aligned base
+    if (tid == 0) atomicOr(a.err, kErrLayout);
+    return;
+  }
+  const int sp = (int)(blockIdx.x % a.n_splits);
+  const int hk = (int)(blockIdx.x / a.n_splits) % a.Hkv;
+  const int ti = (int)(blockIdx.x / a.n_splits / a.Hkv);
+  volatile int *abort = &sh.abort;
+  auto wait_warp = [&](uint64_t *b, int phase) {
+    return __all_sync(0xffffffffu, mbar_wait_shared(smem_u32(b), phase & 1, abort, a.err));
+  };
+
+  if (tid == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(smem_u32(&sh.k_full[i]), 1);
+      mbar_init(smem_u32(&sh.v_full[i]), 1);
+      mbar_init(smem_u32(&sh.k_empty[i]), NCW);
+      mbar_init(smem_u32(&sh.v_empty[i]), NCW);
+    }
+    for (int i = 0; i < NDEC; ++i) {
+      mbar_init(smem_u32(&sh.dec_full[i]), 1);
+      mbar_init(smem_u32(&sh.dec_empty[i]), 1);  // the value producer
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == WARP_K) locate(a, ti, sp, lane, blockIdx.x == 0, &sh.tile);
+  __syncthreads();
+  const TileInfo x = sh.tile;
+  const int nb = x.nb;
+  const int rows = x.s >= 0 ? x.ntok * a.G : 0;
+  const bool dense = x.ln_lam == -INFINITY;
+
+  if (x.s < 0) return;
+  if (nb == 0) {  // no visible key: O = 0, LSE = -inf (one split), or a partial of no weight
+    for (int i = tid; i < rows * (D / 8); i += NT) {
+      const int r = i / (D / 8);
+      const int64_t orow = (int64_t)(x.tok0 + r / a.G) * a.Hq + hk * a.G + r % a.G;
+      if (a.n_splits == 1)
+        reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + orow * D)[i % (D / 8)] =
+            make_uint4(0, 0, 0, 0);
+      if (i % (D / 8) == 0)
+        (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] = -INFINITY;
+    }
+    return;
+  }
+
+  if (warp >= WARP_K) {
+    // ----------------------------------------------------------- producers --
+    const bool value = warp == WARP_V;
+    fence_proxy_async_smem();  // the barriers, for every lane's copies
+    Producer pages;
+    producer_init(a, pages, x, hk, lane);
+    uint64_t *full = value ? sh.v_full : sh.k_full, *empty = value ? sh.v_empty : sh.k_empty;
+    int n = 0;  // blocks fetched
+#pragma unroll 1
+    for (int c = 0; c < nb && !*abort; ++c) {
+      if (value && !dense) {  // (a dense tile keeps every block)
+        if (!wait_warp(&sh.dec_full[c % NDEC], c / NDEC)) break;
+        const int keep = sh.dec[c % NDEC];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.dec_empty[c % NDEC]));
+        if (!keep) continue;
+      }
+      const int s = n % NST;
+      if (n >= NST && !wait_warp(&empty[s], n / NST - 1)) break;
+      load_block<FMT>(a, pages, value ? &tm_v : &tm_k, value, x.j0 + c,
+                      base + (value ? L::V : L::K) + s * L::CODES,
+                      base + (value ? L::VX + s * C::BS : L::KX + s * L::KXS), smem_u32(&full[s]),
+                      lane);
+      ++n;
+    }
+    if (!value && __any_sync(0xffffffffu, pages.bad) && lane == 0) atomicOr(a.err, kErrBadArg);
+    if (lane == 0) {  // the last load of each stage has landed before exit
+#pragma unroll 1
+      for (int s = 0; s < NST && s < n; ++s)
+        mbar_wait_drain(smem_u32(&full[s]), ((s + ((n - 1 - s) / NST) * NST) / NST) & 1);
+    }
+    __syncthreads_or(0);  // with the merge below
+    return;
+  }
+
+  // ------------------------------------------------------------ computation --
+  // Lane (g, t): products' row g (and g + 8), columns 2 t, 2 t + 1.
+  const int g = lane >> 2, t = lane & 3;
+  // Queries: row n = g of the tile, dims 32 t .. 32 t + 31; in k-step s, k = 2 t,
+  // 2 t + 1 are dims 32 t + 4 s, + 1 and k = 2 t + 8, + 9 are + 2, + 3.
+  uint32_t qf[16];
+  float qs[2];  // scale * log2(e) * 2^-x of rows 2 t, 2 t + 1
+  int limit[2]; // these rows see keys below it
+  {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = 0u;
+    if (g < rows) {
+      const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q + (int64_t)(x.tok0 + g / a.G) * a.q_tok_stride +
+                               (hk * a.G + g % a.G) * D + 32 * t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+      m = fmaxf(m, fmaxf(isfinite(lo) ? fabsf(lo) : 0.f, isfinite(hi) ? fabsf(hi) : 0.f));
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // The largest 2^e with max|q| 2^e <= 2^15.
+    const int b = __float_as_int(m);
+    int e = 15 + 127 - (b >> 23) - ((b & 0x7fffff) != 0 ? 1 : 0);
+    e = m > 0.f ? min(e, 100) : 0;
+    const float f = __int_as_float((e + 127) << 23);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      qf[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+    const float mine = a.scale * kLog2e * __int_as_float((127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      qs[i] = __shfl_sync(0xffffffffu, mine, (2 * t + i) * 4);
+      limit[i] = a.causal && 2 * t + i < rows ? x.pos0 + (2 * t + i) / a.G + 1 : x.kv;
+    }
+  }
+  const int min_limit = a.causal ? x.pos0 + 1 : x.kv;
+  const float c2 = x.ln_lam * kLog2e;
+  const int k0 = warp * 16;  // the warp's keys of a block
+  const int kr0 = k0 + key_of<FMT>(g), kr1 = kr0 + 8;
+  // Values: keys of k = 2 t, 2 t + 1, 2 t + 8, 2 t + 9; dims 16 g .. 16 g + 15, of
+  // which 16 g + 2 i is row g of m-tile i and 16 g + 2 i + 1 its row g + 8.
+  const int vr0 = k0 + key_of<FMT>(2 * t), vr1 = k0 + key_of<FMT>(2 * t + 1);
+
+  float o[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m2[2] = {-INFINITY, -INFINITY};  // running max of the split (log2 units), with a threshold
+  uint32_t word = 0;
+  uint32_t *bits = a.bits ? a.bits + ((((int64_t)x.s * a.Hkv + hk) * a.n_t + x.t) * a.n_splits + sp) * a.words
+                          : nullptr;
+  bool ok = true;
+  int vi = 0;  // kept blocks
+#pragma unroll 1
+  for (int c = 0; c < nb; ++c) {
+    const int s = c % NST, j = x.j0 + c;
+    // After a failed wait the loop runs on (every later wait fails at once), so
+    // that the warps meet the vote barriers equally often.
+    if (ok) ok = wait_warp(&sh.k_full[s], c / NST);
+    const int left = x.kv - j * BN;  // rows of the block below kv
+    float p[2][2];                   // [key g, g + 8][row 2 t, 2 t + 1]: scores, then P
+    float ev[2], inv[2];             // the keys' value exponents and 2^-e_v
+    {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t kx = base + L::KX + s * L::KXS, kt = base + L::K + s * L::CODES;
+      if constexpr (FMT == kKvE4m3) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 u = lds128(chunk_at<FMT>(kt, kr0, 2 * t + h));
+          const uint4 v = lds128(chunk_at<FMT>(kt, kr1, 2 * t + h));
+          const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4(uw[i], a0, a2);
+            e4m3x4(vw[i], a1, a3);
+            const int st = 4 * h + i;
+            mma16816(acc, a0, a1, a2, a3, qf[2 * st], qf[2 * st + 1]);
+          }
+        }
+      } else {
+        const uint4 u = lds128(chunk_at<FMT>(kt, kr0, t)), v = lds128(chunk_at<FMT>(kt, kr1, t));
+        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+        uint32_t us[2], vs[2];  // the scales of the lane's two blocks of sixteen, as pairs
+        {
+          const uint32_t b0 = lds16(kx + kr0 * 8 + 2 * t), b1 = lds16(kx + kr1 * 8 + 2 * t);
+          e4m3x4(__byte_perm(b0, 0, 0x1100), us[0], us[1]);
+          e4m3x4(__byte_perm(b1, 0, 0x1100), vs[0], vs[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // eight elements of a row: two k-steps
+          uint32_t x0[4], x1[4];
+          e2m1x8(uw[i], x0);
+          e2m1x8(vw[i], x1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x0[k] = mul_f16x2(x0[k], us[i >> 1]);
+            x1[k] = mul_f16x2(x1[k], vs[i >> 1]);
+          }
+          mma16816(acc, x0[0], x1[0], x0[1], x1[1], qf[4 * i], qf[4 * i + 1]);
+          mma16816(acc, x0[2], x1[2], x0[3], x1[3], qf[4 * i + 2], qf[4 * i + 3]);
+        }
+      }
+      const uint32_t sc = kx + C::BS;
+      const uint32_t eb0 = lds8(sc + kr0), eb1 = lds8(sc + kr1);
+      const uint32_t vb0 = lds8(sc + BN + kr0), vb1 = lds8(sc + BN + kr1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.k_empty[s]));  // the stage is in registers
+      const float f0 = scale_of(eb0), f1 = scale_of(eb1);
+      p[0][0] = acc[0] * (qs[0] * f0);
+      p[0][1] = acc[1] * (qs[1] * f0);
+      p[1][0] = acc[2] * (qs[0] * f1);
+      p[1][1] = acc[3] * (qs[1] * f1);
+      ev[0] = vb0 == 255u ? NAN : (float)((int)vb0 - 127);
+      ev[1] = vb1 == 255u ? NAN : (float)((int)vb1 - 127);
+      inv[0] = __uint_as_float(max(1, 254 - (int)vb0) << 23);
+      inv[1] = __uint_as_float(max(1, 254 - (int)vb1) << 23);
+    }
+    if (j * BN + BN > min_limit) {  // keys that a row does not see
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int key = j * BN + (k ? kr1 : kr0);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          if (key >= limit[n]) {
+            p[k][n] = -INFINITY;
+          }
+        if (key >= limit[0] && key >= limit[1]) ev[k] = 0.f;  // (a row's scale may be NaN)
+      }
+    }
+    if (!dense) {
+      // The rows' maxima over the block: this warp's keys, then all eight warps.
+      bool keep = false;
+      if (ok) {
+        float mt[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float m = fmaxf(p[0][n], p[1][n]);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          mt[n] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        }
+        if (g == 0) {
+          sh.rmax[c & 1][warp][2 * t] = mt[0];
+          sh.rmax[c & 1][warp][2 * t + 1] = mt[1];
+        }
+      }
+      named_bar_sync(kVoteBarrier, NCW * 32);
+      if (ok) {
+        bool vote = true;  // this lane's rows leave the block out
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float m = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < NCW; ++w) m = fmaxf(m, sh.rmax[c & 1][w][2 * t + n]);
+          // With ln(lambda) < 0, "rowmax - m_new < c" is "rowmax - m_old < c".
+          const float diff = m == -INFINITY ? -INFINITY : m - m2[n];
+          vote = vote && (2 * t + n >= rows || diff < c2 || m == -INFINITY);
+          m2[n] = fmaxf(m2[n], m);
+        }
+        keep = !__all_sync(0xffffffffu, vote);  // the same in every warp
+        if (tid == 0) {
+          if (c < NDEC || mbar_wait_shared(smem_u32(&sh.dec_empty[c % NDEC]), (c / NDEC - 1) & 1, abort, a.err)) {
+            sh.dec[c % NDEC] = keep ? 1 : 0;
+            mbar_arrive(smem_u32(&sh.dec_full[c % NDEC]));
+          }
+          if (bits) {
+            if (!keep) word |= 1u << (c & 31);
+            if ((c & 31) == 31 || c == nb - 1) {
+              bits[c >> 5] = word;
+              word = 0;
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (!keep) continue;
+    }
+    if (!ok) continue;
+    // The reference moves when a key's s + e_v passes it by more than 2^8 (or it
+    // is the row's first): then by the warp's maximum.
+    float y[2][2];
+    bool move = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        y[k][n] = p[k][n] + ev[k];
+        if (p[k][n] == -INFINITY) y[k][n] = -INFINITY;
+        move |= y[k][n] > ref[n] + kRescaleLog2;  // (-inf is not above -inf)
+      }
+    if (__any_sync(0xffffffffu, move)) {
+      float al[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float m = fmaxf(y[0][n], y[1][n]);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        const float to = fmaxf(ref[n], m);
+        al[n] = to == -INFINITY ? 1.f : ex2(ref[n] - to);
+        ref[n] = to;
+        l[n] *= al[n];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i][0] *= al[0];
+        o[i][1] *= al[1];
+        o[i][2] *= al[0];
+        o[i][3] *= al[1];
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float r = ref[n] == -INFINITY ? 0.f : ref[n];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        p[k][n] = ex2(y[k][n] - r);
+        l[n] = fmaf(p[k][n], inv[k], l[n]);
+      }
+    }
+    // P as the B operand: key pairs of row g.
+    const uint32_t b0 = transpose8x8(pack_f16x2(p[0][0], p[0][1]));
+    const uint32_t b1 = transpose8x8(pack_f16x2(p[1][0], p[1][1]));
+
+    const int vs = vi % NST;
+    ok = wait_warp(&sh.v_full[vs], vi / NST);
+    if (!ok) continue;
+    const uint32_t vt = base + L::V + vs * L::CODES;
+    if constexpr (FMT == kKvE4m3) {
+      uint4 r0 = lds128(chunk_at<FMT>(vt, vr0, g)), r1 = lds128(chunk_at<FMT>(vt, vr1, g));
+      uint4 r2 = lds128(chunk_at<FMT>(vt, vr0 + 8, g)), r3 = lds128(chunk_at<FMT>(vt, vr1 + 8, g));
+      if (left < BN) {  // rows at or past kv may hold anything
+        if (vr0 >= left) r0 = make_uint4(0, 0, 0, 0);
+        if (vr1 >= left) r1 = make_uint4(0, 0, 0, 0);
+        if (vr0 + 8 >= left) r2 = make_uint4(0, 0, 0, 0);
+        if (vr1 + 8 >= left) r3 = make_uint4(0, 0, 0, 0);
+      }
+      const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+      const uint32_t w2[4] = {r2.x, r2.y, r2.z, r2.w}, w3[4] = {r3.x, r3.y, r3.z, r3.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // four dims: two m-tiles
+        uint32_t a0, a1, a2, a3;
+        e4m3x4(__byte_perm(w0[i], w1[i], 0x5140), a0, a1);
+        e4m3x4(__byte_perm(w2[i], w3[i], 0x5140), a2, a3);
+        mma16816(o[2 * i], a0, a1, a2, a3, b0, b1);
+        e4m3x4(__byte_perm(w0[i], w1[i], 0x7362), a0, a1);
+        e4m3x4(__byte_perm(w2[i], w3[i], 0x7362), a2, a3);
+        mma16816(o[2 * i + 1], a0, a1, a2, a3, b0, b1);
+      }
+    } else {
+      // The lane's sixteen dims are one block: eight bytes of half a chunk.
+      auto row8 = [&](int r) { return lds64(chunk_at<FMT>(vt, r, g >> 1) + (g & 1) * 8); };
+      const uint32_t vx = base + L::VX + vs * C::BS;
+      uint2 r0 = row8(vr0), r1 = row8(vr1), r2 = row8(vr0 + 8), r3 = row8(vr1 + 8);
+      uint32_t e0 = lds8(vx + vr0 * 8 + g), e1 = lds8(vx + vr1 * 8 + g);
+      uint32_t e2 = lds8(vx + (vr0 + 8) * 8 + g), e3 = lds8(vx + (vr1 + 8) * 8 + g);
+      if (left < BN) {
+        if (vr0 >= left) r0 = make_uint2(0, 0), e0 = 0;
+        if (vr1 >= left) r1 = make_uint2(0, 0), e1 = 0;
+        if (vr0 + 8 >= left) r2 = make_uint2(0, 0), e2 = 0;
+        if (vr1 + 8 >= left) r3 = make_uint2(0, 0), e3 = 0;
+      }
+      uint32_t s01, s23;
+      e4m3x4(e0 | (e1 << 8) | (e2 << 16) | (e3 << 24), s01, s23);
+      const uint32_t w0[2] = {r0.x, r0.y}, w1[2] = {r1.x, r1.y}, w2[2] = {r2.x, r2.y},
+                     w3[2] = {r3.x, r3.y};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // eight dims: four m-tiles
+        // A byte of a row is dims (2 k, 2 k + 1); a pair byte needs the same dim of
+        // two keys: even dims of both, then odd dims of both.
+        const uint32_t ev01 = (w0[i] & 0x0f0f0f0fu) | ((w1[i] & 0x0f0f0f0fu) << 4);
+        const uint32_t od01 = ((w0[i] >> 4) & 0x0f0f0f0fu) | (w1[i] & 0xf0f0f0f0u);
+        const uint32_t ev23 = (w2[i] & 0x0f0f0f0fu) | ((w3[i] & 0x0f0f0f0fu) << 4);
+        const uint32_t od23 = ((w2[i] >> 4) & 0x0f0f0f0fu) | (w3[i] & 0xf0f0f0f0u);
+        uint32_t x0[4], x1[4], x2[4], x3[4];
+        e2m1x8(ev01, x0);
+        e2m1x8(od01, x1);
+        e2m1x8(ev23, x2);
+        e2m1x8(od23, x3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma16816(o[4 * i + k], mul_f16x2(x0[k], s01), mul_f16x2(x1[k], s01),
+                   mul_f16x2(x2[k], s23), mul_f16x2(x3[k], s23), b0, b1);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.v_empty[vs]));
+    ++vi;
+  }
+
+  // ---- merge of the eight warps: O = sum_w 2^(ref_w - M) O_w / L -------------
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 4);
+    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 8);
+    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 16);
+  }
+  if (g == 0) {
+    sh.ml[0][warp][2 * t] = ref[0];
+    sh.ml[0][warp][2 * t + 1] = ref[1];
+    sh.ml[1][warp][2 * t] = l[0];
+    sh.ml[1][warp][2 * t + 1] = l[1];
+  }
+  // All blocks have been consumed, so the code tiles are free once every warp is here.
+  named_bar_sync(kVoteBarrier, NCW * 32);
+  float *part = reinterpret_cast<float *>(smem_raw) + warp * ROWS * MERGE_STRIDE;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float *at = part + 2 * t * MERGE_STRIDE + 16 * g + 2 * i;
+    *reinterpret_cast<float2 *>(at) = make_float2(o[i][0], o[i][2]);
+    *reinterpret_cast<float2 *>(at + MERGE_STRIDE) = make_float2(o[i][1], o[i][3]);
+  }
+  named_bar_sync(kVoteBarrier, NCW * 32);
+  const int r = tid / (D / 4), col = tid % (D / 4) * 4;  // 8 rows x 32 groups of four columns
+  if (__syncthreads_or(!ok ? 1 : 0) == 0 && r < rows) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NCW; ++w)
+      if (sh.ml[1][w][r] != 0.f) m = fmaxf(m, sh.ml[0][w][r]);
+    float z = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < NCW; ++w) {
+      const float lw = sh.ml[1][w][r];
+      if (lw == 0.f) continue;  // the warp met no key of the row
+      const float f = ex2(sh.ml[0][w][r] - m);
+      z = fmaf(lw, f, z);
+      const float4 u = *reinterpret_cast<const float4 *>(
+          reinterpret_cast<const float *>(smem_raw) + (w * ROWS + r) * MERGE_STRIDE + col);
+      v.x = fmaf(u.x, f, v.x);
+      v.y = fmaf(u.y, f, v.y);
+      v.z = fmaf(u.z, f, v.z);
+      v.w = fmaf(u.w, f, v.w);
+    }
+    const float iz = z == 0.f ? 0.f : 1.f / z;
+    const int64_t orow = (int64_t)(x.tok0 + r / a.G) * a.Hq + hk * a.G + r % a.G;
+    if (a.n_splits == 1)
+      *reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.o + orow * D + col) =
+          make_uint2(pack_bf16x2(v.x * iz, v.y * iz), pack_bf16x2(v.z * iz, v.w * iz));
+    else
+      *reinterpret_cast<float4 *>(a.o_part + (orow * a.n_splits + sp) * D + col) =
+          make_float4(v.x * iz, v.y * iz, v.z * iz, v.w * iz);
+    if (col == 0)
+      (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] =
+          z == 0.f ? -INFINITY : m * kLn2 + logf(z);
+  }
+}
+
+// 4-D map over the code rows of a page pool: (byte, slot, head, page).
+bool make_map_codes(CUtensorMap *m, const KvPages &p, const void *ptr, int row) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)row, (cuuint64_t)p.page_size, (cuuint64_t)p.Hkv,
+                              (cuuint64_t)p.n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)row, (cuuint64_t)p.page_size * row,
+                                 (cuuint64_t)p.page_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)row, (cuuint32_t)(p.page_size < BN ? p.page_size : BN), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const ChunkArgs &a, unsigned grid, cudaStream_t s) {
+  CUtensorMap mk, mv;
+  if (!make_map_codes(&mk, a.pages, a.pages.k, Cfg<FMT>::ROW) ||
+      !make_map_codes(&mv, a.pages, a.pages.v, Cfg<FMT>::ROW))
+    return cudaErrorInvalidValue;
+  constexpr uint32_t smem = Layout<FMT>::END + ((sizeof(Shared) + 15) / 16) * 16;
+  const cudaError_t e = cudaFuncSetAttribute(decode_paged_kernel<FMT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  decode_paged_kernel<FMT><<<grid, NT, smem, s>>>(mk, mv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode_paged(const ChunkArgs &a, unsigned grid, cudaStream_t s) {
+  return a.pages.format == kKvE4m3 ? launch_fmt<kKvE4m3>(a, grid, s) : launch_fmt<kKvNvfp4>(a, grid, s);
+}
+
+}  // namespace attn_skip

@@ -138,6 +138,7 @@ struct ChunkArgs {
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
 cudaError_t launch_kv_gather(const KvGatherArgs &a, cudaStream_t s);
 cudaError_t launch_chunk_paged(const ChunkArgs &a, cudaStream_t s);
+cudaError_t launch_decode_paged(const ChunkArgs &a, unsigned grid, cudaStream_t s);
 int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv, int TT, int format);
 
 cudaError_t launch_prefill_f32(const PrefillArgs &a, cudaStream_t s);
