@@ -151,8 +151,19 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
   return byte == 255u ? NAN : byte == 0u ? 5.877471754111438e-39f : __uint_as_float(byte << 23);
 }
 
-// Block j's rows into stage buffers: codes by TMA (swizzled), scales by bulk
-// copies; part by part, one lane a part.  Whole warp.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// This thread's arrival on `bar` once its cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Block j's rows into stage buffers; whole warp.  Codes by TMA (swizzled), part
+// by part, one lane a part; scales in 16-byte pieces by cp.async of all lanes (a
+// bulk copy a part for each of them made pages of 16 rows half again as slow:
+// 48 copies a block).  `full` takes the byte count's arrival and, where there
+// are scales, one of each lane.
 template <int FMT>
 __device__ __forceinline__ void load_block(const ChunkArgs &a, Producer &p, const CUtensorMap *map,
                                            bool value, int j, uint32_t codes, uint32_t extra,
@@ -160,22 +171,30 @@ __device__ __forceinline__ void load_block(const ChunkArgs &a, Producer &p, cons
   using C = Cfg<FMT>;
   const int sub = p.sub;
   const Part x = part_of(a, p, j, lane);
-  if (lane == 0)
-    mbar_expect_tx(full, x.n * sub * (C::ROW + C::BS / BN + (value ? 0 : 2)));
+  const int rows = x.n * sub;  // rows of the block in the cache's pages
+  const KvPages &g = a.pages;
+  if (lane == 0) mbar_expect_tx(full, rows * C::ROW);
   __syncwarp();
-  if (lane < x.n) {
-    const KvPages &g = a.pages;
-    const int64_t row = ((int64_t)x.page * g.Hkv + p.hk) * g.page_size + x.slot;
-    const uint32_t r0 = lane * sub;
-    tma_load_4d(codes + r0 * C::ROW, map, full, 0, x.slot, p.hk, x.page, p.policy);
-    if constexpr (FMT == kKvNvfp4)
-      bulk_load(extra + r0 * (D / 16), (value ? g.v_bs : g.k_bs) + row * (D / 16), sub * (D / 16),
-                full, p.policy);
-    if (!value) {
-      bulk_load(extra + C::BS + r0, g.k_scale + row, sub, full, p.policy);
-      bulk_load(extra + C::BS + BN + r0, g.v_scale + row, sub, full, p.policy);
+  if (lane < x.n)
+    tma_load_4d(codes + lane * sub * C::ROW, map, full, 0, x.slot, p.hk, x.page, p.policy);
+  // Scale index of row r of the block: that of its part's first row, and on.
+  const int64_t first = ((int64_t)x.page * g.Hkv + p.hk) * g.page_size + x.slot;
+  auto row_at = [&](int r) { return __shfl_sync(0xffffffffu, first, r / sub) + r % sub; };
+  if constexpr (FMT == kKvNvfp4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 2 * (lane + 32 * i);
+      const int64_t at = row_at(r);
+      if (r < rows) cp_async16(extra + r * 8, (value ? g.v_bs : g.k_bs) + at * 8);
     }
   }
+  if (!value) {
+    const int r = 16 * (lane & 7);
+    const int64_t at = row_at(r);
+    if (lane < 16 && r < rows)
+      cp_async16(extra + C::BS + (lane < 8 ? 0 : BN) + r, (lane < 8 ? g.k_scale : g.v_scale) + at);
+  }
+  if (!value || FMT == kKvNvfp4) cp_async_arrive(full);
   __syncwarp();
 }
 
@@ -207,8 +226,8 @@ __global__ void __launch_bounds__(NT, 2)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(smem_u32(&sh.k_full[i]), 1);
-      mbar_init(smem_u32(&sh.v_full[i]), 1);
+      mbar_init(smem_u32(&sh.k_full[i]), 1 + 32);
+      mbar_init(smem_u32(&sh.v_full[i]), FMT == kKvNvfp4 ? 1 + 32 : 1);
       mbar_init(smem_u32(&sh.k_empty[i]), NCW);
       mbar_init(smem_u32(&sh.v_empty[i]), NCW);
     }
