@@ -1208,20 +1208,27 @@ cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
 }  // namespace
 
 // The split count that a host-side model of the launch finds cheapest: waves of
-// one CTA an SM, each a set-up and its share of the blocks.
+// CTAs (one an SM, or two of the decode kernel), each a set-up and its share of
+// the blocks.  A long decode batch takes six at least: sequences of different
+// lengths fill the chip only in smaller pieces (24 sequences of 8192 to 32768
+// tokens over E4M3 pages: 199 us with 3 splits, 173 with 8, 187 with 16).
 int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv, int TT, int format) {
-  const int sms = 152;
+  const int rows = (128 / TT) * (TT < max_chunk ? TT : max_chunk);
+  const bool small = format != kKvBf16 && rows <= 8;
+  const int slots = small ? 304 : 152;
   const int64_t units = tiles_bound(n_seq, total, max_chunk, TT) * Hkv;
   const int nb = (max_kv + BN - 1) / BN;
-  const double block_us = format == kKvBf16 ? 1.2 : 0.8, setup_us = 4.0, merge_us = 3.0;
-  int best = 1;
+  const double block_us = format == kKvBf16 ? 1.2 : small ? 1.5 : 1.8;
+  const double setup_us = small ? 3.0 : 4.0, merge_us = 3.0;
+  const int least = rows <= 32 && n_seq > 1 && nb >= 6 * 32 ? 6 : 1;
+  int best = least;
   double best_t = 0;
-  for (int n = 1; n <= 64 && n <= (nb > 0 ? nb : 1); ++n) {
+  for (int n = least; n <= 64 && n <= (nb > 0 ? nb : 1); ++n) {
     const int bps = (nb + n - 1) / n;
-    if (n > 1 && (nb + bps - 1) / bps < n) continue;  // the last splits would be empty
-    const int64_t waves = (units * n + sms - 1) / sms;
+    if (n > least && (nb + bps - 1) / bps < n) continue;  // the last splits would be empty
+    const int64_t waves = (units * n + slots - 1) / slots;
     const double t = waves * (setup_us + bps * block_us) + (n > 1 ? merge_us : 0);
-    if (n == 1 || t < best_t) {
+    if (n == least || t < best_t) {
       best = n;
       best_t = t;
     }

@@ -146,11 +146,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 2^(byte - 127) as fp32; NaN for 255.
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-  return byte == 255u ? NAN : byte == 0u ? 5.877471754111438e-39f : __uint_as_float(byte << 23);
-}
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -353,19 +348,24 @@ __global__ void __launch_bounds__(NT, 2)
   float o[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // The rows' reference, what the exponents subtract (0 before the first key) and
+  // the score above which the reference moves.
+  float ref[2] = {-INFINITY, -INFINITY}, sub[2] = {0.f, 0.f};
+  float top[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float m2[2] = {-INFINITY, -INFINITY};  // running max of the split (log2 units), with a threshold
   uint32_t word = 0;
   uint32_t *bits = a.bits ? a.bits + ((((int64_t)x.s * a.Hkv + hk) * a.n_t + x.t) * a.n_splits + sp) * a.words
                           : nullptr;
   bool ok = true;
-  int vi = 0;  // kept blocks
+  int s = -1, vs = 0, kphase = 1, vphase = 0;  // stages and their phases
 #pragma unroll 1
   for (int c = 0; c < nb; ++c) {
-    const int s = c % NST, j = x.j0 + c;
+    const int j = x.j0 + c;
+    s = s == NST - 1 ? 0 : s + 1;
+    if (s == 0) kphase ^= 1;
     // After a failed wait the loop runs on (every later wait fails at once), so
     // that the warps meet the vote barriers equally often.
-    if (ok) ok = wait_warp(&sh.k_full[s], c / NST);
+    if (ok) ok = wait_warp(&sh.k_full[s], kphase);
     const int left = x.kv - j * BN;  // rows of the block below kv
     float p[2][2];                   // [key g, g + 8][row 2 t, 2 t + 1]: scores, then P
     float ev[2], inv[2];             // the keys' value exponents and 2^-e_v
@@ -415,27 +415,40 @@ __global__ void __launch_bounds__(NT, 2)
       const uint32_t vb0 = lds8(sc + BN + kr0), vb1 = lds8(sc + BN + kr1);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.k_empty[s]));  // the stage is in registers
-      const float f0 = scale_of(eb0), f1 = scale_of(eb1);
+      const float f0 = __uint_as_float(eb0 << 23), f1 = __uint_as_float(eb1 << 23);
       p[0][0] = acc[0] * (qs[0] * f0);
       p[0][1] = acc[1] * (qs[1] * f0);
       p[1][0] = acc[2] * (qs[0] * f1);
       p[1][1] = acc[3] * (qs[1] * f1);
-      ev[0] = vb0 == 255u ? NAN : (float)((int)vb0 - 127);
-      ev[1] = vb1 == 255u ? NAN : (float)((int)vb1 - 127);
-      inv[0] = __uint_as_float(max(1, 254 - (int)vb0) << 23);
-      inv[1] = __uint_as_float(max(1, 254 - (int)vb1) << 23);
+      // byte - 127 as fp32, by the fraction bits of 2^23 + byte.
+      ev[0] = __uint_as_float(0x4b000000u + vb0) - 8388735.f;
+      ev[1] = __uint_as_float(0x4b000000u + vb1) - 8388735.f;
+      inv[0] = __uint_as_float((254u - vb0) << 23);
+      inv[1] = __uint_as_float((254u - vb1) << 23);
+      if (__any_sync(0xffffffffu, max(max(eb0, eb1), max(vb0, vb1)) >= 254u)) {
+        // NaN rows (255), and 2^127, whose inverse is no normal number.
+        if (eb0 == 255u) p[0][0] = p[0][1] = NAN;
+        if (eb1 == 255u) p[1][0] = p[1][1] = NAN;
+        if (vb0 >= 254u) inv[0] = vb0 == 255u ? 1.f : 5.877471754111438e-39f;
+        if (vb1 >= 254u) inv[1] = vb1 == 255u ? 1.f : 5.877471754111438e-39f;
+        if (vb0 == 255u) ev[0] = NAN;
+        if (vb1 == 255u) ev[1] = NAN;
+      }
     }
-    if (j * BN + BN > min_limit) {  // keys that a row does not see
+    float y[2][2];  // s + e_v
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int key = j * BN + (k ? kr1 : kr0);
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) y[k][n] = p[k][n] + ev[k];
+    if (j * BN + BN > min_limit) {  // keys that a row does not see, whatever they hold
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          if (key >= limit[n]) {
-            p[k][n] = -INFINITY;
+          if (j * BN + (k ? kr1 : kr0) >= limit[n]) {
+            p[k][n] = y[k][n] = -INFINITY;
+            if (ev[k] != ev[k] || inv[k] == 0.f) inv[k] = 1.f;
           }
-        if (key >= limit[0] && key >= limit[1]) ev[k] = 0.f;  // (a row's scale may be NaN)
-      }
     }
     if (!dense) {
       // The rows' maxima over the block: this warp's keys, then all eight warps.
@@ -488,16 +501,7 @@ __global__ void __launch_bounds__(NT, 2)
     if (!ok) continue;
     // The reference moves when a key's s + e_v passes it by more than 2^8 (or it
     // is the row's first): then by the warp's maximum.
-    float y[2][2];
-    bool move = false;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        y[k][n] = p[k][n] + ev[k];
-        if (p[k][n] == -INFINITY) y[k][n] = -INFINITY;
-        move |= y[k][n] > ref[n] + kRescaleLog2;  // (-inf is not above -inf)
-      }
+    const bool move = fmaxf(y[0][0], y[1][0]) > top[0] || fmaxf(y[0][1], y[1][1]) > top[1];
     if (__any_sync(0xffffffffu, move)) {
       float al[2];
 #pragma unroll
@@ -509,6 +513,8 @@ __global__ void __launch_bounds__(NT, 2)
         const float to = fmaxf(ref[n], m);
         al[n] = to == -INFINITY ? 1.f : ex2(ref[n] - to);
         ref[n] = to;
+        sub[n] = to == -INFINITY ? 0.f : to;
+        top[n] = to + kRescaleLog2;
         l[n] *= al[n];
       }
 #pragma unroll
@@ -520,20 +526,17 @@ __global__ void __launch_bounds__(NT, 2)
       }
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const float r = ref[n] == -INFINITY ? 0.f : ref[n];
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        p[k][n] = ex2(y[k][n] - r);
+      for (int n = 0; n < 2; ++n) {
+        p[k][n] = ex2(y[k][n] - sub[n]);
         l[n] = fmaf(p[k][n], inv[k], l[n]);
       }
-    }
     // P as the B operand: key pairs of row g.
     const uint32_t b0 = transpose8x8(pack_f16x2(p[0][0], p[0][1]));
     const uint32_t b1 = transpose8x8(pack_f16x2(p[1][0], p[1][1]));
 
-    const int vs = vi % NST;
-    ok = wait_warp(&sh.v_full[vs], vi / NST);
+    ok = wait_warp(&sh.v_full[vs], vphase);
     if (!ok) continue;
     const uint32_t vt = base + L::V + vs * L::CODES;
     if constexpr (FMT == kKvE4m3) {
@@ -595,7 +598,8 @@ __global__ void __launch_bounds__(NT, 2)
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.v_empty[vs]));
-    ++vi;
+    vs = vs == NST - 1 ? 0 : vs + 1;
+    if (vs == 0) vphase ^= 1;
   }
 
   // ---- merge of the eight warps: O = sum_w 2^(ref_w - M) O_w / L -------------

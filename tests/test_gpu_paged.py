@@ -424,7 +424,7 @@ def test_chunk_reports_bad_device_arguments():
     q = torch.randn(9, 4, 128, device=DEV).to(torch.bfloat16)
     lam = torch.zeros(3, device=DEV)
     want, wl, _ = bs.attn_skip_chunk_paged(kv, q, i32([0, 3, 6, 9]), 3, i32([300, 200, 100]), 300,
-                                           table, lam)
+                                           table, lam, n_splits=1)
     bs.attn_skip_last_device_error()
 
     def bad(cu=(0, 3, 6, 9), lens=(300, 200, 100), t=table, lam=lam, n_splits=1, max_chunk=3):
