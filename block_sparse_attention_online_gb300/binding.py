@@ -8,6 +8,7 @@ fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -641,7 +642,7 @@ class PagedKV:
                 raise ValueError("tensors must be on one CUDA device")
         self.format, self.n_pages, self.Hkv, self.page_size, self.d = fmt, n_pages, Hkv, page_size, d
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.k_bs, self.v_bs, self.device = k_bs, v_bs, k.device
+        self.k_bs, self.v_bs, self.device, self.index = k_bs, v_bs, k.device, k.get_device()
         p = [x.data_ptr() if x is not None else None for x in (k, v, k_scale, v_scale, k_bs, v_bs)]
         # The page stride matters, and is meaningful, only between pages.
         stride = k.stride(0) * k.element_size() if n_pages > 1 else 0
@@ -663,46 +664,61 @@ class PagedKV:
                    u8(*rows, d // 16), u8(*rows, d // 16))
 
 
-def _paged_call(kv, stream, call, *tensors):
-    """Run ``call(stream pointer)`` on the cache's device.  What it allocates
-    belongs to the stream it launches on."""
-    for x in tensors:
-        if x.device != kv.device:
-            raise ValueError("tensors must be on the cache's device")
-    if stream is None and torch.cuda.current_device() == kv.device.index:
-        return call(torch._C._cuda_getCurrentRawStream(kv.device.index))
+def _elsewhere(kv, stream):
+    """Whether a call has to switch to another device or stream first."""
+    return stream is not None or torch.cuda.current_device() != kv.index
+
+
+@contextlib.contextmanager
+def _switched(kv, stream):
+    """The cache's device, and ``stream`` on it, as the current ones: what a call
+    allocates belongs to the stream that it launches on."""
     with torch.cuda.device(kv.device):
         if stream is None:
             stream = torch.cuda.current_stream()
         elif not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream))
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            yield
 
 
-def _int32(n_seq, page_table, **lengths):
-    """Shapes of the device arrays of a batch."""
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n_seq \
-            or not page_table.is_contiguous():
-        raise ValueError(f"page_table must be a contiguous int32 tensor [{n_seq}, max_pages]")
-    for name, x in lengths.items():
-        if x.dtype != torch.int32 or x.shape != (n_seq,) or not x.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor [{n_seq}]")
+def _raw_stream(kv):
+    return torch._C._cuda_getCurrentRawStream(kv.index)
 
 
-def _cu(name, cu):
-    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 2 or not cu.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor [n_seq + 1]")
-    return cu.numel() - 1
+def _batch(kv, cu, page_table, lengths, dtype=torch.int32):
+    """Number of sequences of the device arrays ``cu`` [n_seq + 1], ``page_table``
+    [n_seq, max_pages] and ``lengths`` [n_seq] (or None), checked."""
+    n = cu.shape[0] - 1 if cu.dim() == 1 else 0
+    if n < 1 or cu.dtype is not torch.int32 or not cu.is_contiguous() \
+            or cu.get_device() != kv.index:
+        raise ValueError("the row bounds must be a contiguous int32 tensor [n_seq + 1] on the "
+                         "cache's device")
+    if page_table.dim() != 2 or page_table.shape[0] != n or page_table.dtype is not torch.int32 \
+            or not page_table.is_contiguous() or page_table.get_device() != kv.index:
+        raise ValueError(f"page_table must be a contiguous int32 tensor [{n}, max_pages] on the "
+                         "cache's device")
+    if lengths is not None:
+        _per_sequence("kv_len (or start)", lengths, n, torch.int32, kv)
+    return n
 
 
-def _token_rows(name, x, heads, d):
-    """Token stride of x [total, heads, d]; the rows of a token must be dense."""
-    if x.dim() != 3 or x.shape[1:] != (heads, d):
-        raise ValueError(f"{name} must have shape [total, {heads}, {d}]")
-    if x.shape[0] and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != d)):
+def _per_sequence(name, x, n, dtype, kv):
+    if x.dim() != 1 or x.shape[0] != n or x.dtype is not dtype or not x.is_contiguous() \
+            or x.get_device() != kv.index:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}] on the cache's device")
+
+
+def _token_stride(name, x, heads, kv):
+    """Token stride of x [total, heads, 128]; the rows of a token must be dense."""
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != kv.d:
+        raise ValueError(f"{name} must have shape [total, {heads}, {kv.d}]")
+    if x.get_device() != kv.index:
+        raise ValueError(f"{name} must be on the cache's device")
+    s = x.stride()
+    if x.shape[0] and (s[2] != 1 or (heads > 1 and s[1] != kv.d)):
         raise ValueError(f"the heads of a token of {name} must be dense")
-    return x.stride(0) if x.shape[0] > 1 else heads * d
+    return s[0] if x.shape[0] > 1 else heads * kv.d
 
 
 def attn_skip_kv_append(kv, k_new, v_new, cu_seqlens, kv_len, page_table, stream=None):
@@ -710,46 +726,44 @@ def attn_skip_kv_append(kv, k_new, v_new, cu_seqlens, kv_len, page_table, stream
     stride is free) into the cache ``kv``, quantised for its format.  Sequence
     s's rows cu_seqlens[s] .. cu_seqlens[s+1] take the last positions below
     kv_len[s]; int32 device tensors, page_table [n_seq, max_pages]."""
-    n_seq = _cu("cu_seqlens", cu_seqlens)
-    _int32(n_seq, page_table, kv_len=kv_len)
-    ks, vs = _token_rows("k_new", k_new, kv.Hkv, kv.d), _token_rows("v_new", v_new, kv.Hkv, kv.d)
-    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+    if _elsewhere(kv, stream):
+        with _switched(kv, stream):
+            return attn_skip_kv_append(kv, k_new, v_new, cu_seqlens, kv_len, page_table)
+    n = _batch(kv, cu_seqlens, page_table, kv_len)
+    ks = _token_stride("k_new", k_new, kv.Hkv, kv)
+    vs = _token_stride("v_new", v_new, kv.Hkv, kv)
+    total = k_new.shape[0]
+    if v_new.shape[0] != total or v_new.dtype is not k_new.dtype:
         raise ValueError("k_new and v_new must agree in shape and dtype")
-    dt = _dtype_code(k_new)
-    _check("attn_skip_kv_append", _paged_call(
-        kv, stream, lambda s: load().attn_skip_kv_append(
-            kv._ref, k_new.data_ptr(), v_new.data_ptr(), dt, ks, vs, n_seq, k_new.shape[0],
-            cu_seqlens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.shape[1],
-            s), k_new, v_new, cu_seqlens, kv_len, page_table))
+    _check("attn_skip_kv_append", (_lib or load()).attn_skip_kv_append(
+        kv._ref, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), ks, vs, n, total,
+        cu_seqlens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+        _raw_stream(kv)))
 
 
 def attn_skip_kv_gather(kv, cu_rows, start, page_table, total, out_dtype=torch.bfloat16, out=None,
                         stream=None):
     """Read rows back: positions start[s] (``None``: 0) and on of sequence s,
     cu_rows[s+1] - cu_rows[s] of them.  Returns dense ``(k, v)`` [total, Hkv,
-    128] of ``out_dtype`` (bf16 or fp32)."""
-    n_seq = _cu("cu_rows", cu_rows)
-    _int32(n_seq, page_table, **({} if start is None else {"start": start}))
-
-    def call(s):
-        if out is None:
-            k, v = (torch.empty(total, kv.Hkv, kv.d, dtype=out_dtype, device=kv.device)
-                    for _ in range(2))
-        else:
-            k, v = out
-            if total and k.data_ptr() == v.data_ptr():
-                raise ValueError("the two outputs must be different tensors")
-            for x in out:
-                if x.shape != (total, kv.Hkv, kv.d) or x.dtype != k.dtype or not x.is_contiguous() \
-                        or x.device != kv.device:
-                    raise ValueError(f"out must be contiguous [{total}, {kv.Hkv}, {kv.d}] tensors")
-        st = load().attn_skip_kv_gather(
-            kv._ref, n_seq, total, cu_rows.data_ptr(), None if start is None else start.data_ptr(),
-            page_table.data_ptr(), page_table.shape[1], _dtype_code(k), k.data_ptr(), v.data_ptr(),
-            s)
-        _check("attn_skip_kv_gather", st)
-        return k, v
-    return _paged_call(kv, stream, call, cu_rows, page_table, *(() if start is None else (start,)))
+    128] of ``out_dtype`` (bf16 or fp32), or ``out``, rows of which behind the
+    last sequence stay as they were."""
+    if _elsewhere(kv, stream):
+        with _switched(kv, stream):
+            return attn_skip_kv_gather(kv, cu_rows, start, page_table, total, out_dtype, out)
+    n = _batch(kv, cu_rows, page_table, start)
+    if out is None:
+        k, v = torch.empty((2, total, kv.Hkv, kv.d), dtype=out_dtype, device=kv.device).unbind()
+    else:
+        k, v = out
+        if total and k.data_ptr() == v.data_ptr():
+            raise ValueError("the two outputs must be different tensors")
+        for x in out:
+            _like("out", x, (total, kv.Hkv, kv.d), k.dtype, kv)
+    _check("attn_skip_kv_gather", (_lib or load()).attn_skip_kv_gather(
+        kv._ref, n, total, cu_rows.data_ptr(), None if start is None else start.data_ptr(),
+        page_table.data_ptr(), page_table.shape[1], _dtype_code(k), k.data_ptr(), v.data_ptr(),
+        _raw_stream(kv)))
+    return k, v
 
 
 def attn_skip_chunk_paged_splits(kv, n_seq, total, Hq, max_chunk, max_kv):
@@ -776,58 +790,60 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
     ``None`` without ``with_bits``.  ``out`` may pass these three, ``workspace``
     the partials ``(o_part [total, Hq, n_splits, 128], lse_part [total, Hq,
     n_splits])`` fp32 of n_splits > 1."""
-    n_seq = _cu("cu_seqlens", cu_seqlens)
-    _int32(n_seq, page_table, kv_len=kv_len)
+    if _elsewhere(kv, stream):
+        with _switched(kv, stream):
+            return attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_table,
+                                         lambdas, causal, scale, n_splits, with_bits, out,
+                                         workspace)
+    n = _batch(kv, cu_seqlens, page_table, kv_len)
+    _per_sequence("lambdas", lambdas, n, torch.float32, kv)
+    if q.dtype is not torch.bfloat16 or q.dim() != 3:
+        raise TypeError("q must be a bfloat16 tensor [total, Hq, 128]")
     total, Hq, d = q.shape
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"unsupported dtype {q.dtype}")
-    qs = _token_rows("q", q, Hq, kv.d)
-    if lambdas.dtype != torch.float32 or lambdas.shape != (n_seq,) or not lambdas.is_contiguous():
-        raise ValueError(f"lambdas must be a contiguous float32 tensor [{n_seq}]")
+    qs = _token_stride("q", q, Hq, kv)
     if Hq % kv.Hkv or Hq // kv.Hkv > 128:
         raise ValueError(f"{Hq} query heads do not fit {kv.Hkv} KV heads")
+    lib = _lib or load()
     if n_splits == 0:
-        n_splits = attn_skip_chunk_paged_splits(kv, n_seq, total, Hq, max_chunk, max_kv)
-
-    def call(s):
-        bits = None
-        if out is not None:
-            o, lse, bits = out
-            _like("out", o, (total, Hq, d), torch.bfloat16, kv.device)
-            _like("out", lse, (total, Hq), torch.float32, kv.device)
+        n_splits = lib.attn_skip_chunk_paged_splits(kv._c.format, n, total, Hq, kv.Hkv, max_chunk,
+                                                    max_kv)
+    bits = None
+    if out is None:
+        o = q.new_empty((total, Hq, d))
+        lse = lambdas.new_empty((total, Hq))
+    else:
+        o, lse, bits = out
+        _like("out", o, (total, Hq, d), torch.bfloat16, kv)
+        _like("out", lse, (total, Hq), torch.float32, kv)
+    if with_bits or bits is not None:
+        shape = chunk_bitmap_shape(n, Hq, kv.Hkv, max_chunk, max_kv, n_splits)
+        if bits is None:
+            bits = cu_seqlens.new_empty(shape)
         else:
-            o = torch.empty(total, Hq, d, dtype=torch.bfloat16, device=kv.device)
-            lse = torch.empty(total, Hq, dtype=torch.float32, device=kv.device)
-        if with_bits and bits is None:
-            bits = torch.empty(chunk_bitmap_shape(n_seq, Hq, kv.Hkv, max_chunk, max_kv, n_splits),
-                               dtype=torch.int32, device=kv.device)
-        elif bits is not None:
-            _like("skip_bits", bits, chunk_bitmap_shape(n_seq, Hq, kv.Hkv, max_chunk, max_kv,
-                                                        n_splits), torch.int32, kv.device)
-        op = lp = None
-        if n_splits > 1:
-            if workspace is None:
-                op = torch.empty(total, Hq, n_splits, d, dtype=torch.float32, device=kv.device)
-                lp = torch.empty(total, Hq, n_splits, dtype=torch.float32, device=kv.device)
-            else:
-                op, lp = workspace
-                _like("workspace", op, (total, Hq, n_splits, d), torch.float32, kv.device)
-                _like("workspace", lp, (total, Hq, n_splits), torch.float32, kv.device)
-        st = load().attn_skip_chunk_paged(
-            kv._ref, q.data_ptr(), qs, Hq, n_seq, total, cu_seqlens.data_ptr(), max_chunk,
-            kv_len.data_ptr(), max_kv, page_table.data_ptr(), page_table.shape[1], scale,
-            lambdas.data_ptr(), int(bool(causal)), n_splits, o.data_ptr(), lse.data_ptr(),
-            None if bits is None else bits.data_ptr(), None if op is None else op.data_ptr(),
-            None if lp is None else lp.data_ptr(), s)
-        _check("attn_skip_chunk_paged", st)
-        return o, lse, bits
-    return _paged_call(kv, stream, call, q, cu_seqlens, kv_len, page_table, lambdas)
+            _like("skip_bits", bits, shape, torch.int32, kv)
+    op = lp = 0
+    if n_splits > 1:
+        rows = total * Hq * n_splits
+        if workspace is None:
+            work = lambdas.new_empty(rows * (d + 1))
+            op = work.data_ptr()
+            lp = op + rows * d * 4
+        else:
+            _like("workspace", workspace[0], (total, Hq, n_splits, d), torch.float32, kv)
+            _like("workspace", workspace[1], (total, Hq, n_splits), torch.float32, kv)
+            op, lp = workspace[0].data_ptr(), workspace[1].data_ptr()
+    _check("attn_skip_chunk_paged", lib.attn_skip_chunk_paged(
+        kv._ref, q.data_ptr(), qs, Hq, n, total, cu_seqlens.data_ptr(), max_chunk,
+        kv_len.data_ptr(), max_kv, page_table.data_ptr(), page_table.shape[1], scale,
+        lambdas.data_ptr(), 1 if causal else 0, n_splits, o.data_ptr(), lse.data_ptr(),
+        None if bits is None else bits.data_ptr(), op, lp, _raw_stream(kv)))
+    return o, lse, bits
 
 
-def _like(name, x, shape, dtype, device):
-    if tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous() \
-            or x.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+def _like(name, x, shape, dtype, kv):
+    if x.shape != shape or x.dtype is not dtype or not x.is_contiguous() \
+            or x.get_device() != kv.index:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {kv.device}")
 
 
 def attn_skip_selftest_wait_timeout(stream=None, device=None):
