@@ -809,8 +809,8 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
                                                     max_kv)
     bits = None
     if out is None:
-        o = q.new_empty((total, Hq, d))
-        lse = lambdas.new_empty((total, Hq))
+        o = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=kv.device)
+        lse = torch.empty((total, Hq), device=kv.device, dtype=torch.float32)
     else:
         o, lse, bits = out
         _like("out", o, (total, Hq, d), torch.bfloat16, kv)
@@ -818,14 +818,14 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
     if with_bits or bits is not None:
         shape = chunk_bitmap_shape(n, Hq, kv.Hkv, max_chunk, max_kv, n_splits)
         if bits is None:
-            bits = cu_seqlens.new_empty(shape)
+            bits = torch.empty(shape, dtype=torch.int32, device=kv.device)
         else:
             _like("skip_bits", bits, shape, torch.int32, kv)
     op = lp = 0
     if n_splits > 1:
         rows = total * Hq * n_splits
         if workspace is None:
-            work = lambdas.new_empty(rows * (d + 1))
+            work = torch.empty(rows * (d + 1), dtype=torch.float32, device=kv.device)
             op = work.data_ptr()
             lp = op + rows * d * 4
         else:

@@ -537,7 +537,7 @@ attn_status pages_check(const attn_kv_pages *kv, int n_seq, int total, const int
   const int ps = kv->page_size;
   if (kv->d != 128) return ATTN_EUNSUPPORTED;
   if (ps != 16 && ps != 32 && ps != 64 && ps % 128 != 0) return ATTN_EUNSUPPORTED;
-  if ((int64_t)max_pages * ps > kMaxPositions || ps > kMaxPositions || kv->Hkv > (1 << 16))
+  if ((int64_t)max_pages * ps > kMaxPositions || (int64_t)kv->Hkv * ps > kMaxPositions)
     return ATTN_EUNSUPPORTED;
   const int64_t row = kv->format == ATTN_KV_BF16 ? 256 : kv->format == ATTN_KV_E4M3 ? 128 : 64;
   const int64_t dense = (int64_t)kv->Hkv * ps * row;
@@ -554,6 +554,7 @@ attn_status pages_check(const attn_kv_pages *kv, int n_seq, int total, const int
     return ATTN_EINVAL;
   p.format = (int)kv->format;
   p.n_pages = kv->n_pages; p.page_size = ps; p.Hkv = kv->Hkv;
+  p.page_shift = (ps & (ps - 1)) ? -1 : __builtin_ctz((unsigned)ps);
   p.page_stride = kv->page_stride ? kv->page_stride : dense;
   p.k = kv->k; p.v = kv->v;
   p.k_scale = kv->k_scale; p.v_scale = kv->v_scale;
@@ -580,7 +581,7 @@ extern "C" attn_status attn_skip_kv_append(const attn_kv_pages *kv, const void *
   const int64_t dense = (int64_t)kv->Hkv * 128;
   if (k_tok_stride < dense || v_tok_stride < dense || k_tok_stride % 8 || v_tok_stride % 8)
     return ATTN_EINVAL;
-  if ((int64_t)total * 2 * kv->Hkv > (int64_t)0x7fffffff * 16) return ATTN_EUNSUPPORTED;
+  if ((int64_t)total * kv->Hkv > 0x7fffffff) return ATTN_EUNSUPPORTED;
   a.k_new = k_new; a.v_new = v_new;
   a.k_tok_stride = k_tok_stride; a.v_tok_stride = v_tok_stride;
   a.src_f32 = dt == ATTN_F32; a.n_seq = n_seq; a.total = total; a.max_pages = max_pages;
@@ -601,7 +602,7 @@ extern "C" attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, i
   if (!aligned4(start) || (out_dt != ATTN_BF16 && out_dt != ATTN_F32)) return ATTN_EINVAL;
   if (total == 0) return ATTN_OK;
   if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return ATTN_EINVAL;
-  if ((int64_t)total * 2 * kv->Hkv > (int64_t)0x7fffffff * 16) return ATTN_EUNSUPPORTED;
+  if ((int64_t)total * kv->Hkv > 0x7fffffff) return ATTN_EUNSUPPORTED;
   a.k_out = k_out; a.v_out = v_out;
   a.out_f32 = out_dt == ATTN_F32; a.n_seq = n_seq; a.total = total; a.max_pages = max_pages;
   a.cu_rows = cu_rows; a.start = start; a.page_table = page_table;

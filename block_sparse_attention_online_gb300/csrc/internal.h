@@ -94,6 +94,7 @@ enum : int { kKvBf16 = 0, kKvE4m3 = 1, kKvNvfp4 = 2 };
 
 struct KvPages {
   int format, n_pages, page_size, Hkv;
+  int page_shift;             // log2(page_size), -1 if it is no power of two
   int64_t page_stride;        // bytes from page to page in k and v
   void *k, *v;                // rows [n_pages][Hkv][page_size]
   uint8_t *k_scale, *v_scale; // E8M0 row scales [n_pages][Hkv][page_size]

@@ -15,10 +15,11 @@
 // (e >= -110 keeps the smallest product, 2^-10 * 2^-110, a bf16 normal).
 //
 // Both kernels only move bytes: DRAM traffic bounds the large calls, latency
-// the small ones.  Sixteen lanes own a row (16 bytes of bf16 each), so every
-// row is read and written as whole 32-byte sectors and the row's maximum is
-// four shuffles; a half warp takes kRows consecutive tokens of one head, whose
-// pool rows are contiguous within a page, with all loads issued first.
+// the small ones.  Sixteen lanes own a row, so every row is read and written as
+// whole 32-byte sectors and the row's maximum is four shuffles.  A half warp
+// takes the key and the value rows of a few consecutive tokens of one head,
+// whose place in the cache it works out once a token and whose pool rows are
+// contiguous within a page; all its loads are issued first.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -50,23 +51,26 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int n, int t, int hl,
 }
 
 struct Place {
-  int64_t row;  // (page * Hkv + head) * page_size + slot: the row's scale index
-  int64_t byte; // the row's first byte in k and v
-  int ok;       // 0: no such row (out of range: reported by the caller)
+  int64_t row;  // (page * Hkv + head) * page_size + slot: the rows' scale index
+  int64_t byte; // the rows' first byte in k and v
+  bool ok;      // false: no such rows
 };
 
+// Rows of position pos of sequence s, head h.
 template <int ROW_BYTES>
 __device__ __forceinline__ Place place_of(const KvPages &p, const int32_t *table, int max_pages,
                                           int s, int64_t pos, int h) {
-  Place x{0, 0, 0};
-  const int64_t pi = pos / p.page_size;
-  const int slot = (int)(pos - pi * p.page_size);
-  if (pos < 0 || pi >= max_pages) return x;
+  Place x{0, 0, false};
+  if (pos < 0 || pos >= (int64_t)max_pages * p.page_size) return x;
+  const unsigned u = (unsigned)pos;
+  const unsigned pi = p.page_shift >= 0 ? u >> p.page_shift : u / (unsigned)p.page_size;
+  const int slot = (int)(u - pi * (unsigned)p.page_size);
   const int page = __ldg(table + (int64_t)s * max_pages + pi);
   if (page < 0 || page >= p.n_pages) return x;
-  x.row = ((int64_t)page * p.Hkv + h) * p.page_size + slot;
-  x.byte = (int64_t)page * p.page_stride + ((int64_t)h * p.page_size + slot) * ROW_BYTES;
-  x.ok = 1;
+  const int in_page = h * p.page_size + slot;
+  x.row = (int64_t)page * (p.Hkv * p.page_size) + in_page;
+  x.byte = (int64_t)page * p.page_stride + (int64_t)in_page * ROW_BYTES;
+  x.ok = true;
   return x;
 }
 
@@ -74,19 +78,14 @@ template <int FMT> struct RowBytes {
   static constexpr int value = FMT == kKvBf16 ? 2 * D : FMT == kKvE4m3 ? D : D / 2;
 };
 
-__device__ __forceinline__ float half_max(float m, unsigned hmask) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(hmask, m, o));
-  return m;
-}
-
 // 2^i for i in [-126, 127].
 __device__ __forceinline__ float pow2i(int i) { return __int_as_float((i + 127) << 23); }
 
-// Smallest e with a <= top * 2^e for a > 0, top = 1.F * 2^TE (fraction bits TF).
+// Smallest e with a <= top * 2^e for the fp32 a > 0 of bits b, top = 1.F * 2^TE
+// (fraction bits TF), clamped.
 template <int TE, int TF>
-__device__ __forceinline__ int scale_exponent(float a) {
-  int b = __float_as_int(a), ex = b >> 23;
+__device__ __forceinline__ int scale_exponent(uint32_t b) {
+  const int ex = (int)(b >> 23);
   if (ex == 0) return EMIN;  // fp32 subnormal: far below the clamp
   return min(EMAX, max(EMIN, ex - 127 - TE + ((b & 0x7fffff) > TF ? 1 : 0)));
 }
@@ -109,24 +108,43 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return r;
 }
 
-// Eight elements of a new row (this lane's share) as fp32.
-template <bool F32>
-__device__ __forceinline__ void load8(const void *src, int64_t elem, float (&x)[8]) {
-  if constexpr (F32) {
+// This lane's eight elements of a new row, as they come.
+template <bool F32> struct New;
+template <> struct New<false> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const void *src, int64_t elem) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)src + elem));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+  // Bits of the largest |element| (fp32; infinities and NaN compare above all).
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t x = __vmaxu2(__vmaxu2(w[0] & m, w[1] & m), __vmaxu2(w[2] & m, w[3] & m));
+    return max(x << 16, x & 0xffff0000u);
+  }
+};
+template <> struct New<true> {
+  float x[8];
+  __device__ __forceinline__ void load(const void *src, int64_t elem) {
     const float4 *p = reinterpret_cast<const float4 *>((const float *)src + elem);
     const float4 a = __ldg(p), b = __ldg(p + 1);
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    const uint4 v = __ldg(reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)src + elem));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
   }
-}
+  __device__ __forceinline__ float at(int i) const { return x[i]; }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    return m;
+  }
+};
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
@@ -134,131 +152,131 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
-template <int FMT>
+// The row whose eight elements a lane holds is x, to its place; half warp.
+template <int FMT, bool F32>
 __device__ __forceinline__ void store_row(const KvPages &p, bool value, const Place &at,
-                                          const float (&x)[8], int hl, unsigned hmask) {
+                                          const New<F32> &x, int hl, unsigned hmask) {
   uint8_t *codes = (uint8_t *)(value ? p.v : p.k) + at.byte;
   if constexpr (FMT == kKvBf16) {
-    if (at.ok)
-      *reinterpret_cast<uint4 *>(codes + hl * 16) =
-          make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
-    return;
-  }
-  float m = 0.f;
-  bool fin = true;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m = fmaxf(m, fabsf(x[i]));
-    fin = fin && isfinite(x[i]);
-  }
-  const bool bad = (__ballot_sync(hmask, !fin) & hmask) != 0u;
-  const float amax = half_max(m, hmask);
-  // top = 448 = 1.75 * 2^8, or 2688 = 1.3125 * 2^11.
-  const int e = bad || !(amax > 0.f) ? 0
-                : FMT == kKvE4m3     ? scale_exponent<8, 0x600000>(amax)
-                                     : scale_exponent<11, 0x280000>(amax);
-  const float inv = pow2i(-e);
-  uint8_t *scale = (value ? p.v_scale : p.k_scale) + at.row;
-  if (at.ok && hl == 0) *scale = bad ? 255 : (uint8_t)(e + 127);
-  if constexpr (FMT == kKvE4m3) {
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-    if (at.ok)
-      *reinterpret_cast<uint2 *>(codes + hl * 8) =
-          bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    if (!at.ok) return;
+    uint4 v;
+    if constexpr (F32)
+      v = make_uint4(bf16x2(x.at(0), x.at(1)), bf16x2(x.at(2), x.at(3)), bf16x2(x.at(4), x.at(5)),
+                     bf16x2(x.at(6), x.at(7)));
+    else
+      v = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    *reinterpret_cast<uint4 *>(codes + hl * 16) = v;
   } else {
-    // Two lanes share a block of sixteen.
-    const float bmax = fmaxf(m, __shfl_xor_sync(hmask, m, 1)) * inv;
-    // Nearest E4M3 to bmax / 6, then one code up if it lies below.
-    uint32_t b = e4m3x2(__fdiv_rn(bmax, 6.f), 0.f) & 0xffu;
-    if (6.f * e4m3_value(b) < bmax) ++b;
-    const float s = e4m3_value(b), by = s > 0.f ? s : 1.f;  // b = 0 only for sixteen zeros
-    uint32_t w = 0;
+    const uint32_t mine = x.top();
+    const uint32_t pair = max(mine, __shfl_xor_sync(hmask, mine, 1));
+    uint32_t m = pair;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // y / s in fp32 rounds to an E2M1 midpoint only when it is one: a
-      // midpoint times s has at most 7 significant bits, so y either equals it
-      // or is at least one fp32 step away from it.
-      w |= e2m1x2(__fdiv_rn(x[2 * i] * inv, by), __fdiv_rn(x[2 * i + 1] * inv, by)) << (8 * i);
-    }
-    if (at.ok) {
-      *reinterpret_cast<uint32_t *>(codes + hl * 4) = bad ? 0u : w;
-      if ((hl & 1) == 0) (value ? p.v_bs : p.k_bs)[at.row * (D / 16) + (hl >> 1)] = bad ? 0 : b;
+    for (int o = 2; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(hmask, m, o));
+    const bool bad = m >= 0x7f800000u;  // an infinity or a NaN
+    // top = 448 = 1.75 * 2^8, or 2688 = 1.3125 * 2^11.
+    const int e = bad || m == 0u     ? 0
+                  : FMT == kKvE4m3 ? scale_exponent<8, 0x600000>(m)
+                                   : scale_exponent<11, 0x280000>(m);
+    const float inv = pow2i(-e);
+    if (at.ok && hl == 0) (value ? p.v_scale : p.k_scale)[at.row] = bad ? 255 : (uint8_t)(e + 127);
+    if constexpr (FMT == kKvE4m3) {
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = e4m3x2(x.at(2 * i) * inv, x.at(2 * i + 1) * inv);
+      if (at.ok)
+        *reinterpret_cast<uint2 *>(codes + hl * 8) =
+            bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    } else {
+      // Two lanes share a block of sixteen.
+      const float bmax = __uint_as_float(pair) * inv;
+      // Nearest E4M3 to bmax / 6, then one code up if it lies below.
+      uint32_t b = e4m3x2(__fdiv_rn(bmax, 6.f), 0.f) & 0xffu;
+      if (6.f * e4m3_value(b) < bmax) ++b;
+      const float s = e4m3_value(b), by = s > 0.f ? s : 1.f;  // b = 0 only for sixteen zeros
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // y / s in fp32 rounds to an E2M1 midpoint only when it is one: a
+        // midpoint times s has at most 7 significant bits, so y either equals it
+        // or is at least one fp32 step away from it.
+        w |= e2m1x2(__fdiv_rn(x.at(2 * i) * inv, by), __fdiv_rn(x.at(2 * i + 1) * inv, by)) << (8 * i);
+      }
+      if (at.ok) {
+        *reinterpret_cast<uint32_t *>(codes + hl * 4) = bad ? 0u : w;
+        if ((hl & 1) == 0) (value ? p.v_bs : p.k_bs)[at.row * (D / 16) + (hl >> 1)] = bad ? 0 : b;
+      }
     }
   }
 }
 
-// One half warp: kRows consecutive tokens of one (head, key or value).
-template <int FMT, bool F32, int kRows>
-__global__ void __launch_bounds__(NT) kv_append_kernel(const KvAppendArgs a) {
+// One half warp: the key and value rows of kTok consecutive tokens of one head.
+template <int FMT, bool F32, int kTok>
+__global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
   const int hl = threadIdx.x & 15;
   const unsigned hmask = 0xffffu << (threadIdx.x & 16);
-  const int64_t unit = (int64_t)blockIdx.x * HALVES + (threadIdx.x >> 4);
-  const int per = 2 * a.pages.Hkv;
-  const int64_t t0 = unit / per * kRows;
+  const unsigned unit = blockIdx.x * HALVES + (threadIdx.x >> 4);
+  const unsigned tg = unit / (unsigned)a.pages.Hkv;
+  const int h = (int)(unit - tg * (unsigned)a.pages.Hkv);
+  const int64_t t0 = (int64_t)tg * kTok;
   if (t0 >= a.total) return;
-  const int hv = (int)(unit % per);
-  const bool value = hv >= a.pages.Hkv;
-  const int h = value ? hv - a.pages.Hkv : hv;
-  const void *src = value ? a.v_new : a.k_new;
-  const int64_t ts = value ? a.v_tok_stride : a.k_tok_stride;
-  float x[kRows][8];
+  New<F32> x[kTok][2];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r)
-    if (t0 + r < a.total) load8<F32>(src, (t0 + r) * ts + (int64_t)h * D + hl * 8, x[r]);
+  for (int r = 0; r < kTok; ++r)
+    if (t0 + r < a.total) {
+      x[r][0].load(a.k_new, (t0 + r) * a.k_tok_stride + h * D + hl * 8);
+      x[r][1].load(a.v_new, (t0 + r) * a.v_tok_stride + h * D + hl * 8);
+    }
   int s = find_seq(a.cu_seqlens, a.n_seq, (int)t0, hl, hmask);
-  Place at[kRows];
   bool bad = false;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    at[r].ok = 0;
+  for (int r = 0; r < kTok; ++r) {
     const int t = (int)t0 + r;
+    if (t >= a.total) break;
     while (s < a.n_seq && __ldg(a.cu_seqlens + s + 1) <= t) ++s;
-    if (t >= a.total || s >= a.n_seq) continue;  // behind the last sequence
+    if (s >= a.n_seq) break;  // behind the last sequence
     const int c0 = __ldg(a.cu_seqlens + s), c1 = __ldg(a.cu_seqlens + s + 1);
     const int len = __ldg(a.kv_len + s);
+    Place at{0, 0, false};
     // The sequence's bounds and its length are checked as a whole, so that no
     // row of a sequence with a bad length is written.
     if (c0 < 0 || c0 > t || c1 > a.total || len < 0 ||
         len > (int64_t)a.max_pages * a.pages.page_size) {
       bad = true;
-      continue;
+    } else if ((int64_t)len - c1 + t >= 0) {  // else the chunk is longer than the cache
+      at = place_of<RowBytes<FMT>::value>(a.pages, a.page_table, a.max_pages, s,
+                                          (int64_t)len - c1 + t, h);
+      bad |= !at.ok;
     }
-    const int64_t pos = (int64_t)len - c1 + t;
-    if (pos < 0) continue;  // the chunk is longer than the cache: no such position
-    at[r] = place_of<RowBytes<FMT>::value>(a.pages, a.page_table, a.max_pages, s, pos, h);
-    bad |= !at[r].ok;
-  }
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (t0 + r < a.total) store_row<FMT>(a.pages, value, at[r], x[r], hl, hmask);
+    store_row<FMT, F32>(a.pages, false, at, x[r][0], hl, hmask);
+    store_row<FMT, F32>(a.pages, true, at, x[r][1], hl, hmask);
   }
   if (bad && hl == 0) atomicOr(a.err, kErrBadArg);
 }
 
-// This lane's eight elements of a stored row as fp32 (exact).
+// This lane's share of a stored row: two runs of four elements, for which the
+// outputs' 16-byte (fp32) or 8-byte (bf16) stores are contiguous over the lanes.
+// Run i: elements 64 i + 4 hl and on.
 struct Raw {
-  uint4 c;       // codes
-  uint32_t s, b; // row scale byte, block scale byte
+  uint2 c[2];     // codes (bf16: the elements)
+  uint32_t s;     // row scale byte
+  uint32_t b[2];  // block scale bytes
 };
 
 template <int FMT>
 __device__ __forceinline__ Raw load_raw(const KvPages &p, bool value, const Place &at, int hl) {
-  Raw r{make_uint4(0, 0, 0, 0), 127, 0};
+  Raw r{{make_uint2(0, 0), make_uint2(0, 0)}, 127, {0, 0}};
   if (!at.ok) return r;
   const uint8_t *codes = (const uint8_t *)(value ? p.v : p.k) + at.byte;
-  if constexpr (FMT == kKvBf16) {
-    r.c = __ldg(reinterpret_cast<const uint4 *>(codes + hl * 16));
-  } else {
-    r.s = __ldg((value ? p.v_scale : p.k_scale) + at.row);
-    if constexpr (FMT == kKvE4m3) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(codes + hl * 8));
-      r.c.x = v.x;
-      r.c.y = v.y;
+  if constexpr (FMT != kKvBf16) r.s = __ldg((value ? p.v_scale : p.k_scale) + at.row);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (FMT == kKvBf16) {
+      r.c[i] = __ldg(reinterpret_cast<const uint2 *>(codes + i * 128) + hl);
+    } else if constexpr (FMT == kKvE4m3) {
+      r.c[i].x = __ldg(reinterpret_cast<const uint32_t *>(codes + i * 64) + hl);
     } else {
-      r.c.x = __ldg(reinterpret_cast<const uint32_t *>(codes + hl * 4));
-      r.b = __ldg((value ? p.v_bs : p.k_bs) + at.row * (D / 16) + (hl >> 1));
+      r.c[i].x = __ldg(reinterpret_cast<const uint16_t *>(codes + i * 32) + hl);
+      r.b[i] = __ldg((value ? p.v_bs : p.k_bs) + at.row * (D / 16) + i * 4 + (hl >> 2));
     }
   }
   return r;
@@ -269,116 +287,112 @@ __device__ __forceinline__ void f16x2_to_f32(uint32_t h, float f, float &lo, flo
   hi = __half2float(__ushort_as_half((unsigned short)(h >> 16))) * f;
 }
 
+// Run i as fp32 (exact).
 template <int FMT>
-__device__ __forceinline__ void decode_raw(const Raw &r, float (&x)[8]) {
+__device__ __forceinline__ void decode_raw(const Raw &r, int i, float f, float (&x)[4]) {
   if constexpr (FMT == kKvBf16) {
-    const uint32_t w[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-    return;
-  }
-  // Byte 0 stands for 2^-127 (an fp32 subnormal), 255 for NaN.
-  const float f = r.s == 255u ? NAN : r.s == 0u ? 5.877471754111438e-39f : __uint_as_float(r.s << 23);
-  if constexpr (FMT == kKvE4m3) {
-    const uint32_t w[2] = {r.c.x, r.c.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t h;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
-          : "=r"(h)
-          : "h"((unsigned short)(w[i >> 1] >> (16 * (i & 1)))));
-      f16x2_to_f32(h, f, x[2 * i], x[2 * i + 1]);
-    }
+    x[0] = __uint_as_float(r.c[i].x << 16);
+    x[1] = __uint_as_float(r.c[i].x & 0xffff0000u);
+    x[2] = __uint_as_float(r.c[i].y << 16);
+    x[3] = __uint_as_float(r.c[i].y & 0xffff0000u);
   } else {
-    const float s = e4m3_value(r.b);
+    uint32_t h[2];
+    if constexpr (FMT == kKvE4m3) {
+      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+          "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+          : "=r"(h[0]), "=r"(h[1])
+          : "r"(r.c[i].x));
+      f16x2_to_f32(h[0], f, x[0], x[1]);
+      f16x2_to_f32(h[1], f, x[2], x[3]);
+    } else {
+      asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %2;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
+          : "=r"(h[0]), "=r"(h[1])
+          : "r"(r.c[i].x));
+      const float s = e4m3_value(r.b[i]);  // code times block scale: exact, at most six bits
+      f16x2_to_f32(h[0], s, x[0], x[1]);
+      f16x2_to_f32(h[1], s, x[2], x[3]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t h;
-      asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
-          : "=r"(h)
-          : "r"((r.c.x >> (8 * i)) & 0xffu));
-      f16x2_to_f32(h, s, x[2 * i], x[2 * i + 1]);  // exact: at most six bits
-      x[2 * i] *= f;
-      x[2 * i + 1] *= f;
+      for (int k = 0; k < 4; ++k) x[k] *= f;
     }
   }
 }
 
-template <int FMT, bool F32, int kRows>
-__global__ void __launch_bounds__(NT) kv_gather_kernel(const KvGatherArgs a) {
+template <int FMT, bool F32, int kTok>
+__global__ void __launch_bounds__(NT) kv_gather_kernel(const __grid_constant__ KvGatherArgs a) {
   const int hl = threadIdx.x & 15;
   const unsigned hmask = 0xffffu << (threadIdx.x & 16);
-  const int64_t unit = (int64_t)blockIdx.x * HALVES + (threadIdx.x >> 4);
-  const int per = 2 * a.pages.Hkv;
-  const int64_t t0 = unit / per * kRows;
+  const unsigned unit = blockIdx.x * HALVES + (threadIdx.x >> 4);
+  const unsigned tg = unit / (unsigned)a.pages.Hkv;
+  const int h = (int)(unit - tg * (unsigned)a.pages.Hkv);
+  const int64_t t0 = (int64_t)tg * kTok;
   if (t0 >= a.total) return;
-  const int hv = (int)(unit % per);
-  const bool value = hv >= a.pages.Hkv;
-  const int h = value ? hv - a.pages.Hkv : hv;
   int s = find_seq(a.cu_rows, a.n_seq, (int)t0, hl, hmask);
-  Place at[kRows];
-  Raw raw[kRows];
-  bool bad = false, write[kRows];
+  Raw raw[kTok][2];
+  bool bad = false;
+  int n = 0;  // rows of sequences (the others stay as they were)
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
+  for (int r = 0; r < kTok; ++r) {
     const int t = (int)t0 + r;
-    at[r].ok = 0;
-    write[r] = false;
     while (s < a.n_seq && __ldg(a.cu_rows + s + 1) <= t) ++s;
-    if (t >= a.total || s >= a.n_seq) continue;
+    if (t >= a.total || s >= a.n_seq) break;
+    n = r + 1;
     const int c0 = __ldg(a.cu_rows + s);
-    write[r] = true;
-    if (c0 >= 0 && c0 <= t) {
-      const int64_t pos = (int64_t)(a.start ? __ldg(a.start + s) : 0) + (t - c0);
-      at[r] = place_of<RowBytes<FMT>::value>(a.pages, a.page_table, a.max_pages, s, pos, h);
-    }
-    bad |= !at[r].ok;
+    Place at{0, 0, false};
+    if (c0 >= 0 && c0 <= t)
+      at = place_of<RowBytes<FMT>::value>(a.pages, a.page_table, a.max_pages, s,
+                                          (int64_t)(a.start ? __ldg(a.start + s) : 0) + (t - c0), h);
+    bad |= !at.ok;
+    raw[r][0] = load_raw<FMT>(a.pages, false, at, hl);
+    raw[r][1] = load_raw<FMT>(a.pages, true, at, hl);
   }
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) raw[r] = load_raw<FMT>(a.pages, value, at[r], hl);
+  for (int r = 0; r < kTok; ++r) {
+    if (r >= n) break;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (!write[r]) continue;
-    float x[8];
-    decode_raw<FMT>(raw[r], x);
-    const int64_t elem = ((t0 + r) * a.pages.Hkv + h) * D + hl * 8;
-    if constexpr (F32) {
-      float4 *o = reinterpret_cast<float4 *>((float *)(value ? a.v_out : a.k_out) + elem);
-      o[0] = make_float4(x[0], x[1], x[2], x[3]);
-      o[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      *reinterpret_cast<uint4 *>((__nv_bfloat16 *)(value ? a.v_out : a.k_out) + elem) =
-          make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
+    for (int w = 0; w < 2; ++w) {
+      const Raw &y = raw[r][w];
+      // Byte 0 stands for 2^-127 (an fp32 subnormal), 255 for NaN.
+      const float f = y.s == 255u ? NAN : y.s == 0u ? 5.877471754111438e-39f : __uint_as_float(y.s << 23);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x[4];
+        decode_raw<FMT>(y, i, f, x);
+        const int64_t elem = ((t0 + r) * a.pages.Hkv + h) * D + i * 64 + hl * 4;
+        void *out = w ? a.v_out : a.k_out;
+        if constexpr (F32)
+          *reinterpret_cast<float4 *>((float *)out + elem) = make_float4(x[0], x[1], x[2], x[3]);
+        else
+          *reinterpret_cast<uint2 *>((__nv_bfloat16 *)out + elem) =
+              make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
+      }
     }
   }
   if (bad && hl == 0) atomicOr(a.err, kErrBadArg);
 }
 
-// Rows per half warp: four when that still gives every SM a full set of
-// blocks, else one, so that a small call spreads over the chip.
-constexpr int kManyRows = 4;
-bool many_rows(int64_t total, int Hkv) {
-  return total * 2 * Hkv >= (int64_t)kManyRows * HALVES * 152 * 8;
-}
-unsigned grid_of(int64_t total, int Hkv, int rows) {
-  const int64_t units = (total + rows - 1) / rows * 2 * Hkv;
+// Tokens per half warp: four (two of fp32 rows) when that still gives every SM
+// eight blocks, else one, so that a small call spreads over the chip.
+template <bool F32> constexpr int kMany = F32 ? 2 : 4;
+bool many(int64_t total, int Hkv) { return total * Hkv >= (int64_t)4 * HALVES * 152 * 8; }
+unsigned grid_of(int64_t total, int Hkv, int tok) {
+  const int64_t units = (total + tok - 1) / tok * Hkv;
   return (unsigned)((units + HALVES - 1) / HALVES);
 }
 
 template <int FMT, bool F32>
 void append_fmt(const KvAppendArgs &a, cudaStream_t s) {
-  if (many_rows(a.total, a.pages.Hkv))
-    kv_append_kernel<FMT, F32, kManyRows><<<grid_of(a.total, a.pages.Hkv, kManyRows), NT, 0, s>>>(a);
+  constexpr int M = kMany<F32>;
+  if (many(a.total, a.pages.Hkv))
+    kv_append_kernel<FMT, F32, M><<<grid_of(a.total, a.pages.Hkv, M), NT, 0, s>>>(a);
   else
     kv_append_kernel<FMT, F32, 1><<<grid_of(a.total, a.pages.Hkv, 1), NT, 0, s>>>(a);
 }
 template <int FMT, bool F32>
 void gather_fmt(const KvGatherArgs &a, cudaStream_t s) {
-  if (many_rows(a.total, a.pages.Hkv))
-    kv_gather_kernel<FMT, F32, kManyRows><<<grid_of(a.total, a.pages.Hkv, kManyRows), NT, 0, s>>>(a);
+  constexpr int M = kMany<F32>;
+  if (many(a.total, a.pages.Hkv))
+    kv_gather_kernel<FMT, F32, M><<<grid_of(a.total, a.pages.Hkv, M), NT, 0, s>>>(a);
   else
     kv_gather_kernel<FMT, F32, 1><<<grid_of(a.total, a.pages.Hkv, 1), NT, 0, s>>>(a);
 }
