@@ -33,7 +33,8 @@ EXPORTED = ("attn_skip_prefill", "attn_skip_prefill_from_host", "attn_skip_prefi
             "attn_skip_last_device_error", "attn_skip_status_string",
             "attn_skip_santa_workspace", "attn_skip_santa_decode",
             "attn_skip_santa_decode_noalloc", "attn_skip_kv_append", "attn_skip_kv_gather",
-            "attn_skip_chunk_paged", "attn_skip_chunk_paged_splits")
+            "attn_skip_chunk_paged", "attn_skip_chunk_paged_splits",
+            "attn_skip_chunk_paged_kv_bytes")
 
 #: Samplers of attn_skip_santa_decode.
 SANTA_MODES = {"iid": 0, "sys": 1, "strat": 2}
@@ -104,7 +105,9 @@ def load() -> ctypes.CDLL:
     lib.attn_skip_kv_append.argtypes = [P, P, P, i, i64, i64, i, i, P, P, P, i, P]
     lib.attn_skip_kv_gather.argtypes = [P, i, i, P, P, P, i, i, P, P, P]
     lib.attn_skip_chunk_paged.argtypes = [P, P, i64, i, i, i, P, i, P, i, P, i, f, P, i, i, P, P,
-                                          P, P, P, P]
+                                          P, P, P, P, P]
+    lib.attn_skip_chunk_paged_kv_bytes.argtypes = [i] * 6
+    lib.attn_skip_chunk_paged_kv_bytes.restype = ctypes.c_size_t
     lib.attn_skip_chunk_paged_splits.argtypes = [i] * 7
     lib.attn_skip_chunk_paged_splits.restype = ctypes.c_int
     lib.attn_skip_status_string.argtypes = [i]
@@ -772,6 +775,12 @@ def attn_skip_chunk_paged_splits(kv, n_seq, total, Hq, max_chunk, max_kv):
                                                max_chunk, max_kv)
 
 
+def attn_skip_chunk_paged_kv_bytes(kv, n_seq, Hq, max_chunk, max_kv):
+    """Bytes of workspace in which attn_skip_chunk_paged widens ``kv`` first."""
+    return load().attn_skip_chunk_paged_kv_bytes(KV_FORMATS[kv.format], n_seq, Hq, kv.Hkv,
+                                                 max_chunk, max_kv)
+
+
 def chunk_bitmap_shape(n_seq, Hq, Hkv, max_chunk, max_kv, n_splits):
     tt = 128 // (Hq // Hkv)
     bps = -(-(-(-max_kv // 128)) // n_splits)
@@ -780,7 +789,7 @@ def chunk_bitmap_shape(n_seq, Hq, Hkv, max_chunk, max_kv, n_splits):
 
 def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_table, lambdas,
                           causal=True, scale=0.0, n_splits=0, with_bits=False, out=None,
-                          workspace=None, stream=None):
+                          workspace=None, rows=None, stream=None):
     """Attention of the new tokens q [total, Hq, 128] bf16 (the token stride is
     free) of a batch of sequences over the paged cache ``kv``, which already
     holds their keys and values; one new token per sequence is a decode step.
@@ -789,12 +798,13 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
     Returns ``(o [total, Hq, 128] bf16, lse [total, Hq], skip_bits)``, skip_bits
     ``None`` without ``with_bits``.  ``out`` may pass these three, ``workspace``
     the partials ``(o_part [total, Hq, n_splits, 128], lse_part [total, Hq,
-    n_splits])`` fp32 of n_splits > 1."""
+    n_splits])`` fp32 of n_splits > 1 and ``rows`` a uint8 tensor of at least
+    attn_skip_chunk_paged_kv_bytes bytes; they are allocated otherwise."""
     if _elsewhere(kv, stream):
         with _switched(kv, stream):
             return attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_table,
                                          lambdas, causal, scale, n_splits, with_bits, out,
-                                         workspace)
+                                         workspace, rows)
     n = _batch(kv, cu_seqlens, page_table, kv_len)
     _per_sequence("lambdas", lambdas, n, torch.float32, kv)
     if q.dtype is not torch.bfloat16 or q.dim() != 3:
@@ -823,20 +833,28 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
             _like("skip_bits", bits, shape, torch.int32, kv)
     op = lp = 0
     if n_splits > 1:
-        rows = total * Hq * n_splits
+        parts = total * Hq * n_splits
         if workspace is None:
-            work = torch.empty(rows * (d + 1), dtype=torch.float32, device=kv.device)
+            work = torch.empty(parts * (d + 1), dtype=torch.float32, device=kv.device)
             op = work.data_ptr()
-            lp = op + rows * d * 4
+            lp = op + parts * d * 4
         else:
             _like("workspace", workspace[0], (total, Hq, n_splits, d), torch.float32, kv)
             _like("workspace", workspace[1], (total, Hq, n_splits), torch.float32, kv)
             op, lp = workspace[0].data_ptr(), workspace[1].data_ptr()
+    size = lib.attn_skip_chunk_paged_kv_bytes(kv._c.format, n, Hq, kv.Hkv, max_chunk, max_kv)
+    if rows is None:
+        if size:
+            rows = torch.empty(size, dtype=torch.uint8, device=kv.device)
+    elif rows.dtype is not torch.uint8 or rows.numel() < size or not rows.is_contiguous() \
+            or rows.get_device() != kv.index:
+        raise ValueError(f"rows must be a contiguous uint8 tensor of {size} bytes on {kv.device}")
     _check("attn_skip_chunk_paged", lib.attn_skip_chunk_paged(
         kv._ref, q.data_ptr(), qs, Hq, n, total, cu_seqlens.data_ptr(), max_chunk,
         kv_len.data_ptr(), max_kv, page_table.data_ptr(), page_table.shape[1], scale,
         lambdas.data_ptr(), 1 if causal else 0, n_splits, o.data_ptr(), lse.data_ptr(),
-        None if bits is None else bits.data_ptr(), op, lp, _raw_stream(kv)))
+        None if bits is None else bits.data_ptr(), op, lp,
+        None if rows is None else rows.data_ptr(), _raw_stream(kv)))
     return o, lse, bits
 
 

@@ -619,12 +619,20 @@ extern "C" int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, in
   return chunk_paged_splits(n_seq, total, max_chunk, max_kv, Hkv, 128 / (Hq / Hkv), (int)format);
 }
 
+extern "C" size_t attn_skip_chunk_paged_kv_bytes(attn_kv_format format, int n_seq, int Hq, int Hkv,
+                                                 int max_chunk, int max_kv) {
+  if (n_seq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || max_chunk <= 0 ||
+      max_kv <= 0 || max_kv > kMaxPositions)
+    return 0;
+  return chunk_paged_kv_bytes(n_seq, max_chunk, max_kv, Hkv, 128 / (Hq / Hkv), (int)format);
+}
+
 extern "C" attn_status attn_skip_chunk_paged(
     const attn_kv_pages *kv, const void *q, int64_t q_tok_stride, int Hq, int n_seq, int total,
     const int32_t *cu_seqlens, int max_chunk, const int32_t *kv_len, int max_kv,
     const int32_t *page_table, int max_pages, float scale, const float *lambda, int causal,
     int n_splits, void *o, float *lse, uint32_t *skip_bits, float *o_part, float *lse_part,
-    void *stream) {
+    void *kv_work, void *stream) {
   ChunkArgs a{};
   const attn_status st =
       pages_check(kv, n_seq, total, cu_seqlens, page_table, max_pages, a.pages);
@@ -655,7 +663,9 @@ extern "C" attn_status attn_skip_chunk_paged(
   if (n_splits > 1 && (!o_part || !lse_part || !aligned16(o_part) || !aligned4(lse_part)))
     return ATTN_EINVAL;
   a.q = q; a.q_tok_stride = q_tok_stride;
+  if (!aligned16(kv_work)) return ATTN_EINVAL;
   a.o = o; a.lse = lse; a.bits = skip_bits; a.o_part = o_part; a.lse_part = lse_part;
+  a.kv_work = kv_work;
   a.n_seq = n_seq; a.Hq = Hq; a.Hkv = kv->Hkv; a.G = G; a.total = total;
   a.max_chunk = max_chunk; a.max_kv = max_kv; a.max_pages = max_pages; a.causal = causal ? 1 : 0;
   a.n_splits = n_splits;

@@ -225,9 +225,9 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&s)[32], uint64_t sl2x
 
 // Block j's rows (codes and scales) into the staging area or tile at dst, part by
 // part, one lane a part; whole warp.  The arrival with the byte count comes
-// first.  Out of line: its four callers share the instruction cache.
+// first.
 template <int FMT>
-__device__ __noinline__ void load_block(const ChunkArgs &a, Producer &p, const CUtensorMap *map,
+__device__ __forceinline__ void load_block_here(const ChunkArgs &a, Producer &p, const CUtensorMap *map,
                                         bool value, int j, uint32_t dst, uint32_t full, int lane) {
   using C = Cfg<FMT>;
   constexpr bool QUANT = FMT != kKvBf16;
@@ -256,6 +256,24 @@ __device__ __noinline__ void load_block(const ChunkArgs &a, Producer &p, const C
     }
   }
   __syncwarp();
+}
+
+// Out of line for the quantised formats, whose converters need the instruction
+// cache; in line for bf16 (decode of 16 x 32768: 339 against 322 us).
+template <int FMT>
+__device__ __noinline__ void load_block_call(const ChunkArgs &a, Producer &p, const CUtensorMap *map,
+                                             bool value, int j, uint32_t dst, uint32_t full,
+                                             int lane) {
+  load_block_here<FMT>(a, p, map, value, j, dst, full, lane);
+}
+template <int FMT>
+__device__ __forceinline__ void load_block(const ChunkArgs &a, Producer &p, const CUtensorMap *map,
+                                           bool value, int j, uint32_t dst, uint32_t full,
+                                           int lane) {
+  if constexpr (FMT == kKvBf16)
+    load_block_here<FMT>(a, p, map, value, j, dst, full, lane);
+  else
+    load_block_call<FMT>(a, p, map, value, j, dst, full, lane);
 }
 
 // ------------------------------------------------------------- conversions --
@@ -1236,7 +1254,41 @@ int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv,
   return best;
 }
 
-cudaError_t launch_chunk_paged(const ChunkArgs &a, cudaStream_t s) {
+// Bytes of the bf16 rows that a quantised cache is widened to first, 0 where it
+// is not.  Widening a 128-key block of a KV head once moves about 100 KB (15 ns
+// of the memory's time); converting it on the way costs each tile that reads it
+// 0.7 us of an SM, 5 ns of the chip, so from four tiles of a sequence on the
+// rows are written out (a chunk of 4096 on 16384 over E4M3 pages: 1318 us with
+// converters, 790 with widened rows).  Not where they would take over 4 GiB: the
+// bound is the longest sequence's, for every sequence.
+size_t chunk_paged_kv_bytes(int n_seq, int max_chunk, int max_kv, int Hkv, int TT, int format) {
+  if (format == kKvBf16 || (max_chunk + TT - 1) / TT < 4) return 0;
+  const size_t rows = (size_t)n_seq * Hkv * (((size_t)max_kv + BN - 1) / BN * BN);
+  return rows * D * 2 * 2 <= (size_t)4 << 30 ? rows * D * 2 * 2 : 0;
+}
+
+cudaError_t launch_chunk_paged(const ChunkArgs &args, cudaStream_t s) {
+  ChunkArgs a = args;
+  if (a.kv_work) {
+    const size_t bytes = chunk_paged_kv_bytes(a.n_seq, a.max_chunk, a.max_kv, a.Hkv, a.TT, a.pages.format);
+    if (bytes && (int64_t)a.n_seq * a.Hkv <= 65535) {
+      KvWidenArgs w{};
+      w.pages = a.pages;
+      w.k_out = a.kv_work;
+      w.v_out = (char *)a.kv_work + bytes / 2;
+      w.n_seq = a.n_seq; w.max_kv = a.max_kv; w.max_pages = a.max_pages;
+      w.stride = (a.max_kv + BN - 1) / BN * BN;
+      w.kv_len = a.kv_len; w.page_table = a.page_table; w.err = a.err;
+      const cudaError_t e = launch_kv_widen(w, s);
+      if (e != cudaSuccess) return e;
+      KvPages &p = a.pages;  // from here on a bf16 cache of one page a sequence
+      p.format = kKvBf16;
+      p.k = w.k_out; p.v = w.v_out;
+      p.n_pages = a.n_seq; p.page_size = w.stride; p.page_shift = -1;
+      p.page_stride = (int64_t)a.Hkv * w.stride * D * 2;
+      a.page_table = nullptr;
+    }
+  }
   const int64_t units = tiles_bound(a.n_seq, a.total, a.max_chunk, a.TT) * a.Hkv * a.n_splits;
   if (units > 0x7fffffffL) return cudaErrorNotYetImplemented;  // more CTAs than a grid has
   const int q_tokens = a.TT < a.max_chunk ? a.TT : a.max_chunk;

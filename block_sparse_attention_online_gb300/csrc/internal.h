@@ -118,6 +118,14 @@ struct KvGatherArgs {
   unsigned *err;
 };
 
+struct KvWidenArgs {
+  KvPages pages;
+  void *k_out, *v_out;                 // bf16 [n_seq][Hkv][stride][128]
+  int n_seq, max_kv, stride, max_pages;
+  const int32_t *kv_len, *page_table;
+  unsigned *err;
+};
+
 // Attention of a chunk of new tokens per sequence over the paged cache.
 struct ChunkArgs {
   KvPages pages;
@@ -127,16 +135,20 @@ struct ChunkArgs {
   float *lse;                          // [total][Hq]
   uint32_t *bits;                      // [n_seq][Hkv][n_t][n_splits][words], or null
   float *o_part, *lse_part;            // [total][Hq][n_splits][128] / [..][n_splits] (n_splits > 1)
+  void *kv_work;                       // bf16 rows of a quantised cache, or null
   int n_seq, Hq, Hkv, G, TT;           // TT: tokens per tile, floor(128 / G)
   int total, max_chunk, max_kv, max_pages, causal;
   int n_splits, bps, n_t, words;       // bps: blocks per split
-  const int32_t *cu_seqlens, *kv_len, *page_table;
+  const int32_t *cu_seqlens, *kv_len;
+  const int32_t *page_table;           // null: sequence s's rows are page s
   const float *lambda;
   float scale;
   unsigned *err;
 };
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
+cudaError_t launch_kv_widen(const KvWidenArgs &a, cudaStream_t s);
+size_t chunk_paged_kv_bytes(int n_seq, int max_chunk, int max_kv, int Hkv, int TT, int format);
 cudaError_t launch_kv_gather(const KvGatherArgs &a, cudaStream_t s);
 cudaError_t launch_chunk_paged(const ChunkArgs &a, cudaStream_t s);
 cudaError_t launch_decode_paged(const ChunkArgs &a, unsigned grid, cudaStream_t s);

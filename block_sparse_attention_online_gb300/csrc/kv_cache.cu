@@ -287,6 +287,11 @@ __device__ __forceinline__ void f16x2_to_f32(uint32_t h, float f, float &lo, flo
   hi = __half2float(__ushort_as_half((unsigned short)(h >> 16))) * f;
 }
 
+// Byte 0 stands for 2^-127 (an fp32 subnormal), 255 for NaN.
+__device__ __forceinline__ float row_scale(uint32_t byte) {
+  return byte == 255u ? NAN : byte == 0u ? 5.877471754111438e-39f : __uint_as_float(byte << 23);
+}
+
 // Run i as fp32 (exact).
 template <int FMT>
 __device__ __forceinline__ void decode_raw(const Raw &r, int i, float f, float (&x)[4]) {
@@ -352,8 +357,7 @@ __global__ void __launch_bounds__(NT) kv_gather_kernel(const __grid_constant__ K
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const Raw &y = raw[r][w];
-      // Byte 0 stands for 2^-127 (an fp32 subnormal), 255 for NaN.
-      const float f = y.s == 255u ? NAN : y.s == 0u ? 5.877471754111438e-39f : __uint_as_float(y.s << 23);
+      const float f = row_scale(y.s);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float x[4];
@@ -365,6 +369,50 @@ __global__ void __launch_bounds__(NT) kv_gather_kernel(const __grid_constant__ K
         else
           *reinterpret_cast<uint2 *>((__nv_bfloat16 *)out + elem) =
               make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
+      }
+    }
+  }
+  if (bad && hl == 0) atomicOr(a.err, kErrBadArg);
+}
+
+// Every cached row of a quantised cache as bf16 (exact), sequence s's head h at
+// rows [(s * Hkv + h) * stride, ..) of k_out and v_out, for a bf16 kernel that
+// reads them many times.  One half warp: the key and value rows of four
+// consecutive positions of one (sequence, head).  A row of a page id out of range
+// becomes zeros.
+template <int FMT>
+__global__ void __launch_bounds__(NT) kv_widen_kernel(const __grid_constant__ KvWidenArgs a) {
+  constexpr int kTok = 4;
+  const int hl = threadIdx.x & 15;
+  const int p0 = (int)(blockIdx.x * HALVES + (threadIdx.x >> 4)) * kTok;
+  const int h = (int)(blockIdx.y % (unsigned)a.pages.Hkv), s = (int)(blockIdx.y / (unsigned)a.pages.Hkv);
+  int len = __ldg(a.kv_len + s);
+  if (len > a.max_kv) len = 0;  // (a bad length is an empty cache; the attention reports it)
+  if (p0 >= len) return;
+  Raw raw[kTok][2];
+  bool bad = false;
+#pragma unroll
+  for (int r = 0; r < kTok; ++r) {
+    if (p0 + r >= len) break;
+    const Place at = place_of<RowBytes<FMT>::value>(a.pages, a.page_table, a.max_pages, s, p0 + r, h);
+    bad |= !at.ok;
+    raw[r][0] = load_raw<FMT>(a.pages, false, at, hl);
+    raw[r][1] = load_raw<FMT>(a.pages, true, at, hl);
+  }
+  const int64_t row0 = ((int64_t)s * a.pages.Hkv + h) * a.stride + p0;
+#pragma unroll
+  for (int r = 0; r < kTok; ++r) {
+    if (p0 + r >= len) break;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const Raw &y = raw[r][w];
+      const float f = row_scale(y.s);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x[4];
+        decode_raw<FMT>(y, i, f, x);
+        *reinterpret_cast<uint2 *>((__nv_bfloat16 *)(w ? a.v_out : a.k_out) + (row0 + r) * D + i * 64 + hl * 4) =
+            make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
       }
     }
   }
@@ -414,6 +462,16 @@ cudaError_t launch_kv_gather(const KvGatherArgs &a, cudaStream_t s) {
     case kKvE4m3: a.out_f32 ? gather_fmt<kKvE4m3, true>(a, s) : gather_fmt<kKvE4m3, false>(a, s); break;
     default: a.out_f32 ? gather_fmt<kKvNvfp4, true>(a, s) : gather_fmt<kKvNvfp4, false>(a, s); break;
   }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_widen(const KvWidenArgs &a, cudaStream_t s) {
+  const dim3 grid((unsigned)((a.max_kv + 4 * HALVES - 1) / (4 * HALVES)),
+                  (unsigned)(a.n_seq * a.pages.Hkv));
+  if (a.pages.format == kKvE4m3)
+    kv_widen_kernel<kKvE4m3><<<grid, NT, 0, s>>>(a);
+  else
+    kv_widen_kernel<kKvNvfp4><<<grid, NT, 0, s>>>(a);
   return cudaGetLastError();
 }
 

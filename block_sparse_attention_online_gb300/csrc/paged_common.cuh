@@ -125,7 +125,8 @@ __device__ __noinline__ void locate(const ChunkArgs &a, int i, int split, int la
 // loaded one window ahead.  A page id out of range is reported and page 0 read
 // in its place.
 struct Producer {
-  const int32_t *table;  // the sequence's row
+  const int32_t *table;  // the sequence's row; null: its rows are page `seq`
+  int seq;
   int sub, per_page;     // rows of a part, parts of a page
   int n_parts, base, cur, nxt, hk;
   uint64_t policy;
@@ -134,6 +135,7 @@ struct Producer {
 
 __device__ __forceinline__ int page_of_part(const ChunkArgs &a, Producer &p, int u) {
   if (u >= p.n_parts) return 0;
+  if (!p.table) return p.seq;
   const int id = __ldg(p.table + (unsigned)u / (unsigned)p.per_page);
   if (id < 0 || id >= a.pages.n_pages) {
     p.bad = true;
@@ -142,9 +144,10 @@ __device__ __forceinline__ int page_of_part(const ChunkArgs &a, Producer &p, int
   return id;
 }
 
-__device__ __noinline__ void producer_init(const ChunkArgs &a, Producer &p, const TileInfo &x, int hk,
+__device__ __forceinline__ void producer_init(const ChunkArgs &a, Producer &p, const TileInfo &x, int hk,
                                            int lane) {
-  p.table = a.page_table + (int64_t)x.s * a.max_pages;
+  p.table = a.page_table ? a.page_table + (int64_t)x.s * a.max_pages : nullptr;
+  p.seq = x.s;
   p.sub = min(a.pages.page_size, BN);
   p.per_page = a.pages.page_size / p.sub;
   p.n_parts = (x.kv + p.sub - 1) / p.sub;

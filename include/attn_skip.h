@@ -629,9 +629,15 @@ attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
  *  o_part, lse_part  workspace of total * Hq * n_splits * 128 and total * Hq *
  *              n_splits floats for n_splits > 1 (else NULL is fine); calls
  *              that overlap on the GPU need their own
- * A quantised cache is widened to bf16 on the chip (exact), products
- * accumulate in fp32, P is rounded to bf16 for the P.V product; statistics
- * are fp32.  Cache rows at or past kv_len may hold anything.  A value row that
+ *  kv_work     NULL, or attn_skip_chunk_paged_kv_bytes bytes of workspace: a
+ *              quantised cache that many tiles read is first written there as
+ *              bf16 rows (exact); with NULL, or 0 bytes, it is widened on the
+ *              chip by every tile.  Calls that overlap need their own
+ * Products accumulate in fp32; statistics and row sums are fp32.  P is rounded
+ * to bf16 for the P.V product (to fp16 where a quantised cache is widened on the
+ * chip, with steps of 2^-24 of the largest contribution at the small end).
+ * There a row whose scale is 2^15 or more below the largest of its 128-row block
+ * is rounded to 2^-25 of that scale.  Cache rows at or past kv_len may hold anything.  A value row that
  * is not finite, and in sight of some row of a tile, reaches every row of it.
  * EINVAL as for attn_skip_kv_append, for max_chunk or max_kv < 0 or beyond the
  * page table and for n_splits out of range; head size or G out of range are
@@ -647,10 +653,12 @@ attn_status attn_skip_chunk_paged(const attn_kv_pages *kv, const void *q, int64_
                                   const int32_t *page_table, int max_pages, float scale,
                                   const float *lambda, int causal, int n_splits, void *o,
                                   float *lse, uint32_t *skip_bits, float *o_part,
-                                  float *lse_part, void *stream);
+                                  float *lse_part, void *kv_work, void *stream);
 
-/* A split count for attn_skip_chunk_paged (host only; 1 for sizes that the call
- * itself refuses). */
+/* Host only: the bytes of kv_work (0: not needed), and a split count for
+ * attn_skip_chunk_paged (1 for sizes that the call itself refuses). */
+size_t attn_skip_chunk_paged_kv_bytes(attn_kv_format format, int n_seq, int Hq, int Hkv,
+                                      int max_chunk, int max_kv);
 int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, int total, int Hq, int Hkv,
                                  int max_chunk, int max_kv);
 

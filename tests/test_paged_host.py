@@ -52,7 +52,7 @@ def gather(lib, kv=None, **kw):
 def chunk(lib, kv=None, **kw):
     a = dict(kv=ctypes.byref(kv or pages()), q=A, qs=8 * 128, Hq=8, n_seq=2, total=5, cu=A,
              max_chunk=3, kv_len=A, max_kv=256, table=A, max_pages=4, scale=0.0, lam=A, causal=1,
-             n_splits=2, o=A, lse=A, bits=None, op=A, lp=A, stream=None)
+             n_splits=2, o=A, lse=A, bits=None, op=A, lp=A, work=None, stream=None)
     a.update(kw)
     return lib.attn_skip_chunk_paged(*a.values())
 
@@ -94,7 +94,7 @@ def test_gather_rejects(lib, kw):
     dict(max_chunk=-1), dict(max_chunk=0), dict(max_kv=-1), dict(max_kv=257), dict(kv_len=None),
     dict(lam=None), dict(lam=A + 2), dict(scale=float("nan")), dict(n_splits=0),
     dict(n_splits=1025), dict(o=None), dict(o=A + 8), dict(lse=None), dict(bits=A + 2),
-    dict(op=None), dict(lp=None), dict(op=A + 4),
+    dict(op=None), dict(lp=None), dict(op=A + 4), dict(work=A + 8),
 ])
 def test_chunk_rejects(lib, kw):
     assert chunk(lib, **kw) == bs.ATTN_EINVAL
@@ -116,6 +116,16 @@ def test_splits_proposal(lib):
         assert 1 <= n <= max(1, -(-max_kv // 128))
     assert f(0, 1, 1, 32, 8, 1, 32768) > 1  # few rows: the key axis is split
     assert f(0, 1, 16384, 32, 8, 16384, 16384) == 1  # many tiles: it is not
+
+
+def test_widening_workspace(lib):
+    f = lib.attn_skip_chunk_paged_kv_bytes
+    assert f(0, 1, 32, 8, 4096, 16384) == 0   # a bf16 cache
+    assert f(1, 1, 32, 8, 64, 16384) == 0     # two tiles
+    assert f(1, 1, 32, 8, 4096, 16300) == 16384 * 8 * 512
+    assert f(2, 3, 32, 8, 4096, 100) == 3 * 128 * 8 * 512
+    assert f(1, 1000, 32, 8, 4096, 1 << 20) == 0  # more than 4 GiB
+    assert f(1, 1, 33, 8, 4096, 16384) == 0 and f(1, 0, 32, 8, 4096, 16384) == 0
 
 
 def test_binding_refuses_tensors_off_the_gpu():
