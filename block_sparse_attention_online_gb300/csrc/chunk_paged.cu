@@ -1257,12 +1257,13 @@ int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv,
 // Bytes of the bf16 rows that a quantised cache is widened to first, 0 where it
 // is not.  Widening a 128-key block of a KV head once moves about 100 KB (15 ns
 // of the memory's time); converting it on the way costs each tile that reads it
-// 0.7 us of an SM, 5 ns of the chip, so from four tiles of a sequence on the
-// rows are written out (a chunk of 4096 on 16384 over E4M3 pages: 1318 us with
-// converters, 790 with widened rows).  Not where they would take over 4 GiB: the
+// 0.7 us of an SM, 5 ns of the chip, so from three tiles of a sequence on the
+// rows are written out (E4M3, 32 heads on 8: a chunk of 4096 on 16384, 1318 us
+// with converters and 698 with widened rows; 16 chunks of 96 on 8192, 419 and
+// 362; of 64, 290 and 304).  Not where they would take over 4 GiB: the
 // bound is the longest sequence's, for every sequence.
 size_t chunk_paged_kv_bytes(int n_seq, int max_chunk, int max_kv, int Hkv, int TT, int format) {
-  if (format == kKvBf16 || (max_chunk + TT - 1) / TT < 4) return 0;
+  if (format == kKvBf16 || (max_chunk + TT - 1) / TT < 3) return 0;
   const size_t rows = (size_t)n_seq * Hkv * (((size_t)max_kv + BN - 1) / BN * BN);
   return rows * D * 2 * 2 <= (size_t)4 << 30 ? rows * D * 2 * 2 : 0;
 }
