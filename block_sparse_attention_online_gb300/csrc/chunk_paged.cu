@@ -74,7 +74,7 @@ constexpr int NS = 3;     // TMEM S buffers
 constexpr int NDEC = 4;   // decision ring
 constexpr int NE = 8;     // scale exponent ring of the quantised formats
 constexpr int NQ = 4;     // warps per row role
-constexpr int kDeciderBarrier = 1, kSetupBarrier = 2, kMergeBarrier = 3;
+constexpr int kDeciderBarrier = 1, kMergeBarrier = 2;
 constexpr int MERGE_STRIDE = D + 4;  // floats a row: a row's 16-byte stores meet other banks than the next's
 constexpr int WARP_K = 8, WARP_MMA = 9, WARP_V = 10, WARP_PV = 11;
 constexpr int WARP_MMA2 = 12;             // bf16 cache
@@ -231,7 +231,7 @@ __device__ __forceinline__ void load_block_here(const ChunkArgs &a, Producer &p,
                                         bool value, int j, uint32_t dst, uint32_t full, int lane) {
   using C = Cfg<FMT>;
   constexpr bool QUANT = FMT != kKvBf16;
-  const int sub = p.sub;
+  const int sub = 1 << p.lsub;
   const Part x = part_of(a, p, j, lane);
   const int n = x.n, page = x.page, slot = x.slot;
   if (lane == 0) mbar_expect_tx(full, n * sub * (C::ROW + (QUANT ? (value ? 1 : 2) + C::BS / BN : 0)));
@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     if (tid == 0) atomicOr(a.err, kErrLayout);
     return;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge waits for this grid's end)
   const int sp = (int)(blockIdx.x % a.n_splits);
   const int hk = (int)(blockIdx.x / a.n_splits) % a.Hkv;
   const int ti = (int)(blockIdx.x / a.n_splits / a.Hkv);
@@ -498,82 +499,57 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     load_block<FMT>(a, pages, &tm_k, false, sh.tile.j0 + c, k_dst(c), bar(k_bar(c)), lane);
   };
 
-  // Set-up: the key producer initialises the barriers while the value
-  // producer's warp locates the tile; Q and the first keys are then in flight
-  // during the rest of the set-up.
+  // Set-up: the producers find the tile and its first pages; meanwhile other warps
+  // initialise the barriers and allocate TMEM.
   constexpr int K_AHEAD = QUANT ? NC : NKD;  // key blocks that the ring holds
-  int p_c = 0;
-  if (warp == WARP_K && lane == 0) {
-    prefetch_tmap(&tm_q);
-    if constexpr (!QUANT) prefetch_tmap(&tm_k);
-    mbar_init(bar(&sh.q_full), 1);
-    mbar_init(bar(&sh.q_ready), 8);
-    for (int i = 0; i < NR; ++i) {
-      if (!QUANT) mbar_init(bar(&sh.ready[i]), 2);  // the key tile, the S buffer
-      mbar_init(bar(&sh.qk_done[i]), 1);
-    }
-    for (int i = 0; i < NV; ++i) {
-      if (!QUANT) mbar_init(bar(&sh.v_full[i]), 1);
-      mbar_init(bar(&sh.v_empty[i]), 1);
-    }
-    for (int i = 0; i < NS; ++i) mbar_init(bar(&sh.pv_done[i]), 1);
-    mbar_init(bar(&sh.v_tail), 1);
-    for (int i = 0; i < NDEC; ++i) {
-      mbar_init(bar(&sh.dec_full[i]), 1);
-    }
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(bar(&sh.kc_full[i]), 1);
-      mbar_init(bar(&sh.vc_full[i]), 1);
-    }
-    sh.abort = 0;
-    fence_mbar_init();
-    fence_proxy_async_smem();  // the initialised barriers, seen by the TMA loads
-  }
-  if (warp == WARP_MMA) tmem_alloc(smem_u32(&sh.tmem_base), TMEM_COLS);
-  if (warp == WARP_V) {
-    if constexpr (!QUANT) {
-      if (lane == 0) prefetch_tmap(&tm_v);
-    }
-    locate(a, ti, sp, lane, blockIdx.x == 0, &sh.tile);
-  }
-  if (warp == WARP_V || warp == WARP_K) named_bar_sync(kSetupBarrier, 64);
-  if (warp == WARP_K && sh.tile.s >= 0 && sh.tile.nb > 0) {
-    const TileInfo x = sh.tile;
-    if (lane == 0) {
+  if (warp == WARP_K || warp == WARP_V) {
+    const TileInfo t = producer_tile(a, pages, ti, sp, hk, lane);
+    if (warp == WARP_K && lane == 0) {
+      sh.tile = t;
       // Readers of a decision: the P.V issuer and the exponential warps that have
       // rows; with a threshold also the value producer and converters.
-      const int nq = REP ? NQ : (x.ntok * a.G + 31) / 32, nc = 8 - nq;  // see below
-      const int readers = 1 + nq + (x.ln_lam == -INFINITY ? 0 : QUANT ? 1 + nc : 1);
+      const int nq = REP ? NQ : (t.ntok * a.G + 31) / 32, nc = 8 - nq;  // see below
+      const int readers = 1 + nq + (t.ln_lam == -INFINITY ? 0 : QUANT ? 1 + nc : 1);
       for (int i = 0; i < NDEC; ++i) mbar_init(bar(&sh.dec_read[i]), readers);
+      for (int i = 0; i < NR; ++i)
+        mbar_init(bar(&sh.ready[i]), QUANT ? nc + 1 : 2);  // the key tile, the S buffer
+      for (int i = 0; i < NS; ++i) mbar_arrive(bar(&sh.ready[i]));  // S buffers free at first
       if constexpr (QUANT) {
-        for (int i = 0; i < NR; ++i) mbar_init(bar(&sh.ready[i]), nc + 1);
         for (int i = 0; i < NV; ++i) mbar_init(bar(&sh.v_full[i]), nc);
         for (int i = 0; i < 3; ++i) {
           mbar_init(bar(&sh.kc_empty[i]), nc);
           mbar_init(bar(&sh.vc_empty[i]), nc);
         }
       }
-      for (int i = 0; i < NS; ++i) mbar_arrive(bar(&sh.ready[i]));  // S buffers free at first
       for (int i = 0; i < NS; ++i) mbar_init(bar(&sh.p_full[i]), nq);
       mbar_init(bar(&sh.l_full), nq);
       fence_mbar_init();
     }
-    fence_proxy_async_smem();  // lane 0's barriers, for every lane's copies
-    producer_init(a, pages, x, hk, lane);
-    if (lane == 0) {
-      const uint64_t once = policy_evict_first();
-      constexpr int COPIES = REP ? 4 : 1;
-      mbar_expect_tx(bar(&sh.q_full), COPIES * 2 * 128 * a.G * q_box_tokens);
-      for (int i = 0; i < COPIES; ++i) {
-        const uint32_t dst = base + L::Q + i * 32 * 128;
-        tma_load_3d(dst, &tm_q, bar(&sh.q_full), 0, hk * a.G, x.tok0, once);
-        tma_load_3d(dst + HALF_BYTES, &tm_q, bar(&sh.q_full), 64, hk * a.G, x.tok0, once);
-      }
-    }
-    __syncwarp();
-#pragma unroll 1
-    for (; p_c < x.nb && p_c < K_AHEAD; ++p_c) load_k(p_c);
   }
+  if (warp == WARP_PV && lane == 0) {
+    prefetch_tmap(&tm_q);
+    if constexpr (!QUANT) {
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
+    mbar_init(bar(&sh.q_full), 1);
+    mbar_init(bar(&sh.q_ready), 8);
+    mbar_init(bar(&sh.v_tail), 1);
+    for (int i = 0; i < NR; ++i) mbar_init(bar(&sh.qk_done[i]), 1);
+    for (int i = 0; i < NV; ++i) {
+      if (!QUANT) mbar_init(bar(&sh.v_full[i]), 1);
+      mbar_init(bar(&sh.v_empty[i]), 1);
+    }
+    for (int i = 0; i < NS; ++i) mbar_init(bar(&sh.pv_done[i]), 1);
+    for (int i = 0; i < NDEC; ++i) mbar_init(bar(&sh.dec_full[i]), 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(bar(&sh.kc_full[i]), 1);
+      mbar_init(bar(&sh.vc_full[i]), 1);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == WARP_MMA) tmem_alloc(smem_u32(&sh.tmem_base), TMEM_COLS);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -591,6 +567,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   // End of the query rows in [r, r + 16).
   auto q_end = [&](int r) { return min(r + 16, REP ? (r & ~31) + rows : rows); };
 
+  if (blockIdx.x == 0 && (x.s < 0 || nb == 0) && warp == WARP_PV) check_batch(a, lane);
   if (x.s < 0) {
     // no tile for this CTA
   } else if (nb == 0) {
@@ -606,12 +583,25 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] = -INFINITY;
     }
   } else if (warp == WARP_K) {
-    // -------------------------------------------------------- key producer --
-    int issued = p_c;
+    // ---------------------------------------------- query and key producer --
+    fence_proxy_async_smem();  // the initialised barriers, for every lane's copies
+    if (lane == 0) {
+      const uint64_t once = policy_evict_first();
+      constexpr int COPIES = REP ? 4 : 1;
+      mbar_expect_tx(bar(&sh.q_full), COPIES * 2 * 128 * a.G * q_box_tokens);
+      for (int i = 0; i < COPIES; ++i) {
+        const uint32_t dst = base + L::Q + i * 32 * 128;
+        tma_load_3d(dst, &tm_q, bar(&sh.q_full), 0, hk * a.G, x.tok0, once);
+        tma_load_3d(dst + HALF_BYTES, &tm_q, bar(&sh.q_full), 64, hk * a.G, x.tok0, once);
+      }
+    }
+    __syncwarp();
+    int issued = 0;
 #pragma unroll 1
-    for (int c = p_c; c < nb && !*abort; ++c) {
+    for (int c = 0; c < nb && !*abort; ++c) {
       // The ring's slot last held block c - K_AHEAD.
-      if (!(QUANT ? wait_warp(&sh.kc_empty[c % NC], c / NC - 1)
+      if (c >= K_AHEAD &&
+          !(QUANT ? wait_warp(&sh.kc_empty[c % NC], c / NC - 1)
                   : wait_warp(&sh.qk_done[c % NR], c / NR - 1)))
         break;
       load_k(c);
@@ -629,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     }
   } else if (warp == WARP_V) {
     // ------------------------------------------------------ value producer --
-    producer_init(a, pages, x, hk, lane);
+    fence_proxy_async_smem();
     int vi = 0;
     bool tail = false;
 #pragma unroll 1
@@ -697,6 +687,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
     }
   } else if (warp == WARP_PV) {
     // ---------------------------------------------------------- P.V issuer --
+    if (blockIdx.x == 0) check_batch(a, lane);
     if (lane == 0) {
       int kc = 0;
 #pragma unroll 1
@@ -1057,6 +1048,27 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
       }
       const float inv = lrow == 0.f ? 0.f : w / lrow;
       const bool none = w == 0.f;  // (the accumulator may hold anything)
+      // The rows leave through 4 KB of the query tile a warp (free by now): a lane's
+      // row in 16-byte pieces, then 128-byte runs of four rows an instruction.
+      const uint32_t stage = base + L::Q + warp * 4096;
+      auto put_row = [&](int piece, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+        st_shared_v4(stage + lane * 128 + ((piece ^ (lane & 7)) * 16), v0, v1, v2, v3);
+      };
+      auto store_rows = [&](uint8_t *out, int64_t row_bytes) {
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int l2 = it * 4 + (lane >> 3), piece = lane & 7;
+          const int64_t at = __shfl_sync(0xffffffffu, orow, l2);
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(stage + l2 * 128 + ((piece ^ (l2 & 7)) * 16))
+                       : "memory");
+          if (quarter * 32 + l2 < rows) *reinterpret_cast<uint4 *>(out + at * row_bytes + piece * 16) = v;
+        }
+        __syncwarp();
+      };
 #pragma unroll 1
       for (int cc = 0; cc < 2; ++cc) {
         uint32_t o[32];
@@ -1066,26 +1078,25 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-        if (!valid) continue;
         if constexpr (REP) {
+          if (!valid) continue;
           const uint32_t at = base + L::K + (uint32_t)((r * MERGE_STRIDE + col) * 4);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             st_shared_v4(at + q * 16, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         } else if (a.n_splits == 1) {
-          uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + orow * D + col);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            dst[q] = make_uint4(
-                pack_bf16x2(__uint_as_float(o[8 * q]), __uint_as_float(o[8 * q + 1])),
-                pack_bf16x2(__uint_as_float(o[8 * q + 2]), __uint_as_float(o[8 * q + 3])),
-                pack_bf16x2(__uint_as_float(o[8 * q + 4]), __uint_as_float(o[8 * q + 5])),
-                pack_bf16x2(__uint_as_float(o[8 * q + 6]), __uint_as_float(o[8 * q + 7])));
+            put_row(cc * 4 + q, pack_bf16x2(__uint_as_float(o[8 * q]), __uint_as_float(o[8 * q + 1])),
+                    pack_bf16x2(__uint_as_float(o[8 * q + 2]), __uint_as_float(o[8 * q + 3])),
+                    pack_bf16x2(__uint_as_float(o[8 * q + 4]), __uint_as_float(o[8 * q + 5])),
+                    pack_bf16x2(__uint_as_float(o[8 * q + 6]), __uint_as_float(o[8 * q + 7])));
+          if (cc == 1) store_rows((uint8_t *)a.o + col0 * 2, D * 2);
         } else {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.o_part + (orow * a.n_splits + sp) * D + col);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            put_row(q, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          store_rows((uint8_t *)(a.o_part + (int64_t)sp * D + col), (int64_t)a.n_splits * D * 4);
         }
       }
       if (valid && !decider && (!REP || quarter == 0))
@@ -1134,6 +1145,7 @@ constexpr int MERGE_WARPS = 4;
 __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const ChunkArgs a) {
   const int64_t row = (int64_t)blockIdx.x * MERGE_WARPS + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
   if (row >= (int64_t)a.total * a.Hq) return;
   const int tok = (int)(row / a.Hq);
   // A token outside every (valid) sequence has no partial.
@@ -1314,8 +1326,18 @@ cudaError_t launch_chunk_paged(const ChunkArgs &args, cudaStream_t s) {
   }
   if (e != cudaSuccess || a.n_splits == 1) return e;
   const int64_t rows = (int64_t)a.total * a.Hq;
-  merge_kernel<<<(unsigned)((rows + MERGE_WARPS - 1) / MERGE_WARPS), MERGE_WARPS * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  // Launched as a programmatic dependent of the attention kernel, whose CTAs
+  // release it as they start: its own launch is over by the time they end.
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((rows + MERGE_WARPS - 1) / MERGE_WARPS));
+  cfg.blockDim = dim3(MERGE_WARPS * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel, a);
 }
 
 }  // namespace attn_skip

@@ -164,7 +164,7 @@ __device__ __forceinline__ void load_block(const ChunkArgs &a, Producer &p, cons
                                            bool value, int j, uint32_t codes, uint32_t extra,
                                            uint32_t full, int lane) {
   using C = Cfg<FMT>;
-  const int sub = p.sub;
+  const int sub = 1 << p.lsub;
   const Part x = part_of(a, p, j, lane);
   const int rows = x.n * sub;  // rows of the block in the cache's pages
   const KvPages &g = a.pages;
@@ -174,7 +174,7 @@ __device__ __forceinline__ void load_block(const ChunkArgs &a, Producer &p, cons
     tma_load_4d(codes + lane * sub * C::ROW, map, full, 0, x.slot, p.hk, x.page, p.policy);
   // Scale index of row r of the block: that of its part's first row, and on.
   const int64_t first = ((int64_t)x.page * g.Hkv + p.hk) * g.page_size + x.slot;
-  auto row_at = [&](int r) { return __shfl_sync(0xffffffffu, first, r / sub) + r % sub; };
+  auto row_at = [&](int r) { return __shfl_sync(0xffffffffu, first, r >> p.lsub) + (r & (sub - 1)); };
   if constexpr (FMT == kKvNvfp4) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(NT, 2)
     if (tid == 0) atomicOr(a.err, kErrLayout);
     return;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge waits for this grid's end)
   const int sp = (int)(blockIdx.x % a.n_splits);
   const int hk = (int)(blockIdx.x / a.n_splits) % a.Hkv;
   const int ti = (int)(blockIdx.x / a.n_splits / a.Hkv);
@@ -234,13 +235,18 @@ __global__ void __launch_bounds__(NT, 2)
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == WARP_K) locate(a, ti, sp, lane, blockIdx.x == 0, &sh.tile);
+  Producer pages;  // of the two producer warps
+  if (warp >= WARP_K) {
+    const TileInfo t = producer_tile(a, pages, ti, sp, hk, lane);
+    if (warp == WARP_K && lane == 0) sh.tile = t;
+  }
   __syncthreads();
   const TileInfo x = sh.tile;
   const int nb = x.nb;
   const int rows = x.s >= 0 ? x.ntok * a.G : 0;
   const bool dense = x.ln_lam == -INFINITY;
 
+  if (blockIdx.x == 0 && warp == WARP_V) check_batch(a, lane);
   if (x.s < 0) return;
   if (nb == 0) {  // no visible key: O = 0, LSE = -inf (one split), or a partial of no weight
     for (int i = tid; i < rows * (D / 8); i += NT) {
@@ -259,8 +265,6 @@ __global__ void __launch_bounds__(NT, 2)
     // ----------------------------------------------------------- producers --
     const bool value = warp == WARP_V;
     fence_proxy_async_smem();  // the barriers, for every lane's copies
-    Producer pages;
-    producer_init(a, pages, x, hk, lane);
     uint64_t *full = value ? sh.v_full : sh.k_full, *empty = value ? sh.v_empty : sh.k_empty;
     int n = 0;  // blocks fetched
 #pragma unroll 1

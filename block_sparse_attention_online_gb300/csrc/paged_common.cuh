@@ -63,60 +63,91 @@ struct TileInfo {
 };
 
 // ------------------------------------------------------------- tile of a CTA --
-// Tiles run sequence by sequence, each sequence's last (longest) tile first;
-// one warp locates tile i by running sums over 32 sequences at a time.
-__device__ __noinline__ void locate(const ChunkArgs &a, int i, int split, int lane, bool report,
-                                    TileInfo *out) {
-  bool bad = false, found = false;
-  int before = 0;
-#pragma unroll 1
-  for (int b = 0; b < a.n_seq && (report || !found); b += 32) {
-    const int s = b + lane;
-    int c0 = 0, len = 0, kv = 0;
-    float lam = 0.f;
-    if (s < a.n_seq) {
-      c0 = __ldg(a.cu_seqlens + s);
-      const int c1 = __ldg(a.cu_seqlens + s + 1);
-      kv = __ldg(a.kv_len + s);
-      lam = __ldg(a.lambda + s);
-      len = c1 - c0;
-      // Bad bounds: the sequence has no tile.  A bad cached length: an empty
-      // cache.  A bad threshold: 0.
-      if (c0 < 0 || c1 < c0 || len > a.max_chunk || c1 > a.total) { len = 0; bad = true; }
-      if (kv < 0 || kv > a.max_kv) { kv = 0; bad = true; }
-      if (!(lam >= 0.f && lam < 1.f)) { lam = 0.f; bad = true; }
-    }
-    const int nt = (len + a.TT - 1) / a.TT;
-    int upto = nt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    upto += before;
-    if (!found && i >= upto - nt && i < upto) {
-      TileInfo x;
-      x.s = s;
-      x.t = upto - 1 - i;
-      x.tok0 = c0 + x.t * a.TT;
-      x.ntok = min(a.TT, len - x.t * a.TT);
-      x.pos0 = kv - len + x.t * a.TT;
-      x.kv = kv;
-      // Keys that some row of the tile sees, then this split's blocks of them.
-      const int seen = a.causal ? max(0, x.pos0 + x.ntok) : kv;
-      const int blocks = (seen + BN - 1) / BN;
-      x.j0 = split * a.bps;
-      x.nb = max(0, min(blocks, x.j0 + a.bps) - x.j0);
-      x.ln_lam = lam > 0.f ? logf(lam) : -INFINITY;
-      *out = x;
-      found = true;
-    }
-    found = __any_sync(0xffffffffu, found);
-    before = __shfl_sync(0xffffffffu, upto, 31);
+// Tiles run sequence by sequence, each sequence's last (longest) tile first.  Set-up
+// code runs once a CTA from a cold instruction cache, so the common cases are
+// kept short: where every chunk is at most one tile, CTA tile i is sequence i's;
+// where there is one sequence, it is its; otherwise running sums over 32
+// sequences at a time find it.
+__device__ __forceinline__ int known_sequence(const ChunkArgs &a, int i) {
+  return a.max_chunk <= a.TT ? i : a.n_seq == 1 ? 0 : -1;
+}
+
+// Length of a chunk, 0 where its bounds are bad (the sequence then has no tile).
+__device__ __forceinline__ int chunk_of(const ChunkArgs &a, int c0, int c1, bool &bad) {
+  if (c0 < 0 || c1 < c0 || c1 - c0 > a.max_chunk || c1 > a.total) {
+    bad = true;
+    return 0;
   }
-  if (!found && lane == 0) out->s = -1;
-  if (report && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err, kErrBadArg);
-  __syncwarp();
+  return c1 - c0;
+}
+
+// The tile with number i, for the whole warp; `known`: its sequence, or -1.  A bad
+// cached length is an empty cache, a bad threshold 0.
+__device__ __forceinline__ TileInfo locate(const ChunkArgs &a, int i, int split, int lane,
+                                           int known) {
+  bool bad = false;
+  int s = known, first = 0;  // the sequence and the number of its first tile
+  if (known < 0) {
+#pragma unroll 1
+    for (int b = 0; b < a.n_seq && s < 0; b += 32) {
+      const int q = b + lane;
+      int nt = 0;
+      if (q < a.n_seq)
+        nt = (chunk_of(a, __ldg(a.cu_seqlens + q), __ldg(a.cu_seqlens + q + 1), bad) + a.TT - 1) / a.TT;
+      int upto = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      upto += first;
+      const unsigned mine = __ballot_sync(0xffffffffu, i >= upto - nt && i < upto);
+      if (mine) {
+        const int l = __ffs(mine) - 1;
+        s = b + l;
+        first = __shfl_sync(0xffffffffu, upto - nt, l);
+      } else {
+        first = __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
+  }
+  TileInfo x{};
+  x.s = -1;
+  if (s < 0) return x;
+  const int c0 = __ldg(a.cu_seqlens + s), c1 = __ldg(a.cu_seqlens + s + 1);
+  int kv = __ldg(a.kv_len + s);
+  const float lam = __ldg(a.lambda + s);
+  const int len = chunk_of(a, c0, c1, bad);
+  const int nt = (len + a.TT - 1) / a.TT;
+  const int t = known < 0 || a.n_seq == 1 ? nt - 1 - (i - first) : 0;
+  if (t < 0 || t >= nt) return x;
+  if (kv < 0 || kv > a.max_kv) kv = 0;
+  x.s = s;
+  x.t = t;
+  x.tok0 = c0 + t * a.TT;
+  x.ntok = min(a.TT, len - t * a.TT);
+  x.pos0 = kv - len + t * a.TT;
+  x.kv = kv;
+  // Keys that some row of the tile sees, then this split's blocks of them.
+  const int seen = a.causal ? max(0, x.pos0 + x.ntok) : kv;
+  const int blocks = (seen + BN - 1) / BN;
+  x.j0 = split * a.bps;
+  x.nb = max(0, min(blocks, x.j0 + a.bps) - x.j0);
+  x.ln_lam = lam > 0.f && lam < 1.f ? logf(lam) : -INFINITY;
+  return x;
+}
+
+// Reports the batch's bad bounds, lengths and thresholds; one warp of one CTA.
+__device__ __noinline__ void check_batch(const ChunkArgs &a, int lane) {
+  bool bad = false;
+#pragma unroll 1
+  for (int s = lane; s < a.n_seq; s += 32) {
+    chunk_of(a, __ldg(a.cu_seqlens + s), __ldg(a.cu_seqlens + s + 1), bad);
+    const int kv = __ldg(a.kv_len + s);
+    const float lam = __ldg(a.lambda + s);
+    bad |= kv < 0 || kv > a.max_kv || !(lam >= 0.f && lam < 1.f);
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err, kErrBadArg);
 }
 
 // ------------------------------------------------------------------- pages --
@@ -127,37 +158,44 @@ __device__ __noinline__ void locate(const ChunkArgs &a, int i, int split, int la
 struct Producer {
   const int32_t *table;  // the sequence's row; null: its rows are page `seq`
   int seq;
-  int sub, per_page;     // rows of a part, parts of a page
+  int lsub, per_page;    // log2 of a part's rows, parts of a page
   int n_parts, base, cur, nxt, hk;
   uint64_t policy;
   bool bad;
 };
 
-__device__ __forceinline__ int page_of_part(const ChunkArgs &a, Producer &p, int u) {
-  if (u >= p.n_parts) return 0;
+__device__ __forceinline__ int page_of_part(const ChunkArgs &a, const Producer &p, int u) {
   if (!p.table) return p.seq;
-  const int id = __ldg(p.table + (unsigned)u / (unsigned)p.per_page);
-  if (id < 0 || id >= a.pages.n_pages) {
-    p.bad = true;
-    return 0;
-  }
-  return id;
+  const int i = p.per_page == 1 ? u : (int)((unsigned)u / (unsigned)p.per_page);
+  return i < a.max_pages ? __ldg(p.table + i) : 0;
 }
 
-__device__ __forceinline__ void producer_init(const ChunkArgs &a, Producer &p, const TileInfo &x, int hk,
-                                           int lane) {
-  p.table = a.page_table ? a.page_table + (int64_t)x.s * a.max_pages : nullptr;
-  p.seq = x.s;
-  p.sub = min(a.pages.page_size, BN);
-  p.per_page = a.pages.page_size / p.sub;
-  p.n_parts = (x.kv + p.sub - 1) / p.sub;
+// The first pages' ids load before the sequence's length is known (n_parts is set
+// then): entries of its row of the table, whether or not they stand for pages.
+__device__ __forceinline__ void producer_start(const ChunkArgs &a, Producer &p, int s, int split,
+                                               int hk, int lane) {
+  p.table = a.page_table ? a.page_table + (int64_t)s * a.max_pages : nullptr;
+  p.seq = s;
+  p.lsub = a.pages.page_size < BN ? 31 - __clz(a.pages.page_size) : 7;
+  p.per_page = a.pages.page_size < BN ? 1 : a.pages.page_size / BN;
   p.bad = false;
   p.hk = hk;
   // Keys and values are read again by the other tiles of the sequence, or once.
   p.policy = a.max_chunk > a.TT ? policy_evict_last() : policy_evict_first();
-  p.base = (x.j0 * (BN / p.sub)) & ~31;
+  p.base = ((split * a.bps) << (7 - p.lsub)) & ~31;
   p.cur = page_of_part(a, p, p.base + lane);
   p.nxt = page_of_part(a, p, p.base + 32 + lane);
+}
+
+// A producer warp's set-up: its tile, and the pages' ids in flight as early as may be.
+__device__ __forceinline__ TileInfo producer_tile(const ChunkArgs &a, Producer &p, int i, int split,
+                                                  int hk, int lane) {
+  const int known = known_sequence(a, i);
+  if (known >= 0) producer_start(a, p, known, split, hk, lane);
+  const TileInfo x = locate(a, i, split, lane, known);
+  if (known < 0 && x.s >= 0) producer_start(a, p, x.s, split, hk, lane);
+  p.n_parts = (x.kv + (1 << p.lsub) - 1) >> p.lsub;
+  return x;
 }
 
 // The parts of block j for the lanes of the warp: lane l < n has part l's page and
@@ -166,16 +204,20 @@ struct Part {
   int n, page, slot;
 };
 __device__ __forceinline__ Part part_of(const ChunkArgs &a, Producer &p, int j, int lane) {
-  const int ppb = BN / p.sub, u0 = j * ppb, b = u0 & ~31;
+  const int u0 = j << (7 - p.lsub), b = u0 & ~31;
   if (b != p.base) {
     p.cur = b == p.base + 32 ? p.nxt : page_of_part(a, p, b + lane);
     p.base = b;
     p.nxt = page_of_part(a, p, b + 32 + lane);
   }
   Part x;
-  x.n = min(ppb, p.n_parts - u0);
+  x.n = min(1 << (7 - p.lsub), p.n_parts - u0);
   x.page = __shfl_sync(0xffffffffu, p.cur, (u0 - b + lane) & 31);
-  x.slot = (int)((unsigned)(u0 + lane) % (unsigned)p.per_page) * p.sub;
+  if (lane < x.n && (x.page < 0 || x.page >= a.pages.n_pages)) {
+    p.bad = true;
+    x.page = 0;
+  }
+  x.slot = p.per_page == 1 ? 0 : (int)((unsigned)(u0 + lane) % (unsigned)p.per_page) << p.lsub;
   return x;
 }
 
