@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -649,6 +650,7 @@ class PagedKV:
         p = [x.data_ptr() if x is not None else None for x in (k, v, k_scale, v_scale, k_bs, v_bs)]
         # The page stride matters, and is meaningful, only between pages.
         stride = k.stride(0) * k.element_size() if n_pages > 1 else 0
+        self._fmt = code
         self._c = _KvPages(code, n_pages, page_size, Hkv, d, stride, *p)
         self._ref = ctypes.byref(self._c)
 
@@ -781,6 +783,14 @@ def attn_skip_chunk_paged_kv_bytes(kv, n_seq, Hq, max_chunk, max_kv):
                                                  max_chunk, max_kv)
 
 
+@functools.lru_cache(maxsize=1024)
+def _chunk_plan(fmt, n_seq, total, Hq, Hkv, max_chunk, max_kv):
+    """(proposed splits, widening bytes) of these sizes."""
+    lib = load()
+    return (lib.attn_skip_chunk_paged_splits(fmt, n_seq, total, Hq, Hkv, max_chunk, max_kv),
+            lib.attn_skip_chunk_paged_kv_bytes(fmt, n_seq, Hq, Hkv, max_chunk, max_kv))
+
+
 def chunk_bitmap_shape(n_seq, Hq, Hkv, max_chunk, max_kv, n_splits):
     tt = 128 // (Hq // Hkv)
     bps = -(-(-(-max_kv // 128)) // n_splits)
@@ -813,10 +823,8 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
     qs = _token_stride("q", q, Hq, kv)
     if Hq % kv.Hkv or Hq // kv.Hkv > 128:
         raise ValueError(f"{Hq} query heads do not fit {kv.Hkv} KV heads")
-    lib = _lib or load()
-    if n_splits == 0:
-        n_splits = lib.attn_skip_chunk_paged_splits(kv._c.format, n, total, Hq, kv.Hkv, max_chunk,
-                                                    max_kv)
+    splits, size = _chunk_plan(kv._fmt, n, total, Hq, kv.Hkv, max_chunk, max_kv)
+    n_splits = n_splits or splits
     bits = None
     if out is None:
         o = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=kv.device)
@@ -842,14 +850,13 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
             _like("workspace", workspace[0], (total, Hq, n_splits, d), torch.float32, kv)
             _like("workspace", workspace[1], (total, Hq, n_splits), torch.float32, kv)
             op, lp = workspace[0].data_ptr(), workspace[1].data_ptr()
-    size = lib.attn_skip_chunk_paged_kv_bytes(kv._c.format, n, Hq, kv.Hkv, max_chunk, max_kv)
     if rows is None:
         if size:
             rows = torch.empty(size, dtype=torch.uint8, device=kv.device)
     elif rows.dtype is not torch.uint8 or rows.numel() < size or not rows.is_contiguous() \
             or rows.get_device() != kv.index:
         raise ValueError(f"rows must be a contiguous uint8 tensor of {size} bytes on {kv.device}")
-    _check("attn_skip_chunk_paged", lib.attn_skip_chunk_paged(
+    _check("attn_skip_chunk_paged", (_lib or load()).attn_skip_chunk_paged(
         kv._ref, q.data_ptr(), qs, Hq, n, total, cu_seqlens.data_ptr(), max_chunk,
         kv_len.data_ptr(), max_kv, page_table.data_ptr(), page_table.shape[1], scale,
         lambdas.data_ptr(), 1 if causal else 0, n_splits, o.data_ptr(), lse.data_ptr(),

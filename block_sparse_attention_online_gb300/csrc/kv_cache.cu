@@ -21,6 +21,7 @@
 // whose place in the cache it works out once a token and whose pool rows are
 // contiguous within a page; all its loads are issued first.
 #include <cuda_bf16.h>
+#include <limits.h>
 #include <math.h>
 
 #include "internal.h"
@@ -53,14 +54,15 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int n, int t, int hl,
 struct Place {
   int64_t row;  // (page * Hkv + head) * page_size + slot: the rows' scale index
   int64_t byte; // the rows' first byte in k and v
-  bool ok;      // false: no such rows
+  int left;     // rows of the page from this one on; 0: no such rows
+  __device__ __forceinline__ bool ok() const { return left > 0; }
 };
 
 // Rows of position pos of sequence s, head h.
 template <int ROW_BYTES>
 __device__ __forceinline__ Place place_of(const KvPages &p, const int32_t *table, int max_pages,
                                           int s, int64_t pos, int h) {
-  Place x{0, 0, false};
+  Place x{0, 0, 0};
   if (pos < 0 || pos >= (int64_t)max_pages * p.page_size) return x;
   const unsigned u = (unsigned)pos;
   const unsigned pi = p.page_shift >= 0 ? u >> p.page_shift : u / (unsigned)p.page_size;
@@ -70,8 +72,16 @@ __device__ __forceinline__ Place place_of(const KvPages &p, const int32_t *table
   const int in_page = h * p.page_size + slot;
   x.row = (int64_t)page * (p.Hkv * p.page_size) + in_page;
   x.byte = (int64_t)page * p.page_stride + (int64_t)in_page * ROW_BYTES;
-  x.ok = true;
+  x.left = p.page_size - slot;
   return x;
+}
+
+// The next position's: the next row of the page, or a page to look up.
+template <int ROW_BYTES>
+__device__ __forceinline__ Place next_place(const Place &at, const KvPages &p, const int32_t *table,
+                                            int max_pages, int s, int64_t pos, int h) {
+  if (at.left > 1) return Place{at.row + 1, at.byte + ROW_BYTES, at.left - 1};
+  return place_of<ROW_BYTES>(p, table, max_pages, s, pos, h);
 }
 
 template <int FMT> struct RowBytes {
@@ -152,13 +162,49 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
-// The row whose eight elements a lane holds is x, to its place; half warp.
+// Largest |element| of a token's key row and value row (fp32 bits), over the
+// row's sixteen lanes, and over this lane and its neighbour (a block of sixteen).
+struct Tops {
+  uint32_t row[2], pair[2];
+};
+template <bool F32>
+__device__ __forceinline__ Tops tops_of(const New<F32> &k, const New<F32> &v, unsigned hmask) {
+  Tops t;
+  if constexpr (F32) {
+    t.row[0] = k.top();
+    t.row[1] = v.top();
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        t.row[w] = max(t.row[w], __shfl_xor_sync(hmask, t.row[w], o));
+        if (o == 1) t.pair[w] = t.row[w];
+      }
+    }
+  } else {  // both rows' as the halves of one word
+    uint32_t m = (k.top() >> 16) | v.top();
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      m = __vmaxu2(m, __shfl_xor_sync(hmask, m, o));
+      if (o == 1) {
+        t.pair[0] = m << 16;
+        t.pair[1] = m & 0xffff0000u;
+      }
+    }
+    t.row[0] = m << 16;
+    t.row[1] = m & 0xffff0000u;
+  }
+  return t;
+}
+
+// The row whose eight elements a lane holds is x, to its place; half warp.  m,
+// pair: its tops.
 template <int FMT, bool F32>
 __device__ __forceinline__ void store_row(const KvPages &p, bool value, const Place &at,
-                                          const New<F32> &x, int hl, unsigned hmask) {
+                                          const New<F32> &x, uint32_t m, uint32_t pair, int hl) {
   uint8_t *codes = (uint8_t *)(value ? p.v : p.k) + at.byte;
   if constexpr (FMT == kKvBf16) {
-    if (!at.ok) return;
+    if (!at.ok()) return;
     uint4 v;
     if constexpr (F32)
       v = make_uint4(bf16x2(x.at(0), x.at(1)), bf16x2(x.at(2), x.at(3)), bf16x2(x.at(4), x.at(5)),
@@ -167,23 +213,18 @@ __device__ __forceinline__ void store_row(const KvPages &p, bool value, const Pl
       v = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
     *reinterpret_cast<uint4 *>(codes + hl * 16) = v;
   } else {
-    const uint32_t mine = x.top();
-    const uint32_t pair = max(mine, __shfl_xor_sync(hmask, mine, 1));
-    uint32_t m = pair;
-#pragma unroll
-    for (int o = 2; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(hmask, m, o));
     const bool bad = m >= 0x7f800000u;  // an infinity or a NaN
     // top = 448 = 1.75 * 2^8, or 2688 = 1.3125 * 2^11.
     const int e = bad || m == 0u     ? 0
                   : FMT == kKvE4m3 ? scale_exponent<8, 0x600000>(m)
                                    : scale_exponent<11, 0x280000>(m);
     const float inv = pow2i(-e);
-    if (at.ok && hl == 0) (value ? p.v_scale : p.k_scale)[at.row] = bad ? 255 : (uint8_t)(e + 127);
+    if (at.ok() && hl == 0) (value ? p.v_scale : p.k_scale)[at.row] = bad ? 255 : (uint8_t)(e + 127);
     if constexpr (FMT == kKvE4m3) {
       uint32_t c[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) c[i] = e4m3x2(x.at(2 * i) * inv, x.at(2 * i + 1) * inv);
-      if (at.ok)
+      if (at.ok())
         *reinterpret_cast<uint2 *>(codes + hl * 8) =
             bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
     } else {
@@ -201,7 +242,7 @@ __device__ __forceinline__ void store_row(const KvPages &p, bool value, const Pl
         // or is at least one fp32 step away from it.
         w |= e2m1x2(__fdiv_rn(x.at(2 * i) * inv, by), __fdiv_rn(x.at(2 * i + 1) * inv, by)) << (8 * i);
       }
-      if (at.ok) {
+      if (at.ok()) {
         *reinterpret_cast<uint32_t *>(codes + hl * 4) = bad ? 0u : w;
         if ((hl & 1) == 0) (value ? p.v_bs : p.k_bs)[at.row * (D / 16) + (hl >> 1)] = bad ? 0 : b;
       }
@@ -226,29 +267,39 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ K
       x[r][0].load(a.k_new, (t0 + r) * a.k_tok_stride + h * D + hl * 8);
       x[r][1].load(a.v_new, (t0 + r) * a.v_tok_stride + h * D + hl * 8);
     }
-  int s = find_seq(a.cu_seqlens, a.n_seq, (int)t0, hl, hmask);
-  bool bad = false;
+  int s = find_seq(a.cu_seqlens, a.n_seq, (int)t0, hl, hmask) - 1;
+  bool bad = false, fine = false;
+  int end = INT_MIN;  // the current sequence's last row + 1
+  int64_t shift = 0;  // position minus row
+  Place at{0, 0, 0};
 #pragma unroll
   for (int r = 0; r < kTok; ++r) {
     const int t = (int)t0 + r;
     if (t >= a.total) break;
-    while (s < a.n_seq && __ldg(a.cu_seqlens + s + 1) <= t) ++s;
-    if (s >= a.n_seq) break;  // behind the last sequence
-    const int c0 = __ldg(a.cu_seqlens + s), c1 = __ldg(a.cu_seqlens + s + 1);
-    const int len = __ldg(a.kv_len + s);
-    Place at{0, 0, false};
-    // The sequence's bounds and its length are checked as a whole, so that no
-    // row of a sequence with a bad length is written.
-    if (c0 < 0 || c0 > t || c1 > a.total || len < 0 ||
-        len > (int64_t)a.max_pages * a.pages.page_size) {
-      bad = true;
-    } else if ((int64_t)len - c1 + t >= 0) {  // else the chunk is longer than the cache
-      at = place_of<RowBytes<FMT>::value>(a.pages, a.page_table, a.max_pages, s,
-                                          (int64_t)len - c1 + t, h);
-      bad |= !at.ok;
+    if (t >= end) {  // the next sequence that has rows
+      do {
+        ++s;
+      } while (s < a.n_seq && __ldg(a.cu_seqlens + s + 1) <= t);
+      if (s >= a.n_seq) break;  // behind the last sequence
+      const int c0 = __ldg(a.cu_seqlens + s), len = __ldg(a.kv_len + s);
+      end = __ldg(a.cu_seqlens + s + 1);
+      shift = (int64_t)len - end;
+      // The sequence's bounds and its length are checked as a whole, so that no
+      // row of a sequence with a bad length is written.
+      fine = c0 >= 0 && c0 <= t && end <= a.total && len >= 0 &&
+             len <= (int64_t)a.max_pages * a.pages.page_size;
+      bad |= !fine;
+      at.left = 0;
     }
-    store_row<FMT, F32>(a.pages, false, at, x[r][0], hl, hmask);
-    store_row<FMT, F32>(a.pages, true, at, x[r][1], hl, hmask);
+    // (A chunk may be longer than its cache: rows before position 0 have no place.)
+    if (fine && shift + t >= 0) {
+      at = next_place<RowBytes<FMT>::value>(at, a.pages, a.page_table, a.max_pages, s, shift + t, h);
+      bad |= !at.ok();
+    }
+    Tops m{};
+    if constexpr (FMT != kKvBf16) m = tops_of<F32>(x[r][0], x[r][1], hmask);
+    store_row<FMT, F32>(a.pages, false, at, x[r][0], m.row[0], m.pair[0], hl);
+    store_row<FMT, F32>(a.pages, true, at, x[r][1], m.row[1], m.pair[1], hl);
   }
   if (bad && hl == 0) atomicOr(a.err, kErrBadArg);
 }
@@ -265,7 +316,7 @@ struct Raw {
 template <int FMT>
 __device__ __forceinline__ Raw load_raw(const KvPages &p, bool value, const Place &at, int hl) {
   Raw r{{make_uint2(0, 0), make_uint2(0, 0)}, 127, {0, 0}};
-  if (!at.ok) return r;
+  if (!at.ok()) return r;
   const uint8_t *codes = (const uint8_t *)(value ? p.v : p.k) + at.byte;
   if constexpr (FMT != kKvBf16) r.s = __ldg((value ? p.v_scale : p.k_scale) + at.row);
 #pragma unroll
@@ -332,22 +383,32 @@ __global__ void __launch_bounds__(NT) kv_gather_kernel(const __grid_constant__ K
   const int h = (int)(unit - tg * (unsigned)a.pages.Hkv);
   const int64_t t0 = (int64_t)tg * kTok;
   if (t0 >= a.total) return;
-  int s = find_seq(a.cu_rows, a.n_seq, (int)t0, hl, hmask);
+  int s = find_seq(a.cu_rows, a.n_seq, (int)t0, hl, hmask) - 1;
   Raw raw[kTok][2];
-  bool bad = false;
+  bool bad = false, fine = false;
   int n = 0;  // rows of sequences (the others stay as they were)
+  int end = INT_MIN;
+  int64_t shift = 0;  // position minus row
+  Place at{0, 0, 0};
 #pragma unroll
   for (int r = 0; r < kTok; ++r) {
     const int t = (int)t0 + r;
-    while (s < a.n_seq && __ldg(a.cu_rows + s + 1) <= t) ++s;
-    if (t >= a.total || s >= a.n_seq) break;
+    if (t >= a.total) break;
+    if (t >= end) {  // the next sequence that has rows
+      do {
+        ++s;
+      } while (s < a.n_seq && __ldg(a.cu_rows + s + 1) <= t);
+      if (s >= a.n_seq) break;
+      const int c0 = __ldg(a.cu_rows + s);
+      end = __ldg(a.cu_rows + s + 1);
+      shift = (int64_t)(a.start ? __ldg(a.start + s) : 0) - c0;
+      fine = c0 >= 0 && c0 <= t;
+      at.left = 0;
+    }
     n = r + 1;
-    const int c0 = __ldg(a.cu_rows + s);
-    Place at{0, 0, false};
-    if (c0 >= 0 && c0 <= t)
-      at = place_of<RowBytes<FMT>::value>(a.pages, a.page_table, a.max_pages, s,
-                                          (int64_t)(a.start ? __ldg(a.start + s) : 0) + (t - c0), h);
-    bad |= !at.ok;
+    if (fine)
+      at = next_place<RowBytes<FMT>::value>(at, a.pages, a.page_table, a.max_pages, s, shift + t, h);
+    bad |= !at.ok();
     raw[r][0] = load_raw<FMT>(a.pages, false, at, hl);
     raw[r][1] = load_raw<FMT>(a.pages, true, at, hl);
   }
@@ -391,11 +452,12 @@ __global__ void __launch_bounds__(NT) kv_widen_kernel(const __grid_constant__ Kv
   if (p0 >= len) return;
   Raw raw[kTok][2];
   bool bad = false;
+  Place at{0, 0, 0};
 #pragma unroll
   for (int r = 0; r < kTok; ++r) {
     if (p0 + r >= len) break;
-    const Place at = place_of<RowBytes<FMT>::value>(a.pages, a.page_table, a.max_pages, s, p0 + r, h);
-    bad |= !at.ok;
+    at = next_place<RowBytes<FMT>::value>(at, a.pages, a.page_table, a.max_pages, s, p0 + r, h);
+    bad |= !at.ok();
     raw[r][0] = load_raw<FMT>(a.pages, false, at, hl);
     raw[r][1] = load_raw<FMT>(a.pages, true, at, hl);
   }
