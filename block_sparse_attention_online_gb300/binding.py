@@ -671,7 +671,7 @@ class PagedKV:
 
 def _elsewhere(kv, stream):
     """Whether a call has to switch to another device or stream first."""
-    return stream is not None or torch.cuda.current_device() != kv.index
+    return stream is not None or torch._C._cuda_getDevice() != kv.index
 
 
 @contextlib.contextmanager
@@ -687,43 +687,46 @@ def _switched(kv, stream):
             yield
 
 
-def _raw_stream(kv):
-    return torch._C._cuda_getCurrentRawStream(kv.index)
-
-
-def _batch(kv, cu, page_table, lengths, dtype=torch.int32):
-    """Number of sequences of the device arrays ``cu`` [n_seq + 1], ``page_table``
-    [n_seq, max_pages] and ``lengths`` [n_seq] (or None), checked."""
-    n = cu.shape[0] - 1 if cu.dim() == 1 else 0
-    if n < 1 or cu.dtype is not torch.int32 or not cu.is_contiguous() \
-            or cu.get_device() != kv.index:
-        raise ValueError("the row bounds must be a contiguous int32 tensor [n_seq + 1] on the "
-                         "cache's device")
-    if page_table.dim() != 2 or page_table.shape[0] != n or page_table.dtype is not torch.int32 \
-            or not page_table.is_contiguous() or page_table.get_device() != kv.index:
-        raise ValueError(f"page_table must be a contiguous int32 tensor [{n}, max_pages] on the "
-                         "cache's device")
-    if lengths is not None:
-        _per_sequence("kv_len (or start)", lengths, n, torch.int32, kv)
-    return n
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else None  # (a build of torch without CUDA: no cache can be made there)
+_int32, _float32 = torch.int32, torch.float32
 
 
 def _per_sequence(name, x, n, dtype, kv):
-    if x.dim() != 1 or x.shape[0] != n or x.dtype is not dtype or not x.is_contiguous() \
+    if x.shape != (n,) or x.dtype is not dtype or not x.is_contiguous() \
             or x.get_device() != kv.index:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}] on the cache's device")
 
 
-def _token_stride(name, x, heads, kv):
-    """Token stride of x [total, heads, 128]; the rows of a token must be dense."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != kv.d:
-        raise ValueError(f"{name} must have shape [total, {heads}, {kv.d}]")
+def _batch(kv, cu, page_table, lengths):
+    """Number of sequences of the device arrays ``cu`` [n_seq + 1], ``page_table``
+    [n_seq, max_pages] and ``lengths`` [n_seq] (or None), checked, and max_pages."""
+    index = kv.index
+    n = cu.numel() - 1
+    if n < 1 or cu.dim() != 1 or cu.dtype is not _int32 or not cu.is_contiguous() \
+            or cu.get_device() != index:
+        raise ValueError("the row bounds must be a contiguous int32 tensor [n_seq + 1] on the "
+                         "cache's device")
+    shape = page_table.shape
+    if len(shape) != 2 or shape[0] != n or page_table.dtype is not _int32 \
+            or not page_table.is_contiguous() or page_table.get_device() != index:
+        raise ValueError(f"page_table must be a contiguous int32 tensor [{n}, max_pages] on the "
+                         "cache's device")
+    if lengths is not None:
+        _per_sequence("kv_len (or start)", lengths, n, _int32, kv)
+    return n, shape[1]
+
+
+def _token_stride(name, x, shape, kv):
+    """Token stride of x, whose shape [total, heads, 128] is given; the rows of a
+    token must be dense."""
+    heads, d = shape[1], kv.d
+    s = x.stride()
     if x.get_device() != kv.index:
         raise ValueError(f"{name} must be on the cache's device")
-    s = x.stride()
-    if x.shape[0] and (s[2] != 1 or (heads > 1 and s[1] != kv.d)):
+    if shape[0] and (s[2] != 1 or (heads > 1 and s[1] != d)):
         raise ValueError(f"the heads of a token of {name} must be dense")
-    return s[0] if x.shape[0] > 1 else heads * kv.d
+    return s[0] if shape[0] > 1 else heads * d
 
 
 def attn_skip_kv_append(kv, k_new, v_new, cu_seqlens, kv_len, page_table, stream=None):
@@ -734,16 +737,19 @@ def attn_skip_kv_append(kv, k_new, v_new, cu_seqlens, kv_len, page_table, stream
     if _elsewhere(kv, stream):
         with _switched(kv, stream):
             return attn_skip_kv_append(kv, k_new, v_new, cu_seqlens, kv_len, page_table)
-    n = _batch(kv, cu_seqlens, page_table, kv_len)
-    ks = _token_stride("k_new", k_new, kv.Hkv, kv)
-    vs = _token_stride("v_new", v_new, kv.Hkv, kv)
-    total = k_new.shape[0]
-    if v_new.shape[0] != total or v_new.dtype is not k_new.dtype:
+    n, max_pages = _batch(kv, cu_seqlens, page_table, kv_len)
+    shape = k_new.shape
+    if len(shape) != 3 or shape[1] != kv.Hkv or shape[2] != kv.d:
+        raise ValueError(f"k_new must have shape [total, {kv.Hkv}, {kv.d}]")
+    if v_new.shape != shape or v_new.dtype is not k_new.dtype:
         raise ValueError("k_new and v_new must agree in shape and dtype")
-    _check("attn_skip_kv_append", (_lib or load()).attn_skip_kv_append(
-        kv._ref, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), ks, vs, n, total,
-        cu_seqlens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.shape[1],
-        _raw_stream(kv)))
+    st = (_lib or load()).attn_skip_kv_append(
+        kv._ref, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new),
+        _token_stride("k_new", k_new, shape, kv), _token_stride("v_new", v_new, shape, kv), n,
+        shape[0], cu_seqlens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), max_pages,
+        _raw_stream(kv.index))
+    if st:
+        _check("attn_skip_kv_append", st)
 
 
 def attn_skip_kv_gather(kv, cu_rows, start, page_table, total, out_dtype=torch.bfloat16, out=None,
@@ -755,19 +761,22 @@ def attn_skip_kv_gather(kv, cu_rows, start, page_table, total, out_dtype=torch.b
     if _elsewhere(kv, stream):
         with _switched(kv, stream):
             return attn_skip_kv_gather(kv, cu_rows, start, page_table, total, out_dtype, out)
-    n = _batch(kv, cu_rows, page_table, start)
+    n, max_pages = _batch(kv, cu_rows, page_table, start)
     if out is None:
-        k, v = torch.empty((2, total, kv.Hkv, kv.d), dtype=out_dtype, device=kv.device).unbind()
+        k = torch.empty((total, kv.Hkv, kv.d), dtype=out_dtype, device=kv.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
         if total and k.data_ptr() == v.data_ptr():
             raise ValueError("the two outputs must be different tensors")
         for x in out:
             _like("out", x, (total, kv.Hkv, kv.d), k.dtype, kv)
-    _check("attn_skip_kv_gather", (_lib or load()).attn_skip_kv_gather(
+    st = (_lib or load()).attn_skip_kv_gather(
         kv._ref, n, total, cu_rows.data_ptr(), None if start is None else start.data_ptr(),
-        page_table.data_ptr(), page_table.shape[1], _dtype_code(k), k.data_ptr(), v.data_ptr(),
-        _raw_stream(kv)))
+        page_table.data_ptr(), max_pages, _dtype_code(k), k.data_ptr(), v.data_ptr(),
+        _raw_stream(kv.index))
+    if st:
+        _check("attn_skip_kv_gather", st)
     return k, v
 
 
@@ -815,20 +824,20 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
             return attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_table,
                                          lambdas, causal, scale, n_splits, with_bits, out,
                                          workspace, rows)
-    n = _batch(kv, cu_seqlens, page_table, kv_len)
-    _per_sequence("lambdas", lambdas, n, torch.float32, kv)
-    if q.dtype is not torch.bfloat16 or q.dim() != 3:
+    n, max_pages = _batch(kv, cu_seqlens, page_table, kv_len)
+    _per_sequence("lambdas", lambdas, n, _float32, kv)
+    qshape = q.shape
+    if q.dtype is not torch.bfloat16 or len(qshape) != 3 or qshape[2] != kv.d:
         raise TypeError("q must be a bfloat16 tensor [total, Hq, 128]")
-    total, Hq, d = q.shape
-    qs = _token_stride("q", q, Hq, kv)
+    total, Hq, d = qshape
     if Hq % kv.Hkv or Hq // kv.Hkv > 128:
         raise ValueError(f"{Hq} query heads do not fit {kv.Hkv} KV heads")
     splits, size = _chunk_plan(kv._fmt, n, total, Hq, kv.Hkv, max_chunk, max_kv)
     n_splits = n_splits or splits
     bits = None
     if out is None:
-        o = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=kv.device)
-        lse = torch.empty((total, Hq), device=kv.device, dtype=torch.float32)
+        o = torch.empty(qshape, dtype=torch.bfloat16, device=kv.device)
+        lse = torch.empty((total, Hq), dtype=_float32, device=kv.device)
     else:
         o, lse, bits = out
         _like("out", o, (total, Hq, d), torch.bfloat16, kv)
@@ -856,12 +865,14 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
     elif rows.dtype is not torch.uint8 or rows.numel() < size or not rows.is_contiguous() \
             or rows.get_device() != kv.index:
         raise ValueError(f"rows must be a contiguous uint8 tensor of {size} bytes on {kv.device}")
-    _check("attn_skip_chunk_paged", (_lib or load()).attn_skip_chunk_paged(
-        kv._ref, q.data_ptr(), qs, Hq, n, total, cu_seqlens.data_ptr(), max_chunk,
-        kv_len.data_ptr(), max_kv, page_table.data_ptr(), page_table.shape[1], scale,
-        lambdas.data_ptr(), 1 if causal else 0, n_splits, o.data_ptr(), lse.data_ptr(),
-        None if bits is None else bits.data_ptr(), op, lp,
-        None if rows is None else rows.data_ptr(), _raw_stream(kv)))
+    st = (_lib or load()).attn_skip_chunk_paged(
+        kv._ref, q.data_ptr(), _token_stride("q", q, qshape, kv), Hq, n, total,
+        cu_seqlens.data_ptr(), max_chunk, kv_len.data_ptr(), max_kv, page_table.data_ptr(),
+        max_pages, scale, lambdas.data_ptr(), 1 if causal else 0, n_splits, o.data_ptr(),
+        lse.data_ptr(), None if bits is None else bits.data_ptr(), op, lp,
+        None if rows is None else rows.data_ptr(), _raw_stream(kv.index))
+    if st:
+        _check("attn_skip_chunk_paged", st)
     return o, lse, bits
 
 
