@@ -614,7 +614,8 @@ extern "C" attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, i
 extern "C" int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, int total, int Hq,
                                             int Hkv, int max_chunk, int max_kv) {
   if (n_seq <= 0 || total <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 ||
-      max_chunk <= 0 || max_kv <= 0 || max_kv > kMaxPositions)
+      max_chunk <= 0 || max_kv <= 0 || max_kv > kMaxPositions || max_chunk > kMaxPositions ||
+      total > kMaxPositions)
     return 1;
   return chunk_paged_splits(n_seq, total, max_chunk, max_kv, Hkv, 128 / (Hq / Hkv), (int)format);
 }
@@ -622,7 +623,7 @@ extern "C" int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, in
 extern "C" size_t attn_skip_chunk_paged_kv_bytes(attn_kv_format format, int n_seq, int Hq, int Hkv,
                                                  int max_chunk, int max_kv) {
   if (n_seq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || max_chunk <= 0 ||
-      max_kv <= 0 || max_kv > kMaxPositions)
+      max_kv <= 0 || max_kv > kMaxPositions || max_chunk > kMaxPositions)
     return 0;
   return chunk_paged_kv_bytes(n_seq, max_chunk, max_kv, Hkv, 128 / (Hq / Hkv), (int)format);
 }
@@ -642,6 +643,7 @@ extern "C" attn_status attn_skip_chunk_paged(
     return ATTN_EINVAL;
   if (n_splits < 1 || n_splits > 1024) return ATTN_EINVAL;
   if (max_kv > (int64_t)max_pages * kv->page_size) return ATTN_EINVAL;
+  if (max_chunk > kMaxPositions || total > kMaxPositions) return ATTN_EUNSUPPORTED;
   const int G = Hq / kv->Hkv;
   if (G > 128) return ATTN_EUNSUPPORTED;
   if (total == 0 && max_chunk == 0) return ATTN_OK;

@@ -193,6 +193,34 @@ __device__ __forceinline__ void load_block(const ChunkArgs &a, Producer &p, cons
   __syncwarp();
 }
 
+// The scale byte of the value row at position pos, as the reference should see it:
+// a row of zeros, which the writer gives byte 127, has no contribution to make room
+// for, so its exponent becomes the smallest (17).  `mine`: the lane has a row of
+// byte 127 below kv; the row's four lanes look at a quarter of its codes each.
+template <int FMT>
+__device__ __noinline__ uint32_t settle_zero_row(const ChunkArgs &a, int s, int hk, int pos, bool mine,
+                                                 uint32_t byte, int t) {
+  const KvPages &p = a.pages;
+  constexpr uint32_t QUARTER = Cfg<FMT>::ROW / 4;
+  uint32_t any = 0;
+  if (mine) {
+    int page = __ldg(a.page_table + (int64_t)s * a.max_pages + pos / p.page_size);
+    if (page < 0 || page >= p.n_pages) page = 0;
+    const uint4 *c = reinterpret_cast<const uint4 *>(
+        (const uint8_t *)p.v + page * p.page_stride +
+        ((int64_t)hk * p.page_size + pos % p.page_size) * Cfg<FMT>::ROW + t * QUARTER);
+#pragma unroll
+    for (uint32_t k = 0; k < QUARTER / 16; ++k) {
+      const uint4 w = __ldg(c + k);
+      any |= w.x | w.y | w.z | w.w;
+    }
+    any &= FMT == kKvE4m3 ? 0x7f7f7f7fu : 0x77777777u;
+  }
+  any |= __shfl_xor_sync(0xffffffffu, any, 1);
+  any |= __shfl_xor_sync(0xffffffffu, any, 2);
+  return mine && any == 0 ? 17u : byte;
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(NT, 2)
     decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -416,9 +444,13 @@ __global__ void __launch_bounds__(NT, 2)
       }
       const uint32_t sc = kx + C::BS;
       const uint32_t eb0 = lds8(sc + kr0), eb1 = lds8(sc + kr1);
-      const uint32_t vb0 = lds8(sc + BN + kr0), vb1 = lds8(sc + BN + kr1);
+      uint32_t vb0 = lds8(sc + BN + kr0), vb1 = lds8(sc + BN + kr1);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.k_empty[s]));  // the stage is in registers
+      if (__any_sync(0xffffffffu, vb0 == 127u || vb1 == 127u)) {
+        vb0 = settle_zero_row<FMT>(a, x.s, hk, j * BN + kr0, vb0 == 127u && kr0 < left, vb0, t);
+        vb1 = settle_zero_row<FMT>(a, x.s, hk, j * BN + kr1, vb1 == 127u && kr1 < left, vb1, t);
+      }
       const float f0 = __uint_as_float(eb0 << 23), f1 = __uint_as_float(eb1 << 23);
       p[0][0] = acc[0] * (qs[0] * f0);
       p[0][1] = acc[1] * (qs[1] * f0);

@@ -104,6 +104,7 @@ def special_rows(g, n, Hkv, dtype):
     ((1,), (0,), 16, 1),
     ((3, 0, 17, 1), (5, 9, 0, 63), 16, 3),
     ((130, 64, 1), (0, 64, 127), 64, 2),
+    ((390, 5), (379, 0), 384, 1),
     ((2500, 700), (3, 1000), 128, 8),  # the kernel's four rows a half warp
 ])
 def test_append_writes_what_the_formats_define(fmt, dtype, chunks, before, ps, Hkv):
@@ -218,6 +219,7 @@ def test_gather_reads_every_code_exactly():
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("lens,starts,ps,Hkv", [
     ((1,), None, 16, 1), ((5, 0, 33), (11, 3, 0), 16, 3), ((3000, 1), (77, 12), 256, 8),
+    ((500, 9), (300, 380), 384, 1),
 ])
 def test_gather_matches_the_pool(fmt, lens, starts, ps, Hkv):
     ends = [a + b for a, b in zip(lens, starts or (0,) * len(lens))]
@@ -337,6 +339,10 @@ CASES = [
     ((2, 3), (0, 2), 16, 1, 2, 1),       # an empty cache; a chunk longer than its cache
     ((4, 6), (0, 3), 16, 1, 2, 2),
     ((130,), (1,), 16, 1, 1, 1),
+    ((3, 7), (500, 900), 384, 2, 4, 3),  # a page size that is no power of two, not four whole parts
+    ((1, 2), (400, 260), 16, 1, 16, 2),  # 32 rows
+    ((20, 9), (1030, 300), 64, 2, 4, 2),  # 80 rows of one tile
+    ((60, 33), (700, 256), 32, 1, 4, 1),  # two tiles
 ]
 
 
@@ -357,6 +363,9 @@ def test_chunk_dense(fmt, case, causal):
     ((200, 64, 3), (1500, 2100, 4000), 8, 1, (0.02, 1e-3, 0.3), True),
     ((50, 1), (5000, 4000), 4, 5, (0.02, 1e-3), False),  # salient keys in every split: none
     ((1, 1), (5000, 4000), 4, 4, (0.5, 0.4), True),
+    ((3, 2, 1), (3000, 1111, 640), 8, 1, (0.02, 1e-2, 0.3), True),  # 24 rows
+    ((3, 2), (5000, 4000), 8, 3, (0.6, 0.5), False),
+    ((20, 4), (3000, 2222), 4, 1, (0.02, 0.1), True),               # 80 rows of one tile
 ])
 def test_chunk_skips_by_the_threshold(fmt, chunks, lens, G, n_splits, lams, some):
     Hkv = 2
@@ -408,15 +417,35 @@ def test_chunk_scale_and_large_values(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "nvfp4", "bf16"])
-def test_chunk_nan_row_reaches_the_rows_that_see_it(fmt):
+@pytest.mark.parametrize("Hq", [2, 8, 40])  # 4, 16 and 80 rows
+def test_chunk_nan_row_reaches_the_rows_that_see_it(fmt, Hq):
     kv, table = cache_of(fmt, (300, 300), 16, 1, 61)
     bad = torch.full((1, 1, 128), float("nan"), device=DEV)
     good = torch.ones(1, 1, 128, device=DEV)
     # Position 299 of sequence 0 gets a NaN key.
     bs.attn_skip_kv_append(kv, bad, good, i32([0, 1, 1]), i32([300, 300]), table)
-    q, (o, lse, _) = attend(kv, table, (2, 2), (300, 300), 2, [0.0, 0.0])
+    q, (o, lse, _) = attend(kv, table, (2, 2), (300, 300), Hq, [0.0, 0.0])
     assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
     assert torch.isfinite(o[0]).all() and torch.isfinite(o[2:]).all()  # it is masked, or another's
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4"])
+@pytest.mark.parametrize("chunks,Hq", [((2, 1), 4), ((4, 3), 4), ((40, 9), 4), ((200, 90), 4)])
+def test_chunk_rows_of_very_different_scales(fmt, chunks, Hq):
+    """Small rows next to rows of zeros (whose scale byte is 127) and rows 2^12
+    apart: one exponent a block has to serve them all."""
+    lens, g = (300, 260), np.random.default_rng(63)
+    table, n_pages = tables(lens, 16, g)
+    kv = filled_cache(fmt, n_pages, 16, 1)
+    x = [g.standard_normal((560, 1, 128)) * 2.0 ** -17 for _ in range(2)]
+    for y in x:
+        y[g.random(560) < 0.1] = 0.0
+        y[g.random(560) < 0.3] *= 2.0 ** -12
+    k, v = (torch.from_numpy(y).to(DEV, torch.float32) for y in x)
+    bs.attn_skip_kv_append(kv, k, v, cu_of(lens), i32(lens), table)
+    q = (torch.randn(sum(chunks), Hq, 128, device=DEV) * 2.0 ** 17).to(torch.bfloat16)
+    q, out = attend(kv, table, chunks, lens, Hq, [0.0, 0.0], q=q)
+    check(kv, table, chunks, lens, Hq, [0.0, 0.0], q, out)
 
 
 def test_chunk_reports_bad_device_arguments():

@@ -102,6 +102,8 @@ def test_chunk_rejects(lib, kw):
 
 def test_chunk_too_many_heads_and_empty_calls(lib):
     assert chunk(lib, Hq=2 * 129, qs=2 * 129 * 128) == bs.ATTN_EUNSUPPORTED
+    assert chunk(lib, max_chunk=0x7fffffff) == bs.ATTN_EUNSUPPORTED
+    assert chunk(lib, total=0x7fffffff) == bs.ATTN_EUNSUPPORTED
     assert append(lib, total=0, k=None, v=None) == bs.ATTN_OK
     assert gather(lib, total=0, k=None, v=None) == bs.ATTN_OK
     assert chunk(lib, total=0, q=None, o=None, lse=None) == bs.ATTN_OK
