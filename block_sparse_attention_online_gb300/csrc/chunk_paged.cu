@@ -35,10 +35,11 @@
 // that cost nothing per score: with E_k and E_v the largest row-scale exponents
 // of a block's keys and values, the tiles hold code * 2^(e - E) (exact for e >=
 // E - 15, otherwise off by at most 2^-25 2^E), the scores of the block are
-// scaled by 2^E_k, and P takes 2^E_v: P'_c = 2^(s_c + E_v - ref), with ref the
-// running max of (row max + E_v) over the blocks, so P' stays in fp16's range
-// and its smallest step, 2^-24, is that fraction of the largest contribution;
-// the row sum takes sum P' * 2^-E_v.  A query row enters as fp16(q * 2^x), 2^x
+// scaled by 2^E_k, and P takes 2^E_v: P'_c = 2^(s_c + E_v - ref + 7), with ref the
+// running max of (row max + E_v) over the blocks, which may lag by 2^8: P' stays
+// below fp16's 2^16, has its 11 bits down to 2^-21 of the largest contribution and
+// steps of 2^-31 of it below (it counts where the row with the large weight holds
+// a zero); the row sum takes sum P' * 2^(-E_v - 7).  A query row enters as fp16(q * 2^x), 2^x
 // the largest power of two with max|q| 2^x <= 2^15.
 //
 // A warp quarter whose 32 rows lie past the tile's last row (decode: G rows) has
@@ -931,7 +932,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
           rescale = true;
         }
         // A row without a visible key so far has only -inf scores: P = 0.
-        const float nref = mref == -INFINITY ? 0.f : (float)(ev - 127) - mref;
+        const float nref = mref == -INFINITY ? 0.f : (float)(ev - 127) - mref + (QUANT ? kPLog2 : 0.f);
         const uint64_t sl2x2 = f2(bl2, bl2), negref2 = f2(nref, nref);
         uint64_t acc2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
         if constexpr (REP) {
@@ -976,7 +977,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         f2_split(acc2[0], acc[0], acc[1]);
         f2_split(acc2[1], acc[2], acc[3]);
         float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-        if constexpr (QUANT) sum *= __int_as_float(max(1, 254 - ev) << 23);  // sum P' 2^-E_v
+        if constexpr (QUANT) sum = sum * kPDown * __int_as_float(max(1, 254 - ev) << 23);
         l = l * alpha + sum;
         if (__any_sync(0xffffffffu, rescale) && kc >= 1) {
           if (!wait_warp(&sh.pv_done[(kc - 1) % NS], (kc - 1) / NS)) {
@@ -1046,7 +1047,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
         lref = sh.mdec[1][r];
         w = lrow == 0.f ? 0.f : 1.f;  // no key kept for this row: O = 0
       }
-      const float inv = lrow == 0.f ? 0.f : w / lrow;
+      const float inv = lrow == 0.f ? 0.f : (QUANT ? kPDown * w : w) / lrow;
       const bool none = w == 0.f;  // (the accumulator may hold anything)
       // The rows leave through 4 KB of the query tile a warp (free by now): a lane's
       // row in 16-byte pieces, then 128-byte runs of four rows an instruction.

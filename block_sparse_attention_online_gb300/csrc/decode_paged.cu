@@ -9,11 +9,13 @@
 // and a row scale multiplies one score instead of 128 elements:
 //   S^T = K Q^T        A = codes of 16 keys, B = fp16 queries (2^x scaled)
 //   s_c = S_c * scale * 2^(e_k,c - x)         (log2 units)
-//   P_c = 2^(s_c + e_v,c - ref),  ref the running max of s_c + e_v,c of the warp
+//   P_c = 2^(s_c + e_v,c - ref + 7),  ref the running max of s_c + e_v,c of the warp
 //   O^T += V^T P       A = codes of 16 keys, transposed by byte pairs, B = P
-//   l += P_c 2^(-e_v,c)
-// An NVFP4 code times its block scale is an fp16 (exact); P is rounded to fp16,
-// whose smallest step, 2^-24, is that fraction of the largest contribution.
+//   l += P_c 2^(-e_v,c - 7)
+// An NVFP4 code times its block scale is an fp16 (exact); P is rounded to fp16.
+// The reference may lag by 2^8, so with 2^7 P stays below fp16's 2^16, has its 11
+// bits down to 2^-21 of the largest contribution and steps of 2^-31 of it below
+// (it counts where the row with the large weight holds a zero).
 //
 // One CTA per (sequence, KV head, split), two on an SM.  Eight warps share each
 // 128-key block, 16 keys a warp, each with its own running reference, row sums
@@ -535,6 +537,8 @@ __global__ void __launch_bounds__(NT, 2)
       if (!keep) continue;
     }
     if (!ok) continue;
+    inv[0] *= kPDown;
+    inv[1] *= kPDown;
     // The reference moves when a key's s + e_v passes it by more than 2^8 (or it
     // is the row's first): then by the warp's maximum.
     const bool move = fmaxf(y[0][0], y[1][0]) > top[0] || fmaxf(y[0][1], y[1][1]) > top[1];
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(NT, 2)
         const float to = fmaxf(ref[n], m);
         al[n] = to == -INFINITY ? 1.f : ex2(ref[n] - to);
         ref[n] = to;
-        sub[n] = to == -INFINITY ? 0.f : to;
+        sub[n] = to == -INFINITY ? 0.f : to - kPLog2;
         top[n] = to + kRescaleLog2;
         l[n] *= al[n];
       }
@@ -682,7 +686,7 @@ __global__ void __launch_bounds__(NT, 2)
       v.z = fmaf(u.z, f, v.z);
       v.w = fmaf(u.w, f, v.w);
     }
-    const float iz = z == 0.f ? 0.f : 1.f / z;
+    const float iz = z == 0.f ? 0.f : kPDown / z;
     const int64_t orow = (int64_t)(x.tok0 + r / a.G) * a.Hq + hk * a.G + r % a.G;
     if (a.n_splits == 1)
       *reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.o + orow * D + col) =

@@ -404,6 +404,79 @@ def test_chunk_many_sequences(n_splits):
     check(kv, table, chunks, lens, 4, [0.0] * 77, q, out, n_splits=n_splits)
 
 
+def batch(n, longest, seed, kinds=(1, 1, 1, 2)):
+    """n sequences of mixed lengths, some of them empty, one of them the longest."""
+    g = np.random.default_rng(seed)
+    lens = [int(x) for x in g.integers(1, longest, n)]
+    chunks = [int(c) for c in g.choice(kinds, n)]
+    lens[n // 2], lens[n // 3], lens[n - 1], chunks[n // 4] = longest, 0, 1, 0
+    return chunks, lens
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4"])
+@pytest.mark.parametrize("n,longest,Hkv,G,n_splits", [
+    (24, 2500, 4, 4, 7),    # tiles cut where the CTAs' runs end
+    (3, 9000, 8, 1, 20),    # few long tiles: a run per block
+    (40, 130, 4, 2, 2),     # two blocks at most
+    (100, 300, 4, 4, 1),    # whole tiles, several a CTA
+    (33, 1500, 2, 3, 64),   # more slots than blocks
+    (128, 700, 1, 4, 3),
+    (129, 700, 1, 4, 3),    # more sequences than are shared out
+])
+def test_decode_of_more_pieces_than_ctas(fmt, n, longest, Hkv, G, n_splits):
+    assert n * Hkv * n_splits > 304
+    chunks, lens = batch(n, longest, n + G)
+    kv, table = cache_of(fmt, lens, 16, Hkv, n)
+    q, out = attend(kv, table, chunks, lens, Hkv * G, [0.0] * n, n_splits=n_splits, seed=n)
+    check(kv, table, chunks, lens, Hkv * G, [0.0] * n, q, out, n_splits=n_splits)
+    again = attend(kv, table, chunks, lens, Hkv * G, [0.0] * n, n_splits=n_splits, q=q)[1]
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4"])
+@pytest.mark.parametrize("n,longest,n_splits", [(24, 2500, 7), (100, 400, 2), (160, 200, 1)])
+def test_decode_of_more_pieces_than_ctas_skips(fmt, n, longest, n_splits):
+    """Thresholds on some sequences: the splits' bounds hold for every tile."""
+    Hkv, G = 2, 4
+    chunks, lens = batch(n, longest, n)
+    lams = [(0.0, 0.3, 0.6)[s % 3] for s in range(n)]
+    kv, table = cache_of(fmt, lens, 32, Hkv, n, sink=1.0)
+    g = np.random.default_rng(n)
+    q = torch.from_numpy(g.standard_normal((sum(chunks), Hkv * G, 128)) + 0.7).to(DEV, torch.bfloat16)
+    q, out = attend(kv, table, chunks, lens, Hkv * G, lams, True, n_splits, q=q)
+    skipped = check(kv, table, chunks, lens, Hkv * G, lams, q, out, True, n_splits)
+    assert skipped > 0
+
+
+@pytest.mark.parametrize("n_splits", [1, 4])
+def test_decode_of_more_pieces_than_ctas_with_bad_device_arguments(n_splits):
+    n, Hkv, Hq = 110, 3, 6
+    lens = [200 + s for s in range(n)]
+    kv, table = cache_of("e4m3", lens, 16, Hkv, 14)
+    q = torch.randn(n + 4, Hq, 128, device=DEV).to(torch.bfloat16)
+    cu, kl, lam = i32(range(n + 1)), i32(lens), torch.zeros(n, device=DEV)
+    want, wl, _ = bs.attn_skip_chunk_paged(kv, q, cu, 1, kl, max(lens), table, lam, n_splits=n_splits)
+    bs.attn_skip_last_device_error()
+    bad_cu, bad_kl, bad_t, bad_lam = cu.clone(), kl.clone(), table.clone(), lam.clone()
+    bad_cu[41:] += 1                       # sequence 40: two tokens, one allowed
+    bad_kl[7], bad_kl[50] = max(lens) + 1, -1
+    bad_t[3, 2], bad_t[3, 5] = -4, 10 ** 6
+    bad_lam[9] = float("nan")
+    o, lse = torch.full_like(want, 2.0), torch.full_like(wl, 2.0)
+    bs.attn_skip_chunk_paged(kv, q, bad_cu, 1, bad_kl, max(lens), bad_t, bad_lam, n_splits=n_splits,
+                             out=(o, lse, None))
+    with pytest.raises(bs.AttnSkipError) as e:
+        bs.attn_skip_last_device_error()
+    assert e.value.status == bs.ATTN_EINVAL
+    for s in (7, 50):
+        r = s + (s > 40)
+        assert (o[r] == 0).all() and torch.isneginf(lse[r]).all()
+    for r in (40, 41, n + 1, n + 2, n + 3):  # the sequence left out; rows behind the last one
+        assert (o[r] == 2).all() and (lse[r] == 2).all()
+    for s in (0, 1, 2, 4, 9, 39):
+        assert torch.allclose(o[s].float(), want[s].float(), atol=0.02)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_chunk_scale_and_large_values(fmt):
     """An explicit score scale, and rows whose scale byte needs a second bf16
@@ -446,6 +519,24 @@ def test_chunk_rows_of_very_different_scales(fmt, chunks, Hq):
     q = (torch.randn(sum(chunks), Hq, 128, device=DEV) * 2.0 ** 17).to(torch.bfloat16)
     q, out = attend(kv, table, chunks, lens, Hq, [0.0, 0.0], q=q)
     check(kv, table, chunks, lens, Hq, [0.0, 0.0], q, out)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [1, 7, 20])  # 4, 28 and 80 rows
+def test_chunk_distant_key_behind_zeros(fmt, n):
+    """Where the key with all the weight has a value of zero, an output is what a
+    key 13.6 nats below it brings: it is as exact as any other."""
+    Hkv, G = 1, 4
+    kv = filled_cache(fmt, 2, 16, Hkv)
+    table = i32([1]).view(1, 1)
+    k = torch.ones(3, Hkv, 128, device=DEV, dtype=torch.bfloat16)
+    k[0], k[2] = -1, 0.5
+    v = torch.randn(3, Hkv, 128, device=DEV).to(torch.bfloat16)
+    v[1, :, ::2], v[2] = 0, 0
+    bs.attn_skip_kv_append(kv, k, v, cu_of([3]), i32([3]), table)
+    q = torch.full((n, Hkv * G, 128), 0.6, device=DEV, dtype=torch.bfloat16)
+    q, out = attend(kv, table, (n,), (3,), Hkv * G, [0.0], False, q=q)
+    check(kv, table, (n,), (3,), Hkv * G, [0.0], q, out, False)
 
 
 def test_chunk_reports_bad_device_arguments():
