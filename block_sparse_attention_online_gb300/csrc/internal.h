@@ -143,6 +143,7 @@ struct ChunkArgs {
   const int32_t *page_table;           // null: sequence s's rows are page s
   const float *lambda;
   float scale;
+  int shared_out;                      // decode: the CTAs share the batch out among themselves
   unsigned *err;
 };
 

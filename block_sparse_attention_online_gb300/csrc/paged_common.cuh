@@ -174,7 +174,7 @@ __device__ __forceinline__ int page_of_part(const ChunkArgs &a, const Producer &
 
 // The first pages' ids load before the sequence's length is known (n_parts is set
 // then): entries of its row of the table, whether or not they stand for pages.
-__device__ __forceinline__ void producer_start(const ChunkArgs &a, Producer &p, int s, int split,
+__device__ __forceinline__ void producer_start(const ChunkArgs &a, Producer &p, int s, int j0,
                                                int hk, int lane) {
   p.table = a.page_table ? a.page_table + (int64_t)s * a.max_pages : nullptr;
   p.seq = s;
@@ -184,7 +184,7 @@ __device__ __forceinline__ void producer_start(const ChunkArgs &a, Producer &p, 
   p.hk = hk;
   // Keys and values are read again by the other tiles of the sequence, or once.
   p.policy = a.max_chunk > a.TT ? policy_evict_last() : policy_evict_first();
-  p.base = ((split * a.bps) << (7 - p.lsub)) & ~31;
+  p.base = (j0 << (7 - p.lsub)) & ~31;
   p.cur = page_of_part(a, p, p.base + lane);
   p.nxt = page_of_part(a, p, p.base + 32 + lane);
 }
@@ -193,11 +193,18 @@ __device__ __forceinline__ void producer_start(const ChunkArgs &a, Producer &p, 
 __device__ __forceinline__ TileInfo producer_tile(const ChunkArgs &a, Producer &p, int i, int split,
                                                   int hk, int lane) {
   const int known = known_sequence(a, i);
-  if (known >= 0) producer_start(a, p, known, split, hk, lane);
+  if (known >= 0) producer_start(a, p, known, split * a.bps, hk, lane);
   const TileInfo x = locate(a, i, split, lane, known);
-  if (known < 0 && x.s >= 0) producer_start(a, p, x.s, split, hk, lane);
+  if (known < 0 && x.s >= 0) producer_start(a, p, x.s, split * a.bps, hk, lane);
   p.n_parts = (x.kv + (1 << p.lsub) - 1) >> p.lsub;
   return x;
+}
+
+// A producer warp's set-up for the blocks of x from x.j0 on.
+__device__ __forceinline__ void producer_at(const ChunkArgs &a, Producer &p, const TileInfo &x, int hk,
+                                            int lane) {
+  producer_start(a, p, x.s, x.j0, hk, lane);
+  p.n_parts = (x.kv + (1 << p.lsub) - 1) >> p.lsub;
 }
 
 // The parts of block j for the lanes of the warp: lane l < n has part l's page and

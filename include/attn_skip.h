@@ -620,7 +620,8 @@ attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
  *              max_kv <= max_pages * page_size
  *  lambda      [n_seq] fp32 (device), each in [0, 1); 0 = dense
  *  n_splits    1 .. 1024.  attn_skip_chunk_paged_splits proposes a count (it
- *              has no influence on the result at lambda = 0 beyond rounding)
+ *              has no influence on the result at lambda = 0 beyond rounding; a
+ *              batch whose lambdas are all 0 may be cut elsewhere, into as many)
  *  o           [total, Hq, 128] bf16, lse [total, Hq] fp32: written for the
  *              rows of the sequences, others stay as they were
  *  skip_bits   [n_seq, Hkv, ceil(max_chunk / TT), n_splits, ceil(bps / 32)]
@@ -635,10 +636,11 @@ attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
  *              chip by every tile.  Calls that overlap need their own
  * Products accumulate in fp32; statistics and row sums are fp32.  P is rounded
  * to bf16 for the P.V product (to fp16 where a quantised cache is widened on the
- * chip, with steps of 2^-24 of the largest contribution at the small end).
+ * chip, with steps of 2^-31 of the largest contribution at the small end).
  * There a row whose scale is 2^15 or more below the largest of its 128-row block
- * is rounded to 2^-25 of that scale.  Cache rows at or past kv_len may hold anything.  A value row that
- * is not finite, and in sight of some row of a tile, reaches every row of it.
+ * is rounded to 2^-25 of that scale.  Cache rows at or past kv_len may hold
+ * anything.  A value row that is not finite, and in sight of some row of a tile,
+ * reaches every row of it.
  * EINVAL as for attn_skip_kv_append, for max_chunk or max_kv < 0 or beyond the
  * page table and for n_splits out of range; head size or G out of range are
  * EUNSUPPORTED.  Checked by the kernel and reported by
