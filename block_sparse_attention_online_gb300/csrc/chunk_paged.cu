@@ -1138,6 +1138,592 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
   }
 }
 
+// ------------------------------------------------------------ bf16 prompts --
+// Tiles of more than 32 rows over a bf16 cache (prompts, chunks of them, and the
+// widened rows of a quantised cache): the same loop, in CTAs that stay.  A CTA that
+// has issued its tile's key loads takes over a CTA of the grid that has not started
+// (cluster launch control) and goes on to load that one's queries and keys, so that
+// set-up, the first loads and the first scores of a tile lie under the end of the
+// one before, and TMEM and barriers are set up once.  Rings run on from tile to
+// tile: block g is the CTA's g-th.  Two query tiles, of which an epilogue also takes
+// the free one's place to put its rows in order, three key and two value tiles.
+// Bound for short tiles: the scores' way to the last P.V and out, which the next
+// tile's decisions wait for.
+constexpr int PK = 3, PQ = 2;
+constexpr uint32_t P_Q = 0, P_K = PQ * TILE_BYTES, P_V = P_K + PK * TILE_BYTES;
+constexpr uint32_t P_END = P_V + NV * TILE_BYTES;
+constexpr int P_WARPS = 13;
+constexpr int kTileBarrier = 2;
+
+struct PromptShared {
+  uint4 next;            // answer of the cluster launch control
+  uint64_t next_full;
+  uint64_t tile_full[2]; // ring of the tiles: set,
+  uint64_t tile_empty[2];  // and left by twelve warps (all but the key producer)
+  uint64_t q_full[2];
+  uint64_t ready[NR];    // slot g % NR: block g's key tile is in and its S buffer free
+  uint64_t qk_done[NR];
+  uint64_t v_full[NV], v_empty[NV];
+  uint64_t p_full[NS], pv_done[NS];
+  uint64_t dec_full[NDEC], dec_read[NDEC];
+  uint64_t l_full[2];
+  uint64_t v_tail;
+  int dec[NDEC];
+  float mdec[NS][BM];    // running max after the buffer's block (log2 units)
+  float sum[BM], ref[BM];  // row sums and references for the epilogue
+  TileInfo tile[2];
+  int hk[2], sp[2];
+  uint32_t word;         // the bitmap's current word
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(P_END + sizeof(PromptShared) <= 227 * 1024, "shared memory budget");
+
+// Asks for a CTA of this grid that has not started; the answer lands in `at` and
+// completes 16 bytes on `b`.
+__device__ __forceinline__ void take_cta(uint32_t at, uint32_t b) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(at),
+      "r"(b)
+      : "memory");
+}
+// The taken CTA's blockIdx.x, or -1: none was left.
+__device__ __forceinline__ int taken_cta(uint32_t at) {
+  uint32_t some, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(some), "=r"(x)
+      : "r"(at)
+      : "memory");
+  return some ? (int)x : -1;
+}
+
+__global__ void __launch_bounds__(P_WARPS * 32, 1)
+    prompt_paged_kernel(const __grid_constant__ CUtensorMap tm_q,
+                        const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ ChunkArgs a, const int q_box_tokens) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  PromptShared &sh = *reinterpret_cast<PromptShared *>(smem_raw + P_END);
+  const uint32_t base = smem_u32(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (base & 1023u) {  // the swizzled layouts need a 1024-byte aligned base
+    if (tid == 0) atomicOr(a.err, kErrLayout);
+    return;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge waits for this grid's end)
+  volatile int *abort = &sh.abort;
+  auto bar = [&](uint64_t *b) { return smem_u32(b); };
+  auto wait = [&](uint64_t *b, unsigned phase) {
+    return mbar_wait_shared(smem_u32(b), phase & 1, abort, a.err);
+  };
+  auto wait_warp = [&](uint64_t *b, unsigned phase) {
+    return __all_sync(0xffffffffu, mbar_wait_shared(smem_u32(b), phase & 1, abort, a.err));
+  };
+
+  Producer pages;  // of the two producer warps
+  TileInfo found{};  // the key producer's first tile
+  int unit = (int)blockIdx.x;
+  if (warp == WARP_K) {
+    found = producer_tile(a, pages, unit / a.n_splits / a.Hkv, unit % a.n_splits,
+                          unit / a.n_splits % a.Hkv, lane);
+  } else if (warp == WARP_PV && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    mbar_init(bar(&sh.next_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(&sh.tile_full[i]), 1);
+      mbar_init(bar(&sh.tile_empty[i]), P_WARPS - 1);
+      mbar_init(bar(&sh.q_full[i]), 1);
+      mbar_init(bar(&sh.l_full[i]), NQ);
+    }
+    mbar_init(bar(&sh.v_tail), 1);
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(bar(&sh.ready[i]), 2);  // the key tile, the S buffer
+      mbar_init(bar(&sh.qk_done[i]), 1);
+    }
+    for (int i = 0; i < NS; ++i) mbar_arrive(bar(&sh.ready[i]));  // S buffers free at first
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(bar(&sh.v_full[i]), 1);
+      mbar_init(bar(&sh.v_empty[i]), 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bar(&sh.p_full[i]), NQ);
+      mbar_init(bar(&sh.pv_done[i]), 1);
+    }
+    for (int i = 0; i < NDEC; ++i) {
+      mbar_init(bar(&sh.dec_full[i]), 1);
+      mbar_init(bar(&sh.dec_read[i]), 2 + NQ);  // both value warps, the exponential warps
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == WARP_MMA) tmem_alloc(smem_u32(&sh.tmem_base), TMEM_COLS);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;
+  if (blockIdx.x == 0 && warp == WARP_PV) check_batch(a, lane);
+
+  if (warp == WARP_K) {
+    // ------------------------------------------ tiles; queries and keys --
+    fence_proxy_async_smem();
+    const uint64_t once = policy_evict_first();
+    unsigned it = 0, g = 0, asked = 0;
+    auto ask = [&]() {
+      if (lane == 0) {
+        mbar_expect_tx(bar(&sh.next_full), 16);
+        take_cta(smem_u32(&sh.next), bar(&sh.next_full));
+      }
+      __syncwarp();
+      ++asked;
+    };
+#pragma unroll 1
+    while (true) {
+      const int sp = unit % a.n_splits, hk = unit / a.n_splits % a.Hkv;
+      if (asked) found = producer_tile(a, pages, unit / a.n_splits / a.Hkv, sp, hk, lane);
+      // As late as may be, so that the last CTAs share what is left: with the last
+      // keys that the ring can take.
+      const int ask_at = max(0, found.nb - PK);
+      if (found.nb == 0) ask();
+      if (found.s >= 0 && found.nb == 0) {
+        // No visible key: O = 0, LSE = -inf (one split), or a partial of no weight.
+        const int rows = found.ntok * a.G;
+#pragma unroll 1
+        for (int i = lane; i < rows * (D / 8); i += 32) {
+          const int r = i / (D / 8);
+          const int64_t orow = (int64_t)(found.tok0 + r / a.G) * a.Hq + hk * a.G + r % a.G;
+          if (a.n_splits == 1)
+            reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + orow * D)[i % (D / 8)] =
+                make_uint4(0, 0, 0, 0);
+          if (i % (D / 8) == 0)
+            (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] = -INFINITY;
+        }
+      } else if (found.s >= 0) {
+        const unsigned slot = it & 1;
+        if (it >= 2 && !wait_warp(&sh.tile_empty[slot], (it >> 1) - 1)) break;
+        if (lane == 0) {
+          sh.tile[slot] = found;
+          sh.hk[slot] = hk;
+          sh.sp[slot] = sp;
+          mbar_arrive(bar(&sh.tile_full[slot]));
+          mbar_expect_tx(bar(&sh.q_full[slot]), 2 * 128 * a.G * q_box_tokens);
+          const uint32_t dst = base + P_Q + slot * TILE_BYTES;
+          tma_load_3d(dst, &tm_q, bar(&sh.q_full[slot]), 0, hk * a.G, found.tok0, once);
+          tma_load_3d(dst + HALF_BYTES, &tm_q, bar(&sh.q_full[slot]), 64, hk * a.G, found.tok0, once);
+        }
+        __syncwarp();
+        ++it;
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < found.nb; ++c, ++g) {
+          if (c == ask_at) ask();
+          ok = g < PK || wait_warp(&sh.qk_done[(g - PK) % NR], (g - PK) / NR);
+          if (!ok) break;
+          load_block_here<kKvBf16>(a, pages, &tm_k, false, found.j0 + c,
+                                   base + P_K + (g % PK) * TILE_BYTES, bar(&sh.ready[g % NR]), lane);
+        }
+        if (__any_sync(0xffffffffu, pages.bad) && lane == 0) atomicOr(a.err, kErrBadArg);
+        if (!ok) break;
+      }
+      if (!wait_warp(&sh.next_full, asked - 1)) break;
+      unit = taken_cta(smem_u32(&sh.next));
+      __syncwarp();
+      fence_proxy_async_smem();
+      if (unit == 0) check_batch(a, lane);  // (that CTA's part)
+      if (unit < 0) {
+        const unsigned slot = it & 1;
+        if (it >= 2 && !wait_warp(&sh.tile_empty[slot], (it >> 1) - 1)) break;
+        if (lane == 0) {
+          sh.tile[slot].s = -1;
+          mbar_arrive(bar(&sh.tile_full[slot]));
+        }
+        break;
+      }
+    }
+    if (lane == 0) {
+      // Drain: the last answer and the last load of each slot have landed before exit.
+      if (asked) mbar_wait_drain(bar(&sh.next_full), (asked - 1) & 1);
+#pragma unroll 1
+      for (unsigned i = it < 2 ? 0 : it - 2; i < it; ++i) mbar_wait_drain(bar(&sh.q_full[i & 1]), (i >> 1) & 1);
+#pragma unroll 1
+      for (unsigned i = g < PK ? 0 : g - PK; i < g; ++i) mbar_wait_drain(bar(&sh.ready[i % NR]), (i / NR) & 1);
+    }
+  } else if (warp == WARP_V) {
+    // ------------------------------------------------------ value producer --
+    fence_proxy_async_smem();
+    unsigned vi = 0, g = 0, tails = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (unsigned it = 0; ok; ++it) {
+      if (!wait_warp(&sh.tile_full[it & 1], it >> 1)) break;
+      const TileInfo x = sh.tile[it & 1];
+      if (x.s < 0) break;
+      const bool dense = x.ln_lam == -INFINITY;
+      producer_at(a, pages, x, sh.hk[it & 1], lane);
+#pragma unroll 1
+      for (int c = 0; c < x.nb; ++c, ++g) {
+        // A dense tile keeps every block: its values need no decision.
+        if (!dense) {
+          ok = wait_warp(&sh.dec_full[g % NDEC], g / NDEC);
+          if (!ok) break;
+          const int keep = sh.dec[g % NDEC];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&sh.dec_read[g % NDEC]));
+          if (!keep) continue;
+        }
+        const int j = x.j0 + c;
+        const unsigned s = vi % NV;
+        ok = vi < NV || wait_warp(&sh.v_empty[s], vi / NV - 1);
+        if (!ok) break;
+        const uint32_t dst = base + P_V + s * TILE_BYTES;
+        const int left = x.kv - j * BN;  // rows of the block below kv
+        load_block_here<kKvBf16>(a, pages, &tm_v, true, j, dst,
+                                 bar(left < BN ? &sh.v_tail : &sh.v_full[s]), lane);
+        if (left < BN) {  // the last block: zero the rows at or past kv
+          ok = wait_warp(&sh.v_tail, tails++);
+          if (!ok) break;
+#pragma unroll 1
+          for (int i = lane; i < (BN - left) * 16; i += 32)
+            st_shared_v4(dst + (i & 8 ? HALF_BYTES : 0) + (left + (i >> 4)) * 128 + (i & 7) * 16, 0, 0,
+                         0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&sh.v_full[s]));
+        }
+        ++vi;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&sh.tile_empty[it & 1]));
+    }
+    if (lane == 0) {
+      if (tails) mbar_wait_drain(bar(&sh.v_tail), (tails - 1) & 1);
+#pragma unroll 1
+      for (unsigned i = vi < NV ? 0 : vi - NV; i < vi; ++i) mbar_wait_drain(bar(&sh.v_full[i % NV]), (i / NV) & 1);
+    }
+  } else if (warp == WARP_MMA || warp == WARP_MMA2) {
+    // ------------------------------------------------------ Q.K^T issuers --
+    const unsigned mine = warp == WARP_MMA ? 0 : 1;
+    unsigned g0 = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (unsigned it = 0; ok; ++it) {
+      if (!wait_warp(&sh.tile_full[it & 1], it >> 1)) break;
+      const int s = sh.tile[it & 1].s, nb = sh.tile[it & 1].nb;
+      if (s < 0 || !wait_warp(&sh.q_full[it & 1], it >> 1)) break;
+      fence_after_sync();
+      const uint64_t qdesc = kmajor_base(base + P_Q + (it & 1) * TILE_BYTES);
+#pragma unroll 1
+      for (unsigned g = g0 + ((g0 ^ mine) & 1); g < g0 + nb; g += 2) {
+        ok = wait_warp(&sh.ready[g % NR], g / NR);
+        if (!ok) break;
+        fence_after_sync();
+        if (lane == 0) {
+          const uint64_t kd = kmajor_base(base + P_K + (g % PK) * TILE_BYTES);
+          const uint32_t d_s = tmem + (g % NS) * BN;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16_ss(d_s, qdesc + kmajor_step(kk), kd + kmajor_step(kk), IDESC_QK, kk > 0);
+          mma_commit(bar(&sh.qk_done[g % NR]));
+        }
+        __syncwarp();
+      }
+      g0 += nb;
+      if (lane == 0) mbar_arrive(bar(&sh.tile_empty[it & 1]));
+    }
+  } else if (warp == WARP_PV) {
+    // ---------------------------------------------------------- P.V issuer --
+    if (lane == 0) {
+      unsigned kc = 0, g = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (unsigned it = 0; ok; ++it) {
+        if (!wait(&sh.tile_full[it & 1], it >> 1)) break;
+        const int s = sh.tile[it & 1].s, nb = sh.tile[it & 1].nb;
+        if (s < 0) break;
+        bool first = true;
+#pragma unroll 1
+        for (int c = 0; c < nb; ++c, ++g) {
+          ok = wait(&sh.dec_full[g % NDEC], g / NDEC);
+          if (!ok) break;
+          const int keep = sh.dec[g % NDEC];
+          mbar_arrive(bar(&sh.dec_read[g % NDEC]));
+          if (!keep) continue;
+          const unsigned pb = kc % NS, vs = kc % NV;
+          // O is the last tile's until its epilogue has read it.
+          if (first && it) ok = wait(&sh.tile_empty[(it - 1) & 1], (it - 1) >> 1);
+          ok = ok && wait(&sh.p_full[pb], kc / NS) && wait(&sh.v_full[vs], kc / NV);
+          if (!ok) break;
+          fence_after_sync();
+          const uint32_t pt = tmem + (g % NS) * BN;
+          const uint64_t vd = vmajor_base(base + P_V + vs * TILE_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_bf16_ts(tmem + TMEM_O, pt + kk * 8, vd + vmajor_step(kk), IDESC_PV,
+                        kk > 0 || !first ? 1u : 0u);
+          mma_commit(bar(&sh.v_empty[vs]));
+          mma_commit(bar(&sh.ready[(g + NS) % NR]));  // S buffer free for block g + NS
+          mma_commit(bar(&sh.pv_done[pb]));
+          ++kc;
+          first = false;
+        }
+        mbar_arrive(bar(&sh.tile_empty[it & 1]));
+      }
+    }
+  } else {
+    // ------------------------------------------------- deciders / exponentials --
+    const bool decider = warp < NQ;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // TMEM lane, row of the tile
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const float sl2 = a.scale * kLog2e;
+    unsigned g = 0, kc = 0;  // blocks; of those, kept
+    bool ok = true;
+#pragma unroll 1
+    for (unsigned it = 0;; ++it) {
+      ok = ok && wait_warp(&sh.tile_full[it & 1], it >> 1);
+      if (decider ? bar_red_or(kTileBarrier, NQ * 32, !ok) : !ok) break;  // (deciders meet at votes)
+      // Read again where it is used: the loops need the registers.
+      const TileInfo &x = sh.tile[it & 1];
+      if (x.s < 0) break;
+      const int nb = x.nb;
+      const int nq = (x.ntok * a.G + 31) / 32;  // quarters that have rows
+      const bool valid = r < x.ntok * a.G;
+      if (quarter >= nq) {
+        // A quarter without rows has no decider; its exponential warp follows the
+        // decisions, to keep count.
+        if (decider) {
+          g += nb;
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < nb && ok; ++c, ++g) {
+            ok = wait_warp(&sh.dec_full[g % NDEC], g / NDEC);
+            const int keep = sh.dec[g % NDEC];
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(&sh.dec_read[g % NDEC]));
+              if (keep) mbar_arrive(bar(&sh.p_full[kc % NS]));
+            }
+            if (keep) ++kc;
+          }
+          if (lane == 0) mbar_arrive(bar(&sh.l_full[it & 1]));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh.tile_empty[it & 1]));
+        continue;
+      }
+      if (decider) {
+        const bool dense = x.ln_lam == -INFINITY;
+        const int tok = r / a.G;
+        const int key0 = x.j0 * BN;
+        // The row sees keys below key0 + limit; the tile's smallest limit.
+        const int limit = (a.causal && valid ? x.pos0 + tok + 1 : x.kv) - key0;
+        const int min_limit = (a.causal ? x.pos0 + 1 : x.kv) - key0;
+        const float c2 = x.ln_lam * kLog2e;
+        float m2 = -INFINITY;  // running max (log2 units)
+#pragma unroll 1
+        for (int c = 0; c < nb; ++c, ++g) {
+          // After a failed wait the loop still runs to its end, so that the
+          // warps meet the vote barrier equally often.
+          if (ok) ok = wait_warp(&sh.qk_done[g % NR], g / NR);
+          bool keep_vote = false;
+          if (ok) {
+            fence_after_sync();
+            const uint32_t sa = lane_base + (g % NS) * BN;
+            if (c * BN + BN > min_limit) mask_block_tmem(sa, limit - c * BN, 4);
+            float mt = -INFINITY;
+#pragma unroll 1
+            for (int hh = 0; hh < 2; ++hh) {
+              uint32_t x0[32], x1[32];
+              tmem_ld32(sa + 64 * hh, x0);
+              tmem_ld32(sa + 64 * hh + 32, x1);
+              tmem_wait_ld_regs(x0);
+              tmem_wait_ld_regs(x1);
+              mt = fmax3(mt, chunk_max(x0), chunk_max(x1));
+            }
+            const float pm2 = mt * sl2;
+            // With ln(lambda) < 0, "rowmax - m_new < c" is "rowmax - m_old < c".
+            const float diff = mt == -INFINITY ? -INFINITY : pm2 - m2;
+            keep_vote = dense || !__all_sync(0xffffffffu, !valid || diff < c2 || mt == -INFINITY);
+            m2 = fmaxf(m2, pm2);
+            sh.mdec[g % NS][r] = m2;
+            fence_before_sync();  // this warp's reads of S are complete
+          }
+          const bool keep = bar_red_or(kDeciderBarrier, nq * 32, keep_vote);
+          if (!ok) continue;
+          if (lane == 0 && warp == (nq == NQ ? c & (NQ - 1) : 0)) {
+            if (!keep) mbar_arrive(bar(&sh.ready[(g + NS) % NR]));  // its S buffer is free
+            if (g < NDEC || wait(&sh.dec_read[g % NDEC], g / NDEC - 1)) {
+              sh.dec[g % NDEC] = keep ? 1 : 0;
+              mbar_arrive(bar(&sh.dec_full[g % NDEC]));
+              if (dense) mbar_arrive(bar(&sh.dec_read[g % NDEC]));  // the value producer does not read it
+            }
+          }
+          if (tid == 0 && a.bits) {
+            const uint32_t word = ((c & 31) ? sh.word : 0u) | (keep ? 0u : 1u << (c & 31));
+            sh.word = word;
+            if ((c & 31) == 31 || c == nb - 1) {
+              const int64_t tile = ((int64_t)x.s * a.Hkv + sh.hk[it & 1]) * a.n_t + x.t;
+              a.bits[(tile * a.n_splits + sh.sp[it & 1]) * a.words + (c >> 5)] = word;
+            }
+          }
+        }
+      } else {
+        float mref = -INFINITY, l = 0.f;
+        const unsigned kc0 = kc;
+#pragma unroll 1
+        for (int c = 0; c < nb; ++c, ++g) {
+          ok = wait_warp(&sh.dec_full[g % NDEC], g / NDEC);
+          if (!ok) break;
+          const int keep = sh.dec[g % NDEC];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&sh.dec_read[g % NDEC]));
+          if (!keep) continue;
+          fence_after_sync();
+          const uint32_t sa = lane_base + (g % NS) * BN;  // masked by the deciders
+          const float mnew = sh.mdec[g % NS][r];
+          bool rescale = false;
+          float alpha = 1.f;
+          if (mref == -INFINITY) {
+            mref = mnew;
+          } else if (valid && mnew > mref + kRescaleLog2) {
+            alpha = ex2(mref - mnew);
+            mref = mnew;
+            rescale = true;
+          }
+          // A row without a visible key so far has only -inf scores: P = 0.
+          const float nref = mref == -INFINITY ? 0.f : -mref;
+          const uint64_t sl2x2 = f2(sl2, sl2), negref2 = f2(nref, nref);
+          uint64_t acc2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll 1
+          for (int hh = 0; hh < 2; ++hh) {
+            // The P pairs of keys [64 hh, 64 hh + 64) land in columns [32 hh,
+            // 32 hh + 32), whose scores this or the previous half has loaded.
+            uint32_t s0[32], s1[32], pk[32];
+            tmem_ld32(sa + 64 * hh, s0);
+            tmem_ld32(sa + 64 * hh + 32, s1);
+            tmem_wait_ld_regs(s0);
+            tmem_wait_ld_regs(s1);
+            chunk_exp<false>(s0, sl2x2, negref2, acc2, pk);
+            chunk_exp<false>(s1, sl2x2, negref2, acc2, pk + 16);
+            tmem_st32(sa + 32 * hh, pk);
+          }
+          tmem_wait_st();
+          float acc[4];
+          f2_split(acc2[0], acc[0], acc[1]);
+          f2_split(acc2[1], acc[2], acc[3]);
+          l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+          if (__any_sync(0xffffffffu, rescale) && kc > kc0) {
+            ok = wait_warp(&sh.pv_done[(kc - 1) % NS], (kc - 1) / NS);
+            if (!ok) break;
+            fence_after_sync();
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t o[32];
+              const uint32_t oa = lane_base + TMEM_O + cc * 32;
+              tmem_ld32(oa, o);
+              tmem_wait_ld_regs(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(oa, o);
+            }
+            tmem_wait_st();
+          }
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&sh.p_full[kc % NS]));
+          ++kc;
+        }
+        if (ok && kc > kc0) ok = wait_warp(&sh.pv_done[(kc - 1) % NS], (kc - 1) / NS);
+        // No kept block: O was never written.
+        sh.sum[r] = kc > kc0 ? l : 0.f;
+        sh.ref[r] = mref;
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&sh.l_full[it & 1]));
+      }
+
+      // ---- epilogue: deciders take O columns [0,64), exponential warps [64,128)
+      if (ok) ok = wait_warp(&sh.l_full[it & 1], it >> 1);
+      if (ok) {
+        fence_after_sync();
+        const int tok = r / a.G, sp = sh.sp[it & 1], rows = x.ntok * a.G;
+        const int64_t orow = (int64_t)(x.tok0 + tok) * a.Hq + sh.hk[it & 1] * a.G + (r - tok * a.G);
+        const int col0 = decider ? 0 : 64;
+        const float lrow = sh.sum[r], lref = sh.ref[r];
+        const bool none = lrow == 0.f;  // no key kept for this row: the accumulator may hold anything
+        const float inv = none ? 0.f : 1.f / lrow;
+        // The rows leave through 4 KB of the tile's queries a warp (no longer needed): a
+        // lane's row in 16-byte pieces, then 128-byte runs of four rows an instruction.
+        const uint32_t stage = base + P_Q + (it & 1) * TILE_BYTES + warp * 4096;
+        auto put_row = [&](int piece, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+          st_shared_v4(stage + lane * 128 + ((piece ^ (lane & 7)) * 16), v0, v1, v2, v3);
+        };
+        auto store_rows = [&](uint8_t *out, int64_t row_bytes) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int l2 = i * 4 + (lane >> 3), piece = lane & 7;
+            const int64_t at = __shfl_sync(0xffffffffu, orow, l2);
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(stage + l2 * 128 + ((piece ^ (l2 & 7)) * 16))
+                         : "memory");
+            if (quarter * 32 + l2 < rows) *reinterpret_cast<uint4 *>(out + at * row_bytes + piece * 16) = v;
+          }
+          __syncwarp();
+        };
+#pragma unroll 1
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t o[32];
+          const int col = col0 + cc * 32;
+          tmem_ld32(lane_base + TMEM_O + col, o);
+          tmem_wait_ld_regs(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+          if (a.n_splits == 1) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              put_row(cc * 4 + q, pack_bf16x2(__uint_as_float(o[8 * q]), __uint_as_float(o[8 * q + 1])),
+                      pack_bf16x2(__uint_as_float(o[8 * q + 2]), __uint_as_float(o[8 * q + 3])),
+                      pack_bf16x2(__uint_as_float(o[8 * q + 4]), __uint_as_float(o[8 * q + 5])),
+                      pack_bf16x2(__uint_as_float(o[8 * q + 6]), __uint_as_float(o[8 * q + 7])));
+            if (cc == 1) store_rows((uint8_t *)a.o + col0 * 2, D * 2);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              put_row(q, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            store_rows((uint8_t *)(a.o_part + (int64_t)sp * D + col), (int64_t)a.n_splits * D * 4);
+          }
+        }
+        if (valid && !decider)
+          (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] =
+              none ? -INFINITY : lref * kLn2 + logf(lrow);
+      }
+      fence_proxy_async_smem();  // the staged rows, before the next queries
+      fence_before_sync();       // and this warp's reads of O
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&sh.tile_empty[it & 1]));
+    }
+  }
+
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    fence_after_sync();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
 // Merge of the split partials: LSE = ln sum_s exp(LSE_s), O = sum_s
 // exp(LSE_s - LSE) O_s, splits without a key (LSE_s = -inf, O_s not written)
 // left out.  One warp a row (token, query head), four columns a lane; rows
@@ -1229,11 +1815,31 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
   return cudaGetLastError();
 }
 
+cudaError_t launch_prompt(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                          const ChunkArgs &a, int q_tokens, unsigned grid, cudaStream_t s) {
+  constexpr uint32_t smem = P_END + ((sizeof(PromptShared) + 15) / 16) * 16;
+  const cudaError_t e = cudaFuncSetAttribute(prompt_paged_kernel,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  prompt_paged_kernel<<<grid, P_WARPS * 32, smem, s>>>(mq, mk, mv, a, q_tokens);
+  return cudaGetLastError();
+}
+
 template <int FMT>
 cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                        const ChunkArgs &a, int q_tokens, unsigned grid, cudaStream_t s) {
-  return a.G * q_tokens <= 32 ? launch_one<FMT, true>(mq, mk, mv, a, q_tokens, grid, s)
-                              : launch_one<FMT, false>(mq, mk, mv, a, q_tokens, grid, s);
+  if (a.G * q_tokens <= 32) return launch_one<FMT, true>(mq, mk, mv, a, q_tokens, grid, s);
+  if constexpr (FMT == kKvBf16) {
+    // CTAs that stay pay where there are more tiles than SMs and these are short:
+    // whole prompts of 256 tokens (64 of them) 137 us against 209, of 1024 (16) 203
+    // and 270, of 4096 (4) 479 and 529, of 8192 (2) 835 and 868; a chunk of 4096 on
+    // 16384, a hundred blocks a tile, 697 and 671 (a loop over tiles costs the loop
+    // over blocks some registers).
+    const int64_t keys = (int64_t)a.max_kv - a.max_chunk / 2;  // of a middle tile
+    if (grid > 152 && keys < (int64_t)64 * BN * a.n_splits)
+      return launch_prompt(mq, mk, mv, a, q_tokens, grid, s);
+  }
+  return launch_one<FMT, false>(mq, mk, mv, a, q_tokens, grid, s);
 }
 
 }  // namespace

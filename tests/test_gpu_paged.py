@@ -477,6 +477,111 @@ def test_decode_of_more_pieces_than_ctas_with_bad_device_arguments(n_splits):
         assert torch.allclose(o[s].float(), want[s].float(), atol=0.02)
 
 
+PROMPTS = [
+    # (sequences, longest chunk, tokens before it, Hkv, G, splits): more tiles than SMs
+    (40, 200, 300, 2, 4, 1),
+    (30, 150, 500, 2, 7, 3),    # 126 rows a tile, splits without a block
+    (10, 40, 90, 1, 128, 1),    # a tile a token
+    (70, 60, 0, 2, 16, 2),
+    (100, 33, 100, 4, 3, 1),    # one tile a sequence, partly filled quarters
+]
+
+
+def prompts(case):
+    n, longest, before, Hkv, G, n_splits = PROMPTS[case]
+    g = np.random.default_rng(case)
+    chunks = [int(c) for c in g.integers(0, longest + 1, n)]
+    chunks[1], chunks[2] = longest, 0
+    lens = [int(c + g.integers(0, before + 1)) for c in chunks]
+    lens[3], lens[4] = 0, max(0, chunks[4] - 2)  # an empty cache; a chunk longer than its cache
+    tt = 128 // G
+    assert sum(-(-c // tt) for c in chunks) * Hkv * n_splits > 152
+    return chunks, lens, Hkv, G, n_splits
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", range(len(PROMPTS)))
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_of_many_tiles(fmt, case, causal):
+    chunks, lens, Hkv, G, n = prompts(case)
+    kv, table = cache_of(fmt, lens, 32, Hkv, case)
+    lams = [0.0] * len(lens)
+    q, out = attend(kv, table, chunks, lens, Hkv * G, lams, causal, n, case)
+    check(kv, table, chunks, lens, Hkv * G, lams, q, out, causal, n)
+    again = attend(kv, table, chunks, lens, Hkv * G, lams, causal, n, q=q)[1]
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+@pytest.mark.parametrize("case", range(len(PROMPTS)))
+def test_prompts_of_many_tiles_skip(case):
+    chunks, lens, Hkv, G, n = prompts(case)
+    kv, table = cache_of("bf16", lens, 64, Hkv, case, sink=1.0)
+    lams = [(0.0, 0.3, 0.6)[s % 3] for s in range(len(lens))]
+    g = np.random.default_rng(case)
+    q = torch.from_numpy(g.standard_normal((sum(chunks), Hkv * G, 128)) + 0.7).to(DEV, torch.bfloat16)
+    q, out = attend(kv, table, chunks, lens, Hkv * G, lams, True, n, q=q)
+    check(kv, table, chunks, lens, Hkv * G, lams, q, out, True, n)
+
+
+def test_prompts_of_many_tiles_with_bad_device_arguments():
+    n, Hkv, Hq, C = 60, 2, 8, 70
+    lens = [C + s for s in range(n)]
+    kv, table = cache_of("bf16", lens, 16, Hkv, 15)
+    q = torch.randn(n * C + 5, Hq, 128, device=DEV).to(torch.bfloat16)
+    cu, kl, lam = i32(range(0, n * C + 1, C)), i32(lens), torch.zeros(n, device=DEV)
+    args = dict(max_chunk=C, max_kv=max(lens), n_splits=1)
+    want, wl, _ = bs.attn_skip_chunk_paged(kv, q, cu, kv_len=kl, page_table=table, lambdas=lam, **args)
+    bs.attn_skip_last_device_error()
+    bad_cu, bad_kl, bad_t, bad_lam = cu.clone(), kl.clone(), table.clone(), lam.clone()
+    bad_cu[31:] += 1                     # sequence 30: 71 tokens, 70 allowed
+    bad_kl[7], bad_kl[50] = max(lens) + 1, -1
+    bad_t[3, 2], bad_t[3, 4] = -4, 10 ** 6
+    bad_lam[9] = float("nan")
+    o, lse = torch.full_like(want, 2.0), torch.full_like(wl, 2.0)
+    bs.attn_skip_chunk_paged(kv, q, bad_cu, kv_len=bad_kl, page_table=bad_t, lambdas=bad_lam,
+                             out=(o, lse, None), **args)
+    with pytest.raises(bs.AttnSkipError) as e:
+        bs.attn_skip_last_device_error()
+    assert e.value.status == bs.ATTN_EINVAL
+    for s in (7, 50):
+        r = slice(s * C + (s > 30), (s + 1) * C + (s > 30))
+        assert (o[r] == 0).all() and torch.isneginf(lse[r]).all()
+    assert (o[30 * C:31 * C + 1] == 2).all() and (lse[30 * C:31 * C + 1] == 2).all()
+    assert (o[n * C + 1:] == 2).all() and (lse[n * C + 1:] == 2).all()
+    for s in (0, 1, 2, 4, 9, 29):
+        assert torch.equal(o[s * C:(s + 1) * C], want[s * C:(s + 1) * C])
+
+
+@pytest.mark.parametrize("fmt,n,C,L", [("bf16", 40, 100, 400), ("nvfp4", 64, 1, 1500)])
+def test_large_batches_on_two_streams_and_in_a_graph(fmt, n, C, L):
+    """Grids whose CTAs take over one another's work, or share it out, next to
+    each other."""
+    kv, table = cache_of(fmt, [L] * n, 16, 2, 3)
+    cu, kl, lam = i32(range(0, n * C + 1, C)), i32([L] * n), torch.zeros(n, device=DEV)
+    qs = [torch.randn(n * C, 8, 128, device=DEV).to(torch.bfloat16) for _ in range(2)]
+
+    def call(q, **kw):
+        return bs.attn_skip_chunk_paged(kv, q, cu, C, kl, L, table, lam, n_splits=3, **kw)[:2]
+
+    want = [call(q) for q in qs]
+    bs.attn_skip_last_device_error()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[call(q, stream=st) for _ in range(3)] for q, st in zip(qs, streams) for _ in range(2)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = [call(q) for q in qs]
+    for _ in range(2):
+        graph.replay()
+    bs.attn_skip_last_device_error()
+    for i, calls in enumerate(got):
+        for o, lse in calls:
+            assert torch.equal(o, want[i // 2][0]) and torch.equal(lse, want[i // 2][1])
+    for (o, lse), (wo, wl) in zip(captured, want):
+        assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_chunk_scale_and_large_values(fmt):
     """An explicit score scale, and rows whose scale byte needs a second bf16
