@@ -1154,6 +1154,9 @@ constexpr uint32_t P_Q = 0, P_K = PQ * TILE_BYTES, P_V = P_K + PK * TILE_BYTES;
 constexpr uint32_t P_END = P_V + NV * TILE_BYTES;
 constexpr int P_WARPS = 13;
 constexpr int kTileBarrier = 2;
+// In the place of a row's first LSE: its outputs are written (a NaN that no
+// computation gives).
+constexpr uint32_t kWholeRow = 0x7fc5a5a5u;
 
 struct PromptShared {
   uint4 next;            // answer of the cluster launch control
@@ -1172,7 +1175,7 @@ struct PromptShared {
   float mdec[NS][BM];    // running max after the buffer's block (log2 units)
   float sum[BM], ref[BM];  // row sums and references for the epilogue
   TileInfo tile[2];
-  int hk[2], sp[2];
+  int hk[2], sp[2];      // KV head; split, -1: the rows go to the outputs
   uint32_t word;         // the bitmap's current word
   uint32_t tmem_base;
   int abort;
@@ -1202,6 +1205,8 @@ __device__ __forceinline__ int taken_cta(uint32_t at) {
   return some ? (int)x : -1;
 }
 
+// SPLIT: n_splits > 1.
+template <bool SPLIT>
 __global__ void __launch_bounds__(P_WARPS * 32, 1)
     prompt_paged_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
@@ -1229,8 +1234,7 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
   TileInfo found{};  // the key producer's first tile
   int unit = (int)blockIdx.x;
   if (warp == WARP_K) {
-    found = producer_tile(a, pages, unit / a.n_splits / a.Hkv, unit % a.n_splits,
-                          unit / a.n_splits % a.Hkv, lane);
+    found = producer_tile(a, pages, unit / a.Hkv, 0, unit % a.Hkv, lane);
   } else if (warp == WARP_PV && lane == 0) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
@@ -1286,32 +1290,29 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
     };
 #pragma unroll 1
     while (true) {
-      const int sp = unit % a.n_splits, hk = unit / a.n_splits % a.Hkv;
-      if (asked) found = producer_tile(a, pages, unit / a.n_splits / a.Hkv, sp, hk, lane);
-      // As late as may be, so that the last CTAs share what is left: with the last
-      // keys that the ring can take.
-      const int ask_at = max(0, found.nb - PK);
-      if (found.nb == 0) ask();
-      if (found.s >= 0 && found.nb == 0) {
-        // No visible key: O = 0, LSE = -inf (one split), or a partial of no weight.
-        const int rows = found.ntok * a.G;
+      const int hk = unit % a.Hkv;
+      if (asked) found = producer_tile(a, pages, unit / a.Hkv, 0, hk, lane);
+      // The tile's splits, one after the other; those without a block are a partial of
+      // no weight (where there is one split: O = 0, LSE = -inf).  A dense tile needs no
+      // cut: its rows go to the outputs, and the merge leaves them alone.
+      const int seen = a.causal ? max(0, found.pos0 + found.ntok) : found.kv;
+      const int blocks = (seen + BN - 1) / BN, rows = found.s >= 0 ? found.ntok * a.G : 0;
+      const bool whole = found.ln_lam == -INFINITY;
+      const int run = !SPLIT || whole ? blocks : a.bps;
+      const int splits = !rows || !blocks ? 0 : SPLIT ? (blocks + run - 1) / run : 1;
+      if (splits == 0) ask();
+      bool ok = true;
 #pragma unroll 1
-        for (int i = lane; i < rows * (D / 8); i += 32) {
-          const int r = i / (D / 8);
-          const int64_t orow = (int64_t)(found.tok0 + r / a.G) * a.Hq + hk * a.G + r % a.G;
-          if (a.n_splits == 1)
-            reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + orow * D)[i % (D / 8)] =
-                make_uint4(0, 0, 0, 0);
-          if (i % (D / 8) == 0)
-            (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] = -INFINITY;
-        }
-      } else if (found.s >= 0) {
+      for (int sp = 0; sp < splits && ok; ++sp, ++it) {
         const unsigned slot = it & 1;
-        if (it >= 2 && !wait_warp(&sh.tile_empty[slot], (it >> 1) - 1)) break;
+        found.j0 = sp * run;
+        found.nb = min(blocks - found.j0, run);
+        ok = it < 2 || wait_warp(&sh.tile_empty[slot], (it >> 1) - 1);
+        if (!ok) break;
         if (lane == 0) {
           sh.tile[slot] = found;
           sh.hk[slot] = hk;
-          sh.sp[slot] = sp;
+          sh.sp[slot] = SPLIT && !whole ? sp : -1;
           mbar_arrive(bar(&sh.tile_full[slot]));
           mbar_expect_tx(bar(&sh.q_full[slot]), 2 * 128 * a.G * q_box_tokens);
           const uint32_t dst = base + P_Q + slot * TILE_BYTES;
@@ -1319,8 +1320,9 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
           tma_load_3d(dst + HALF_BYTES, &tm_q, bar(&sh.q_full[slot]), 64, hk * a.G, found.tok0, once);
         }
         __syncwarp();
-        ++it;
-        bool ok = true;
+        // The next CTA as late as may be, so that the last ones share what is left:
+        // with the last keys that the ring can take.
+        const int ask_at = sp == splits - 1 ? max(0, found.nb - PK) : -1;
 #pragma unroll 1
         for (int c = 0; c < found.nb; ++c, ++g) {
           if (c == ask_at) ask();
@@ -1329,8 +1331,23 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
           load_block_here<kKvBf16>(a, pages, &tm_k, false, found.j0 + c,
                                    base + P_K + (g % PK) * TILE_BYTES, bar(&sh.ready[g % NR]), lane);
         }
-        if (__any_sync(0xffffffffu, pages.bad) && lane == 0) atomicOr(a.err, kErrBadArg);
-        if (!ok) break;
+      }
+      if (__any_sync(0xffffffffu, pages.bad) && lane == 0) atomicOr(a.err, kErrBadArg);
+      if (!ok) break;
+      if (splits < (!SPLIT || whole ? 1 : a.n_splits)) {
+#pragma unroll 1
+        for (int r = lane; r < rows; r += 32) {
+          const int tok = r / a.G;
+          const int64_t orow = (int64_t)(found.tok0 + tok) * a.Hq + hk * a.G + (r - tok * a.G);
+          if constexpr (!SPLIT) {
+#pragma unroll 1
+            for (int i = 0; i < D / 8; ++i)
+              reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + orow * D)[i] = make_uint4(0, 0, 0, 0);
+          }
+          float *lse = SPLIT ? a.lse_part + orow * a.n_splits : a.lse + orow;
+#pragma unroll 1
+          for (int sp = splits; sp < (SPLIT ? a.n_splits : 1); ++sp) lse[sp] = -INFINITY;
+        }
       }
       if (!wait_warp(&sh.next_full, asked - 1)) break;
       unit = taken_cta(smem_u32(&sh.next));
@@ -1565,12 +1582,12 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
               if (dense) mbar_arrive(bar(&sh.dec_read[g % NDEC]));  // the value producer does not read it
             }
           }
-          if (tid == 0 && a.bits) {
+          if (tid == 0 && a.bits && !dense) {
             const uint32_t word = ((c & 31) ? sh.word : 0u) | (keep ? 0u : 1u << (c & 31));
             sh.word = word;
             if ((c & 31) == 31 || c == nb - 1) {
               const int64_t tile = ((int64_t)x.s * a.Hkv + sh.hk[it & 1]) * a.n_t + x.t;
-              a.bits[(tile * a.n_splits + sh.sp[it & 1]) * a.words + (c >> 5)] = word;
+              a.bits[(tile * a.n_splits + (SPLIT ? sh.sp[it & 1] : 0)) * a.words + (c >> 5)] = word;
             }
           }
         }
@@ -1653,7 +1670,7 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
       if (ok) ok = wait_warp(&sh.l_full[it & 1], it >> 1);
       if (ok) {
         fence_after_sync();
-        const int tok = r / a.G, sp = sh.sp[it & 1], rows = x.ntok * a.G;
+        const int tok = r / a.G, sp = SPLIT ? sh.sp[it & 1] : -1, rows = x.ntok * a.G;
         const int64_t orow = (int64_t)(x.tok0 + tok) * a.Hq + sh.hk[it & 1] * a.G + (r - tok * a.G);
         const int col0 = decider ? 0 : 64;
         const float lrow = sh.sum[r], lref = sh.ref[r];
@@ -1689,7 +1706,7 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-          if (a.n_splits == 1) {
+          if (sp < 0) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               put_row(cc * 4 + q, pack_bf16x2(__uint_as_float(o[8 * q]), __uint_as_float(o[8 * q + 1])),
@@ -1704,9 +1721,11 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
             store_rows((uint8_t *)(a.o_part + (int64_t)sp * D + col), (int64_t)a.n_splits * D * 4);
           }
         }
-        if (valid && !decider)
-          (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + sp] =
+        if (valid && !decider) {
+          (sp < 0 ? a.lse + orow : a.lse_part + orow * a.n_splits + sp)[0] =
               none ? -INFINITY : lref * kLn2 + logf(lrow);
+          if (SPLIT && sp < 0) a.lse_part[orow * a.n_splits] = __uint_as_float(kWholeRow);
+        }
       }
       fence_proxy_async_smem();  // the staged rows, before the next queries
       fence_before_sync();       // and this warp's reads of O
@@ -1726,50 +1745,62 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
 
 // Merge of the split partials: LSE = ln sum_s exp(LSE_s), O = sum_s
 // exp(LSE_s - LSE) O_s, splits without a key (LSE_s = -inf, O_s not written)
-// left out.  One warp a row (token, query head), four columns a lane; rows
-// behind the last sequence keep what they held.
-constexpr int MERGE_WARPS = 4;
+// left out.  A warp takes ROWS query heads of a token, one after the other, four
+// columns a lane; rows behind the last sequence keep what they held.  One row a warp
+// is quickest for a decode step; with many rows the search for the sequence, once a
+// row, was half the merge (16 prompts of 1024 tokens, 32 heads: 325 us in all with four
+// rows a warp, 365 with one).
+constexpr int MERGE_WARPS = 4, MERGE_ROWS = 4;
+template <int ROWS>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const ChunkArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * MERGE_WARPS + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  const unsigned unit = blockIdx.x * MERGE_WARPS + (threadIdx.x >> 5), groups = (a.Hq + ROWS - 1) / ROWS;
+  const unsigned tok = unit / groups, h0 = (unit - tok * groups) * ROWS;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
-  if (row >= (int64_t)a.total * a.Hq) return;
-  const int tok = (int)(row / a.Hq);
-  // A token outside every (valid) sequence has no partial.
-  int hi = a.n_seq, lo = 0;
-  while (lo < hi) {  // entries of cu[1..n] that are <= tok
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu_seqlens + mid + 1) <= tok) lo = mid + 1;
-    else hi = mid;
+  if (tok >= (unsigned)a.total) return;
+  // A token outside every (valid) sequence has no partial.  The number of entries of
+  // cu[1..n] that are <= tok, by 32 probes a round.
+  int lo = 0, hi = a.n_seq;
+  while (lo < hi) {
+    const int step = (hi - lo) / 33 + 1, at = lo + (lane + 1) * step;
+    const bool ge = at <= hi && __ldg(a.cu_seqlens + at) <= (int)tok;
+    const int c = __popc(__ballot_sync(0xffffffffu, ge));
+    lo += c * step;
+    hi = min(hi, lo + step - 1);
   }
   if (lo >= a.n_seq) return;
   const int c0 = __ldg(a.cu_seqlens + lo), c1 = __ldg(a.cu_seqlens + lo + 1);
-  if (c0 < 0 || c0 > tok || c1 - c0 > a.max_chunk || c1 > a.total) return;
-  const float *ls = a.lse_part + row * a.n_splits;
-  float m = -INFINITY;
+  if (c0 < 0 || c0 > (int)tok || c1 - c0 > a.max_chunk || c1 > a.total) return;
 #pragma unroll 1
-  for (int s = lane; s < a.n_splits; s += 32) m = fmaxf(m, ls[s]);
+  for (unsigned h = h0; h < h0 + ROWS && h < (unsigned)a.Hq; ++h) {
+    const int64_t row = (int64_t)tok * a.Hq + h;
+    const float *ls = a.lse_part + row * a.n_splits;
+    if (__float_as_uint(ls[0]) == kWholeRow) continue;
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int s = lane; s < a.n_splits; s += 32) m = fmaxf(m, ls[s]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float z = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4 *op = reinterpret_cast<const float4 *>(a.o_part + row * a.n_splits * D) + lane;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float z = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 *op = reinterpret_cast<const float4 *>(a.o_part + row * a.n_splits * D) + lane;
 #pragma unroll 4
-  for (int s = 0; s < a.n_splits; ++s) {
-    const float x = ls[s];
-    if (x == -INFINITY) continue;
-    const float w = expf(x - m);
-    const float4 v = op[s * (D / 4)];
-    z += w;
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
+    for (int s = 0; s < a.n_splits; ++s) {
+      const float x = ls[s];
+      if (x == -INFINITY) continue;
+      const float w = expf(x - m);
+      const float4 v = op[s * (D / 4)];
+      z += w;
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
+    }
+    const float inv = m == -INFINITY ? 0.f : 1.f / z;
+    reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.o + row * D)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : m + logf(z);
   }
-  const float inv = m == -INFINITY ? 0.f : 1.f / z;
-  reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.o + row * D)[lane] =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : m + logf(z);
 }
 
 // 4-D map over the rows of a bf16 page pool: (column, slot, head, page).
@@ -1815,20 +1846,21 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
   return cudaGetLastError();
 }
 
+template <bool SPLIT>
 cudaError_t launch_prompt(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                           const ChunkArgs &a, int q_tokens, unsigned grid, cudaStream_t s) {
   constexpr uint32_t smem = P_END + ((sizeof(PromptShared) + 15) / 16) * 16;
-  const cudaError_t e = cudaFuncSetAttribute(prompt_paged_kernel,
+  const cudaError_t e = cudaFuncSetAttribute(prompt_paged_kernel<SPLIT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  prompt_paged_kernel<<<grid, P_WARPS * 32, smem, s>>>(mq, mk, mv, a, q_tokens);
+  prompt_paged_kernel<SPLIT><<<grid, P_WARPS * 32, smem, s>>>(mq, mk, mv, a, q_tokens);
   return cudaGetLastError();
 }
 
 template <int FMT>
 cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
-                       const ChunkArgs &a, int q_tokens, unsigned grid, cudaStream_t s) {
-  if (a.G * q_tokens <= 32) return launch_one<FMT, true>(mq, mk, mv, a, q_tokens, grid, s);
+                       const ChunkArgs &a, int q_tokens, unsigned units, cudaStream_t s) {
+  if (a.G * q_tokens <= 32) return launch_one<FMT, true>(mq, mk, mv, a, q_tokens, units, s);
   if constexpr (FMT == kKvBf16) {
     // CTAs that stay pay where there are more tiles than SMs and these are short:
     // whole prompts of 256 tokens (64 of them) 137 us against 209, of 1024 (16) 203
@@ -1836,10 +1868,12 @@ cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
     // 16384, a hundred blocks a tile, 697 and 671 (a loop over tiles costs the loop
     // over blocks some registers).
     const int64_t keys = (int64_t)a.max_kv - a.max_chunk / 2;  // of a middle tile
+    const unsigned grid = units / a.n_splits;  // (a tile's splits go to one CTA)
     if (grid > 152 && keys < (int64_t)64 * BN * a.n_splits)
-      return launch_prompt(mq, mk, mv, a, q_tokens, grid, s);
+      return a.n_splits > 1 ? launch_prompt<true>(mq, mk, mv, a, q_tokens, grid, s)
+                            : launch_prompt<false>(mq, mk, mv, a, q_tokens, grid, s);
   }
-  return launch_one<FMT, false>(mq, mk, mv, a, q_tokens, grid, s);
+  return launch_one<FMT, false>(mq, mk, mv, a, q_tokens, units, s);
 }
 
 }  // namespace
@@ -1932,11 +1966,14 @@ cudaError_t launch_chunk_paged(const ChunkArgs &args, cudaStream_t s) {
                                     : launch_fmt<kKvNvfp4>(mq, mk, mv, a, q_tokens, grid, s);
   }
   if (e != cudaSuccess || a.n_splits == 1) return e;
-  const int64_t rows = (int64_t)a.total * a.Hq;
+  // Several rows a warp once there are more than the chip's warps.
+  const bool many = (int64_t)a.total * a.Hq > 152 * 64;
+  const int per = many ? MERGE_ROWS : 1;
+  const int64_t warps = (int64_t)a.total * ((a.Hq + per - 1) / per);
   // Launched as a programmatic dependent of the attention kernel, whose CTAs
   // release it as they start: its own launch is over by the time they end.
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((rows + MERGE_WARPS - 1) / MERGE_WARPS));
+  cfg.gridDim = dim3((unsigned)((warps + MERGE_WARPS - 1) / MERGE_WARPS));
   cfg.blockDim = dim3(MERGE_WARPS * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
@@ -1944,7 +1981,7 @@ cudaError_t launch_chunk_paged(const ChunkArgs &args, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel, a);
+  return cudaLaunchKernelEx(&cfg, many ? merge_kernel<MERGE_ROWS> : merge_kernel<1>, a);
 }
 
 }  // namespace attn_skip
