@@ -630,6 +630,8 @@ class PagedKV:
                 raise ValueError("k and v must be dense within a page")
         if k.stride(0) != v.stride(0):
             raise ValueError("k and v must have the same page stride")
+        if n_pages > 1 and k.stride(0) < Hkv * page_size * width:
+            raise ValueError("pages must not overlap")
         rows = (n_pages, Hkv, page_size)
         need = {"bf16": (), "e4m3": ((k_scale, rows), (v_scale, rows)),
                 "nvfp4": ((k_scale, rows), (v_scale, rows), (k_bs, rows + (d // 16,)),

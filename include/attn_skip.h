@@ -620,8 +620,8 @@ attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
  *              max_kv <= max_pages * page_size
  *  lambda      [n_seq] fp32 (device), each in [0, 1); 0 = dense
  *  n_splits    1 .. 1024.  attn_skip_chunk_paged_splits proposes a count (it
- *              has no influence on the result at lambda = 0 beyond rounding; a
- *              batch whose lambdas are all 0 may be cut elsewhere, into as many)
+ *              has no influence on the result at lambda = 0 beyond rounding: a
+ *              tile of lambda 0 may be cut elsewhere, or not at all)
  *  o           [total, Hq, 128] bf16, lse [total, Hq] fp32: written for the
  *              rows of the sequences, others stay as they were
  *  skip_bits   [n_seq, Hkv, ceil(max_chunk / TT), n_splits, ceil(bps / 32)]

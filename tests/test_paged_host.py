@@ -142,6 +142,17 @@ def test_binding_refuses_tensors_off_the_gpu():
         bs.PagedKV("fp16", k, k)
 
 
+def test_binding_refuses_pages_that_overlap():
+    """A pool of one page expanded to four has page stride 0, which the C entry
+    takes for a dense pool."""
+    k = torch.zeros(1, 1, 16, 128, dtype=torch.bfloat16).expand(4, 1, 16, 128)
+    with pytest.raises(ValueError, match="overlap"):
+        bs.PagedKV("bf16", k, k)
+    k = torch.zeros(4096, dtype=torch.bfloat16).as_strided((2, 1, 16, 128), (1024, 2048, 128, 1))
+    with pytest.raises(ValueError, match="overlap"):
+        bs.PagedKV("bf16", k, k)
+
+
 @pytest.mark.parametrize("fmt,step", [("e4m3", 2.0 ** -4), ("nvfp4", 0.25)])
 def test_plain_formats_round_to_nearest(fmt, step):
     """Reading back is off by at most half a step: 2^-4 of the value for E4M3
