@@ -15,7 +15,9 @@
 // leave a decode step 1 row of 128).  Row r is token r / G, head r % G: one
 // TMA box of G heads x TT tokens.  A split owns bps blocks of the key axis and
 // restarts its running max; with more than one split the partial outputs are
-// merged by log-sum-exp in a second launch.
+// merged by log-sum-exp in a second launch.  Many short tiles over bf16 rows run in
+// CTAs that stay (prompt_paged_kernel, below), tiles of at most eight rows over a
+// quantised cache on warp-level products (decode_paged.cu).
 //
 // Warp roles:
 //   0-3   deciders: row max of S_j, vote against the running max, AND;
