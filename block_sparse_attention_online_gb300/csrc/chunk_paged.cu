@@ -107,9 +107,11 @@ template <> struct Cfg<kKvNvfp4> {
   static constexpr int NKD = 2, NC = 3, WARPS = 20;
   static constexpr uint32_t ROW = D / 2, CODES = BN * D / 2, BS = BN * D / 16;
 };
-template <int FMT> struct Layout {
+// PAIR: two CTAs an SM, one tile each for keys and values.
+template <int FMT, bool PAIR = false> struct Layout {
   using C = Cfg<FMT>;
-  static constexpr uint32_t Q = 0, K = TILE_BYTES, V = K + C::NKD * TILE_BYTES;
+  static constexpr int NKD = PAIR ? 1 : C::NKD, NV = PAIR ? 1 : attn_skip::NV;
+  static constexpr uint32_t Q = 0, K = TILE_BYTES, V = K + NKD * TILE_BYTES;
   // A staged block: codes, block scales, row scales; a key block's stage also
   // holds the row scales of its values (needed before the values are).
   static constexpr uint32_t SCALES = C::CODES + C::BS, KSTAGE = SCALES + 2 * BN, VSTAGE = SCALES + BN;
@@ -147,7 +149,8 @@ struct Shared {
 static_assert(Layout<kKvBf16>::END + sizeof(Shared) <= 227 * 1024, "shared memory budget");
 static_assert(Layout<kKvE4m3>::END + sizeof(Shared) <= 227 * 1024, "shared memory budget");
 static_assert(Layout<kKvNvfp4>::END + sizeof(Shared) <= 227 * 1024, "shared memory budget");
-static_assert(NQ * 32 * MERGE_STRIDE * 4 <= (2 + NV) * TILE_BYTES, "merge area: the key and value tiles");
+static_assert(2 * (Layout<kKvBf16, true>::END + sizeof(Shared) + 1024) <= 228 * 1024, "two CTAs an SM");
+static_assert(NQ * 32 * MERGE_STRIDE * 4 <= 3 * TILE_BYTES, "merge area: query, key and value tiles");
 static_assert(NR % 2 == 0 && NR > NS, "barrier ring: even, and longer than the S buffer ring");
 
 __device__ __forceinline__ uint64_t kmajor_base(uint32_t tile) {
@@ -464,16 +467,20 @@ __device__ __forceinline__ void convert_q(uint32_t tile, int r0, int r1, int lan
 }
 
 // REP: tiles of at most 32 rows, once in each quarter of the products' 128 rows.
-template <int FMT, bool REP>
-__global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
+// PAIR (REP): in half an SM, for splits of few blocks, whose set-up and last steps
+// then lie under another CTA's loads.
+template <int FMT, bool REP, bool PAIR>
+__global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
     chunk_paged_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ ChunkArgs a, const int q_box_tokens) {
   using C = Cfg<FMT>;
-  using L = Layout<FMT>;
+  using L = Layout<FMT, PAIR>;
   constexpr bool QUANT = FMT != kKvBf16;
-  constexpr int NKD = C::NKD, NC = QUANT ? C::NC : 1;
+  constexpr int NKD = L::NKD, NV = L::NV, NC = QUANT ? C::NC : 1;
+  constexpr int NS = PAIR ? 1 : attn_skip::NS;
+  constexpr uint32_t TMEM_O = NS * BN, TMEM_COLS = PAIR ? 256 : attn_skip::TMEM_COLS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Shared &sh = *reinterpret_cast<Shared *>(smem_raw + L::END);
   const uint32_t base = smem_u32(smem_raw);
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
       // The ring's slot last held block c - K_AHEAD.
       if (c >= K_AHEAD &&
           !(QUANT ? wait_warp(&sh.kc_empty[c % NC], c / NC - 1)
-                  : wait_warp(&sh.qk_done[c % NR], c / NR - 1)))
+                  : wait_warp(&sh.qk_done[(c - K_AHEAD) % NR], (c - K_AHEAD) / NR)))
         break;
       load_k(c);
       ++issued;
@@ -615,10 +622,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
       // Drain: the last load of each slot has landed before exit.
       mbar_wait_drain(bar(&sh.q_full), 0);
 #pragma unroll 1
-      for (int s = 0; s < K_AHEAD && s < issued; ++s) {
-        const int last = s + ((issued - 1 - s) / K_AHEAD) * K_AHEAD;
-        mbar_wait_drain(bar(k_bar(s)), (last / K_AHEAD) & 1);
-      }
+      for (int c = max(0, issued - K_AHEAD); c < issued; ++c)
+        mbar_wait_drain(bar(k_bar(c)), (c / (QUANT ? NC : NR)) & 1);
     }
   } else if (warp == WARP_V) {
     // ------------------------------------------------------ value producer --
@@ -1083,7 +1088,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
           o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
         if constexpr (REP) {
           if (!valid) continue;
-          const uint32_t at = base + L::K + (uint32_t)((r * MERGE_STRIDE + col) * 4);
+          const uint32_t at = base + (uint32_t)((r * MERGE_STRIDE + col) * 4);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             st_shared_v4(at + q * 16, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
@@ -1107,8 +1112,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
             lrow == 0.f ? -INFINITY : lref * kLn2 + logf(lrow);
     }
     if constexpr (REP) {
-      // The four quarters' weighted rows stand in the key and value tiles, which
-      // nothing reads any more; 256 threads add them up, four columns each.
+      // The four quarters' weighted rows stand in the query, key and value tiles,
+      // which nothing reads any more; 256 threads add them up, four columns each.
       named_bar_sync(kMergeBarrier, 2 * NQ * 32);
       if (ok) {
 #pragma unroll 1
@@ -1118,7 +1123,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, 1)
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             const float4 u = *reinterpret_cast<const float4 *>(
-                smem_raw + L::K + ((q * 32 + rr) * MERGE_STRIDE + col) * 4);
+                smem_raw + ((q * 32 + rr) * MERGE_STRIDE + col) * 4);
             v.x += u.x;
             v.y += u.y;
             v.z += u.z;
@@ -1837,14 +1842,14 @@ int64_t tiles_bound(int n_seq, int total, int max_chunk, int TT) {
   return by_len < by_total ? by_len : by_total;
 }
 
-template <int FMT, bool REP>
+template <int FMT, bool REP, bool PAIR>
 cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                        const ChunkArgs &a, int q_tokens, unsigned grid, cudaStream_t s) {
-  constexpr uint32_t smem = Layout<FMT>::END + ((sizeof(Shared) + 15) / 16) * 16;
-  cudaError_t e = cudaFuncSetAttribute(chunk_paged_kernel<FMT, REP>,
+  constexpr uint32_t smem = Layout<FMT, PAIR>::END + ((sizeof(Shared) + 15) / 16) * 16;
+  cudaError_t e = cudaFuncSetAttribute(chunk_paged_kernel<FMT, REP, PAIR>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  chunk_paged_kernel<FMT, REP><<<grid, Cfg<FMT>::WARPS * 32, smem, s>>>(mq, mk, mv, a, q_tokens);
+  chunk_paged_kernel<FMT, REP, PAIR><<<grid, Cfg<FMT>::WARPS * 32, smem, s>>>(mq, mk, mv, a, q_tokens);
   return cudaGetLastError();
 }
 
@@ -1859,10 +1864,21 @@ cudaError_t launch_prompt(const CUtensorMap &mq, const CUtensorMap &mk, const CU
   return cudaGetLastError();
 }
 
+// Splits of at most this many blocks take half an SM a CTA where there are more CTAs
+// than SMs: 64 sequences of up to 300 tokens 24 us against 32, of up to 1000 42 and
+// 48, of 4 new tokens on 300 in three splits 47 and 75; with 16 blocks a split 71 and
+// 72 (83 and 71 with a threshold: values arrive later), with 52 blocks 368 and 329.
+constexpr int PAIR_BLOCKS = 12;
+
 template <int FMT>
 cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                        const ChunkArgs &a, int q_tokens, unsigned units, cudaStream_t s) {
-  if (a.G * q_tokens <= 32) return launch_one<FMT, true>(mq, mk, mv, a, q_tokens, units, s);
+  if (a.G * q_tokens <= 32) {
+    if constexpr (FMT == kKvBf16)
+      if (units > 152 && a.bps <= PAIR_BLOCKS)
+        return launch_one<FMT, true, true>(mq, mk, mv, a, q_tokens, units, s);
+    return launch_one<FMT, true, false>(mq, mk, mv, a, q_tokens, units, s);
+  }
   if constexpr (FMT == kKvBf16) {
     // CTAs that stay pay where there are more tiles than SMs and these are short:
     // whole prompts of 256 tokens (64 of them) 137 us against 209, of 1024 (16) 203
@@ -1875,7 +1891,7 @@ cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
       return a.n_splits > 1 ? launch_prompt<true>(mq, mk, mv, a, q_tokens, grid, s)
                             : launch_prompt<false>(mq, mk, mv, a, q_tokens, grid, s);
   }
-  return launch_one<FMT, false>(mq, mk, mv, a, q_tokens, units, s);
+  return launch_one<FMT, false, false>(mq, mk, mv, a, q_tokens, units, s);
 }
 
 }  // namespace

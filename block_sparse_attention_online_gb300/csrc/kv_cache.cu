@@ -14,8 +14,8 @@
 // or 6 (E2M1 times E4M3) significant bits, so reading back in bf16 is exact
 // (e >= -110 keeps the smallest product, 2^-10 * 2^-110, a bf16 normal).
 //
-// Both kernels only move bytes: DRAM traffic bounds the large calls, latency
-// the small ones.  Sixteen lanes own a row, so every row is read and written as
+// DRAM traffic bounds the large calls, instruction issue those that quantise (E4M3,
+// 16384 tokens of 8 heads: 22 us, 15 for the bytes), latency the small ones.  Sixteen lanes own a row, so every row is read and written as
 // whole 32-byte sectors and the row's maximum is four shuffles.  A half warp
 // takes the key and the value rows of a few consecutive tokens of one head,
 // whose place in the cache it works out once a token and whose pool rows are
