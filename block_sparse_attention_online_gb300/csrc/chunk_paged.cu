@@ -1152,8 +1152,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
 // (cluster launch control) and goes on to load that one's queries and keys, so that
 // set-up, the first loads and the first scores of a tile lie under the end of the
 // one before, and TMEM and barriers are set up once.  Rings run on from tile to
-// tile: block g is the CTA's g-th.  Two query tiles, of which an epilogue also takes
-// the free one's place to put its rows in order, three key and two value tiles.
+// tile: block g is the CTA's g-th.  Two query tiles (an epilogue puts its rows in
+// order where its queries were), three key and two value tiles.
 // Bound for short tiles: the scores' way to the last P.V and out, which the next
 // tile's decisions wait for.
 constexpr int PK = 3, PQ = 2;
@@ -1168,8 +1168,8 @@ constexpr uint32_t kWholeRow = 0x7fc5a5a5u;
 struct PromptShared {
   uint4 next;            // answer of the cluster launch control
   uint64_t next_full;
-  uint64_t tile_full[2]; // ring of the tiles: set,
-  uint64_t tile_empty[2];  // and left by twelve warps (all but the key producer)
+  uint64_t tile_full[2];   // ring of the tiles: set, ..
+  uint64_t tile_empty[2];  // .. left by twelve warps (all but the key producer)
   uint64_t q_full[2];
   uint64_t ready[NR];    // slot g % NR: block g's key tile is in and its S buffer free
   uint64_t qk_done[NR];
