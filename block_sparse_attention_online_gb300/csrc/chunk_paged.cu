@@ -1898,7 +1898,9 @@ cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
 
 // The split count that a host-side model of the launch finds cheapest: waves of
 // CTAs (one an SM, or two of the decode kernel), each a set-up and its share of
-// the blocks.  A long decode batch takes six at least: sequences of different
+// the blocks, and the merge, a second launch (one sequence of 1000 tokens, bf16: 14.5
+// us without it and 10.9 in eight splits where the calls are captured in a graph, 17
+// and 23 where the host makes them one after another).  A long decode batch takes six at least: sequences of different
 // lengths fill the chip only in smaller pieces (24 sequences of 8192 to 32768
 // tokens, bf16: 295 us with 1 split, 288 with 3, 280 with 6, 303 with 16).
 int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv, int TT, int format) {
@@ -1907,8 +1909,10 @@ int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv,
   const int slots = small ? 304 : 152;
   const int64_t units = tiles_bound(n_seq, total, max_chunk, TT) * Hkv;
   const int nb = (max_kv + BN - 1) / BN;
-  const double block_us = format == kKvBf16 ? 1.2 : small ? 1.5 : 1.8;
-  const double setup_us = small ? 3.0 : 4.0, merge_us = 3.0;
+  // A block alone on its SM, and what it takes more on a full chip.
+  const double block_us = format == kKvBf16 ? 0.65 : small ? 0.85 : 1.8;
+  const double full_us = format == kKvBf16 ? 0.55 : small ? 0.65 : 0.0;
+  const double setup_us = small ? 3.0 : 4.0, merge_us = 5.0;
   const int least = rows <= 32 && n_seq > 1 && nb >= 6 * 32 ? 6 : 1;
   int best = least;
   double best_t = 0;
@@ -1916,7 +1920,8 @@ int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv,
     const int bps = (nb + n - 1) / n;
     if (n > least && (nb + bps - 1) / bps < n) continue;  // the last splits would be empty
     const int64_t waves = (units * n + slots - 1) / slots;
-    const double t = waves * (setup_us + bps * block_us) + (n > 1 ? merge_us : 0);
+    const double full = units * n < slots ? (double)(units * n) / slots : 1.0;
+    const double t = waves * (setup_us + bps * (block_us + full * full_us)) + (n > 1 ? merge_us : 0);
     if (n == least || t < best_t) {
       best = n;
       best_t = t;
