@@ -552,6 +552,46 @@ def test_prompts_of_many_tiles_with_bad_device_arguments():
         assert torch.equal(o[s * C:(s + 1) * C], want[s * C:(s + 1) * C])
 
 
+@pytest.mark.parametrize("ps", [128, 256, 384])
+@pytest.mark.parametrize("fmt,n,C,G,n_splits", [
+    ("e4m3", 20, 2, 4, 9), ("nvfp4", 20, 1, 8, 9), ("bf16", 20, 90, 4, 1), ("bf16", 20, 90, 4, 3),
+    ("e4m3", 20, 100, 4, 2), ("bf16", 60, 3, 4, 2),
+])
+def test_large_batches_share_pages_of_many_rows(fmt, ps, n, C, G, n_splits):
+    """Grids of more pieces or tiles than the chip takes at once, over pages of one
+    to three blocks; every sequence stands twice in the batch, on the same pages."""
+    Hkv, g = 2, np.random.default_rng(n + ps)
+    lens = [int(x) for x in g.integers(max(C, 700), 1400, n // 2)]
+    chunks = [int(x) for x in g.integers(1, C + 1, n)]
+    kv, table = cache_of(fmt, lens, ps, Hkv, n)
+    lens, table = lens + lens, torch.cat([table, table]).contiguous()
+    q, out = attend(kv, table, chunks, lens, Hkv * G, [0.0] * n, n_splits=n_splits, seed=ps)
+    check(kv, table, chunks, lens, Hkv * G, [0.0] * n, q, out, n_splits=n_splits)
+
+
+@pytest.mark.parametrize("fmt,n,C", [("bf16", 40, 100), ("e4m3", 64, 1), ("bf16", 3, 60)])
+def test_a_workspace_serves_calls_of_any_kind(fmt, n, C):
+    """What one call leaves in the partials means nothing to the next: dense calls and
+    calls with thresholds, sound ones and ones with a bad sequence, in turn."""
+    Hkv, Hq, L, ns = 2, 8, 900, 3
+    kv, table = cache_of(fmt, [L] * n, 32, Hkv, n, sink=1.0)
+    cu, kl = i32(range(0, n * C + 1, C)), i32([L] * n)
+    q = (torch.randn(n * C, Hq, 128, device=DEV) + 0.7).to(torch.bfloat16)
+    dense = torch.zeros(n, device=DEV)
+    some = torch.where(torch.arange(n, device=DEV) % 2 == 0, 0.5, 0.0)
+    short = kl.clone()
+    short[0] = 0
+    calls = [(cu, kl, dense), (cu, kl, some), (cu, short, dense), (cu, short, some), (cu, kl, dense)]
+    work = (torch.full((n * C, Hq, ns, 128), float("nan"), device=DEV),
+            torch.full((n * C, Hq, ns), float("nan"), device=DEV))
+    for c, k, lam in calls:
+        want = bs.attn_skip_chunk_paged(kv, q, c, C, k, L, table, lam, n_splits=ns)
+        got = bs.attn_skip_chunk_paged(kv, q, c, C, k, L, table, lam, n_splits=ns, workspace=work)
+        bs.attn_skip_last_device_error()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.isfinite(got[0].float()).all()
+
+
 @pytest.mark.parametrize("fmt,n,C,L", [("bf16", 40, 100, 400), ("nvfp4", 64, 1, 1500)])
 def test_large_batches_on_two_streams_and_in_a_graph(fmt, n, C, L):
     """Grids whose CTAs take over one another's work, or share it out, next to
