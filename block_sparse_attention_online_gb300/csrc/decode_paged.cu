@@ -249,7 +249,10 @@ __device__ __noinline__ uint32_t settle_zero_row(const ChunkArgs &a, const Item 
 // takes every gridDim.x-th.  24 sequences of 8192 to 32768 tokens, NVFP4: 152 us,
 // 188 with a CTA a piece; E4M3 154 and 164.  (16 sequences of one length, E4M3, bound
 // by memory: 177 and 172, since equal runs do not follow the SMs' different distances
-// to memory; two or three rounds of shorter runs cost more than they bring.)
+// to memory; two or three rounds of shorter runs cost more than they bring.  Whole
+// pieces the hardware's scheduler spreads better: with thresholds 233 us against 242;
+// whole tiles, one split, are left to it: 100 sequences of up to 4000, NVFP4, 104 and
+// 121.)
 constexpr int SEQS = 4;  // sequences a lane keeps: up to 128
 
 struct Plan {  // (32 sequences at a time: mostly there are no more)
@@ -264,9 +267,9 @@ __device__ __forceinline__ unsigned entries_of(const ChunkArgs &a, bool runs, un
   return runs ? nb : (nb + a.bps - 1) / a.bps;
 }
 
-// One warp; also writes the outputs of the sequences without a visible key.
+// One warp; also marks the partials of the sequences without a visible key.
 __device__ __noinline__ void plan_start(const ChunkArgs &a, Plan &p, int lane) {
-  bool cut = a.n_splits > 1, none[SEQS], bad = false;
+  bool cut = true, none[SEQS], bad = false;
   unsigned longest = 0;
   const int chunks = (a.n_seq + 31) / 32;
 #pragma unroll 1
@@ -320,11 +323,7 @@ __device__ __noinline__ void plan_start(const ChunkArgs &a, Plan &p, int lane) {
       if (s % gridDim.x != blockIdx.x) continue;
       const int64_t r0 = (int64_t)__ldg(a.cu_seqlens + s) * a.Hq;
       const int64_t n = (int64_t)__ldg(a.cu_seqlens + s + 1) * a.Hq - r0;
-      float *lse = a.n_splits == 1 ? a.lse : a.lse_part;
-      for (int64_t r = lane; r < n * a.n_splits; r += 32) lse[r0 * a.n_splits + r] = -INFINITY;
-      if (a.n_splits == 1)
-        for (int64_t r = lane; r < n * (D / 8); r += 32)
-          reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + r0 * D)[r] = make_uint4(0, 0, 0, 0);
+      for (int64_t r = lane; r < n * a.n_splits; r += 32) a.lse_part[r0 * a.n_splits + r] = -INFINITY;
     }
   }
 }
@@ -958,10 +957,8 @@ __global__ void __launch_bounds__(NT, 2)
                 make_uint2(pack_bf16x2(v[0] * iz, v[1] * iz), pack_bf16x2(v[2] * iz, v[3] * iz));
           else
             *reinterpret_cast<float4 *>(part) = make_float4(v[0] * iz, v[1] * iz, v[2] * iz, v[3] * iz);
-        } else if (a.n_splits == 1) {
-          *out = __float2bfloat16_rn(v[0] * iz);
         } else {
-          *part = v[0] * iz;
+          *part = v[0] * iz;  // (more than one split)
         }
       }
     };
@@ -1012,7 +1009,7 @@ cudaError_t launch_decode_paged(const ChunkArgs &args, unsigned grid, cudaStream
   // More pieces than CTAs fit: shared out on the device, up to 128 sequences (with
   // more of them a CTA's search through the list costs what it saves).
   const int64_t list = (int64_t)a.n_seq * a.Hkv * ((a.max_kv + BN - 1) / BN);
-  if (grid > kCtas && a.n_seq <= 32 * SEQS && list > 0 && list < (int64_t)1 << 30) {
+  if (grid > kCtas && a.n_splits > 1 && a.n_seq <= 32 * SEQS && list > 0 && list < (int64_t)1 << 30) {
     a.shared_out = 1;
     grid = kCtas;
   }
