@@ -54,9 +54,12 @@
 // all 128 keys of a handful of rows was what bounded decode over the quantised
 // caches (3600 cycles a block on an SM whose other warps convert).
 //
-// Rows of the last block at or past kv (a page's unwritten tail, pages never
-// loaded) may hold anything: their scores are replaced by -inf and their value
-// rows by zeros in shared memory.
+// Rows of the last block at or past the last key that some row of the tile sees
+// (later tokens, a page's unwritten tail, pages never loaded) may hold anything:
+// their scores are replaced by -inf, and their values are left out of the product:
+// over bf16 rows P.V goes over whole sixteens of keys, up to the one with the last
+// such key, and the value rows behind that key become zeros in shared memory;
+// converters write zeros for all of them.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -164,6 +167,26 @@ __device__ __forceinline__ uint64_t vmajor_base(uint32_t tile) {
 }
 __device__ __forceinline__ constexpr uint64_t vmajor_step(int kk) {
   return (uint64_t)(((uint32_t)kk * 2048u) >> 4);
+}
+
+// O (+)= P V over the sixteens of a block's keys with one below `left`: the last
+// block's, out of line, and whole blocks'.  (A test before every instruction costs
+// the issuer 6 % of a chunk of 4096 on 16384.)
+__device__ __noinline__ void issue_pv_part(uint32_t o, uint32_t p, uint64_t v, uint32_t idesc, uint32_t add,
+                                           int left) {
+#pragma unroll 1
+  for (int kk = 0; kk * 16 < left; ++kk)
+    mma_bf16_ts(o, p + kk * 8, v + vmajor_step(kk), idesc, kk > 0 ? 1u : add);
+}
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, uint32_t idesc, bool add,
+                                         int left) {
+  if (left >= BN) {
+#pragma unroll
+    for (int kk = 0; kk < BN / 16; ++kk)
+      mma_bf16_ts(o, p + kk * 8, v + vmajor_step(kk), idesc, kk > 0 || add ? 1u : 0u);
+  } else {
+    issue_pv_part(o, p, v, idesc, add ? 1u : 0u, left);
+  }
 }
 
 // Of 32 * chunks keys, those at or past the row's `left` become -inf in this
@@ -647,14 +670,15 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
       if (vi >= N && !wait_warp(QUANT ? &sh.vc_empty[s] : &sh.v_empty[s], vi / N - 1)) break;
       const uint32_t dst = base + (QUANT ? L::VC + s * L::VSTAGE : L::V + s * TILE_BYTES);
       const int left = x.kv - j * BN;  // rows of the block below kv
-      const bool cut = !QUANT && left < BN;  // the last block: zero the rows at or past kv
+      // The last block, where its product does not end at kv: zero the rows behind.
+      const bool cut = !QUANT && left < BN && (left & 15);
       load_block<FMT>(a, pages, &tm_v, true, j, dst,
                       bar(QUANT ? &sh.vc_full[s] : cut ? &sh.v_tail : &sh.v_full[s]), lane);
       if (cut) {
         tail = true;
         if (!wait_warp(&sh.v_tail, 0)) break;
 #pragma unroll 1
-        for (int i = lane; i < (BN - left) * 16; i += 32)
+        for (int i = lane; i < (-left & 15) * 16; i += 32)
           st_shared_v4(dst + (i & 8 ? HALF_BYTES : 0) + (left + (i >> 4)) * 128 + (i & 7) * 16, 0, 0,
                        0, 0);
         fence_proxy_async_smem();
@@ -709,10 +733,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
         fence_after_sync();
         const uint32_t pt = tmem + (c % NS) * BN;
         const uint64_t vd = vmajor_base(base + L::V + vs * TILE_BYTES);
-#pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_bf16_ts(tmem + TMEM_O, pt + kk * 8, vd + vmajor_step(kk), QUANT ? IDESC_PV16 : IDESC_PV,
-                      kk > 0 || kc > 0 ? 1u : 0u);
+        issue_pv(tmem + TMEM_O, pt, vd, QUANT ? IDESC_PV16 : IDESC_PV, kc > 0,
+                 QUANT || c != nb - 1 ? BN : x.kv - (x.j0 + c) * BN);
         mma_commit(bar(&sh.v_empty[vs]));
         mma_commit(bar(&sh.ready[(c + NS) % NR]));  // S buffer free for block c + NS
         mma_commit(bar(&sh.pv_done[pb]));
@@ -1302,8 +1324,7 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
       // The tile's splits, one after the other; those without a block are a partial of
       // no weight (where there is one split: O = 0, LSE = -inf).  A dense tile needs no
       // cut: its rows go to the outputs, and the merge leaves them alone.
-      const int seen = a.causal ? max(0, found.pos0 + found.ntok) : found.kv;
-      const int blocks = (seen + BN - 1) / BN, rows = found.s >= 0 ? found.ntok * a.G : 0;
+      const int blocks = (found.kv + BN - 1) / BN, rows = found.s >= 0 ? found.ntok * a.G : 0;
       const bool whole = found.ln_lam == -INFINITY;
       const int run = !SPLIT || whole ? blocks : a.bps;
       const int splits = !rows || !blocks ? 0 : SPLIT ? (blocks + run - 1) / run : 1;
@@ -1408,13 +1429,15 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
         if (!ok) break;
         const uint32_t dst = base + P_V + s * TILE_BYTES;
         const int left = x.kv - j * BN;  // rows of the block below kv
+        // The last block, where its product does not end at kv: zero the rows behind.
+        const bool cut = left < BN && (left & 15);
         load_block_here<kKvBf16>(a, pages, &tm_v, true, j, dst,
-                                 bar(left < BN ? &sh.v_tail : &sh.v_full[s]), lane);
-        if (left < BN) {  // the last block: zero the rows at or past kv
+                                 bar(cut ? &sh.v_tail : &sh.v_full[s]), lane);
+        if (cut) {
           ok = wait_warp(&sh.v_tail, tails++);
           if (!ok) break;
 #pragma unroll 1
-          for (int i = lane; i < (BN - left) * 16; i += 32)
+          for (int i = lane; i < (-left & 15) * 16; i += 32)
             st_shared_v4(dst + (i & 8 ? HALF_BYTES : 0) + (left + (i >> 4)) * 128 + (i & 7) * 16, 0, 0,
                          0, 0);
           fence_proxy_async_smem();
@@ -1471,6 +1494,7 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
         if (!wait(&sh.tile_full[it & 1], it >> 1)) break;
         const int s = sh.tile[it & 1].s, nb = sh.tile[it & 1].nb;
         if (s < 0) break;
+        const int keys = sh.tile[it & 1].kv - sh.tile[it & 1].j0 * BN;
         bool first = true;
 #pragma unroll 1
         for (int c = 0; c < nb; ++c, ++g) {
@@ -1487,10 +1511,7 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
           fence_after_sync();
           const uint32_t pt = tmem + (g % NS) * BN;
           const uint64_t vd = vmajor_base(base + P_V + vs * TILE_BYTES);
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_bf16_ts(tmem + TMEM_O, pt + kk * 8, vd + vmajor_step(kk), IDESC_PV,
-                        kk > 0 || !first ? 1u : 0u);
+          issue_pv(tmem + TMEM_O, pt, vd, IDESC_PV, !first, c != nb - 1 ? BN : keys - c * BN);
           mma_commit(bar(&sh.v_empty[vs]));
           mma_commit(bar(&sh.ready[(g + NS) % NR]));  // S buffer free for block g + NS
           mma_commit(bar(&sh.pv_done[pb]));

@@ -59,7 +59,7 @@ struct TileInfo {
   int t;          // tile of the sequence
   int tok0, ntok; // its first packed token, its tokens
   int pos0;       // position of its first token
-  int kv;         // the sequence's cached length
+  int kv;         // the end of the keys that some row of the tile sees
   int j0, nb;     // first block, blocks
   float ln_lam;   // -inf: dense, every block is kept
 };
@@ -129,10 +129,10 @@ __device__ __forceinline__ TileInfo locate(const ChunkArgs &a, int i, int split,
   x.tok0 = c0 + t * a.TT;
   x.ntok = min(a.TT, len - t * a.TT);
   x.pos0 = kv - len + t * a.TT;
-  x.kv = kv;
-  // Keys that some row of the tile sees, then this split's blocks of them.
-  const int seen = a.causal ? max(0, x.pos0 + x.ntok) : kv;
-  const int blocks = (seen + BN - 1) / BN;
+  // Rows behind the last key that some row of the tile sees (later tokens of the
+  // chunk among them) may hold anything: they are not there for the tile.
+  x.kv = a.causal ? max(0, x.pos0 + x.ntok) : kv;
+  const int blocks = (x.kv + BN - 1) / BN;  // then this split's share of them
   x.j0 = split * a.bps;
   x.nb = max(0, min(blocks, x.j0 + a.bps) - x.j0);
   x.ln_lam = lam > 0.f && lam < 1.f ? logf(lam) : -INFINITY;

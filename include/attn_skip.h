@@ -638,9 +638,10 @@ attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
  * to bf16 for the P.V product (to fp16 where a quantised cache is widened on the
  * chip, with steps of 2^-31 of the largest contribution at the small end).
  * There a row whose scale is 2^15 or more below the largest of its 128-row block
- * is rounded to 2^-25 of that scale.  Cache rows at or past kv_len may hold
- * anything.  A value row that is not finite, and in sight of some row of a tile,
- * reaches every row of it.
+ * (of the rows that the tile sees) is rounded to 2^-25 of that scale.  Cache rows
+ * that no row of a tile sees (later tokens, rows at or past kv_len) may hold
+ * anything: they have no part in its outputs.  A value row that is not finite, and
+ * in sight of some row of a tile, reaches every row of it.
  * EINVAL as for attn_skip_kv_append, for max_chunk or max_kv < 0 or beyond the
  * page table and for n_splits out of range; head size or G out of range are
  * EUNSUPPORTED.  Checked by the kernel and reported by
