@@ -9,13 +9,17 @@
 // and a row scale multiplies one score instead of 128 elements:
 //   S^T = K Q^T        A = codes of 16 keys, B = fp16 queries (2^x scaled)
 //   s_c = S_c * scale * 2^(e_k,c - x)         (log2 units)
-//   P_c = 2^(s_c + e_v,c - ref + 7),  ref the running max of s_c + e_v,c of the warp
+//   w_c = 2^(s_c - sref),  sref the running max of s_c of the warp
+//   P_c = w_c 2^e_v,c 2^x,  x = sref - ref + 7, ref the running max of s_c + e_v,c
 //   O^T += V^T P       A = codes of 16 keys, transposed by byte pairs, B = P
-//   l += P_c 2^(-e_v,c - 7)
+//   l += w_c
 // An NVFP4 code times its block scale is an fp16 (exact); P is rounded to fp16.
-// The reference may lag by 2^8, so with 2^7 P stays below fp16's 2^16, has its 11
+// The references may lag by 2^8, so with 2^7 P stays below fp16's 2^16, has its 11
 // bits down to 2^-21 of the largest contribution and steps of 2^-31 of it below
-// (it counts where the row with the large weight holds a zero).
+// (it counts where the row with the large weight holds a zero).  A row of zeros has
+// no part in ref (2^e_v,c counts as 0).  Two references, since the values' exponents
+// span as much as fp32's: with ref alone the weights of rows of small values, or of
+// zeros, were lost beside rows of large ones.
 //
 // One CTA per (sequence, KV head, split), two on an SM; where these are more than
 // fit, the CTAs share the blocks out (below).  Eight warps share each 128-key block,
@@ -49,6 +53,8 @@ constexpr int NDEC = 4;           // decision ring
 constexpr int kVoteBarrier = 1;
 constexpr int MERGE_COLS = 32;
 constexpr unsigned kCtas = 2 * 152;  // two on each SM
+constexpr float kNoRef = -3e38f;     // sref of a row without a key so far
+constexpr float kBelow = 118.f;      // ref stays above sref - 118: x and what undoes it are normal
 
 template <int FMT> struct Cfg;
 template <> struct Cfg<kKvE4m3> {
@@ -83,7 +89,7 @@ struct Shared {
   uint64_t item_full[2], item_empty[2];
   int dec[NDEC];
   float rmax[2][NCW][ROWS];        // row maxima of the warps' keys, blocks of either parity
-  float ml[2][NCW][ROWS];          // the warps' references and row sums
+  float ml[3][NCW][ROWS];          // the warps' ref - 7, row sums and sref
   Item item[2];                    // ring of the CTA's work
   uint32_t word;                   // the bitmap's current word
   int abort;
@@ -209,13 +215,12 @@ __device__ __forceinline__ void load_block(const ChunkArgs &a, Producer &p, cons
   __syncwarp();
 }
 
-// The scale byte of value row r of a block with `left` rows to kv, as the reference should see it:
-// a row of zeros, which the writer gives byte 127, has no contribution to make room
-// for, so its exponent becomes the smallest (17).  The row's
-// four lanes look at a quarter of its codes each.
+// Whether value row r of a block with `left` rows to kv, of scale byte `byte`, holds
+// zeros, to which the writer gives byte 127.  The row's four lanes look at a quarter
+// of its codes each.
 template <int FMT>
-__device__ __noinline__ uint32_t settle_zero_row(const ChunkArgs &a, const Item &item, int r, int left,
-                                                 uint32_t byte, int t) {
+__device__ __noinline__ bool zero_row(const ChunkArgs &a, const Item &item, int r, int left,
+                                      uint32_t byte, int t) {
   const KvPages &p = a.pages;
   constexpr uint32_t QUARTER = Cfg<FMT>::ROW / 4;
   const bool mine = byte == 127u && r < left;
@@ -236,7 +241,7 @@ __device__ __noinline__ uint32_t settle_zero_row(const ChunkArgs &a, const Item 
   }
   any |= __shfl_xor_sync(0xffffffffu, any, 1);
   any |= __shfl_xor_sync(0xffffffffu, any, 2);
-  return mine && any == 0 ? 17u : byte;
+  return mine && any == 0;
 }
 
 // ------------------------------------------------------- shares of a batch --
@@ -583,9 +588,9 @@ __global__ void __launch_bounds__(NT, 2)
     float o[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    // The score above which a row's reference moves, 2^8 above the reference (whole
-    // numbers: sums with them are exact), and what the exponents subtract.
-    float top[2] = {-INFINITY, -INFINITY}, sub[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+    // sref (whole numbers: sums with them are exact), 2^x, row sum.
+    float sref[2] = {kNoRef, kNoRef}, px[2] = {1.f, 1.f}, l[2] = {0.f, 0.f};
+    auto x_of = [](float f) { return (float)((__float_as_int(f) >> 23) - 127); };  // of f = 2^x
     float m2[2] = {-INFINITY, -INFINITY};  // running max of the split (log2 units), with a threshold
     int left = x.kv - x.j0 * BN + BN;      // rows below kv from the block on
     // With a threshold, a block's product with its values comes after the next block's
@@ -608,7 +613,8 @@ __global__ void __launch_bounds__(NT, 2)
           // that the warps meet the vote barriers equally often.
           if (ok) ok = wait_warp(&sh.k_full[s], kn >= NST);
           float p[2][2];        // [key g, g + 8][row 2 t, 2 t + 1]: scores, then P
-          float ev[2], inv[2];  // the keys' value exponents and 2^-e_v
+          float vf[2];          // 2^e_v, the keys' value scales; 0 for rows of zeros
+          bool nan_rows = false;
           {
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
             const uint32_t kx = base + L::KX + s * L::KXS, kt = base + L::K + s * L::CODES;
@@ -652,47 +658,37 @@ __global__ void __launch_bounds__(NT, 2)
             }
             const uint32_t sc = kx + C::BS;
             const uint32_t eb0 = lds8(sc + kr0), eb1 = lds8(sc + kr1);
-            uint32_t vb0 = lds8(sc + BN + kr0), vb1 = lds8(sc + BN + kr1);
+            const uint32_t vb0 = lds8(sc + BN + kr0), vb1 = lds8(sc + BN + kr1);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.k_empty[s]));  // the stage is in registers
-            if (__any_sync(0xffffffffu, vb0 == 127u || vb1 == 127u)) {
-              vb0 = settle_zero_row<FMT>(a, item, kr0, left, vb0, t);
-              vb1 = settle_zero_row<FMT>(a, item, kr1, left, vb1, t);
-            }
             const float f0 = __uint_as_float(eb0 << 23), f1 = __uint_as_float(eb1 << 23);
             p[0][0] = acc[0] * (qs[0] * f0);
             p[0][1] = acc[1] * (qs[1] * f0);
             p[1][0] = acc[2] * (qs[0] * f1);
             p[1][1] = acc[3] * (qs[1] * f1);
-            // byte - 127 as fp32, by the fraction bits of 2^23 + byte.
-            ev[0] = __uint_as_float(0x4b000000u + vb0) - 8388735.f;
-            ev[1] = __uint_as_float(0x4b000000u + vb1) - 8388735.f;
-            inv[0] = __uint_as_float((254u - vb0) << 23);
-            inv[1] = __uint_as_float((254u - vb1) << 23);
-            if (__any_sync(0xffffffffu, max(max(eb0, eb1), max(vb0, vb1)) >= 254u)) {
-              // NaN rows (255), and 2^127, whose inverse is no normal number.
+            vf[0] = __uint_as_float(vb0 << 23);
+            vf[1] = __uint_as_float(vb1 << 23);
+            if (__any_sync(0xffffffffu, vb0 == 127u || vb1 == 127u)) {
+              if (zero_row<FMT>(a, item, kr0, left, vb0, t)) vf[0] = 0.f;
+              if (zero_row<FMT>(a, item, kr1, left, vb1, t)) vf[1] = 0.f;
+            }
+            // NaN rows (255), and 2^-127, which is no normal number (0).
+            if (__any_sync(0xffffffffu, max(max(eb0, eb1), max(vb0 - 1u, vb1 - 1u)) >= 254u)) {
               if (eb0 == 255u) p[0][0] = p[0][1] = NAN;
               if (eb1 == 255u) p[1][0] = p[1][1] = NAN;
-              if (vb0 >= 254u) inv[0] = vb0 == 255u ? 1.f : 5.877471754111438e-39f;
-              if (vb1 >= 254u) inv[1] = vb1 == 255u ? 1.f : 5.877471754111438e-39f;
-              if (vb0 == 255u) ev[0] = NAN;
-              if (vb1 == 255u) ev[1] = NAN;
+              if (vb0 == 255u || vb0 == 0u) vf[0] = vb0 ? NAN : 5.877471754111438e-39f;
+              if (vb1 == 255u || vb1 == 0u) vf[1] = vb1 ? NAN : 5.877471754111438e-39f;
+              nan_rows = true;
             }
           }
-          float y[2][2];  // s + e_v
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) y[k][n] = p[k][n] + ev[k];
           if (BN > left + min_rel) {  // keys that a row does not see, whatever they hold
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
               for (int n = 0; n < 2; ++n)
-                if ((k ? kr1 : kr0) >= left + rel[n]) {
-                  p[k][n] = y[k][n] = -INFINITY;
-                  if (ev[k] != ev[k] || inv[k] == 0.f) inv[k] = 1.f;
-                }
+                if ((k ? kr1 : kr0) >= left + rel[n]) p[k][n] = -INFINITY;
+            if (kr0 >= left) vf[0] = 0.f;  // (NaN times 0)
+            if (kr1 >= left) vf[1] = 0.f;
           }
           bool keep = true;
           if constexpr (LATE) {
@@ -746,25 +742,41 @@ __global__ void __launch_bounds__(NT, 2)
             }
           }
           if (keep && ok) {
-            inv[0] *= kPDown;
-            inv[1] *= kPDown;
-            // The reference moves when a key's s + e_v passes it by more than 2^8 (or it
-            // is the row's first): then by the warp's maximum.
-            const bool move = fmaxf(y[0][0], y[1][0]) > top[0] || fmaxf(y[0][1], y[1][1]) > top[1];
-            if (__any_sync(0xffffffffu, move)) {
+            float w[2][2], pv[2][2];
+            auto weigh = [&]() {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  w[k][n] = ex2(p[k][n] - sref[n]);
+                  pv[k][n] = w[k][n] * vf[k] * px[n];
+                }
+            };
+            weigh();
+            // The references move when a key passes one of them by more than 2^8 (or it
+            // is the row's first): then by the warp's maxima.
+            const float wm = fmaxf(fmax3(w[0][0], w[1][0], w[0][1]), w[1][1]);
+            const float pm = max_nan(max3_nan(pv[0][0], pv[1][0], pv[0][1]), pv[1][1]);
+            if (__any_sync(0xffffffffu, wm > 256.f || !(pm <= 32768.f))) {  // 2^8, 2^(8 + 7)
               float al[2];
 #pragma unroll
               for (int n = 0; n < 2; ++n) {
-                float m = fmaxf(y[0][n], y[1][n]);
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                const float to = fmaxf(top[n], ceilf(m) + kRescaleLog2);
-                al[n] = to == -INFINITY ? 1.f : ex2(top[n] - to);
-                sub[n] = to == -INFINITY ? 0.f : to - kRescaleLog2 - kPLog2;
-                top[n] = to;
-                l[n] *= al[n];
+                float x = fmaxf(p[0][n], p[1][n]);
+                float m = fmaxf(p[0][n] + x_of(vf[0]), p[1][n] + x_of(vf[1]));  // (0 counts as 2^-127)
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) {
+                  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                }
+                x = fmaxf(sref[n], ceilf(x));
+                const float from = sref[n] - x_of(px[n]);  // ref - 7
+                const float to = fmaxf(fmaxf(from, ceilf(m) - kPLog2), x - kBelow - kPLog2);
+                al[n] = ex2(from - to);
+                l[n] *= ex2(sref[n] - x);
+                sref[n] = x;
+                px[n] = __int_as_float(((int)(x - to) + 127) << 23);
               }
+              weigh();
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 o[i][0] *= al[0];
@@ -779,16 +791,18 @@ __global__ void __launch_bounds__(NT, 2)
                 b1 = mul_f16x2(b1, pack_f16x2(by, by));
               }
             }
+            l[0] += w[0][0] + w[1][0];
+            l[1] += w[0][1] + w[1][1];
+            if (nan_rows) {  // (they do not reach the rows that they are hidden from)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+              for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                p[k][n] = ex2(y[k][n] - sub[n]);
-                l[n] = fmaf(p[k][n], inv[k], l[n]);
-              }
+                for (int n = 0; n < 2; ++n)
+                  if (p[k][n] == -INFINITY) pv[k][n] = 0.f;
+            }
             // P as the B operand: key pairs of row g.
-            n0 = transpose8x8(pack_f16x2(p[0][0], p[0][1]));
-            n1 = transpose8x8(pack_f16x2(p[1][0], p[1][1]));
+            n0 = transpose8x8(pack_f16x2(pv[0][0], pv[0][1]));
+            n1 = transpose8x8(pack_f16x2(pv[1][0], pv[1][1]));
             fresh = true;
           }
         }
@@ -875,7 +889,8 @@ __global__ void __launch_bounds__(NT, 2)
     else
       blocks(std::true_type{});
 
-    // ---- merge of the eight warps: O = sum_w 2^(ref_w - M) O_w / L -------------
+    // ---- merge of the eight warps: O = sum_w 2^(ref_w - S - 7) O_w / L, L = sum_w
+    // 2^(sref_w - S) l_w, S the largest sref ----------------------------------------
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       l[n] += __shfl_xor_sync(0xffffffffu, l[n], 4);
@@ -885,10 +900,12 @@ __global__ void __launch_bounds__(NT, 2)
     // Every warp is here: the merge area's last readers have left it.
     if (bar_red_or(kVoteBarrier, NCW * 32, !ok)) return;
     if (g == 0) {
-      sh.ml[0][warp][2 * t] = top[0] - kRescaleLog2;
-      sh.ml[0][warp][2 * t + 1] = top[1] - kRescaleLog2;
+      sh.ml[0][warp][2 * t] = sref[0] - x_of(px[0]);
+      sh.ml[0][warp][2 * t + 1] = sref[1] - x_of(px[1]);
       sh.ml[1][warp][2 * t] = l[0];
       sh.ml[1][warp][2 * t + 1] = l[1];
+      sh.ml[2][warp][2 * t] = sref[0];
+      sh.ml[2][warp][2 * t + 1] = sref[1];
     }
     // Warp r sums row r of the warps' outputs, COLS columns at a time: PER of every
     // sixteen.  A CTA with one tile has the code tiles to do it in, at once; where
@@ -913,17 +930,20 @@ __global__ void __launch_bounds__(NT, 2)
         named_bar_sync(kVoteBarrier, NCW * 32);
         if (r >= rows) continue;
         if (q == 0) {
-          float m = -INFINITY, z = 0.f;
+          float m = -INFINITY, y = -INFINITY, z = 0.f;
 #pragma unroll
           for (int w = 0; w < NCW; ++w)
-            if (sh.ml[1][w][r] != 0.f) m = fmaxf(m, sh.ml[0][w][r]);
+            if (sh.ml[1][w][r] != 0.f) {
+              m = fmaxf(m, sh.ml[2][w][r]);
+              y = fmaxf(y, sh.ml[0][w][r]);
+            }
 #pragma unroll
           for (int w = 0; w < NCW; ++w) {
             const float lw = sh.ml[1][w][r];
-            f[w] = lw == 0.f ? 0.f : ex2(sh.ml[0][w][r] - m);  // 0: the warp met no key of the row
-            z = fmaf(lw, f[w], z);
+            f[w] = lw == 0.f ? 0.f : ex2(sh.ml[0][w][r] - y);  // 0: the warp met no key of the row
+            if (lw != 0.f) z = fmaf(lw, ex2(sh.ml[2][w][r] - m), z);
           }
-          iz = z == 0.f ? 0.f : kPDown / z;
+          iz = z == 0.f ? 0.f : ex2(y - m) / z;
           if (lane == 0)
             (a.n_splits == 1 ? a.lse : a.lse_part)[orow * a.n_splits + item.slot] =
                 z == 0.f ? -INFINITY : m * kLn2 + logf(z);
@@ -937,7 +957,6 @@ __global__ void __launch_bounds__(NT, 2)
         for (int i = 0; i < VEC; ++i) v[i] = 0.f;
 #pragma unroll
         for (int w = 0; w < NCW; ++w) {
-          if (f[w] == 0.f) continue;
           const float *u = area + (w * ROWS + r) * STRIDE + pos;
           if constexpr (VEC == 4) {
             const float4 y = *reinterpret_cast<const float4 *>(u);

@@ -20,6 +20,18 @@ constexpr float kRescaleLog2 = 8.0f;  // an exp reference may lag the max by 2^8
 // fp16 weights carry a factor 2^7: with the lag, up to fp16's 2^15.
 constexpr float kPLog2 = 7.0f, kPDown = 0.0078125f;
 
+// The larger one, or a NaN if there is one (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // The bounded waits of the other kernels with their slow path out of line (some
 // forty waits share the instruction cache) and with sixteen tries between two
 // looks at the abort flag and the clock (most warps wait most of the time, and
