@@ -37,12 +37,17 @@
 // that cost nothing per score: with E_k and E_v the largest row-scale exponents
 // of a block's keys and values, the tiles hold code * 2^(e - E) (exact for e >=
 // E - 15, otherwise off by at most 2^-25 2^E), the scores of the block are
-// scaled by 2^E_k, and P takes 2^E_v: P'_c = 2^(s_c + E_v - ref + 7), with ref the
-// running max of (row max + E_v) over the blocks, which may lag by 2^8: P' stays
-// below fp16's 2^16, has its 11 bits down to 2^-21 of the largest contribution and
-// steps of 2^-31 of it below (it counts where the row with the large weight holds
-// a zero); the row sum takes sum P' * 2^(-E_v - 7).  A query row enters as fp16(q * 2^x), 2^x
-// the largest power of two with max|q| 2^x <= 2^15.
+// scaled by 2^E_k, and P takes 2^E_v: with sref the running max of the row maxima and
+// ref that of (row max + E_v), both of which may lag by 2^8,
+//     P'_c = 2^(s_c - sref + f),  f = sref + E_v - ref + 7,  l += 2^-f sum P'_c.
+// P' stays below fp16's 2^16, has its 11 bits down to 2^-21 of the largest contribution
+// and steps of 2^-31 of it below (it counts where the row with the large weight
+// holds a zero).  f is -40 at least, where P' is 0 in fp16, so that the weights stay
+// in fp32's range: the values' exponents span as much, and without a reference on
+// the scores alone the weights of blocks of small values were lost beside blocks of
+// large ones.  A block whose values are all zero (E_v = -inf) has no part in ref.
+// A query row enters as fp16(q * 2^x), 2^x the largest power of two with max|q| 2^x
+// <= 2^15.
 //
 // A warp quarter whose 32 rows lie past the tile's last row (decode: G rows) has
 // no decider and no exponential warp: they convert, or go to the end at once.
@@ -134,14 +139,15 @@ struct Shared {
   uint64_t kc_full[3], kc_empty[3], vc_full[3], vc_empty[3];
   uint64_t q_ready;      // Q as fp16
   int dec[NDEC];
-  // Scale bytes (E_k, E_v) of block c, slot c % NE.  Slot reuse: block c + NE is
-  // converted after block c + NE - NKD's Q.K^T, whose S buffer was block c +
+  // Scale bytes (E_k, E_v; 0 where all values are) of block c, slot c % NE.  Slot
+  // reuse: block c + NE is converted after block c + NE - NKD's Q.K^T, whose S buffer was block c +
   // NE - NKD - NS's (NE - NKD - NS > 0), by then read by everyone.
   uint16_t esc[NE];
   int8_t qexp[BM];       // x of the query rows
-  // [S buffer][row] running max after the buffer's block (log2 units).  Row
-  // sums and exp references for the epilogue take the first two buffers' place
-  // at the end: row r's words are read and written by its two threads alone.
+  // [S buffer][row] running max after the buffer's block (log2 units; a quantised
+  // cache: the block's maximum).  Row sums and exp references (sref, ref) for the
+  // epilogue take the buffers' place at the end: row r's words are read and written
+  // by its two threads alone.
   // REP: the exponential warps take the maximum themselves, and the last buffer
   // holds the row maxima of the quarters' keys.
   float mdec[NS][BM];
@@ -340,15 +346,17 @@ __device__ __forceinline__ uint32_t row_factor(int byte, int top) {
 // brings the bytes of rows 4 l .. 4 l + 3.  Rows of byte 255 (NaN) do not count,
 // nor rows of zeros, which the writer gives byte 127: where that is the largest
 // byte, the codes are looked up in the cache (not in the staging area: a block's
-// values come after its scales).
+// values come after its scales).  0 for zeros alone.
 template <int FMT>
 __device__ __noinline__ int block_top_slow(const ChunkArgs &a, const TileInfo &x, int hk, int j,
                                            bool value, const uint8_t *scales, int lane, int left) {
   const KvPages &p = a.pages;
   int top = 0;
+  bool nan = false;
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * lane + i;
+    if (r < left && scales[r] == 255) nan = true;
     if (r >= left || scales[r] == 255) continue;
     uint32_t any = 1;
     if (scales[r] == 127) {
@@ -368,7 +376,7 @@ __device__ __noinline__ int block_top_slow(const ChunkArgs &a, const TileInfo &x
     if (any) top = max(top, (int)scales[r]);
   }
   top = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
-  return top ? top : 127;
+  return top || !__any_sync(0xffffffffu, nan) ? top : 127;
 }
 
 template <int FMT>
@@ -815,8 +823,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
     const int min_limit = a.causal ? x.pos0 + 1 : x.kv;             // the tile's smallest
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const float sl2 = a.scale * kLog2e;
-    float t2 = -INFINITY;  // running max of (row max + E_v), the exponentials' reference
-    float mref = -INFINITY, l = 0.f;
+    // Running maxima: of the row maxima, of (row max + E_v) (the same over bf16 rows);
+    // the exponentials' references, which lag behind them; row sum.
+    float t2 = -INFINITY, y2 = -INFINITY;
+    float mref = -INFINITY, yref = -INFINITY, l = 0.f;
     int kc = 0;
     bool ok = true;
     // A quantised cache: raw score to log2 units for a block of key exponent E_k,
@@ -877,13 +887,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
             tmem_wait_ld_regs(x3);
             mt = fmaxf(fmaxf(chunk_max(x0), chunk_max(x1)), fmaxf(chunk_max(x2), chunk_max(x3)));
           }
-          int ek = 0, ev = 127;
-          if constexpr (QUANT) {
-            const int e = sh.esc[c % NE];
-            ek = e & 255;
-            ev = e >> 8;
-          }
-          const float bl2 = QUANT ? block_sl2(ek) : sl2;
+          const float bl2 = QUANT ? block_sl2(sh.esc[c % NE] & 255) : sl2;
           if constexpr (REP) {
             if (!dense) {  // the rows' maxima over all four quarters' keys
               sh.mdec[2][r] = mt;  // (read before the vote barrier of the last block)
@@ -892,8 +896,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
                          fmaxf(sh.mdec[2][64 + lane], sh.mdec[2][96 + lane]));
             }
           } else {
-            t2 = fmaxf(t2, mt * bl2 + (float)(ev - 127));
-            sh.mdec[c % NS][r] = t2;
+            t2 = fmaxf(t2, mt * bl2);
+            sh.mdec[c % NS][r] = QUANT ? mt * bl2 : t2;
           }
           const float pm2 = mt * bl2;
           // With ln(lambda) < 0, "rowmax - m_new < c" is "rowmax - m_old < c".
@@ -934,34 +938,48 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
         if (!keep) continue;
         fence_after_sync();
         const uint32_t sa = lane_base + (c % NS) * BN;  // masked by the deciders
-        int ek = 0, ev = 127;
+        float e_v = 0.f, bl2 = sl2;
         if constexpr (QUANT) {
           const int e = sh.esc[c % NE];
-          ek = e & 255;
-          ev = e >> 8;
+          e_v = e >> 8 ? (float)((e >> 8) - 127) : -INFINITY;
+          bl2 = block_sl2(e & 255);
         }
-        const float bl2 = QUANT ? block_sl2(ek) : sl2;
         uint32_t own[REP ? 32 : 1];  // REP: the scores of the quarter's 32 keys
-        float mnew;
+        float mrow;
         if constexpr (REP) {
           tmem_ld32(sa + 32 * quarter, own);
           tmem_wait_ld_regs(own);
-          t2 = fmaxf(t2, chunk_max(own) * bl2 + (float)(ev - 127));
-          mnew = t2;
+          mrow = chunk_max(own) * bl2;
         } else {
-          mnew = sh.mdec[c % NS][r];
+          mrow = sh.mdec[c % NS][r];
         }
+        t2 = fmaxf(t2, mrow);
         bool rescale = false;
-        float alpha = 1.f;
-        if (mref == -INFINITY) {
-          mref = mnew;
-        } else if (valid && mnew > mref + kRescaleLog2) {
-          alpha = ex2(mref - mnew);
-          mref = mnew;
-          rescale = true;
+        float alpha = 1.f, lalpha = 1.f;  // of O, of l
+        auto follow = [&](float &ref, float now, float &factor) {
+          if (ref == -INFINITY) {
+            ref = now;
+          } else if (valid && now > ref + kRescaleLog2) {
+            factor = ex2(ref - now);
+            ref = now;
+            return true;
+          }
+          return false;
+        };
+        float f = 0.f;  // P is 2^f times a weight
+        if constexpr (QUANT) {
+          y2 = fmaxf(y2, mrow + e_v);
+          follow(mref, t2, lalpha);
+          rescale = follow(yref, y2, alpha);
+          // (Below 2^-40 P is 0 in fp16, whatever the weight, which has to stay in fp32's
+          // range; above 2^120 the weights are below 2^-100.)
+          if (yref != -INFINITY) f = fminf(fmaxf(mref + e_v - yref + kPLog2, -40.f), 120.f);
+        } else {
+          rescale = follow(mref, t2, alpha);
+          lalpha = alpha;
         }
         // A row without a visible key so far has only -inf scores: P = 0.
-        const float nref = mref == -INFINITY ? 0.f : (float)(ev - 127) - mref + (QUANT ? kPLog2 : 0.f);
+        const float nref = mref == -INFINITY ? 0.f : f - mref;
         const uint64_t sl2x2 = f2(bl2, bl2), negref2 = f2(nref, nref);
         uint64_t acc2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
         if constexpr (REP) {
@@ -1006,8 +1024,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
         f2_split(acc2[0], acc[0], acc[1]);
         f2_split(acc2[1], acc[2], acc[3]);
         float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-        if constexpr (QUANT) sum = sum * kPDown * __int_as_float(max(1, 254 - ev) << 23);
-        l = l * alpha + sum;
+        if constexpr (QUANT) sum *= ex2(-f);
+        l = l * lalpha + sum;
         if (__any_sync(0xffffffffu, rescale) && kc >= 1) {
           if (!wait_warp(&sh.pv_done[(kc - 1) % NS], (kc - 1) / NS)) {
             ok = false;
@@ -1035,6 +1053,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
       // No kept block: O was never written.
       sh.mdec[0][r] = kc > 0 ? l : 0.f;
       sh.mdec[1][r] = mref;
+      if constexpr (QUANT) sh.mdec[2][r] = yref;
       fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(&sh.l_full));
@@ -1076,7 +1095,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
         lref = sh.mdec[1][r];
         w = lrow == 0.f ? 0.f : 1.f;  // no key kept for this row: O = 0
       }
-      const float inv = lrow == 0.f ? 0.f : (QUANT ? kPDown * w : w) / lrow;
+      if (QUANT && w != 0.f) w = ex2(sh.mdec[2][r] - lref - kPLog2);
+      const float inv = lrow == 0.f ? 0.f : w / lrow;
       const bool none = w == 0.f;  // (the accumulator may hold anything)
       // The rows leave through 4 KB of the query tile a warp (free by now): a lane's
       // row in 16-byte pieces, then 128-byte runs of four rows an instruction.

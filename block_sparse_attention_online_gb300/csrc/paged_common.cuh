@@ -17,8 +17,7 @@ constexpr int BN = 128;  // keys per block
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;  // an exp reference may lag the max by 2^8
-// fp16 weights carry a factor 2^7: with the lag, up to fp16's 2^15.
-constexpr float kPLog2 = 7.0f, kPDown = 0.0078125f;
+constexpr float kPLog2 = 7.0f;  // fp16 weights carry a factor 2^7: with the lag, up to fp16's 2^15
 
 // The larger one, or a NaN if there is one (fmaxf drops it).
 __device__ __forceinline__ float max_nan(float a, float b) {

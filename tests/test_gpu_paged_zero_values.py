@@ -12,8 +12,8 @@ from tests.test_gpu_paged import DEV, FORMATS, attend, check, cu_of, filled_cach
 
 pytestmark = pytest.mark.gpu
 LN2 = math.log(2.0)
-# Tokens of 4 heads.
-TOKENS = (1,)
+# Tokens of 4 heads: 4, 20 and 80 rows of one tile, two tiles.
+TOKENS = (1, 5, 20, 40)
 
 
 def planted(fmt, scores, values, n, n_splits, lam=0.0, G=4):
