@@ -229,16 +229,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// A NaN among the scores is their maximum: a block that holds one is not skipped.
 __device__ __forceinline__ float chunk_max(const uint32_t (&s)[32]) {
   float m[11];
 #pragma unroll
   for (int i = 0; i < 10; ++i)
-    m[i] = fmax3(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]),
-                 __uint_as_float(s[3 * i + 2]));
-  m[10] = fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31]));
-  const float a = fmax3(m[0], m[1], m[2]), b = fmax3(m[3], m[4], m[5]);
-  const float c = fmax3(m[6], m[7], m[8]), d = fmaxf(m[9], m[10]);
-  return fmaxf(fmax3(a, b, c), d);
+    m[i] = max3_nan(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]),
+                    __uint_as_float(s[3 * i + 2]));
+  m[10] = max_nan(__uint_as_float(s[30]), __uint_as_float(s[31]));
+  const float a = max3_nan(m[0], m[1], m[2]), b = max3_nan(m[3], m[4], m[5]);
+  const float c = max3_nan(m[6], m[7], m[8]), d = max_nan(m[9], m[10]);
+  return max_nan(max3_nan(a, b, c), d);
 }
 
 // P = exp2(s * sl2 - ref) for 32 keys as 16 packed bf16 (fp16) pairs, the P.V
@@ -873,7 +874,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
               tmem_ld32(sa + 64 * hh + 32, x1);
               tmem_wait_ld_regs(x0);
               tmem_wait_ld_regs(x1);
-              mt = fmax3(mt, chunk_max(x0), chunk_max(x1));
+              mt = max3_nan(mt, chunk_max(x0), chunk_max(x1));
             }
           } else {
             uint32_t x0[32], x1[32], x2[32], x3[32];
@@ -885,15 +886,15 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
             tmem_wait_ld_regs(x1);
             tmem_wait_ld_regs(x2);
             tmem_wait_ld_regs(x3);
-            mt = fmaxf(fmaxf(chunk_max(x0), chunk_max(x1)), fmaxf(chunk_max(x2), chunk_max(x3)));
+            mt = max_nan(max_nan(chunk_max(x0), chunk_max(x1)), max_nan(chunk_max(x2), chunk_max(x3)));
           }
           const float bl2 = QUANT ? block_sl2(sh.esc[c % NE] & 255) : sl2;
           if constexpr (REP) {
             if (!dense) {  // the rows' maxima over all four quarters' keys
               sh.mdec[2][r] = mt;  // (read before the vote barrier of the last block)
               named_bar_sync(kDeciderBarrier, NQ * 32);
-              mt = fmaxf(fmaxf(sh.mdec[2][lane], sh.mdec[2][32 + lane]),
-                         fmaxf(sh.mdec[2][64 + lane], sh.mdec[2][96 + lane]));
+              mt = max_nan(max_nan(sh.mdec[2][lane], sh.mdec[2][32 + lane]),
+                           max_nan(sh.mdec[2][64 + lane], sh.mdec[2][96 + lane]));
             }
           } else {
             t2 = fmaxf(t2, mt * bl2);
@@ -903,7 +904,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
           // With ln(lambda) < 0, "rowmax - m_new < c" is "rowmax - m_old < c".
           const float diff = mt == -INFINITY ? -INFINITY : pm2 - m2;
           keep_vote = dense || !__all_sync(0xffffffffu, !valid || diff < c2 || mt == -INFINITY);
-          m2 = fmaxf(m2, pm2);
+          m2 = max_nan(m2, pm2);
           fence_before_sync();  // this warp's reads of S_j are complete
         } else if (REP && !dense) {
           named_bar_sync(kDeciderBarrier, NQ * 32);
@@ -1610,13 +1611,13 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
               tmem_ld32(sa + 64 * hh + 32, x1);
               tmem_wait_ld_regs(x0);
               tmem_wait_ld_regs(x1);
-              mt = fmax3(mt, chunk_max(x0), chunk_max(x1));
+              mt = max3_nan(mt, chunk_max(x0), chunk_max(x1));
             }
             const float pm2 = mt * sl2;
             // With ln(lambda) < 0, "rowmax - m_new < c" is "rowmax - m_old < c".
             const float diff = mt == -INFINITY ? -INFINITY : pm2 - m2;
             keep_vote = dense || !__all_sync(0xffffffffu, !valid || diff < c2 || mt == -INFINITY);
-            m2 = fmaxf(m2, pm2);
+            m2 = max_nan(m2, pm2);
             sh.mdec[g % NS][r] = m2;
             fence_before_sync();  // this warp's reads of S are complete
           }

@@ -697,10 +697,10 @@ __global__ void __launch_bounds__(NT, 2)
               float mt[2];
 #pragma unroll
               for (int n = 0; n < 2; ++n) {
-                float m = fmaxf(p[0][n], p[1][n]);
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                mt[n] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                float m = max_nan(p[0][n], p[1][n]);  // (a block with a NaN is not skipped)
+                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                mt[n] = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
               }
               if (g == 0) {
                 sh.rmax[c & 1][warp][2 * t] = mt[0];
@@ -715,11 +715,11 @@ __global__ void __launch_bounds__(NT, 2)
               for (int n = 0; n < 2; ++n) {
                 float m = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < NCW; ++w) m = fmaxf(m, sh.rmax[c & 1][w][2 * t + n]);
+                for (int w = 0; w < NCW; ++w) m = max_nan(m, sh.rmax[c & 1][w][2 * t + n]);
                 // With ln(lambda) < 0, "rowmax - m_new < c" is "rowmax - m_old < c".
                 const float diff = m == -INFINITY ? -INFINITY : m - m2[n];
                 vote = vote && (2 * t + n >= rows || diff < c2 || m == -INFINITY);
-                m2[n] = fmaxf(m2[n], m);
+                m2[n] = max_nan(m2[n], m);
               }
               keep = !__all_sync(0xffffffffu, vote);  // the same in every warp
               if (tid == 0) {

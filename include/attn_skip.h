@@ -609,8 +609,9 @@ attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
  * block axis is cut into n_splits ranges of bps = ceil(ceil(max_kv / 128) /
  * n_splits) blocks; each restarts its running max (FlashDecoding) and the
  * results are merged by log-sum-exp.  A tile skips a block of its split when
- * rowmax - m_new < ln(lambda) for all its rows.  A row that sees no key gets
- * O = 0, LSE = -inf.
+ * rowmax - m_new < ln(lambda) for all its rows; a NaN score is its row's maximum,
+ * so that a block in which a row sees one is kept, and the split's later ones.  A
+ * row that sees no key gets O = 0, LSE = -inf.
  *
  *  q           [total, Hq, 128] bf16, tokens q_tok_stride elements apart (a
  *              multiple of 8); query head h reads KV head h / G, 1 <= G <= 128
