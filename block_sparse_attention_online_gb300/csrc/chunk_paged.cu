@@ -1794,11 +1794,11 @@ __global__ void __launch_bounds__(P_WARPS * 32, 1)
 
 // Merge of the split partials: LSE = ln sum_s exp(LSE_s), O = sum_s
 // exp(LSE_s - LSE) O_s, splits without a key (LSE_s = -inf, O_s not written)
-// left out.  A warp takes ROWS query heads of a token, one after the other, four
-// columns a lane; rows behind the last sequence keep what they held.  One row a warp
-// is quickest for a decode step; with many rows the search for the sequence, once a
-// row, was half the merge (16 prompts of 1024 tokens, 32 heads: 325 us in all with four
-// rows a warp, 365 with one).
+// left out; a NaN in one of them is the row's.  A warp takes ROWS query heads of a
+// token, one after the other, four columns a lane; rows behind the last sequence keep
+// what they held.  One row a warp is quickest for a decode step; with many rows the
+// search for the sequence, once a row, was half the merge (16 prompts of 1024 tokens,
+// 32 heads: 325 us in all with four rows a warp, 365 with one).
 constexpr int MERGE_WARPS = 4, MERGE_ROWS = 4;
 template <int ROWS>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const ChunkArgs a) {
@@ -1827,9 +1827,9 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const ChunkArgs
     if (__float_as_uint(ls[0]) == kWholeRow) continue;
     float m = -INFINITY;
 #pragma unroll 1
-    for (int s = lane; s < a.n_splits; s += 32) m = fmaxf(m, ls[s]);
+    for (int s = lane; s < a.n_splits; s += 32) m = max_nan(m, ls[s]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     float z = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const float4 *op = reinterpret_cast<const float4 *>(a.o_part + row * a.n_splits * D) + lane;

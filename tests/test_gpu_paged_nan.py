@@ -53,3 +53,25 @@ def test_a_nan_key_is_not_skipped(fmt, n_seq, chunk, L, Hq, n_splits):
                 # its block and all behind it, as its maximum is NaN from there on.
                 kept = j % bps == 0 or (s % 2 == 0 and j >= at // 128 and j // bps == at // 128 // bps)
                 assert (b[s, :, t, j // bps, j % bps] == (not kept)).all(), (s, t, j)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [1, 6, 20, 60, 300])
+@pytest.mark.parametrize("n_splits", [1, 3])
+def test_a_nan_query_has_a_nan_lse(fmt, n, n_splits):
+    g = np.random.default_rng(n)
+    L, Hkv, Hq = 900, 2, 8
+    table, n_pages = tables((L,), 32, g)
+    kv = filled_cache(fmt, n_pages, 32, Hkv)
+    k, v = (torch.from_numpy(g.standard_normal((L, Hkv, 128))).to(DEV, torch.bfloat16)
+            for _ in range(2))
+    bs.attn_skip_kv_append(kv, k, v, cu_of([L]), i32([L]), table)
+    q = torch.from_numpy(g.standard_normal((n, Hq, 128))).to(DEV, torch.bfloat16)
+    bad = q.clone()
+    bad[n // 2, 3, 17] = float("nan")
+    _, (o, lse, _) = attend(kv, table, (n,), (L,), Hq, [0.0], n_splits=n_splits, q=bad)
+    _, (o0, l0, _) = attend(kv, table, (n,), (L,), Hq, [0.0], n_splits=n_splits, q=q)
+    assert torch.isnan(o[n // 2, 3]).all() and torch.isnan(lse[n // 2, 3])
+    here = torch.ones(n, Hq, dtype=torch.bool, device=DEV)
+    here[n // 2, 3] = False
+    assert torch.equal(o[here], o0[here]) and torch.equal(lse[here], l0[here])
