@@ -758,8 +758,8 @@ def attn_skip_kv_gather(kv, cu_rows, start, page_table, total, out_dtype=torch.b
                         stream=None):
     """Read rows back: positions start[s] (``None``: 0) and on of sequence s,
     cu_rows[s+1] - cu_rows[s] of them.  Returns dense ``(k, v)`` [total, Hkv,
-    128] of ``out_dtype`` (bf16 or fp32), or ``out``, rows of which behind the
-    last sequence stay as they were."""
+    128] of ``out_dtype`` (bf16 or fp32), or ``out``, rows of which before the
+    first sequence and behind the last one stay as they were."""
     if _elsewhere(kv, stream):
         with _switched(kv, stream):
             return attn_skip_kv_gather(kv, cu_rows, start, page_table, total, out_dtype, out)

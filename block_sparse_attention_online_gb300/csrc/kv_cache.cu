@@ -286,9 +286,10 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ K
       x[r][1].load(a.v_new, (t0 + r) * a.v_tok_stride + h * D + hl * 8);
     }
   int s = find_seq(a.cu_seqlens, a.n_seq, (int)t0, hl, hmask) - 1;
-  bool bad = false, fine = false;
-  int end = INT_MIN;  // the current sequence's last row + 1
-  int64_t shift = 0;  // position minus row
+  bool bad = false;
+  int end = INT_MIN;    // the current sequence's last row + 1
+  int first = INT_MAX;  // its first row that has a position
+  int64_t shift = 0;    // position minus row
   Place at{0, 0, 0};
 #pragma unroll
   for (int r = 0; r < kTok; ++r) {
@@ -304,13 +305,15 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ K
       shift = (int64_t)len - end;
       // The sequence's bounds and its length are checked as a whole, so that no
       // row of a sequence with a bad length is written.
-      fine = c0 >= 0 && c0 <= t && end <= a.total && len >= 0 &&
-             len <= (int64_t)a.max_pages * a.pages.page_size;
+      const bool fine = c0 >= 0 && c0 <= end && end <= a.total && len >= 0 &&
+                        len <= (int64_t)a.max_pages * a.pages.page_size;
       bad |= !fine;
       at.left = 0;
+      // (A chunk may be longer than its cache: rows before position 0 have no place.
+      // Nor have rows before the first sequence.)
+      first = fine ? max(c0, end - len) : INT_MAX;
     }
-    // (A chunk may be longer than its cache: rows before position 0 have no place.)
-    if (fine && shift + t >= 0) {
+    if (t >= first) {
       at = next_place<RowBytes<FMT>::value>(at, a.pages, a.page_table, a.max_pages, s, shift + t, h);
       bad |= !at.ok();
     }
@@ -404,8 +407,8 @@ __global__ void __launch_bounds__(NT) kv_gather_kernel(const __grid_constant__ K
   int s = find_seq(a.cu_rows, a.n_seq, (int)t0, hl, hmask) - 1;
   Raw raw[kTok][2];
   bool bad = false, fine = false;
-  int n = 0;  // rows of sequences (the others stay as they were)
-  int end = INT_MIN;
+  unsigned mine = 0;  // rows of sequences (the others stay as they were)
+  int c0 = 0, end = INT_MIN;
   int64_t shift = 0;  // position minus row
   Place at{0, 0, 0};
 #pragma unroll
@@ -417,13 +420,14 @@ __global__ void __launch_bounds__(NT) kv_gather_kernel(const __grid_constant__ K
         ++s;
       } while (s < a.n_seq && __ldg(a.cu_rows + s + 1) <= t);
       if (s >= a.n_seq) break;
-      const int c0 = __ldg(a.cu_rows + s);
+      c0 = __ldg(a.cu_rows + s);
       end = __ldg(a.cu_rows + s + 1);
       shift = (int64_t)(a.start ? __ldg(a.start + s) : 0) - c0;
-      fine = c0 >= 0 && c0 <= t;
+      fine = c0 >= 0 && c0 <= end;
       at.left = 0;
     }
-    n = r + 1;
+    if (fine && t < c0) continue;  // before the first sequence
+    mine |= 1u << r;
     if (fine)
       at = next_place<RowBytes<FMT>::value>(at, a.pages, a.page_table, a.max_pages, s, shift + t, h);
     bad |= !at.ok();
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(NT) kv_gather_kernel(const __grid_constant__ K
   }
 #pragma unroll
   for (int r = 0; r < kTok; ++r) {
-    if (r >= n) break;
+    if (!(mine >> r & 1u)) continue;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const Raw &y = raw[r][w];

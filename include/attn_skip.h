@@ -556,8 +556,8 @@ typedef struct {
  *                k_tok_stride / v_tok_stride elements apart (multiples of 8;
  *                slices of one fused projection are fine)
  *  cu_seqlens    [n_seq + 1] int32 (device): sequence s's new tokens are rows
- *                [cu_seqlens[s], cu_seqlens[s+1]); rows from cu_seqlens[n_seq]
- *                on are ignored
+ *                [cu_seqlens[s], cu_seqlens[s+1]); rows before cu_seqlens[0] and
+ *                from cu_seqlens[n_seq] on are ignored
  *  kv_len        [n_seq] int32 (device): cached length with the new tokens;
  *                the n new tokens take positions kv_len - n .. kv_len - 1
  *                (a position below 0, of a chunk longer than kv_len, is not
@@ -585,8 +585,8 @@ attn_status attn_skip_kv_append(const attn_kv_pages *kv, const void *k_new, cons
  *
  *  cu_rows  [n_seq + 1] int32 (device), start [n_seq] int32 (device) or NULL
  *           (all 0)
- *  k_out, v_out  [total, Hkv, 128] (out_dt); rows from cu_rows[n_seq] on stay
- *           as they were
+ *  k_out, v_out  [total, Hkv, 128] (out_dt); rows before cu_rows[0] and from
+ *           cu_rows[n_seq] on stay as they were
  * Errors as for attn_skip_kv_append; a position outside [0, max_pages *
  * page_size), of a page id out of range or of a sequence with bad bounds reads
  * as zeros and is reported by attn_skip_last_device_error (ATTN_EINVAL).
