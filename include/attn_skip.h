@@ -567,9 +567,10 @@ typedef struct {
  * EINVAL: a null pointer that the format needs, n_seq <= 0, total < 0, a bad
  * size, stride or alignment (16 bytes, 4 for int32 arrays).  The device arrays
  * are checked by the kernel: nothing is written for a sequence whose bounds or
- * length are out of range (kv_len above max_pages * page_size among them) nor
- * for a page id outside [0, n_pages), and attn_skip_last_device_error then
- * returns ATTN_EINVAL.  total = 0 launches nothing.
+ * length are out of range (bounds beyond total or decreasing, kv_len above
+ * max_pages * page_size) nor for a page id outside [0, n_pages), and
+ * attn_skip_last_device_error then returns ATTN_EINVAL (for a length: if the
+ * sequence has new rows).  total = 0 launches nothing.
  */
 attn_status attn_skip_kv_append(const attn_kv_pages *kv, const void *k_new, const void *v_new,
                                 attn_dtype dt, int64_t k_tok_stride, int64_t v_tok_stride,
