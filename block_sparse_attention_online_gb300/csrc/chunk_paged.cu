@@ -36,7 +36,8 @@
 // rate of any other; a bf16 pair takes five.  fp16's range is met by exponents
 // that cost nothing per score: with E_k and E_v the largest row-scale exponents
 // of a block's keys and values, the tiles hold code * 2^(e - E) (exact for e >=
-// E - 15, otherwise off by at most 2^-25 2^E), the scores of the block are
+// E - 15, otherwise off by at most 2^-25 2^E; NVFP4, whose block scale takes the
+// factor first, 7 times that), the scores of the block are
 // scaled by 2^E_k, and P takes 2^E_v: with sref the running max of the row maxima and
 // ref that of (row max + E_v), both of which may lag by 2^8,
 //     P'_c = 2^(s_c - sref + f),  f = sref + E_v - ref + 7,  l += 2^-f sum P'_c.
@@ -973,8 +974,9 @@ __global__ void __launch_bounds__(Cfg<FMT>::WARPS * 32, PAIR ? 2 : 1)
           follow(mref, t2, lalpha);
           rescale = follow(yref, y2, alpha);
           // (Below 2^-40 P is 0 in fp16, whatever the weight, which has to stay in fp32's
-          // range; above 2^120 the weights are below 2^-100.)
-          if (yref != -INFINITY) f = fminf(fmaxf(mref + e_v - yref + kPLog2, -40.f), 120.f);
+          // range; above 2^100 the weights are below 2^-85, and what is lost of them is
+          // nothing beside the row sum.)
+          if (yref != -INFINITY) f = fmaxf(mref + e_v - yref + kPLog2, -40.f);
         } else {
           rescale = follow(mref, t2, alpha);
           lalpha = alpha;

@@ -639,8 +639,9 @@ attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
  * Products accumulate in fp32; statistics and row sums are fp32.  P is rounded
  * to bf16 for the P.V product (to fp16 where a quantised cache is widened on the
  * chip, with steps of 2^-31 of the largest contribution at the small end).
- * There a row whose scale is 2^15 or more below the largest of its 128-row block
- * (of the rows that the tile sees) is rounded to 2^-25 of that scale.  Cache rows
+ * There, in tiles of more than 8 rows, the elements of a row whose scale is less
+ * than 2^-15 of the largest of its 128-row block (of the rows that the tile sees)
+ * are off by at most 2^-25 of that largest scale (NVFP4: 7 * 2^-25).  Cache rows
  * that no row of a tile sees (later tokens, rows at or past kv_len) may hold
  * anything: they have no part in its outputs.  A value row that is not finite, and
  * in sight of some row of a tile, reaches every row of it.
