@@ -789,7 +789,8 @@ def attn_skip_chunk_paged_splits(kv, n_seq, total, Hq, max_chunk, max_kv):
 
 
 def attn_skip_chunk_paged_kv_bytes(kv, n_seq, Hq, max_chunk, max_kv):
-    """Bytes of workspace in which attn_skip_chunk_paged widens ``kv`` first."""
+    """Bytes of workspace (up to 4 GiB) in which attn_skip_chunk_paged widens ``kv``
+    first."""
     return load().attn_skip_chunk_paged_kv_bytes(KV_FORMATS[kv.format], n_seq, Hq, kv.Hkv,
                                                  max_chunk, max_kv)
 
@@ -820,7 +821,8 @@ def attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_tab
     ``None`` without ``with_bits``.  ``out`` may pass these three, ``workspace``
     the partials ``(o_part [total, Hq, n_splits, 128], lse_part [total, Hq,
     n_splits])`` fp32 of n_splits > 1 and ``rows`` a uint8 tensor of at least
-    attn_skip_chunk_paged_kv_bytes bytes; they are allocated otherwise."""
+    attn_skip_chunk_paged_kv_bytes bytes (up to 4 GiB); they are allocated otherwise,
+    call by call."""
     if _elsewhere(kv, stream):
         with _switched(kv, stream):
             return attn_skip_chunk_paged(kv, q, cu_seqlens, max_chunk, kv_len, max_kv, page_table,

@@ -527,7 +527,8 @@ attn_status attn_skip_santa_decode_noalloc(const void *q, const void *k, const v
  *  page_size    16, 32, 64 or a multiple of 128; d = 128
  * Page tables are int32 [n_seq, max_pages] on the device: position p of
  * sequence s is slot p % page_size of page page_table[s, p / page_size].
- * Entries behind a sequence's last position are not read.
+ * All of the table has to be readable; entries behind a sequence's last position
+ * may hold anything, and may change during a call: they have no effect.
  */
 typedef enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1, ATTN_KV_NVFP4 = 2 } attn_kv_format;
 
@@ -632,10 +633,12 @@ attn_status attn_skip_kv_gather(const attn_kv_pages *kv, int n_seq, int total,
  *  o_part, lse_part  workspace of total * Hq * n_splits * 128 and total * Hq *
  *              n_splits floats for n_splits > 1 (else NULL is fine); calls
  *              that overlap on the GPU need their own
- *  kv_work     NULL, or attn_skip_chunk_paged_kv_bytes bytes of workspace: a
- *              quantised cache that many tiles read is first written there as
- *              bf16 rows (exact); with NULL, or 0 bytes, it is widened on the
- *              chip by every tile.  Calls that overlap need their own
+ *  kv_work     NULL, or attn_skip_chunk_paged_kv_bytes bytes of workspace (up to
+ *              4 GiB: 512 bytes for each KV head and position of n_seq sequences
+ *              of max_kv): a quantised cache that many tiles read is first
+ *              written there as bf16 rows (exact); with NULL, or 0 bytes, it is
+ *              widened on the chip by every tile.  Calls that overlap need their
+ *              own
  * Products accumulate in fp32; statistics and row sums are fp32.  P is rounded
  * to bf16 for the P.V product (to fp16 where a quantised cache is widened on the
  * chip, with steps of 2^-31 of the largest contribution at the small end).
