@@ -1942,11 +1942,13 @@ cudaError_t launch_fmt(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
 
 // The split count that a host-side model of the launch finds cheapest: waves of
 // CTAs (one an SM, or two of the decode kernel), each a set-up and its share of
-// the blocks, and the merge, a second launch (one sequence of 1000 tokens, bf16: 14.5
-// us without it and 10.9 in eight splits where the calls are captured in a graph, 17
-// and 23 where the host makes them one after another).  A long decode batch takes six at least: sequences of different
-// lengths fill the chip only in smaller pieces (24 sequences of 8192 to 32768
-// tokens, bf16: 295 us with 1 split, 288 with 3, 280 with 6, 303 with 16).
+// the blocks, and the merge, a second launch (one sequence of 1000 tokens, bf16: 14.4
+// us without it and 12.0 in eight splits where the calls are captured in a graph, 18
+// and 23 where the host makes them one after another; the count is for the latter,
+// and goes from 1 to 9 behind 1024 tokens).  A long decode batch takes six at least:
+// sequences of different lengths fill the chip only in smaller pieces (24 sequences
+// of 8192 to 32768 tokens, bf16: 295 us with 1 split, 288 with 3, 280 with 6, 303
+// with 16).
 int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv, int TT, int format) {
   const int rows = (128 / TT) * (TT < max_chunk ? TT : max_chunk);
   const bool small = format != kKvBf16 && rows <= 8;
@@ -1978,10 +1980,11 @@ int chunk_paged_splits(int n_seq, int total, int max_chunk, int max_kv, int Hkv,
 // is not.  Widening a 128-key block of a KV head once moves about 100 KB (15 ns
 // of the memory's time); converting it on the way costs each tile that reads it
 // 0.7 us of an SM, 5 ns of the chip, so from three tiles of a sequence on the
-// rows are written out (E4M3, 32 heads on 8: a chunk of 4096 on 16384, 1318 us
-// with converters and 698 with widened rows; 16 chunks of 96 on 8192, 419 and
-// 362; of 64, 290 and 304).  Not where they would take over 4 GiB: the
-// bound is the longest sequence's, for every sequence.
+// rows are written out (E4M3, 32 heads on 8: a chunk of 4096 on 16384, 1351 us
+// with converters and 677 with widened rows; 16 chunks of 96 on 8192, 341 and 298;
+// of 64, 227 and 249.  NVFP4: 1467 and 679, 367 and 301, 246 and 251).  Not where
+// they would take over 4 GiB: the bound is the longest sequence's, for every
+// sequence.
 size_t chunk_paged_kv_bytes(int n_seq, int max_chunk, int max_kv, int Hkv, int TT, int format) {
   if (format == kKvBf16 || (max_chunk + TT - 1) / TT < 3) return 0;
   const size_t rows = (size_t)n_seq * Hkv * (((size_t)max_kv + BN - 1) / BN * BN);

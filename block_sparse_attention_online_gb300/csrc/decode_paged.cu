@@ -251,13 +251,14 @@ __device__ __noinline__ bool zero_row(const ChunkArgs &a, const Item &item, int 
 // one list, sequence by sequence and head by head, cut into equal runs (a tile may
 // be cut anywhere; its partials take the slots in order); otherwise the list is of
 // the pieces that have blocks, whose bounds the running maxima need, and a CTA
-// takes every gridDim.x-th.  24 sequences of 8192 to 32768 tokens, NVFP4: 152 us,
-// 188 with a CTA a piece; E4M3 154 and 164.  (16 sequences of one length, E4M3, bound
-// by memory: 177 and 172, since equal runs do not follow the SMs' different distances
+// takes every gridDim.x-th.  24 sequences of 8192 to 32768 tokens, NVFP4: 153 us,
+// 189 with a CTA a piece; E4M3 152 and 170.  (16 sequences of one length, E4M3, bound
+// by memory: 178 and 172, since equal runs do not follow the SMs' different distances
 // to memory; two or three rounds of shorter runs cost more than they bring.  Whole
-// pieces the hardware's scheduler spreads better: with thresholds 233 us against 242;
-// whole tiles, one split, are left to it: 100 sequences of up to 4000, NVFP4, 104 and
-// 121.)
+// pieces the hardware's scheduler spreads better, but the host cannot tell which
+// batches have thresholds: NVFP4 261 us against the list's 280, E4M3 238 and 252;
+// whole tiles, one split, are left to it: 100 sequences of up to 4000, NVFP4, 104 us
+// and 121.)
 constexpr int SEQS = 4;  // sequences a lane keeps: up to 128
 
 struct Plan {  // (32 sequences at a time: mostly there are no more)
@@ -596,7 +597,9 @@ __global__ void __launch_bounds__(NT, 2)
     // With a threshold, a block's product with its values comes after the next block's
     // scores: between the decision to keep a block and the use of its values lies a
     // block's time, in which they arrive (16 sequences of 32768 tokens, E4M3, lambda
-    // 1e-3: 221 us, 301 without).  A dense tile has its values in time anyway.
+    // 1e-3: 221 us, 301 without, before the row sums' own reference; 220 with it).
+    // Dense, the same takes 178: the vote, an exchange of all warps a block, costs more
+    // than the values that it saves.  A dense tile has its values in time anyway.
     uint32_t b0 = 0, b1 = 0;  // P of the product to come
     bool pending = false;
     auto blocks = [&](auto threshold) {
