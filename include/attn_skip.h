@@ -550,8 +550,9 @@ typedef struct {
  * NVFP4: with y = x / 2^e, the block scale b is the smallest E4M3 value with
  * 6 b >= max|y| over the 16 elements, code = E2M1(y / b) rounded to nearest
  * even.  A row with an infinity or a NaN is stored as a NaN row (scale byte
- * 255, codes 0).  ATTN_KV_BF16 rounds fp32 rows to nearest even and keeps
- * bf16 rows, whatever they hold.
+ * 255, codes 0).  An element of 1.6 * 2^127 and more may round to 2^128, which
+ * reads back as an infinity.  ATTN_KV_BF16 rounds fp32 rows to nearest even and
+ * keeps bf16 rows, whatever they hold.
  *
  *  k_new, v_new  [total, Hkv, 128] (dt: ATTN_BF16 or ATTN_F32), tokens
  *                k_tok_stride / v_tok_stride elements apart (multiples of 8;
