@@ -35,7 +35,8 @@ EXPORTED = ("attn_skip_prefill", "attn_skip_prefill_from_host", "attn_skip_prefi
             "attn_skip_santa_workspace", "attn_skip_santa_decode",
             "attn_skip_santa_decode_noalloc", "attn_skip_kv_append", "attn_skip_kv_gather",
             "attn_skip_chunk_paged", "attn_skip_chunk_paged_splits",
-            "attn_skip_chunk_paged_kv_bytes")
+            "attn_skip_chunk_paged_kv_bytes", "attn_skip_pages_reserve", "attn_skip_pages_fork",
+            "attn_skip_kv_copy_pages", "attn_skip_kv_compact", "attn_skip_verify_drafts")
 
 #: Samplers of attn_skip_santa_decode.
 SANTA_MODES = {"iid": 0, "sys": 1, "strat": 2}
@@ -111,6 +112,11 @@ def load() -> ctypes.CDLL:
     lib.attn_skip_chunk_paged_kv_bytes.restype = ctypes.c_size_t
     lib.attn_skip_chunk_paged_splits.argtypes = [i] * 7
     lib.attn_skip_chunk_paged_splits.restype = ctypes.c_int
+    lib.attn_skip_pages_reserve.argtypes = [P, i, P, i, i, i, P, P, P, P, P, P]
+    lib.attn_skip_pages_fork.argtypes = [P, i, P, i, i, i, P, P, i, P, P, P]
+    lib.attn_skip_kv_copy_pages.argtypes = [P, i, i, P, P, P]
+    lib.attn_skip_kv_compact.argtypes = [P, i, i, i, P, P, i, P, P, i, P, i, P]
+    lib.attn_skip_verify_drafts.argtypes = [P, i64, P, i64, i, i, i, i, i, P, P, P, P, P, P, P]
     lib.attn_skip_status_string.argtypes = [i]
     lib.attn_skip_status_string.restype = ctypes.c_char_p
     for fn in ("attn_skip_prefill", "attn_skip_prefill_blocks", "attn_skip_prefill_varlen",
@@ -121,7 +127,8 @@ def load() -> ctypes.CDLL:
                "attn_skip_selftest_wait_timeout", "attn_skip_last_device_error",
                "attn_skip_santa_workspace", "attn_skip_santa_decode",
                "attn_skip_santa_decode_noalloc", "attn_skip_kv_append", "attn_skip_kv_gather",
-               "attn_skip_chunk_paged"):
+               "attn_skip_chunk_paged", "attn_skip_pages_reserve", "attn_skip_pages_fork",
+               "attn_skip_kv_copy_pages", "attn_skip_kv_compact", "attn_skip_verify_drafts"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -652,7 +659,7 @@ class PagedKV:
         p = [x.data_ptr() if x is not None else None for x in (k, v, k_scale, v_scale, k_bs, v_bs)]
         # The page stride matters, and is meaningful, only between pages.
         stride = k.stride(0) * k.element_size() if n_pages > 1 else 0
-        self._fmt = code
+        self._fmt, self.n_layers = code, 1
         self._c = _KvPages(code, n_pages, page_size, Hkv, d, stride, *p)
         self._ref = ctypes.byref(self._c)
 
@@ -884,6 +891,208 @@ def _like(name, x, shape, dtype, kv):
     if x.shape != shape or x.dtype is not dtype or not x.is_contiguous() \
             or x.get_device() != kv.index:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {kv.device}")
+
+
+class PagedLayers:
+    """The caches (:class:`PagedKV`) of several layers, one shape and one device,
+    for the calls that move pages or rows in all of them at once."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        if not caches:
+            raise ValueError("at least one cache is needed")
+        one = caches[0]
+        for kv in caches:
+            if (kv.format, kv.n_pages, kv.page_size, kv.Hkv, kv.index) != \
+                    (one.format, one.n_pages, one.page_size, one.Hkv, one.index) or \
+                    kv._c.page_stride != one._c.page_stride:
+                raise ValueError("the caches must agree in format, shape, page stride and device")
+        self.caches = caches
+        self.n_layers, self.Hkv, self.device, self.index = len(caches), one.Hkv, one.device, one.index
+        self._c = (_KvPages * len(caches))(*(kv._c for kv in caches))
+        self._ref = ctypes.byref(self._c)
+
+
+def _ints(name, x, shape, where):
+    if x.shape != shape or x.dtype is not _int32 or not x.is_contiguous() \
+            or x.get_device() != where.index:
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {where.device}")
+
+
+def attn_skip_kv_copy_pages(kv, src, dst, stream=None):
+    """Copy page src[i] to page dst[i] (int32 device tensors [n_pairs]; -1 in
+    either: nothing to copy) of the cache ``kv``, a :class:`PagedKV` or
+    :class:`PagedLayers` (in every layer)."""
+    if _elsewhere(kv, stream):
+        with _switched(kv, stream):
+            return attn_skip_kv_copy_pages(kv, src, dst)
+    n = src.numel()
+    _ints("src", src, (n,), kv)
+    _ints("dst", dst, (n,), kv)
+    st = (_lib or load()).attn_skip_kv_copy_pages(kv._ref, kv.n_layers, n, src.data_ptr(),
+                                                  dst.data_ptr(), _raw_stream(kv.index))
+    if st:
+        _check("attn_skip_kv_copy_pages", st)
+
+
+def attn_skip_kv_compact(kv, keep, cu_keep, page_table, start=None, out_table=None, stream=None):
+    """Move the rows that are kept together: the row of position keep[cu_keep[s] + j]
+    of sequence s becomes that of position start[s] + j (``None``: j), in place or in
+    the pages of ``out_table`` [n_seq, out_max_pages].  ``kv`` is a :class:`PagedKV`
+    or :class:`PagedLayers`; keep is int32 [total], or [Hkv, total] for rows of each
+    head's own; cu_keep [n_seq + 1], page_table [n_seq, max_pages], start [n_seq]
+    int32.  In place keep[cu_keep[s] + j] >= start[s] + j has to hold."""
+    if _elsewhere(kv, stream):
+        with _switched(kv, stream):
+            return attn_skip_kv_compact(kv, keep, cu_keep, page_table, start, out_table)
+    n, max_pages = _batch(kv, cu_keep, page_table, start)
+    total = keep.shape[-1]
+    per_head = keep.dim() == 2
+    _ints("keep", keep, (kv.Hkv, total) if per_head else (total,), kv)
+    out, out_pages = None, 0
+    if out_table is not None:
+        out_pages = out_table.shape[-1]
+        _ints("out_table", out_table, (n, out_pages), kv)
+        out = out_table.data_ptr()
+    st = (_lib or load()).attn_skip_kv_compact(
+        kv._ref, kv.n_layers, n, total, cu_keep.data_ptr(), keep.data_ptr(), per_head,
+        None if start is None else start.data_ptr(), page_table.data_ptr(), max_pages, out,
+        out_pages, _raw_stream(kv.index))
+    if st:
+        _check("attn_skip_kv_compact", st)
+
+
+class _On:
+    """A tensor's device, for the calls without a cache."""
+
+    def __init__(self, x):
+        if not x.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        self.index, self.device = x.get_device(), x.device
+
+
+def _tables(refs, page_table, kv_len, new_len, on):
+    if refs.dim() != 1 or page_table.dim() != 2:
+        raise ValueError("refs must be [n_pages] and page_table [n_seq, max_pages]")
+    n = page_table.shape[0]
+    _ints("refs", refs, (refs.numel(),), on)
+    _ints("page_table", page_table, page_table.shape, on)
+    _ints("kv_len", kv_len, (n,), on)
+    return n
+
+
+def attn_skip_pages_reserve(refs, page_table, kv_len, new_len, page_size, out=None, stream=None):
+    """Pages for sequences that grow from kv_len to new_len positions: refs
+    [n_pages] and page_table [n_seq, max_pages] are updated.  Returns ``(got_len,
+    copy_src, copy_dst)`` [n_seq] (or fills ``out``, whose got_len may be kv_len): the
+    length that each sequence now has room for (kv_len where the pages ran out) and
+    the pages to copy, for :func:`attn_skip_kv_copy_pages`.  All int32."""
+    on = _On(refs)
+    if _elsewhere(on, stream):
+        with _switched(on, stream):
+            return attn_skip_pages_reserve(refs, page_table, kv_len, new_len, page_size, out)
+    n = _tables(refs, page_table, kv_len, new_len, on)
+    _ints("new_len", new_len, (n,), on)
+    if out is None:
+        got, src, dst = out = torch.empty((3, n), dtype=_int32, device=on.device).unbind(0)
+    else:
+        got, src, dst = out
+        for x in out:
+            _ints("out", x, (n,), on)
+    st = (_lib or load()).attn_skip_pages_reserve(
+        refs.data_ptr(), refs.numel(), page_table.data_ptr(), n, page_table.shape[1], page_size,
+        kv_len.data_ptr(), new_len.data_ptr(), got.data_ptr(), src.data_ptr(), dst.data_ptr(),
+        _raw_stream(on.index))
+    if st:
+        _check("attn_skip_pages_reserve", st)
+    return out
+
+
+def attn_skip_pages_fork(refs, page_table, kv_len, new_len, page_size, parent=None, out_table=None,
+                         stream=None):
+    """The next batch takes over pages of this one's: its sequence d the first
+    new_len[d] positions of row parent[d] of page_table [n_seq, max_pages] (-1: an
+    empty sequence), as row d of ``out_table`` [n_new, max_pages] (made here if not
+    given, filled up with -1); refs follows.  Without ``parent`` every sequence
+    keeps its row and is cut to new_len.  Returns the new batch's table.  All int32."""
+    on = _On(refs)
+    if _elsewhere(on, stream):
+        with _switched(on, stream):
+            return attn_skip_pages_fork(refs, page_table, kv_len, new_len, page_size, parent,
+                                        out_table)
+    n = _tables(refs, page_table, kv_len, new_len, on)
+    n_new, par, out = n, None, None
+    if parent is None:
+        if out_table is not None:
+            raise ValueError("out_table goes with parent")
+    else:
+        n_new = parent.numel()
+        _ints("parent", parent, (n_new,), on)
+        shape = (n_new, page_table.shape[1])
+        if out_table is None:
+            out_table = torch.full(shape, -1, dtype=_int32, device=on.device)
+        else:
+            _ints("out_table", out_table, shape, on)
+        par, out = parent.data_ptr(), out_table.data_ptr()
+    _ints("new_len", new_len, (n_new,), on)
+    st = (_lib or load()).attn_skip_pages_fork(
+        refs.data_ptr(), refs.numel(), page_table.data_ptr(), n, page_table.shape[1], page_size,
+        kv_len.data_ptr(), new_len.data_ptr(), n_new, par, out, _raw_stream(on.index))
+    if st:
+        _check("attn_skip_pages_fork", st)
+    return page_table if parent is None else out_table
+
+
+def _rows_of(name, x, rows, V, dtype, on):
+    """Row stride of the probabilities x [at least rows, V]."""
+    if x.dim() != 2 or x.shape[0] < rows or x.shape[1] != V or x.dtype is not dtype \
+            or x.get_device() != on.index:
+        raise ValueError(f"{name} must be a {dtype} tensor [{rows}, {V}] on {on.device}")
+    if V > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < V:
+        raise ValueError(f"the rows of {name} must be dense and must not overlap")
+    return x.stride(0) if rows > 1 else V
+
+
+def attn_skip_verify_drafts(target, drafted, cu_drafts, max_draft, u_accept, u_sample, draft=None,
+                            out=None, stream=None):
+    """Accept or replace drafted tokens.  ``target`` [total + n_seq, V] fp32 or bf16
+    holds the target's probabilities (sequence s from row cu_drafts[s] + s on, one
+    more than it has drafted tokens), ``draft`` [total, V] those that the tokens
+    ``drafted`` [total] were drawn from (``None``: they are not random); cu_drafts
+    [n_seq + 1] int32; u_accept [total] and u_sample [n_seq] fp32 random numbers in
+    [0, 1).  Returns int32 ``(tokens [n_seq, max_draft + 1], n_accepted [n_seq])``, or
+    fills ``out``: the accepted tokens, one drawn token, -1 behind it."""
+    on = _On(target)
+    if _elsewhere(on, stream):
+        with _switched(on, stream):
+            return attn_skip_verify_drafts(target, drafted, cu_drafts, max_draft, u_accept,
+                                           u_sample, draft, out)
+    n, total, dt = cu_drafts.numel() - 1, drafted.numel(), _dtype_code(target)
+    if target.dim() != 2 or n < 1 or max_draft < 0:
+        raise ValueError("target must be [total + n_seq, V], cu_drafts [n_seq + 1], max_draft >= 0")
+    V = target.shape[1]
+    stride = _rows_of("target", target, total + n, V, target.dtype, on)
+    draft_stride = 0
+    if draft is not None:
+        draft_stride = _rows_of("draft", draft, total, V, target.dtype, on)
+    _ints("drafted", drafted, (total,), on)
+    _ints("cu_drafts", cu_drafts, (n + 1,), on)
+    _per_sequence("u_accept", u_accept, total, _float32, on)
+    _per_sequence("u_sample", u_sample, n, _float32, on)
+    if out is None:
+        tokens = torch.empty((n, max_draft + 1), dtype=_int32, device=on.device)
+        accepted = torch.empty((n,), dtype=_int32, device=on.device)
+    else:
+        tokens, accepted = out
+        _ints("tokens", tokens, (n, max_draft + 1), on)
+        _ints("n_accepted", accepted, (n,), on)
+    st = (_lib or load()).attn_skip_verify_drafts(
+        target.data_ptr(), stride, None if draft is None else draft.data_ptr(), draft_stride, dt, V,
+        n, total, max_draft, drafted.data_ptr(), cu_drafts.data_ptr(), u_accept.data_ptr(),
+        u_sample.data_ptr(), tokens.data_ptr(), accepted.data_ptr(), _raw_stream(on.index))
+    if st:
+        _check("attn_skip_verify_drafts", st)
+    return tokens, accepted
 
 
 def attn_skip_selftest_wait_timeout(stream=None, device=None):

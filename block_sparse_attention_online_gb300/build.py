@@ -20,7 +20,7 @@ LIB = os.path.join(BUILD, "libattn_skip.so")
 SOURCES = ["api.cu", "prefill_f32.cu", "prefill_tc.cu", "decode.cu", "mla_decode.cu",
            "combine.cu", "selftest.cu", "santa.cu", "santa_noalloc.cu", "decode_fp8.cu",
            "decode_nvfp4.cu", "mla_cluster.cu", "kv_cache.cu", "chunk_paged.cu",
-           "decode_paged.cu"]
+           "decode_paged.cu", "page_tables.cu", "kv_move.cu", "verify_drafts.cu"]
 HEADERS = [os.path.join(ROOT, "include", "attn_skip.h")] + [
     os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

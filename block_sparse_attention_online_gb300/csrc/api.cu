@@ -525,27 +525,22 @@ constexpr int kMaxPositions = 1 << 30;  // positions of a sequence: int arithmet
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
-// The checks that the paged-cache calls share; fills the kernels' view.
-attn_status pages_check(const attn_kv_pages *kv, int n_seq, int total, const int32_t *cu,
-                        const int32_t *page_table, int max_pages, KvPages &p) {
-  if (!kv || !kv->k || !kv->v || !cu || !page_table) return ATTN_EINVAL;
+// The cache's own description; fills the kernels' view of it.
+attn_status cache_check(const attn_kv_pages *kv, KvPages &p) {
+  if (!kv || !kv->k || !kv->v) return ATTN_EINVAL;
   if (kv->format != ATTN_KV_BF16 && kv->format != ATTN_KV_E4M3 && kv->format != ATTN_KV_NVFP4)
     return ATTN_EINVAL;
-  if (n_seq <= 0 || total < 0 || kv->n_pages <= 0 || kv->page_size <= 0 || kv->Hkv <= 0 ||
-      kv->d <= 0 || max_pages <= 0)
-    return ATTN_EINVAL;
+  if (kv->n_pages <= 0 || kv->page_size <= 0 || kv->Hkv <= 0 || kv->d <= 0) return ATTN_EINVAL;
   const int ps = kv->page_size;
   if (kv->d != 128) return ATTN_EUNSUPPORTED;
   if (ps != 16 && ps != 32 && ps != 64 && ps % 128 != 0) return ATTN_EUNSUPPORTED;
-  if ((int64_t)max_pages * ps > kMaxPositions || (int64_t)kv->Hkv * ps > kMaxPositions)
-    return ATTN_EUNSUPPORTED;
+  if ((int64_t)kv->Hkv * ps > kMaxPositions) return ATTN_EUNSUPPORTED;
   const int64_t row = kv->format == ATTN_KV_BF16 ? 256 : kv->format == ATTN_KV_E4M3 ? 128 : 64;
   const int64_t dense = (int64_t)kv->Hkv * ps * row;
   if (kv->page_stride != 0 && (kv->page_stride < dense || kv->page_stride % 16 != 0 ||
                                kv->page_stride >= (int64_t)1 << 40))
     return ATTN_EINVAL;
-  if (!aligned16(kv->k) || !aligned16(kv->v) || !aligned4(cu) || !aligned4(page_table))
-    return ATTN_EINVAL;
+  if (!aligned16(kv->k) || !aligned16(kv->v)) return ATTN_EINVAL;
   if (kv->format != ATTN_KV_BF16 && (!kv->k_scale || !kv->v_scale || !aligned16(kv->k_scale) ||
                                      !aligned16(kv->v_scale)))
     return ATTN_EINVAL;
@@ -560,6 +555,51 @@ attn_status pages_check(const attn_kv_pages *kv, int n_seq, int total, const int
   p.k_scale = kv->k_scale; p.v_scale = kv->v_scale;
   p.k_bs = kv->k_bs; p.v_bs = kv->v_bs;
   return ATTN_OK;
+}
+
+// The checks that the calls over a batch of sequences share.
+attn_status pages_check(const attn_kv_pages *kv, int n_seq, int total, const int32_t *cu,
+                        const int32_t *page_table, int max_pages, KvPages &p) {
+  if (!cu || !page_table) return ATTN_EINVAL;
+  if (n_seq <= 0 || total < 0 || max_pages <= 0) return ATTN_EINVAL;
+  const attn_status st = cache_check(kv, p);
+  if (st != ATTN_OK) return st;
+  if ((int64_t)max_pages * kv->page_size > kMaxPositions) return ATTN_EUNSUPPORTED;
+  if (!aligned4(cu) || !aligned4(page_table)) return ATTN_EINVAL;
+  return ATTN_OK;
+}
+
+// The caches of several layers have to be of one shape; a launch takes up to
+// kMaxLayers of them.
+attn_status layers_check(const attn_kv_pages *kv, int n_layers) {
+  if (!kv || n_layers <= 0) return ATTN_EINVAL;
+  for (int i = 0; i < n_layers; ++i) {
+    KvPages p{};
+    const attn_status st = cache_check(kv + i, p);
+    if (st != ATTN_OK) return st;
+    if (kv[i].format != kv->format || kv[i].n_pages != kv->n_pages ||
+        kv[i].page_size != kv->page_size || kv[i].Hkv != kv->Hkv ||
+        kv[i].page_stride != kv->page_stride)
+      return ATTN_EINVAL;
+  }
+  return ATTN_OK;
+}
+
+void layers_take(const attn_kv_pages *kv, int n_layers, KvLayers &l) {
+  KvPages p{};
+  cache_check(kv, p);
+  l.n = n_layers < kMaxLayers ? n_layers : kMaxLayers;
+  l.format = p.format; l.n_pages = p.n_pages; l.page_size = p.page_size; l.Hkv = p.Hkv;
+  l.page_shift = p.page_shift; l.page_stride = p.page_stride;
+  for (int i = 0; i < l.n; ++i) {
+    l.layer[i].k = (uint8_t *)kv[i].k; l.layer[i].v = (uint8_t *)kv[i].v;
+    l.layer[i].k_scale = kv[i].k_scale; l.layer[i].v_scale = kv[i].v_scale;
+    l.layer[i].k_bs = kv[i].k_bs; l.layer[i].v_bs = kv[i].v_bs;
+  }
+}
+
+attn_status from_launch(cudaError_t e) {
+  return e == cudaErrorNotYetImplemented ? ATTN_EUNSUPPORTED : from_cuda(e);
 }
 
 }  // namespace
@@ -678,6 +718,150 @@ extern "C" attn_status attn_skip_chunk_paged(
   if ((int64_t)total * Hq > (int64_t)0x7fffffff * 4) return ATTN_EUNSUPPORTED;
   const cudaError_t l = launch_chunk_paged(a, (cudaStream_t)stream);
   return l == cudaErrorNotYetImplemented ? ATTN_EUNSUPPORTED : from_cuda(l);
+}
+
+extern "C" attn_status attn_skip_kv_copy_pages(const attn_kv_pages *kv, int n_layers, int n_pairs,
+                                               const int32_t *src, const int32_t *dst,
+                                               void *stream) {
+  const attn_status st = layers_check(kv, n_layers);
+  if (st != ATTN_OK) return st;
+  if (n_pairs < 0) return ATTN_EINVAL;
+  if (n_pairs == 0) return ATTN_OK;
+  if (!src || !dst || !aligned4(src) || !aligned4(dst)) return ATTN_EINVAL;
+  CopyPagesArgs a{};
+  a.n_pairs = n_pairs; a.src = src; a.dst = dst;
+  const cudaError_t e = error_word(&a.err);
+  if (e != cudaSuccess) return from_cuda(e);
+  for (int i = 0; i < n_layers; i += kMaxLayers) {
+    layers_take(kv + i, n_layers - i, a.kv);
+    const attn_status l = from_launch(launch_kv_copy_pages(a, (cudaStream_t)stream));
+    if (l != ATTN_OK) return l;
+  }
+  return ATTN_OK;
+}
+
+extern "C" attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layers, int n_seq,
+                                            int total, const int32_t *cu_keep,
+                                            const int32_t *keep, int per_head,
+                                            const int32_t *start, const int32_t *page_table,
+                                            int max_pages, const int32_t *out_table,
+                                            int out_max_pages, void *stream) {
+  attn_status st = layers_check(kv, n_layers);
+  if (st != ATTN_OK) return st;
+  KvPages p{};
+  st = pages_check(kv, n_seq, total, cu_keep, page_table, max_pages, p);
+  if (st != ATTN_OK) return st;
+  if (!aligned4(start) || !aligned4(out_table)) return ATTN_EINVAL;
+  if (out_table && out_max_pages <= 0) return ATTN_EINVAL;
+  if (out_table && (int64_t)out_max_pages * kv->page_size > kMaxPositions) return ATTN_EUNSUPPORTED;
+  if (total == 0) return ATTN_OK;
+  if (!keep || !aligned4(keep)) return ATTN_EINVAL;
+  CompactArgs a{};
+  a.n_seq = n_seq; a.total = total; a.max_pages = max_pages; a.out_max_pages = out_max_pages;
+  a.per_head = per_head ? 1 : 0;
+  a.cu_keep = cu_keep; a.keep = keep; a.start = start; a.table = page_table;
+  a.out_table = out_table == page_table ? nullptr : out_table;
+  const cudaError_t e = error_word(&a.err);
+  if (e != cudaSuccess) return from_cuda(e);
+  for (int i = 0; i < n_layers; i += kMaxLayers) {
+    layers_take(kv + i, n_layers - i, a.kv);
+    st = from_launch(launch_kv_compact(a, (cudaStream_t)stream));
+    if (st != ATTN_OK) return st;
+  }
+  return ATTN_OK;
+}
+
+namespace attn_skip {
+namespace {
+
+// What reserve and fork take alike.
+attn_status tables_check(const int32_t *refs, int n_pages, const int32_t *page_table, int n_seq,
+                         int max_pages, int page_size, const int32_t *kv_len,
+                         const int32_t *new_len) {
+  if (!refs || !page_table || !kv_len || !new_len || n_pages <= 0 || n_seq <= 0 || max_pages <= 0 ||
+      page_size <= 0)
+    return ATTN_EINVAL;
+  if (!aligned4(refs) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(new_len))
+    return ATTN_EINVAL;
+  if ((int64_t)max_pages * page_size > kMaxPositions) return ATTN_EUNSUPPORTED;
+  return ATTN_OK;
+}
+
+}  // namespace
+}  // namespace attn_skip
+
+extern "C" attn_status attn_skip_pages_reserve(int32_t *refs, int n_pages, int32_t *page_table,
+                                               int n_seq, int max_pages, int page_size,
+                                               const int32_t *kv_len, const int32_t *new_len,
+                                               int32_t *got_len, int32_t *copy_src,
+                                               int32_t *copy_dst, void *stream) {
+  const attn_status st =
+      tables_check(refs, n_pages, page_table, n_seq, max_pages, page_size, kv_len, new_len);
+  if (st != ATTN_OK) return st;
+  if (!got_len || !copy_src || !copy_dst || !aligned4(got_len) || !aligned4(copy_src) ||
+      !aligned4(copy_dst))
+    return ATTN_EINVAL;
+  if ((size_t)n_seq > pages_reserve_max_seqs() || (size_t)n_pages > pages_reserve_max_pages())
+    return ATTN_EUNSUPPORTED;
+  ReserveArgs a{};
+  a.refs = refs; a.table = page_table;
+  a.n_pages = n_pages; a.n_seq = n_seq; a.max_pages = max_pages; a.page_size = page_size;
+  a.kv_len = kv_len; a.new_len = new_len;
+  a.got_len = got_len; a.copy_src = copy_src; a.copy_dst = copy_dst;
+  const cudaError_t e = error_word(&a.err);
+  if (e != cudaSuccess) return from_cuda(e);
+  return from_cuda(launch_pages_reserve(a, (cudaStream_t)stream));
+}
+
+extern "C" attn_status attn_skip_pages_fork(int32_t *refs, int n_pages, const int32_t *page_table,
+                                            int n_seq, int max_pages, int page_size,
+                                            const int32_t *kv_len, const int32_t *new_len,
+                                            int n_new, const int32_t *parent, int32_t *out_table,
+                                            void *stream) {
+  const attn_status st =
+      tables_check(refs, n_pages, page_table, n_seq, max_pages, page_size, kv_len, new_len);
+  if (st != ATTN_OK) return st;
+  if (parent && (n_new <= 0 || !out_table || out_table == page_table || !aligned4(parent) ||
+                 !aligned4(out_table)))
+    return ATTN_EINVAL;
+  if ((int64_t)n_seq + (parent ? n_new : 0) > 0x7fffffff) return ATTN_EUNSUPPORTED;
+  ForkArgs a{};
+  a.refs = refs; a.out_table = out_table; a.table = page_table;
+  a.kv_len = kv_len; a.new_len = new_len; a.parent = parent;
+  a.n_pages = n_pages; a.n_seq = n_seq; a.n_new = n_new; a.max_pages = max_pages;
+  a.page_size = page_size;
+  const cudaError_t e = error_word(&a.err);
+  if (e != cudaSuccess) return from_cuda(e);
+  return from_cuda(launch_pages_fork(a, (cudaStream_t)stream));
+}
+
+extern "C" attn_status attn_skip_verify_drafts(
+    const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,
+    attn_dtype dt, int V, int n_seq, int total, int max_draft, const int32_t *drafted,
+    const int32_t *cu_drafts, const float *u_accept, const float *u_sample, int32_t *tokens,
+    int32_t *n_accepted, void *stream) {
+  if (!target || !cu_drafts || !u_sample || !tokens || !n_accepted) return ATTN_EINVAL;
+  if (V <= 0 || n_seq <= 0 || total < 0 || max_draft < 0) return ATTN_EINVAL;
+  if (dt != ATTN_BF16 && dt != ATTN_F32) return ATTN_EINVAL;
+  const uintptr_t low = dt == ATTN_F32 ? 3 : 1;  // rows need their elements' alignment only
+  if (((uintptr_t)target & low) || ((uintptr_t)draft & low)) return ATTN_EINVAL;
+  if (target_stride < V || target_stride >= (int64_t)1 << 40) return ATTN_EINVAL;
+  if (draft && (draft_stride < V || draft_stride >= (int64_t)1 << 40)) return ATTN_EINVAL;
+  if (total > 0 && max_draft > 0 && (!drafted || !u_accept)) return ATTN_EINVAL;
+  if (!aligned4(drafted) || !aligned4(cu_drafts) || !aligned4(u_accept) || !aligned4(u_sample) ||
+      !aligned4(tokens) || !aligned4(n_accepted))
+    return ATTN_EINVAL;
+  if (V > 1 << 28 || n_seq > 1 << 24 || max_draft > kMaxPositions || total > kMaxPositions)
+    return ATTN_EUNSUPPORTED;
+  VerifyArgs a{};
+  a.target = target; a.draft = draft;
+  a.target_stride = target_stride; a.draft_stride = draft_stride;
+  a.bf16 = dt == ATTN_BF16; a.V = V; a.n_seq = n_seq; a.total = total; a.max_draft = max_draft;
+  a.drafted = drafted; a.cu = cu_drafts; a.u_accept = u_accept; a.u_sample = u_sample;
+  a.tokens = tokens; a.n_accepted = n_accepted;
+  const cudaError_t e = error_word(&a.err);
+  if (e != cudaSuccess) return from_cuda(e);
+  return from_cuda(launch_verify_drafts(a, (cudaStream_t)stream));
 }
 
 extern "C" attn_status attn_skip_last_device_error(void *stream) {

@@ -147,6 +147,71 @@ struct ChunkArgs {
   unsigned *err;
 };
 
+// Pages of several layers' caches (of one shape) in one launch.
+constexpr int kMaxLayers = 64;
+
+struct KvLayers {
+  int n;
+  int format, n_pages, page_size, Hkv, page_shift;
+  int64_t page_stride;
+  struct {
+    uint8_t *k, *v, *k_scale, *v_scale, *k_bs, *v_bs;
+  } layer[kMaxLayers];
+};
+
+struct CopyPagesArgs {
+  KvLayers kv;
+  int n_pairs;
+  const int32_t *src, *dst;
+  int chunks;                          // pieces of a page's k (and v)
+  unsigned *err;
+};
+
+struct CompactArgs {
+  KvLayers kv;
+  int n_seq, total, max_pages, out_max_pages, per_head;
+  const int32_t *cu_keep, *keep;       // keep [total], or [Hkv][total]
+  const int32_t *start;                // [n_seq] or null
+  const int32_t *table, *out_table;    // out_table null: in place
+  int splits;                          // CTAs that share a sequence's rows (not in place)
+  unsigned *err;
+};
+
+struct ReserveArgs {
+  int32_t *refs, *table;
+  int n_pages, n_seq, max_pages, page_size;
+  const int32_t *kv_len, *new_len;
+  int32_t *got_len, *copy_src, *copy_dst;
+  int warp_words;                      // words of 32 pages of a warp
+  unsigned *err;
+};
+
+struct ForkArgs {
+  int32_t *refs, *out_table;
+  const int32_t *table, *kv_len, *new_len, *parent;  // parent null: rows stay in place
+  int n_pages, n_seq, n_new, max_pages, page_size;
+  unsigned *err;
+};
+
+// Drafted tokens against the target's probabilities.
+struct VerifyArgs {
+  const void *target, *draft;          // rows of V; draft null: each drafted token had q = 1
+  int64_t target_stride, draft_stride; // elements
+  int bf16, V, n_seq, total, max_draft;
+  const int32_t *drafted, *cu;
+  const float *u_accept, *u_sample;
+  int32_t *tokens, *n_accepted;
+  unsigned *err;
+};
+
+cudaError_t launch_kv_copy_pages(CopyPagesArgs a, cudaStream_t s);
+cudaError_t launch_kv_compact(CompactArgs a, cudaStream_t s);
+size_t pages_reserve_max_seqs();
+size_t pages_reserve_max_pages();
+cudaError_t launch_pages_reserve(ReserveArgs a, cudaStream_t s);
+cudaError_t launch_pages_fork(const ForkArgs &a, cudaStream_t s);
+cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s);
+
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
 cudaError_t launch_kv_widen(const KvWidenArgs &a, cudaStream_t s);
 size_t chunk_paged_kv_bytes(int n_seq, int max_chunk, int max_kv, int Hkv, int TT, int format);

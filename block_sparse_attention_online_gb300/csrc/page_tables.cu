@@ -1,0 +1,321 @@
+// Ownership of a paged cache's pages: reference counts, page tables.
+//
+// refs[p] is the number of page-table entries that name page p; a page with
+// refs[p] = 0 is free.  There is no list of free pages to keep: reserve finds the
+// lowest free ones in refs, fork moves the counts by what changes hands.  All of it
+// is whole numbers, and no result depends on the order of atomics.
+#include <cooperative_groups.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace attn_skip {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int NT = 1024;  // threads a CTA of reserve
+constexpr int NW = NT / 32;
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ int pages_of(int len, int ps) {  // ceil(len / ps), len >= 0
+  return (int)(((unsigned)len + (unsigned)ps - 1u) / (unsigned)ps);
+}
+
+// Sum over the lanes below and this one's.
+template <typename T>
+__device__ __forceinline__ T scan_warp(T x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T v = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += v;
+  }
+  return x;
+}
+
+// Exclusive sum over the block's threads, and the block's total.  `tmp`: NW + 1
+// values of shared memory, free again after the next barrier.
+template <typename T>
+__device__ __forceinline__ T scan_block(T x, T *tmp, T &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T upto = scan_warp(x, lane);
+  if (lane == 31) tmp[warp] = upto;
+  __syncthreads();
+  if (warp == 0) {
+    const T w = tmp[lane], u = scan_warp(w, lane);
+    tmp[lane] = u - w;
+    if (lane == 31) tmp[NW] = u;
+  }
+  __syncthreads();
+  total = tmp[NW];
+  return tmp[warp] + upto - x;
+}
+
+// Per-sequence state in shared memory.
+struct Seqs {
+  int *begin;     // [n + 1] requests of the sequences before (saturated at INT_MAX)
+  int *first;     // [n] first entry past the cached ones
+  int *page;      // [n] shared page that the sequence is about to write into, -1: none, -2: bad
+  uint8_t *cow;   // [n] it gets a copy
+};
+__host__ __device__ constexpr size_t seq_bytes(int n) { return ((size_t)n * 13 + 4 + 15) / 16 * 16; }
+
+// One cluster.  Every CTA works out the sequences' requests for itself and looks at a
+// slice of refs; the CTAs' counts of free pages go round through distributed shared
+// memory, after which each hands out its own free pages: the k-th lowest free page is
+// the k-th request's, in the order of sequences, a copied page first, then the new
+// entries.  refs, the table and the lengths are read before the cluster's barrier and
+// written behind it, so that got_len may be kv_len.
+__global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ ReserveArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int tmp[NW + 1];
+  __shared__ long long tmp64[NW + 1];
+  __shared__ int free_of[kMaxCluster];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_seq, ps = a.page_size;
+  Seqs q;
+  q.begin = reinterpret_cast<int *>(smem);
+  q.first = q.begin + n + 1;
+  q.page = q.first + n;
+  q.cow = reinterpret_cast<uint8_t *>(q.page + n);
+  // Words of 32 pages: warp w of CTA r has a.warp_words of them from (r * NW + w) * warp_words.
+  uint32_t *words = reinterpret_cast<uint32_t *>(smem + seq_bytes(n)) + warp * a.warp_words;
+  const int word0 = (rank * NW + warp) * a.warp_words;
+
+  // The free pages of this warp's slice.
+  int free_warp = 0;
+  for (int i0 = 0; i0 < a.warp_words; i0 += 8) {
+    int r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = (word0 + i0 + i) * 32 + lane;
+      r[i] = i0 + i < a.warp_words && p < a.n_pages ? a.refs[p] : 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const unsigned m = __ballot_sync(0xffffffffu, r[i] == 0);
+      if (i0 + i < a.warp_words && lane == 0) words[i0 + i] = m;
+      free_warp += __popc(m);
+    }
+  }
+
+  // What each sequence asks for.
+  bool bad = false;
+  for (int s = tid; s < n; s += NT) {
+    const int from = a.kv_len[s], to = a.new_len[s];
+    int need = 0, first = 0, page = -1;
+    if (from < 0 || to < from || to > (int64_t)a.max_pages * ps) {
+      page = -2;
+    } else {
+      first = pages_of(from, ps);
+      need = pages_of(to, ps) - first;
+      if (to > from && first * (int64_t)ps != from) {  // it writes into its last page
+        page = a.table[(int64_t)s * a.max_pages + first - 1];
+        if (page < 0 || page >= a.n_pages) {
+          page = -2;
+          need = 0;
+        } else if (a.refs[page] <= 1) {
+          page = -1;
+        }
+      }
+    }
+    bad |= page == -2;
+    q.begin[s] = need;
+    q.first[s] = first;
+    q.page[s] = page;
+  }
+  if (bad && rank == 0) atomicOr(a.err, kErrBadArg);
+  __syncthreads();
+  // A sequence that writes into a shared page gets a copy of it, but for the last one
+  // that still holds it: with h holders, those with h - 1 such sequences before them
+  // (in the batch) write into the page itself.
+  for (int s = tid; s < n; s += NT) {
+    const int page = q.page[s];
+    int before = 0;
+    if (page >= 0) {
+      for (int t = 0; t < s; ++t) before += q.page[t] == page;
+      before = before < a.refs[page] - 1;
+    }
+    q.cow[s] = (uint8_t)before;
+  }
+  __syncthreads();
+  // Requests of the sequences before each.  Every thread takes `per` sequences.
+  {
+    const int per = (n + NT - 1) / NT, s0 = min(n, tid * per), s1 = min(n, s0 + per);
+    long long sum = 0, total;
+    for (int s = s0; s < s1; ++s) sum += q.begin[s] + q.cow[s];
+    long long at = scan_block(sum, tmp64, total);
+    for (int s = s0; s < s1; ++s) {
+      const int need = q.begin[s] + q.cow[s];
+      q.begin[s] = (int)min(at, 0x7fffffffll);
+      at += need;
+    }
+    if (tid == 0) q.begin[n] = (int)min(total, 0x7fffffffll);
+  }
+  int free_cta;
+  int k = scan_block(lane == 0 ? free_warp : 0, tmp, free_cta);
+  k = __shfl_sync(0xffffffffu, k, 0);  // free pages of the CTA's warps before this one
+  if (tid < n_cta) *cluster.map_shared_rank(&free_of[rank], tid) = free_cta;
+  cluster.sync();
+  int n_free = 0;
+  for (int r = 0; r < n_cta; ++r) {
+    if (r < rank) k += free_of[r];
+    n_free += free_of[r];
+  }
+  // Sequences in order are served as far as the pages go (`taken` requests), and
+  // those that need none and write into no shared page.
+  int taken;
+  {
+    int lo = 0, hi = n;  // the largest i with begin[i] <= n_free
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (q.begin[mid] <= n_free) lo = mid;
+      else hi = mid - 1;
+    }
+    taken = q.begin[lo];
+  }
+  for (int s = rank * NT + tid; s < n; s += n_cta * NT) {
+    const int page = q.page[s], upto = q.begin[s + 1];
+    const bool served = page != -2 && (upto <= n_free || (upto == q.begin[s] && page == -1));
+    const bool cow = served && q.cow[s];
+    a.got_len[s] = served ? a.new_len[s] : a.kv_len[s];
+    a.copy_src[s] = cow ? page : -1;
+    if (!cow) a.copy_dst[s] = -1;
+    if (cow) atomicSub(a.refs + page, 1);
+  }
+  // This warp's free pages, a word of 32 a lane.
+  for (int i0 = 0; i0 < a.warp_words && k < taken; i0 += 32) {
+    uint32_t m = i0 + lane < a.warp_words ? words[i0 + lane] : 0u;
+    const int upto = scan_warp(__popc(m), lane);
+    int r = k + upto - __popc(m);
+    k += __shfl_sync(0xffffffffu, upto, 31);
+    if (!m || r >= taken) continue;
+    int s = 0;
+    {
+      int hi = n - 1;  // the largest s with begin[s] <= r
+      while (s < hi) {
+        const int mid = (s + hi + 1) >> 1;
+        if (q.begin[mid] <= r) s = mid;
+        else hi = mid - 1;
+      }
+    }
+    for (; m && r < taken; m &= m - 1, ++r) {
+      const int p = (word0 + i0 + lane) * 32 + __ffs(m) - 1;
+      while (q.begin[s + 1] <= r) ++s;
+      const int i = r - q.begin[s] - q.cow[s];  // -1: the copy
+      a.refs[p] = 1;
+      a.table[(int64_t)s * a.max_pages + q.first[s] + i] = p;
+      if (i < 0) a.copy_dst[s] = p;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- fork --
+constexpr int FT = 256;
+
+// A length in range, or the nearest that is.
+__device__ __forceinline__ int clip(int x, int hi, bool &bad) {
+  bad |= x < 0 || x > hi;
+  return min(max(x, 0), hi);
+}
+
+// One CTA a row: first the rows of the new batch, then those of the old one.  The
+// counts change only where pages change hands: a sequence's first follower takes its
+// references over, others add theirs, and what no follower takes over is given back.
+__global__ void __launch_bounds__(FT) fork_kernel(const __grid_constant__ ForkArgs a) {
+  const int tid = threadIdx.x, ps = a.page_size;
+  const int64_t room = (int64_t)a.max_pages * ps;
+  const int most = (int)min(room, (int64_t)0x7fffffff);
+  const int n_new = a.parent ? a.n_new : 0;  // (without parents the rows stay where they are)
+  bool bad = false;
+  if ((int)blockIdx.x < n_new) {
+    const int d = blockIdx.x, s = a.parent[d];
+    bad = s < -1 || s >= a.n_seq;
+    const int len0 = a.new_len[d];
+    if (s < 0 || s >= a.n_seq) {
+      if ((bad || len0 != 0) && tid == 0) atomicOr(a.err, kErrBadArg);
+      return;
+    }
+    bool follows = false;  // a follower of s comes before
+    for (int e = tid; e < d; e += FT) follows |= a.parent[e] == s;
+    follows = __syncthreads_or(follows);
+    bool lost = false;
+    const int old = a.kv_len[s];
+    lost = old < 0 || old > most;  // (the old row reports it)
+    const int n = pages_of(clip(len0, lost ? 0 : old, bad), ps);
+    const int32_t *from = a.table + (int64_t)s * a.max_pages;
+    int32_t *to = a.out_table + (int64_t)d * a.max_pages;
+    for (int e = tid; e < n; e += FT) {
+      const int p = from[e];
+      to[e] = p;
+      if (p < 0 || p >= a.n_pages) bad = true;
+      else if (follows) atomicAdd(a.refs + p, 1);
+    }
+  } else {
+    const int s = blockIdx.x - n_new;
+    const int old = a.kv_len[s];
+    int keep = 0;  // pages that a follower takes over
+    if (old < 0 || old > most) {
+      if (tid == 0) atomicOr(a.err, kErrBadArg);
+      return;
+    }
+    if (!a.parent) {
+      keep = pages_of(clip(a.new_len[s], old, bad), ps);
+    } else {
+      __shared__ int first;
+      if (tid == 0) first = n_new;
+      __syncthreads();
+      int d = n_new;
+      for (int e = tid; e < n_new && d == n_new; e += FT)
+        if (a.parent[e] == s) d = e;
+      if (d < n_new) atomicMin(&first, d);
+      __syncthreads();
+      bool unused = false;
+      if (first < n_new) keep = pages_of(clip(a.new_len[first], old, unused), ps);
+    }
+    const int n = pages_of(old, ps);
+    const int32_t *from = a.table + (int64_t)s * a.max_pages;
+    for (int e = keep + tid; e < n; e += FT) {
+      const int p = from[e];
+      if (p < 0 || p >= a.n_pages) bad = true;
+      else atomicSub(a.refs + p, 1);
+    }
+  }
+  if (bad) atomicOr(a.err, kErrBadArg);
+}
+
+}  // namespace
+
+size_t pages_reserve_max_seqs() { return 8192; }
+size_t pages_reserve_max_pages() { return (size_t)1 << 22; }
+
+cudaError_t launch_pages_reserve(ReserveArgs a, cudaStream_t s) {
+  // A CTA alone for small pools; from 8192 pages on a cluster of eight.
+  const int n_cta = a.n_pages > 8192 ? kMaxCluster : 1;
+  const int all = (a.n_pages + 31) / 32;
+  a.warp_words = (all + n_cta * NW - 1) / (n_cta * NW);
+  const size_t smem = seq_bytes(a.n_seq) + (size_t)a.warp_words * NW * 4;
+  cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)n_cta);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)n_cta;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, reserve_kernel, a);
+}
+
+cudaError_t launch_pages_fork(const ForkArgs &a, cudaStream_t s) {
+  fork_kernel<<<(unsigned)(a.n_seq + (a.parent ? a.n_new : 0)), FT, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace attn_skip

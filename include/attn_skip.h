@@ -673,6 +673,165 @@ int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, int total, in
                                  int max_chunk, int max_kv);
 
 /*
+ * Who owns which page.  The library keeps nothing between calls: the state is one
+ * device array, refs [n_pages] int32, with the number of page-table entries that
+ * name each page (0: free).  A program starts with zeros and tables of any content,
+ * and keeps one refs and one set of tables for the caches of all layers.  A
+ * sequence of length L uses the first ceil(L / page_size) entries of its row;
+ * entries behind them may hold anything.  Calls that share refs go on one stream,
+ * or are ordered by events.
+ *
+ * A step with drafted tokens: attn_skip_pages_reserve (room for the chunk),
+ * attn_skip_kv_copy_pages (what reserve says), attn_skip_kv_append and
+ * attn_skip_chunk_paged in every layer, attn_skip_verify_drafts on the
+ * target's probabilities, attn_skip_pages_fork without parents (back to the
+ * accepted length).
+ */
+
+/*
+ * Pages for the tokens that are about to come.  Sequence s grows from kv_len[s] to
+ * new_len[s] positions:
+ *  - its new entries ceil(kv_len / page_size) .. ceil(new_len / page_size) - 1
+ *    get free pages;
+ *  - if it grows at all and its last page is partly filled and shared (refs > 1),
+ *    it gets a page of its own in that one's place: the entry changes, the old
+ *    page loses a reference, and copy_src[s], copy_dst[s] name the two pages for
+ *    attn_skip_kv_copy_pages.  Sequences count in order: the last holder of a page
+ *    (refs[page] - 1 of the batch before it get copies) writes into the page
+ *    itself.  copy_src[s] = copy_dst[s] = -1 for the others.
+ * The k-th page asked for, over the sequences in order (a sequence's copy first,
+ * then its entries), is the k-th lowest page with refs = 0 at the start of the
+ * call; its refs become 1.  Where the pages run out, the first sequence that does
+ * not fit and all after it stay as they are, but for those that need no page and
+ * write into no shared one.
+ *
+ *  refs        [n_pages] int32 (device), updated; n_pages <= 4,194,304
+ *  page_table  [n_seq, max_pages] int32 (device), updated; n_seq <= 8192
+ *  kv_len, new_len  [n_seq] int32 (device)
+ *  got_len     [n_seq] int32 (device): new_len[s], or kv_len[s] for a sequence
+ *              that stays as it is; may be kv_len
+ *  copy_src, copy_dst  [n_seq] int32 (device)
+ *  page_size   at least 1
+ * EINVAL: a null or misaligned (4 bytes) pointer, a size that is not positive.
+ * Checked by the kernel and reported by attn_skip_last_device_error (ATTN_EINVAL):
+ * a kv_len below 0, a new_len below kv_len or above max_pages * page_size, a partly
+ * filled page's id out of range (the sequence stays as it is).
+ */
+attn_status attn_skip_pages_reserve(int32_t *refs, int n_pages, int32_t *page_table, int n_seq,
+                                    int max_pages, int page_size, const int32_t *kv_len,
+                                    const int32_t *new_len, int32_t *got_len, int32_t *copy_src,
+                                    int32_t *copy_dst, void *stream);
+
+/*
+ * The sequences of the next batch take over pages of this one's: forks (a parent
+ * with several followers), reordered beams, sequences that end (no follower), and
+ * shorter ones.  Sequence d of the new batch gets the first ceil(new_len[d] /
+ * page_size) entries of row parent[d]; refs loses the old batch's references
+ * (kv_len) and gains the new one's.  Without parents (NULL) every sequence keeps
+ * its row and is cut to new_len[s]: page_table is only read.  Pages whose refs
+ * reach 0 are free, and hold their rows until they are given out again.
+ *
+ *  refs        [n_pages] int32 (device), updated
+ *  page_table  [n_seq, max_pages], kv_len [n_seq] int32 (device): the old batch
+ *  parent      [n_new] int32 (device), -1: an empty sequence (new_len 0); or NULL
+ *  new_len     [n_new] (without parents [n_seq]) int32 (device), at most the
+ *              parent's kv_len
+ *  out_table   [n_new, max_pages] int32 (device), not page_table; entries behind a
+ *              sequence's last page stay as they were (without parents unused)
+ * Errors as for attn_skip_pages_reserve.  Reported by attn_skip_last_device_error:
+ * a parent outside [-1, n_seq) or one of -1 with a length (an empty sequence), a
+ * new_len out of range (the nearest length in range counts), a kv_len outside
+ * [0, max_pages * page_size] (treated as 0), a page id out of range (not counted).
+ */
+attn_status attn_skip_pages_fork(int32_t *refs, int n_pages, const int32_t *page_table, int n_seq,
+                                 int max_pages, int page_size, const int32_t *kv_len,
+                                 const int32_t *new_len, int n_new, const int32_t *parent,
+                                 int32_t *out_table, void *stream);
+
+/*
+ * Whole pages copied, keys, values and scales, in the caches of n_layers layers:
+ * page src[i] to page dst[i].  kv is an array of n_layers descriptions that agree
+ * in format, sizes and page stride.
+ *
+ *  src, dst   [n_pairs] int32 (device); -1 in either, or a page onto itself:
+ *             nothing to copy
+ * A page may be copied to several places; a page that two entries write, or that
+ * one writes and another reads, holds a mixture.  EINVAL as for
+ * attn_skip_kv_append, for caches that differ and n_pairs < 0; a page id below -1
+ * or not below n_pages is left out and reported by attn_skip_last_device_error.
+ */
+attn_status attn_skip_kv_copy_pages(const attn_kv_pages *kv, int n_layers, int n_pairs,
+                                    const int32_t *src, const int32_t *dst, void *stream);
+
+/*
+ * The cached rows that a sequence keeps move together, in the caches of n_layers
+ * layers: the row of position keep[cu_keep[s] + j] of page_table's sequence s
+ * becomes the row of position start[s] + j, of the same table (out_table NULL:
+ * in place) or of out_table.  For dropping rows that attention no longer needs (a
+ * window with the first tokens, blocks that are always skipped), and for moving
+ * the accepted path of a drafted tree up behind the cached rows.
+ *
+ *  cu_keep    [n_seq + 1] int32 (device)
+ *  keep       [total] int32 (device), or with per_head [Hkv, total]: every KV head
+ *             keeps rows of its own
+ *  start      [n_seq] int32 (device) or NULL (all 0)
+ *  out_table  [n_seq, out_max_pages] int32 (device) or NULL
+ * In place keep[cu_keep[s] + j] >= start[s] + j has to hold (it does for
+ * ascending positions from start[s] on); other positions than start[s] .. are
+ * left as they were.  The rows written must be no other sequence's (attn_skip_pages_reserve
+ * gives a copy of the last page only), and with out_table none that is read.
+ * EINVAL as for attn_skip_kv_append.  Left out and reported by
+ * attn_skip_last_device_error: sequences with bad bounds, rows of positions or
+ * page ids out of range, in place rows with keep below their new position.
+ */
+attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layers, int n_seq, int total,
+                                 const int32_t *cu_keep, const int32_t *keep, int per_head,
+                                 const int32_t *start, const int32_t *page_table, int max_pages,
+                                 const int32_t *out_table, int out_max_pages, void *stream);
+
+/*
+ * Drafted tokens against the target's probabilities (speculative sampling): the
+ * tokens that a batch of sequences goes on with, distributed as the target's.
+ *
+ * Sequence s has n = cu_drafts[s+1] - cu_drafts[s] drafted tokens x_i, drawn from
+ * q_i, and n + 1 rows of the target's probabilities: p_i for the place of x_i, p_n
+ * for the one behind them (those of attn_skip_chunk_paged's chunk of n + 1 tokens).
+ * With u_i, u in [0, 1) the caller's random numbers:
+ *  - x_i is accepted iff u_i * q_i(x_i) < p_i(x_i) and all before it are;
+ *  - at the first rejected x_i a token is drawn from max(p_i - q_i, 0) (from p_i
+ *    where that is zero throughout), with all accepted from p_n;
+ *  - a draw is the smallest t with w_0 + .. + w_t > u * (w_0 + .. + w_{V-1}), the
+ *    weights w truncated to multiples of 2^-60 and their sums exact.
+ * A row whose weights are all zero gives token V - 1.
+ *
+ *  target     [total + n_seq, V] (dt), rows target_stride elements apart: p_i of
+ *             sequence s is row cu_drafts[s] + s + i
+ *  draft      [total, V] (dt), rows draft_stride elements apart, or NULL: the
+ *             drafted tokens are not random (a look-up, an argmax), q_i(x_i) = 1
+ *  dt         ATTN_F32 or ATTN_BF16; rows need no more than their elements'
+ *             alignment.  Probabilities lie in [0, 2), rows sum to about one (to
+ *             less than 16)
+ *  drafted    [total] int32, u_accept [total] fp32, u_sample [n_seq] fp32,
+ *             cu_drafts [n_seq + 1] int32 (device); tokens before cu_drafts[0]
+ *             and from cu_drafts[n_seq] on are ignored.  n = 0 samples one token
+ *  max_draft  host bound on n
+ *  tokens     [n_seq, max_draft + 1] int32: the accepted tokens, the drawn one,
+ *             -1 behind it; n_accepted [n_seq] int32
+ * EINVAL: a null or misaligned pointer, a size that is not positive (total,
+ * max_draft: below 0), a stride below V; V above 2^28 is EUNSUPPORTED.  Reported by
+ * attn_skip_last_device_error: a sequence with bad bounds (tokens and n_accepted -1),
+ * a drafted token outside [0, V) (rejected), a probability in a row that is drawn from
+ * outside [0, 2), or NaN (it counts as 0), a random number outside [0, 1) (u_sample:
+ * the nearest, 0 for NaN).
+ */
+attn_status attn_skip_verify_drafts(const void *target, int64_t target_stride, const void *draft,
+                                    int64_t draft_stride, attn_dtype dt, int V, int n_seq,
+                                    int total, int max_draft, const int32_t *drafted,
+                                    const int32_t *cu_drafts, const float *u_accept,
+                                    const float *u_sample, int32_t *tokens, int32_t *n_accepted,
+                                    void *stream);
+
+/*
  * Diagnostic: launches one small CTA that allocates TMEM and then waits, with
  * the same bounded wait as every kernel, on an mbarrier phase that nothing
  * completes.  After the 1 s limit the wait gives up, the CTA raises its abort
@@ -686,8 +845,8 @@ attn_status attn_skip_selftest_wait_timeout(void *stream);
  * Synchronises `stream`, then reads and clears the current device's error
  * word: ATTN_ETIMEOUT if a kernel gave up a bounded wait since the last read,
  * ATTN_EINVAL if a kernel found a device-side argument out of range (the
- * varlen and paged-cache lengths, page ids and thresholds), ATTN_EINTERNAL if a kernel found its shared
- * memory misaligned, ATTN_ECUDA on a CUDA error, else ATTN_OK.
+ * varlen and paged-cache lengths, page ids and thresholds, drafted tokens,
+ * probabilities), ATTN_EINTERNAL if a kernel found its shared memory misaligned, ATTN_ECUDA on a CUDA error, else ATTN_OK.
  */
 attn_status attn_skip_last_device_error(void *stream);
 
