@@ -801,7 +801,8 @@ extern "C" attn_status attn_skip_pages_reserve(int32_t *refs, int n_pages, int32
   if (!got_len || !copy_src || !copy_dst || !aligned4(got_len) || !aligned4(copy_src) ||
       !aligned4(copy_dst))
     return ATTN_EINVAL;
-  if ((size_t)n_seq > pages_reserve_max_seqs() || (size_t)n_pages > pages_reserve_max_pages())
+  if ((size_t)n_seq > pages_reserve_max_seqs() || (size_t)n_pages > pages_reserve_max_pages() ||
+      max_pages >= 1 << 30)  // (the kernel keeps a flag in bit 30 of an entry's number)
     return ATTN_EUNSUPPORTED;
   ReserveArgs a{};
   a.refs = refs; a.table = page_table;

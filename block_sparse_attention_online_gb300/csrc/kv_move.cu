@@ -1,6 +1,7 @@
 // Rows and pages of the paged cache moved as they are: whole pages copied, and the
 // rows that a sequence keeps moved together, in the caches of all layers at once.
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "internal.h"
 
@@ -87,12 +88,18 @@ template <int FMT> struct RowBytes {
   static constexpr int value = FMT == kKvBf16 ? 256 : FMT == kKvE4m3 ? 128 : 64;
 };
 
-template <int FMT, int GROUP>
+// BOTH: the unit's rows are keys and values; else one of the two, by the unit's number,
+// and 16 * LPR bytes of each row.
+template <int FMT, int LPR, int GROUP, bool BOTH>
 __global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ CompactArgs a) {
-  constexpr int LPR = RowBytes<FMT>::value / 16;  // lanes a row
-  constexpr int U = 4;                            // rows a lane
-  constexpr int BATCH = GROUP / LPR * U;
+  constexpr int VECS = RowBytes<FMT>::value / 16, PARTS = VECS / LPR;
+  constexpr int KV = BOTH ? 2 : 1;
+  constexpr int U = BOTH ? 2 : 4;                  // rows a thread loads at a time
+  constexpr int CHUNK = GROUP / LPR * U;           // rows of the group
+  constexpr int BATCH = GROUP == 32 ? 32 : 1024;
+  constexpr int MINE = BATCH / GROUP;              // rows of the batch whose scales a thread moves
   constexpr int GROUPS = NT / GROUP;
+  static_assert(BATCH % CHUNK == 0, "whole chunks");
   __shared__ RowAt rows_at[GROUPS][BATCH];
   const int g = threadIdx.x / GROUP, t = threadIdx.x % GROUP;
   RowAt *at = rows_at[g];
@@ -101,12 +108,13 @@ __global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ Com
     else __syncthreads();
   };
   unsigned unit = blockIdx.x * GROUPS + g;
-  const unsigned heads = (unsigned)a.kv.Hkv;
-  const unsigned split = unit % (unsigned)a.splits;
-  unit /= (unsigned)a.splits;
-  const int h = (int)(unit % heads);
-  unit /= heads;
-  const int s = (int)(unit % (unsigned)a.n_seq), layer = (int)(unit / (unsigned)a.n_seq);
+  auto next = [&](unsigned n) {
+    const unsigned q = unit / n, r = unit - q * n;
+    unit = q;
+    return (int)r;
+  };
+  const int split = next((unsigned)a.splits), part = next(PARTS), w0 = next(3 - KV);
+  const int h = next((unsigned)a.kv.Hkv), s = next((unsigned)a.n_seq), layer = (int)unit;
   if (layer >= a.kv.n) return;  // (whole groups)
   const int c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
   if (c0 < 0 || c1 < c0 || c1 > a.total) {
@@ -121,10 +129,23 @@ __global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ Com
   const int64_t from_room = (int64_t)a.max_pages * a.kv.page_size;
   const int64_t to_room = in_place ? from_room : (int64_t)a.out_max_pages * a.kv.page_size;
   const auto &l = a.kv.layer[layer];
+  uint8_t *codes[KV], *scale[KV], *block[KV];
+#pragma unroll
+  for (int w = 0; w < KV; ++w) {
+    const bool value = BOTH ? w == 1 : w0 == 1;
+    codes[w] = (value ? l.v : l.k) + (part * LPR + t % LPR) * 16;
+    scale[w] = value ? l.v_scale : l.k_scale;
+    block[w] = value ? l.v_bs : l.k_bs;
+  }
+  const int head_row = h * a.kv.page_size, page_rows = a.kv.Hkv * a.kv.page_size;
   bool bad = false;
-  for (int j0 = (int)split * BATCH; j0 < n; j0 += a.splits * BATCH) {
+  for (int j0 = split * BATCH; j0 < n; j0 += a.splits * BATCH) {
     sync();  // the batch before is done with the places
-    for (int b = t; b < BATCH && j0 + b < n; b += GROUP) {
+    const int m = min(BATCH, n - j0);
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      const int b = t + i * GROUP;
+      if (b >= m) break;
       const int64_t src = keep[j0 + b], dst = (int64_t)start + j0 + b;
       RowAt x{-1, 0, 0, 0};
       if (src < 0 || src >= from_room || dst < 0 || dst >= to_room || (in_place && src < dst)) {
@@ -143,73 +164,96 @@ __global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ Com
       at[b] = x;
     }
     sync();
-    const int m = min(BATCH, n - j0);
-    uint4 x[U][2];
-    uint8_t sc[U][2];
-    uint2 bs[U][2];
-    const int lane = t % LPR;
+    uint8_t sc[MINE][KV];
+    uint2 bs[MINE][KV];
+    if (FMT != kKvBf16 && part == 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int b = t / LPR + u * (GROUP / LPR);
-      if (b >= m || at[b].from_page < 0) continue;
-      const int in_page = h * a.kv.page_size + at[b].from_slot;
-      const int64_t byte = at[b].from_page * a.kv.page_stride +
-                           (int64_t)in_page * RowBytes<FMT>::value + lane * 16;
-      x[u][0] = *reinterpret_cast<const uint4 *>(l.k + byte);
-      x[u][1] = *reinterpret_cast<const uint4 *>(l.v + byte);
-      const int64_t row = (int64_t)at[b].from_page * (a.kv.Hkv * a.kv.page_size) + in_page;
-      if constexpr (FMT != kKvBf16)
-        if (lane == 0) {
-          sc[u][0] = l.k_scale[row];
-          sc[u][1] = l.v_scale[row];
+      for (int i = 0; i < MINE; ++i) {
+        const int b = t + i * GROUP;
+        if (b >= m || at[b].from_page < 0) continue;
+        const int64_t row = (int64_t)at[b].from_page * page_rows + head_row + at[b].from_slot;
+#pragma unroll
+        for (int w = 0; w < KV; ++w) {
+          sc[i][w] = scale[w][row];
+          if (FMT == kKvNvfp4) bs[i][w] = *reinterpret_cast<const uint2 *>(block[w] + row * 8);
         }
-      if constexpr (FMT == kKvNvfp4)
-        if (lane == 1) {
-          bs[u][0] = *reinterpret_cast<const uint2 *>(l.k_bs + row * 8);
-          bs[u][1] = *reinterpret_cast<const uint2 *>(l.v_bs + row * 8);
-        }
+      }
     }
-    sync();
+    auto load = [&](int c, uint4 (&x)[U][KV]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int b = t / LPR + u * (GROUP / LPR);
-      if (b >= m || at[b].from_page < 0) continue;
-      const int in_page = h * a.kv.page_size + at[b].to_slot;
-      const int64_t byte =
-          at[b].to_page * a.kv.page_stride + (int64_t)in_page * RowBytes<FMT>::value + lane * 16;
-      *reinterpret_cast<uint4 *>(l.k + byte) = x[u][0];
-      *reinterpret_cast<uint4 *>(l.v + byte) = x[u][1];
-      const int64_t row = (int64_t)at[b].to_page * (a.kv.Hkv * a.kv.page_size) + in_page;
-      if constexpr (FMT != kKvBf16)
-        if (lane == 0) {
-          l.k_scale[row] = sc[u][0];
-          l.v_scale[row] = sc[u][1];
+      for (int u = 0; u < U; ++u) {
+        const int b = c + t / LPR + u * (GROUP / LPR);
+        if (b >= m || at[b].from_page < 0) continue;
+        const int64_t byte = at[b].from_page * a.kv.page_stride +
+                             (int64_t)(head_row + at[b].from_slot) * RowBytes<FMT>::value;
+#pragma unroll
+        for (int w = 0; w < KV; ++w) x[u][w] = *reinterpret_cast<const uint4 *>(codes[w] + byte);
+      }
+    };
+    auto store = [&](int c, const uint4 (&x)[U][KV]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int b = c + t / LPR + u * (GROUP / LPR);
+        if (b >= m || at[b].from_page < 0) continue;
+        const int64_t byte = at[b].to_page * a.kv.page_stride +
+                             (int64_t)(head_row + at[b].to_slot) * RowBytes<FMT>::value;
+#pragma unroll
+        for (int w = 0; w < KV; ++w) *reinterpret_cast<uint4 *>(codes[w] + byte) = x[u][w];
+      }
+    };
+    uint4 x[U][KV], y[U][KV];
+    load(0, x);
+    for (int c = 0; c < m; c += 2 * CHUNK) {
+      load(c + CHUNK, y);
+      sync();  // all loads up to here come before the stores below
+      if (FMT != kKvBf16 && part == 0 && c == 0) {
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          const int b = t + i * GROUP;
+          if (b >= m || at[b].from_page < 0) continue;
+          const int64_t row = (int64_t)at[b].to_page * page_rows + head_row + at[b].to_slot;
+#pragma unroll
+          for (int w = 0; w < KV; ++w) {
+            scale[w][row] = sc[i][w];
+            if (FMT == kKvNvfp4) *reinterpret_cast<uint2 *>(block[w] + row * 8) = bs[i][w];
+          }
         }
-      if constexpr (FMT == kKvNvfp4)
-        if (lane == 1) {
-          *reinterpret_cast<uint2 *>(l.k_bs + row * 8) = bs[u][0];
-          *reinterpret_cast<uint2 *>(l.v_bs + row * 8) = bs[u][1];
-        }
+      }
+      store(c, x);
+      load(c + 2 * CHUNK, x);
+      sync();
+      store(c + CHUNK, y);
     }
   }
   if (bad) atomicOr(a.err, kErrBadArg);
 }
 
+template <int FMT, int LPR, int GROUP, bool BOTH>
+cudaError_t compact_launch(const CompactArgs &a, cudaStream_t s) {
+  constexpr int PER_HEAD = RowBytes<FMT>::value / 16 / LPR * (BOTH ? 1 : 2);
+  constexpr int GROUPS = NT / GROUP;
+  const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * PER_HEAD * a.splits;
+  if (units > 0x7fffffff) return cudaErrorNotYetImplemented;
+  compact_kernel<FMT, LPR, GROUP, BOTH><<<(unsigned)((units + GROUPS - 1) / GROUPS), NT, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <int FMT>
 cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
+  constexpr int VECS = RowBytes<FMT>::value / 16;
   const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv;
   const int64_t mean = a.total / a.n_seq;
-  if (mean <= 64) {
-    a.splits = 1;
-    compact_kernel<FMT, 32><<<(unsigned)((units + NT / 32 - 1) / (NT / 32)), NT, 0, s>>>(a);
-  } else {
-    // Rows may be shared out where none is overwritten.
-    a.splits = 1;
-    while (a.out_table && a.splits < 64 && units * a.splits < 152 * 16 && mean / a.splits > 256)
-      a.splits *= 2;
-    compact_kernel<FMT, NT><<<(unsigned)(units * a.splits), NT, 0, s>>>(a);
+  a.splits = 1;
+  if (mean <= 64) return compact_launch<FMT, VECS, 32, true>(a, s);
+  if (!a.out_table) {
+    // In place a (layer, sequence, head) goes through its rows in order; where these are
+    // few, keys and values are cut into columns of 32 (64) bytes.
+    if (units * 2 < 152 * 8 && !getenv("NOCUT")) return compact_launch<FMT, VECS == 4 ? 2 : VECS / 4, NT, false>(a, s);
+    return compact_launch<FMT, VECS, NT, false>(a, s);
   }
-  return cudaGetLastError();
+  // Rows may be shared out where none is overwritten.
+  while (a.splits < 64 && units * 2 * a.splits < 152 * 8 && mean / a.splits > 1024) a.splits *= 2;
+  return compact_launch<FMT, VECS, NT, false>(a, s);
 }
 
 }  // namespace
@@ -225,7 +269,6 @@ cudaError_t launch_kv_copy_pages(CopyPagesArgs a, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_compact(CompactArgs a, cudaStream_t s) {
-  if ((int64_t)a.kv.n * a.n_seq * a.kv.Hkv * 64 > 0x7fffffff) return cudaErrorNotYetImplemented;
   return a.kv.format == kKvBf16   ? compact_fmt<kKvBf16>(a, s)
          : a.kv.format == kKvE4m3 ? compact_fmt<kKvE4m3>(a, s)
                                   : compact_fmt<kKvNvfp4>(a, s);

@@ -53,12 +53,18 @@ __device__ __forceinline__ T scan_block(T x, T *tmp, T &total) {
 
 // Per-sequence state in shared memory.
 struct Seqs {
-  int *begin;     // [n + 1] requests of the sequences before (saturated at INT_MAX)
-  int *first;     // [n] first entry past the cached ones
-  int *page;      // [n] shared page that the sequence is about to write into, -1: none, -2: bad
-  uint8_t *cow;   // [n] it gets a copy
+  int *begin;      // [n + 1] requests of the sequences before (saturated at INT_MAX)
+  int *first;      // [n] first entry past the cached ones; bit 30: it gets a copy of its last page
+  int *page;       // [n] shared page that the sequence is about to write into, -1: none, -2: bad
+  int2 *slots;     // hash of the shared pages: page + 1 (0: none), a number
 };
-__host__ __device__ constexpr size_t seq_bytes(int n) { return ((size_t)n * 13 + 4 + 15) / 16 * 16; }
+constexpr int kCopy = 1 << 30;
+__host__ __device__ constexpr int hash_slots(int n) {  // a power of two, twice n where there is room
+  int m = 2;
+  while (m < 2 * n && m < 8192) m *= 2;
+  return m;
+}
+__host__ __device__ constexpr size_t seq_bytes(int n) { return ((size_t)n * 12 + 4 + 15) / 16 * 16; }
 
 // One cluster.  Every CTA works out the sequences' requests for itself and looks at a
 // slice of refs; the CTAs' counts of free pages go round through distributed shared
@@ -78,10 +84,31 @@ __global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ Res
   q.begin = reinterpret_cast<int *>(smem);
   q.first = q.begin + n + 1;
   q.page = q.first + n;
-  q.cow = reinterpret_cast<uint8_t *>(q.page + n);
+  q.slots = reinterpret_cast<int2 *>(smem + seq_bytes(n));
+  const int slots = hash_slots(n);
   // Words of 32 pages: warp w of CTA r has a.warp_words of them from (r * NW + w) * warp_words.
-  uint32_t *words = reinterpret_cast<uint32_t *>(smem + seq_bytes(n)) + warp * a.warp_words;
+  uint32_t *words = reinterpret_cast<uint32_t *>(q.slots + slots) + warp * a.warp_words;
   const int word0 = (rank * NW + warp) * a.warp_words;
+
+  // What each sequence asks for: the loads of the first ones before those of refs.
+  auto last_page = [&](int s, int from, int to, int &page, int &first, int &need) {
+    page = -1;
+    first = need = 0;
+    if (from < 0 || to < from || to > (int64_t)a.max_pages * ps) {
+      page = -2;
+      return;
+    }
+    first = pages_of(from, ps);
+    need = pages_of(to, ps) - first;
+    if (to > from && first * (int64_t)ps != from) {  // it writes into its last page
+      page = a.table[(int64_t)s * a.max_pages + first - 1];
+      if (page < 0 || page >= a.n_pages) page = -2;
+    }
+    if (page == -2) need = 0;
+  };
+  int page0 = -1, first0 = 0, need0 = 0;
+  if (tid < n) last_page(tid, a.kv_len[tid], a.new_len[tid], page0, first0, need0);
+  for (int i = tid; i < slots; i += NT) q.slots[i] = make_int2(0, 0);
 
   // The free pages of this warp's slice.
   int free_warp = 0;
@@ -100,54 +127,60 @@ __global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ Res
     }
   }
 
-  // What each sequence asks for.
-  bool bad = false;
+  bool bad = false, shared = false;
   for (int s = tid; s < n; s += NT) {
-    const int from = a.kv_len[s], to = a.new_len[s];
-    int need = 0, first = 0, page = -1;
-    if (from < 0 || to < from || to > (int64_t)a.max_pages * ps) {
-      page = -2;
-    } else {
-      first = pages_of(from, ps);
-      need = pages_of(to, ps) - first;
-      if (to > from && first * (int64_t)ps != from) {  // it writes into its last page
-        page = a.table[(int64_t)s * a.max_pages + first - 1];
-        if (page < 0 || page >= a.n_pages) {
-          page = -2;
-          need = 0;
-        } else if (a.refs[page] <= 1) {
-          page = -1;
-        }
-      }
-    }
+    int page = page0, first = first0, need = need0;
+    if (s != tid) last_page(s, a.kv_len[s], a.new_len[s], page, first, need);
+    if (page >= 0 && a.refs[page] <= 1) page = -1;
     bad |= page == -2;
+    shared |= page >= 0;
     q.begin[s] = need;
     q.first[s] = first;
     q.page[s] = page;
   }
   if (bad && rank == 0) atomicOr(a.err, kErrBadArg);
-  __syncthreads();
   // A sequence that writes into a shared page gets a copy of it, but for the last one
-  // that still holds it: with h holders, those with h - 1 such sequences before them
-  // (in the batch) write into the page itself.
-  for (int s = tid; s < n; s += NT) {
-    const int page = q.page[s];
-    int before = 0;
-    if (page >= 0) {
-      for (int t = 0; t < s; ++t) before += q.page[t] == page;
-      before = before < a.refs[page] - 1;
-    }
-    q.cow[s] = (uint8_t)before;
+  // that holds it: where as many sequences write into a page as refs counts, the last of
+  // them in the batch writes into the page itself.
+  if (__syncthreads_or(shared)) {
+    auto slot_of = [&](int page) {  // (each page has one by the second use)
+      unsigned i = ((unsigned)page * 2654435769u) >> 15;
+      while (true) {
+        i &= (unsigned)slots - 1;
+        const int was = atomicCAS(&q.slots[i].x, 0, page + 1);
+        if (was == 0 || was == page + 1) return &q.slots[i].y;
+        ++i;
+      }
+    };
+    for (int s = tid; s < n; s += NT)
+      if (q.page[s] >= 0) atomicAdd(slot_of(q.page[s]), 1);
+    __syncthreads();
+    for (int s = tid; s < n; s += NT)
+      if (q.page[s] >= 0) {
+        q.first[s] |= kCopy;
+        if (*slot_of(q.page[s]) >= a.refs[q.page[s]]) q.begin[s] |= kCopy;  // one of them stays
+      }
+    __syncthreads();
+    for (int i = tid; i < slots; i += NT) q.slots[i].y = -1;
+    __syncthreads();
+    for (int s = tid; s < n; s += NT)
+      if (q.begin[s] & kCopy) atomicMax(slot_of(q.page[s]), s);
+    __syncthreads();
+    for (int s = tid; s < n; s += NT)
+      if (q.begin[s] & kCopy) {
+        q.begin[s] &= ~kCopy;
+        if (*slot_of(q.page[s]) == s) q.first[s] &= ~kCopy;
+      }
+    __syncthreads();
   }
-  __syncthreads();
   // Requests of the sequences before each.  Every thread takes `per` sequences.
   {
     const int per = (n + NT - 1) / NT, s0 = min(n, tid * per), s1 = min(n, s0 + per);
     long long sum = 0, total;
-    for (int s = s0; s < s1; ++s) sum += q.begin[s] + q.cow[s];
+    for (int s = s0; s < s1; ++s) sum += q.begin[s] + (q.first[s] >> 30);
     long long at = scan_block(sum, tmp64, total);
     for (int s = s0; s < s1; ++s) {
-      const int need = q.begin[s] + q.cow[s];
+      const int need = q.begin[s] + (q.first[s] >> 30);
       q.begin[s] = (int)min(at, 0x7fffffffll);
       at += need;
     }
@@ -178,7 +211,7 @@ __global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ Res
   for (int s = rank * NT + tid; s < n; s += n_cta * NT) {
     const int page = q.page[s], upto = q.begin[s + 1];
     const bool served = page != -2 && (upto <= n_free || (upto == q.begin[s] && page == -1));
-    const bool cow = served && q.cow[s];
+    const bool cow = served && (q.first[s] & kCopy);
     a.got_len[s] = served ? a.new_len[s] : a.kv_len[s];
     a.copy_src[s] = cow ? page : -1;
     if (!cow) a.copy_dst[s] = -1;
@@ -203,9 +236,9 @@ __global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ Res
     for (; m && r < taken; m &= m - 1, ++r) {
       const int p = (word0 + i0 + lane) * 32 + __ffs(m) - 1;
       while (q.begin[s + 1] <= r) ++s;
-      const int i = r - q.begin[s] - q.cow[s];  // -1: the copy
+      const int first = q.first[s] & ~kCopy, i = r - q.begin[s] - (q.first[s] >> 30);  // -1: the copy
       a.refs[p] = 1;
-      a.table[(int64_t)s * a.max_pages + q.first[s] + i] = p;
+      a.table[(int64_t)s * a.max_pages + first + i] = p;
       if (i < 0) a.copy_dst[s] = p;
     }
   }
@@ -213,6 +246,7 @@ __global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ Res
 
 // ---------------------------------------------------------------------- fork --
 constexpr int FT = 256;
+constexpr int kEntries = 4;  // table entries a thread loads at a time
 
 // A length in range, or the nearest that is.
 __device__ __forceinline__ int clip(int x, int hi, bool &bad) {
@@ -246,11 +280,17 @@ __global__ void __launch_bounds__(FT) fork_kernel(const __grid_constant__ ForkAr
     const int n = pages_of(clip(len0, lost ? 0 : old, bad), ps);
     const int32_t *from = a.table + (int64_t)s * a.max_pages;
     int32_t *to = a.out_table + (int64_t)d * a.max_pages;
-    for (int e = tid; e < n; e += FT) {
-      const int p = from[e];
-      to[e] = p;
-      if (p < 0 || p >= a.n_pages) bad = true;
-      else if (follows) atomicAdd(a.refs + p, 1);
+    for (int e0 = tid; e0 < n; e0 += kEntries * FT) {
+      int p[kEntries];
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) p[i] = e0 + i * FT < n ? from[e0 + i * FT] : 0;
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) {
+        if (e0 + i * FT >= n) break;
+        to[e0 + i * FT] = p[i];
+        if (p[i] < 0 || p[i] >= a.n_pages) bad = true;
+        else if (follows) atomicAdd(a.refs + p[i], 1);
+      }
     }
   } else {
     const int s = blockIdx.x - n_new;
@@ -276,10 +316,16 @@ __global__ void __launch_bounds__(FT) fork_kernel(const __grid_constant__ ForkAr
     }
     const int n = pages_of(old, ps);
     const int32_t *from = a.table + (int64_t)s * a.max_pages;
-    for (int e = keep + tid; e < n; e += FT) {
-      const int p = from[e];
-      if (p < 0 || p >= a.n_pages) bad = true;
-      else atomicSub(a.refs + p, 1);
+    for (int e0 = keep + tid; e0 < n; e0 += kEntries * FT) {
+      int p[kEntries];
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) p[i] = e0 + i * FT < n ? from[e0 + i * FT] : 0;
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) {
+        if (e0 + i * FT >= n) break;
+        if (p[i] < 0 || p[i] >= a.n_pages) bad = true;
+        else atomicSub(a.refs + p[i], 1);
+      }
     }
   }
   if (bad) atomicOr(a.err, kErrBadArg);
@@ -295,10 +341,13 @@ cudaError_t launch_pages_reserve(ReserveArgs a, cudaStream_t s) {
   const int n_cta = a.n_pages > 8192 ? kMaxCluster : 1;
   const int all = (a.n_pages + 31) / 32;
   a.warp_words = (all + n_cta * NW - 1) / (n_cta * NW);
-  const size_t smem = seq_bytes(a.n_seq) + (size_t)a.warp_words * NW * 4;
-  cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
-  if (e != cudaSuccess) return e;
+  const size_t smem =
+      seq_bytes(a.n_seq) + hash_slots(a.n_seq) * sizeof(int2) + (size_t)a.warp_words * NW * 4;
+  if (smem > 48 * 1024 - 1024) {  // (static shared memory counts too)
+    const cudaError_t e = cudaFuncSetAttribute(
+        reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)n_cta);
   cfg.blockDim = dim3(NT);

@@ -6,17 +6,25 @@
 // accepted one another token from p_n: the tokens are then distributed as the target's.
 //
 // A draw is the inverse CDF: the smallest t with w_0 + ... + w_t > u (w_0 + ... + w_{V-1}).
-// The weights are whole numbers, units of 2^-60 (a probability in [0, 2) truncated to that,
-// exact from 2^-37 on), so that sums are exact in any order: the token does not depend on
-// how the vocabulary is shared out.
+// The weights are whole numbers, units of 2^-60 (a probability in [0, 2) rounded to the
+// nearest, exact from 2^-37 on), so that sums are exact in any order: the token does not
+// depend on how the vocabulary is shared out.
 //
-// One cluster a sequence: every CTA finds the row, sums its warps' stretches of it, and
-// sends the sums round; the warp whose stretch holds the threshold finds the token.
+// A value becomes units by adding constants: x + 6 rounds x to a multiple of 2^-21 whose
+// number is the sum's bits minus those of 6; what is left, exact, goes on with 1.5 * 2^-20
+// (2^-43) and 1.5 * 2^-37 (2^-60).  Three integer sums then do for a row.  p and q take
+// the two halves of packed instructions: about fifteen a pair of values, where shifts by
+// the exponent take fifty and bound the large calls (256 rows of 128000: 190 us).
+//
+// One cluster a sequence: every warp finds the row, sums its stretch of it, and sends the
+// sum round; the warp whose stretch holds the threshold finds the token.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "internal.h"
+#include "tc_common.cuh"
 
 namespace attn_skip {
 namespace {
@@ -34,18 +42,28 @@ __device__ __forceinline__ uint32_t load_bits(const void *row, int64_t i) {  // 
   else return __ldg((const uint32_t *)row + i);
 }
 
-// A probability (fp32 bits) in units of 2^-60, truncated.  What lies outside [0, 2) (a NaN
-// among it) counts as 0 and is noted; -0 is 0.
+constexpr float kM1 = 6.f;                   // 1.5 * 2^2: steps of 2^-21
+constexpr float kM2 = 1.430511474609375e-6f; // 1.5 * 2^-20: steps of 2^-43
+constexpr float kM3 = 1.0913936421275139e-11f; // 1.5 * 2^-37: steps of 2^-60
+constexpr uint32_t kValid = 0x40000000u;     // fp32 bits from here on: 2 and more, NaN, negative
+
+__device__ __forceinline__ u64 join(uint32_t s1, uint32_t s2, uint32_t s3) {
+  return ((u64)(int64_t)(int)s1 << 39) + ((u64)(int64_t)(int)s2 << 17) + (u64)(int64_t)(int)s3;
+}
+
+// A probability (fp32 bits) in units of 2^-60.  What lies outside [0, 2) (a NaN among it)
+// counts as 0 and is noted; -0 is 0.
 __device__ __forceinline__ u64 units(uint32_t b, bool &bad) {
-  const int e = (int)(b >> 23);
-  const uint32_t m = (b & 0x7fffffu) | 0x800000u;
-  if (b >= 0x40000000u) {
+  if (b >= kValid) {
     bad |= b != 0x80000000u;
     return 0;
   }
-  // b = m 2^(e - 150) = m 2^(e - 90) units; subnormals (e = 0) vanish.
-  const int sh = e - 90;
-  return sh >= 0 ? (u64)m << sh : sh > -24 ? (u64)(m >> -sh) : 0;
+  const float x = __uint_as_float(b);
+  const float t1 = x + kM1, r1 = x - (t1 - kM1);
+  const float t2 = r1 + kM2, r2 = r1 - (t2 - kM2);
+  const float t3 = r2 + kM3;
+  return join(__float_as_uint(t1) - __float_as_uint(kM1),
+              __float_as_uint(t2) - __float_as_uint(kM2), __float_as_uint(t3) - __float_as_uint(kM3));
 }
 
 struct Row {
@@ -77,15 +95,87 @@ __device__ __forceinline__ u64 scan_warp(u64 x, int lane) {
   return x;
 }
 
+// Sum of the weights of tokens [i0, i1), for the whole warp.
+template <bool BF16, bool HAS_Q>
+__device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int lane, bool &bad) {
+  constexpr int U = 8;        // tokens a lane loads at a time
+  constexpr int FLUSH = 256;  // tokens a lane sums in 32 bits (2^22 steps each at most)
+  auto two = [](float x, float y) {
+    return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
+  };
+  const uint64_t m1 = two(kM1, kM1), m2 = two(kM2, kM2), m3 = two(kM3, kM3), neg = two(-1.f, -1.f);
+  u64 sum = 0;
+  uint32_t most = 0;  // the largest bits of all values
+  for (int i = i0; i < i1;) {
+    uint32_t s1 = 0, s2 = 0, s3 = 0;  // (modulo 2^32, as signed numbers)
+    const int end = min(i1, i + FLUSH * 32);
+    for (; i < end; i += U * 32) {
+      uint32_t x[U], y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = i + u * 32 + lane;
+        x[u] = t < i1 ? load_bits<BF16>(r.p, t) : 0u;
+        y[u] = HAS_Q && t < i1 ? load_bits<BF16>(r.q, t) : 0u;
+      }
+      auto steps = [&](uint32_t lo, uint32_t hi, uint32_t (&a)[3], uint32_t (&b)[3]) {
+        const uint64_t v = (uint64_t)lo | (uint64_t)hi << 32;
+        const uint64_t t1 = tc::f2_add(v, m1);
+        const uint64_t r1 = tc::f2_add(v, tc::f2_fma(t1, neg, m1));
+        const uint64_t t2 = tc::f2_add(r1, m2);
+        const uint64_t r2 = tc::f2_add(r1, tc::f2_fma(t2, neg, m2));
+        const uint64_t t3 = tc::f2_add(r2, m3);
+        a[0] = (uint32_t)t1; b[0] = (uint32_t)(t1 >> 32);
+        a[1] = (uint32_t)t2; b[1] = (uint32_t)(t2 >> 32);
+        a[2] = (uint32_t)t3; b[2] = (uint32_t)(t3 >> 32);
+      };
+      uint32_t a[3], b[3];
+      if constexpr (HAS_Q) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          most = max(most, max(x[u], y[u]));
+          steps(x[u], y[u], a, b);
+          if (x[u] > y[u]) {  // (valid values: their bits compare as they do)
+            s1 += a[0] - b[0];
+            s2 += a[1] - b[1];
+            s3 += a[2] - b[2];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; u += 2) {
+          most = max(most, max(x[u], x[u + 1]));
+          steps(x[u], x[u + 1], a, b);
+          s1 += a[0] + b[0] - 2 * __float_as_uint(kM1);
+          s2 += a[1] + b[1] - 2 * __float_as_uint(kM2);
+          s3 += a[2] + b[2] - 2 * __float_as_uint(kM3);
+        }
+      }
+    }
+    sum += join(s1, s2, s3);
+  }
+  if (__any_sync(0xffffffffu, most >= kValid)) {  // values to leave out: one by one
+    sum = 0;
+    Row all = r;
+    all.hole = -1;
+    for (int i = i0 + lane; i < i1; i += 32) sum += weight<BF16>(all, i, bad);
+  }
+  sum = sum_warp(sum);
+  if (r.hole >= i0 && r.hole < i1) {
+    bool noted = false;
+    sum -= units(load_bits<BF16>(r.p, r.hole), noted);
+  }
+  return sum;
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ u64 sums[2][kMaxCluster * NW];  // of every warp of the cluster
-  __shared__ int first_rejected;
   const cg::cluster_group cluster = cg::this_cluster();
   const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x / n_cta;
   const int c0 = a.cu[s], c1 = a.cu[s + 1], n = c1 - c0;
+  float us = a.u_sample[s];
   int32_t *out = a.tokens + (int64_t)s * (a.max_draft + 1);
   if (c0 < 0 || c1 < c0 || c1 > a.total || n > a.max_draft) {  // (the whole cluster)
     if (rank == 0) {
@@ -105,30 +195,36 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Veri
     return (const uint8_t *)a.draft + ((int64_t)c0 + i) * a.draft_stride * esize;
   };
 
-  // The first rejected token.
+  // The first rejected token: every warp for itself.
   bool bad = false;
-  if (tid == 0) first_rejected = n;
-  __syncthreads();
-  for (int i = tid; i < n; i += NT) {
-    const int x = a.drafted[c0 + i];
-    const float u = a.u_accept[c0 + i];
-    bool ok = false;
-    if (x < 0 || x >= a.V || !(u >= 0.f && u < 1.f)) {
-      bad = true;
+  int acc = n, rejected = -1;  // accepted tokens; the rejected one
+  for (int b = 0; b < n; b += 32) {
+    const int i = b + lane;
+    bool ok = true;
+    int x = -1;
+    if (i < n) {
+      x = a.drafted[c0 + i];
+      const float u = a.u_accept[c0 + i];
+      const bool known = x >= 0 && x < a.V;
+      bad |= !known || !(u >= 0.f && u < 1.f);
+      ok = false;
+      if (known) {
+        const float p = __uint_as_float(load_bits<BF16>(target_row(i), x));
+        const float q = a.draft ? __uint_as_float(load_bits<BF16>(draft_row(i), x)) : 1.f;
+        ok = (double)u * (double)q < (double)p;  // (exact)
+      }
     }
-    if (x >= 0 && x < a.V) {
-      const float p = __uint_as_float(load_bits<BF16>(target_row(i), x));
-      const float q = a.draft ? __uint_as_float(load_bits<BF16>(draft_row(i), x)) : 1.f;
-      ok = (double)u * (double)q < (double)p;  // (exact)
+    const unsigned no = __ballot_sync(0xffffffffu, !ok);
+    if (no) {
+      acc = b + __ffs(no) - 1;
+      rejected = __shfl_sync(0xffffffffu, x, acc - b);
+      break;
     }
-    if (!ok) atomicMin(&first_rejected, i);
   }
-  __syncthreads();
-  const int acc = first_rejected;
   Row row{target_row(acc), nullptr, -1};
   if (acc < n) {
     if (a.draft) row.q = draft_row(acc);
-    else row.hole = a.drafted[c0 + acc];
+    else row.hole = rejected;
   }
 
   // Every warp's stretch, a multiple of 32 tokens.
@@ -137,11 +233,9 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Veri
   const int i0 = (int)min((int64_t)mine * len, (int64_t)a.V), i1 = min(i0 + len, a.V);
   u64 total = 0, before = 0, stretch = 0;
   for (int round = 0; round < 2; ++round) {  // the second one only where p - q is 0 throughout
-    u64 w = 0;
-#pragma unroll 8
-    for (int i = i0 + lane; i < i1; i += 32) w += weight<BF16>(row, i, bad);
-    w = sum_warp(w);
-    if (lane < n_cta) *cluster.map_shared_rank(&sums[round][mine], lane) = w;
+    stretch = row.q ? sum_stretch<BF16, true>(row, i0, i1, lane, bad)
+                    : sum_stretch<BF16, false>(row, i0, i1, lane, bad);
+    if (lane < n_cta) *cluster.map_shared_rank(&sums[round][mine], lane) = stretch;
     cluster.sync();
     // Sums of all warps, and of those before this one.
     u64 below = 0, every = 0;
@@ -152,19 +246,16 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Veri
     }
     total = sum_warp(every);
     before = sum_warp(below);
-    stretch = w;
     if (total || acc == n) break;
     row.q = nullptr;
     row.hole = -1;
   }
-  if (bad) atomicOr(a.err, kErrBadArg);
-
-  float u = a.u_sample[s];
-  if (!(u >= 0.f && u < 1.f)) {
-    if (rank == 0 && tid == 0) atomicOr(a.err, kErrBadArg);
-    u = u >= 1.f ? 0.99999994f : 0.f;
+  if (!(us >= 0.f && us < 1.f)) {
+    bad = true;
+    us = us >= 1.f ? 0.99999994f : 0.f;
   }
-  const u64 threshold = __umul64hi(total, (u64)(u * 18446744073709551616.f));
+  if (bad) atomicOr(a.err, kErrBadArg);
+  const u64 threshold = __umul64hi(total, (u64)(us * 18446744073709551616.f));
   if (rank == 0)
     for (int i = tid; i <= a.max_draft; i += NT)
       if (i != acc) out[i] = i < acc ? a.drafted[c0 + i] : -1;
@@ -177,6 +268,7 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Veri
   const int piece = len / 32, j0 = min(i0 + lane * piece, i1), j1 = min(j0 + piece, i1);
   u64 w = 0;
   bool noted = false;
+#pragma unroll 8
   for (int i = j0; i < j1; ++i) w += weight<BF16>(row, i, noted);
   const u64 upto = before + scan_warp(w, lane);
   if (threshold < upto && threshold >= upto - w) {
@@ -217,6 +309,7 @@ cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
   // CTAs a sequence: as many as leave every warp 128 tokens, up to eight.
   int n_cta = 1;
   while (n_cta < 8 && (int64_t)n_cta * NW * 128 < a.V) n_cta *= 2;
+  if (const char *e = getenv("VERIFY_CTAS")) n_cta = atoi(e);
   return a.bf16 ? launch<true>(a, n_cta, s) : launch<false>(a, n_cta, s);
 }
 

@@ -801,7 +801,7 @@ attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layers, int n_se
  *  - at the first rejected x_i a token is drawn from max(p_i - q_i, 0) (from p_i
  *    where that is zero throughout), with all accepted from p_n;
  *  - a draw is the smallest t with w_0 + .. + w_t > u * (w_0 + .. + w_{V-1}), the
- *    weights w truncated to multiples of 2^-60 and their sums exact.
+ *    weights w made of p and q rounded to multiples of 2^-60 and their sums exact.
  * A row whose weights are all zero gives token V - 1.
  *
  *  target     [total + n_seq, V] (dt), rows target_stride elements apart: p_i of

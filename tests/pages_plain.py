@@ -84,11 +84,11 @@ def compact(x, keep, cu, table, ps, start=None, out_table=None):
 
 
 def units(p):
-    """Probabilities as whole multiples of 2^-60, truncated; what is outside [0, 2) as 0."""
+    """Probabilities as whole multiples of 2^-60, the nearest; what is outside [0, 2) as 0."""
     p = np.asarray(p, dtype=np.float64)
     with np.errstate(invalid="ignore"):
         p = np.where((p >= 0) & (p < 2), p, 0.0)
-    return np.floor(np.ldexp(p, 60)).astype(np.int64)
+    return np.rint(np.ldexp(p, 60)).astype(np.int64)
 
 
 def draw(w, u):
