@@ -753,6 +753,7 @@ extern "C" attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layer
   if (st != ATTN_OK) return st;
   if (!aligned4(start) || !aligned4(out_table)) return ATTN_EINVAL;
   if (out_table && out_max_pages <= 0) return ATTN_EINVAL;
+  if (total > kMaxPositions) return ATTN_EUNSUPPORTED;
   if (out_table && (int64_t)out_max_pages * kv->page_size > kMaxPositions) return ATTN_EUNSUPPORTED;
   if (total == 0) return ATTN_OK;
   if (!keep || !aligned4(keep)) return ATTN_EINVAL;

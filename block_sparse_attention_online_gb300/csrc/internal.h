@@ -182,7 +182,7 @@ struct ReserveArgs {
   int n_pages, n_seq, max_pages, page_size;
   const int32_t *kv_len, *new_len;
   int32_t *got_len, *copy_src, *copy_dst;
-  int warp_words;                      // words of 32 pages of a warp
+  int rounds;                          // chunks of pages of a warp
   unsigned *err;
 };
 

@@ -1,7 +1,6 @@
 // Rows and pages of the paged cache moved as they are: whole pages copied, and the
 // rows that a sequence keeps moved together, in the caches of all layers at once.
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "internal.h"
 
@@ -80,161 +79,300 @@ __global__ void __launch_bounds__(NT) copy_pages_kernel(const __grid_constant__ 
 // checked: row j is read in its own batch, and what overwrites its place is row
 // keep[j] - start >= j, of the same batch or a later one, stored after a barrier that
 // follows the loads.
-struct RowAt {
-  int from_page, from_slot, to_page, to_slot;  // from_page -1: nothing to move
+struct Place {  // as the tables say it
+  int from_page, from_slot, to_page, to_slot;  // from_page < 0: nothing to move
+};
+constexpr Place kNowhere{-1, 0, 0, -1};  // (a slot below 0: it is no fault)
+
+struct Move {  // of a head's row, in bytes of k and v
+  int64_t from, to;  // from < 0: nothing to move
 };
 
 template <int FMT> struct RowBytes {
   static constexpr int value = FMT == kKvBf16 ? 256 : FMT == kKvE4m3 ? 128 : 64;
 };
 
-// BOTH: the unit's rows are keys and values; else one of the two, by the unit's number,
-// and 16 * LPR bytes of each row.
-template <int FMT, int LPR, int GROUP, bool BOTH>
+// What a group works on.
+struct Unit {
+  int layer, s, h;
+  int n, start;              // kept rows of the sequence, position of the first
+  const int32_t *keep;
+  const int32_t *from, *to;  // the sequence's rows of the tables
+  int from_room, to_room;    // positions that they have
+};
+
+// False where there is nothing to do (bad bounds are reported).
+__device__ __forceinline__ bool unit_of(const CompactArgs &a, int layer, int s, int h, bool first,
+                                        Unit &x) {
+  if (layer >= a.kv.n) return false;
+  const int c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
+  if (c0 < 0 || c1 < c0 || c1 > a.total) {
+    if (first) atomicOr(a.err, kErrBadArg);
+    return false;
+  }
+  x.layer = layer;
+  x.s = s;
+  x.h = h;
+  x.n = c1 - c0;
+  x.start = a.start ? a.start[s] : 0;
+  x.keep = a.keep + (a.per_head ? (int64_t)h * a.total : 0) + c0;
+  x.from = a.table + (int64_t)s * a.max_pages;
+  x.to = a.out_table ? a.out_table + (int64_t)s * a.out_max_pages : x.from;
+  x.from_room = a.max_pages * a.kv.page_size;  // (at most 2^30)
+  x.to_room = a.out_table ? a.out_max_pages * a.kv.page_size : x.from_room;
+  return true;
+}
+
+// Where row j, of position src, comes from and goes to (from_page -1: nothing to move);
+// the page ids are as they come from the tables.
+__device__ __forceinline__ Place place_of(const CompactArgs &a, const Unit &x, int j, int src,
+                                          bool &bad) {
+  const int64_t dst = (int64_t)x.start + j;
+  if (src < 0 || src >= x.from_room || dst < 0 || dst >= x.to_room || (!a.out_table && src < dst)) {
+    bad = true;
+    return kNowhere;
+  }
+  if (!a.out_table && src == dst) return kNowhere;
+  const unsigned ps = (unsigned)a.kv.page_size, d = (unsigned)dst;
+  const unsigned pf = a.kv.page_shift >= 0 ? (unsigned)src >> a.kv.page_shift : (unsigned)src / ps;
+  const unsigned pt = a.kv.page_shift >= 0 ? d >> a.kv.page_shift : d / ps;
+  return Place{x.from[pf], (int)((unsigned)src - pf * ps), x.to[pt], (int)(d - pt * ps)};
+}
+
+__device__ __forceinline__ void check_place(const CompactArgs &a, Place &r, bool &bad) {
+  if (r.from_page < 0 || r.from_page >= a.kv.n_pages || r.to_page < 0 || r.to_page >= a.kv.n_pages) {
+    bad |= r.to_slot >= 0;
+    r.from_page = -1;
+  }
+}
+
+template <int ROW>
+__device__ __forceinline__ Move move_of(const CompactArgs &a, const Place &r, int head_row) {
+  if (r.from_page < 0) return Move{-1, -1};
+  return Move{r.from_page * a.kv.page_stride + (int64_t)(head_row + r.from_slot) * ROW,
+              r.to_page * a.kv.page_stride + (int64_t)(head_row + r.to_slot) * ROW};
+}
+
+// One group of threads (a CTA, or a warp where sequences keep few rows): the key and
+// value rows of one (layer, sequence, head), or a share of them.
+template <int FMT, int GROUP>
 __global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ CompactArgs a) {
-  constexpr int VECS = RowBytes<FMT>::value / 16, PARTS = VECS / LPR;
-  constexpr int KV = BOTH ? 2 : 1;
-  constexpr int U = BOTH ? 2 : 4;                  // rows a thread loads at a time
-  constexpr int CHUNK = GROUP / LPR * U;           // rows of the group
-  constexpr int BATCH = GROUP == 32 ? 32 : 1024;
-  constexpr int MINE = BATCH / GROUP;              // rows of the batch whose scales a thread moves
+  constexpr int LPR = RowBytes<FMT>::value / 16;  // lanes a row
+  constexpr int U = GROUP == 32 ? 2 : 4;          // rows a thread loads at a time
+  constexpr int CHUNK = GROUP / LPR * U;          // rows of the group
+  constexpr int BATCH = GROUP == 32 ? 32 : NT;    // rows whose places are found at once
   constexpr int GROUPS = NT / GROUP;
-  static_assert(BATCH % CHUNK == 0, "whole chunks");
-  __shared__ RowAt rows_at[GROUPS][BATCH];
+  static_assert(BATCH == GROUP && BATCH % CHUNK == 0, "a row a thread, whole chunks");
+  __shared__ Move moves[GROUPS][BATCH];
   const int g = threadIdx.x / GROUP, t = threadIdx.x % GROUP;
-  RowAt *at = rows_at[g];
+  Move *at = moves[g];
   auto sync = [&] {
     if constexpr (GROUP == 32) __syncwarp();
     else __syncthreads();
   };
-  unsigned unit = blockIdx.x * GROUPS + g;
+  unsigned i = blockIdx.x * GROUPS + g;
   auto next = [&](unsigned n) {
-    const unsigned q = unit / n, r = unit - q * n;
-    unit = q;
+    const unsigned q = i / n, r = i - q * n;
+    i = q;
     return (int)r;
   };
-  const int split = next((unsigned)a.splits), part = next(PARTS), w0 = next(3 - KV);
-  const int h = next((unsigned)a.kv.Hkv), s = next((unsigned)a.n_seq), layer = (int)unit;
-  if (layer >= a.kv.n) return;  // (whole groups)
-  const int c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
-  if (c0 < 0 || c1 < c0 || c1 > a.total) {
-    if (t == 0) atomicOr(a.err, kErrBadArg);
-    return;
-  }
-  const int n = c1 - c0, start = a.start ? a.start[s] : 0;
-  const int32_t *keep = a.keep + (a.per_head ? (int64_t)h * a.total : 0) + c0;
-  const bool in_place = !a.out_table;
-  const int32_t *from = a.table + (int64_t)s * a.max_pages;
-  const int32_t *to = in_place ? from : a.out_table + (int64_t)s * a.out_max_pages;
-  const int64_t from_room = (int64_t)a.max_pages * a.kv.page_size;
-  const int64_t to_room = in_place ? from_room : (int64_t)a.out_max_pages * a.kv.page_size;
-  const auto &l = a.kv.layer[layer];
-  uint8_t *codes[KV], *scale[KV], *block[KV];
-#pragma unroll
-  for (int w = 0; w < KV; ++w) {
-    const bool value = BOTH ? w == 1 : w0 == 1;
-    codes[w] = (value ? l.v : l.k) + (part * LPR + t % LPR) * 16;
-    scale[w] = value ? l.v_scale : l.k_scale;
-    block[w] = value ? l.v_bs : l.k_bs;
-  }
+  const int split = next((unsigned)a.splits), h = next((unsigned)a.kv.Hkv), s = next((unsigned)a.n_seq);
+  Unit x;
+  if (!unit_of(a, (int)i, s, h, t == 0, x)) return;  // (whole groups)
+  const auto &l = a.kv.layer[x.layer];
   const int head_row = h * a.kv.page_size, page_rows = a.kv.Hkv * a.kv.page_size;
+  uint8_t *keys = l.k + t % LPR * 16, *values = l.v + t % LPR * 16;
   bool bad = false;
-  for (int j0 = split * BATCH; j0 < n; j0 += a.splits * BATCH) {
+  for (int j0 = split * BATCH; j0 < x.n; j0 += a.splits * BATCH) {
     sync();  // the batch before is done with the places
-    const int m = min(BATCH, n - j0);
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-      const int b = t + i * GROUP;
-      if (b >= m) break;
-      const int64_t src = keep[j0 + b], dst = (int64_t)start + j0 + b;
-      RowAt x{-1, 0, 0, 0};
-      if (src < 0 || src >= from_room || dst < 0 || dst >= to_room || (in_place && src < dst)) {
-        bad = true;
-      } else if (!in_place || src != dst) {
-        const unsigned ps = (unsigned)a.kv.page_size;
-        const unsigned pf = a.kv.page_shift >= 0 ? (unsigned)src >> a.kv.page_shift : (unsigned)src / ps;
-        const unsigned pt = a.kv.page_shift >= 0 ? (unsigned)dst >> a.kv.page_shift : (unsigned)dst / ps;
-        x = RowAt{from[pf], (int)((unsigned)src - pf * ps), to[pt], (int)((unsigned)dst - pt * ps)};
-        if (x.from_page < 0 || x.from_page >= a.kv.n_pages || x.to_page < 0 ||
-            x.to_page >= a.kv.n_pages) {
-          bad = true;
-          x.from_page = -1;
-        }
-      }
-      at[b] = x;
-    }
+    const int m = min(BATCH, x.n - j0);
+    Place mine = kNowhere;
+    if (t < m) mine = place_of(a, x, j0 + t, x.keep[j0 + t], bad);
+    check_place(a, mine, bad);
+    at[t] = move_of<RowBytes<FMT>::value>(a, mine, head_row);
     sync();
-    uint8_t sc[MINE][KV];
-    uint2 bs[MINE][KV];
-    if (FMT != kKvBf16 && part == 0) {
-#pragma unroll
-      for (int i = 0; i < MINE; ++i) {
-        const int b = t + i * GROUP;
-        if (b >= m || at[b].from_page < 0) continue;
-        const int64_t row = (int64_t)at[b].from_page * page_rows + head_row + at[b].from_slot;
-#pragma unroll
-        for (int w = 0; w < KV; ++w) {
-          sc[i][w] = scale[w][row];
-          if (FMT == kKvNvfp4) bs[i][w] = *reinterpret_cast<const uint2 *>(block[w] + row * 8);
-        }
+    uint8_t sc[2];
+    uint2 bs[2];
+    if (FMT != kKvBf16 && mine.from_page >= 0) {
+      const int64_t row = (int64_t)mine.from_page * page_rows + head_row + mine.from_slot;
+      sc[0] = l.k_scale[row];
+      sc[1] = l.v_scale[row];
+      if (FMT == kKvNvfp4) {
+        bs[0] = *reinterpret_cast<const uint2 *>(l.k_bs + row * 8);
+        bs[1] = *reinterpret_cast<const uint2 *>(l.v_bs + row * 8);
       }
     }
-    auto load = [&](int c, uint4 (&x)[U][KV]) {
+    for (int c = 0; c < m; c += CHUNK) {
+      uint4 v[U][2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int b = c + t / LPR + u * (GROUP / LPR);
-        if (b >= m || at[b].from_page < 0) continue;
-        const int64_t byte = at[b].from_page * a.kv.page_stride +
-                             (int64_t)(head_row + at[b].from_slot) * RowBytes<FMT>::value;
-#pragma unroll
-        for (int w = 0; w < KV; ++w) x[u][w] = *reinterpret_cast<const uint4 *>(codes[w] + byte);
+        const int64_t byte = at[c + t / LPR + u * (GROUP / LPR)].from;
+        if (byte < 0) continue;
+        v[u][0] = *reinterpret_cast<const uint4 *>(keys + byte);
+        v[u][1] = *reinterpret_cast<const uint4 *>(values + byte);
       }
-    };
-    auto store = [&](int c, const uint4 (&x)[U][KV]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int b = c + t / LPR + u * (GROUP / LPR);
-        if (b >= m || at[b].from_page < 0) continue;
-        const int64_t byte = at[b].to_page * a.kv.page_stride +
-                             (int64_t)(head_row + at[b].to_slot) * RowBytes<FMT>::value;
-#pragma unroll
-        for (int w = 0; w < KV; ++w) *reinterpret_cast<uint4 *>(codes[w] + byte) = x[u][w];
-      }
-    };
-    uint4 x[U][KV], y[U][KV];
-    load(0, x);
-    for (int c = 0; c < m; c += 2 * CHUNK) {
-      load(c + CHUNK, y);
       sync();  // all loads up to here come before the stores below
-      if (FMT != kKvBf16 && part == 0 && c == 0) {
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-          const int b = t + i * GROUP;
-          if (b >= m || at[b].from_page < 0) continue;
-          const int64_t row = (int64_t)at[b].to_page * page_rows + head_row + at[b].to_slot;
-#pragma unroll
-          for (int w = 0; w < KV; ++w) {
-            scale[w][row] = sc[i][w];
-            if (FMT == kKvNvfp4) *reinterpret_cast<uint2 *>(block[w] + row * 8) = bs[i][w];
-          }
+      if (FMT != kKvBf16 && c == 0 && mine.from_page >= 0) {
+        const int64_t row = (int64_t)mine.to_page * page_rows + head_row + mine.to_slot;
+        l.k_scale[row] = sc[0];
+        l.v_scale[row] = sc[1];
+        if (FMT == kKvNvfp4) {
+          *reinterpret_cast<uint2 *>(l.k_bs + row * 8) = bs[0];
+          *reinterpret_cast<uint2 *>(l.v_bs + row * 8) = bs[1];
         }
       }
-      store(c, x);
-      load(c + 2 * CHUNK, x);
-      sync();
-      store(c + CHUNK, y);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t byte = at[c + t / LPR + u * (GROUP / LPR)].to;
+        if (byte < 0) continue;
+        *reinterpret_cast<uint4 *>(keys + byte) = v[u][0];
+        *reinterpret_cast<uint4 *>(values + byte) = v[u][1];
+      }
     }
   }
   if (bad) atomicOr(a.err, kErrBadArg);
 }
 
-template <int FMT, int LPR, int GROUP, bool BOTH>
-cudaError_t compact_launch(const CompactArgs &a, cudaStream_t s) {
-  constexpr int PER_HEAD = RowBytes<FMT>::value / 16 / LPR * (BOTH ? 1 : 2);
-  constexpr int GROUPS = NT / GROUP;
-  const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * PER_HEAD * a.splits;
+// In place, sequences that keep many rows: they have to go in order, so what bounds a
+// (layer, sequence, head) is how much it has under way.  A CTA takes keys or values,
+// and 16 * LPR bytes of each row.  Rows go chunk by chunk through a ring in shared
+// memory by asynchronous copies, kStages - 1 chunks ahead of the one that is stored
+// (every thread stores what it has loaded itself).  Their places are found a batch of
+// rows at a time, the page ids of the batch after the next and the positions of the one
+// behind it under way meanwhile.
+constexpr int kStages = 4;
+
+__device__ __forceinline__ void copy_async(uint32_t smem, const void *gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+
+template <int FMT, int LPR>
+__global__ void __launch_bounds__(NT) compact_ring_kernel(const __grid_constant__ CompactArgs a) {
+  constexpr int PARTS = RowBytes<FMT>::value / 16 / LPR;
+  constexpr int U = 4;                  // rows a thread loads
+  constexpr int CHUNK = NT / LPR * U;   // rows of the CTA
+  constexpr int MINE = CHUNK < NT ? 2 : 4;  // places a thread finds
+  constexpr int BATCH = MINE * NT, PER = BATCH / CHUNK;  // rows, chunks
+  static_assert(PER >= kStages - 1, "the first loads are of the first batch, the last of the next");
+  extern __shared__ __align__(16) uint4 ring[];  // [kStages][U][NT], then the places
+  Move *at = reinterpret_cast<Move *>(ring + kStages * U * NT);  // [2][BATCH]
+  const int t = threadIdx.x;
+  unsigned i = blockIdx.x;
+  auto next = [&](unsigned n) {
+    const unsigned q = i / n, r = i - q * n;
+    i = q;
+    return (int)r;
+  };
+  const int part = next(PARTS), value = next(2), h = next((unsigned)a.kv.Hkv), s = next((unsigned)a.n_seq);
+  Unit x;
+  if (!unit_of(a, (int)i, s, h, t == 0, x)) return;
+  const auto &l = a.kv.layer[x.layer];
+  uint8_t *codes = (value ? l.v : l.k) + (part * LPR + t % LPR) * 16;
+  uint8_t *scale = value ? l.v_scale : l.k_scale, *block = value ? l.v_bs : l.k_bs;
+  const int head_row = h * a.kv.page_size, page_rows = a.kv.Hkv * a.kv.page_size;
+  const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring) + t * 16;
+  const bool with_scales = FMT != kKvBf16 && part == 0;
+  bool bad = false;
+
+  // The places of batch b, in three steps.
+  auto positions = [&](int b, int (&src)[MINE]) {
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+      const int j = b * BATCH + k * NT + t;
+      src[k] = j < x.n ? x.keep[j] : -1;
+    }
+  };
+  auto page_ids = [&](int b, const int (&src)[MINE], Place (&r)[MINE]) {
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+      const int j = b * BATCH + k * NT + t;
+      r[k] = j < x.n ? place_of(a, x, j, src[k], bad) : kNowhere;
+    }
+  };
+  uint8_t sc[MINE];      // the scales of the batch that is in `at`,
+  uint2 bs[MINE];
+  int64_t sc_to[MINE];   // and the rows that they go to
+  auto put = [&](int b, Place (&r)[MINE]) {
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+      check_place(a, r[k], bad);
+      at[(b & 1) * BATCH + k * NT + t] = move_of<RowBytes<FMT>::value>(a, r[k], head_row);
+      sc_to[k] = -1;
+      if (with_scales && r[k].from_page >= 0) {
+        const int64_t row = (int64_t)r[k].from_page * page_rows + head_row + r[k].from_slot;
+        sc[k] = scale[row];
+        if (FMT == kKvNvfp4) bs[k] = *reinterpret_cast<const uint2 *>(block + row * 8);
+        sc_to[k] = (int64_t)r[k].to_page * page_rows + head_row + r[k].to_slot;
+      }
+    }
+  };
+  auto load = [&](int g) {  // chunk g
+    const Move *chunk = at + g * CHUNK % (2 * BATCH) + t / LPR;
+    const uint32_t slot = slot0 + (g % kStages) * (U * NT * 16);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t byte = chunk[u * (NT / LPR)].from;
+      if (byte >= 0) copy_async(slot + u * (NT * 16), codes + byte);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  Place ids[MINE];
+  int src[MINE];
+  {
+    int src1[MINE];
+    Place ids0[MINE];
+    positions(0, src);
+    positions(1, src1);
+    page_ids(0, src, ids0);
+    page_ids(1, src1, ids);
+    positions(2, src);
+    put(0, ids0);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int g = 0; g < kStages - 1; ++g) load(g);
+  for (int b = 0; b * BATCH < x.n; ++b) {
+    __syncthreads();  // the batch before is done, and every thread has this one's scales
+    if (with_scales) {
+#pragma unroll
+      for (int k = 0; k < MINE; ++k) {
+        if (sc_to[k] < 0) continue;
+        scale[sc_to[k]] = sc[k];
+        if (FMT == kKvNvfp4) *reinterpret_cast<uint2 *>(block + sc_to[k] * 8) = bs[k];
+      }
+    }
+    put(b + 1, ids);
+    page_ids(b + 2, src, ids);
+    positions(b + 3, src);
+    __syncthreads();
+    for (int g = b * PER; g < (b + 1) * PER && g * CHUNK < x.n; ++g) {
+      load(g + kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncthreads();  // every thread has chunk g
+      const Move *chunk = at + g * CHUNK % (2 * BATCH) + t / LPR;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t byte = chunk[u * (NT / LPR)].to;
+        if (byte >= 0)
+          *reinterpret_cast<uint4 *>(codes + byte) = ring[(g % kStages) * (U * NT) + u * NT + t];
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (bad) atomicOr(a.err, kErrBadArg);
+}
+
+template <int FMT, int LPR>
+cudaError_t compact_ring(const CompactArgs &a, int64_t units, cudaStream_t s) {
+  units *= 2 * (RowBytes<FMT>::value / 16 / LPR);
   if (units > 0x7fffffff) return cudaErrorNotYetImplemented;
-  compact_kernel<FMT, LPR, GROUP, BOTH><<<(unsigned)((units + GROUPS - 1) / GROUPS), NT, 0, s>>>(a);
+  constexpr int batch = (NT / LPR * 4 < NT ? 2 : 4) * NT;
+  constexpr int smem = kStages * 4 * NT * 16 + 2 * batch * (int)sizeof(Move);
+  const cudaError_t e = cudaFuncSetAttribute(compact_ring_kernel<FMT, LPR>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  compact_ring_kernel<FMT, LPR><<<(unsigned)units, NT, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -242,18 +380,27 @@ template <int FMT>
 cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
   constexpr int VECS = RowBytes<FMT>::value / 16;
   const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv;
-  const int64_t mean = a.total / a.n_seq;
+  const int mean = a.total / a.n_seq;
   a.splits = 1;
-  if (mean <= 64) return compact_launch<FMT, VECS, 32, true>(a, s);
-  if (!a.out_table) {
-    // In place a (layer, sequence, head) goes through its rows in order; where these are
-    // few, keys and values are cut into columns of 32 (64) bytes.
-    if (units * 2 < 152 * 8 && !getenv("NOCUT")) return compact_launch<FMT, VECS == 4 ? 2 : VECS / 4, NT, false>(a, s);
-    return compact_launch<FMT, VECS, NT, false>(a, s);
+  if (mean <= 64) {
+    const int64_t grid = (units + NT / 32 - 1) / (NT / 32);
+    if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
+    compact_kernel<FMT, 32><<<(unsigned)grid, NT, 0, s>>>(a);
+    return cudaGetLastError();
   }
-  // Rows may be shared out where none is overwritten.
-  while (a.splits < 64 && units * 2 * a.splits < 152 * 8 && mean / a.splits > 1024) a.splits *= 2;
-  return compact_launch<FMT, VECS, NT, false>(a, s);
+  if (a.out_table) {  // rows may be shared out where none is overwritten
+    a.splits = (mean + NT - 1) / NT;
+    if (units * a.splits > 0x7fffffff) return cudaErrorNotYetImplemented;
+    compact_kernel<FMT, NT><<<(unsigned)(units * a.splits), NT, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  int cut = 1;
+  while (cut < 4 && units * 2 * cut < 128) cut *= 2;
+  if constexpr (VECS >= 16)
+    if (cut == 4) return compact_ring<FMT, VECS / 4>(a, units, s);
+  if constexpr (VECS >= 8)
+    if (cut >= 2) return compact_ring<FMT, VECS / 2>(a, units, s);
+  return compact_ring<FMT, VECS>(a, units, s);
 }
 
 }  // namespace

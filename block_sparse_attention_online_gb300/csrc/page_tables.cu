@@ -7,6 +7,7 @@
 #include <cooperative_groups.h>
 #include <stdint.h>
 
+#include "cluster.cuh"
 #include "internal.h"
 
 namespace attn_skip {
@@ -17,6 +18,8 @@ namespace cg = cooperative_groups;
 constexpr int NT = 1024;  // threads a CTA of reserve
 constexpr int NW = NT / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kChunkWords = 8;  // words of 32 pages that a warp takes at a time
+constexpr int kMaxRounds = 16;  // chunks a warp has at most (2^20 pages in a cluster of eight)
 
 __device__ __forceinline__ int pages_of(int len, int ps) {  // ceil(len / ps), len >= 0
   return (int)(((unsigned)len + (unsigned)ps - 1u) / (unsigned)ps);
@@ -33,10 +36,13 @@ __device__ __forceinline__ T scan_warp(T x, int lane) {
   return x;
 }
 
+__device__ __forceinline__ int sum_warp(int x) { return __reduce_add_sync(0xffffffffu, x); }
+
 // Exclusive sum over the block's threads, and the block's total.  `tmp`: NW + 1
 // values of shared memory, free again after the next barrier.
 template <typename T>
 __device__ __forceinline__ T scan_block(T x, T *tmp, T &total) {
+  static_assert(NW == 32, "one lane a warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T upto = scan_warp(x, lane);
   if (lane == 31) tmp[warp] = upto;
@@ -56,7 +62,9 @@ struct Seqs {
   int *begin;      // [n + 1] requests of the sequences before (saturated at INT_MAX)
   int *first;      // [n] first entry past the cached ones; bit 30: it gets a copy of its last page
   int *page;       // [n] shared page that the sequence is about to write into, -1: none, -2: bad
-  int2 *slots;     // hash of the shared pages: page + 1 (0: none), a number
+  int *key;        // hash of the shared pages: page + 1 (0: none),
+  int *writers;    // how many sequences write into the page,
+  int *last;       // and the last of them
 };
 constexpr int kCopy = 1 << 30;
 __host__ __device__ constexpr int hash_slots(int n) {  // a power of two, twice n where there is room
@@ -72,23 +80,27 @@ __host__ __device__ constexpr size_t seq_bytes(int n) { return ((size_t)n * 12 +
 // the k-th request's, in the order of sequences, a copied page first, then the new
 // entries.  refs, the table and the lengths are read before the cluster's barrier and
 // written behind it, so that got_len may be kv_len.
-__global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ ReserveArgs a) {
+__global__ void __launch_bounds__(NT, 1) reserve_kernel(const __grid_constant__ ReserveArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int tmp[NW + 1];
   __shared__ long long tmp64[NW + 1];
-  __shared__ int free_of[kMaxCluster];
   const cg::cluster_group cluster = cg::this_cluster();
+  cluster_started();
   const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_seq, ps = a.page_size;
   Seqs q;
   q.begin = reinterpret_cast<int *>(smem);
   q.first = q.begin + n + 1;
   q.page = q.first + n;
-  q.slots = reinterpret_cast<int2 *>(smem + seq_bytes(n));
   const int slots = hash_slots(n);
-  // Words of 32 pages: warp w of CTA r has a.warp_words of them from (r * NW + w) * warp_words.
-  uint32_t *words = reinterpret_cast<uint32_t *>(q.slots + slots) + warp * a.warp_words;
-  const int word0 = (rank * NW + warp) * a.warp_words;
+  q.key = reinterpret_cast<int *>(smem + seq_bytes(n));
+  q.writers = q.key + slots;
+  q.last = q.writers + slots;
+  // Chunk c of 256 pages is that of warp c / n_cta % NW in CTA c % n_cta, so that the low
+  // pages, which go first, are spread over the cluster.  A warp's chunks: rounds.
+  const int all_warps = n_cta * NW, me = warp * n_cta + rank;
+  uint32_t *words = reinterpret_cast<uint32_t *>(q.last + slots) + warp * a.rounds * kChunkWords;
+  uint16_t *counts = reinterpret_cast<uint16_t *>(  // free pages of every chunk
+      reinterpret_cast<uint32_t *>(q.last + slots) + NW * a.rounds * kChunkWords);
 
   // What each sequence asks for: the loads of the first ones before those of refs.
   auto last_page = [&](int s, int from, int to, int &page, int &first, int &need) {
@@ -108,23 +120,26 @@ __global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ Res
   };
   int page0 = -1, first0 = 0, need0 = 0;
   if (tid < n) last_page(tid, a.kv_len[tid], a.new_len[tid], page0, first0, need0);
-  for (int i = tid; i < slots; i += NT) q.slots[i] = make_int2(0, 0);
+  for (int i = tid; i < 3 * slots; i += NT) q.key[i] = 0;
 
-  // The free pages of this warp's slice.
-  int free_warp = 0;
-  for (int i0 = 0; i0 < a.warp_words; i0 += 8) {
-    int r[8];
+  // The free pages of this warp's chunks.
+  cluster_wait();  // (the others' shared memory is there)
+#pragma unroll 4
+  for (int k = 0; k < a.rounds; ++k) {
+    const int c = k * all_warps + me;
+    int r[kChunkWords], found = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int p = (word0 + i0 + i) * 32 + lane;
-      r[i] = i0 + i < a.warp_words && p < a.n_pages ? a.refs[p] : 1;
+    for (int i = 0; i < kChunkWords; ++i) {
+      const int p = (c * kChunkWords + i) * 32 + lane;
+      r[i] = p < a.n_pages ? a.refs[p] : 1;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kChunkWords; ++i) {
       const unsigned m = __ballot_sync(0xffffffffu, r[i] == 0);
-      if (i0 + i < a.warp_words && lane == 0) words[i0 + i] = m;
-      free_warp += __popc(m);
+      if (lane == 0) words[k * kChunkWords + i] = m;
+      found += __popc(m);
     }
+    if (lane < n_cta) *cluster.map_shared_rank(counts + c, lane) = (uint16_t)found;
   }
 
   bool bad = false, shared = false;
@@ -143,33 +158,26 @@ __global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ Res
   // that holds it: where as many sequences write into a page as refs counts, the last of
   // them in the batch writes into the page itself.
   if (__syncthreads_or(shared)) {
-    auto slot_of = [&](int page) {  // (each page has one by the second use)
+    auto slot_of = [&](int page) {  // (there are at least as many slots as sequences)
       unsigned i = ((unsigned)page * 2654435769u) >> 15;
       while (true) {
         i &= (unsigned)slots - 1;
-        const int was = atomicCAS(&q.slots[i].x, 0, page + 1);
-        if (was == 0 || was == page + 1) return &q.slots[i].y;
+        const int was = atomicCAS(q.key + i, 0, page + 1);
+        if (was == 0 || was == page + 1) return i;
         ++i;
       }
     };
     for (int s = tid; s < n; s += NT)
-      if (q.page[s] >= 0) atomicAdd(slot_of(q.page[s]), 1);
+      if (q.page[s] >= 0) {
+        const unsigned i = slot_of(q.page[s]);
+        atomicAdd(q.writers + i, 1);
+        atomicMax(q.last + i, s);
+      }
     __syncthreads();
     for (int s = tid; s < n; s += NT)
       if (q.page[s] >= 0) {
-        q.first[s] |= kCopy;
-        if (*slot_of(q.page[s]) >= a.refs[q.page[s]]) q.begin[s] |= kCopy;  // one of them stays
-      }
-    __syncthreads();
-    for (int i = tid; i < slots; i += NT) q.slots[i].y = -1;
-    __syncthreads();
-    for (int s = tid; s < n; s += NT)
-      if (q.begin[s] & kCopy) atomicMax(slot_of(q.page[s]), s);
-    __syncthreads();
-    for (int s = tid; s < n; s += NT)
-      if (q.begin[s] & kCopy) {
-        q.begin[s] &= ~kCopy;
-        if (*slot_of(q.page[s]) == s) q.first[s] &= ~kCopy;
+        const unsigned i = slot_of(q.page[s]);
+        if (q.last[i] != s || q.writers[i] < a.refs[q.page[s]]) q.first[s] |= kCopy;
       }
     __syncthreads();
   }
@@ -186,16 +194,11 @@ __global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ Res
     }
     if (tid == 0) q.begin[n] = (int)min(total, 0x7fffffffll);
   }
-  int free_cta;
-  int k = scan_block(lane == 0 ? free_warp : 0, tmp, free_cta);
-  k = __shfl_sync(0xffffffffu, k, 0);  // free pages of the CTA's warps before this one
-  if (tid < n_cta) *cluster.map_shared_rank(&free_of[rank], tid) = free_cta;
   cluster.sync();
+  // Free pages of all chunks (every warp for itself).
   int n_free = 0;
-  for (int r = 0; r < n_cta; ++r) {
-    if (r < rank) k += free_of[r];
-    n_free += free_of[r];
-  }
+  for (int i = lane; i < a.rounds * all_warps; i += 32) n_free += counts[i];
+  n_free = sum_warp(n_free);
   // Sequences in order are served as far as the pages go (`taken` requests), and
   // those that need none and write into no shared page.
   int taken;
@@ -217,36 +220,54 @@ __global__ void __launch_bounds__(NT) reserve_kernel(const __grid_constant__ Res
     if (!cow) a.copy_dst[s] = -1;
     if (cow) atomicSub(a.refs + page, 1);
   }
-  // This warp's free pages, a word of 32 a lane.
-  for (int i0 = 0; i0 < a.warp_words && k < taken; i0 += 32) {
-    uint32_t m = i0 + lane < a.warp_words ? words[i0 + lane] : 0u;
-    const int upto = scan_warp(__popc(m), lane);
-    int r = k + upto - __popc(m);
-    k += __shfl_sync(0xffffffffu, upto, 31);
-    if (!m || r >= taken) continue;
-    int s = 0;
-    {
-      int hi = n - 1;  // the largest s with begin[s] <= r
-      while (s < hi) {
-        const int mid = (s + hi + 1) >> 1;
-        if (q.begin[mid] <= r) s = mid;
-        else hi = mid - 1;
-      }
+  // This warp's free pages, a word at a time: neighbours go to neighbouring requests, most
+  // often the same sequence's.
+  auto owner = [&](int r, int s) {  // the largest s with begin[s] <= r, which asks for something
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (q.begin[s + 1] > r) return s;
+      ++s;
     }
-    for (; m && r < taken; m &= m - 1, ++r) {
-      const int p = (word0 + i0 + lane) * 32 + __ffs(m) - 1;
-      while (q.begin[s + 1] <= r) ++s;
-      const int first = q.first[s] & ~kCopy, i = r - q.begin[s] - (q.first[s] >> 30);  // -1: the copy
-      a.refs[p] = 1;
-      a.table[(int64_t)s * a.max_pages + first + i] = p;
-      if (i < 0) a.copy_dst[s] = p;
+    int hi = n - 1;
+    while (s < hi) {
+      const int mid = (s + hi + 1) >> 1;
+      if (q.begin[mid] <= r) s = mid;
+      else hi = mid - 1;
+    }
+    return s;
+  };
+  int r0 = 0, c0 = 0, s0 = 0;  // free pages of the chunks before c0; a sequence at or before r0's
+  for (int k = 0; k < a.rounds; ++k) {
+    const int c = k * all_warps + me;
+    int more = 0;
+    for (int i = c0 + lane; i < c; i += 32) more += counts[i];
+    r0 += sum_warp(more);
+    if (r0 >= taken) break;
+    c0 = c + 1;
+    s0 = owner(r0, s0);
+#pragma unroll 2
+    for (int i = 0; i < kChunkWords; ++i) {
+      const uint32_t m = words[k * kChunkWords + i];
+      const int r = r0 + __popc(m & ((1u << lane) - 1u));
+      r0 += __popc(m);
+      const bool mine = (m >> lane & 1u) && r < taken;
+      if (mine) {
+        const int s = owner(r, s0), first = q.first[s];
+        const int p = (c * kChunkWords + i) * 32 + lane;
+        const int e = r - q.begin[s] - (first >> 30);  // -1: the copy
+        a.refs[p] = 1;
+        a.table[(int64_t)s * a.max_pages + (first & ~kCopy) + e] = p;
+        if (e < 0) a.copy_dst[s] = p;
+        s0 = s;
+      }
+      s0 = __reduce_max_sync(0xffffffffu, s0);
     }
   }
 }
 
 // ---------------------------------------------------------------------- fork --
 constexpr int FT = 256;
-constexpr int kEntries = 4;  // table entries a thread loads at a time
+constexpr int kEntries = 8;  // table entries a thread loads at a time
 
 // A length in range, or the nearest that is.
 __device__ __forceinline__ int clip(int x, int hi, bool &bad) {
@@ -271,19 +292,23 @@ __global__ void __launch_bounds__(FT) fork_kernel(const __grid_constant__ ForkAr
       if ((bad || len0 != 0) && tid == 0) atomicOr(a.err, kErrBadArg);
       return;
     }
+    const int old = a.kv_len[s];
+    const int32_t *from = a.table + (int64_t)s * a.max_pages;
+    int32_t *to = a.out_table + (int64_t)d * a.max_pages;
+    int p[kEntries];  // (entries behind the last page may be read)
+    auto load = [&](int e0) {
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i)
+        p[i] = e0 + i * FT < a.max_pages ? from[e0 + i * FT] : 0;
+    };
+    load(tid);
     bool follows = false;  // a follower of s comes before
     for (int e = tid; e < d; e += FT) follows |= a.parent[e] == s;
     follows = __syncthreads_or(follows);
-    bool lost = false;
-    const int old = a.kv_len[s];
-    lost = old < 0 || old > most;  // (the old row reports it)
+    const bool lost = old < 0 || old > most;  // (the old row reports it)
     const int n = pages_of(clip(len0, lost ? 0 : old, bad), ps);
-    const int32_t *from = a.table + (int64_t)s * a.max_pages;
-    int32_t *to = a.out_table + (int64_t)d * a.max_pages;
     for (int e0 = tid; e0 < n; e0 += kEntries * FT) {
-      int p[kEntries];
-#pragma unroll
-      for (int i = 0; i < kEntries; ++i) p[i] = e0 + i * FT < n ? from[e0 + i * FT] : 0;
+      if (e0 != tid) load(e0);
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) {
         if (e0 + i * FT >= n) break;
@@ -334,15 +359,15 @@ __global__ void __launch_bounds__(FT) fork_kernel(const __grid_constant__ ForkAr
 }  // namespace
 
 size_t pages_reserve_max_seqs() { return 8192; }
-size_t pages_reserve_max_pages() { return (size_t)1 << 22; }
+size_t pages_reserve_max_pages() { return (size_t)kMaxRounds * kMaxCluster * NW * kChunkWords * 32; }
 
 cudaError_t launch_pages_reserve(ReserveArgs a, cudaStream_t s) {
-  // A CTA alone for small pools; from 8192 pages on a cluster of eight.
-  const int n_cta = a.n_pages > 8192 ? kMaxCluster : 1;
-  const int all = (a.n_pages + 31) / 32;
-  a.warp_words = (all + n_cta * NW - 1) / (n_cta * NW);
-  const size_t smem =
-      seq_bytes(a.n_seq) + hash_slots(a.n_seq) * sizeof(int2) + (size_t)a.warp_words * NW * 4;
+  // A CTA alone looks at 8192 pages in one round, a cluster of eight at 65536.
+  const int n_cta = a.n_pages > NW * kChunkWords * 32 ? kMaxCluster : 1;
+  const int per_round = n_cta * NW * kChunkWords * 32;
+  a.rounds = (a.n_pages + per_round - 1) / per_round;
+  const size_t smem = seq_bytes(a.n_seq) + hash_slots(a.n_seq) * 3 * sizeof(int) +
+                      (size_t)a.rounds * NW * (kChunkWords * 4 + n_cta * 2);
   if (smem > 48 * 1024 - 1024) {  // (static shared memory counts too)
     const cudaError_t e = cudaFuncSetAttribute(
         reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -21,8 +21,8 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
-#include <stdlib.h>
 
+#include "cluster.cuh"
 #include "internal.h"
 #include "tc_common.cuh"
 
@@ -98,7 +98,7 @@ __device__ __forceinline__ u64 scan_warp(u64 x, int lane) {
 // Sum of the weights of tokens [i0, i1), for the whole warp.
 template <bool BF16, bool HAS_Q>
 __device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int lane, bool &bad) {
-  constexpr int U = 8;        // tokens a lane loads at a time
+    constexpr int U = 8;        // tokens a lane loads at a time
   constexpr int FLUSH = 256;  // tokens a lane sums in 32 bits (2^22 steps each at most)
   auto two = [](float x, float y) {
     return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
@@ -168,9 +168,10 @@ __device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int lan
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(NT, 3) verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ u64 sums[2][kMaxCluster * NW];  // of every warp of the cluster
   const cg::cluster_group cluster = cg::this_cluster();
+  cluster_started();
   const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x / n_cta;
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Veri
         atomicOr(a.err, kErrBadArg);
       }
     }
+    cluster_wait();
     return;
   }
   const int esize = BF16 ? 2 : 4;
@@ -227,26 +229,28 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Veri
     else row.hole = rejected;
   }
 
+  cluster_wait();  // (the others' shared memory is there)
   // Every warp's stretch, a multiple of 32 tokens.
   const int all = n_cta * NW, mine = rank * NW + warp;
   const int len = ((a.V + all - 1) / all + 31) & ~31;
   const int i0 = (int)min((int64_t)mine * len, (int64_t)a.V), i1 = min(i0 + len, a.V);
-  u64 total = 0, before = 0, stretch = 0;
-  for (int round = 0; round < 2; ++round) {  // the second one only where p - q is 0 throughout
-    stretch = row.q ? sum_stretch<BF16, true>(row, i0, i1, lane, bad)
-                    : sum_stretch<BF16, false>(row, i0, i1, lane, bad);
+  u64 total = 0, below = 0;  // sums of all warps, and of those of the CTAs before this one
+  int round = 0;
+  while (true) {  // a second time only where p - q is 0 throughout
+    const u64 stretch = row.q ? sum_stretch<BF16, true>(row, i0, i1, lane, bad)
+                              : sum_stretch<BF16, false>(row, i0, i1, lane, bad);
     if (lane < n_cta) *cluster.map_shared_rank(&sums[round][mine], lane) = stretch;
     cluster.sync();
-    // Sums of all warps, and of those before this one.
-    u64 below = 0, every = 0;
+    u64 before = 0, every = 0;
     for (int i = lane; i < all; i += 32) {
       const u64 v = sums[round][i];
       every += v;
-      below += i < mine ? v : 0;
+      before += i < rank * NW ? v : 0;
     }
     total = sum_warp(every);
-    before = sum_warp(below);
-    if (total || acc == n) break;
+    below = sum_warp(before);
+    if (round == 1 || total || acc == n) break;
+    round = 1;
     row.q = nullptr;
     row.hole = -1;
   }
@@ -263,23 +267,37 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Veri
     a.n_accepted[s] = acc;
     if (!total) out[acc] = a.V - 1;
   }
-  if (threshold < before || threshold - before >= stretch) return;
-  // The stretch that holds the threshold: a piece a lane, then the lane's piece.
-  const int piece = len / 32, j0 = min(i0 + lane * piece, i1), j1 = min(j0 + piece, i1);
-  u64 w = 0;
-  bool noted = false;
-#pragma unroll 8
-  for (int i = j0; i < j1; ++i) w += weight<BF16>(row, i, noted);
-  const u64 upto = before + scan_warp(w, lane);
-  if (threshold < upto && threshold >= upto - w) {
-    u64 f = upto - w;
-    for (int i = j0; i < j1; ++i) {
-      f += weight<BF16>(row, i, noted);
-      if (f > threshold) {
-        out[acc] = i;
-        break;
-      }
-    }
+  // The CTA whose stretches hold the threshold narrows them down: to one warp's, to a
+  // warp's part of that one, and so on to 32 tokens.
+  const u64 *part = &sums[round][rank * NW];
+  int lo = rank * NW * len, step = len;
+  while (true) {
+    const u64 v = lane < NW ? part[lane] : 0, upto = below + scan_warp(v, lane);
+    const unsigned here = __ballot_sync(0xffffffffu, threshold < upto && threshold >= upto - v);
+    if (!here) return;  // (the same for the whole CTA)
+    const int w = __ffs(here) - 1;
+    lo += w * step;
+    below = __shfl_sync(0xffffffffu, upto - v, w);
+    if (step == 32) break;
+    const int end = min(lo + step, a.V);
+    step = ((step + NW - 1) / NW + 31) & ~31;
+    u64 sum = 0;
+    const int first = lo + warp * step, last = min(first + step, end);
+    bool noted = false;
+#pragma unroll 4
+    for (int i = first + lane; i < last; i += 32) sum += weight<BF16>(row, i, noted);
+    sum = sum_warp(sum);
+    __syncthreads();  // the sums before are no longer needed
+    if (lane == 0) sums[0][warp] = sum;
+    __syncthreads();
+    part = sums[0];
+  }
+  if (warp == 0) {
+    const int i = lo + lane;
+    bool noted = false;
+    const u64 w = i < a.V ? weight<BF16>(row, i, noted) : 0;
+    const u64 upto = below + scan_warp(w, lane);
+    if (threshold < upto && threshold >= upto - w) out[acc] = i;
   }
 }
 
@@ -306,10 +324,11 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
-  // CTAs a sequence: as many as leave every warp 128 tokens, up to eight.
+  // CTAs a sequence.
   int n_cta = 1;
-  while (n_cta < 8 && (int64_t)n_cta * NW * 128 < a.V) n_cta *= 2;
-  if (const char *e = getenv("VERIFY_CTAS")) n_cta = atoi(e);
+  while (n_cta < 8 && (int64_t)n_cta * NW * 128 < a.V &&
+         ((int64_t)n_cta * 2 * a.n_seq <= 456 || a.V / n_cta > 32768))
+    n_cta *= 2;
   return a.bf16 ? launch<true>(a, n_cta, s) : launch<false>(a, n_cta, s);
 }
 

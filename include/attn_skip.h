@@ -705,7 +705,7 @@ int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, int total, in
  * not fit and all after it stay as they are, but for those that need no page and
  * write into no shared one.
  *
- *  refs        [n_pages] int32 (device), updated; n_pages <= 4,194,304
+ *  refs        [n_pages] int32 (device), updated; n_pages <= 1,048,576
  *  page_table  [n_seq, max_pages] int32 (device), updated; n_seq <= 8192
  *  kv_len, new_len  [n_seq] int32 (device)
  *  got_len     [n_seq] int32 (device): new_len[s], or kv_len[s] for a sequence

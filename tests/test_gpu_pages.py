@@ -94,7 +94,7 @@ def test_reserve_holders_outside_of_the_batch():
 
 
 def test_reserve_the_largest_pool_and_every_page_free():
-    n_pages = 1 << 22
+    n_pages = 1 << 20
     R = torch.zeros(n_pages, dtype=torch.int32, device=DEV)
     T = torch.full((3, 5000), -1, dtype=torch.int32, device=DEV)
     got, _, _ = bs.attn_skip_pages_reserve(R, T, i32([0, 0, 0]), i32([16 * 5000, 1, 16 * 4000]), 16)

@@ -69,7 +69,7 @@ def test_reserve_rejects_invalid_arguments(lib, kw):
     assert reserve(lib, **kw) == bs.ATTN_EINVAL
 
 
-@pytest.mark.parametrize("kw", [dict(n_seq=8193), dict(n_pages=(1 << 22) + 1),
+@pytest.mark.parametrize("kw", [dict(n_seq=8193), dict(n_pages=(1 << 20) + 1),
                                 dict(max_pages=1 << 28), dict(ps=1 << 30, max_pages=2)])
 def test_reserve_limits(lib, kw):
     assert reserve(lib, **kw) == bs.ATTN_EUNSUPPORTED
