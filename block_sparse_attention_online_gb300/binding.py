@@ -963,22 +963,30 @@ def attn_skip_kv_compact(kv, keep, cu_keep, page_table, start=None, out_table=No
 
 
 class _On:
-    """A tensor's device, for the calls without a cache."""
+    """A device, for the calls without a cache."""
+    __slots__ = ("index", "device")
 
-    def __init__(self, x):
-        if not x.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        self.index, self.device = x.get_device(), x.device
+    def __init__(self, index):
+        self.index, self.device = index, torch.device("cuda", index)
 
 
-def _tables(refs, page_table, kv_len, new_len, on):
-    if refs.dim() != 1 or page_table.dim() != 2:
-        raise ValueError("refs must be [n_pages] and page_table [n_seq, max_pages]")
-    n = page_table.shape[0]
-    _ints("refs", refs, (refs.numel(),), on)
-    _ints("page_table", page_table, page_table.shape, on)
-    _ints("kv_len", kv_len, (n,), on)
-    return n
+@functools.lru_cache(maxsize=64)
+def _on(index):
+    """The device that a tensor's get_device() names."""
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    return _On(index)
+
+
+def _tables(refs, page_table, kv_len, on):
+    """n_pages, n_seq and max_pages of the arrays, checked."""
+    pages, shape = refs.numel(), page_table.shape
+    if len(shape) != 2:
+        raise ValueError("page_table must be [n_seq, max_pages]")
+    _ints("refs", refs, (pages,), on)
+    _ints("page_table", page_table, shape, on)
+    _ints("kv_len", kv_len, shape[:1], on)
+    return pages, shape[0], shape[1]
 
 
 def attn_skip_pages_reserve(refs, page_table, kv_len, new_len, page_size, out=None, stream=None):
@@ -987,20 +995,21 @@ def attn_skip_pages_reserve(refs, page_table, kv_len, new_len, page_size, out=No
     copy_src, copy_dst)`` [n_seq] (or fills ``out``, whose got_len may be kv_len): the
     length that each sequence now has room for (kv_len where the pages ran out) and
     the pages to copy, for :func:`attn_skip_kv_copy_pages`.  All int32."""
-    on = _On(refs)
+    on = _on(refs.get_device())
     if _elsewhere(on, stream):
         with _switched(on, stream):
             return attn_skip_pages_reserve(refs, page_table, kv_len, new_len, page_size, out)
-    n = _tables(refs, page_table, kv_len, new_len, on)
+    n_pages, n, max_pages = _tables(refs, page_table, kv_len, on)
     _ints("new_len", new_len, (n,), on)
     if out is None:
-        got, src, dst = out = torch.empty((3, n), dtype=_int32, device=on.device).unbind(0)
+        out = got, src, dst = (torch.empty_like(kv_len), torch.empty_like(kv_len),
+                               torch.empty_like(kv_len))
     else:
         got, src, dst = out
         for x in out:
             _ints("out", x, (n,), on)
     st = (_lib or load()).attn_skip_pages_reserve(
-        refs.data_ptr(), refs.numel(), page_table.data_ptr(), n, page_table.shape[1], page_size,
+        refs.data_ptr(), n_pages, page_table.data_ptr(), n, max_pages, page_size,
         kv_len.data_ptr(), new_len.data_ptr(), got.data_ptr(), src.data_ptr(), dst.data_ptr(),
         _raw_stream(on.index))
     if st:
@@ -1015,12 +1024,12 @@ def attn_skip_pages_fork(refs, page_table, kv_len, new_len, page_size, parent=No
     empty sequence), as row d of ``out_table`` [n_new, max_pages] (made here if not
     given, filled up with -1); refs follows.  Without ``parent`` every sequence
     keeps its row and is cut to new_len.  Returns the new batch's table.  All int32."""
-    on = _On(refs)
+    on = _on(refs.get_device())
     if _elsewhere(on, stream):
         with _switched(on, stream):
             return attn_skip_pages_fork(refs, page_table, kv_len, new_len, page_size, parent,
                                         out_table)
-    n = _tables(refs, page_table, kv_len, new_len, on)
+    n_pages, n, max_pages = _tables(refs, page_table, kv_len, on)
     n_new, par, out = n, None, None
     if parent is None:
         if out_table is not None:
@@ -1028,7 +1037,7 @@ def attn_skip_pages_fork(refs, page_table, kv_len, new_len, page_size, parent=No
     else:
         n_new = parent.numel()
         _ints("parent", parent, (n_new,), on)
-        shape = (n_new, page_table.shape[1])
+        shape = (n_new, max_pages)
         if out_table is None:
             out_table = torch.full(shape, -1, dtype=_int32, device=on.device)
         else:
@@ -1036,7 +1045,7 @@ def attn_skip_pages_fork(refs, page_table, kv_len, new_len, page_size, parent=No
         par, out = parent.data_ptr(), out_table.data_ptr()
     _ints("new_len", new_len, (n_new,), on)
     st = (_lib or load()).attn_skip_pages_fork(
-        refs.data_ptr(), refs.numel(), page_table.data_ptr(), n, page_table.shape[1], page_size,
+        refs.data_ptr(), n_pages, page_table.data_ptr(), n, max_pages, page_size,
         kv_len.data_ptr(), new_len.data_ptr(), n_new, par, out, _raw_stream(on.index))
     if st:
         _check("attn_skip_pages_fork", st)
@@ -1045,12 +1054,13 @@ def attn_skip_pages_fork(refs, page_table, kv_len, new_len, page_size, parent=No
 
 def _rows_of(name, x, rows, V, dtype, on):
     """Row stride of the probabilities x [at least rows, V]."""
-    if x.dim() != 2 or x.shape[0] < rows or x.shape[1] != V or x.dtype is not dtype \
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 2 or shape[0] < rows or shape[1] != V or x.dtype is not dtype \
             or x.get_device() != on.index:
         raise ValueError(f"{name} must be a {dtype} tensor [{rows}, {V}] on {on.device}")
-    if V > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < V:
+    if V > 1 and stride[1] != 1 or rows > 1 and stride[0] < V:
         raise ValueError(f"the rows of {name} must be dense and must not overlap")
-    return x.stride(0) if rows > 1 else V
+    return stride[0] if rows > 1 else V
 
 
 def attn_skip_verify_drafts(target, drafted, cu_drafts, max_draft, u_accept, u_sample, draft=None,
@@ -1062,37 +1072,38 @@ def attn_skip_verify_drafts(target, drafted, cu_drafts, max_draft, u_accept, u_s
     [n_seq + 1] int32; u_accept [total] and u_sample [n_seq] fp32 random numbers in
     [0, 1).  Returns int32 ``(tokens [n_seq, max_draft + 1], n_accepted [n_seq])``, or
     fills ``out``: the accepted tokens, one drawn token, -1 behind it."""
-    on = _On(target)
+    on = _on(target.get_device())
     if _elsewhere(on, stream):
         with _switched(on, stream):
             return attn_skip_verify_drafts(target, drafted, cu_drafts, max_draft, u_accept,
                                            u_sample, draft, out)
-    n, total, dt = cu_drafts.numel() - 1, drafted.numel(), _dtype_code(target)
-    if target.dim() != 2 or n < 1 or max_draft < 0:
+    n, total, shape, dtype = cu_drafts.numel() - 1, drafted.numel(), target.shape, target.dtype
+    if len(shape) != 2 or n < 1 or max_draft < 0:
         raise ValueError("target must be [total + n_seq, V], cu_drafts [n_seq + 1], max_draft >= 0")
-    V = target.shape[1]
-    stride = _rows_of("target", target, total + n, V, target.dtype, on)
-    draft_stride = 0
+    V = shape[1]
+    stride = _rows_of("target", target, total + n, V, dtype, on)
+    q, draft_stride = None, 0
     if draft is not None:
-        draft_stride = _rows_of("draft", draft, total, V, target.dtype, on)
+        draft_stride = _rows_of("draft", draft, total, V, dtype, on)
+        q = draft.data_ptr()
     _ints("drafted", drafted, (total,), on)
     _ints("cu_drafts", cu_drafts, (n + 1,), on)
     _per_sequence("u_accept", u_accept, total, _float32, on)
     _per_sequence("u_sample", u_sample, n, _float32, on)
     if out is None:
-        tokens = torch.empty((n, max_draft + 1), dtype=_int32, device=on.device)
-        accepted = torch.empty((n,), dtype=_int32, device=on.device)
+        out = tokens, accepted = (torch.empty((n, max_draft + 1), dtype=_int32, device=on.device),
+                                  torch.empty((n,), dtype=_int32, device=on.device))
     else:
         tokens, accepted = out
         _ints("tokens", tokens, (n, max_draft + 1), on)
         _ints("n_accepted", accepted, (n,), on)
     st = (_lib or load()).attn_skip_verify_drafts(
-        target.data_ptr(), stride, None if draft is None else draft.data_ptr(), draft_stride, dt, V,
-        n, total, max_draft, drafted.data_ptr(), cu_drafts.data_ptr(), u_accept.data_ptr(),
-        u_sample.data_ptr(), tokens.data_ptr(), accepted.data_ptr(), _raw_stream(on.index))
+        target.data_ptr(), stride, q, draft_stride, _dtype_code(target), V, n, total, max_draft,
+        drafted.data_ptr(), cu_drafts.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
+        tokens.data_ptr(), accepted.data_ptr(), _raw_stream(on.index))
     if st:
         _check("attn_skip_verify_drafts", st)
-    return tokens, accepted
+    return out
 
 
 def attn_skip_selftest_wait_timeout(stream=None, device=None):

@@ -70,15 +70,15 @@ __global__ void __launch_bounds__(NT) copy_pages_kernel(const __grid_constant__ 
 }
 
 // ----------------------------------------------------------------- kept rows --
-// Row keep[j] of a sequence to position start + j.  One group of threads (a CTA, or a
-// warp where sequences keep few rows) takes the key and value rows of one (layer,
-// sequence, head), in batches: first the batch's places (position -> page, slot)
-// into shared memory, then its rows, loads before stores.
+// Row keep[j] of a sequence to position start + j, in each head, in each layer.  A row's
+// place is found once (position -> page, slot -> bytes) and shared by the threads that
+// move it, 16 bytes each.
 //
-// In place this is safe without a second buffer, because keep[j] >= start + j is
-// checked: row j is read in its own batch, and what overwrites its place is row
-// keep[j] - start >= j, of the same batch or a later one, stored after a barrier that
-// follows the loads.
+// Into other pages any row may go at any time: CTAs take 256 rows of the batch each.  In
+// place no second buffer is needed either, because keep[j] >= start + j is checked: what
+// overwrites the place that row j comes from is row keep[j] - start >= j.  So a (layer,
+// sequence, head) goes through its rows in chunks, the chunk's loads before its stores,
+// with a barrier between them.
 struct Place {  // as the tables say it
   int from_page, from_slot, to_page, to_slot;  // from_page < 0: nothing to move
 };
@@ -92,35 +92,36 @@ template <int FMT> struct RowBytes {
   static constexpr int value = FMT == kKvBf16 ? 256 : FMT == kKvE4m3 ? 128 : 64;
 };
 
-// What a group works on.
+// What a group of threads works on in place, or a row's sequence.
 struct Unit {
-  int layer, s, h;
   int n, start;              // kept rows of the sequence, position of the first
   const int32_t *keep;
   const int32_t *from, *to;  // the sequence's rows of the tables
-  int from_room, to_room;    // positions that they have
+  int from_room, to_room;    // positions that they have (at most 2^30)
 };
 
-// False where there is nothing to do (bad bounds are reported).
-__device__ __forceinline__ bool unit_of(const CompactArgs &a, int layer, int s, int h, bool first,
-                                        Unit &x) {
-  if (layer >= a.kv.n) return false;
-  const int c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
-  if (c0 < 0 || c1 < c0 || c1 > a.total) {
-    if (first) atomicOr(a.err, kErrBadArg);
-    return false;
-  }
-  x.layer = layer;
-  x.s = s;
-  x.h = h;
+__device__ __forceinline__ bool good_bounds(const CompactArgs &a, int c0, int c1) {
+  return c0 >= 0 && c1 >= c0 && c1 <= a.total;
+}
+
+// Head h of sequence s, whose rows of keep are [c0, c1).
+__device__ __forceinline__ Unit unit_of(const CompactArgs &a, int s, int h, int c0, int c1) {
+  Unit x;
   x.n = c1 - c0;
   x.start = a.start ? a.start[s] : 0;
   x.keep = a.keep + (a.per_head ? (int64_t)h * a.total : 0) + c0;
   x.from = a.table + (int64_t)s * a.max_pages;
   x.to = a.out_table ? a.out_table + (int64_t)s * a.out_max_pages : x.from;
-  x.from_room = a.max_pages * a.kv.page_size;  // (at most 2^30)
+  x.from_room = a.max_pages * a.kv.page_size;
   x.to_room = a.out_table ? a.out_max_pages * a.kv.page_size : x.from_room;
-  return true;
+  return x;
+}
+
+// Remainder by n, the quotient stays.
+__device__ __forceinline__ int take(unsigned &i, unsigned n) {
+  const unsigned q = i / n, r = i - q * n;
+  i = q;
+  return (int)r;
 }
 
 // Where row j, of position src, comes from and goes to (from_page -1: nothing to move);
@@ -153,82 +154,135 @@ __device__ __forceinline__ Move move_of(const CompactArgs &a, const Place &r, in
               r.to_page * a.kv.page_stride + (int64_t)(head_row + r.to_slot) * ROW};
 }
 
-// One group of threads (a CTA, or a warp where sequences keep few rows): the key and
-// value rows of one (layer, sequence, head), or a share of them.
-template <int FMT, int GROUP>
-__global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ CompactArgs a) {
+// A thread's row's scales, of keys and values.
+template <int FMT> struct Scales {
+  uint8_t s[2];
+  uint2 b[2];
+  __device__ __forceinline__ void load(const KvLayers &kv, int layer, int64_t row) {
+    const auto &l = kv.layer[layer];
+    s[0] = l.k_scale[row];
+    s[1] = l.v_scale[row];
+    if constexpr (FMT == kKvNvfp4) {
+      b[0] = *reinterpret_cast<const uint2 *>(l.k_bs + row * 8);
+      b[1] = *reinterpret_cast<const uint2 *>(l.v_bs + row * 8);
+    }
+  }
+  __device__ __forceinline__ void store(const KvLayers &kv, int layer, int64_t row) const {
+    const auto &l = kv.layer[layer];
+    l.k_scale[row] = s[0];
+    l.v_scale[row] = s[1];
+    if constexpr (FMT == kKvNvfp4) {
+      *reinterpret_cast<uint2 *>(l.k_bs + row * 8) = b[0];
+      *reinterpret_cast<uint2 *>(l.v_bs + row * 8) = b[1];
+    }
+  }
+};
+template <> struct Scales<kKvBf16> {
+  __device__ __forceinline__ void load(const KvLayers &, int, int64_t) {}
+  __device__ __forceinline__ void store(const KvLayers &, int, int64_t) const {}
+};
+
+// The key and value rows of a group's threads (its `at`, one row a thread, is filled by
+// all of them) move, in chunks; `mine` is this thread's own place.
+template <int FMT, int GROUP, int U, typename Sync>
+__device__ __forceinline__ void move_rows(const CompactArgs &a, int layer, int head_row, const Move *at,
+                                          const Place &mine, int t, int m, Sync sync) {
   constexpr int LPR = RowBytes<FMT>::value / 16;  // lanes a row
-  constexpr int U = GROUP == 32 ? 2 : 4;          // rows a thread loads at a time
   constexpr int CHUNK = GROUP / LPR * U;          // rows of the group
-  constexpr int BATCH = GROUP == 32 ? 32 : NT;    // rows whose places are found at once
-  constexpr int GROUPS = NT / GROUP;
-  static_assert(BATCH == GROUP && BATCH % CHUNK == 0, "a row a thread, whole chunks");
-  __shared__ Move moves[GROUPS][BATCH];
-  const int g = threadIdx.x / GROUP, t = threadIdx.x % GROUP;
-  Move *at = moves[g];
-  auto sync = [&] {
-    if constexpr (GROUP == 32) __syncwarp();
-    else __syncthreads();
-  };
-  unsigned i = blockIdx.x * GROUPS + g;
-  auto next = [&](unsigned n) {
-    const unsigned q = i / n, r = i - q * n;
-    i = q;
-    return (int)r;
-  };
-  const int split = next((unsigned)a.splits), h = next((unsigned)a.kv.Hkv), s = next((unsigned)a.n_seq);
-  Unit x;
-  if (!unit_of(a, (int)i, s, h, t == 0, x)) return;  // (whole groups)
-  const auto &l = a.kv.layer[x.layer];
-  const int head_row = h * a.kv.page_size, page_rows = a.kv.Hkv * a.kv.page_size;
+  static_assert(GROUP % CHUNK == 0, "whole chunks");
+  const auto &l = a.kv.layer[layer];
   uint8_t *keys = l.k + t % LPR * 16, *values = l.v + t % LPR * 16;
+  const int page_rows = a.kv.Hkv * a.kv.page_size;
+  Scales<FMT> sc;
+  if (mine.from_page >= 0)
+    sc.load(a.kv, layer, (int64_t)mine.from_page * page_rows + head_row + mine.from_slot);
+  for (int c = 0; c < m; c += CHUNK) {
+    uint4 v[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t byte = at[c + t / LPR + u * (GROUP / LPR)].from;
+      if (byte < 0) continue;
+      v[u][0] = *reinterpret_cast<const uint4 *>(keys + byte);
+      v[u][1] = *reinterpret_cast<const uint4 *>(values + byte);
+    }
+    sync();  // in place: all loads up to here come before the stores below
+    if (c == 0 && mine.from_page >= 0)
+      sc.store(a.kv, layer, (int64_t)mine.to_page * page_rows + head_row + mine.to_slot);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t byte = at[c + t / LPR + u * (GROUP / LPR)].to;
+      if (byte < 0) continue;
+      *reinterpret_cast<uint4 *>(keys + byte) = v[u][0];
+      *reinterpret_cast<uint4 *>(values + byte) = v[u][1];
+    }
+  }
+}
+
+// Into other pages: one CTA for 256 rows of the batch in one (layer, head), and one that
+// looks at all bounds.
+template <int FMT>
+__global__ void __launch_bounds__(NT, 4) compact_out_kernel(const __grid_constant__ CompactArgs a) {
+  __shared__ Move at[NT];
+  const int t = threadIdx.x;
   bool bad = false;
-  for (int j0 = split * BATCH; j0 < x.n; j0 += a.splits * BATCH) {
-    sync();  // the batch before is done with the places
-    const int m = min(BATCH, x.n - j0);
+  if (blockIdx.x == gridDim.x - 1) {
+    for (int s = t; s < a.n_seq; s += NT) bad |= !good_bounds(a, a.cu_keep[s], a.cu_keep[s + 1]);
+    if (bad) atomicOr(a.err, kErrBadArg);
+    return;
+  }
+  unsigned i = blockIdx.x;
+  const int j0 = take(i, (unsigned)((a.total + NT - 1) / NT)) * NT, h = take(i, (unsigned)a.kv.Hkv);
+  const int layer = (int)i, row = j0 + t;
+  const int head_row = h * a.kv.page_size;
+  Place mine = kNowhere;
+  if (row < a.total) {
+    int s = 0, hi = a.n_seq;  // entries of cu_keep[1..] at or before the row: its sequence
+    while (s < hi) {
+      const int mid = (s + hi) >> 1;
+      if (a.cu_keep[mid + 1] <= row) s = mid + 1;
+      else hi = mid;
+    }
+    if (s < a.n_seq) {
+      const int c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
+      if (good_bounds(a, c0, c1) && row >= c0 && row < c1) {
+        const Unit x = unit_of(a, s, h, c0, c1);
+        mine = place_of(a, x, row - c0, x.keep[row - c0], bad);
+      }
+    }
+  }
+  check_place(a, mine, bad);
+  at[t] = move_of<RowBytes<FMT>::value>(a, mine, head_row);
+  __syncthreads();
+  move_rows<FMT, NT, 4>(a, layer, head_row, at, mine, t, min(NT, a.total - j0), [] {});
+  if (bad) atomicOr(a.err, kErrBadArg);
+}
+
+// In place, sequences that keep at most a.few rows: a warp for a (layer, sequence, head).
+template <int FMT>
+__global__ void __launch_bounds__(NT, 4) compact_warp_kernel(const __grid_constant__ CompactArgs a) {
+  __shared__ Move moves[NT / 32][32];
+  const int t = threadIdx.x & 31;
+  Move *at = moves[threadIdx.x >> 5];
+  unsigned i = blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
+  const int h = take(i, (unsigned)a.kv.Hkv), s = take(i, (unsigned)a.n_seq), layer = (int)i;
+  if (layer >= a.kv.n) return;
+  const int c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
+  if (!good_bounds(a, c0, c1)) {
+    if (t == 0) atomicOr(a.err, kErrBadArg);
+    return;
+  }
+  const Unit x = unit_of(a, s, h, c0, c1);
+  if (x.n > a.few) return;  // the other kernel's
+  const int head_row = h * a.kv.page_size;
+  bool bad = false;
+  for (int j0 = 0; j0 < x.n; j0 += 32) {
+    __syncwarp();  // the rows before are done with the places
     Place mine = kNowhere;
-    if (t < m) mine = place_of(a, x, j0 + t, x.keep[j0 + t], bad);
+    if (j0 + t < x.n) mine = place_of(a, x, j0 + t, x.keep[j0 + t], bad);
     check_place(a, mine, bad);
     at[t] = move_of<RowBytes<FMT>::value>(a, mine, head_row);
-    sync();
-    uint8_t sc[2];
-    uint2 bs[2];
-    if (FMT != kKvBf16 && mine.from_page >= 0) {
-      const int64_t row = (int64_t)mine.from_page * page_rows + head_row + mine.from_slot;
-      sc[0] = l.k_scale[row];
-      sc[1] = l.v_scale[row];
-      if (FMT == kKvNvfp4) {
-        bs[0] = *reinterpret_cast<const uint2 *>(l.k_bs + row * 8);
-        bs[1] = *reinterpret_cast<const uint2 *>(l.v_bs + row * 8);
-      }
-    }
-    for (int c = 0; c < m; c += CHUNK) {
-      uint4 v[U][2];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t byte = at[c + t / LPR + u * (GROUP / LPR)].from;
-        if (byte < 0) continue;
-        v[u][0] = *reinterpret_cast<const uint4 *>(keys + byte);
-        v[u][1] = *reinterpret_cast<const uint4 *>(values + byte);
-      }
-      sync();  // all loads up to here come before the stores below
-      if (FMT != kKvBf16 && c == 0 && mine.from_page >= 0) {
-        const int64_t row = (int64_t)mine.to_page * page_rows + head_row + mine.to_slot;
-        l.k_scale[row] = sc[0];
-        l.v_scale[row] = sc[1];
-        if (FMT == kKvNvfp4) {
-          *reinterpret_cast<uint2 *>(l.k_bs + row * 8) = bs[0];
-          *reinterpret_cast<uint2 *>(l.v_bs + row * 8) = bs[1];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t byte = at[c + t / LPR + u * (GROUP / LPR)].to;
-        if (byte < 0) continue;
-        *reinterpret_cast<uint4 *>(keys + byte) = v[u][0];
-        *reinterpret_cast<uint4 *>(values + byte) = v[u][1];
-      }
-    }
+    __syncwarp();
+    move_rows<FMT, 32, 2>(a, layer, head_row, at, mine, t, min(32, x.n - j0), [] { __syncwarp(); });
   }
   if (bad) atomicOr(a.err, kErrBadArg);
 }
@@ -246,33 +300,31 @@ __device__ __forceinline__ void copy_async(uint32_t smem, const void *gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
 
-template <int FMT, int LPR>
-__global__ void __launch_bounds__(NT) compact_ring_kernel(const __grid_constant__ CompactArgs a) {
-  constexpr int PARTS = RowBytes<FMT>::value / 16 / LPR;
-  constexpr int U = 4;                  // rows a thread loads
-  constexpr int CHUNK = NT / LPR * U;   // rows of the CTA
-  constexpr int MINE = CHUNK < NT ? 2 : 4;  // places a thread finds
-  constexpr int BATCH = MINE * NT, PER = BATCH / CHUNK;  // rows, chunks
+// The chunk and batch sizes of a CTA, and its shared memory.
+template <int FMT, int LPR> struct Ring {
+  static constexpr int PARTS = RowBytes<FMT>::value / 16 / LPR;
+  static constexpr int U = 4;                          // rows a thread loads
+  static constexpr int CHUNK = NT / LPR * U;           // rows of the CTA
+  static constexpr int MINE = CHUNK < NT ? 2 : 4;      // places a thread finds
+  static constexpr int BATCH = MINE * NT, PER = BATCH / CHUNK;  // rows, chunks
+  static constexpr int BYTES = kStages * U * NT * 16 + 2 * BATCH * (int)sizeof(Move);
   static_assert(PER >= kStages - 1, "the first loads are of the first batch, the last of the next");
-  extern __shared__ __align__(16) uint4 ring[];  // [kStages][U][NT], then the places
-  Move *at = reinterpret_cast<Move *>(ring + kStages * U * NT);  // [2][BATCH]
+};
+
+// One (layer, sequence, head), keys or values, some columns.
+template <int FMT, int LPR>
+__device__ __forceinline__ void compact_unit(const CompactArgs &a, const Unit &x, int layer, int h,
+                                             int value, int part, uint4 *ring, bool &bad) {
+  using R = Ring<FMT, LPR>;
+  constexpr int U = R::U, CHUNK = R::CHUNK, MINE = R::MINE, BATCH = R::BATCH, PER = R::PER;
+  Move *at = reinterpret_cast<Move *>(ring + kStages * U * NT);  // [2][BATCH], behind [kStages][U][NT]
   const int t = threadIdx.x;
-  unsigned i = blockIdx.x;
-  auto next = [&](unsigned n) {
-    const unsigned q = i / n, r = i - q * n;
-    i = q;
-    return (int)r;
-  };
-  const int part = next(PARTS), value = next(2), h = next((unsigned)a.kv.Hkv), s = next((unsigned)a.n_seq);
-  Unit x;
-  if (!unit_of(a, (int)i, s, h, t == 0, x)) return;
-  const auto &l = a.kv.layer[x.layer];
+  const auto &l = a.kv.layer[layer];
   uint8_t *codes = (value ? l.v : l.k) + (part * LPR + t % LPR) * 16;
   uint8_t *scale = value ? l.v_scale : l.k_scale, *block = value ? l.v_bs : l.k_bs;
   const int head_row = h * a.kv.page_size, page_rows = a.kv.Hkv * a.kv.page_size;
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring) + t * 16;
   const bool with_scales = FMT != kKvBf16 && part == 0;
-  bool bad = false;
 
   // The places of batch b, in three steps.
   auto positions = [&](int b, int (&src)[MINE]) {
@@ -360,19 +412,49 @@ __global__ void __launch_bounds__(NT) compact_ring_kernel(const __grid_constant_
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (bad) atomicOr(a.err, kErrBadArg);
+  __syncthreads();  // the unit is done with the places
 }
 
 template <int FMT, int LPR>
-cudaError_t compact_ring(const CompactArgs &a, int64_t units, cudaStream_t s) {
-  units *= 2 * (RowBytes<FMT>::value / 16 / LPR);
-  if (units > 0x7fffffff) return cudaErrorNotYetImplemented;
-  constexpr int batch = (NT / LPR * 4 < NT ? 2 : 4) * NT;
-  constexpr int smem = kStages * 4 * NT * 16 + 2 * batch * (int)sizeof(Move);
+__global__ void __launch_bounds__(NT) compact_ring_kernel(const __grid_constant__ CompactArgs a) {
+  constexpr int PARTS = Ring<FMT, LPR>::PARTS;
+  extern __shared__ __align__(16) uint4 ring[];
+  bool bad = false;
+  // The units with more than a.few rows among this CTA's, which lie gridDim.x apart; 32 of
+  // them are looked at at a time (by every warp).
+  const int64_t all = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * 2 * PARTS;
+  for (int64_t u0 = blockIdx.x; u0 < all; u0 += 32ll * gridDim.x) {
+    const int64_t u = u0 + (int64_t)(threadIdx.x & 31) * gridDim.x;
+    bool is = false;
+    if (u < all) {
+      unsigned i = (unsigned)(u / (2 * PARTS * a.kv.Hkv));
+      const int s = take(i, (unsigned)a.n_seq), c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
+      is = good_bounds(a, c0, c1) && c1 - c0 > a.few;
+      bad |= !good_bounds(a, c0, c1);
+    }
+    for (unsigned many = __ballot_sync(0xffffffffu, is); many; many &= many - 1) {
+      const int64_t unit = u0 + (int64_t)(__ffs(many) - 1) * gridDim.x;
+      unsigned i = (unsigned)(unit / (2 * PARTS));
+      const int part = (int)(unit % PARTS), value = (int)(unit / PARTS & 1);
+      const int h = take(i, (unsigned)a.kv.Hkv), s = take(i, (unsigned)a.n_seq);
+      const Unit x = unit_of(a, s, h, a.cu_keep[s], a.cu_keep[s + 1]);
+      compact_unit<FMT, LPR>(a, x, (int)i, h, value, part, ring, bad);
+    }
+  }
+  if (bad) atomicOr(a.err, kErrBadArg);
+}
+
+
+template <int FMT, int LPR>
+cudaError_t compact_ring(const CompactArgs &a, cudaStream_t s) {
+  constexpr int smem = Ring<FMT, LPR>::BYTES;
   const cudaError_t e = cudaFuncSetAttribute(compact_ring_kernel<FMT, LPR>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  compact_ring_kernel<FMT, LPR><<<(unsigned)units, NT, smem, s>>>(a);
+  const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * 2 * Ring<FMT, LPR>::PARTS;
+  const int64_t grid = a.few > 0 ? min(units, (int64_t)152 * 2) : units;
+  if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
+  compact_ring_kernel<FMT, LPR><<<(unsigned)grid, NT, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -380,27 +462,29 @@ template <int FMT>
 cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
   constexpr int VECS = RowBytes<FMT>::value / 16;
   const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv;
-  const int mean = a.total / a.n_seq;
-  a.splits = 1;
-  if (mean <= 64) {
-    const int64_t grid = (units + NT / 32 - 1) / (NT / 32);
+  if (a.out_table) {
+    const int64_t grid = (int64_t)a.kv.n * a.kv.Hkv * ((a.total + NT - 1) / NT) + 1;
     if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
-    compact_kernel<FMT, 32><<<(unsigned)grid, NT, 0, s>>>(a);
+    compact_out_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
     return cudaGetLastError();
   }
-  if (a.out_table) {  // rows may be shared out where none is overwritten
-    a.splits = (mean + NT - 1) / NT;
-    if (units * a.splits > 0x7fffffff) return cudaErrorNotYetImplemented;
-    compact_kernel<FMT, NT><<<(unsigned)(units * a.splits), NT, 0, s>>>(a);
-    return cudaGetLastError();
+  // Sequences of up to 64 rows go to warps, but where most are longer; then longer ones, if
+  // there can be any, to CTAs.
+  a.few = a.total / a.n_seq > 64 ? 0 : 64;
+  if (a.few > 0) {
+    const int64_t grid = (units + NT / 32 - 1) / (NT / 32);
+    if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
+    compact_warp_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || a.total <= a.few) return e;
   }
   int cut = 1;
   while (cut < 4 && units * 2 * cut < 128) cut *= 2;
   if constexpr (VECS >= 16)
-    if (cut == 4) return compact_ring<FMT, VECS / 4>(a, units, s);
+    if (cut == 4) return compact_ring<FMT, VECS / 4>(a, s);
   if constexpr (VECS >= 8)
-    if (cut >= 2) return compact_ring<FMT, VECS / 2>(a, units, s);
-  return compact_ring<FMT, VECS>(a, units, s);
+    if (cut >= 2) return compact_ring<FMT, VECS / 2>(a, s);
+  return compact_ring<FMT, VECS>(a, s);
 }
 
 }  // namespace

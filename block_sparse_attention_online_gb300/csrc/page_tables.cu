@@ -19,7 +19,7 @@ constexpr int NT = 1024;  // threads a CTA of reserve
 constexpr int NW = NT / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kChunkWords = 8;  // words of 32 pages that a warp takes at a time
-constexpr int kMaxRounds = 16;  // chunks a warp has at most (2^20 pages in a cluster of eight)
+constexpr int kMaxRounds = (1 << 20) / (kMaxCluster * NW * kChunkWords * 32);  // chunks of a warp
 
 __device__ __forceinline__ int pages_of(int len, int ps) {  // ceil(len / ps), len >= 0
   return (int)(((unsigned)len + (unsigned)ps - 1u) / (unsigned)ps);
@@ -42,14 +42,14 @@ __device__ __forceinline__ int sum_warp(int x) { return __reduce_add_sync(0xffff
 // values of shared memory, free again after the next barrier.
 template <typename T>
 __device__ __forceinline__ T scan_block(T x, T *tmp, T &total) {
-  static_assert(NW == 32, "one lane a warp");
+  static_assert(NW <= 32, "a lane a warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T upto = scan_warp(x, lane);
   if (lane == 31) tmp[warp] = upto;
   __syncthreads();
   if (warp == 0) {
-    const T w = tmp[lane], u = scan_warp(w, lane);
-    tmp[lane] = u - w;
+    const T w = lane < NW ? tmp[lane] : T(0), u = scan_warp(w, lane);
+    if (lane < NW) tmp[lane] = u - w;
     if (lane == 31) tmp[NW] = u;
   }
   __syncthreads();
@@ -203,11 +203,12 @@ __global__ void __launch_bounds__(NT, 1) reserve_kernel(const __grid_constant__ 
   // those that need none and write into no shared page.
   int taken;
   {
-    int lo = 0, hi = n;  // the largest i with begin[i] <= n_free
+    int lo = 0, hi = n;  // the largest i with begin[i] <= n_free, by 32 probes at a time
     while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (q.begin[mid] <= n_free) lo = mid;
-      else hi = mid - 1;
+      const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
+      const int c = __popc(__ballot_sync(0xffffffffu, i <= hi && q.begin[min(i, hi)] <= n_free));
+      lo += c * step;
+      hi = min(hi, lo + step - 1);
     }
     taken = q.begin[lo];
   }

@@ -71,15 +71,14 @@ def copy_pages(x, src, dst):
 
 
 def compact(x, keep, cu, table, ps, start=None, out_table=None):
-    """x [n_pages, Hkv, ps, ...] after the rows moved, one after the other from a copy."""
+    """x [n_pages, Hkv, ps, ...] after the rows moved, from a copy."""
     y = x.copy()
     out = table if out_table is None else out_table
     for s in range(len(cu) - 1):
-        for j in range(cu[s + 1] - cu[s]):
-            to = (0 if start is None else start[s]) + j
-            for h in range(x.shape[1]):
-                k = keep[h][cu[s] + j] if np.ndim(keep) == 2 else keep[cu[s] + j]
-                y[out[s][to // ps], h, to % ps] = x[table[s][k // ps], h, k % ps]
+        to = (0 if start is None else start[s]) + np.arange(cu[s + 1] - cu[s])
+        for h in range(x.shape[1]):
+            k = np.asarray((keep[h] if np.ndim(keep) == 2 else keep)[cu[s]:cu[s + 1]], dtype=int)
+            y[np.asarray(out[s])[to // ps], h, to % ps] = x[np.asarray(table[s])[k // ps], h, k % ps]
     return y
 
 

@@ -313,6 +313,34 @@ def test_compact_moves_rows_by_one(fmt):
                      for p in before])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "nvfp4"])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_compact_one_long_sequence_among_many(fmt, in_place):
+    """Most sequences keep nothing or a few rows, one keeps thousands; kept positions in any
+    order, some twice (in place at least at their own place)."""
+    r, ps, n = random.Random(5), 32, 90
+    L = [r.randint(1, 70) for _ in range(n)]
+    L[17], L[60] = 4000, 200
+    per = [plain.up(x, ps) for x in L]
+    n_pages = 2 * sum(per)
+    ids, width = r.sample(range(n_pages), n_pages), max(per)
+    table = [[ids.pop() for _ in range(p)] + [-1] * (width - p) for p in per]
+    out = None if in_place else [[ids.pop() for _ in range(p)] + [-1] * (width - p) for p in per]
+    keep, cu = [], [0]
+    for s, x in enumerate(L):
+        c = r.randint(2500, 3000) if s == 17 else 100 if s == 60 else r.choice((0, 0, r.randint(0, x)))
+        keep += [r.randrange(j, x) if r.random() < 0.9 else j for j in range(c)]
+        cu.append(len(keep))
+    assert cu[-1] < 64 * n
+    kv, parts = pools(fmt, 2, n_pages, 2, ps, 3)
+    before = host(parts)
+    bs.attn_skip_kv_compact(kv, i32(keep), i32(cu), i32(table),
+                            out_table=None if out is None else i32(out))
+    no_error()
+    same(parts, [{m: plain.compact(x, keep, cu, table, ps, None, out) for m, x in p.items()}
+                 for p in before])
+
+
 def test_compact_leaves_rows_outside_the_sequences_alone_and_reports():
     kv, parts = pool("e4m3", 6, 2, 16, 9)
     before = host([parts])
