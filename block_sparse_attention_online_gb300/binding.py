@@ -946,12 +946,14 @@ def attn_skip_kv_compact(kv, keep, cu_keep, page_table, start=None, out_table=No
         with _switched(kv, stream):
             return attn_skip_kv_compact(kv, keep, cu_keep, page_table, start, out_table)
     n, max_pages = _batch(kv, cu_keep, page_table, start)
-    total = keep.shape[-1]
-    per_head = keep.dim() == 2
+    shape = keep.shape
+    if not shape:
+        raise ValueError("keep must be [total] or [Hkv, total]")
+    total, per_head = shape[-1], len(shape) == 2
     _ints("keep", keep, (kv.Hkv, total) if per_head else (total,), kv)
     out, out_pages = None, 0
     if out_table is not None:
-        out_pages = out_table.shape[-1]
+        out_pages = out_table.shape[-1] if out_table.dim() else 0
         _ints("out_table", out_table, (n, out_pages), kv)
         out = out_table.data_ptr()
     st = (_lib or load()).attn_skip_kv_compact(

@@ -826,7 +826,7 @@ extern "C" attn_status attn_skip_pages_fork(int32_t *refs, int n_pages, const in
   if (parent && (n_new <= 0 || !out_table || out_table == page_table || !aligned4(parent) ||
                  !aligned4(out_table)))
     return ATTN_EINVAL;
-  if ((int64_t)n_seq + (parent ? n_new : 0) > 0x7fffffff) return ATTN_EUNSUPPORTED;
+  if (n_seq > 65536 || (parent && n_new > 65536)) return ATTN_EUNSUPPORTED;
   ForkArgs a{};
   a.refs = refs; a.out_table = out_table; a.table = page_table;
   a.kv_len = kv_len; a.new_len = new_len; a.parent = parent;

@@ -34,7 +34,7 @@ typedef unsigned long long u64;
 
 constexpr int NT = 512;
 constexpr int NW = NT / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t load_bits(const void *row, int64_t i) {  // as fp32 bits
@@ -303,11 +303,6 @@ __global__ void __launch_bounds__(NT, 3) verify_kernel(const __grid_constant__ V
 
 template <bool BF16>
 cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
-  if (n_cta > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        verify_kernel<BF16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.n_seq * (unsigned)n_cta);
   cfg.blockDim = dim3(NT);
@@ -326,7 +321,7 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
   // CTAs a sequence.
   int n_cta = 1;
-  while (n_cta < 8 && (int64_t)n_cta * NW * 128 < a.V &&
+  while (n_cta < kMaxCluster && (int64_t)n_cta * NW * 128 < a.V &&
          ((int64_t)n_cta * 2 * a.n_seq <= 456 || a.V / n_cta > 32768))
     n_cta *= 2;
   return a.bf16 ? launch<true>(a, n_cta, s) : launch<false>(a, n_cta, s);

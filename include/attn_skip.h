@@ -732,7 +732,8 @@ attn_status attn_skip_pages_reserve(int32_t *refs, int n_pages, int32_t *page_ta
  * reach 0 are free, and hold their rows until they are given out again.
  *
  *  refs        [n_pages] int32 (device), updated
- *  page_table  [n_seq, max_pages], kv_len [n_seq] int32 (device): the old batch
+ *  page_table  [n_seq, max_pages], kv_len [n_seq] int32 (device): the old batch;
+ *              n_seq and n_new at most 65536
  *  parent      [n_new] int32 (device), -1: an empty sequence (new_len 0); or NULL
  *  new_len     [n_new] (without parents [n_seq]) int32 (device), at most the
  *              parent's kv_len
@@ -780,8 +781,8 @@ attn_status attn_skip_kv_copy_pages(const attn_kv_pages *kv, int n_layers, int n
  * ascending positions from start[s] on); other positions than start[s] .. are
  * left as they were.  The rows written must be no other sequence's (attn_skip_pages_reserve
  * gives a copy of the last page only), and with out_table none that is read.
- * EINVAL as for attn_skip_kv_append.  Left out and reported by
- * attn_skip_last_device_error: sequences with bad bounds, rows of positions or
+ * EINVAL as for attn_skip_kv_append.  out_table = page_table is in place.  Left out
+ * and reported by attn_skip_last_device_error: sequences with bad bounds, rows of positions or
  * page ids out of range, in place rows with keep below their new position.
  */
 attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layers, int n_seq, int total,

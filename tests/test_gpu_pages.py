@@ -409,3 +409,47 @@ def test_calls_on_another_stream_and_in_a_graph():
         assert R.tolist() == back[0] and T.tolist() == want[1]
         same(parts, copied)
     no_error()
+
+
+# ------------------------------------------------------------------ large pools --
+def test_offsets_beyond_32_bits():
+    """k and v of 5 GB each: pages whose first byte lies behind 2^32."""
+    n_pages, Hkv, ps = 20000, 8, 128
+    shape = (n_pages, Hkv, ps, 128)
+    k, v = (torch.empty(shape, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    high = [n_pages - 1 - i for i in range(6)]
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for x in (k, v):
+        for p in high + [0, 1, 2]:
+            x[p] = torch.randn(shape[1:], device=DEV, generator=g).to(torch.bfloat16)
+    kv = bs.PagedKV("bf16", k, v)
+    before = [[x[p].clone() for p in high] for x in (k, v)]
+    bs.attn_skip_kv_copy_pages(kv, i32([high[0], high[1]]), i32([1, high[2]]))
+    for x, b in zip((k, v), before):
+        assert torch.equal(x[1], b[0]) and torch.equal(x[high[2]], b[1])
+    # Rows of two pages move up by 100; the same into other pages.
+    table, n = [[high[3], high[4]]], 2 * ps - 100
+    bs.attn_skip_kv_compact(kv, i32(range(100, 2 * ps)), i32([0, n]), i32(table),
+                            out_table=i32([[high[5], 0]]))
+    bs.attn_skip_kv_compact(kv, i32(range(100, 2 * ps)), i32([0, n]), i32(table))
+    for x, b in zip((k, v), before):
+        rows = torch.cat((b[3], b[4]), 1)  # [Hkv, 2 ps, 128]
+        want = torch.cat((rows[:, 100:], rows[:, 2 * ps - 100:]), 1)
+        assert torch.equal(torch.cat((x[high[3]], x[high[4]]), 1), want)
+        assert torch.equal(x[high[5]], want[:, :ps])
+        assert torch.equal(x[0][:, :n - ps], want[:, ps:n])
+    no_error()
+
+
+def test_long_sequences_use_a_few_pages_of_a_wide_table():
+    # 2^30 positions in the table, of which three pages are used.
+    width = (1 << 30) // 256
+    T = torch.full((2, width), -1, dtype=torch.int32, device=DEV)
+    T[1, -2:] = i32([5, 7])
+    R = i32([0, 0, 0, 0, 0, 1, 0, 1])
+    top = (1 << 30) - 300
+    # (A length that the pages do not cover would do for the arithmetic: only its end is used.)
+    got, src, dst = bs.attn_skip_pages_reserve(R, T, i32([0, top]), i32([256, 1 << 30]), 256)
+    assert got.tolist() == [256, 1 << 30] and T[0, 0] == 0 and T[1, -1] == 1 and T[1, -2] == 5
+    assert src.tolist() == dst.tolist() == [-1, -1] and R.tolist() == [1, 1, 0, 0, 0, 1, 0, 1]
+    no_error()

@@ -225,3 +225,33 @@ def test_given_outputs_another_stream_and_a_graph():
         t, n = want(b)
         assert np.array_equal(out[0].cpu().numpy(), t) and np.array_equal(out[1].cpu().numpy(), n)
     no_error()
+
+
+def test_rows_far_apart():
+    """Rows 2^30 elements apart: the last one starts behind 2^32."""
+    V, stride = 5000, 1 << 30
+    a = inputs(31, [3, 1], V, torch.bfloat16)
+    far = torch.empty(5 * stride + V, dtype=torch.bfloat16, device=DEV)
+    target = far.as_strided((6, V), (stride, 1))
+    target.copy_(a["target"])
+    t, n = want(a)
+    tokens, accepted = call(dict(a, target=target))
+    assert np.array_equal(tokens.cpu().numpy(), t) and np.array_equal(accepted.cpu().numpy(), n)
+    draft = far[7:].as_strided((4, V), (stride, 1))
+    draft.copy_(a["draft"])
+    tokens, accepted = call(dict(a, draft=draft))
+    assert np.array_equal(tokens.cpu().numpy(), t) and np.array_equal(accepted.cpu().numpy(), n)
+    no_error()
+
+
+def test_calls_on_two_streams_at_once():
+    cases = [inputs(40 + i, [2, 0, 4, 1], 30000) for i in range(2)]
+    wants = [want(a) for a in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[call(a, stream=s) for _ in range(5)] for a, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for runs, (t, n) in zip(got, wants):
+        for tokens, accepted in runs:
+            assert np.array_equal(tokens.cpu().numpy(), t) and np.array_equal(accepted.cpu().numpy(), n)
+    no_error()

@@ -81,6 +81,16 @@ def test_fork_rejects_invalid_arguments(lib, kw):
     assert fork(lib, **kw) == bs.ATTN_EINVAL
 
 
+@pytest.mark.parametrize("kw", [dict(n_seq=65537), dict(n_new=65537), dict(max_pages=1 << 28)])
+def test_fork_limits(lib, kw):
+    assert fork(lib, **kw) == bs.ATTN_EUNSUPPORTED
+
+
+def test_fork_without_parents_needs_no_second_table(lib):
+    # (Refused for another reason: the call has got past the tables.)
+    assert fork(lib, parent=None, out=None, n_new=0, n_seq=65537) == bs.ATTN_EUNSUPPORTED
+
+
 @pytest.mark.parametrize("call", [copy, compact])
 def test_layers_are_checked(lib, call):
     for kw in BAD_PAGES:
