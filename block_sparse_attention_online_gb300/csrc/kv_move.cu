@@ -468,9 +468,11 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
     compact_out_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
     return cudaGetLastError();
   }
-  // Sequences of up to 64 rows go to warps, but where most are longer; then longer ones, if
-  // there can be any, to CTAs.
-  a.few = a.total / a.n_seq > 64 ? 0 : 64;
+  // Short sequences go to warps, longer ones, if there can be any, to CTAs behind them, or
+  // all to CTAs where most are long.
+  constexpr int row = 2 * RowBytes<FMT>::value;
+  a.few = (int)(min(48 * units, (int64_t)98304) / row);
+  if (a.total / a.n_seq > a.few) a.few = 0;
   if (a.few > 0) {
     const int64_t grid = (units + NT / 32 - 1) / (NT / 32);
     if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;

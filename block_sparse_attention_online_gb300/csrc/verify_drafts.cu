@@ -319,10 +319,9 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
-  // CTAs a sequence.
   int n_cta = 1;
-  while (n_cta < kMaxCluster && (int64_t)n_cta * NW * 128 < a.V &&
-         ((int64_t)n_cta * 2 * a.n_seq <= 456 || a.V / n_cta > 32768))
+  while (n_cta < kMaxCluster && (((int64_t)n_cta * 2 * a.n_seq <= 152 && a.V > n_cta * NW * 256) ||
+                                 a.V / n_cta > 32768))
     n_cta *= 2;
   return a.bf16 ? launch<true>(a, n_cta, s) : launch<false>(a, n_cta, s);
 }
