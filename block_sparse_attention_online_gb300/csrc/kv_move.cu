@@ -13,20 +13,20 @@ constexpr int NT = 256;
 constexpr int kVec = 4;                    // 16-byte vectors a thread
 constexpr int kPiece = NT * kVec * 16;     // bytes a CTA
 
-// One CTA: a piece of one page's k or v in one layer, or all its scales.
+// One CTA: a piece of one page's k or v in one layer, or all its scales.  DRAM bounds it:
+// 96 pages of 64 bf16 rows and 8 heads in 32 layers, 1.6 GB, 231 us (6.9 TB/s); entries
+// without a page cost a CTA that looks at them (32 of these 128).
 __global__ void __launch_bounds__(NT) copy_pages_kernel(const __grid_constant__ CopyPagesArgs a) {
   const unsigned per_page = 2u * a.chunks + (a.kv.format != kKvBf16);
   const unsigned unit = blockIdx.x / per_page;
   unsigned c = blockIdx.x - unit * per_page;
   const unsigned layer = unit / (unsigned)a.n_pairs, i = unit - layer * (unsigned)a.n_pairs;
   const int src = a.src[i], dst = a.dst[i];
-  if (src == dst) return;
-  if (src < 0 || dst < 0 || src >= a.kv.n_pages || dst >= a.kv.n_pages) {
-    // (an entry with -1 stands for none)
-    if ((src < -1 || dst < -1 || src >= a.kv.n_pages || dst >= a.kv.n_pages) && threadIdx.x == 0)
-      atomicOr(a.err, kErrBadArg);
+  if (src < -1 || dst < -1 || src >= a.kv.n_pages || dst >= a.kv.n_pages) {
+    if (threadIdx.x == 0) atomicOr(a.err, kErrBadArg);
     return;
   }
+  if (src == dst || src < 0 || dst < 0) return;  // (-1 stands for none)
   const int rows = a.kv.Hkv * a.kv.page_size;
   const auto &l = a.kv.layer[layer];
   if (c < 2u * a.chunks) {
@@ -218,8 +218,10 @@ __device__ __forceinline__ void move_rows(const CompactArgs &a, int layer, int h
   }
 }
 
-// Into other pages: one CTA for 256 rows of the batch in one (layer, head), and one that
-// looks at all bounds.
+// Into other pages: one CTA for 256 rows of the batch in one (layer, head), whatever
+// sequences they are of, and one that looks at all bounds.  11000 rows of 4 heads in 4
+// layers, NVFP4: 7.2 us, 5.4 for the bytes; 8196 of 8 heads in 8 layers, bf16: 83 us, 80 for
+// the bytes.  (A CTA a stretch of one sequence in turn: 10 and 85 us.)
 template <int FMT>
 __global__ void __launch_bounds__(NT, 4) compact_out_kernel(const __grid_constant__ CompactArgs a) {
   __shared__ Move at[NT];
@@ -258,6 +260,8 @@ __global__ void __launch_bounds__(NT, 4) compact_out_kernel(const __grid_constan
 }
 
 // In place, sequences that keep at most a.few rows: a warp for a (layer, sequence, head).
+// Latency bounds it (bounds, positions, page ids, rows: 16 sequences of up to 4 rows, 8
+// heads, 32 layers, E4M3 3.4 us).
 template <int FMT>
 __global__ void __launch_bounds__(NT, 4) compact_warp_kernel(const __grid_constant__ CompactArgs a) {
   __shared__ Move moves[NT / 32][32];
@@ -293,7 +297,8 @@ __global__ void __launch_bounds__(NT, 4) compact_warp_kernel(const __grid_consta
 // memory by asynchronous copies, kStages - 1 chunks ahead of the one that is stored
 // (every thread stores what it has loaded itself).  Their places are found a batch of
 // rows at a time, the page ids of the batch after the next and the positions of the one
-// behind it under way meanwhile.
+// behind it under way meanwhile.  8196 rows of 8 heads in 8 layers, bf16: 85 us, 80 for the
+// bytes at the copy rate; with loads one chunk ahead in registers 110, without 244.
 constexpr int kStages = 4;
 
 __device__ __forceinline__ void copy_async(uint32_t smem, const void *gmem) {
@@ -469,7 +474,10 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
     return cudaGetLastError();
   }
   // Short sequences go to warps, longer ones, if there can be any, to CTAs behind them, or
-  // all to CTAs where most are long.
+  // all to CTAs where most are long.  Warps are as quick as CTAs up to about 20 KB of a
+  // (layer, sequence, head) where there are 256 of these, 70 KB where there are 1024, 130 KB
+  // where there are 4096 (bf16, sequences of up to 128 rows: 14.4 us by warps and 7.4 by
+  // CTAs; 18.9 and 22.0; 57 and 83), less where lengths differ.
   constexpr int row = 2 * RowBytes<FMT>::value;
   a.few = (int)(min(48 * units, (int64_t)98304) / row);
   if (a.total / a.n_seq > a.few) a.few = 0;
@@ -480,6 +488,8 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.total <= a.few) return e;
   }
+  // Columns, until there are 128 CTAs: bf16, 8196 rows of 8 heads in one layer 62 us uncut,
+  // 37 in halves, 24 in quarters; in 8 layers 85, 95 and 90.
   int cut = 1;
   while (cut < 4 && units * 2 * cut < 128) cut *= 2;
   if constexpr (VECS >= 16)

@@ -249,6 +249,9 @@ def test_copy_pages(fmt, n_layers, n_pages, Hkv, ps, n, together):
     reported()
     bs.attn_skip_kv_copy_pages(kv, i32([]), i32([]))
     no_error()
+    for bad in (n_pages, -2):  # onto itself
+        bs.attn_skip_kv_copy_pages(kv, i32([-1, bad]), i32([0, bad]))
+        reported()
     same(parts, now)
 
 
