@@ -800,7 +800,7 @@ extern "C" attn_status attn_skip_pages_reserve(int32_t *refs, int n_pages, int32
       tables_check(refs, n_pages, page_table, n_seq, max_pages, page_size, kv_len, new_len);
   if (st != ATTN_OK) return st;
   if (!got_len || !copy_src || !copy_dst || !aligned4(got_len) || !aligned4(copy_src) ||
-      !aligned4(copy_dst))
+      !aligned4(copy_dst) || got_len == copy_src || got_len == copy_dst || copy_src == copy_dst)
     return ATTN_EINVAL;
   if ((size_t)n_seq > pages_reserve_max_seqs() || (size_t)n_pages > pages_reserve_max_pages() ||
       max_pages >= 1 << 30)  // (the kernel keeps a flag in bit 30 of an entry's number)
@@ -851,7 +851,7 @@ extern "C" attn_status attn_skip_verify_drafts(
   if (draft && (draft_stride < V || draft_stride >= (int64_t)1 << 40)) return ATTN_EINVAL;
   if (total > 0 && max_draft > 0 && (!drafted || !u_accept)) return ATTN_EINVAL;
   if (!aligned4(drafted) || !aligned4(cu_drafts) || !aligned4(u_accept) || !aligned4(u_sample) ||
-      !aligned4(tokens) || !aligned4(n_accepted))
+      !aligned4(tokens) || !aligned4(n_accepted) || tokens == n_accepted)
     return ATTN_EINVAL;
   if (V > 1 << 28 || n_seq > 1 << 24 || max_draft > kMaxPositions || total > kMaxPositions)
     return ATTN_EUNSUPPORTED;

@@ -712,7 +712,8 @@ int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, int total, in
  *              that stays as it is; may be kv_len
  *  copy_src, copy_dst  [n_seq] int32 (device)
  *  page_size   at least 1
- * EINVAL: a null or misaligned (4 bytes) pointer, a size that is not positive.
+ * EINVAL: a null or misaligned (4 bytes) pointer, a size that is not positive, one
+ * array for two outputs.
  * Checked by the kernel and reported by attn_skip_last_device_error (ATTN_EINVAL):
  * a kv_len below 0, a new_len below kv_len or above max_pages * page_size, a partly
  * filled page's id out of range (the sequence stays as it is).
@@ -818,8 +819,8 @@ attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layers, int n_se
  *  max_draft  host bound on n
  *  tokens     [n_seq, max_draft + 1] int32: the accepted tokens, the drawn one,
  *             -1 behind it; n_accepted [n_seq] int32
- * EINVAL: a null or misaligned pointer, a size that is not positive (total,
- * max_draft: below 0), a stride below V; V above 2^28 is EUNSUPPORTED.  Reported by
+ * EINVAL: a null or misaligned pointer, one array for both outputs, a size that is
+ * not positive (total, max_draft: below 0), a stride below V; V above 2^28 is EUNSUPPORTED.  Reported by
  * attn_skip_last_device_error: a sequence with bad bounds (tokens and n_accepted -1),
  * a drafted token outside [0, V) (rejected), a probability in a row that is drawn from
  * outside [0, 2), or NaN (it counts as 0), a random number outside [0, 1) (u_sample:

@@ -27,7 +27,7 @@ def layers(*kv):
 
 def reserve(lib, **kw):
     a = dict(refs=A, n_pages=9, table=A, n_seq=2, max_pages=4, ps=16, kv_len=A, new_len=A, got=A,
-             src=A, dst=A, stream=None)
+             src=2 * A, dst=3 * A, stream=None)
     a.update(kw)
     return lib.attn_skip_pages_reserve(*a.values())
 
@@ -54,7 +54,7 @@ def compact(lib, one=None, **kw):
 
 def verify(lib, **kw):
     a = dict(target=A, ts=100, draft=A, ds=100, dt=1, V=100, n_seq=2, total=3, max_draft=2,
-             drafted=A, cu=A, ua=A, us=A, tokens=A, acc=A, stream=None)
+             drafted=A, cu=A, ua=A, us=A, tokens=A, acc=2 * A, stream=None)
     a.update(kw)
     return lib.attn_skip_verify_drafts(*a.values())
 
@@ -64,7 +64,8 @@ TABLES = [dict(refs=None), dict(refs=A + 2), dict(n_pages=0), dict(table=None), 
           dict(new_len=None), dict(new_len=A + 1)]
 
 
-@pytest.mark.parametrize("kw", TABLES + [dict(got=None), dict(src=None), dict(dst=A + 2)])
+@pytest.mark.parametrize("kw", TABLES + [dict(got=None), dict(src=None), dict(dst=A + 2),
+                                         dict(got=2 * A), dict(src=3 * A), dict(dst=A)])
 def test_reserve_rejects_invalid_arguments(lib, kw):
     assert reserve(lib, **kw) == bs.ATTN_EINVAL
 
@@ -129,7 +130,7 @@ def test_compact_rejects_invalid_arguments(lib, kw):
     dict(target=None), dict(target=A + 2), dict(draft=A + 1), dict(ts=99), dict(ds=99), dict(dt=2),
     dict(V=0), dict(n_seq=0), dict(total=-1), dict(max_draft=-1), dict(drafted=None), dict(cu=None),
     dict(ua=None), dict(us=None), dict(tokens=None), dict(acc=None), dict(us=A + 2),
-    dict(tokens=A + 1), dict(ts=1 << 40), dict(dt=0, target=A + 1),
+    dict(tokens=A + 1), dict(ts=1 << 40), dict(dt=0, target=A + 1), dict(tokens=2 * A),
 ])
 def test_verify_rejects_invalid_arguments(lib, kw):
     assert verify(lib, **kw) == bs.ATTN_EINVAL
