@@ -1,11 +1,15 @@
 // Rows and pages of the paged cache moved as they are: whole pages copied, and the
 // rows that a sequence keeps moved together, in the caches of all layers at once.
+#include <cooperative_groups.h>
 #include <stdint.h>
 
+#include "cluster.cuh"
 #include "internal.h"
 
 namespace attn_skip {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int NT = 256;
 
@@ -292,70 +296,90 @@ __global__ void __launch_bounds__(NT, 4) compact_warp_kernel(const __grid_consta
 }
 
 // In place, sequences that keep many rows: they have to go in order, so what bounds a
-// (layer, sequence, head) is how much it has under way.  A CTA takes keys or values,
-// and 16 * LPR bytes of each row.  Rows go chunk by chunk through a ring in shared
-// memory by asynchronous copies, kStages - 1 chunks ahead of the one that is stored
-// (every thread stores what it has loaded itself).  Their places are found a batch of
-// rows at a time, the page ids of the batch after the next and the positions of the one
-// behind it under way meanwhile.  8196 rows of 8 heads in 8 layers, bf16: 85 us, 80 for the
-// bytes at the copy rate; with loads one chunk ahead in registers 110, without 244.
-constexpr int kStages = 4;
+// (layer, sequence, head) is how much it has under way, and at what rate an SM loads and
+// stores rows.  A CTA takes keys or values; where there are few of these, the CTAs of a
+// cluster share the rows out, chunk by chunk in turn, with the cluster's barrier in place of
+// the CTA's.  Chunks go through a ring in shared memory by asynchronous copies, kStages - 1
+// ahead of the one that is stored (every thread stores what it has loaded itself).  Their
+// places are found a batch of chunks at a time, the page ids of the batch after the next
+// and the positions of the one behind it under way meanwhile.  8196 rows of 8 heads in 8
+// layers, bf16: 85 us, 80 for the bytes at the copy rate; with loads one chunk ahead in
+// registers 110, without 244.
+constexpr int kStages = 5;
 
 __device__ __forceinline__ void copy_async(uint32_t smem, const void *gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
 
 // The chunk and batch sizes of a CTA, and its shared memory.
-template <int FMT, int LPR> struct Ring {
-  static constexpr int PARTS = RowBytes<FMT>::value / 16 / LPR;
-  static constexpr int U = 4;                          // rows a thread loads
-  static constexpr int CHUNK = NT / LPR * U;           // rows of the CTA
-  static constexpr int MINE = CHUNK < NT ? 2 : 4;      // places a thread finds
+template <int FMT> struct Ring {
+  static constexpr int LPR = RowBytes<FMT>::value / 16;  // lanes a row
+  static constexpr int U = 4;                            // rows a thread loads
+  static constexpr int CHUNK = NT / LPR * U;             // rows of the CTA
+  static constexpr int MINE = CHUNK < NT ? 2 : 4;        // places a thread finds
   static constexpr int BATCH = MINE * NT, PER = BATCH / CHUNK;  // rows, chunks
   static constexpr int BYTES = kStages * U * NT * 16 + 2 * BATCH * (int)sizeof(Move);
   static_assert(PER >= kStages - 1, "the first loads are of the first batch, the last of the next");
 };
 
-// One (layer, sequence, head), keys or values, some columns.
-template <int FMT, int LPR>
+// One (layer, sequence, head), keys or values; the whole cluster of n_cta CTAs.
+template <int FMT>
 __device__ __forceinline__ void compact_unit(const CompactArgs &a, const Unit &x, int layer, int h,
-                                             int value, int part, uint4 *ring, bool &bad) {
-  using R = Ring<FMT, LPR>;
-  constexpr int U = R::U, CHUNK = R::CHUNK, MINE = R::MINE, BATCH = R::BATCH, PER = R::PER;
+                                             int value, int n_cta, int rank, uint4 *ring, bool &bad) {
+  using R = Ring<FMT>;
+  constexpr int LPR = R::LPR, U = R::U, CHUNK = R::CHUNK, MINE = R::MINE, BATCH = R::BATCH;
+  constexpr int PER = R::PER;
   Move *at = reinterpret_cast<Move *>(ring + kStages * U * NT);  // [2][BATCH], behind [kStages][U][NT]
   const int t = threadIdx.x;
   const auto &l = a.kv.layer[layer];
-  uint8_t *codes = (value ? l.v : l.k) + (part * LPR + t % LPR) * 16;
+  uint8_t *codes = (value ? l.v : l.k) + t % LPR * 16;
   uint8_t *scale = value ? l.v_scale : l.k_scale, *block = value ? l.v_bs : l.k_bs;
   const int head_row = h * a.kv.page_size, page_rows = a.kv.Hkv * a.kv.page_size;
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring) + t * 16;
-  const bool with_scales = FMT != kKvBf16 && part == 0;
+  // The barrier orders the loads of one CTA before the stores of another.  They are complete
+  // when their thread arrives, so that the cluster's barrier has nothing to release (to
+  // release is to wait for the thread's stores too: 0.6 us a chunk).
+  auto sync = [&] {
+    if (n_cta == 1) {
+      __syncthreads();
+    } else {
+      cluster_started();
+      cluster_wait();
+    }
+  };
+  // The sequence's row of place k of this thread in batch b: chunk c of this CTA is chunk
+  // c * n_cta + rank of the sequence.
+  auto row_of = [&](int b, int k) {
+    const int r = k * NT + t;
+    return ((b * PER + r / CHUNK) * n_cta + rank) * CHUNK + r % CHUNK;
+  };
 
   // The places of batch b, in three steps.
   auto positions = [&](int b, int (&src)[MINE]) {
 #pragma unroll
     for (int k = 0; k < MINE; ++k) {
-      const int j = b * BATCH + k * NT + t;
+      const int j = row_of(b, k);
       src[k] = j < x.n ? x.keep[j] : -1;
     }
   };
   auto page_ids = [&](int b, const int (&src)[MINE], Place (&r)[MINE]) {
 #pragma unroll
     for (int k = 0; k < MINE; ++k) {
-      const int j = b * BATCH + k * NT + t;
+      const int j = row_of(b, k);
       r[k] = j < x.n ? place_of(a, x, j, src[k], bad) : kNowhere;
     }
   };
   uint8_t sc[MINE];      // the scales of the batch that is in `at`,
   uint2 bs[MINE];
   int64_t sc_to[MINE];   // and the rows that they go to
+  __shared__ volatile uint32_t loaded[FMT == kKvBf16 ? 1 : NT];
   auto put = [&](int b, Place (&r)[MINE]) {
 #pragma unroll
     for (int k = 0; k < MINE; ++k) {
       check_place(a, r[k], bad);
       at[(b & 1) * BATCH + k * NT + t] = move_of<RowBytes<FMT>::value>(a, r[k], head_row);
       sc_to[k] = -1;
-      if (with_scales && r[k].from_page >= 0) {
+      if (FMT != kKvBf16 && r[k].from_page >= 0) {
         const int64_t row = (int64_t)r[k].from_page * page_rows + head_row + r[k].from_slot;
         sc[k] = scale[row];
         if (FMT == kKvNvfp4) bs[k] = *reinterpret_cast<const uint2 *>(block + row * 8);
@@ -389,9 +413,16 @@ __device__ __forceinline__ void compact_unit(const CompactArgs &a, const Unit &x
   __syncthreads();
 #pragma unroll
   for (int g = 0; g < kStages - 1; ++g) load(g);
-  for (int b = 0; b * BATCH < x.n; ++b) {
-    __syncthreads();  // the batch before is done, and every thread has this one's scales
-    if (with_scales) {
+  for (int b = 0; b * BATCH * n_cta < x.n; ++b) {
+    if (FMT != kKvBf16) {  // (writing them down waits for the loads of the scales)
+      uint32_t all = 0;
+#pragma unroll
+      for (int k = 0; k < MINE; ++k)
+        if (sc_to[k] >= 0) all ^= FMT == kKvNvfp4 ? sc[k] ^ bs[k].x ^ bs[k].y : sc[k];
+      loaded[t] = all;
+    }
+    sync();  // the batch before is done, and every thread has this one's scales
+    if (FMT != kKvBf16) {
 #pragma unroll
       for (int k = 0; k < MINE; ++k) {
         if (sc_to[k] < 0) continue;
@@ -403,10 +434,10 @@ __device__ __forceinline__ void compact_unit(const CompactArgs &a, const Unit &x
     page_ids(b + 2, src, ids);
     positions(b + 3, src);
     __syncthreads();
-    for (int g = b * PER; g < (b + 1) * PER && g * CHUNK < x.n; ++g) {
+    for (int g = b * PER; g < (b + 1) * PER && g * CHUNK * n_cta < x.n; ++g) {
       load(g + kStages - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      __syncthreads();  // every thread has chunk g
+      sync();  // every thread has chunk g
       const Move *chunk = at + g * CHUNK % (2 * BATCH) + t / LPR;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -420,52 +451,65 @@ __device__ __forceinline__ void compact_unit(const CompactArgs &a, const Unit &x
   __syncthreads();  // the unit is done with the places
 }
 
-template <int FMT, int LPR>
+template <int FMT>
 __global__ void __launch_bounds__(NT) compact_ring_kernel(const __grid_constant__ CompactArgs a) {
-  constexpr int PARTS = Ring<FMT, LPR>::PARTS;
   extern __shared__ __align__(16) uint4 ring[];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const unsigned first = blockIdx.x / n_cta, clusters = gridDim.x / n_cta;
   bool bad = false;
-  // The units with more than a.few rows among this CTA's, which lie gridDim.x apart; 32 of
-  // them are looked at at a time (by every warp).
-  const int64_t all = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * 2 * PARTS;
-  for (int64_t u0 = blockIdx.x; u0 < all; u0 += 32ll * gridDim.x) {
-    const int64_t u = u0 + (int64_t)(threadIdx.x & 31) * gridDim.x;
+  // The units with more than a.few rows among this cluster's, which lie `clusters` apart; 32
+  // of them are looked at at a time (by every warp).
+  const int64_t all = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * 2;
+  for (int64_t u0 = first; u0 < all; u0 += 32ll * clusters) {
+    const int64_t u = u0 + (int64_t)(threadIdx.x & 31) * clusters;
     bool is = false;
     if (u < all) {
-      unsigned i = (unsigned)(u / (2 * PARTS * a.kv.Hkv));
+      unsigned i = (unsigned)(u / (2 * a.kv.Hkv));
       const int s = take(i, (unsigned)a.n_seq), c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
       is = good_bounds(a, c0, c1) && c1 - c0 > a.few;
       bad |= !good_bounds(a, c0, c1);
     }
     for (unsigned many = __ballot_sync(0xffffffffu, is); many; many &= many - 1) {
-      const int64_t unit = u0 + (int64_t)(__ffs(many) - 1) * gridDim.x;
-      unsigned i = (unsigned)(unit / (2 * PARTS));
-      const int part = (int)(unit % PARTS), value = (int)(unit / PARTS & 1);
+      const int64_t unit = u0 + (int64_t)(__ffs(many) - 1) * clusters;
+      unsigned i = (unsigned)(unit >> 1);
       const int h = take(i, (unsigned)a.kv.Hkv), s = take(i, (unsigned)a.n_seq);
       const Unit x = unit_of(a, s, h, a.cu_keep[s], a.cu_keep[s + 1]);
-      compact_unit<FMT, LPR>(a, x, (int)i, h, value, part, ring, bad);
+      compact_unit<FMT>(a, x, (int)i, h, (int)(unit & 1), n_cta, rank, ring, bad);
     }
   }
   if (bad) atomicOr(a.err, kErrBadArg);
 }
 
-
-template <int FMT, int LPR>
+template <int FMT>
 cudaError_t compact_ring(const CompactArgs &a, cudaStream_t s) {
-  constexpr int smem = Ring<FMT, LPR>::BYTES;
-  const cudaError_t e = cudaFuncSetAttribute(compact_ring_kernel<FMT, LPR>,
+  constexpr int smem = Ring<FMT>::BYTES;
+  const cudaError_t e = cudaFuncSetAttribute(compact_ring_kernel<FMT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * 2 * Ring<FMT, LPR>::PARTS;
-  const int64_t grid = a.few > 0 ? min(units, (int64_t)152 * 2) : units;
-  if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
-  compact_ring_kernel<FMT, LPR><<<(unsigned)grid, NT, smem, s>>>(a);
-  return cudaGetLastError();
+  const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * 2;
+  // CTAs a cluster, until there are 128 of them: bf16, 8196 rows of 8 heads in one layer 70 us
+  // by one, 41, 22 and 17 by two, four and eight; in 8 layers 85, 97, 89 and 90.
+  int n_cta = 1;
+  while (n_cta < 8 && units * n_cta < 128) n_cta *= 2;
+  const int64_t clusters = a.few > 0 ? min(units, (int64_t)152 * 2 / n_cta) : units;
+  if (clusters * n_cta > 0x7fffffff) return cudaErrorNotYetImplemented;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(clusters * n_cta));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)n_cta;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, compact_ring_kernel<FMT>, a);
 }
 
 template <int FMT>
 cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
-  constexpr int VECS = RowBytes<FMT>::value / 16;
   const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv;
   if (a.out_table) {
     const int64_t grid = (int64_t)a.kv.n * a.kv.Hkv * ((a.total + NT - 1) / NT) + 1;
@@ -488,15 +532,7 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.total <= a.few) return e;
   }
-  // Columns, until there are 128 CTAs: bf16, 8196 rows of 8 heads in one layer 62 us uncut,
-  // 37 in halves, 24 in quarters; in 8 layers 85, 95 and 90.
-  int cut = 1;
-  while (cut < 4 && units * 2 * cut < 128) cut *= 2;
-  if constexpr (VECS >= 16)
-    if (cut == 4) return compact_ring<FMT, VECS / 4>(a, s);
-  if constexpr (VECS >= 8)
-    if (cut >= 2) return compact_ring<FMT, VECS / 2>(a, s);
-  return compact_ring<FMT, VECS>(a, s);
+  return compact_ring<FMT>(a, s);
 }
 
 }  // namespace
