@@ -173,7 +173,7 @@ struct CompactArgs {
   const int32_t *cu_keep, *keep;       // keep [total], or [Hkv][total]
   const int32_t *start;                // [n_seq] or null
   const int32_t *table, *out_table;    // out_table null: in place
-  int few;                             // in place: rows up to which a sequence is a warp's
+  int few, many;                       // in place: rows of the sequences of a launch
   unsigned *err;
 };
 

@@ -295,6 +295,55 @@ __global__ void __launch_bounds__(NT, 4) compact_warp_kernel(const __grid_consta
   if (bad) atomicOr(a.err, kErrBadArg);
 }
 
+// Calls f(unit) for the units whose sequence keeps more than a.few rows and at most a.many,
+// out of every `step`th from `first` on; 32 are looked at at a time, by every warp.
+// `per_seq`: units a sequence (and layer).
+template <typename F>
+__device__ __forceinline__ void for_units(const CompactArgs &a, unsigned per_seq, unsigned first,
+                                         unsigned step, bool &bad, F f) {
+  const int64_t all = (int64_t)a.kv.n * a.n_seq * per_seq;
+  for (int64_t u0 = first; u0 < all; u0 += 32ll * step) {
+    const int64_t u = u0 + (int64_t)(threadIdx.x & 31) * step;
+    bool is = false;
+    if (u < all) {
+      unsigned i = (unsigned)(u / per_seq);
+      const int s = take(i, (unsigned)a.n_seq), c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
+      is = good_bounds(a, c0, c1) && c1 - c0 > a.few && c1 - c0 <= a.many;
+      bad |= !good_bounds(a, c0, c1);
+    }
+    for (unsigned many = __ballot_sync(0xffffffffu, is); many; many &= many - 1)
+      f(u0 + (int64_t)(__ffs(many) - 1) * step);
+  }
+}
+
+// In place, many (layer, sequence, head) of medium length: a CTA each, 256 rows at a time,
+// keys and values.  Four CTAs an SM hide each other's way (bounds, positions, page ids, then
+// loads and stores in turn): 1024 of 512 rows, bf16, 55 us, 52 by rings; 4096 of up to 512
+// at the copy rate.
+template <int FMT>
+__global__ void __launch_bounds__(NT, 4) compact_cta_kernel(const __grid_constant__ CompactArgs a) {
+  __shared__ Move at[NT];
+  const int t = threadIdx.x;
+  bool bad = false;
+  for_units(a, (unsigned)a.kv.Hkv, blockIdx.x, gridDim.x, bad, [&](int64_t unit) {
+    unsigned i = (unsigned)unit;
+    const int h = take(i, (unsigned)a.kv.Hkv), s = take(i, (unsigned)a.n_seq);
+    const Unit x = unit_of(a, s, h, a.cu_keep[s], a.cu_keep[s + 1]);
+    const int head_row = h * a.kv.page_size;
+    for (int j0 = 0; j0 < x.n; j0 += NT) {
+      Place mine = kNowhere;
+      if (j0 + t < x.n) mine = place_of(a, x, j0 + t, x.keep[j0 + t], bad);
+      check_place(a, mine, bad);
+      __syncthreads();  // the rows before are done with the places
+      at[t] = move_of<RowBytes<FMT>::value>(a, mine, head_row);
+      __syncthreads();
+      move_rows<FMT, NT, 4>(a, (int)i, head_row, at, mine, t, min(NT, x.n - j0),
+                            [] { __syncthreads(); });
+    }
+  });
+  if (bad) atomicOr(a.err, kErrBadArg);
+}
+
 // In place, sequences that keep many rows: they have to go in order, so what bounds a
 // (layer, sequence, head) is how much it has under way, and at what rate an SM loads and
 // stores rows.  A CTA takes keys or values; where there are few of these, the CTAs of a
@@ -456,33 +505,18 @@ __global__ void __launch_bounds__(NT) compact_ring_kernel(const __grid_constant_
   extern __shared__ __align__(16) uint4 ring[];
   const cg::cluster_group cluster = cg::this_cluster();
   const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const unsigned first = blockIdx.x / n_cta, clusters = gridDim.x / n_cta;
   bool bad = false;
-  // The units with more than a.few rows among this cluster's, which lie `clusters` apart; 32
-  // of them are looked at at a time (by every warp).
-  const int64_t all = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * 2;
-  for (int64_t u0 = first; u0 < all; u0 += 32ll * clusters) {
-    const int64_t u = u0 + (int64_t)(threadIdx.x & 31) * clusters;
-    bool is = false;
-    if (u < all) {
-      unsigned i = (unsigned)(u / (2 * a.kv.Hkv));
-      const int s = take(i, (unsigned)a.n_seq), c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
-      is = good_bounds(a, c0, c1) && c1 - c0 > a.few;
-      bad |= !good_bounds(a, c0, c1);
-    }
-    for (unsigned many = __ballot_sync(0xffffffffu, is); many; many &= many - 1) {
-      const int64_t unit = u0 + (int64_t)(__ffs(many) - 1) * clusters;
-      unsigned i = (unsigned)(unit >> 1);
-      const int h = take(i, (unsigned)a.kv.Hkv), s = take(i, (unsigned)a.n_seq);
-      const Unit x = unit_of(a, s, h, a.cu_keep[s], a.cu_keep[s + 1]);
-      compact_unit<FMT>(a, x, (int)i, h, (int)(unit & 1), n_cta, rank, ring, bad);
-    }
-  }
+  for_units(a, 2u * a.kv.Hkv, blockIdx.x / n_cta, gridDim.x / n_cta, bad, [&](int64_t unit) {
+    unsigned i = (unsigned)(unit >> 1);
+    const int h = take(i, (unsigned)a.kv.Hkv), s = take(i, (unsigned)a.n_seq);
+    const Unit x = unit_of(a, s, h, a.cu_keep[s], a.cu_keep[s + 1]);
+    compact_unit<FMT>(a, x, (int)i, h, (int)(unit & 1), n_cta, rank, ring, bad);
+  });
   if (bad) atomicOr(a.err, kErrBadArg);
 }
 
 template <int FMT>
-cudaError_t compact_ring(const CompactArgs &a, cudaStream_t s) {
+cudaError_t compact_ring(const CompactArgs &a, int64_t at_once, cudaStream_t s) {
   constexpr int smem = Ring<FMT>::BYTES;
   const cudaError_t e = cudaFuncSetAttribute(compact_ring_kernel<FMT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -491,7 +525,7 @@ cudaError_t compact_ring(const CompactArgs &a, cudaStream_t s) {
   // CTAs a cluster, until there are 128 of them: bf16, 8196 rows of 8 heads in one layer 70 us
   // by one, 41, 22 and 17 by two, four and eight; in 8 layers 85, 97, 89 and 90.
   int n_cta = 1;
-  while (n_cta < 8 && units * n_cta < 128) n_cta *= 2;
+  while (n_cta < 8 && 2 * at_once * n_cta < 128) n_cta *= 2;
   const int64_t clusters = a.few > 0 ? min(units, (int64_t)152 * 2 / n_cta) : units;
   if (clusters * n_cta > 0x7fffffff) return cudaErrorNotYetImplemented;
   cudaLaunchConfig_t cfg{};
@@ -517,14 +551,11 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
     compact_out_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
     return cudaGetLastError();
   }
-  // Short sequences go to warps, longer ones, if there can be any, to CTAs behind them, or
-  // all to CTAs where most are long.  Warps are as quick as CTAs up to about 20 KB of a
-  // (layer, sequence, head) where there are 256 of these, 70 KB where there are 1024, 130 KB
-  // where there are 4096 (bf16, sequences of up to 128 rows: 14.4 us by warps and 7.4 by
-  // CTAs; 18.9 and 22.0; 57 and 83), less where lengths differ.
-  constexpr int row = 2 * RowBytes<FMT>::value;
-  a.few = (int)(min(48 * units, (int64_t)98304) / row);
-  if (a.total / a.n_seq > a.few) a.few = 0;
+  // Many (layer, sequence, head) of few rows go to warps, where that is all there is to do
+  // (1024 of them, 8 rows of bf16: 3.4 us by warps, 5.4 by CTAs) or saves more than the
+  // launch for others (4096, up to 8 rows: 7.2 us with it, 14.5 by CTAs; up to 32: 18 and 17).
+  const int mean = a.total / a.n_seq, few = 12288 / (2 * RowBytes<FMT>::value);
+  a.few = units >= 608 && (a.total <= few || (units >= 2048 && mean <= few / 2)) ? few : 0;
   if (a.few > 0) {
     const int64_t grid = (units + NT / 32 - 1) / (NT / 32);
     if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
@@ -532,7 +563,24 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.total <= a.few) return e;
   }
-  return compact_ring<FMT>(a, s);
+  // Fewer of them than SMs and long: through rings (bf16: 32 of 1500 rows 11 us by rings, 21
+  // by CTAs; 128 of 1500 22 and 30, of 256 7.0 and 6.3; 320 of 1500 51 and 52).
+  a.many = 0x7fffffff;
+  if (units < 160 && mean > 256) return compact_ring<FMT>(a, units, s);
+  // Lone long sequences among many short ones, in few layers, are too few CTAs: they go
+  // through rings behind the others (8200 rows of 8 heads in one layer among 60 sequences: 20
+  // us, 111 without; in vain 2 to 3 us).
+  const int64_t lone = (int64_t)a.kv.n * a.kv.Hkv;
+  const bool rings = lone <= 64 && a.total > 4096;
+  if (rings) a.many = max(1024, a.total / 4);
+  const int64_t grid = a.few > 0 ? min(units, (int64_t)152 * 4) : units;
+  if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
+  compact_cta_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !rings) return e;
+  a.few = a.many;
+  a.many = 0x7fffffff;
+  return compact_ring<FMT>(a, lone, s);
 }
 
 }  // namespace

@@ -344,6 +344,30 @@ def test_compact_one_long_sequence_among_many(fmt, in_place):
                  for p in before])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "nvfp4"])
+@pytest.mark.parametrize("n_layers,n,longest", [(40, 16, 0), (64, 40, 0), (64, 40, 190), (5, 140, 60)])
+def test_compact_paths_of_trees(fmt, n_layers, n, longest):
+    """Many short moves behind the cached rows in many layers, in place; one may be long."""
+    r, ps = random.Random(n), 16
+    L = [r.randint(20, 60) for _ in range(n)]
+    count = [r.choice((0, 1)) for _ in range(n)]
+    if longest:
+        L[7], count[7] = 2 * longest, longest
+    per = [plain.up(x, ps) for x in L]
+    ids, width = r.sample(range(sum(per)), sum(per)), max(per)
+    table = [[ids.pop() for _ in range(p)] + [-1] * (width - p) for p in per]
+    # Positions ascend from the start on, so that a kept one is at least its new one.
+    start = [max(0, x - 2 * c - 1) for x, c in zip(L, count)]
+    keep = [k for x, c, st in zip(L, count, start) for k in sorted(r.sample(range(st, x), c))]
+    cu = np.concatenate(([0], np.cumsum(count))).tolist()
+    kv, parts = pools(fmt, n_layers, sum(per), 1, ps, 6)
+    before = host(parts)
+    bs.attn_skip_kv_compact(kv, i32(keep), i32(cu), i32(table), start=i32(start))
+    no_error()
+    same(parts, [{m: plain.compact(x, keep, cu, table, ps, start) for m, x in p.items()}
+                 for p in before])
+
+
 def test_compact_leaves_rows_outside_the_sequences_alone_and_reports():
     kv, parts = pool("e4m3", 6, 2, 16, 9)
     before = host([parts])
