@@ -128,7 +128,7 @@ __device__ __forceinline__ int take(unsigned &i, unsigned n) {
   return (int)r;
 }
 
-// Where row j, of position src, comes from and goes to (from_page -1: nothing to move);
+// Where row j, of position src, comes from and goes to (kNowhere: nothing to move);
 // the page ids are as they come from the tables.
 __device__ __forceinline__ Place place_of(const CompactArgs &a, const Unit &x, int j, int src,
                                           bool &bad) {
@@ -385,9 +385,10 @@ __device__ __forceinline__ void compact_unit(const CompactArgs &a, const Unit &x
   uint8_t *scale = value ? l.v_scale : l.k_scale, *block = value ? l.v_bs : l.k_bs;
   const int head_row = h * a.kv.page_size, page_rows = a.kv.Hkv * a.kv.page_size;
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring) + t * 16;
-  // The barrier orders the loads of one CTA before the stores of another.  They are complete
-  // when their thread arrives, so that the cluster's barrier has nothing to release (to
-  // release is to wait for the thread's stores too: 0.6 us a chunk).
+  // The barrier orders the loads of one CTA before the stores of another.  The loads are
+  // complete when their thread arrives (copies have been waited for, scales written down),
+  // and the wait keeps the stores behind it, so that the cluster's barrier has nothing to
+  // release: that would wait for the thread's earlier stores too, 0.6 us a chunk.
   auto sync = [&] {
     if (n_cta == 1) {
       __syncthreads();

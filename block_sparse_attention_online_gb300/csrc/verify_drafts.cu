@@ -17,16 +17,17 @@
 // the exponent take fifty and bound the large calls (256 sequences, 128000 tokens: 193 us,
 // 84 without them).
 //
-// One cluster a sequence: every warp finds the row, sums its stretch of it, and sends the
-// sum round; the CTA whose stretches hold the threshold narrows them down to the token.
+// One cluster a sequence: every warp finds the row, sums its stretch of it, 256 tokens at a
+// time, and sends the sum round; the CTA whose stretches hold the threshold goes on from
+// the sums of a stretch's pieces, which its warps have kept, to the token.
 //
 // What bounds it: a small call its way through six dependent steps (bounds, drafted
 // tokens, their probabilities, the row, the sums of all, the search: one sequence, 32000
-// tokens, 5.5 us); a large one DRAM (256 sequences, 128000 tokens, up to 5 drafts: 47 us for
-// 190 MB, 60 % of the copy rate; without the search it takes 42, and what is left goes to
-// the steps before a CTA's stream, with two or three CTAs an SM to cover them).  Not kept:
-// loads one round ahead in registers (57 us), the search from 256 tokens on by one warp
-// (spills; 51), acceptance in a kernel of its own (51).
+// tokens, 5.3 us); a large one the loads under way, then DRAM (256 sequences, 128000 tokens,
+// up to 5 drafts, 190 MB: 45 us; 600 with 4 drafts, 614 MB: 98, 94 % of the copy rate).  Six
+// CTAs of 256 threads an SM hide one another's steps better than three of 512 (48 us) or
+// four of 384 (46).  Not kept: loads one round ahead in registers (57 us), acceptance in a
+// kernel of its own (no gain), a search that sums the stretch again (5 us more).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -41,7 +42,7 @@ namespace {
 namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
-constexpr int NT = 512;
+constexpr int NT = 256;
 constexpr int NW = NT / 32;
 constexpr int kMaxCluster = 8;
 
@@ -104,81 +105,90 @@ __device__ __forceinline__ u64 scan_warp(u64 x, int lane) {
   return x;
 }
 
-// Sum of the weights of tokens [i0, i1), for the whole warp.
+constexpr int kSpan = 256;    // tokens a warp sums at a time
+constexpr int kPieces = 64;   // sums of its stretch that a warp keeps
+
+// Sum of the weights of tokens [i, min(i + kSpan, i1)), in every lane of the warp.
 template <bool BF16, bool HAS_Q>
-__device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int lane, bool &bad) {
-    constexpr int U = 8;        // tokens a lane loads at a time
-  constexpr int FLUSH = 256;  // tokens a lane sums in 32 bits (2^22 steps each at most)
+__device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int lane, bool &bad) {
+  constexpr int U = kSpan / 32;
   auto two = [](float x, float y) {
     return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
   };
   const uint64_t m1 = two(kM1, kM1), m2 = two(kM2, kM2), m3 = two(kM3, kM3), neg = two(-1.f, -1.f);
-  u64 sum = 0;
+  uint32_t x[U], y[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int t = i + u * 32 + lane;
+    x[u] = t < i1 ? load_bits<BF16>(r.p, t) : 0u;
+    y[u] = HAS_Q && t < i1 ? load_bits<BF16>(r.q, t) : 0u;
+  }
+  auto steps = [&](uint32_t lo, uint32_t hi, uint32_t (&a)[3], uint32_t (&b)[3]) {
+    const uint64_t v = (uint64_t)lo | (uint64_t)hi << 32;
+    const uint64_t t1 = tc::f2_add(v, m1);
+    const uint64_t r1 = tc::f2_add(v, tc::f2_fma(t1, neg, m1));
+    const uint64_t t2 = tc::f2_add(r1, m2);
+    const uint64_t r2 = tc::f2_add(r1, tc::f2_fma(t2, neg, m2));
+    const uint64_t t3 = tc::f2_add(r2, m3);
+    a[0] = (uint32_t)t1; b[0] = (uint32_t)(t1 >> 32);
+    a[1] = (uint32_t)t2; b[1] = (uint32_t)(t2 >> 32);
+    a[2] = (uint32_t)t3; b[2] = (uint32_t)(t3 >> 32);
+  };
+  // Modulo 2^32, as signed numbers: a value has at most 2^22 steps, a span 2^30.
+  uint32_t s1 = 0, s2 = 0, s3 = 0, a[3], b[3];
   uint32_t most = 0;  // the largest bits of all values
-  for (int i = i0; i < i1;) {
-    uint32_t s1 = 0, s2 = 0, s3 = 0;  // (modulo 2^32, as signed numbers)
-    const int end = min(i1, i + FLUSH * 32);
-    for (; i < end; i += U * 32) {
-      uint32_t x[U], y[U];
+  if constexpr (HAS_Q) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = i + u * 32 + lane;
-        x[u] = t < i1 ? load_bits<BF16>(r.p, t) : 0u;
-        y[u] = HAS_Q && t < i1 ? load_bits<BF16>(r.q, t) : 0u;
-      }
-      auto steps = [&](uint32_t lo, uint32_t hi, uint32_t (&a)[3], uint32_t (&b)[3]) {
-        const uint64_t v = (uint64_t)lo | (uint64_t)hi << 32;
-        const uint64_t t1 = tc::f2_add(v, m1);
-        const uint64_t r1 = tc::f2_add(v, tc::f2_fma(t1, neg, m1));
-        const uint64_t t2 = tc::f2_add(r1, m2);
-        const uint64_t r2 = tc::f2_add(r1, tc::f2_fma(t2, neg, m2));
-        const uint64_t t3 = tc::f2_add(r2, m3);
-        a[0] = (uint32_t)t1; b[0] = (uint32_t)(t1 >> 32);
-        a[1] = (uint32_t)t2; b[1] = (uint32_t)(t2 >> 32);
-        a[2] = (uint32_t)t3; b[2] = (uint32_t)(t3 >> 32);
-      };
-      uint32_t a[3], b[3];
-      if constexpr (HAS_Q) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          most = max(most, max(x[u], y[u]));
-          steps(x[u], y[u], a, b);
-          if (x[u] > y[u]) {  // (valid values: their bits compare as they do)
-            s1 += a[0] - b[0];
-            s2 += a[1] - b[1];
-            s3 += a[2] - b[2];
-          }
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < U; u += 2) {
-          most = max(most, max(x[u], x[u + 1]));
-          steps(x[u], x[u + 1], a, b);
-          s1 += a[0] + b[0] - 2 * __float_as_uint(kM1);
-          s2 += a[1] + b[1] - 2 * __float_as_uint(kM2);
-          s3 += a[2] + b[2] - 2 * __float_as_uint(kM3);
-        }
+    for (int u = 0; u < U; ++u) {
+      most = max(most, max(x[u], y[u]));
+      steps(x[u], y[u], a, b);
+      if (x[u] > y[u]) {  // (valid values: their bits compare as they do)
+        s1 += a[0] - b[0];
+        s2 += a[1] - b[1];
+        s3 += a[2] - b[2];
       }
     }
-    sum += join(s1, s2, s3);
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; u += 2) {
+      most = max(most, max(x[u], x[u + 1]));
+      steps(x[u], x[u + 1], a, b);
+      s1 += a[0] + b[0] - 2 * __float_as_uint(kM1);
+      s2 += a[1] + b[1] - 2 * __float_as_uint(kM2);
+      s3 += a[2] + b[2] - 2 * __float_as_uint(kM3);
+    }
   }
   if (__any_sync(0xffffffffu, most >= kValid)) {  // values to leave out: one by one
-    sum = 0;
-    Row all = r;
-    all.hole = -1;
-    for (int i = i0 + lane; i < i1; i += 32) sum += weight<BF16>(all, i, bad);
+    u64 w = 0;
+    for (int t = i + lane; t < min(i + kSpan, i1); t += 32) w += weight<BF16>(r, t, bad);
+    return sum_warp(w);
   }
-  sum = sum_warp(sum);
-  if (r.hole >= i0 && r.hole < i1) {
-    bool noted = false;
-    sum -= units(load_bits<BF16>(r.p, r.hole), noted);
+  const u64 sum = join(__reduce_add_sync(0xffffffffu, s1), __reduce_add_sync(0xffffffffu, s2),
+                       __reduce_add_sync(0xffffffffu, s3));
+  if (r.hole < i || r.hole >= min(i + kSpan, i1)) return sum;
+  bool noted = false;
+  return sum - units(load_bits<BF16>(r.p, r.hole), noted);
+}
+
+// Sum of the weights of tokens [i0, i1), in every lane, and of each `piece` of them.
+template <bool BF16, bool HAS_Q>
+__device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int piece, u64 *pieces,
+                                           int lane, bool &bad) {
+  u64 sum = 0;
+  for (int i = i0, k = 0; i < i1; ++k) {
+    u64 part = 0;
+    for (const int end = min(i1, i + piece); i < end; i += kSpan)
+      part += sum_span<BF16, HAS_Q>(r, i, i1, lane, bad);
+    if (lane == 0) pieces[k] = part;
+    sum += part;
   }
   return sum;
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(NT, 3) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(NT, 6) verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ u64 sums[2][kMaxCluster * NW];  // of every warp of the cluster
+  __shared__ u64 pieces[NW][kPieces];        // of this CTA's stretches
   const cg::cluster_group cluster = cg::this_cluster();
   cluster_started();
   const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -243,11 +253,12 @@ __global__ void __launch_bounds__(NT, 3) verify_kernel(const __grid_constant__ V
   const int all = n_cta * NW, mine = rank * NW + warp;
   const int len = ((a.V + all - 1) / all + 31) & ~31;
   const int i0 = (int)min((int64_t)mine * len, (int64_t)a.V), i1 = min(i0 + len, a.V);
+  const int piece = (len + kPieces * kSpan - 1) / (kPieces * kSpan) * kSpan;
   u64 total = 0, below = 0;  // sums of all warps, and of those of the CTAs before this one
   int round = 0;
   while (true) {  // a second time only where p - q is 0 throughout
-    const u64 stretch = row.q ? sum_stretch<BF16, true>(row, i0, i1, lane, bad)
-                              : sum_stretch<BF16, false>(row, i0, i1, lane, bad);
+    const u64 stretch = row.q ? sum_stretch<BF16, true>(row, i0, i1, piece, pieces[warp], lane, bad)
+                              : sum_stretch<BF16, false>(row, i0, i1, piece, pieces[warp], lane, bad);
     if (lane < n_cta) *cluster.map_shared_rank(&sums[round][mine], lane) = stretch;
     cluster.sync();
     u64 before = 0, every = 0;
@@ -276,38 +287,51 @@ __global__ void __launch_bounds__(NT, 3) verify_kernel(const __grid_constant__ V
     a.n_accepted[s] = acc;
     if (!total) out[acc] = a.V - 1;
   }
-  // The CTA whose stretches hold the threshold narrows them down: to one warp's, to a
-  // warp's part of that one, and so on to 32 tokens.
-  const u64 *part = &sums[round][rank * NW];
-  int lo = rank * NW * len, step = len;
-  while (true) {
-    const u64 v = lane < NW ? part[lane] : 0, upto = below + scan_warp(v, lane);
-    const unsigned here = __ballot_sync(0xffffffffu, threshold < upto && threshold >= upto - v);
-    if (!here) return;  // (the same for the whole CTA)
-    const int w = __ffs(here) - 1;
-    lo += w * step;
-    below = __shfl_sync(0xffffffffu, upto - v, w);
-    if (step == 32) break;
-    const int end = min(lo + step, a.V);
-    step = ((step + NW - 1) / NW + 31) & ~31;
+  // The CTA whose stretches hold the threshold looks up the warp's, then the piece of it;
+  // parts of that, where it is long, are summed again, until a token a thread is left.
+  // `find`: which of n sums holds it; below becomes the sum before.
+  auto find = [&](const u64 *part, int n) {
+    for (int k = 0; k < n; k += 32) {
+      const u64 v = k + lane < n ? part[k + lane] : 0, upto = below + scan_warp(v, lane);
+      const unsigned here = __ballot_sync(0xffffffffu, threshold < upto && threshold >= upto - v);
+      if (here) {
+        below = __shfl_sync(0xffffffffu, upto - v, __ffs(here) - 1);
+        return k + __ffs(here) - 1;
+      }
+      below = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return -1;
+  };
+  // (The same for the whole CTA.  Rows that sum to 16 and more may be found nowhere.)
+  const int holder = find(&sums[round][rank * NW], NW);
+  if (holder < 0) return;
+  const int first = (rank * NW + holder) * len;
+  const int k = find(pieces[holder], (min(len, a.V - first) + piece - 1) / piece);
+  if (k < 0) return;
+  int lo = first + k * piece, end = min(min(lo + piece, first + len), a.V);
+  bool noted = false;
+  while (end - lo > NT) {
+    const int step = ((end - lo + NW - 1) / NW + 31) & ~31;
     u64 sum = 0;
-    const int first = lo + warp * step, last = min(first + step, end);
-    bool noted = false;
+    const int last = min(lo + (warp + 1) * step, end);
 #pragma unroll 4
-    for (int i = first + lane; i < last; i += 32) sum += weight<BF16>(row, i, noted);
+    for (int i = lo + warp * step + lane; i < last; i += 32) sum += weight<BF16>(row, i, noted);
     sum = sum_warp(sum);
     __syncthreads();  // the sums before are no longer needed
     if (lane == 0) sums[0][warp] = sum;
     __syncthreads();
-    part = sums[0];
+    const int part = find(sums[0], NW);
+    if (part < 0) return;
+    lo += part * step;
+    end = min(lo + step, end);
   }
-  if (warp == 0) {
-    const int i = lo + lane;
-    bool noted = false;
-    const u64 w = i < a.V ? weight<BF16>(row, i, noted) : 0;
-    const u64 upto = below + scan_warp(w, lane);
-    if (threshold < upto && threshold >= upto - w) out[acc] = i;
-  }
+  const u64 w = lo + tid < end ? weight<BF16>(row, lo + tid, noted) : 0, mine_sum = sum_warp(w);
+  __syncthreads();
+  if (lane == 0) sums[0][warp] = mine_sum;
+  __syncthreads();
+  if (find(sums[0], NW) != warp) return;
+  const u64 upto = below + scan_warp(w, lane);
+  if (threshold < upto && threshold >= upto - w) out[acc] = lo + tid;
 }
 
 template <bool BF16>
@@ -328,14 +352,16 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
-  // CTAs a sequence: more while they all fit one an SM and every warp has 256 tokens (128000
-  // tokens of one sequence: 26.6 us by one CTA, 8.1 by eight; 8000 of 100: 6.8 by one, 15.1
-  // by eight), and while one would have more than 32768 tokens, so that many sequences end
-  // about together (128000 of 300: 67 by one, 59 by four; 32000 of 300: 17 by one, 25 by four).
+  // CTAs a sequence: more while every warp has more than 256 tokens and all fit about three an
+  // SM (128000 tokens of one sequence: 38.8 us by one CTA, 9.0 by eight; 8000 of 300: 8.2 by
+  // one, 18.7 by eight), or four an SM where each still has 16000 tokens (128000 of 150: 39 by
+  // two, 30 by four, 33 by eight; 32000 of 300: 20 by one, 17 by two, 23 by eight).
   int n_cta = 1;
-  while (n_cta < kMaxCluster && (((int64_t)n_cta * 2 * a.n_seq <= 152 && a.V > n_cta * NW * 256) ||
-                                 a.V / n_cta > 32768))
+  while (n_cta < kMaxCluster && a.V > n_cta * NW * 256) {
+    const int64_t ctas = (int64_t)n_cta * 2 * a.n_seq;
+    if (ctas > 400 && (ctas > 608 || a.V < 32000 * n_cta)) break;
     n_cta *= 2;
+  }
   return a.bf16 ? launch<true>(a, n_cta, s) : launch<false>(a, n_cta, s);
 }
 

@@ -78,6 +78,25 @@ def test_tokens(V, n, pad, probs, dtype):
     no_error()
 
 
+@pytest.mark.parametrize("V,dtype", [(1300003, torch.float32), (9000001, torch.bfloat16)])
+def test_vocabularies_of_millions(V, dtype):
+    for seed, probs in ((1, True), (2, False)):
+        check(inputs(seed, [1, 0], V, dtype, probs, sharp=1.0))
+    no_error()
+
+
+def test_rows_that_sum_to_too_much_harm_nothing():
+    """(Their token means nothing.)"""
+    for V in (40, 3000, 100000):
+        a = inputs(1, [1, 0, 0], V, probs=False)
+        good = want(a)
+        a["target"][2] = 1.9
+        tokens, n = call(a)
+        assert n.tolist() == good[1].tolist()
+        assert np.array_equal(tokens[[0, 2]].cpu().numpy(), good[0][[0, 2]])
+    no_error()
+
+
 def test_many_drafts_and_many_sequences():
     check(inputs(1, [600, 3], 50, noise=0.0))      # more drafts than threads of a CTA
     check(inputs(2, [1] * 700 + [0] * 300, 1000))
