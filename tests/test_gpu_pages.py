@@ -438,6 +438,62 @@ def test_calls_on_another_stream_and_in_a_graph():
     no_error()
 
 
+@pytest.mark.parametrize("n,max_kv", [(1, 3000), (40, 60)])  # rings and a cluster; a CTA each
+def test_compact_on_another_stream_and_in_a_graph(n, max_kv):
+    n_pages, table, _, keep, cu, start = rows(8, n, 16, max_kv, True)
+    kv, parts = pools("e4m3", 2, n_pages, 2, 16, 4)
+    before = host(parts)
+    saved = [{m: x.clone() for m, x in p.items()} for p in parts]
+    args = i32(keep), i32(cu), i32(table)
+    st = i32(start)
+    want = [{m: plain.compact(x, keep, cu, table, 16, start) for m, x in p.items()} for p in before]
+
+    def back():
+        for p, b in zip(parts, saved):
+            for m, x in p.items():
+                x.copy_(b[m])
+        torch.cuda.synchronize()
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    bs.attn_skip_kv_compact(kv, *args, start=st, stream=side)
+    side.synchronize()
+    same(parts, want)
+    back()
+    # The table given twice is in place too.
+    bs.attn_skip_kv_compact(kv, *args, start=st, out_table=args[2])
+    same(parts, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bs.attn_skip_kv_compact(kv, *args, start=st)
+    for _ in range(2):
+        back()
+        graph.replay()
+        torch.cuda.synchronize()
+        same(parts, want)
+    no_error()
+
+
+def test_fork_and_reserve_on_another_stream():
+    refs, table, old, new = batch(7, 20, 16, 200, 700, 0.3, 40)
+    parent = [19 - d for d in range(20)]
+    cut = [old[p] // 2 for p in parent]
+    want = plain.fork(refs, table, old, cut, 16, parent, [[-1] * len(table[0])] * 20)
+    R, T = i32(refs), i32(table)
+    side = torch.cuda.Stream()
+    a, b, p = i32(old), i32(cut), i32(parent)
+    torch.cuda.synchronize()
+    out = bs.attn_skip_pages_fork(R, T, a, b, 16, parent=p, stream=side)
+    grown = i32([c + 5 for c in cut])
+    torch.cuda.synchronize()
+    got = bs.attn_skip_pages_reserve(R, out, b, grown, 16, stream=side)
+    side.synchronize()
+    want = plain.reserve(want[0], want[1], cut, [c + 5 for c in cut], 16)
+    assert R.tolist() == want[0] and out.tolist() == want[1]
+    assert [x.tolist() for x in got] == list(want[2:5])
+    no_error()
+
+
 # ------------------------------------------------------------------ large pools --
 def test_offsets_beyond_32_bits():
     """k and v of 5 GB each: pages whose first byte lies behind 2^32."""

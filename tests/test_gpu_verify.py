@@ -210,6 +210,19 @@ def test_bad_bounds_and_rows_behind_the_last_sequence():
     assert np.array_equal(tokens.cpu().numpy(), t) and np.array_equal(acc.cpu().numpy(), n)
 
 
+def test_max_draft_is_a_bound():
+    a = inputs(14, [3, 0, 1], 5000)
+    t, n = want(dict(a, max_draft=9))
+    assert t.shape == (3, 10)
+    tokens, accepted = call(dict(a, max_draft=9))
+    assert np.array_equal(tokens.cpu().numpy(), t) and np.array_equal(accepted.cpu().numpy(), n)
+    no_error()
+    tokens, accepted = call(dict(a, max_draft=2))  # one sequence has more
+    reported()
+    assert accepted.tolist() == [-1] + n[1:].tolist() and (tokens[0] == -1).all()
+    assert np.array_equal(tokens[1:].cpu().numpy(), t[1:, :3])
+
+
 def test_refusals():
     a = inputs(1, [2, 1], 60)
     for bad in (dict(target=a["target"].double()), dict(target=a["target"][:4]),
