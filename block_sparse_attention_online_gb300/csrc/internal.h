@@ -163,7 +163,6 @@ struct CopyPagesArgs {
   KvLayers kv;
   int n_pairs;
   const int32_t *src, *dst;
-  int chunks;                          // pieces of a page's k (and v)
   unsigned *err;
 };
 
@@ -204,7 +203,7 @@ struct VerifyArgs {
   unsigned *err;
 };
 
-cudaError_t launch_kv_copy_pages(CopyPagesArgs a, cudaStream_t s);
+cudaError_t launch_kv_copy_pages(const CopyPagesArgs &a, cudaStream_t s);
 cudaError_t launch_kv_compact(CompactArgs a, cudaStream_t s);
 size_t pages_reserve_max_seqs();
 size_t pages_reserve_max_pages();

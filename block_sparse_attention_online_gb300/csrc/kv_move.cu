@@ -14,62 +14,171 @@ namespace cg = cooperative_groups;
 constexpr int NT = 256;
 
 // ---------------------------------------------------------------- whole pages --
-constexpr int kVec = 4;                    // 16-byte vectors a thread
-constexpr int kPiece = NT * kVec * 16;     // bytes a CTA
+// A page of one layer has six parts: k, v, their scales and block scales, each of whole
+// 16-byte vectors (a page has at least 16 rows).
+//
+// Large pages go in pieces of 1024 vectors.  The parts of small ones go together, by a warp
+// or a CTA; there CTAs stay and share out what there is to copy: first the entries that stand
+// for a copy are listed.  DRAM bounds both.
+constexpr int kVec = 4;            // vectors a thread has under way
+constexpr int kPiece = NT * kVec;  // vectors of a piece
+constexpr int kPairs = 512;        // entries looked at at a time
 
-// One CTA: a piece of one page's k or v in one layer, or all its scales.  DRAM bounds it:
-// 96 pages of 64 bf16 rows and 8 heads in 32 layers, 1.6 GB, 231 us (6.9 TB/s); entries
-// without a page cost a CTA that looks at them (32 of these 128).
-__global__ void __launch_bounds__(NT) copy_pages_kernel(const __grid_constant__ CopyPagesArgs a) {
-  const unsigned per_page = 2u * a.chunks + (a.kv.format != kKvBf16);
-  const unsigned unit = blockIdx.x / per_page;
-  unsigned c = blockIdx.x - unit * per_page;
-  const unsigned layer = unit / (unsigned)a.n_pairs, i = unit - layer * (unsigned)a.n_pairs;
-  const int src = a.src[i], dst = a.dst[i];
+struct Parts {
+  int codes, scales, blocks, all;  // vectors of k (and v), of their scales, of all parts
+};
+
+__host__ __device__ __forceinline__ Parts parts_of(const KvLayers &kv) {
+  const int rows = kv.Hkv * kv.page_size;
+  Parts x;
+  x.codes = rows * (kv.format == kKvBf16 ? 16 : kv.format == kKvE4m3 ? 8 : 4);
+  x.scales = kv.format == kKvBf16 ? 0 : rows / 16;
+  x.blocks = kv.format == kKvNvfp4 ? rows / 2 : 0;
+  x.all = 2 * (x.codes + x.scales + x.blocks);
+  return x;
+}
+
+// Vectors [from, to) of one layer's page src, all parts in a row, to page dst; `t` of GROUP
+// threads.
+template <int GROUP>
+__device__ __forceinline__ void copy_vectors(const KvLayers &kv, const Parts &x, int layer, int2 pair,
+                                             int from, int to, int t) {
+  const auto &l = kv.layer[layer];
+  const int64_t src = pair.x, dst = pair.y;
+  for (int i0 = from + t; i0 < to; i0 += kVec * GROUP) {
+    uint4 v[kVec];
+    uint8_t *out[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      int i = i0 + k * GROUP;
+      if (i >= to) break;
+      uint8_t *base;
+      int64_t stride;
+      if (i < 2 * x.codes) {
+        base = i < x.codes ? l.k : l.v;
+        i -= i < x.codes ? 0 : x.codes;
+        stride = kv.page_stride;
+      } else if (i < 2 * (x.codes + x.scales)) {
+        i -= 2 * x.codes;
+        base = i < x.scales ? l.k_scale : l.v_scale;
+        i -= i < x.scales ? 0 : x.scales;
+        stride = x.scales * 16ll;
+      } else {
+        i -= 2 * (x.codes + x.scales);
+        base = i < x.blocks ? l.k_bs : l.v_bs;
+        i -= i < x.blocks ? 0 : x.blocks;
+        stride = x.blocks * 16ll;
+      }
+      base += (int64_t)i * 16;
+      out[k] = base + dst * stride;
+      v[k] = *reinterpret_cast<const uint4 *>(base + src * stride);
+    }
+#pragma unroll
+    for (int k = 0; k < kVec; ++k)
+      if (i0 + k * GROUP < to) *reinterpret_cast<uint4 *>(out[k]) = v[k];
+  }
+}
+
+// Lists the entries [i0, i0 + kPairs) that stand for a copy, in their order (it is the same
+// in every CTA); returns how many.
+__device__ __forceinline__ int list_pairs(const CopyPagesArgs &a, int i0, int2 *pairs, int *counts,
+                                          bool &bad) {
+  constexpr int ROUNDS = kPairs / NT, WARPS = NT / 32;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  int2 mine[ROUNDS];
+  unsigned is[ROUNDS];
+#pragma unroll
+  for (int k = 0; k < ROUNDS; ++k) {
+    const int i = i0 + k * NT + t;
+    mine[k].x = i < a.n_pairs ? a.src[i] : -1;
+    mine[k].y = i < a.n_pairs ? a.dst[i] : -1;
+  }
+  __syncthreads();  // the entries before are done with
+#pragma unroll
+  for (int k = 0; k < ROUNDS; ++k) {
+    const int2 p = mine[k];
+    const bool fine = p.x >= -1 && p.y >= -1 && p.x < a.kv.n_pages && p.y < a.kv.n_pages;
+    bad |= !fine;
+    is[k] = __ballot_sync(0xffffffffu, fine && p.x >= 0 && p.y >= 0 && p.x != p.y);
+    if (lane == 0) counts[k * WARPS + warp] = __popc(is[k]);
+  }
+  __syncthreads();
+  int n = 0, before[ROUNDS];
+#pragma unroll
+  for (int k = 0; k < ROUNDS * WARPS; ++k) {
+    if (k % WARPS == warp) before[k / WARPS] = n;
+    n += counts[k];
+  }
+#pragma unroll
+  for (int k = 0; k < ROUNDS; ++k)
+    if (is[k] >> lane & 1u) pairs[before[k] + __popc(is[k] & ((1u << lane) - 1u))] = mine[k];
+  __syncthreads();
+  return n;
+}
+
+// GROUP threads for all parts of a page in one layer.
+template <int GROUP>
+__global__ void __launch_bounds__(NT, 4) copy_small_kernel(const __grid_constant__ CopyPagesArgs a) {
+  __shared__ int2 pairs[kPairs];
+  __shared__ int counts[kPairs / 32];
+  const Parts x = parts_of(a.kv);
+  bool bad = false;
+  for (int i0 = 0; i0 < a.n_pairs; i0 += kPairs) {
+    const int n = list_pairs(a, i0, pairs, counts, bad);
+    const int64_t all = (int64_t)n * a.kv.n, step = (int64_t)gridDim.x * (NT / GROUP);
+    for (int64_t w = (int64_t)blockIdx.x * (NT / GROUP) + threadIdx.x / GROUP; w < all; w += step) {
+      const int layer = (int)(w / n);
+      copy_vectors<GROUP>(a.kv, x, layer, pairs[w - (int64_t)layer * n], 0, x.all, threadIdx.x % GROUP);
+    }
+  }
+  if (bad) atomicOr(a.err, kErrBadArg);
+}
+
+// Large pages: a CTA for up to kTogether pieces of a page's k or v in one layer, or for all
+// its scales; entries without a page cost a CTA that looks at them.  96 pages of 64 bf16 rows
+// and 8 heads in 32 layers, 1.6 GB: 234 us (6.9 TB/s), 32 entries without a page among them;
+// one page of 256 rows in 40 layers among 35 such entries 21 us (a CTA a piece: 55).
+constexpr int kTogether = 4;
+
+__global__ void __launch_bounds__(NT, 8) copy_pages_kernel(const __grid_constant__ CopyPagesArgs a) {
+  const Parts x = parts_of(a.kv);
+  const unsigned of_codes = (unsigned)(x.codes + kTogether * kPiece - 1) / (kTogether * kPiece);
+  const unsigned per_page = 2 * of_codes + (x.scales > 0);
+  const unsigned page = blockIdx.x / per_page, layer = page / (unsigned)a.n_pairs;
+  const unsigned c = blockIdx.x - page * per_page, i = page - layer * (unsigned)a.n_pairs;
+  const int t = threadIdx.x, src = a.src[i], dst = a.dst[i];
   if (src < -1 || dst < -1 || src >= a.kv.n_pages || dst >= a.kv.n_pages) {
-    if (threadIdx.x == 0) atomicOr(a.err, kErrBadArg);
+    if (t == 0) atomicOr(a.err, kErrBadArg);
     return;
   }
   if (src == dst || src < 0 || dst < 0) return;  // (-1 stands for none)
-  const int rows = a.kv.Hkv * a.kv.page_size;
   const auto &l = a.kv.layer[layer];
-  if (c < 2u * a.chunks) {
-    const int row = a.kv.format == kKvBf16 ? 256 : a.kv.format == kKvE4m3 ? 128 : 64;
-    const int64_t bytes = (int64_t)rows * row;
-    const bool value = c >= (unsigned)a.chunks;
-    if (value) c -= a.chunks;
-    uint8_t *base = value ? l.v : l.k;
-    const int64_t at = (int64_t)c * kPiece + threadIdx.x * 16;
-    const uint8_t *from = base + src * a.kv.page_stride + at;
-    uint8_t *to = base + dst * a.kv.page_stride + at;
-    uint4 x[kVec];
+  if (c < 2 * of_codes) {
+    int64_t v0 = (int64_t)(c < of_codes ? c : c - of_codes) * (kTogether * kPiece) + t;
+    uint8_t *base = c < of_codes ? l.k : l.v;
+    const uint8_t *in = base + src * a.kv.page_stride;
+    uint8_t *out = base + dst * a.kv.page_stride;
+#pragma unroll 1
+    for (int r = 0; r < kTogether; ++r, v0 += kPiece) {
+      uint4 v[kVec];
 #pragma unroll
-    for (int v = 0; v < kVec; ++v)
-      if (at + v * (NT * 16) < bytes) x[v] = *reinterpret_cast<const uint4 *>(from + v * (NT * 16));
+      for (int k = 0; k < kVec; ++k)
+        if (v0 + k * NT < x.codes) v[k] = *reinterpret_cast<const uint4 *>(in + (v0 + k * NT) * 16);
 #pragma unroll
-    for (int v = 0; v < kVec; ++v)
-      if (at + v * (NT * 16) < bytes) *reinterpret_cast<uint4 *>(to + v * (NT * 16)) = x[v];
+      for (int k = 0; k < kVec; ++k)
+        if (v0 + k * NT < x.codes) *reinterpret_cast<uint4 *>(out + (v0 + k * NT) * 16) = v[k];
+    }
     return;
   }
-  // Scale bytes (a multiple of 16: pages have at least 16 rows).
-  const int n_bs = a.kv.format == kKvNvfp4 ? rows / 2 : 0;  // vectors of 16 block scales
-  const int n_s = rows / 16, all = 2 * (n_s + n_bs);
-  for (int v = threadIdx.x; v < all; v += NT) {
-    int w = v;
-    uint8_t *base;
-    int64_t page;
-    if (w < 2 * n_s) {
-      base = w < n_s ? l.k_scale : l.v_scale;
-      w = w < n_s ? w : w - n_s;
-      page = rows;
-    } else {
-      w -= 2 * n_s;
-      base = w < n_bs ? l.k_bs : l.v_bs;
-      w = w < n_bs ? w : w - n_bs;
-      page = (int64_t)rows * 8;
-    }
-    *reinterpret_cast<uint4 *>(base + dst * page + w * 16) =
-        *reinterpret_cast<const uint4 *>(base + src * page + w * 16);
+  const int all = 2 * (x.scales + x.blocks);
+  for (int v = t; v < all; v += NT) {
+    const bool block = v >= 2 * x.scales;
+    const int each = block ? x.blocks : x.scales, w = block ? v - 2 * x.scales : v;
+    const bool value = w >= each;
+    uint8_t *base = (block ? (value ? l.v_bs : l.k_bs) : (value ? l.v_scale : l.k_scale)) +
+                    (int64_t)(value ? w - each : w) * 16;
+    *reinterpret_cast<uint4 *>(base + (int64_t)dst * each * 16) =
+        *reinterpret_cast<const uint4 *>(base + (int64_t)src * each * 16);
   }
 }
 
@@ -556,7 +665,9 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
   // (1024 of them, 8 rows of bf16: 3.4 us by warps, 5.4 by CTAs) or saves more than the
   // launch for others (4096, up to 8 rows: 7.2 us with it, 14.5 by CTAs; up to 32: 18 and 17).
   const int mean = a.total / a.n_seq, few = 12288 / (2 * RowBytes<FMT>::value);
-  a.few = units >= 608 && (a.total <= few || (units >= 2048 && mean <= few / 2)) ? few : 0;
+  const bool all_few = a.total <= 4 * few;  // (at worst one sequence has them all: 11 us)
+  a.few = units >= 608 && (all_few || (units >= 2048 && mean <= few / 2)) ? few : 0;
+  if (a.few > 0 && all_few) a.few = a.total;
   if (a.few > 0) {
     const int64_t grid = (units + NT / 32 - 1) / (NT / 32);
     if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
@@ -564,16 +675,17 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.total <= a.few) return e;
   }
-  // Fewer of them than SMs and long: through rings (bf16: 32 of 1500 rows 11 us by rings, 21
-  // by CTAs; 128 of 1500 22 and 30, of 256 7.0 and 6.3; 320 of 1500 51 and 52).
+  // Few of them and long: through rings (bf16: 32 of 1500 rows 11 us by rings, 21 by CTAs;
+  // 128 of 1500 22 and 30, of 256 7.0 and 6.3; 320 of 1500 51 and 52).
   a.many = 0x7fffffff;
-  if (units < 160 && mean > 256) return compact_ring<FMT>(a, units, s);
-  // Lone long sequences among many short ones, in few layers, are too few CTAs: they go
+  if ((units < 160 && mean > 256) || (units < 320 && mean > 1024))
+    return compact_ring<FMT>(a, units, s);
+  // A lone long sequence among many short ones, in few layers, is too few CTAs: it goes
   // through rings behind the others (8200 rows of 8 heads in one layer among 60 sequences: 20
   // us, 111 without; in vain 2 to 3 us).
   const int64_t lone = (int64_t)a.kv.n * a.kv.Hkv;
   const bool rings = lone <= 64 && a.total > 4096;
-  if (rings) a.many = max(1024, a.total / 4);
+  if (rings) a.many = max(1024, a.total / 2);
   const int64_t grid = a.few > 0 ? min(units, (int64_t)152 * 4) : units;
   if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
   compact_cta_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
@@ -586,13 +698,24 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_kv_copy_pages(CopyPagesArgs a, cudaStream_t s) {
-  const int row = a.kv.format == kKvBf16 ? 256 : a.kv.format == kKvE4m3 ? 128 : 64;
-  const int64_t bytes = (int64_t)a.kv.Hkv * a.kv.page_size * row;
-  a.chunks = (int)((bytes + kPiece - 1) / kPiece);
-  const int64_t grid = (2LL * a.chunks + (a.kv.format != kKvBf16)) * a.n_pairs * a.kv.n;
-  if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
-  copy_pages_kernel<<<(unsigned)grid, NT, 0, s>>>(a);
+cudaError_t launch_kv_copy_pages(const CopyPagesArgs &a, cudaStream_t s) {
+  const Parts x = parts_of(a.kv);
+  const int64_t pages = (int64_t)a.n_pairs * a.kv.n;
+  // By a warp, by a CTA, or in pieces (NVFP4, 446 pages of 146 vectors in 40 layers: 11 us by
+  // warps, 53 in pieces; 391 of 876 vectors: 71 us by CTAs, 200 in pieces; E4M3, 96 of 8256
+  // in 32 layers: 136 by CTAs, 120 in pieces; 4 pages of 2064 3.5 and 2.1).
+  const bool many = pages > 152 * 4;
+  if (many && x.all <= 512) {
+    const int64_t grid = min((pages + NT / 32 - 1) / (NT / 32), (int64_t)152 * 4);
+    copy_small_kernel<32><<<(unsigned)grid, NT, 0, s>>>(a);
+  } else if (many && x.codes <= 2048) {
+    copy_small_kernel<NT><<<(unsigned)min(pages, (int64_t)152 * 4), NT, 0, s>>>(a);
+  } else {
+    const int64_t each = (x.codes + kTogether * kPiece - 1) / (kTogether * kPiece);
+    const int64_t grid = pages * (2 * each + (x.scales > 0));
+    if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
+    copy_pages_kernel<<<(unsigned)grid, NT, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 

@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(NT, 1) reserve_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------------- fork --
 constexpr int FT = 256;
 constexpr int kEntries = 8;  // table entries a thread loads at a time
+constexpr int kListed = 1024;  // followers of a row that are listed
 
 // A length in range, or the nearest that is.
 __device__ __forceinline__ int clip(int x, int hi, bool &bad) {
@@ -283,24 +284,21 @@ __device__ __forceinline__ int clip(int x, int hi, bool &bad) {
   return min(max(x, 0), hi);
 }
 
-// One CTA a row: first the rows of the new batch, then those of the old one.  The
-// counts change only where pages change hands: a sequence's first follower takes its
-// references over, others add theirs, and what no follower takes over is given back.
-// (Every follower and every old row looks through the parents before it, a few loads a
-// thread.)  Latency bounds it: 512 rows of up to 2048 entries 5.8 us, eight entries a
-// thread in flight (6.4 with four).
+// One CTA a row.  Those of the new batch copy entries.  Those of the old one look through
+// the parents for their followers and move each page's count by how many of these have it,
+// less one for the row itself: an addition a page, however many followers there are, and
+// none where one follower takes the page over.  (With every follower adding for itself, 355
+// followers of one sequence of 765 pages: 28 us.)  Latency bounds it: 512 rows of up to
+// 2048 entries 5.8 us.
 __global__ void __launch_bounds__(FT) fork_kernel(const __grid_constant__ ForkArgs a) {
   const int tid = threadIdx.x, ps = a.page_size;
-  const int64_t room = (int64_t)a.max_pages * ps;
-  const int most = (int)min(room, (int64_t)0x7fffffff);
+  const int most = (int)min((int64_t)a.max_pages * ps, (int64_t)0x7fffffff);
   const int n_new = a.parent ? a.n_new : 0;  // (without parents the rows stay where they are)
   bool bad = false;
   if ((int)blockIdx.x < n_new) {
-    const int d = blockIdx.x, s = a.parent[d];
-    bad = s < -1 || s >= a.n_seq;
-    const int len0 = a.new_len[d];
+    const int d = blockIdx.x, s = a.parent[d], len = a.new_len[d];
     if (s < 0 || s >= a.n_seq) {
-      if ((bad || len0 != 0) && tid == 0) atomicOr(a.err, kErrBadArg);
+      if ((s != -1 || len != 0) && tid == 0) atomicOr(a.err, kErrBadArg);
       return;
     }
     const int old = a.kv_len[s];
@@ -313,54 +311,69 @@ __global__ void __launch_bounds__(FT) fork_kernel(const __grid_constant__ ForkAr
         p[i] = e0 + i * FT < a.max_pages ? from[e0 + i * FT] : 0;
     };
     load(tid);
-    bool follows = false;  // a follower of s comes before
-    for (int e = tid; e < d; e += FT) follows |= a.parent[e] == s;
-    follows = __syncthreads_or(follows);
     const bool lost = old < 0 || old > most;  // (the old row reports it)
-    const int n = pages_of(clip(len0, lost ? 0 : old, bad), ps);
+    const int n = pages_of(clip(len, lost ? 0 : old, bad), ps);
     for (int e0 = tid; e0 < n; e0 += kEntries * FT) {
       if (e0 != tid) load(e0);
 #pragma unroll
-      for (int i = 0; i < kEntries; ++i) {
-        if (e0 + i * FT >= n) break;
-        to[e0 + i * FT] = p[i];
-        if (p[i] < 0 || p[i] >= a.n_pages) bad = true;
-        else if (follows) atomicAdd(a.refs + p[i], 1);
-      }
+      for (int i = 0; i < kEntries; ++i)
+        if (e0 + i * FT < n) to[e0 + i * FT] = p[i];
     }
   } else {
     const int s = blockIdx.x - n_new;
     const int old = a.kv_len[s];
-    int keep = 0;  // pages that a follower takes over
     if (old < 0 || old > most) {
       if (tid == 0) atomicOr(a.err, kErrBadArg);
       return;
     }
-    if (!a.parent) {
-      keep = pages_of(clip(a.new_len[s], old, bad), ps);
-    } else {
-      __shared__ int first;
-      if (tid == 0) first = n_new;
-      __syncthreads();
-      int d = n_new;
-      for (int e = tid; e < n_new && d == n_new; e += FT)
-        if (a.parent[e] == s) d = e;
-      if (d < n_new) atomicMin(&first, d);
-      __syncthreads();
-      bool unused = false;
-      if (first < n_new) keep = pages_of(clip(a.new_len[first], old, unused), ps);
-    }
-    const int n = pages_of(old, ps);
     const int32_t *from = a.table + (int64_t)s * a.max_pages;
-    for (int e0 = keep + tid; e0 < n; e0 += kEntries * FT) {
+    const int n = pages_of(old, ps);
+    // Followers, how many pages they have, and the fewest and the most.
+    __shared__ int followers, fewest, largest, pages_had[kListed];
+    int count, lo, hi;
+    bool unused = false;
+    if (!a.parent) {
+      count = 1;
+      lo = hi = pages_of(clip(a.new_len[s], old, bad), ps);
+    } else {
+      if (tid == 0) {
+        followers = 0;
+        fewest = n;
+        largest = 0;
+      }
+      __syncthreads();
+      for (int e = tid; e < n_new; e += FT)
+        if (a.parent[e] == s) {
+          const int pages = pages_of(clip(a.new_len[e], old, unused), ps);
+          const int i = atomicAdd(&followers, 1);
+          if (i < kListed) pages_had[i] = pages;
+          atomicMin(&fewest, pages);
+          atomicMax(&largest, pages);
+        }
+      __syncthreads();
+      count = followers;
+      lo = count ? fewest : 0;
+      hi = largest;
+    }
+    // All followers have the first `lo` pages, none those from `hi` on.
+    for (int e0 = (count == 1 ? lo : 0) + tid; e0 < n; e0 += kEntries * FT) {
       int p[kEntries];
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) p[i] = e0 + i * FT < n ? from[e0 + i * FT] : 0;
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) {
-        if (e0 + i * FT >= n) break;
+        const int e = e0 + i * FT;
+        if (e >= n) break;
+        int more = (e < lo ? count : 0) - 1;
+        if (e >= lo && e < hi) {
+          if (count <= kListed)
+            for (int d = 0; d < count; ++d) more += pages_had[d] > e;
+          else
+            for (int d = 0; d < n_new; ++d)
+              more += a.parent[d] == s && pages_of(clip(a.new_len[d], old, unused), ps) > e;
+        }
         if (p[i] < 0 || p[i] >= a.n_pages) bad = true;
-        else atomicSub(a.refs + p[i], 1);
+        else if (more) atomicAdd(a.refs + p[i], more);
       }
     }
   }

@@ -229,6 +229,8 @@ def same(parts, want):
 @pytest.mark.parametrize("n_layers,n_pages,Hkv,ps,n,together", [
     (1, 2, 1, 16, 1, False), (1, 9, 3, 16, 4, True), (2, 21, 8, 64, 9, False),
     (65, 7, 1, 32, 3, False), (3, 40, 2, 384, 19, True),
+    (40, 41, 1, 16, 18, False), (40, 45, 3, 32, 20, True),  # by warps, by CTAs
+    (1, 1500, 1, 16, 700, False),  # more entries than are listed at a time
 ])
 def test_copy_pages(fmt, n_layers, n_pages, Hkv, ps, n, together):
     r = random.Random(n_pages)
