@@ -18,19 +18,24 @@
 // 84 without them).
 //
 // One cluster a sequence: every warp finds the row, sums its stretch of it, 256 tokens at a
-// time, and sends the sum round; the CTA whose stretches hold the threshold goes on from
-// the sums of a stretch's pieces, which its warps have kept, to the token.
+// time (512 of bf16, by words of two: 364 rows of 137212 without a draft 35 us, by single
+// values and one CTA a row 76), and sends the sum round; the CTA whose stretches hold the
+// threshold goes on from the sums of a stretch's pieces, which its warps have kept, to the
+// token.
 //
 // What bounds it: a small call its way through six dependent steps (bounds, drafted
 // tokens, their probabilities, the row, the sums of all, the search: one sequence, 32000
 // tokens, 5.3 us); a large one the loads under way, then DRAM (256 sequences, 128000 tokens,
-// up to 5 drafts, 190 MB: 45 us; 600 with 4 drafts, 614 MB: 98, 94 % of the copy rate).  Six
-// CTAs of 256 threads an SM hide one another's steps better than three of 512 (48 us) or
-// four of 384 (46).  Not kept: loads one round ahead in registers (57 us), acceptance in a
-// kernel of its own (no gain), a search that sums the stretch again (5 us more).
+// up to 5 drafts, 190 MB: 47 us; 600 with 4 drafts, 614 MB: 98, 94 % of the copy rate), or,
+// with bf16 rows, the arithmetic (about 17 instructions a token: the same 256 sequences, 95
+// MB: 43 us).  Six CTAs of 256 threads an SM hide one another's steps better than three of
+// 512 (48 us) or four of 384 (46).  Not kept: loads one round ahead in registers (57 us),
+// acceptance in a kernel of its own (no gain), a search that sums the stretch again (5 us
+// more).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "cluster.cuh"
 #include "internal.h"
@@ -57,8 +62,9 @@ constexpr float kM2 = 1.430511474609375e-6f; // 1.5 * 2^-20: steps of 2^-43
 constexpr float kM3 = 1.0913936421275139e-11f; // 1.5 * 2^-37: steps of 2^-60
 constexpr uint32_t kValid = 0x40000000u;     // fp32 bits from here on: 2 and more, NaN, negative
 
+// Units of s1 steps of 2^-21, s2 of 2^-43 and s3 of 2^-60 (these two signed).
 __device__ __forceinline__ u64 join(uint32_t s1, uint32_t s2, uint32_t s3) {
-  return ((u64)(int64_t)(int)s1 << 39) + ((u64)(int64_t)(int)s2 << 17) + (u64)(int64_t)(int)s3;
+  return ((u64)s1 << 39) + ((u64)(int64_t)(int)s2 << 17) + (u64)(int64_t)(int)s3;
 }
 
 // A probability (fp32 bits) in units of 2^-60.  What lies outside [0, 2) (a NaN among it)
@@ -105,80 +111,144 @@ __device__ __forceinline__ u64 scan_warp(u64 x, int lane) {
   return x;
 }
 
-constexpr int kSpan = 256;    // tokens a warp sums at a time
-constexpr int kPieces = 64;   // sums of its stretch that a warp keeps
+constexpr int kPieces = 64;  // sums of its stretch that a warp keeps
 
-// Sum of the weights of tokens [i, min(i + kSpan, i1)), in every lane of the warp.
-template <bool BF16, bool HAS_Q>
-__device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int lane, bool &bad) {
-  constexpr int U = kSpan / 32;
+// Two values' steps plus the constants' bits: a of the first, b of the second.
+__device__ __forceinline__ void steps(uint32_t lo, uint32_t hi, uint32_t (&a)[3], uint32_t (&b)[3]) {
   auto two = [](float x, float y) {
     return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
   };
   const uint64_t m1 = two(kM1, kM1), m2 = two(kM2, kM2), m3 = two(kM3, kM3), neg = two(-1.f, -1.f);
-  uint32_t x[U], y[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int t = i + u * 32 + lane;
-    x[u] = t < i1 ? load_bits<BF16>(r.p, t) : 0u;
-    y[u] = HAS_Q && t < i1 ? load_bits<BF16>(r.q, t) : 0u;
-  }
-  auto steps = [&](uint32_t lo, uint32_t hi, uint32_t (&a)[3], uint32_t (&b)[3]) {
-    const uint64_t v = (uint64_t)lo | (uint64_t)hi << 32;
-    const uint64_t t1 = tc::f2_add(v, m1);
-    const uint64_t r1 = tc::f2_add(v, tc::f2_fma(t1, neg, m1));
-    const uint64_t t2 = tc::f2_add(r1, m2);
-    const uint64_t r2 = tc::f2_add(r1, tc::f2_fma(t2, neg, m2));
-    const uint64_t t3 = tc::f2_add(r2, m3);
-    a[0] = (uint32_t)t1; b[0] = (uint32_t)(t1 >> 32);
-    a[1] = (uint32_t)t2; b[1] = (uint32_t)(t2 >> 32);
-    a[2] = (uint32_t)t3; b[2] = (uint32_t)(t3 >> 32);
-  };
-  // Modulo 2^32, as signed numbers: a value has at most 2^22 steps, a span 2^30.
-  uint32_t s1 = 0, s2 = 0, s3 = 0, a[3], b[3];
+  const uint64_t v = (uint64_t)lo | (uint64_t)hi << 32;
+  const uint64_t t1 = tc::f2_add(v, m1);
+  const uint64_t r1 = tc::f2_add(v, tc::f2_fma(t1, neg, m1));
+  const uint64_t t2 = tc::f2_add(r1, m2);
+  const uint64_t r2 = tc::f2_add(r1, tc::f2_fma(t2, neg, m2));
+  const uint64_t t3 = tc::f2_add(r2, m3);
+  a[0] = (uint32_t)t1; b[0] = (uint32_t)(t1 >> 32);
+  a[1] = (uint32_t)t2; b[1] = (uint32_t)(t2 >> 32);
+  a[2] = (uint32_t)t3; b[2] = (uint32_t)(t3 >> 32);
+}
+
+// A lane's sums.  Those of 512 values (16 a lane) fit in 32 bits: at most 2^22 steps of 2^-21
+// each, none negative, and 2^21 of 2^-43, up or down; but a difference has up to 2^22 of those,
+// so that half a warp's are summed before the others.
+struct Sums {
+  uint32_t s1 = 0, s2 = 0, s3 = 0;
   uint32_t most = 0;  // the largest bits of all values
-  if constexpr (HAS_Q) {
+  __device__ __forceinline__ void difference(uint32_t p, uint32_t q) {
+    uint32_t a[3], b[3];
+    most = max(most, max(p, q));
+    steps(p, q, a, b);
+    if (p > q) {  // (valid values: their bits compare as they do)
+      s1 += a[0] - b[0];
+      s2 += a[1] - b[1];
+      s3 += a[2] - b[2];
+    }
+  }
+  __device__ __forceinline__ void both(uint32_t p0, uint32_t p1) {
+    uint32_t a[3], b[3];
+    most = max(most, max(p0, p1));
+    steps(p0, p1, a, b);
+    s1 += a[0] + b[0] - 2 * __float_as_uint(kM1);
+    s2 += a[1] + b[1] - 2 * __float_as_uint(kM2);
+    s3 += a[2] + b[2] - 2 * __float_as_uint(kM3);
+  }
+  __device__ __forceinline__ u64 of_warp() const {
+    return join(__reduce_add_sync(0xffffffffu, s1), __reduce_add_sync(0xffffffffu, s2),
+                __reduce_add_sync(0xffffffffu, s3));
+  }
+};
+
+// How a lane loads: fp32 values one by one, or bf16 values in aligned words of two; where q
+// starts in the other half of a word than p, its pairs are put together from two words.
+enum : int { kF32 = 0, kBf16 = 1, kBf16Across = 2 };
+constexpr int U = 8;  // values or pairs a lane at a time
+template <bool BF16> constexpr int kSpan = BF16 ? 64 * U : 32 * U;  // tokens of a warp
+
+// Sum of the weights of slots [i, min(i + kSpan, i1)), in every lane of the warp.  Slots are
+// tokens counted from `shift` on: 1 where words are loaded and p's row starts with the second
+// half of one, 0 otherwise.
+template <int HOW, bool HAS_Q>
+__device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int shift, int lane, bool &bad) {
+  constexpr bool BF16 = HOW != kF32, ACROSS = HOW == kBf16Across;
+  uint32_t x[U], y[U];
+  Sums s;
+  u64 sum = 0;
+  if constexpr (BF16) {
+    auto words = [&](const void *row, int back) {
+      return reinterpret_cast<const uint32_t *>((const uint16_t *)row - back) + (i >> 1) + lane;
+    };
+    const uint32_t *p = words(r.p, shift), *q = HAS_Q ? words(r.q, shift + ACROSS) : nullptr;
+    auto pair = [](uint32_t w, uint32_t next) { return __byte_perm(w, next, 0x5432); };
+    if (i >= shift && i + kSpan<BF16> <= i1) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        x[u] = __ldg(p + u * 32);
+        y[u] = !HAS_Q ? 0u : ACROSS ? pair(__ldg(q + u * 32), __ldg(q + u * 32 + 1)) : __ldg(q + u * 32);
+      }
+    } else {  // (no word without a token of the row is loaded; half a neighbour is left out)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = i + 2 * (u * 32 + lane);
+        const bool lo = t >= shift && t < i1, hi = t + 1 < i1;
+        const uint32_t keep = (lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u);
+        x[u] = lo || hi ? __ldg(p + u * 32) & keep : 0u;
+        if constexpr (ACROSS) y[u] = pair(lo ? __ldg(q + u * 32) : 0u, hi ? __ldg(q + u * 32 + 1) : 0u);
+        else y[u] = HAS_Q && (lo || hi) ? __ldg(q + u * 32) & keep : 0u;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      most = max(most, max(x[u], y[u]));
-      steps(x[u], y[u], a, b);
-      if (x[u] > y[u]) {  // (valid values: their bits compare as they do)
-        s1 += a[0] - b[0];
-        s2 += a[1] - b[1];
-        s3 += a[2] - b[2];
+      if (HAS_Q && u == U / 2) {
+        sum = join(0, __reduce_add_sync(0xffffffffu, s.s2), 0);
+        s.s2 = 0;
+      }
+      if constexpr (HAS_Q) {
+        s.difference(x[u] << 16, y[u] << 16);
+        s.difference(x[u] & 0xffff0000u, y[u] & 0xffff0000u);
+      } else {
+        s.both(x[u] << 16, x[u] & 0xffff0000u);
       }
     }
   } else {
 #pragma unroll
-    for (int u = 0; u < U; u += 2) {
-      most = max(most, max(x[u], x[u + 1]));
-      steps(x[u], x[u + 1], a, b);
-      s1 += a[0] + b[0] - 2 * __float_as_uint(kM1);
-      s2 += a[1] + b[1] - 2 * __float_as_uint(kM2);
-      s3 += a[2] + b[2] - 2 * __float_as_uint(kM3);
+    for (int u = 0; u < U; ++u) {
+      const int t = i + u * 32 + lane;
+      x[u] = t < i1 ? load_bits<BF16>(r.p, t) : 0u;
+      y[u] = HAS_Q && t < i1 ? load_bits<BF16>(r.q, t) : 0u;
+    }
+    if constexpr (HAS_Q) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) s.difference(x[u], y[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; u += 2) s.both(x[u], x[u + 1]);
     }
   }
-  if (__any_sync(0xffffffffu, most >= kValid)) {  // values to leave out: one by one
+  if (__any_sync(0xffffffffu, s.most >= kValid)) {  // values to leave out: one by one
     u64 w = 0;
-    for (int t = i + lane; t < min(i + kSpan, i1); t += 32) w += weight<BF16>(r, t, bad);
+    for (int t = max(i, shift) + lane; t < min(i + kSpan<BF16>, i1); t += 32)
+      w += weight<BF16>(r, t - shift, bad);
     return sum_warp(w);
   }
-  const u64 sum = join(__reduce_add_sync(0xffffffffu, s1), __reduce_add_sync(0xffffffffu, s2),
-                       __reduce_add_sync(0xffffffffu, s3));
-  if (r.hole < i || r.hole >= min(i + kSpan, i1)) return sum;
+  if constexpr (BF16) sum += s.of_warp();
+  else sum = s.of_warp();
+  const int hole = r.hole + shift;
+  if (r.hole < 0 || hole < i || hole >= min(i + kSpan<BF16>, i1)) return sum;
   bool noted = false;
   return sum - units(load_bits<BF16>(r.p, r.hole), noted);
 }
 
-// Sum of the weights of tokens [i0, i1), in every lane, and of each `piece` of them.
-template <bool BF16, bool HAS_Q>
+// Sum of the weights of slots [i0, i1), in every lane, and of each `piece` of them.
+template <int HOW, bool HAS_Q>
 __device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int piece, u64 *pieces,
-                                           int lane, bool &bad) {
+                                           int shift, int lane, bool &bad) {
   u64 sum = 0;
   for (int i = i0, k = 0; i < i1; ++k) {
     u64 part = 0;
-    for (const int end = min(i1, i + piece); i < end; i += kSpan)
-      part += sum_span<BF16, HAS_Q>(r, i, i1, lane, bad);
+    for (const int end = min(i1, i + piece); i < end; i += kSpan<HOW != kF32>)
+      part += sum_span<HOW, HAS_Q>(r, i, i1, shift, lane, bad);
     if (lane == 0) pieces[k] = part;
     sum += part;
   }
@@ -249,16 +319,24 @@ __global__ void __launch_bounds__(NT, 6) verify_kernel(const __grid_constant__ V
   }
 
   cluster_wait();  // (the others' shared memory is there)
-  // Every warp's stretch, a multiple of 32 tokens.
   const int all = n_cta * NW, mine = rank * NW + warp;
-  const int len = ((a.V + all - 1) / all + 31) & ~31;
-  const int i0 = (int)min((int64_t)mine * len, (int64_t)a.V), i1 = min(i0 + len, a.V);
-  const int piece = (len + kPieces * kSpan - 1) / (kPieces * kSpan) * kSpan;
+  auto half = [](const void *row) { return (int)((uintptr_t)row >> 1 & 1); };
+  const int shift = BF16 ? half(row.p) : 0, slots = a.V + shift;
+  // Every warp's stretch, a multiple of 64 slots, and the slots of which it keeps the sum.
+  const int len = ((slots + all - 1) / all + 63) & ~63;
+  const int i0 = min(mine * len, slots), i1 = min(i0 + len, slots);
+  const int piece = (len + kPieces * kSpan<BF16> - 1) / (kPieces * kSpan<BF16>) * kSpan<BF16>;
   u64 total = 0, below = 0;  // sums of all warps, and of those of the CTAs before this one
   int round = 0;
   while (true) {  // a second time only where p - q is 0 throughout
-    const u64 stretch = row.q ? sum_stretch<BF16, true>(row, i0, i1, piece, pieces[warp], lane, bad)
-                              : sum_stretch<BF16, false>(row, i0, i1, piece, pieces[warp], lane, bad);
+    auto sum_as = [&](auto how, auto has_q) {
+      return sum_stretch<how.value, has_q.value>(row, i0, i1, piece, pieces[warp], shift, lane, bad);
+    };
+    using std::integral_constant;
+    u64 stretch;
+    if (!row.q) stretch = sum_as(integral_constant<int, BF16>{}, std::false_type{});
+    else if (BF16 && half(row.q) != shift) stretch = sum_as(integral_constant<int, BF16 ? kBf16Across : kF32>{}, std::true_type{});
+    else stretch = sum_as(integral_constant<int, BF16>{}, std::true_type{});
     if (lane < n_cta) *cluster.map_shared_rank(&sums[round][mine], lane) = stretch;
     cluster.sync();
     u64 before = 0, every = 0;
@@ -288,7 +366,7 @@ __global__ void __launch_bounds__(NT, 6) verify_kernel(const __grid_constant__ V
     if (!total) out[acc] = a.V - 1;
   }
   // The CTA whose stretches hold the threshold looks up the warp's, then the piece of it;
-  // parts of that, where it is long, are summed again, until a token a thread is left.
+  // parts of that, where it is long, are summed again, until a load a thread is left.
   // `find`: which of n sums holds it; below becomes the sum before.
   auto find = [&](const u64 *part, int n) {
     for (int k = 0; k < n; k += 32) {
@@ -306,16 +384,17 @@ __global__ void __launch_bounds__(NT, 6) verify_kernel(const __grid_constant__ V
   const int holder = find(&sums[round][rank * NW], NW);
   if (holder < 0) return;
   const int first = (rank * NW + holder) * len;
-  const int k = find(pieces[holder], (min(len, a.V - first) + piece - 1) / piece);
+  const int k = find(pieces[holder], (min(len, slots - first) + piece - 1) / piece);
   if (k < 0) return;
-  int lo = first + k * piece, end = min(min(lo + piece, first + len), a.V);
+  int lo = first + k * piece, end = min(min(lo + piece, first + len), slots);
   bool noted = false;
-  while (end - lo > NT) {
+  auto weight_at = [&](int i) { return i < shift ? 0 : weight<BF16>(row, i - shift, noted); };
+  while (end - lo > kSpan<BF16>) {
     const int step = ((end - lo + NW - 1) / NW + 31) & ~31;
     u64 sum = 0;
     const int last = min(lo + (warp + 1) * step, end);
 #pragma unroll 4
-    for (int i = lo + warp * step + lane; i < last; i += 32) sum += weight<BF16>(row, i, noted);
+    for (int i = lo + warp * step + lane; i < last; i += 32) sum += weight_at(i);
     sum = sum_warp(sum);
     __syncthreads();  // the sums before are no longer needed
     if (lane == 0) sums[0][warp] = sum;
@@ -325,13 +404,17 @@ __global__ void __launch_bounds__(NT, 6) verify_kernel(const __grid_constant__ V
     lo += part * step;
     end = min(lo + step, end);
   }
-  const u64 w = lo + tid < end ? weight<BF16>(row, lo + tid, noted) : 0, mine_sum = sum_warp(w);
+  constexpr int kEach = kSpan<BF16> / NT;
+  const int j = lo + kEach * tid;
+  const u64 w = j < end ? weight_at(j) : 0, all_w = w + (kEach == 2 && j + 1 < end ? weight_at(j + 1) : 0);
+  const u64 of_warp = sum_warp(all_w);
   __syncthreads();
-  if (lane == 0) sums[0][warp] = mine_sum;
+  if (lane == 0) sums[0][warp] = of_warp;
   __syncthreads();
   if (find(sums[0], NW) != warp) return;
-  const u64 upto = below + scan_warp(w, lane);
-  if (threshold < upto && threshold >= upto - w) out[acc] = lo + tid;
+  const u64 upto = below + scan_warp(all_w, lane);
+  if (threshold < upto && threshold >= upto - all_w)
+    out[acc] = (threshold < upto - all_w + w ? j : j + 1) - shift;
 }
 
 template <bool BF16>
@@ -354,12 +437,13 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
   // CTAs a sequence: more while every warp has more than 256 tokens and all fit about three an
   // SM (128000 tokens of one sequence: 38.8 us by one CTA, 9.0 by eight; 8000 of 300: 8.2 by
-  // one, 18.7 by eight), or four an SM where each still has 16000 tokens (128000 of 150: 39 by
-  // two, 30 by four, 33 by eight; 32000 of 300: 20 by one, 17 by two, 23 by eight).
+  // one, 18.7 by eight), or six an SM, all that fit, where each still has 16000 tokens (128000 of
+  // 150: 39 by two, 30 by four, 33 by eight; 128000 of 310: 74 by one, 57 by two; 32000 of 400:
+  // 21.2 by one, 19.5 by two).
   int n_cta = 1;
   while (n_cta < kMaxCluster && a.V > n_cta * NW * 256) {
     const int64_t ctas = (int64_t)n_cta * 2 * a.n_seq;
-    if (ctas > 400 && (ctas > 608 || a.V < 32000 * n_cta)) break;
+    if (ctas > 400 && (ctas > 912 || a.V < 32000 * n_cta)) break;
     n_cta *= 2;
   }
   return a.bf16 ? launch<true>(a, n_cta, s) : launch<false>(a, n_cta, s);

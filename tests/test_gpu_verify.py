@@ -78,10 +78,47 @@ def test_tokens(V, n, pad, probs, dtype):
     no_error()
 
 
+@pytest.mark.parametrize("V", [1, 2, 33, 513, 5000, 60001])
+def test_rows_that_start_in_either_half_of_a_word(V):
+    """bf16 rows at even and odd elements, target and draft alike or not, NaN all round."""
+    a = inputs(61, [2, 0, 1, 3], V, torch.bfloat16)
+    for spare in (2, 3):
+        for at_p in (0, 1):
+            for at_q in (0, 1):
+                b = dict(a)
+                for name, at in (("target", at_p), ("draft", at_q)):
+                    wide = torch.full((a[name].shape[0], V + spare), float("nan"), dtype=torch.bfloat16,
+                                      device=DEV)
+                    wide[:, at:at + V] = a[name]
+                    b[name] = wide[:, at:at + V]
+                for u in (0.0, 0.5, 1 - 2.0 ** -24):
+                    b["u_sample"] = torch.full((4,), u, device=DEV)
+                    check(b)
+                check(dict(b, draft=None, drafted=torch.clamp(a["drafted"], max=V - 1)))
+    no_error()
+
+
 @pytest.mark.parametrize("V,dtype", [(1300003, torch.float32), (9000001, torch.bfloat16)])
 def test_vocabularies_of_millions(V, dtype):
     for seed, probs in ((1, True), (2, False)):
         check(inputs(seed, [1, 0], V, dtype, probs, sharp=1.0))
+    no_error()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("p,q", [(5, 3), (7, 5), (2, 1), (9, 7), (6.5, 0.5)])
+@pytest.mark.parametrize("step", [2.0 ** -22, 2.0 ** -44])
+def test_constant_rows_halfway_between_steps(p, q, step, dtype):
+    """p - q rounds the same way for every token, as far as it can."""
+    V = 20011
+    for rows in (False, True):
+        target = torch.full((2, V), p * step, device=DEV, dtype=dtype)
+        draft = torch.full((1, V), q * step, device=DEV, dtype=dtype) if rows else None
+        target[0, 4097] = 0.0
+        for u in (0.0, 0.25, 0.9, 1 - 2.0 ** -24):
+            check(dict(target=target, drafted=i32([4097]), cu=i32([0, 1]), max_draft=1,
+                       u_accept=torch.full((1,), 0.5, device=DEV),
+                       u_sample=torch.full((1,), u, device=DEV), draft=draft))
     no_error()
 
 
