@@ -726,6 +726,7 @@ extern "C" attn_status attn_skip_kv_copy_pages(const attn_kv_pages *kv, int n_la
   const attn_status st = layers_check(kv, n_layers);
   if (st != ATTN_OK) return st;
   if (n_pairs < 0) return ATTN_EINVAL;
+  if ((int64_t)kv->Hkv * kv->page_size > 1 << 24) return ATTN_EUNSUPPORTED;  // int vectors of a page
   if (n_pairs == 0) return ATTN_OK;
   if (!src || !dst || !aligned4(src) || !aligned4(dst)) return ATTN_EINVAL;
   CopyPagesArgs a{};
@@ -755,6 +756,8 @@ extern "C" attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layer
   if (out_table && out_max_pages <= 0) return ATTN_EINVAL;
   if (total > kMaxPositions) return ATTN_EUNSUPPORTED;
   if (out_table && (int64_t)out_max_pages * kv->page_size > kMaxPositions) return ATTN_EUNSUPPORTED;
+  if ((int64_t)(n_layers < kMaxLayers ? n_layers : kMaxLayers) * kv->Hkv * n_seq > 0x7fffffff)
+    return ATTN_EUNSUPPORTED;
   if (total == 0) return ATTN_OK;
   if (!keep || !aligned4(keep)) return ATTN_EINVAL;
   CompactArgs a{};

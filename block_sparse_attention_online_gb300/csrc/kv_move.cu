@@ -670,7 +670,6 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
   if (a.few > 0 && all_few) a.few = a.total;
   if (a.few > 0) {
     const int64_t grid = (units + NT / 32 - 1) / (NT / 32);
-    if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
     compact_warp_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.total <= a.few) return e;
@@ -687,7 +686,6 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
   const bool rings = lone <= 64 && a.total > 4096;
   if (rings) a.many = max(1024, a.total / 2);
   const int64_t grid = a.few > 0 ? min(units, (int64_t)152 * 4) : units;
-  if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
   compact_cta_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !rings) return e;

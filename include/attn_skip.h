@@ -760,7 +760,8 @@ attn_status attn_skip_pages_fork(int32_t *refs, int n_pages, const int32_t *page
  * A page may be copied to several places; a page that two entries write, or that
  * one writes and another reads, holds a mixture.  EINVAL as for
  * attn_skip_kv_append, for caches that differ and n_pairs < 0; a page id below -1
- * or not below n_pages is left out and reported by attn_skip_last_device_error.
+ * or not below n_pages is left out and reported by attn_skip_last_device_error.  Pages of
+ * more than 2^24 rows (of all heads) are EUNSUPPORTED.
  */
 attn_status attn_skip_kv_copy_pages(const attn_kv_pages *kv, int n_layers, int n_pairs,
                                     const int32_t *src, const int32_t *dst, void *stream);

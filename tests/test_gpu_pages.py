@@ -151,6 +151,17 @@ def test_fork(n, ps, max_kv, share):
         check_fork(refs, table, old, [0] * n, ps, [-1] * n)  # the batch ends
 
 
+@pytest.mark.parametrize("followers", [24, 25, 1300])
+@pytest.mark.parametrize("shortest,longest", [(0, 2500), (700, 720), (1, 1025), (2499, 2500)])
+def test_fork_many_followers_of_different_lengths(followers, shortest, longest):
+    r = random.Random(followers + shortest)
+    refs, table = [1] * 2500 + [3] * 5, [list(range(2500)), [2504] * 2500]
+    parent = [0] * followers + [1, -1]
+    r.shuffle(parent)
+    new = [(0 if p < 0 else 1 if p else r.randint(shortest, longest)) for p in parent]
+    check_fork(refs, table, [2500, 1], new, 1, parent)
+
+
 def test_fork_makes_its_table():
     R, T = i32([1, 1, 0]), i32([[0, 1]])
     out = bs.attn_skip_pages_fork(R, T, i32([20]), i32([20, 3, 0]), 16, parent=i32([0, 0, -1]))

@@ -111,6 +111,13 @@ def test_copy_pages_rejects_invalid_arguments(lib, kw):
     assert copy(lib, **kw) == bs.ATTN_EINVAL
 
 
+def test_copy_pages_and_compact_limits(lib):
+    assert copy(lib, pages(page_size=128, Hkv=(1 << 17) + 1)) == bs.ATTN_EUNSUPPORTED
+    assert copy(lib, pages(page_size=128, Hkv=1 << 17), pairs=0) == bs.ATTN_OK
+    assert compact(lib, pages(Hkv=1 << 10), n_seq=1 << 21) == bs.ATTN_EUNSUPPORTED
+    assert compact(lib, total=(1 << 30) + 1) == bs.ATTN_EUNSUPPORTED
+
+
 def test_nothing_to_do(lib):
     assert copy(lib, pairs=0, src=None, dst=None) == bs.ATTN_OK
     assert compact(lib, total=0, keep=None) == bs.ATTN_OK
