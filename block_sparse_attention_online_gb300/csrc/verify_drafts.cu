@@ -17,21 +17,21 @@
 // the exponent take fifty and bound the large calls (256 sequences, 128000 tokens: 193 us,
 // 84 without them).
 //
-// One cluster a sequence: every warp finds the row, sums its stretch of it, 256 tokens at a
-// time (512 of bf16, by words of two: 364 rows of 137212 without a draft 35 us, by single
-// values and one CTA a row 76), and sends the sum round; the CTA whose stretches hold the
-// threshold goes on from the sums of a stretch's pieces, which its warps have kept, to the
-// token.
+// One cluster a sequence: every warp finds the row, sums its stretch of it in spans of 1 KB
+// of p and of q, and sends the sum round; the CTA whose stretches hold the threshold goes on
+// from the sums of a stretch's pieces, which its warps have kept, to the token.
 //
 // What bounds it: a small call its way through six dependent steps (bounds, drafted
 // tokens, their probabilities, the row, the sums of all, the search: one sequence, 32000
-// tokens, 5.3 us); a large one the loads under way, then DRAM (256 sequences, 128000 tokens,
-// up to 5 drafts, 190 MB: 47 us; 600 with 4 drafts, 614 MB: 98, 94 % of the copy rate), or,
-// with bf16 rows, the arithmetic (about 17 instructions a token: the same 256 sequences, 95
-// MB: 43 us).  Six CTAs of 256 threads an SM hide one another's steps better than three of
-// 512 (48 us) or four of 384 (46).  Not kept: loads one round ahead in registers (57 us),
-// acceptance in a kernel of its own (no gain), a search that sums the stretch again (5 us
-// more).
+// tokens, 5.3 us); a large one DRAM (256 sequences, 128000 tokens, up to 5 drafts, 190 MB:
+// 44 us; 450 with 3, 400 MB: 64, 93 % of the copy rate), or, with bf16 rows, the arithmetic
+// (about 17 instructions a token: the same 256 sequences, 95 MB: 36 us).  Spans come through
+// a ring in shared memory, two ahead, in 16 bytes wherever p and q start: with loads of words
+// into registers instead (six CTAs an SM, whose warps wait for their own loads) 450 sequences
+// took 70 us, 300 without drafts 37 (32 now), the 256 in bf16 43, of 150945 tokens 41 (35);
+// copies of words 57 us for the 256 in fp32.  Four CTAs an SM with two spans ahead: two of
+// three spans ahead 46, five with one 45 (and 52 for 450 without drafts, 45 now); spans of
+// half the size 52 and more, of twice 46.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -111,7 +111,7 @@ __device__ __forceinline__ u64 scan_warp(u64 x, int lane) {
   return x;
 }
 
-constexpr int kPieces = 64;  // sums of its stretch that a warp keeps
+constexpr int kPieces = 64;  // sums of its stretch that a warp keeps, of a span each or several
 
 // Two values' steps plus the constants' bits: a of the first, b of the second.
 __device__ __forceinline__ void steps(uint32_t lo, uint32_t hi, uint32_t (&a)[3], uint32_t (&b)[3]) {
@@ -160,70 +160,79 @@ struct Sums {
   }
 };
 
-// How a lane loads: fp32 values one by one, or bf16 values in aligned words of two; where q
-// starts in the other half of a word than p, its pairs are put together from two words.
+// Slots are a row's tokens counted from the 16 bytes on in which p starts: token t of it is
+// slot t + shift.  A warp takes spans of them, 1 KB of p and of q each, by asynchronous
+// copies of 16 bytes ahead of the sums.  In shared memory slot i's q is `off` elements
+// behind its p; words of two bf16 values come from two words where that is odd.
 enum : int { kF32 = 0, kBf16 = 1, kBf16Across = 2 };
-constexpr int U = 8;  // values or pairs a lane at a time
-template <bool BF16> constexpr int kSpan = BF16 ? 64 * U : 32 * U;  // tokens of a warp
+constexpr int U = 8;  // words of p, and of q, that a lane sums at a time
+template <bool BF16> constexpr int kEach = BF16 ? 8 : 4;            // elements in 16 bytes
+template <bool BF16> constexpr int kSpan = BF16 ? 64 * U : 32 * U;  // slots
+constexpr int kStages = 3;             // spans that a warp has room for
+constexpr int kSlot = 2 * 32 * U + 4;  // words of a span: 16 bytes more of q
 
-// Sum of the weights of slots [i, min(i + kSpan, i1)), in every lane of the warp.  Slots are
-// tokens counted from `shift` on: 1 where words are loaded and p's row starts with the second
-// half of one, 0 otherwise.
+__device__ __forceinline__ void copy_async(uint32_t smem, const void *gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+
+// Starts the copies for slots [i, min(i + kSpan, i1)).  Nothing is read from 16 bytes
+// without a token of the row.
+template <bool BF16, bool HAS_Q>
+__device__ __forceinline__ void load_span(const Row &r, int i, int i1, int shift, int off, int lane,
+                                          uint32_t *to) {
+  constexpr int E = kEach<BF16>, SIZE = 16 / E;
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to) + lane * 16;
+  // (16 bytes of p start where slot i does, those of q `off` elements before.)
+  const uint8_t *p = (const uint8_t *)r.p + ((int64_t)(i - shift) * SIZE + lane * 16);
+  const uint8_t *q = (const uint8_t *)r.q + ((int64_t)(i - shift - off) * SIZE + lane * 16);
+  const int end = min(i + kSpan<BF16>, i1);
+#pragma unroll
+  for (int k = 0; k < U / 4; ++k) {
+    const int t = i + (k * 32 + lane) * E;
+    if (t < end) copy_async(at + k * 512, p + k * 512);
+    if (HAS_Q && t - off < end && t - off + E > shift)
+      copy_async(at + U * 128 + k * 512, q + k * 512);
+  }
+  if (HAS_Q && lane == 0 && i + kSpan<BF16> - off < end) copy_async(at + U * 256, q + U * 128);
+}
+
+// Sum of the weights of slots [i, min(i + kSpan, i1)), in every lane of the warp, out of `from`.
 template <int HOW, bool HAS_Q>
-__device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int shift, int lane, bool &bad) {
-  constexpr bool BF16 = HOW != kF32, ACROSS = HOW == kBf16Across;
-  uint32_t x[U], y[U];
+__device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int shift, int off, int lane,
+                                        uint32_t *from, bool &bad) {
+  constexpr bool BF16 = HOW != kF32;
   Sums s;
   u64 sum = 0;
-  if constexpr (BF16) {
-    auto words = [&](const void *row, int back) {
-      return reinterpret_cast<const uint32_t *>((const uint16_t *)row - back) + (i >> 1) + lane;
-    };
-    const uint32_t *p = words(r.p, shift), *q = HAS_Q ? words(r.q, shift + ACROSS) : nullptr;
-    auto pair = [](uint32_t w, uint32_t next) { return __byte_perm(w, next, 0x5432); };
-    if (i >= shift && i + kSpan<BF16> <= i1) {
+  if (i < shift || i + kSpan<BF16> > i1) {  // what is no token of the stretch counts as 0
+    using Element = std::conditional_t<BF16, uint16_t, uint32_t>;
+    Element *p = reinterpret_cast<Element *>(from);
+    Element *q = reinterpret_cast<Element *>(from + U * 32) + off;
+    if (lane < shift - i) p[lane] = q[lane] = 0;
+#pragma unroll 1
+    for (int t = i1 - i + lane; t < kSpan<BF16>; t += 32) p[t] = q[t] = 0;
+    __syncwarp();
+  }
+  const uint32_t *x = from + lane, *y = x + U * 32 + (BF16 ? off >> 1 : off);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        x[u] = __ldg(p + u * 32);
-        y[u] = !HAS_Q ? 0u : ACROSS ? pair(__ldg(q + u * 32), __ldg(q + u * 32 + 1)) : __ldg(q + u * 32);
-      }
-    } else {  // (no word without a token of the row is loaded; half a neighbour is left out)
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = i + 2 * (u * 32 + lane);
-        const bool lo = t >= shift && t < i1, hi = t + 1 < i1;
-        const uint32_t keep = (lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u);
-        x[u] = lo || hi ? __ldg(p + u * 32) & keep : 0u;
-        if constexpr (ACROSS) y[u] = pair(lo ? __ldg(q + u * 32) : 0u, hi ? __ldg(q + u * 32 + 1) : 0u);
-        else y[u] = HAS_Q && (lo || hi) ? __ldg(q + u * 32) & keep : 0u;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+  for (int u = 0; u < U; ++u) {
+    if constexpr (BF16) {
       if (HAS_Q && u == U / 2) {
         sum = join(0, __reduce_add_sync(0xffffffffu, s.s2), 0);
         s.s2 = 0;
       }
+      const uint32_t p = x[u * 32];
       if constexpr (HAS_Q) {
-        s.difference(x[u] << 16, y[u] << 16);
-        s.difference(x[u] & 0xffff0000u, y[u] & 0xffff0000u);
+        uint32_t q = y[u * 32];
+        if (HOW == kBf16Across) q = __byte_perm(q, y[u * 32 + 1], 0x5432);
+        s.difference(p << 16, q << 16);
+        s.difference(p & 0xffff0000u, q & 0xffff0000u);
       } else {
-        s.both(x[u] << 16, x[u] & 0xffff0000u);
+        s.both(p << 16, p & 0xffff0000u);
       }
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = i + u * 32 + lane;
-      x[u] = t < i1 ? load_bits<BF16>(r.p, t) : 0u;
-      y[u] = HAS_Q && t < i1 ? load_bits<BF16>(r.q, t) : 0u;
-    }
-    if constexpr (HAS_Q) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) s.difference(x[u], y[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; u += 2) s.both(x[u], x[u + 1]);
+    } else if constexpr (HAS_Q) {
+      s.difference(x[u * 32], y[u * 32]);
+    } else if (u % 2 == 0) {
+      s.both(x[u * 32], x[u * 32 + 32]);
     }
   }
   if (__any_sync(0xffffffffu, s.most >= kValid)) {  // values to leave out: one by one
@@ -232,8 +241,7 @@ __device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int shift, 
       w += weight<BF16>(r, t - shift, bad);
     return sum_warp(w);
   }
-  if constexpr (BF16) sum += s.of_warp();
-  else sum = s.of_warp();
+  sum += s.of_warp();
   const int hole = r.hole + shift;
   if (r.hole < 0 || hole < i || hole >= min(i + kSpan<BF16>, i1)) return sum;
   bool noted = false;
@@ -243,12 +251,26 @@ __device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int shift, 
 // Sum of the weights of slots [i0, i1), in every lane, and of each `piece` of them.
 template <int HOW, bool HAS_Q>
 __device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int piece, u64 *pieces,
-                                           int shift, int lane, bool &bad) {
+                                           int shift, int off, int lane, uint32_t *ring, bool &bad) {
+  constexpr bool BF16 = HOW != kF32;
+  constexpr int SPAN = kSpan<BF16>;
+  auto load = [&](int i, int slot) {
+    if (i < i1) load_span<BF16, HAS_Q>(r, i, i1, shift, off, lane, ring + slot * kSlot);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   u64 sum = 0;
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) load(i0 + k * SPAN, k);
+  int slot = 0;
   for (int i = i0, k = 0; i < i1; ++k) {
     u64 part = 0;
-    for (const int end = min(i1, i + piece); i < end; i += kSpan<HOW != kF32>)
-      part += sum_span<HOW, HAS_Q>(r, i, i1, shift, lane, bad);
+    for (const int end = min(i1, i + piece); i < end; i += SPAN) {
+      load(i + (kStages - 1) * SPAN, slot == 0 ? kStages - 1 : slot - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      part += sum_span<HOW, HAS_Q>(r, i, i1, shift, off, lane, ring + slot * kSlot, bad);
+      slot = slot == kStages - 1 ? 0 : slot + 1;
+    }
     if (lane == 0) pieces[k] = part;
     sum += part;
   }
@@ -256,9 +278,10 @@ __device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int pie
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(NT, 6) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(NT, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ u64 sums[2][kMaxCluster * NW];  // of every warp of the cluster
   __shared__ u64 pieces[NW][kPieces];        // of this CTA's stretches
+  extern __shared__ __align__(16) uint32_t ring[];  // [NW][kStages][kSlot]
   const cg::cluster_group cluster = cg::this_cluster();
   cluster_started();
   const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -320,8 +343,11 @@ __global__ void __launch_bounds__(NT, 6) verify_kernel(const __grid_constant__ V
 
   cluster_wait();  // (the others' shared memory is there)
   const int all = n_cta * NW, mine = rank * NW + warp;
-  auto half = [](const void *row) { return (int)((uintptr_t)row >> 1 & 1); };
-  const int shift = BF16 ? half(row.p) : 0, slots = a.V + shift;
+  auto behind = [](const void *row) {  // elements from the 16 bytes on that it starts in
+    return (int)((uintptr_t)row / (16 / kEach<BF16>)) & (kEach<BF16> - 1);
+  };
+  const int shift = behind(row.p), off = (behind(row.q) - shift) & (kEach<BF16> - 1);
+  const int slots = a.V + shift;
   // Every warp's stretch, a multiple of 64 slots, and the slots of which it keeps the sum.
   const int len = ((slots + all - 1) / all + 63) & ~63;
   const int i0 = min(mine * len, slots), i1 = min(i0 + len, slots);
@@ -330,12 +356,14 @@ __global__ void __launch_bounds__(NT, 6) verify_kernel(const __grid_constant__ V
   int round = 0;
   while (true) {  // a second time only where p - q is 0 throughout
     auto sum_as = [&](auto how, auto has_q) {
-      return sum_stretch<how.value, has_q.value>(row, i0, i1, piece, pieces[warp], shift, lane, bad);
+      return sum_stretch<how.value, has_q.value>(row, i0, i1, piece, pieces[warp], shift, off, lane,
+                                                 ring + warp * (kStages * kSlot), bad);
     };
     using std::integral_constant;
     u64 stretch;
     if (!row.q) stretch = sum_as(integral_constant<int, BF16>{}, std::false_type{});
-    else if (BF16 && half(row.q) != shift) stretch = sum_as(integral_constant<int, BF16 ? kBf16Across : kF32>{}, std::true_type{});
+    else if (BF16 && (off & 1))
+      stretch = sum_as(integral_constant<int, BF16 ? kBf16Across : kF32>{}, std::true_type{});
     else stretch = sum_as(integral_constant<int, BF16>{}, std::true_type{});
     if (lane < n_cta) *cluster.map_shared_rank(&sums[round][mine], lane) = stretch;
     cluster.sync();
@@ -404,9 +432,10 @@ __global__ void __launch_bounds__(NT, 6) verify_kernel(const __grid_constant__ V
     lo += part * step;
     end = min(lo + step, end);
   }
-  constexpr int kEach = kSpan<BF16> / NT;
-  const int j = lo + kEach * tid;
-  const u64 w = j < end ? weight_at(j) : 0, all_w = w + (kEach == 2 && j + 1 < end ? weight_at(j + 1) : 0);
+  constexpr int ONE = kSpan<BF16> / NT;
+  const int j = lo + ONE * tid;
+  const u64 w = j < end ? weight_at(j) : 0;
+  const u64 all_w = w + (ONE == 2 && j + 1 < end ? weight_at(j + 1) : 0);
   const u64 of_warp = sum_warp(all_w);
   __syncthreads();
   if (lane == 0) sums[0][warp] = of_warp;
@@ -423,6 +452,11 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)a.n_seq * (unsigned)n_cta);
   cfg.blockDim = dim3(NT);
   cfg.stream = s;
+  constexpr int smem = NW * kStages * kSlot * (int)sizeof(uint32_t);
+  const cudaError_t e = cudaFuncSetAttribute(verify_kernel<BF16>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = (unsigned)n_cta;
@@ -435,15 +469,19 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
-  // CTAs a sequence: more while every warp has more than 256 tokens and all fit about three an
-  // SM (128000 tokens of one sequence: 38.8 us by one CTA, 9.0 by eight; 8000 of 300: 8.2 by
-  // one, 18.7 by eight), or six an SM, all that fit, where each still has 16000 tokens (128000 of
-  // 150: 39 by two, 30 by four, 33 by eight; 128000 of 310: 74 by one, 57 by two; 32000 of 400:
-  // 21.2 by one, 19.5 by two).
+  // CTAs a sequence: more while every warp has more than 256 tokens and
+  //  - there are few (128000 tokens of one sequence: 38.8 us by one CTA, 9.0 by eight; 8000 of
+  //    300: 8.2 by one, 18.7 by eight), or
+  //  - all fit at once, four an SM, and each still has 16000 tokens (32000 of 210: 16.7 by one,
+  //    14.2 by two; 50001 of 64: 10.7 by four, 11.3 by eight), or
+  //  - each still has 60000 probabilities, so that they even out (128000 of 256, with drafts:
+  //    47.2 by two, 44.1 by four, 46.7 by eight; of 300 without: 34.0 by one, 32.4 by two, 36.7
+  //    by four; 32000 of 400, with drafts: 22.1 by one, 21.9 by two, 24.2 by four).
   int n_cta = 1;
   while (n_cta < kMaxCluster && a.V > n_cta * NW * 256) {
     const int64_t ctas = (int64_t)n_cta * 2 * a.n_seq;
-    if (ctas > 400 && (ctas > 912 || a.V < 32000 * n_cta)) break;
+    const int each = a.V / (2 * n_cta);
+    if (ctas > 400 && (ctas > 608 || each < 16000) && each < (a.draft ? 30000 : 60000)) break;
     n_cta *= 2;
   }
   return a.bf16 ? launch<true>(a, n_cta, s) : launch<false>(a, n_cta, s);

@@ -78,6 +78,12 @@ def test_reserve(n, ps, max_kv, n_pages, share, grow):
         check_reserve(*batch(seed + n, n, ps, max_kv, n_pages, share, grow), ps, alias=seed == 1)
 
 
+def test_reserve_goes_on_in_place_behind_one_that_does_not_fit():
+    """The second needs no page: it grows, and the free pages stay free."""
+    got = check_reserve([1, 0, 1, 0], [[0, -1, -1, -1], [2, -1, -1, -1]], [4, 2], [16, 3], 4)
+    assert got[0] == [1, 0, 1, 0] and got[2] == [4, 3]
+
+
 def test_reserve_one_page_shared_by_all():
     # Parallel samples of one prompt: all but the last copy its last page.
     for n, n_pages in ((2, 4), (500, 600), (500, 200), (3000, 9000)):

@@ -106,6 +106,26 @@ def test_vocabularies_of_millions(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [3, 257, 1031, 20000])
+def test_rows_that_start_anywhere_in_sixteen_bytes(V, dtype):
+    """Target and draft as far from a border as each other or not, NaN all round."""
+    a = inputs(62, [1, 0, 2], V, dtype)
+    each = 16 // a["target"].element_size()
+    for at_p in range(each):
+        for at_q in range(each):
+            b = dict(a)
+            for name, at in (("target", at_p), ("draft", at_q)):
+                n = a[name].shape[0]
+                wide = torch.full((n, (V + 2 * each) // each * each), float("nan"), dtype=dtype, device=DEV)
+                wide[:, at:at + V] = a[name]
+                b[name] = wide[:, at:at + V]
+            check(b)
+            b["u_sample"] = torch.tensor([0.0, 1 - 2.0 ** -24, 0.0], device=DEV)
+            check(b)
+    no_error()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("p,q", [(5, 3), (7, 5), (2, 1), (9, 7), (6.5, 0.5)])
 @pytest.mark.parametrize("step", [2.0 ** -22, 2.0 ** -44])
 def test_constant_rows_halfway_between_steps(p, q, step, dtype):
