@@ -49,7 +49,7 @@ typedef unsigned long long u64;
 
 constexpr int NT = 256;
 constexpr int NW = NT / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t load_bits(const void *row, int64_t i) {  // as fp32 bits
@@ -456,6 +456,11 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(verify_kernel<BF16>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  if (n_cta > 8) {
+    const cudaError_t f = cudaFuncSetAttribute(verify_kernel<BF16>,
+                                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (f != cudaSuccess) return f;
+  }
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -470,17 +475,20 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
 
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
   // CTAs a sequence: more while every warp has more than 256 tokens and
-  //  - there are few (128000 tokens of one sequence: 38.8 us by one CTA, 9.0 by eight; 8000 of
+  //  - there are few (128000 tokens of one sequence: 38.8 us by one CTA, 8.4 by eight; 8000 of
   //    300: 8.2 by one, 18.7 by eight), or
   //  - all fit at once, four an SM, and each still has 16000 tokens (32000 of 210: 16.7 by one,
   //    14.2 by two; 50001 of 64: 10.7 by four, 11.3 by eight), or
   //  - each still has 60000 probabilities, so that they even out (128000 of 256, with drafts:
   //    47.2 by two, 44.1 by four, 46.7 by eight; of 300 without: 34.0 by one, 32.4 by two, 36.7
   //    by four; 32000 of 400, with drafts: 22.1 by one, 21.9 by two, 24.2 by four).
+  // Sixteen where there are few and 3000 tokens for each (128000 tokens of one: 8.4 by eight,
+  // 6.6 by sixteen; of 24: 11.2 and 10.3; 32000 of one in bf16: 5.7 and 6.2).
   int n_cta = 1;
   while (n_cta < kMaxCluster && a.V > n_cta * NW * 256) {
     const int64_t ctas = (int64_t)n_cta * 2 * a.n_seq;
     const int each = a.V / (2 * n_cta);
+    if (n_cta == 8 && (ctas > 400 || a.V < 48000)) break;
     if (ctas > 400 && (ctas > 608 || each < 16000) && each < (a.draft ? 30000 : 60000)) break;
     n_cta *= 2;
   }
