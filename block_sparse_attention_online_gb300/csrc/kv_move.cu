@@ -633,9 +633,15 @@ cudaError_t compact_ring(const CompactArgs &a, int64_t at_once, cudaStream_t s) 
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv * 2;
   // CTAs a cluster, until there are 128 of them: bf16, 8196 rows of 8 heads in one layer 70 us
-  // by one, 41, 22 and 17 by two, four and eight; in 8 layers 85, 97, 89 and 90.
+  // by one, 41, 22, 18 and 19.5 by two, four, eight and sixteen; of 4 heads 13.7 by eight, 11.6
+  // by sixteen, of one 13.6 and 8.9; in 8 layers 85 by one, 97, 89 and 90 by two to eight.
   int n_cta = 1;
-  while (n_cta < 8 && 2 * at_once * n_cta < 128) n_cta *= 2;
+  while (n_cta < 16 && 2 * at_once * n_cta < 128) n_cta *= 2;
+  if (n_cta > 8) {
+    const cudaError_t f = cudaFuncSetAttribute(
+        compact_ring_kernel<FMT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (f != cudaSuccess) return f;
+  }
   const int64_t clusters = a.few > 0 ? min(units, (int64_t)152 * 2 / n_cta) : units;
   if (clusters * n_cta > 0x7fffffff) return cudaErrorNotYetImplemented;
   cudaLaunchConfig_t cfg{};

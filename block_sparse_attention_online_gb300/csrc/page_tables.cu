@@ -17,7 +17,7 @@ namespace cg = cooperative_groups;
 
 constexpr int NT = 1024;  // threads a CTA of reserve
 constexpr int NW = NT / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kChunkWords = 8;  // words of 32 pages that a warp takes at a time
 constexpr int kMaxRounds = (1 << 20) / (kMaxCluster * NW * kChunkWords * 32);  // chunks of a warp
 
@@ -83,10 +83,10 @@ __host__ __device__ constexpr size_t seq_bytes(int n) { return ((size_t)n * 12 +
 //
 // Latency bounds it: some ten steps that wait for one another, half of them barriers (64
 // sequences, a pool of 20000 pages: 6.5 us; 1000 prompts, 48000 new pages of a pool of
-// 262144: 12.5 us, of which 2.3 to look at refs and 2.9 to hand out).  With a page's place
-// among the low ones deciding who hands it out, two of eight CTAs had all the work (46 us);
-// hence chunks go round the CTAs, and a word of 32 pages is handed out at a time, so that
-// neighbours write to neighbours.
+// 262144: 11.6 us; by eight CTAs 12.5, of which 2.3 to look at refs and 2.9 to hand out).
+// With a page's place among the low ones deciding who hands it out, two of eight CTAs had all
+// the work (46 us); hence chunks go round the CTAs, and a word of 32 pages is handed out at a
+// time, so that neighbours write to neighbours.
 __global__ void __launch_bounds__(NT, 1) reserve_kernel(const __grid_constant__ ReserveArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ long long tmp64[NW + 1];
@@ -415,17 +415,24 @@ size_t pages_reserve_max_seqs() { return 8192; }
 size_t pages_reserve_max_pages() { return (size_t)kMaxRounds * kMaxCluster * NW * kChunkWords * 32; }
 
 cudaError_t launch_pages_reserve(ReserveArgs a, cudaStream_t s) {
-  // A CTA alone looks at 8192 pages in one round, a cluster of eight at 65536 (pool of 8000
-  // pages, 16 sequences: 6.4 us by one CTA, 6.9 by eight; 20000 and 64: 8.1 and 7.2; 60000
-  // and 200: 12.9 and 9.3).
-  const int n_cta = a.n_pages > NW * kChunkWords * 32 ? kMaxCluster : 1;
-  const int per_round = n_cta * NW * kChunkWords * 32;
+  // A CTA alone looks at 8192 pages in one round, a cluster of eight at 65536, of sixteen at
+  // 131072 (pool of 8000 pages, 16 sequences: 6.4 us by one CTA, 6.9 by eight; 20000 and 64:
+  // 8.1 and 7.2; 60000 and 200: 12.9 and 9.3; by eight and by sixteen 60000 and 64: 6.4 and
+  // 6.9; 70000 and 200: 9.1 and 8.7; 262144 and 64: 9.2 and 8.2).
+  constexpr int kPages = NW * kChunkWords * 32;
+  const int n_cta = a.n_pages > 8 * kPages ? kMaxCluster : a.n_pages > kPages ? 8 : 1;
+  const int per_round = n_cta * kPages;
   a.rounds = (a.n_pages + per_round - 1) / per_round;
   const size_t smem = seq_bytes(a.n_seq) + hash_slots(a.n_seq) * 3 * sizeof(int) +
                       (size_t)a.rounds * NW * (kChunkWords * 4 + n_cta * 2);
   if (smem > 48 * 1024 - 1024) {  // (static shared memory counts too)
     const cudaError_t e = cudaFuncSetAttribute(
         reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  if (n_cta > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        reserve_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};
