@@ -265,9 +265,10 @@ __device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int pie
   for (int i = i0, k = 0; i < i1; ++k) {
     u64 part = 0;
     for (const int end = min(i1, i + piece); i < end; i += SPAN) {
+      __syncwarp();  // every lane is done with the span before, whose room is filled again
       load(i + (kStages - 1) * SPAN, slot == 0 ? kStages - 1 : slot - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      __syncwarp();
+      __syncwarp();  // every lane's copies are there
       part += sum_span<HOW, HAS_Q>(r, i, i1, shift, off, lane, ring + slot * kSlot, bad);
       slot = slot == kStages - 1 ? 0 : slot + 1;
     }
