@@ -24,14 +24,16 @@
 // What bounds it: a small call its way through six dependent steps (bounds, drafted
 // tokens, their probabilities, the row, the sums of all, the search: one sequence, 32000
 // tokens, 5.3 us); a large one DRAM (256 sequences, 128000 tokens, up to 5 drafts, 190 MB:
-// 44 us; 450 with 3, 400 MB: 64, 93 % of the copy rate), or, with bf16 rows, the arithmetic
-// (about 17 instructions a token: the same 256 sequences, 95 MB: 36 us).  Spans come through
-// a ring in shared memory, two ahead, in 16 bytes wherever p and q start: with loads of words
-// into registers instead (six CTAs an SM, whose warps wait for their own loads) 450 sequences
-// took 70 us, 300 without drafts 37 (32 now), the 256 in bf16 43, of 150945 tokens 41 (35);
-// copies of words 57 us for the 256 in fp32.  Four CTAs an SM with two spans ahead: two of
-// three spans ahead 46, five with one 45 (and 52 for 450 without drafts, 45 now); spans of
-// half the size 52 and more, of twice 46.
+// 44 us; 450 with 3, 400 MB: 64, 93 % of the copy rate), or, with bf16 rows, issue slots (72 %
+// of them, for 15 instructions a token and what a span and a cluster cost: the same 256
+// sequences, 95 MB: 36 us, 450 54).
+//
+// Spans come through a ring in shared memory, two ahead, in 16 bytes wherever p and q start.
+// With loads of words into registers instead (six CTAs an SM, whose warps wait for their own
+// loads) 450 sequences took 70 us, 300 without drafts 37 (32 now), the 256 in bf16 43, 248 of
+// 150945 tokens in bf16 41 (35); with copies of words the 256 in fp32 57.  Four CTAs an SM
+// with two spans ahead: two of three spans ahead 46, five with one 45 (and 450 without drafts
+// 52, 45 now); spans of half the size 52 and more, of twice 46.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>

@@ -344,3 +344,36 @@ def test_calls_on_two_streams_at_once():
         for tokens, accepted in runs:
             assert np.array_equal(tokens.cpu().numpy(), t) and np.array_equal(accepted.cpu().numpy(), n)
     no_error()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_few_long_rows_on_two_streams_and_in_graphs(dtype):
+    """Clusters of sixteen side by side, and replayed with other inputs."""
+    cases = [inputs(70 + i, [2, 0, 1], 100001, dtype) for i in range(2)]
+    wants = [want(a) for a in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [call(a) for a in cases]
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in cases]
+    for a, s, out, graph in zip(cases, streams, outs, graphs):
+        with torch.cuda.graph(graph, stream=s):
+            for _ in range(3):
+                call(a, out=out)
+    for again in range(2):
+        if again:  # the other's inputs of the same shape
+            for a, b in zip(cases, [{k: v.clone() for k, v in a.items() if torch.is_tensor(v)}
+                                    for a in reversed(cases)]):
+                for k, v in b.items():
+                    a[k].copy_(v)
+            wants = wants[::-1]
+        for out in outs:
+            out[0].fill_(-7)
+        torch.cuda.synchronize()
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                for _ in range(4):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for (tokens, accepted), (t, n) in zip(outs, wants):
+            assert np.array_equal(tokens.cpu().numpy(), t) and np.array_equal(accepted.cpu().numpy(), n)
+    no_error()
