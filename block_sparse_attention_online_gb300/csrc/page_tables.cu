@@ -411,7 +411,15 @@ __global__ void __launch_bounds__(FT) fork_kernel(const __grid_constant__ ForkAr
 
 }  // namespace
 
-size_t pages_reserve_max_seqs() { return 8192; }
+constexpr int kMaxSeqs = 8192;
+
+// Shared memory of a reserve by n_cta CTAs that look at refs in so many rounds.
+constexpr size_t reserve_bytes(int n_seq, int rounds, int n_cta) {
+  return seq_bytes(n_seq) + hash_slots(n_seq) * 3 * sizeof(int) +
+         (size_t)rounds * NW * (kChunkWords * 4 + n_cta * 2);
+}
+
+size_t pages_reserve_max_seqs() { return kMaxSeqs; }
 size_t pages_reserve_max_pages() { return (size_t)kMaxRounds * kMaxCluster * NW * kChunkWords * 32; }
 
 cudaError_t launch_pages_reserve(ReserveArgs a, cudaStream_t s) {
@@ -423,11 +431,13 @@ cudaError_t launch_pages_reserve(ReserveArgs a, cudaStream_t s) {
   const int n_cta = a.n_pages > 8 * kPages ? kMaxCluster : a.n_pages > kPages ? 8 : 1;
   const int per_round = n_cta * kPages;
   a.rounds = (a.n_pages + per_round - 1) / per_round;
-  const size_t smem = seq_bytes(a.n_seq) + hash_slots(a.n_seq) * 3 * sizeof(int) +
-                      (size_t)a.rounds * NW * (kChunkWords * 4 + n_cta * 2);
+  const size_t smem = reserve_bytes(a.n_seq, a.rounds, n_cta);
   if (smem > 48 * 1024 - 1024) {  // (static shared memory counts too)
+    // The kernel's limit is one for all threads of the program: whoever sets it sets the most
+    // that a call may need, so that no call lowers it under another's launch.
+    constexpr size_t most = reserve_bytes(kMaxSeqs, kMaxRounds, kMaxCluster);
     const cudaError_t e = cudaFuncSetAttribute(
-        reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
   }
   if (n_cta > 8) {
