@@ -88,3 +88,23 @@ def test_the_most_sequences_over_the_largest_pool():
     assert [x.tolist() for x in got] == list(want[2:5])
     assert sum(x >= 0 for x in want[3]) > 500 and any(a != b for a, b in zip(want[2], new))
     bs.attn_skip_last_device_error()
+
+
+def test_requests_of_more_than_two_to_the_31_pages():
+    """Ten sequences that ask for 2^28 pages each: none fits, and only those that ask for nothing
+    go on, before and behind the place where the requests' sum passes 32 bits."""
+    n, width = 13, 1 << 28
+    T = torch.empty((n, width), dtype=torch.int32, device=DEV)
+    T[:, :2] = -1
+    R = i32([0, 1, 0, 1, 0])
+    old, new = [0] * n, [width] * n
+    for s, page in ((1, 1), (12, 3)):  # these grow within their page
+        old[s], new[s] = 1, 2
+        T[s, 0] = page
+    old[11], new[11] = 4, 4  # and this one not at all
+    got, src, dst = bs.attn_skip_pages_reserve(R, T, i32(old), i32([4 * x if x == width else x for x in new]),
+                                               4)
+    assert got.tolist() == [new[s] if s in (1, 11, 12) else 0 for s in range(n)]
+    assert src.tolist() == dst.tolist() == [-1] * n and R.tolist() == [0, 1, 0, 1, 0]
+    assert T[:, :2].tolist() == [[{1: 1, 12: 3}.get(s, -1), -1] for s in range(n)]
+    bs.attn_skip_last_device_error()
