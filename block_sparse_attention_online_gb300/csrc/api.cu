@@ -805,6 +805,8 @@ extern "C" attn_status attn_skip_pages_reserve(int32_t *refs, int n_pages, int32
   if (!got_len || !copy_src || !copy_dst || !aligned4(got_len) || !aligned4(copy_src) ||
       !aligned4(copy_dst) || got_len == copy_src || got_len == copy_dst || copy_src == copy_dst)
     return ATTN_EINVAL;
+  for (const int32_t *in : {kv_len, new_len})  // (lengths are read again where copies are written)
+    if (copy_src == in || copy_dst == in) return ATTN_EINVAL;
   if ((size_t)n_seq > pages_reserve_max_seqs() || (size_t)n_pages > pages_reserve_max_pages() ||
       max_pages >= 1 << 30)  // (the kernel keeps a flag in bit 30 of an entry's number)
     return ATTN_EUNSUPPORTED;

@@ -713,7 +713,7 @@ int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, int total, in
  *  copy_src, copy_dst  [n_seq] int32 (device)
  *  page_size   at least 1
  * EINVAL: a null or misaligned (4 bytes) pointer, a size that is not positive, one
- * array for two outputs.
+ * array for two outputs, or for lengths and pages to copy.
  * Checked by the kernel and reported by attn_skip_last_device_error (ATTN_EINVAL):
  * a kv_len below 0, a new_len below kv_len or above max_pages * page_size, a partly
  * filled page's id out of range (the sequence stays as it is).
