@@ -749,6 +749,11 @@ extern "C" attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layer
                                             int out_max_pages, void *stream) {
   attn_status st = layers_check(kv, n_layers);
   if (st != ATTN_OK) return st;
+  // In place the rows of a cache that stands there twice would move twice.
+  const bool in_place = !out_table || out_table == page_table;
+  for (int i = 1; in_place && i < n_layers; ++i)
+    for (int j = 0; j < i; ++j)
+      if (kv[i].k == kv[j].k || kv[i].v == kv[j].v) return ATTN_EINVAL;
   KvPages p{};
   st = pages_check(kv, n_seq, total, cu_keep, page_table, max_pages, p);
   if (st != ATTN_OK) return st;
@@ -764,7 +769,7 @@ extern "C" attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layer
   a.n_seq = n_seq; a.total = total; a.max_pages = max_pages; a.out_max_pages = out_max_pages;
   a.per_head = per_head ? 1 : 0;
   a.cu_keep = cu_keep; a.keep = keep; a.start = start; a.table = page_table;
-  a.out_table = out_table == page_table ? nullptr : out_table;
+  a.out_table = in_place ? nullptr : out_table;
   const cudaError_t e = error_word(&a.err);
   if (e != cudaSuccess) return from_cuda(e);
   for (int i = 0; i < n_layers; i += kMaxLayers) {

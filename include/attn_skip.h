@@ -783,7 +783,8 @@ attn_status attn_skip_kv_copy_pages(const attn_kv_pages *kv, int n_layers, int n
  * ascending positions from start[s] on); other positions than start[s] .. are
  * left as they were.  The rows written must be no other sequence's (attn_skip_pages_reserve
  * gives a copy of the last page only), and with out_table none that is read.
- * EINVAL as for attn_skip_kv_append.  out_table = page_table is in place.  Left out
+ * EINVAL as for attn_skip_kv_append, for caches that differ, and in place for one cache
+ * twice (layers that share theirs).  out_table = page_table is in place.  Left out
  * and reported by attn_skip_last_device_error: sequences with bad bounds, rows of positions or
  * page ids out of range, in place rows with keep below their new position.
  */
