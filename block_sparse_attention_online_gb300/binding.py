@@ -995,8 +995,9 @@ def attn_skip_pages_reserve(refs, page_table, kv_len, new_len, page_size, out=No
     """Pages for sequences that grow from kv_len to new_len positions: refs
     [n_pages] and page_table [n_seq, max_pages] are updated.  Returns ``(got_len,
     copy_src, copy_dst)`` [n_seq] (or fills ``out``, whose got_len may be kv_len): the
-    length that each sequence now has room for (kv_len where the pages ran out) and
-    the pages to copy, for :func:`attn_skip_kv_copy_pages`.  All int32."""
+    length that each sequence now has room for (kv_len where the pages ran out: such a
+    sequence has no tokens in the step's chunk) and the pages to copy, for
+    :func:`attn_skip_kv_copy_pages`.  All int32."""
     on = _on(refs.get_device())
     if _elsewhere(on, stream):
         with _switched(on, stream):

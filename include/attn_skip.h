@@ -686,6 +686,14 @@ int attn_skip_chunk_paged_splits(attn_kv_format format, int n_seq, int total, in
  * attn_skip_chunk_paged in every layer, attn_skip_verify_drafts on the
  * target's probabilities, attn_skip_pages_fork without parents (back to the
  * accepted length).
+ *
+ * Where the pages run out, reserve leaves a sequence at its old length, and the step
+ * goes on without it: an empty chunk, no part in attn_skip_verify_drafts.  (With
+ * tokens in the chunk attn_skip_kv_append would write them over its last cached
+ * positions, in pages that others may share.)  So a program looks at got_len before
+ * it makes the chunk, unless it knows from a count of its own that the pages
+ * suffice: a sequence asks for at most ceil((new_len - kv_len) / page_size) + 1.  The
+ * copies are due in any case: the table names the new pages already.
  */
 
 /*
