@@ -113,6 +113,24 @@ __device__ __forceinline__ u64 scan_warp(u64 x, int lane) {
   return x;
 }
 
+// Rows that nobody has normalised may sum to 16 and more, past 64 bits: kTooMuch stands for
+// their sum.  A second, coarse sum finds them out, since the two differ by 16 for every time that
+// the first has wrapped.  A lane keeps it in steps of 2^-21, each value (or difference) to one
+// step, and stops at kCoarse, 1024: a row's 2^22 values of a warp, the most that there are, and a
+// token left out, leave it within a half of 16.  (One instruction a span.  By sums of 64 bits 450
+// rows of 128000 in bf16 took 55.2 us, like this 54.2, without any 53.9; in fp32 65.2, 64.7 and
+// 64.5; 300 without drafts 33.8, 33.8 and 33.0.)
+constexpr u64 kTooMuch = ~0ull;
+constexpr uint32_t kCoarse = 1u << 31;
+__device__ __forceinline__ void add_coarse(uint32_t &sum, uint32_t x) {
+  sum = __viaddmin_u32(sum, x, kCoarse);
+}
+__device__ __forceinline__ u64 unwrapped(u64 sum, uint32_t coarse) {
+  const u64 all = ((u64)__reduce_add_sync(0xffffffffu, coarse >> 16) << 16) +
+                  __reduce_add_sync(0xffffffffu, coarse & 0xffffu);
+  return ((int64_t)all - (int64_t)(sum >> 39) + (1 << 24)) >> 25 > 0 ? kTooMuch : sum;
+}
+
 constexpr int kPieces = 64;  // sums of its stretch that a warp keeps, of a span each or several
 
 // Two values' steps plus the constants' bits: a of the first, b of the second.
@@ -198,10 +216,11 @@ __device__ __forceinline__ void load_span(const Row &r, int i, int i1, int shift
   if (HAS_Q && lane == 0 && i + kSpan<BF16> - off < end) copy_async(at + U * 256, q + U * 128);
 }
 
-// Sum of the weights of slots [i, min(i + kSpan, i1)), in every lane of the warp, out of `from`.
+// Sum of the weights of slots [i, min(i + kSpan, i1)), in every lane of the warp, out of `from`;
+// a lane's `coarse` grows by the steps of its own.
 template <int HOW, bool HAS_Q>
 __device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int shift, int off, int lane,
-                                        uint32_t *from, bool &bad) {
+                                        uint32_t *from, uint32_t &coarse, bool &bad) {
   constexpr bool BF16 = HOW != kF32;
   Sums s;
   u64 sum = 0;
@@ -239,10 +258,16 @@ __device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int shift, 
   }
   if (__any_sync(0xffffffffu, s.most >= kValid)) {  // values to leave out: one by one
     u64 w = 0;
-    for (int t = max(i, shift) + lane; t < min(i + kSpan<BF16>, i1); t += 32)
-      w += weight<BF16>(r, t - shift, bad);
+    uint32_t c = 0;
+    for (int t = max(i, shift) + lane; t < min(i + kSpan<BF16>, i1); t += 32) {
+      const u64 one = weight<BF16>(r, t - shift, bad);
+      w += one;
+      c += (uint32_t)(one >> 39);
+    }
+    add_coarse(coarse, c);
     return sum_warp(w);
   }
+  add_coarse(coarse, s.s1);
   sum += s.of_warp();
   const int hole = r.hole + shift;
   if (r.hole < 0 || hole < i || hole >= min(i + kSpan<BF16>, i1)) return sum;
@@ -250,7 +275,8 @@ __device__ __forceinline__ u64 sum_span(const Row &r, int i, int i1, int shift, 
   return sum - units(load_bits<BF16>(r.p, r.hole), noted);
 }
 
-// Sum of the weights of slots [i0, i1), in every lane, and of each `piece` of them.
+// Sum of the weights of slots [i0, i1), in every lane, and of each `piece` of them (those mean
+// nothing where the sum is kTooMuch).
 template <int HOW, bool HAS_Q>
 __device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int piece, u64 *pieces,
                                            int shift, int off, int lane, uint32_t *ring, bool &bad) {
@@ -261,6 +287,7 @@ __device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int pie
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   u64 sum = 0;
+  uint32_t coarse = 0;
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) load(i0 + k * SPAN, k);
   int slot = 0;
@@ -271,13 +298,14 @@ __device__ __forceinline__ u64 sum_stretch(const Row &r, int i0, int i1, int pie
       load(i + (kStages - 1) * SPAN, slot == 0 ? kStages - 1 : slot - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();  // every lane's copies are there
-      part += sum_span<HOW, HAS_Q>(r, i, i1, shift, off, lane, ring + slot * kSlot, bad);
+      part += sum_span<HOW, HAS_Q>(r, i, i1, shift, off, lane, ring + slot * kSlot, coarse,
+                                   bad);
       slot = slot == kStages - 1 ? 0 : slot + 1;
     }
     if (lane == 0) pieces[k] = part;
     sum += part;
   }
-  return sum;
+  return unwrapped(sum, coarse);
 }
 
 template <bool BF16>
@@ -371,12 +399,17 @@ __global__ void __launch_bounds__(NT, 4) verify_kernel(const __grid_constant__ V
     if (lane < n_cta) *cluster.map_shared_rank(&sums[round][mine], lane) = stretch;
     cluster.sync();
     u64 before = 0, every = 0;
+    uint32_t tops = 0;
     for (int i = lane; i < all; i += 32) {
       const u64 v = sums[round][i];
       every += v;
+      tops += (uint32_t)(v >> 44);
       before += i < rank * NW ? v : 0;
     }
     total = sum_warp(every);
+    // (Whether this sum has wrapped, by its terms' bits from 2^44 on.)
+    tops = __reduce_add_sync(0xffffffffu, tops);
+    if ((int)(tops - (uint32_t)(total >> 44) + (1u << 19)) >> 20 > 0) total = kTooMuch;
     below = sum_warp(before);
     if (round == 1 || total || acc == n) break;
     round = 1;
@@ -394,8 +427,9 @@ __global__ void __launch_bounds__(NT, 4) verify_kernel(const __grid_constant__ V
       if (i != acc) out[i] = i < acc ? a.drafted[c0 + i] : -1;
   if (rank == 0 && tid == 0) {
     a.n_accepted[s] = acc;
-    if (!total) out[acc] = a.V - 1;
+    if (!total || total == kTooMuch) out[acc] = a.V - 1;
   }
+  if (total == kTooMuch) return;
   // The CTA whose stretches hold the threshold looks up the warp's, then the piece of it;
   // parts of that, where it is long, are summed again, until a load a thread is left.
   // `find`: which of n sums holds it; below becomes the sum before.
@@ -411,7 +445,7 @@ __global__ void __launch_bounds__(NT, 4) verify_kernel(const __grid_constant__ V
     }
     return -1;
   };
-  // (The same for the whole CTA.  Rows that sum to 16 and more may be found nowhere.)
+  // (The same for the whole CTA.)
   const int holder = find(&sums[round][rank * NW], NW);
   if (holder < 0) return;
   const int first = (rank * NW + holder) * len;

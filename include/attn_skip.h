@@ -814,15 +814,14 @@ attn_status attn_skip_kv_compact(const attn_kv_pages *kv, int n_layers, int n_se
  *    where that is zero throughout), with all accepted from p_n;
  *  - a draw is the smallest t with w_0 + .. + w_t > u * (w_0 + .. + w_{V-1}), the
  *    weights w made of p and q rounded to multiples of 2^-60 and their sums exact.
- * A row whose weights are all zero gives token V - 1.
+ * A row whose weights are all zero, or sum to 16 or more, gives token V - 1.
  *
  *  target     [total + n_seq, V] (dt), rows target_stride elements apart: p_i of
  *             sequence s is row cu_drafts[s] + s + i
  *  draft      [total, V] (dt), rows draft_stride elements apart, or NULL: the
  *             drafted tokens are not random (a look-up, an argmax), q_i(x_i) = 1
  *  dt         ATTN_F32 or ATTN_BF16; rows need no more than their elements'
- *             alignment.  Probabilities lie in [0, 2), rows sum to about one (to
- *             less than 16)
+ *             alignment.  Probabilities lie in [0, 2), rows sum to about one
  *  drafted    [total] int32, u_accept [total] fp32, u_sample [n_seq] fp32,
  *             cu_drafts [n_seq + 1] int32 (device); tokens before cu_drafts[0]
  *             and from cu_drafts[n_seq] on are ignored.  n = 0 samples one token
