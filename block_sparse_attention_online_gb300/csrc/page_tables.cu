@@ -321,7 +321,10 @@ __global__ void __launch_bounds__(FT) fork_kernel(const __grid_constant__ ForkAr
       if (e0 != tid) load(e0);
 #pragma unroll
       for (int i = 0; i < kEntries; ++i)
-        if (e0 + i * FT < n) to[e0 + i * FT] = p[i];
+        if (e0 + i * FT < n) {
+          to[e0 + i * FT] = p[i];
+          bad |= p[i] < 0 || p[i] >= a.n_pages;  // (counts may stay, so that nobody else looks)
+        }
     }
   } else {
     const int s = blockIdx.x - n_new;

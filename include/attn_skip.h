@@ -751,7 +751,8 @@ attn_status attn_skip_pages_reserve(int32_t *refs, int n_pages, int32_t *page_ta
  * Errors as for attn_skip_pages_reserve.  Reported by attn_skip_last_device_error:
  * a parent outside [-1, n_seq) or one of -1 with a length (an empty sequence), a
  * new_len out of range (the nearest length in range counts), a kv_len outside
- * [0, max_pages * page_size] (treated as 0), a page id out of range (not counted).
+ * [0, max_pages * page_size] (treated as 0), a page id out of range (handed on as it is, not
+ * counted; without parents only the entries that are cut off are looked at).
  */
 attn_status attn_skip_pages_fork(int32_t *refs, int n_pages, const int32_t *page_table, int n_seq,
                                  int max_pages, int page_size, const int32_t *kv_len,
