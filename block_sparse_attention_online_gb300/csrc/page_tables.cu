@@ -222,9 +222,9 @@ __global__ void __launch_bounds__(NT, 1) reserve_kernel(const __grid_constant__ 
   for (int s = rank * NT + tid; s < n; s += n_cta * NT) {
     const int page = q.page[s], upto = q.begin[s + 1];
     const int new_len = a.new_len[s];
-    // (By the length: sums that have reached INT_MAX do not say who asks for nothing.)
-    const bool none = page == -1 && pages_of(new_len, ps) == q.first[s];
-    const bool served = page != -2 && (upto <= n_free || none);
+    bool served = page != -2;
+    if (upto > n_free)  // who asks for nothing (by the length: sums stop at INT_MAX)
+      served = page == -1 && pages_of(new_len, ps) == q.first[s];
     const bool cow = served && (q.first[s] & kCopy);
     a.got_len[s] = served ? new_len : a.kv_len[s];
     a.copy_src[s] = cow ? page : -1;
