@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "cluster.cuh"
+#include "cluster_size.h"
 #include "internal.h"
 
 namespace attn_skip {
@@ -636,12 +637,11 @@ cudaError_t compact_ring(const CompactArgs &a, int64_t at_once, cudaStream_t s) 
   // by one, 41, 22, 18 and 19.5 by two, four, eight and sixteen; of 4 heads 13.7 by eight, 11.6
   // by sixteen, of one 13.6 and 8.9; in 8 layers 85 by one, 97, 89 and 90 by two to eight.
   int n_cta = 1;
-  while (n_cta < 16 && 2 * at_once * n_cta < 128) n_cta *= 2;
-  if (n_cta > 8) {
-    const cudaError_t f = cudaFuncSetAttribute(
-        compact_ring_kernel<FMT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (f != cudaSuccess) return f;
-  }
+  while (n_cta < kLargeCluster && 2 * at_once * n_cta < 128) n_cta *= 2;
+  static ClusterRoom room;
+  if (n_cta == kLargeCluster &&
+      !large_cluster_fits((const void *)compact_ring_kernel<FMT>, NT, smem, room))
+    n_cta = kPortableCluster;
   const int64_t clusters = a.few > 0 ? min(units, (int64_t)152 * 2 / n_cta) : units;
   if (clusters * n_cta > 0x7fffffff) return cudaErrorNotYetImplemented;
   cudaLaunchConfig_t cfg{};

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "cluster.cuh"
+#include "cluster_size.h"
 #include "internal.h"
 
 namespace attn_skip {
@@ -17,7 +18,7 @@ namespace cg = cooperative_groups;
 
 constexpr int NT = 1024;  // threads a CTA of reserve
 constexpr int NW = NT / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = kLargeCluster;
 constexpr int kChunkWords = 8;  // words of 32 pages that a warp takes at a time
 constexpr int kMaxRounds = (1 << 20) / (kMaxCluster * NW * kChunkWords * 32);  // chunks of a warp
 
@@ -434,21 +435,27 @@ cudaError_t launch_pages_reserve(ReserveArgs a, cudaStream_t s) {
   // 8.1 and 7.2; 60000 and 200: 12.9 and 9.3; by eight and by sixteen 60000 and 64: 6.4 and
   // 6.9; 70000 and 200: 9.1 and 8.7; 262144 and 64: 9.2 and 8.2).
   constexpr int kPages = NW * kChunkWords * 32;
-  const int n_cta = a.n_pages > 8 * kPages ? kMaxCluster : a.n_pages > kPages ? 8 : 1;
+  // The kernel's limit of shared memory is one for all threads of the program: whoever sets it
+  // sets the most that a call may need, so that no call lowers it under another's launch.
+  constexpr size_t most = reserve_bytes(kMaxSeqs, 2 * kMaxRounds, kPortableCluster);
+  static_assert(most >= reserve_bytes(kMaxSeqs, kMaxRounds, kMaxCluster), "by sixteen too");
+  auto allow = [] {
+    return cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)most);
+  };
+  const bool large = a.n_pages > 8 * kPages;
+  int n_cta = a.n_pages > kPages ? kPortableCluster : 1;
+  if (large) {
+    static ClusterRoom room;
+    const cudaError_t e = allow();
+    if (e != cudaSuccess) return e;
+    if (large_cluster_fits((const void *)reserve_kernel, NT, most, room)) n_cta = kMaxCluster;
+  }
   const int per_round = n_cta * kPages;
   a.rounds = (a.n_pages + per_round - 1) / per_round;
   const size_t smem = reserve_bytes(a.n_seq, a.rounds, n_cta);
-  if (smem > 48 * 1024 - 1024) {  // (static shared memory counts too)
-    // The kernel's limit is one for all threads of the program: whoever sets it sets the most
-    // that a call may need, so that no call lowers it under another's launch.
-    constexpr size_t most = reserve_bytes(kMaxSeqs, kMaxRounds, kMaxCluster);
-    const cudaError_t e = cudaFuncSetAttribute(
-        reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-    if (e != cudaSuccess) return e;
-  }
-  if (n_cta > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        reserve_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (!large && smem > 48 * 1024 - 1024) {  // (static shared memory counts too)
+    const cudaError_t e = allow();
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};

@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "cluster.cuh"
+#include "cluster_size.h"
 #include "internal.h"
 #include "tc_common.cuh"
 
@@ -51,7 +52,7 @@ typedef unsigned long long u64;
 
 constexpr int NT = 256;
 constexpr int NW = NT / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = kLargeCluster;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t load_bits(const void *row, int64_t i) {  // as fp32 bits
@@ -485,20 +486,19 @@ __global__ void __launch_bounds__(NT, 4) verify_kernel(const __grid_constant__ V
 
 template <bool BF16>
 cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)a.n_seq * (unsigned)n_cta);
-  cfg.blockDim = dim3(NT);
-  cfg.stream = s;
   constexpr int smem = NW * kStages * kSlot * (int)sizeof(uint32_t);
   const cudaError_t e = cudaFuncSetAttribute(verify_kernel<BF16>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  if (n_cta > 8) {
-    const cudaError_t f = cudaFuncSetAttribute(verify_kernel<BF16>,
-                                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (f != cudaSuccess) return f;
-  }
+  static ClusterRoom room;
+  if (n_cta == kLargeCluster &&
+      !large_cluster_fits((const void *)verify_kernel<BF16>, NT, smem, room))
+    n_cta = kPortableCluster;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.n_seq * (unsigned)n_cta);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = (unsigned)n_cta;
