@@ -332,21 +332,49 @@ __device__ __forceinline__ void move_rows(const CompactArgs &a, int layer, int h
   }
 }
 
+// Bounds that do not ascend: a row may be of several sequences, and a search for one of them may
+// find none.  The rows of every sequence with good bounds, in one (layer, head), by one CTA; what
+// others move too comes out the same.
+template <int FMT>
+__device__ __noinline__ void compact_out_each(const CompactArgs &a, int layer, int h, Move *at) {
+  const int t = threadIdx.x, head_row = h * a.kv.page_size;
+  bool bad = true;
+  for (int s = 0; s < a.n_seq; ++s) {
+    const int c0 = a.cu_keep[s], c1 = a.cu_keep[s + 1];
+    if (!good_bounds(a, c0, c1)) continue;
+    const Unit x = unit_of(a, s, h, c0, c1);
+    for (int j0 = 0; j0 < x.n; j0 += NT) {
+      Place mine = kNowhere;
+      if (j0 + t < x.n) mine = place_of(a, x, j0 + t, x.keep[j0 + t], bad);
+      check_place(a, mine, bad);
+      __syncthreads();  // the rows before are done with the places
+      at[t] = move_of<RowBytes<FMT>::value>(a, mine, head_row);
+      __syncthreads();
+      move_rows<FMT, NT, 4>(a, layer, head_row, at, mine, t, min(NT, x.n - j0), [] {});
+    }
+  }
+  atomicOr(a.err, kErrBadArg);
+}
+
 // Into other pages: one CTA for 256 rows of the batch in one (layer, head), whatever
-// sequences they are of, and one that looks at all bounds.  11000 rows of 4 heads in 4
-// layers, NVFP4: 7.2 us, 5.4 for the bytes; 8196 of 8 heads in 8 layers, bf16: 83 us, 80 for
+// sequences they are of, and one that looks at all bounds for it.  11000 rows of 4 heads in 4
+// layers, NVFP4: 6.6 us, 5.4 for the bytes; 8196 of 8 heads in 8 layers, bf16: 83 us, 80 for
 // the bytes.  (A CTA a stretch of one sequence in turn: 10 and 85 us.)
 template <int FMT>
 __global__ void __launch_bounds__(NT, 4) compact_out_kernel(const __grid_constant__ CompactArgs a) {
   __shared__ Move at[NT];
   const int t = threadIdx.x;
   bool bad = false;
-  if (blockIdx.x == gridDim.x - 1) {
+  unsigned i = blockIdx.x;
+  const unsigned units = (unsigned)(a.kv.n * a.kv.Hkv), look = gridDim.x - units;
+  if (i >= look) {
     for (int s = t; s < a.n_seq; s += NT) bad |= !good_bounds(a, a.cu_keep[s], a.cu_keep[s + 1]);
-    if (bad) atomicOr(a.err, kErrBadArg);
+    if (!__syncthreads_or(bad)) return;
+    i -= look;
+    const int h = take(i, (unsigned)a.kv.Hkv);
+    compact_out_each<FMT>(a, (int)i, h, at);
     return;
   }
-  unsigned i = blockIdx.x;
   const int j0 = take(i, (unsigned)((a.total + NT - 1) / NT)) * NT, h = take(i, (unsigned)a.kv.Hkv);
   const int layer = (int)i, row = j0 + t;
   const int head_row = h * a.kv.page_size;
@@ -662,7 +690,7 @@ template <int FMT>
 cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
   const int64_t units = (int64_t)a.kv.n * a.n_seq * a.kv.Hkv;
   if (a.out_table) {
-    const int64_t grid = (int64_t)a.kv.n * a.kv.Hkv * ((a.total + NT - 1) / NT) + 1;
+    const int64_t grid = (int64_t)a.kv.n * a.kv.Hkv * ((a.total + NT - 1) / NT + 1);
     if (grid > 0x7fffffff) return cudaErrorNotYetImplemented;
     compact_out_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
     return cudaGetLastError();
