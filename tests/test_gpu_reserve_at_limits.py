@@ -108,3 +108,27 @@ def test_requests_of_more_than_two_to_the_31_pages():
     assert src.tolist() == dst.tolist() == [-1] * n and R.tolist() == [0, 1, 0, 1, 0]
     assert T[:, :2].tolist() == [[{1: 1, 12: 3}.get(s, -1), -1] for s in range(n)]
     bs.attn_skip_last_device_error()
+
+
+@pytest.mark.parametrize("n,n_pages,copies", [
+    (2, 4, 1), (3000, 9000, 2999),     # all but the last holder
+    (500, 600, 399), (500, 200, 132),  # as far as the free pages go: three for every two sequences
+])
+def test_copies_of_one_shared_page(n, n_pages, copies):
+    """Samples of one prompt of 20 positions, pages of 16; every other one grows into a new page."""
+    R = torch.zeros(n_pages, dtype=torch.int32, device=DEV)
+    R[1] = R[n_pages - 1] = n
+    T = i32([[n_pages - 1, 1, -1]] * n)
+    new = [21 + 15 * (s % 2) for s in range(n)]
+    got, src, dst = bs.attn_skip_pages_reserve(R, T, i32([20] * n), i32(new), 16)
+    assert src.tolist() == [1] * copies + [-1] * (n - copies)
+    taken = [p for p in range(n_pages - 1) if p != 1]
+    # Sequence s copies to its first page; an odd one then takes another.
+    first = [3 * (s // 2) + s % 2 for s in range(copies)]
+    assert dst.tolist() == [taken[i] for i in first] + [-1] * (n - copies)
+    assert R[1] == n - copies and R[n_pages - 1] == n
+    served = n if copies == n - 1 else copies
+    assert got.tolist() == new[:served] + [20] * (n - served)
+    assert T[:copies, 1].tolist() == [taken[i] for i in first]
+    assert (T[copies:, 1] == 1).all()
+    bs.attn_skip_last_device_error()
