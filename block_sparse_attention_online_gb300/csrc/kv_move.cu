@@ -718,7 +718,7 @@ cudaError_t compact_fmt(CompactArgs &a, cudaStream_t s) {
   // us, 111 without; in vain 2 to 3 us).
   const int64_t lone = (int64_t)a.kv.n * a.kv.Hkv;
   const bool rings = lone <= 64 && a.total > 4096;
-  if (rings) a.many = max(1024, a.total / 2);
+  if (rings) a.many = a.total / 2;  // (one sequence at most keeps more)
   const int64_t grid = a.few > 0 ? min(units, (int64_t)152 * 4) : units;
   compact_cta_kernel<FMT><<<(unsigned)grid, NT, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
