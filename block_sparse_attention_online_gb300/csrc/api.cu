@@ -565,6 +565,7 @@ attn_status pages_check(const attn_kv_pages *kv, int n_seq, int total, const int
   const attn_status st = cache_check(kv, p);
   if (st != ATTN_OK) return st;
   if ((int64_t)max_pages * kv->page_size > kMaxPositions) return ATTN_EUNSUPPORTED;
+  if (n_seq > kMaxPositions) return ATTN_EUNSUPPORTED;  // (int loops by a block's threads)
   if (!aligned4(cu) || !aligned4(page_table)) return ATTN_EINVAL;
   return ATTN_OK;
 }
@@ -727,6 +728,7 @@ extern "C" attn_status attn_skip_kv_copy_pages(const attn_kv_pages *kv, int n_la
   if (st != ATTN_OK) return st;
   if (n_pairs < 0) return ATTN_EINVAL;
   if ((int64_t)kv->Hkv * kv->page_size > 1 << 24) return ATTN_EUNSUPPORTED;  // int vectors of a page
+  if (n_pairs > kMaxPositions) return ATTN_EUNSUPPORTED;
   if (n_pairs == 0) return ATTN_OK;
   if (!src || !dst || !aligned4(src) || !aligned4(dst)) return ATTN_EINVAL;
   CopyPagesArgs a{};

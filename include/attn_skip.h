@@ -527,6 +527,7 @@ attn_status attn_skip_santa_decode_noalloc(const void *q, const void *k, const v
  *  page_size    16, 32, 64 or a multiple of 128; d = 128
  * Page tables are int32 [n_seq, max_pages] on the device: position p of
  * sequence s is slot p % page_size of page page_table[s, p / page_size].
+ * At most 2^30 sequences, and 2^30 positions of each, are supported.
  * All of the table has to be readable; entries behind a sequence's last position
  * may hold anything, and may change during a call: they have no effect.
  */
@@ -770,7 +771,7 @@ attn_status attn_skip_pages_fork(int32_t *refs, int n_pages, const int32_t *page
  * one writes and another reads, holds a mixture.  EINVAL as for
  * attn_skip_kv_append, for caches that differ and n_pairs < 0; a page id below -1
  * or not below n_pages is left out and reported by attn_skip_last_device_error.  Pages of
- * more than 2^24 rows (of all heads) are EUNSUPPORTED.
+ * more than 2^24 rows (of all heads) and more than 2^30 pairs are EUNSUPPORTED.
  */
 attn_status attn_skip_kv_copy_pages(const attn_kv_pages *kv, int n_layers, int n_pairs,
                                     const int32_t *src, const int32_t *dst, void *stream);

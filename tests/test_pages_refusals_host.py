@@ -3,7 +3,7 @@ another (on the host: no call here reaches a launch)."""
 import pytest
 
 from block_sparse_attention_online_gb300 import binding as bs
-from tests.test_paged_host import pages
+from tests.test_paged_host import append, chunk, gather, pages
 from tests.test_pages_host import A, compact, copy, layers, lib, reserve  # noqa: F401 (lib: the fixture)
 
 
@@ -33,3 +33,14 @@ def test_compact_rejects_a_cache_that_stands_there_twice(lib, again):  # noqa: F
     assert compact(lib, kv=layers(one, other, twice), n=3, out=2 * A, out_pages=4,
                    **many) == bs.ATTN_EUNSUPPORTED
     assert copy(lib, kv=layers(one, other, twice), n=3, pairs=0) == bs.ATTN_OK
+
+
+@pytest.mark.parametrize("number", [(1 << 30) + 1, (1 << 31) - 1])
+def test_numbers_beyond_int_loops(lib, number):  # noqa: F811
+    """A block's threads step through pairs and sequences by its size: beyond 2^31 less that much
+    the step would wrap."""
+    one = dict(kv=layers(pages(Hkv=1)))
+    assert copy(lib, **one, pairs=number) == bs.ATTN_EUNSUPPORTED
+    assert compact(lib, **one, n_seq=number) == bs.ATTN_EUNSUPPORTED
+    for call in (append, gather, chunk):
+        assert call(lib, n_seq=number, total=0) == bs.ATTN_EUNSUPPORTED
