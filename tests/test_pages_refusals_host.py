@@ -26,7 +26,10 @@ def test_compact_rejects_a_cache_that_stands_there_twice(lib, again):  # noqa: F
     one, other = pages(k=2 * A, v=3 * A), pages(k=5 * A, v=6 * A)
     twice = pages(**dict(dict(k=2 * A, v=3 * A), **again))
     assert compact(lib, kv=layers(one, other, twice), n=3) == bs.ATTN_EINVAL
+    assert compact(lib, kv=layers(other, one, twice), n=3) == bs.ATTN_EINVAL
+    assert compact(lib, kv=layers(other, twice, one), n=3) == bs.ATTN_EINVAL
     many = dict(n_seq=1 << 30)
+    assert compact(lib, kv=layers(other, one), n=2, **many) == bs.ATTN_EUNSUPPORTED
     assert compact(lib, kv=layers(one, other), n=2, **many) == bs.ATTN_EUNSUPPORTED
     assert compact(lib, kv=layers(one, other, twice), n=3, out=A) == bs.ATTN_EINVAL  # (its table)
     # Rows that go to other pages, and whole pages, may go twice.
