@@ -526,7 +526,9 @@ __device__ __forceinline__ void compact_unit(const CompactArgs &a, const Unit &x
   // The barrier orders the loads of one CTA before the stores of another.  The loads are
   // complete when their thread arrives (copies have been waited for, scales written down),
   // and the wait keeps the stores behind it, so that the cluster's barrier has nothing to
-  // release: that would wait for the thread's earlier stores too, 0.6 us a chunk.
+  // release: that would wait for the thread's earlier stores too, 0.6 us a chunk.  (The memory
+  // model speaks of a release here; that a load whose value is in hand sees no store made after
+  // it is a matter of the machine that this is written for.)
   auto sync = [&] {
     if (n_cta == 1) {
       __syncthreads();

@@ -30,10 +30,10 @@
 //
 // Spans come through a ring in shared memory, two ahead, in 16 bytes wherever p and q start.
 // With loads of words into registers instead (six CTAs an SM, whose warps wait for their own
-// loads) 450 sequences took 70 us, 300 without drafts 37 (32 now), the 256 in bf16 43, 248 of
+// loads) 450 sequences took 70 us, 300 without drafts 37 (33 now), the 256 in bf16 43, 248 of
 // 150945 tokens in bf16 41 (35); with copies of words the 256 in fp32 57.  Four CTAs an SM
 // with two spans ahead: two of three spans ahead 46, five with one 45 (and 450 without drafts
-// 52, 45 now); spans of half the size 52 and more, of twice 46.
+// 52, 47 now); spans of half the size 52 and more, of twice 46.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -521,6 +521,7 @@ cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
   //    by four; 32000 of 400, with drafts: 22.1 by one, 21.9 by two, 24.2 by four).
   // Sixteen where there are few and 3000 tokens for each (128000 tokens of one: 8.4 by eight,
   // 6.6 by sixteen; of 24: 11.2 and 10.3; 32000 of one in bf16: 5.7 and 6.2).
+  // (Taken without the coarse sums, which add up to 2 % to all of them.)
   int n_cta = 1;
   while (n_cta < kMaxCluster && a.V > n_cta * NW * 256) {
     const int64_t ctas = (int64_t)n_cta * 2 * a.n_seq;
