@@ -4,28 +4,14 @@
 
 #include <cuda_runtime_api.h>
 
-#include <atomic>
-
 namespace attn_skip {
 
 constexpr int kLargeCluster = 16, kPortableCluster = 8;
 
-// What a kernel's callers have found out, by device: 0 not asked yet, 1 there is room, -1 not.
-struct ClusterRoom {
-  static constexpr int kDevices = 64;
-  std::atomic<signed char> known[kDevices];
-};
-
-// Allows `kernel` clusters of kLargeCluster and says whether the current device has room for one.
-// The device is asked once (with the most shared memory that a launch takes, which has to be
-// allowed already).
-inline bool large_cluster_fits(const void *kernel, int threads, size_t smem, ClusterRoom &room) {
-  int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess) return false;
-  std::atomic<signed char> *known =
-      device < ClusterRoom::kDevices ? &room.known[device] : nullptr;
-  if (known)
-    if (const signed char k = known->load(std::memory_order_relaxed)) return k > 0;
+// Allows `kernel` clusters of kLargeCluster and says whether there is room for one, with so much
+// shared memory (which has to be allowed already).  Asked by every call, since the answer is the
+// current context's: 0.4 us of host time.
+inline bool large_cluster_fits(const void *kernel, int threads, size_t smem) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(kLargeCluster);
   cfg.blockDim = dim3((unsigned)threads);
@@ -42,7 +28,6 @@ inline bool large_cluster_fits(const void *kernel, int threads, size_t smem, Clu
           cudaSuccess &&
       cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
   if (!fits) (void)cudaGetLastError();  // (it is no error of the call's: eight will do)
-  if (known) known->store(fits ? 1 : -1, std::memory_order_relaxed);
   return fits;
 }
 

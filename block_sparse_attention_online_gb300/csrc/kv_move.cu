@@ -668,9 +668,8 @@ cudaError_t compact_ring(const CompactArgs &a, int64_t at_once, cudaStream_t s) 
   // by sixteen, of one 13.6 and 8.9; in 8 layers 85 by one, 97, 89 and 90 by two to eight.
   int n_cta = 1;
   while (n_cta < kLargeCluster && 2 * at_once * n_cta < 128) n_cta *= 2;
-  static ClusterRoom room;
   if (n_cta == kLargeCluster &&
-      !large_cluster_fits((const void *)compact_ring_kernel<FMT>, NT, smem, room))
+      !large_cluster_fits((const void *)compact_ring_kernel<FMT>, NT, smem))
     n_cta = kPortableCluster;
   const int64_t clusters = a.few > 0 ? min(units, (int64_t)152 * 2 / n_cta) : units;
   if (clusters * n_cta > 0x7fffffff) return cudaErrorNotYetImplemented;

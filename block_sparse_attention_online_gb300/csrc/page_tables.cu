@@ -446,23 +446,19 @@ cudaError_t launch_pages_reserve(ReserveArgs a, cudaStream_t s) {
   };
   const bool large = a.n_pages > 8 * kPages;
   int n_cta = a.n_pages > kPages ? kPortableCluster : 1;
-  if (large) {
-    static ClusterRoom room;
-    const cudaError_t e = allow();
-    if (e != cudaSuccess) return e;
-    if (large_cluster_fits((const void *)reserve_kernel, NT, most, room)) n_cta = kMaxCluster;
-  }
-  const int per_round = n_cta * kPages;
-  a.rounds = (a.n_pages + per_round - 1) / per_round;
-  const size_t smem = reserve_bytes(a.n_seq, a.rounds, n_cta);
-  if (!large && smem > 48 * 1024 - 1024) {  // (static shared memory counts too)
+  auto rounds_by = [&](int n) { return (a.n_pages + n * kPages - 1) / (n * kPages); };
+  auto bytes_by = [&](int n) { return reserve_bytes(a.n_seq, rounds_by(n), n); };
+  if (large || bytes_by(n_cta) > 48 * 1024 - 1024) {  // (static shared memory counts too)
     const cudaError_t e = allow();
     if (e != cudaSuccess) return e;
   }
+  if (large && large_cluster_fits((const void *)reserve_kernel, NT, bytes_by(kMaxCluster)))
+    n_cta = kMaxCluster;
+  a.rounds = rounds_by(n_cta);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)n_cta);
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = bytes_by(n_cta);
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;

@@ -490,9 +490,7 @@ cudaError_t launch(const VerifyArgs &a, int n_cta, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(verify_kernel<BF16>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  static ClusterRoom room;
-  if (n_cta == kLargeCluster &&
-      !large_cluster_fits((const void *)verify_kernel<BF16>, NT, smem, room))
+  if (n_cta == kLargeCluster && !large_cluster_fits((const void *)verify_kernel<BF16>, NT, smem))
     n_cta = kPortableCluster;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.n_seq * (unsigned)n_cta);
